@@ -109,8 +109,46 @@ class TrimulGrads(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in GRAD_FIELDS]
 
 
+class RelposParams(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("kind", "max_distance", "num_buckets", "bidirectional", "groups")]
+
+
+class ResidualParams(ctypes.Structure):
+    _fields_ = [
+        ("D", ctypes.c_int),
+        ("stream_type", ctypes.c_int),
+        ("post_norm", ctypes.c_int),
+        ("pre_norm", ctypes.c_int),
+        ("post_gamma", ctypes.c_void_p),
+        ("post_beta", ctypes.c_void_p),
+        ("pre_gamma", ctypes.c_void_p),
+        ("pre_beta", ctypes.c_void_p),
+        ("channel", ctypes.c_void_p),
+        ("gate", ctypes.c_int),
+        ("gate_sigmoid", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
+RESIDUAL_GRAD_FIELDS = ("post_gamma", "post_beta", "pre_gamma", "pre_beta", "channel")
+
+
+class ResidualGrads(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in RESIDUAL_GRAD_FIELDS]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("type", ctypes.c_int),
+    ]
+
+
 # Exported entry points: name -> (restype, argtypes).  Mirrors include/trimul.h.
-_VP, _I, _U = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint
+_VP, _I, _U, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
 SIGNATURES = {
     "trimul_create": (_I, [ctypes.POINTER(_VP), ctypes.POINTER(TrimulParams), _I]),
     "trimul_prepare": (_I, [_VP, _I, _I, _I]),
@@ -131,6 +169,19 @@ SIGNATURES = {
     "trimul_backward": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _VP, ctypes.POINTER(TrimulGrads), _VP, _U]),
     "trimul_backward_workspace_bytes": (ctypes.c_size_t, [_VP, _I, _I]),
     "trimul_kernels_per_backward": (_I, [_VP, _I, _I]),
+    "trimul_relpos_create": (_I, [ctypes.POINTER(_VP), ctypes.POINTER(RelposParams), _I]),
+    "trimul_relpos_rows": (_I, [_VP]),
+    "trimul_relpos_forward": (_I, [_VP, _VP, _I] + [_VP] * 5 + [_I] * 5 + [_VP, _I, _VP, _U]),
+    "trimul_relpos_backward_workspace_bytes": (_S, [_VP] + [_I] * 6),
+    "trimul_relpos_backward": (_I, [_VP, _VP, _I] + [_VP] * 4 + [_I] * 5 + [_VP, _VP, _S, _VP, _U]),
+    "trimul_relpos_destroy": (_I, [_VP]),
+    "trimul_residual_forward": (_I, [ctypes.POINTER(ResidualParams)] + [_VP] * 4 + [_I] * 3 + [_VP, _VP, _I, _VP, _U]),
+    "trimul_residual_backward_workspace_bytes": (_S, [ctypes.POINTER(ResidualParams)] + [_I] * 3),
+    "trimul_residual_backward": (_I, [ctypes.POINTER(ResidualParams)] + [_VP] * 7 + [_I] * 3 + [_VP] * 3
+                                 + [ctypes.POINTER(ResidualGrads), _VP, _S, _I, _VP, _U]),
+    "trimul_grad_workspace_bytes": (_S, [_I]),
+    "trimul_grad_norm": (_I, [ctypes.POINTER(GradTensor), _I, _I, _VP, _VP, _S, _I, _VP, _U]),
+    "trimul_grad_clip": (_I, [ctypes.POINTER(GradTensor), _I, ctypes.c_float, _I, _VP, _VP, _S, _I, _VP, _U]),
 }
 
 

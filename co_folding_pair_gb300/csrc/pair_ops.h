@@ -1,0 +1,79 @@
+// pair_ops.h -- argument blocks and launchers of the operators around the layer (internal):
+// relative position bias, residual step, gradient norm and clipping.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "trimul.h"
+
+namespace trimul {
+
+// Division of n < 2^31 by a fixed d in [1, 2^31): q = (umulhi(n, m) + n) >> s
+// with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, the round-up
+// method of Granlund and Montgomery ("Division by Invariant Integers using
+// Multiplication"); n < 2^31 keeps the sum within 32 bits.
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+  __device__ __forceinline__ void divmod(uint32_t n, uint32_t& q, uint32_t& r) const {
+    q = div(n);
+    r = n - q * d;
+  }
+#endif
+};
+
+// ---------------------------------------------------------------- relative position bias
+constexpr int kRelposMaxDistance = 32768;
+constexpr int kRelposMaxRows = 1024;
+
+struct RelposArgs {
+  const int16_t* lut;  // [2M + 1]: the bucket of d + M, |d| <= M (farther distances have M's)
+  int M, rows;         // rows: of the table, the one for different groups (the last) among them
+  const int32_t *q_pos, *k_pos, *q_group, *k_group;  // groups: both null, or neither
+  int B, I, J, D;
+  FastDiv by_I, by_J;
+};
+
+cudaError_t launch_relpos_forward(const RelposArgs& a, const void* table, bool table_f32, const void* base, void* out,
+                                  bool f32, trimul_layout layout, int num_sms, cudaStream_t s);
+size_t relpos_backward_workspace(int rows, int B, int I, int J, int D, trimul_layout layout, bool f32, int num_sms);
+cudaError_t launch_relpos_backward(const RelposArgs& a, const void* dout, bool f32, trimul_layout layout,
+                                   float* dtable, bool accumulate, float* ws, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- residual step
+struct ResidualArgs {
+  trimul_residual_params p;
+  const void* x;
+  const uint16_t *u, *gate, *mask;
+  int B, I, J;
+  FastDiv by_I, by_J;
+  void* out;          // forward
+  uint16_t* normed;
+  const void *dout, *dout2;  // backward
+  const uint16_t* dnormed;
+  void* dx;
+  uint16_t *du, *dgate;
+  trimul_residual_grads g;
+  float* part;        // [blocks][RESIDUAL_SUMS][D] column sums
+};
+constexpr int RESIDUAL_SUMS = 5;  // post_gamma, post_beta, pre_gamma, pre_beta, channel
+
+cudaError_t launch_residual_forward(const ResidualArgs& a, int num_sms, cudaStream_t s);
+size_t residual_backward_workspace(int D, long long rows, int num_sms);
+cudaError_t launch_residual_backward(const ResidualArgs& a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- gradient norm and clipping
+size_t grad_workspace(int n, int num_sms);
+cudaError_t launch_grad_norm(const trimul_grad_tensor* t, int n, trimul_norm_kind kind, float* norm, void* ws,
+                             bool clip, float max_norm, int num_sms, cudaStream_t s);
+
+}  // namespace trimul

@@ -18,11 +18,12 @@
 #include <vector>
 
 #include "trimul.h"
+#include "api_status.h"
 #include "kernels.h"
 
 using namespace trimul;
 
-namespace {
+namespace trimul {
 
 thread_local char g_err[512] = "";
 
@@ -39,11 +40,9 @@ trimul_status cuda_fail(cudaError_t e, const char* what) {
               cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-#define TRY_CUDA(expr, what)                      \
-  do {                                            \
-    cudaError_t e_ = (expr);                      \
-    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-  } while (0)
+}  // namespace trimul
+
+namespace {
 
 // ------------------------------------------------------------------ tensor maps
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

@@ -334,6 +334,202 @@ trimul_status trimul_host_join(trimul_handle h, void* stream);
  */
 int trimul_kernels_per_forward_host(trimul_handle h, int B, int N);
 
+/* ======================================================================
+ * Operators around the layer
+ *
+ * A pair stack starts from a position signal, adds each layer's output back
+ * into its residual stream, and takes an optimiser step from the layers'
+ * gradients.  Three operators cover these steps; each enqueues its kernels on
+ * `stream`, keeps nothing from one call to the next and takes its workspace,
+ * where it needs one, from the caller, so calls on different streams (or
+ * captured graphs) that have workspaces and outputs of their own may run at
+ * once.  They allocate nothing and do not wait on the host (TRIMUL_FLAG_CHECK
+ * aside), so every call may be captured in a CUDA graph.  Tensors are dense
+ * with 16-byte aligned base addresses unless said otherwise, and the calling
+ * thread's current device is left as it was.
+ * ====================================================================== */
+
+/* Element types of the operators below. */
+typedef enum { TRIMUL_BF16 = 0, TRIMUL_F32 = 1, TRIMUL_F16 = 2 } trimul_dtype;
+
+enum {
+  TRIMUL_FLAG_ACCUMULATE = 16u      /* trimul_relpos_backward only: add to dtable instead of overwriting it */
+};
+
+/* ---------------------------------------------------------------- relative position bias
+ * A learned bias for each pair of positions, by buckets of their distance
+ * d = q_pos[b,i] - k_pos[b,j] (computed without overflow for any int32 positions):
+ *
+ *   LINEAR, two-sided:  clip(d, -M, M) + M         2M + 1 buckets
+ *   LINEAR, one-sided:  clip(d, 0, M)              M + 1 buckets
+ *   LOG, one-sided:     K buckets, E = K / 2:  n = max(d, 0);  n below E, else
+ *                       min(K - 1, E + floor(log(n / E) / log(M / E) * (K - E)))
+ *   LOG, two-sided:     num_buckets = 2K: the same with n = |d|, plus K where d < 0
+ *
+ * (M: max_distance.  The borders of the LOG buckets are found in whole
+ * numbers, so a distance that lies exactly on a border is in the upper bucket.)
+ * With `groups` the table has one row more, the last, for the pairs whose
+ * positions are of different groups (chains of a complex, packed sequences);
+ * a position of a negative group is padding: its pairs get no bias and
+ * contribute no gradient, whatever dout holds there.
+ */
+typedef enum { TRIMUL_BUCKETS_LINEAR = 0, TRIMUL_BUCKETS_LOG = 1 } trimul_bucket_kind;
+typedef enum {
+  TRIMUL_LAYOUT_PAIR = 0,           /* [B][I][J][D]: the pair representation, D a multiple of 8 in [8, 256] */
+  TRIMUL_LAYOUT_HEADS = 1           /* [B][D][I][J]: an attention bias, D heads in [1, 256] */
+} trimul_layout;
+
+typedef struct {
+  trimul_bucket_kind kind;
+  int max_distance;                 /* M in [1, 32768]; LOG: M > E */
+  int num_buckets;                  /* LOG: K (one-sided) or 2K, K >= 2; LINEAR: 0 or the number given above */
+  int bidirectional;                /* 0: one-sided, else two-sided */
+  int groups;                       /* nonzero: one more table row, and the calls take groups */
+} trimul_relpos_params;             /* at most 1024 buckets in all */
+
+typedef struct trimul_relpos_s* trimul_relpos;
+
+/* Create a plan on `device` (10.3 required): the bucket of every distance, in device memory.  Synchronous.
+ * On failure *out is set to NULL.  The plan is read-only: any number of calls may use it at once. */
+trimul_status trimul_relpos_create(trimul_relpos* out, const trimul_relpos_params* p, int device);
+
+/* Rows of the plan's table (buckets, and one for different groups); -1 for a null plan. */
+int trimul_relpos_rows(trimul_relpos r);
+
+/*
+ * out = base + table[bucket] (base NULL: 0).  table: [rows][D] of table_type (BF16 or F32); q_pos, q_group:
+ * int32 [B][I]; k_pos, k_group: int32 [B][J] (the groups: both NULL, or both given to a plan made with
+ * `groups`); base, out: `type` (BF16 or F32) in `layout`; out may be base itself, and overlaps nothing else.
+ * The sum is taken in 32 bits and rounded once.  B, I, J >= 1 and B I J < 2^31.
+ */
+trimul_status trimul_relpos_forward(trimul_relpos r, const void* table, trimul_dtype table_type, const int32_t* q_pos,
+                                    const int32_t* k_pos, const int32_t* q_group, const int32_t* k_group,
+                                    const void* base, int B, int I, int J, int D, trimul_layout layout, void* out,
+                                    trimul_dtype type, void* stream, unsigned flags);
+
+/* Bytes of workspace a trimul_relpos_backward of these sizes needs (0 for a null plan or sizes it refuses). */
+size_t trimul_relpos_backward_workspace_bytes(trimul_relpos r, int B, int I, int J, int D, trimul_layout layout,
+                                              trimul_dtype type);
+
+/*
+ * The table's gradient: dtable[n][c] = the sum of dout over the pairs of bucket n (f32 [rows][D]; overwritten,
+ * or added to with TRIMUL_FLAG_ACCUMULATE).  dout: `type` in `layout`.  The sums are fp32 in a fixed order: the
+ * result is deterministic.  (The gradient of base is dout itself.)
+ */
+trimul_status trimul_relpos_backward(trimul_relpos r, const void* dout, trimul_dtype type, const int32_t* q_pos,
+                                     const int32_t* k_pos, const int32_t* q_group, const int32_t* k_group, int B,
+                                     int I, int J, int D, trimul_layout layout, float* dtable, void* workspace,
+                                     size_t workspace_bytes, void* stream, unsigned flags);
+
+/* Release the plan's device memory.  Synchronises the device.  NULL is accepted. */
+trimul_status trimul_relpos_destroy(trimul_relpos r);
+
+/* ---------------------------------------------------------------- residual step
+ * From a layer's output u back into the residual stream x, and on to the next
+ * layer's input, in one pass over the rows [B][I][J] of D channels:
+ *
+ *   y      = Norm_post(u)                        (NONE: u)
+ *   out    = x + scale mask channel G(gate) y    (G: the identity or the sigmoid; absent factors: 1)
+ *   normed = Norm_pre(out)                       (NONE: not computed)
+ *
+ * LAYER is nn.LayerNorm, RMS divides by the root of the mean square alone;
+ * eps is under the square root.  Statistics and everything between the loads
+ * and the stores are fp32; normed is taken from out before its rounding.
+ */
+typedef enum { TRIMUL_NORM_NONE = 0, TRIMUL_NORM_LAYER = 1, TRIMUL_NORM_RMS = 2 } trimul_norm;
+typedef enum {
+  TRIMUL_GATE_NONE = 0,
+  TRIMUL_GATE_PAIR = 1,             /* bf16 [B][I][J][D] */
+  TRIMUL_GATE_ROW = 2,              /* bf16 [B][J][D], shared by all i (row-wise dropout) */
+  TRIMUL_GATE_COL = 3               /* bf16 [B][I][D], shared by all j (column-wise dropout) */
+} trimul_gate;
+
+typedef struct {
+  int D;                            /* a multiple of 8 in [8, 256] */
+  trimul_dtype stream_type;         /* x, out, dout, dx: BF16 or F32 */
+  trimul_norm post_norm, pre_norm;
+  const float* post_gamma;          /* f32 [D]; NULL: 1.  NULL too where the norm is NONE */
+  const float* post_beta;           /* f32 [D]; NULL: 0.  NULL too where the norm is not LAYER */
+  const float* pre_gamma;
+  const float* pre_beta;
+  const float* channel;             /* f32 [D], a learned scale for each channel; NULL: 1 */
+  trimul_gate gate;
+  int gate_sigmoid;                 /* nonzero: the gate holds logits */
+  float scale;                      /* finite */
+  float eps;                        /* finite, > 0 */
+} trimul_residual_params;           /* the pointers are DEVICE pointers, read by the kernels */
+
+/*
+ * x, out: stream_type [B][I][J][D]; u: bf16 [B][I][J][D]; gate: as params->gate says (NULL for NONE); mask: bf16
+ * [B][I][J] or NULL; normed: bf16 [B][I][J][D] (NULL if pre_norm is NONE).  A pair of mask 0 is padding: out is x,
+ * normed is 0, whatever u and the gate hold there.  out may be x itself; nothing else may overlap an output.
+ * B, I, J >= 1 and B I J < 2^31.
+ */
+trimul_status trimul_residual_forward(const trimul_residual_params* p, const void* x, const uint16_t* u,
+                                      const uint16_t* gate, const uint16_t* mask, int B, int I, int J, void* out,
+                                      uint16_t* normed, int device, void* stream, unsigned flags);
+
+/* Where trimul_residual_backward writes the gradients of the parameters (f32 [D], overwritten; NULL: not wanted). */
+typedef struct {
+  float* post_gamma;
+  float* post_beta;
+  float* pre_gamma;
+  float* pre_beta;
+  float* channel;
+} trimul_residual_grads;
+
+size_t trimul_residual_backward_workspace_bytes(const trimul_residual_params* p, int B, int I, int J);
+
+/*
+ * The gradients, for dout (+ dout2, if not NULL: the part of the gradient that comes back through the next layer)
+ * with respect to out, stream_type, and dnormed with respect to normed (bf16; NULL if pre_norm is NONE).  x, u, gate
+ * and mask are the forward's (x not overwritten by out); its statistics are computed again.  dx: stream_type, may be
+ * dout itself; du: bf16; dgate: bf16, for a PAIR gate only (NULL: not wanted).  Gates shared by rows or columns are
+ * dropout masks: data, like the pair mask, without a gradient.  A padding pair passes dout (+ dout2) on to dx, and
+ * gives 0 to du and dgate and nothing to the parameters, whatever the other inputs hold there.  The parameters'
+ * gradients are summed in fp32 in a fixed order: the results are deterministic.
+ */
+trimul_status trimul_residual_backward(const trimul_residual_params* p, const void* x, const uint16_t* u,
+                                       const uint16_t* gate, const uint16_t* mask, const void* dout,
+                                       const void* dout2, const uint16_t* dnormed, int B, int I, int J, void* dx,
+                                       uint16_t* du, uint16_t* dgate, const trimul_residual_grads* grads,
+                                       void* workspace, size_t workspace_bytes, int device, void* stream,
+                                       unsigned flags);
+
+/* ---------------------------------------------------------------- gradient norm and clipping
+ * One norm over all the elements of n tensors, and the tensors scaled so that
+ * it is at most max_norm:  out = g min(1, max_norm / (norm + 1e-6)).
+ */
+typedef enum { TRIMUL_NORM_L2 = 0, TRIMUL_NORM_INF = 1 } trimul_norm_kind;
+
+typedef struct {
+  const void* data;                 /* DEVICE, aligned to its element; NULL only where numel is 0 */
+  void* out;                        /* trimul_grad_clip: data itself (in place) or a buffer of its own */
+  int64_t numel;                    /* >= 0 */
+  trimul_dtype type;
+} trimul_grad_tensor;
+
+/* Bytes of workspace trimul_grad_norm and trimul_grad_clip need for n tensors. */
+size_t trimul_grad_workspace_bytes(int n);
+
+/*
+ * norm (DEVICE f32[1]) = the norm of n >= 0 tensors (0 for none).  `tensors` is a HOST array, read during the call.
+ * Squares are summed so that neither large nor small elements leave the fp32 range, in a fixed order.  A NaN among
+ * the elements gives NaN, an infinity (without NaN) infinity.
+ */
+trimul_status trimul_grad_norm(const trimul_grad_tensor* tensors, int n, trimul_norm_kind kind, float* norm,
+                               void* workspace, size_t workspace_bytes, int device, void* stream, unsigned flags);
+
+/*
+ * The norm, and out = the tensors scaled by min(1, max_norm / (norm + 1e-6)) (max_norm >= 0; infinity: norm alone,
+ * nothing scaled), in 32 bits with one rounding to the tensor's type.  A norm that is not finite leaves the values as
+ * they are (out-of-place: copied), so that the caller can look at the norm and skip its step.  No two tensors may
+ * overlap.
+ */
+trimul_status trimul_grad_clip(const trimul_grad_tensor* tensors, int n, float max_norm, trimul_norm_kind kind,
+                               float* norm, void* workspace, size_t workspace_bytes, int device, void* stream,
+                               unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif

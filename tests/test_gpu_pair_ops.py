@@ -1,0 +1,720 @@
+"""The operators around the layer against their fp64 definitions, on a GB300.
+
+Tolerances: an output is rounded once from fp32, by at most eps / 2 of its type
+(bf16 2^-8, fp32 2^-24) relative to the value; what comes before are fp32
+operations, each off by 2^-24 of the numbers that it works on.  U = 2^-24.
+
+- relpos forward: one fp32 addition, then the rounding.
+- residual forward: y comes from a row's mean and mean square (sums of up to
+  256 terms over a tree of at most 8 + 5 levels), a reciprocal square root
+  (2 ulp), and some ten products and sums: within 64 U of the row's largest
+  magnitudes.  normed divides by out's deviation, which scales the same error.
+- column sums over all pairs: a chain of at most 1024 additions at these
+  sizes, each off by U of the sum of the terms' magnitudes, and terms within
+  64 U of theirs.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import pair_ops_oracle as O
+
+pytestmark = pytest.mark.gpu
+BF, F32, F16 = torch.bfloat16, torch.float32, torch.float16
+U = 2.0**-24
+HALF = {BF: 2.0**-8, F32: 2.0**-24, F16: 2.0**-11}
+
+
+@pytest.fixture(scope="module")
+def P():
+    from co_folding_pair_gb300 import pair_ops
+    return pair_ops
+
+
+def rng_of(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, dtype=F32):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def within(got, ref, tol, what):
+    got = f64(got)
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.nanmax(np.abs(got - ref) / (tol + 1e-300)):.3g} of the bound"
+
+
+# ------------------------------------------------------------------ relative position bias
+def positions(g, B, N, chains, pad):
+    pos = torch.arange(N, device="cuda").repeat(B, 1) + torch.randint(0, 9, (B, 1), generator=g, device="cuda")
+    group = (torch.arange(N, device="cuda") * chains // max(N, 1)).repeat(B, 1)
+    pos = pos - group * (N // (2 * chains) + 1)
+    for b in range(B):
+        n = int(pad * (b + 1) * N / B)
+        if n:
+            group[b, N - n:] = -1
+    return pos.int().contiguous(), group.int().contiguous()
+
+
+RELPOS = [  # B, I, J, D, layout, kind, M, num, two, chains, pad, dtype, table, base
+    (1, 1, 1, 8, "pair", "linear", 32, None, True, 1, 0, BF, BF, False),
+    (1, 64, 64, 32, "pair", "linear", 32, None, True, 1, 0, BF, BF, False),
+    (2, 33, 70, 136, "pair", "linear", 5, None, True, 3, 0.2, BF, F32, True),
+    (3, 57, 57, 256, "pair", "log", 40, 32, True, 2, 0.3, F32, BF, True),
+    (1, 1, 777, 72, "pair", "log", 300, 64, False, 1, 0, F32, F32, False),
+    (1, 777, 1, 24, "pair", "linear", 100, None, False, 1, 0, BF, F32, False),
+    (2, 40, 40, 128, "pair", "linear", 500, None, True, 2, 1.0, BF, BF, True),  # the second batch is all padding
+    (1, 19, 23, 192, "pair", "linear", 511, None, True, 2, 0, F32, F32, False),  # the most rows
+    (1, 1, 1, 1, "heads", "log", 128, 32, True, 1, 0, F32, F32, False),
+    (2, 65, 131, 3, "heads", "log", 128, 32, False, 1, 0, BF, F32, False),
+    (1, 64, 64, 16, "heads", "linear", 32, None, True, 1, 0, BF, BF, True),
+    (2, 37, 41, 17, "heads", "linear", 8, None, True, 2, 0.4, F32, BF, True),
+    (1, 1, 4099, 8, "heads", "log", 1000, 64, False, 1, 0, BF, BF, False),
+    (1, 300, 1, 5, "heads", "linear", 16, None, False, 3, 0.1, F32, F32, True),
+    (1, 90, 90, 256, "heads", "linear", 511, None, True, 2, 0.1, BF, F32, False),
+    (2, 16, 24, 4, "heads", "log", 20, 8, True, 2, 1.0, F32, F32, False),
+]
+
+
+def relpos_case(P, case, seed):
+    B, I, J, D, layout, kind, M, num, two, chains, pad, dtype, table, base = case
+    g = rng_of(seed)
+    r = P.RelPos(kind, M, num, two, groups=chains > 1)
+    qp, qg = positions(g, B, I, chains, pad)
+    kp, kg = positions(g, B, J, chains, pad)
+    if I == J:
+        kp, kg = qp, qg
+    if not two:
+        qp = qp + J // 2
+    groups = {"q_group": qg, "k_group": kg} if chains > 1 else {}
+    b = O.buckets(kind, M, r.rows - (chains > 1), two, qp.cpu().numpy(), kp.cpu().numpy(),
+                  qg.cpu().numpy() if groups else None, kg.cpu().numpy() if groups else None)
+    shape = (B, I, J, D) if layout == "pair" else (B, D, I, J)
+    return r, g, qp, kp, groups, b, shape
+
+
+@pytest.mark.parametrize("case", RELPOS, ids=lambda c: f"{c[4]}-{c[0]}x{c[1]}x{c[2]}x{c[3]}-{c[5]}")
+def test_relpos_forward(P, case):
+    layout, dtype, tdt, has_base = case[4], case[11], case[12], case[13]
+    r, g, qp, kp, groups, b, shape = relpos_case(P, case, 3)
+    table = randn(g, r.rows, case[3], dtype=tdt)
+    base = randn(g, *shape, dtype=dtype) if has_base else None
+    out = r.forward(table, qp, kp, base=base, layout=layout, dtype=dtype, flags=P.FLAG_CHECK, **groups)
+    ref = O.relpos_forward(f64(table), b, f64(base), layout)
+    assert out.dtype == dtype
+    # without a base the result is the table's value, rounded to the type; with one, one fp32 sum is rounded
+    within(out, ref, (HALF[dtype] * (1 + U) + U) * np.abs(ref) if has_base or tdt != dtype else 0.0 * ref, "out")
+    if has_base:
+        same = r.forward(table, qp, kp, base=base, layout=layout, out=base, **groups)
+        assert same.data_ptr() == base.data_ptr() and torch.equal(same, out)
+
+
+@pytest.mark.parametrize("case", RELPOS, ids=lambda c: f"{c[4]}-{c[0]}x{c[1]}x{c[2]}x{c[3]}-{c[5]}")
+def test_relpos_backward(P, case):
+    layout, dtype = case[4], case[11]
+    r, g, qp, kp, groups, b, shape = relpos_case(P, case, 4)
+    dout = randn(g, *shape, dtype=dtype)
+    if case[10]:  # what padding holds does not matter
+        pad = torch.from_numpy(b < 0).cuda()
+        (dout if layout == "pair" else dout.permute(0, 2, 3, 1))[pad] = float("nan")
+    ref, mag = O.relpos_backward(np.nan_to_num(f64(dout)), b, r.rows, layout)
+    got = r.backward(dout, qp, kp, layout=layout, flags=P.FLAG_CHECK, **groups)
+    tol = 1024 * U * mag
+    within(got, ref, tol, "dtable")
+    assert torch.equal(got, r.backward(dout, qp, kp, layout=layout, **groups)), "not deterministic"
+    r.backward(dout, qp, kp, layout=layout, dtable=got, flags=P.FLAG_ACCUMULATE, **groups)
+    within(got, 2 * ref, 2 * tol + U * 2 * np.abs(ref), "accumulated")
+
+
+@pytest.mark.parametrize("kind,M,num,two", [
+    ("linear", 1, None, True), ("linear", 511, None, True), ("linear", 1023, None, False), ("log", 2, 2, False),
+    ("log", 2, 4, True), ("log", 128, 32, True), ("log", 128, 16, False), ("log", 1000, 64, True), ("log", 33, 64, False),
+    ("log", 4096, 256, False), ("log", 32768, 1024, True),
+])
+def test_relpos_every_distance(P, kind, M, num, two):
+    """The bucket of every distance up to past M, and of the farthest that int32 positions have."""
+    r = P.RelPos(kind, M, num, two)
+    step = max(1, M // 3000)
+    d = torch.cat([torch.arange(-M - 3, M + 4, step), torch.tensor([-2**31, 2**31 - 1])]).int().cuda()[None]
+    zero = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    table = torch.arange(r.rows, dtype=F32, device="cuda")[:, None].repeat(1, 8)
+    got = r.forward(table, d, zero, dtype=F32)[0, :, 0, 0].long().cpu().numpy()
+    n = d[0].long().cpu().numpy()
+    if kind == "linear":
+        ref = np.clip(n, -M, M) + M if two else np.clip(n, 0, M)
+    else:
+        K = num // 2 if two else num
+        ref = np.array([O.log_bucket(abs(int(v)) if two else max(int(v), 0), K, M) + (K if two and v < 0 else 0) for v in n])
+    assert (got == ref).all()
+    far = r.forward(table, d[:, -1:], d[:, -2:-1], dtype=F32)  # a distance of 2^32 - 1
+    assert int(far.flatten()[0]) == ref[-1]
+
+
+def test_relpos_scattered_positions(P):
+    """Every pair in a bucket of its own choosing: no runs."""
+    g = rng_of(8)
+    r = P.RelPos("linear", 60)
+    pos = torch.randint(0, 61, (2, 129), generator=g, device="cuda").int()
+    b = O.buckets("linear", 60, 121, True, pos.cpu().numpy(), pos.cpu().numpy())
+    for layout, shape in (("pair", (2, 129, 129, 64)), ("pair", (2, 129, 129, 8)), ("heads", (2, 9, 129, 129))):
+        for dt in (BF, F32):
+            dout = randn(g, *shape, dtype=dt)
+            ref, mag = O.relpos_backward(f64(dout), b, 121, layout)
+            within(r.backward(dout, pos, layout=layout), ref, 1024 * U * mag, layout)
+
+
+def test_relpos_is_its_gradients_adjoint(P):
+    """sum dout (forward(T + E) - forward(T)) = sum dtable E: the forward is linear, with small whole numbers exact."""
+    g = rng_of(9)
+    r = P.RelPos("log", 200, 32, groups=True)
+    pos, group = positions(g, 2, 150, 2, 0.1)
+    for layout, D, shape in (("pair", 40, (2, 150, 150, 40)), ("heads", 6, (2, 6, 150, 150))):
+        t, e = (torch.randint(-8, 9, (33, D), generator=g, device="cuda").float() for _ in range(2))
+        dout = torch.randint(-4, 5, shape, generator=g, device="cuda").float()
+        kw = {"q_group": group, "layout": layout}
+        diff = r.forward(t + e, pos, dtype=F32, **kw).double() - r.forward(t, pos, dtype=F32, **kw).double()
+        assert float((diff * dout).sum()) == float((r.backward(dout, pos, **kw).double() * e).sum())
+
+
+def test_relpos_offsets_past_32_bits(P):
+    """4100 x 4104 pairs of 256 channels: 4.3e9 elements."""
+    r = P.RelPos("linear", 32)
+    g = rng_of(10)
+    table = randn(g, 65, 256, dtype=BF)
+    qp = torch.arange(4100, device="cuda").int()[None]
+    kp = torch.arange(4104, device="cuda").int()[None]
+    out = r.forward(table, qp, kp)
+    for i in (0, 2000, 4099):
+        b = (i - kp[0].long()).clamp(-32, 32) + 32
+        assert torch.equal(out[0, i], table[b]), i
+    dout = torch.zeros_like(out)
+    dout[0, 4099] = 1.0
+    dout[0, 0, 4103] = 2.0
+    got = r.backward(dout, qp, kp)
+    want = torch.zeros(65, 256, device="cuda", dtype=torch.float64)
+    want.index_add_(0, (4099 - kp[0].long()).clamp(-32, 32) + 32, torch.ones(4104, 256, device="cuda", dtype=torch.float64))
+    want[0] += 2.0
+    assert torch.equal(got.double(), want)
+
+
+def test_relpos_refusals(P):
+    r, rg = P.RelPos("linear", 4), P.RelPos("linear", 4, groups=True)
+    pos = torch.zeros(1, 8, dtype=torch.int32, device="cuda")
+    t = torch.zeros(9, 16, device="cuda")
+    with pytest.raises(P.TrimulError, match="without groups"):
+        r.forward(t, pos, q_group=pos)
+    with pytest.raises(ValueError, match=r"table must be \[10, D\]"):
+        rg.forward(t, pos)
+    with pytest.raises(P.TrimulError, match="multiple of 8"):
+        r.forward(t[:, :12].contiguous(), pos)
+    with pytest.raises(ValueError, match="contiguous"):
+        r.forward(t[:, :8], pos)
+    with pytest.raises(TypeError, match="q_pos"):
+        r.forward(t, pos.long())
+    with pytest.raises(P.TrimulError, match="16-byte aligned"):
+        r.forward(torch.zeros(145, device="cuda")[1:].view(9, 16), pos)
+    with pytest.raises(P.TrimulError, match="must be >= 1"):
+        r.forward(t, pos[:, :0])
+    with pytest.raises(TypeError, match="dtype"):
+        r.forward(t, pos, dtype=F16)
+    with pytest.raises(ValueError, match="layout"):
+        r.forward(t, pos, layout="rows")
+    with pytest.raises(ValueError, match="needs dtable"):
+        r.backward(torch.zeros(1, 8, 8, 16, device="cuda"), pos, flags=P.FLAG_ACCUMULATE)
+    with pytest.raises(ValueError, match="dout must be"):
+        r.backward(torch.zeros(1, 8, 7, 16, device="cuda"), pos)
+    with pytest.raises(P.TrimulError, match="flags"):
+        r.forward(t, pos, flags=P.FLAG_ACCUMULATE)
+    out = torch.zeros(1, 8, 8, 16, dtype=BF, device="cuda")
+    with pytest.raises(P.TrimulError, match="overlaps"):
+        r.forward(out.view(-1)[:144].view(9, 16), pos, out=out)
+
+
+# ------------------------------------------------------------------ residual step
+RESIDUAL = [  # B, I, J, D, stream, post, pre, gate, sigmoid, channel, masked, affine
+    (1, 1, 1, 8, BF, "layer", "layer", None, False, False, False, True),
+    (1, 64, 64, 32, BF, None, "layer", None, False, False, False, True),
+    (2, 7, 11, 136, BF, "rms", "layer", "col", False, True, True, True),
+    (1, 13, 5, 256, F32, "layer", "layer", "pair", True, False, True, True),
+    (3, 4, 9, 16, F32, None, None, "row", False, True, True, True),
+    (1, 1, 300, 64, BF, "layer", None, "pair", False, True, False, True),
+    (1, 300, 1, 72, F32, "rms", "rms", "row", True, False, True, True),
+    (2, 17, 17, 128, BF, "layer", "rms", "row", False, False, False, False),
+    (1, 21, 33, 200, BF, None, "rms", "pair", True, True, True, True),
+    (1, 5, 3, 248, F32, "rms", None, "col", True, True, False, False),
+    (1, 129, 40, 24, BF, "layer", "layer", None, False, True, True, True),
+]
+
+
+def residual_case(case, seed, offset=0.0):
+    B, I, J, D, stream, post, pre, gate, sigmoid, channel, masked, affine = case
+    g = rng_of(seed)
+    x, u = randn(g, B, I, J, D, dtype=stream), (randn(g, B, I, J, D) + offset).to(BF)
+    p = {}
+    for name, kind in (("post", post), ("pre", pre)):
+        if kind and affine:
+            p[name + "_gamma"] = 1 + 0.2 * randn(g, D)
+        if kind == "layer" and affine:
+            p[name + "_beta"] = 0.2 * randn(g, D)
+    if channel:
+        p["channel"] = 0.5 + 0.2 * randn(g, D)
+    shape = {None: None, "pair": (B, I, J, D), "row": (B, 1, J, D), "col": (B, I, 1, D)}[gate]
+    gt = None if shape is None else randn(g, *shape, dtype=BF)
+    m = None
+    if masked:
+        m = (torch.rand(B, I, J, generator=g, device="cuda") < 0.7).to(BF)
+        m[0, 0, 0] = 0.5
+        m[-1, -1, -1] = 0
+    kw = {"post_norm": post, "pre_norm": pre, "gate": gt, "gate_sigmoid": sigmoid, "mask": m, "scale": 0.75}
+    okw = {"p": {k: f64(v) for k, v in p.items()}, "post": post, "pre": pre, "gate": f64(gt), "sigmoid": sigmoid,
+           "mask": f64(m), "scale": 0.75}
+    return g, x, u, p, kw, okw
+
+
+def spoil(m, *ts):
+    """NaN and infinities in the padding pairs."""
+    if m is None:
+        return
+    for k, t in enumerate(ts):
+        if t is not None and t.shape[:3] == m.shape:
+            t[m == 0] = float("nan") if k % 2 == 0 else float("inf")
+
+
+def residual_scale(x, u, okw):
+    """For each row: the largest magnitude that its sums work on, and 1 / deviation of its output."""
+    out, _ = O.residual_forward(x, u, **{**okw, "pre": None})
+    y = np.abs(u)
+    if okw["post"]:
+        c = u - u.mean(-1, keepdims=True) if okw["post"] == "layer" else u
+        y = np.abs(u).max(-1, keepdims=True) / np.sqrt((c * c).mean(-1, keepdims=True) + 1e-5)
+        y = y * np.abs(okw["p"].get("post_gamma", 1.0)).max() + np.abs(okw["p"].get("post_beta", 0.0)).max()
+    gate = 1.0 if okw["gate"] is None else np.maximum(np.abs(okw["gate"]), 1.0)
+    big = np.abs(x) + 0.75 * y * gate * np.abs(okw["p"].get("channel", 1.0)).max()
+    big = np.nan_to_num(big, posinf=0, neginf=0).max(-1, keepdims=True)
+    c = out - out.mean(-1, keepdims=True) if okw["pre"] == "layer" else out
+    return out, big, 1.0 / np.sqrt((c * c).mean(-1, keepdims=True) + 1e-5)
+
+
+@pytest.mark.parametrize("offset", [0.0, 30.0])
+@pytest.mark.parametrize("case", RESIDUAL, ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}x{c[3]}-{c[5]}-{c[6]}-{c[7]}")
+def test_residual_forward(P, case, offset):
+    g, x, u, p, kw, okw = residual_case(case, 21, offset)
+    _, big, r = residual_scale(f64(x), f64(u), okw)
+    spoil(kw["mask"], u, kw["gate"])
+    okw["gate"] = f64(kw["gate"])
+    ref, nref = O.residual_forward(f64(x), f64(u), **okw)
+    out, normed = P.trimul_residual_forward(x, u, p, flags=P.FLAG_CHECK, **kw)
+    within(out, ref, HALF[case[4]] * np.abs(ref) + 64 * U * big, "out")
+    if case[6]:
+        gamma = np.abs(okw["p"].get("pre_gamma", 1.0)).max()
+        within(normed, nref, HALF[BF] * np.abs(nref) + 64 * U * big * r * gamma * (1 + np.abs(nref)), "normed")
+    else:
+        assert normed is None
+    keep = out.clone()
+    out2, normed2 = P.trimul_residual_forward(x, u, p, out=x, **kw)
+    assert out2.data_ptr() == x.data_ptr() and torch.equal(out2, keep)
+    assert normed is None or torch.equal(normed, normed2)
+
+
+@pytest.mark.parametrize("second", [False, True])
+@pytest.mark.parametrize("case", RESIDUAL, ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}x{c[3]}-{c[5]}-{c[6]}-{c[7]}")
+def test_residual_backward(P, case, second):
+    g, x, u, p, kw, okw = residual_case(case, 22)
+    _, big, r = residual_scale(f64(x), f64(u), okw)
+    dout, dout2 = randn(g, *x.shape, dtype=case[4]), randn(g, *x.shape, dtype=case[4]) if second else None
+    dn = randn(g, *x.shape, dtype=BF) if case[6] else None
+    spoil(kw["mask"], u, x, dn, kw["gate"])
+    okw["gate"] = f64(kw["gate"])
+    d = f64(dout) + (f64(dout2) if second else 0.0)
+    rdx, rdu, rdg, rp = O.residual_backward(f64(x), f64(u), d, dnormed=f64(dn), **okw)
+    got = P.trimul_residual_backward(x, u, dout, p, dnormed=dn, dout2=dout2, flags=P.FLAG_CHECK, **kw)
+    # a row's gradient: its magnitudes through both norms, relative errors of 64 U of its inputs' on the way
+    dbig = np.abs(d).max(-1, keepdims=True) + (0 if dn is None else 8 * (r * (1 + big * r)) * np.abs(np.nan_to_num(f64(dn), posinf=0)).max(-1, keepdims=True) * np.abs(okw["p"].get("pre_gamma", 1.0)).max())
+    within(got["dx"], rdx, HALF[case[4]] * np.abs(rdx) + 64 * U * dbig, "dx")
+    w = 0.75 * np.abs(okw["p"].get("channel", 1.0)).max() * (1 if okw["gate"] is None else max(1.0, np.nanmax(np.abs(np.where(np.isfinite(okw["gate"]), okw["gate"], 0)))))
+    uu = np.nan_to_num(f64(u), posinf=0, neginf=0)
+    c = uu - uu.mean(-1, keepdims=True) if case[5] == "layer" else uu
+    rp_ = 1.0 / np.sqrt((c * c).mean(-1, keepdims=True) + 1e-5) if case[5] else np.ones_like(uu[..., :1])
+    ybig = np.abs(uu).max(-1, keepdims=True) * rp_
+    within(got["du"], rdu, HALF[BF] * np.abs(rdu) + 64 * U * dbig * w * 8 * rp_ * (1 + ybig * ybig), "du")
+    if case[7] == "pair":
+        within(got["dgate"], rdg, HALF[BF] * np.abs(rdg) + 64 * U * dbig * 2 * w * (1 + ybig), "dgate")
+    else:
+        assert got["dgate"] is None or kw["gate"].shape == x.shape
+    assert sorted(got["grads"]) == sorted(p)
+    for k, v in got["grads"].items():
+        ref, mag = rp[k]
+        # the terms' own errors are relative to the rows' magnitudes, not to the terms
+        rows = x.shape[0] * x.shape[1] * x.shape[2]
+        own = 64 * U * rows * float((dbig * (1 + ybig) * (1 + big * r)).max()) * w
+        within(v, ref, 1024 * U * mag + own, k)
+    again = P.trimul_residual_backward(x, u, dout, p, dnormed=dn, dout2=dout2, dx=dout, **kw)
+    assert again["dx"].data_ptr() == dout.data_ptr()
+    for k in ("dx", "du", "dgate"):
+        a, b = got[k], again[k]
+        assert a is None or torch.equal(a.view(torch.int16 if a.dtype == BF else torch.int32), b.view(torch.int16 if b.dtype == BF else torch.int32)), k
+    for k in p:
+        assert torch.equal(got["grads"][k], again["grads"][k]), f"{k}: not deterministic"
+
+
+def test_residual_gradients_are_the_forwards(P):
+    """The gradients against central differences of the forward (fp32 stream).
+
+    out differs by an fp32 rounding, at most 2^-24 of some 8, from a smooth function; its values are compared with
+    random weights summed in fp64 over n = 12000 elements, so the difference of two sums is off by about
+    sqrt(n) 2^-22, and over 2 h = 0.02 by 1.3e-3; the central difference's own error is h^2 / 6 times third
+    derivatives: for all together 0.02 sqrt(n) of the sum's size, sqrt(n), is some twenty times what is expected."""
+    g = rng_of(31)
+    x, u, gate = randn(g, 1, 10, 12, 96), randn(g, 1, 10, 12, 96, dtype=BF), randn(g, 1, 10, 12, 96, dtype=BF)
+    p = {"post_gamma": 1 + 0.1 * randn(g, 96), "post_beta": 0.1 * randn(g, 96), "channel": 1 + 0.1 * randn(g, 96)}
+    dout = randn(g, *x.shape)
+    kw = {"post_norm": "layer", "gate": gate, "gate_sigmoid": True, "scale": 0.75}
+    got = P.trimul_residual_backward(x, u, dout, p, **kw)
+    def loss(**change):
+        a = {"x": x, "params": p, **kw, **change}
+        return float((P.trimul_residual_forward(a.pop("x"), u, a.pop("params"), **a)[0].double() * dout.double()).sum())
+    h, n = 1e-2, x.numel()
+    e = randn(g, *x.shape)
+    assert abs((loss(x=x + h * e) - loss(x=x - h * e)) / (2 * h) - float((got["dx"].double() * e).sum())) < 0.02 * math.sqrt(n)
+    for k in p:
+        e = randn(g, 96)
+        num = (loss(params={**p, k: p[k] + h * e}) - loss(params={**p, k: p[k] - h * e})) / (2 * h)
+        assert abs(num - float((got["grads"][k].double() * e).sum())) < 0.02 * math.sqrt(n), k
+
+
+def test_residual_all_padding_and_constant_rows(P):
+    """Masks that leave nothing, and rows of one value, whose deviation is 0."""
+    g = rng_of(33)
+    x, u = randn(g, 2, 3, 5, 40, dtype=BF), torch.full((2, 3, 5, 40), 3.0, dtype=BF, device="cuda")
+    p = {"post_gamma": 1 + randn(g, 40), "post_beta": randn(g, 40), "pre_gamma": randn(g, 40), "pre_beta": randn(g, 40)}
+    kw = {"post_norm": "layer", "pre_norm": "layer"}
+    out, normed = P.trimul_residual_forward(x, u, p, **kw)
+    # u - mean is exactly 0, so y is beta, and out the sum of two numbers, rounded
+    assert torch.equal(out, (x.float() + p["post_beta"]).to(BF)) and torch.isfinite(normed).all()
+    m = torch.zeros(2, 3, 5, dtype=BF, device="cuda")
+    dn = randn(g, *x.shape, dtype=BF)
+    out, normed = P.trimul_residual_forward(x, u, p, mask=m, **kw)
+    assert torch.equal(out, x) and not normed.any()
+    got = P.trimul_residual_backward(x, u, x, p, dnormed=dn, mask=m, **kw)
+    assert torch.equal(got["dx"], x) and not got["du"].any()
+    assert all(not v.any() for v in got["grads"].values())
+
+
+def test_residual_offsets_past_32_bits(P):
+    """4100 x 4104 pairs of 256 channels: the last rows are the small call's."""
+    g = rng_of(34)
+    x = torch.empty(1, 4100, 4104, 256, dtype=BF, device="cuda")
+    u = torch.empty_like(x)
+    for i in range(0, 4100, 100):
+        x[0, i:i + 100] = randn(g, 100, 4104, 256, dtype=BF)
+        u[0, i:i + 100] = randn(g, 100, 4104, 256, dtype=BF)
+    p = {"post_gamma": 1 + 0.1 * randn(g, 256)}
+    kw = {"post_norm": "rms", "pre_norm": "layer"}
+    out, normed = P.trimul_residual_forward(x, u, p, **kw)
+    last = (x[:, 4098:].contiguous(), u[:, 4098:].contiguous())
+    o2, n2 = P.trimul_residual_forward(*last, p, **kw)
+    assert torch.equal(out[:, 4098:], o2) and torch.equal(normed[:, 4098:], n2)
+    got = P.trimul_residual_backward(x, u, out, p, dnormed=normed, **kw)
+    g2 = P.trimul_residual_backward(*last, o2, p, dnormed=n2, **kw)
+    assert torch.equal(got["dx"][:, 4098:], g2["dx"]) and torch.equal(got["du"][:, 4098:], g2["du"])
+
+
+def test_residual_refusals(P):
+    x = torch.zeros(1, 4, 6, 16, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="gate must be one of"):
+        P.trimul_residual_forward(x, x.clone(), gate=torch.zeros(1, 1, 1, 16, dtype=BF, device="cuda"))
+    with pytest.raises(ValueError, match="unknown parameter"):
+        P.trimul_residual_forward(x, x.clone(), {"gamma": x})
+    with pytest.raises(TypeError, match="u must be"):
+        P.trimul_residual_forward(x, x.float())
+    with pytest.raises(ValueError, match="contiguous"):
+        P.trimul_residual_forward(x.transpose(1, 2), x.clone())
+    with pytest.raises(P.TrimulError, match="overlaps"):
+        P.trimul_residual_forward(x, x.clone(), pre_norm="rms", normed=x)
+    with pytest.raises(P.TrimulError, match="dnormed and pre_norm"):
+        P.trimul_residual_backward(x, x.clone(), x.clone(), pre_norm="rms")
+    with pytest.raises(P.TrimulError, match="only a gate of every pair"):
+        P.trimul_residual_backward(x, x.clone(), x.clone(), gate=torch.zeros(1, 1, 6, 16, dtype=BF, device="cuda"), dgate=x.clone())
+    with pytest.raises(P.TrimulError, match="must be >= 1"):
+        P.trimul_residual_forward(x[:, :0], x[:, :0].clone())
+
+
+# ------------------------------------------------------------------ gradient norm and clipping
+def grads_of(g, sizes, kinds, scale=1.0):
+    return [(scale * randn(g, n)).to(kinds[k % len(kinds)]) for k, n in enumerate(sizes)]
+
+
+@pytest.mark.parametrize("inf", [False, True])
+@pytest.mark.parametrize("sizes,kinds", [
+    ([], [F32]), ([0], [F32]), ([1], [BF]), ([7, 0, 8193, 1, 0], [F32, BF, F16]), ([16384] * 6 + [128] * 4, [F32]),
+    ([5] * 2503, [BF, F32]), ([1000003, 3, 300000], [F32, F16, BF]), ([4 << 20], [BF]),
+])
+def test_grad_clip(P, sizes, kinds, inf):
+    g = rng_of(41)
+    ts = grads_of(g, sizes, kinds)
+    ref_n = float(O.grad_norm([f64(t) for t in ts], inf))
+    kind = math.inf if inf else 2.0
+    # the norm: squares and their partial sums in fp32 (a chain of at most 64 and a root), the rest in fp64
+    tol = 64 * U * ref_n
+    assert abs(float(P.trimul_grad_norm(ts, kind)) - ref_n) <= tol
+    for share in (0.3, 2.0):
+        max_norm = share * ref_n if ref_n else 1.0
+        _, ref = O.grad_clip([f64(t) for t in ts], max_norm, inf)
+        outs = [torch.full_like(t, 7.0) for t in ts]
+        n = P.trimul_grad_clip(ts, max_norm, kind, outs=outs, flags=P.FLAG_CHECK)
+        assert n.shape == () and abs(float(n) - ref_n) <= tol
+        for o, r, t in zip(outs, ref, ts):
+            if share > 1:
+                assert torch.equal(o, t)
+            # the factor's error, a product and a rounding (of an fp16 subnormal: half its step)
+            within(o, r, (HALF[t.dtype] + 80 * U) * np.abs(r) + (2.0**-25 if t.dtype == F16 else 0), f"clip {share}")
+        same = [t.clone() for t in ts]
+        P.GradSet(same).clip(max_norm, kind)
+        assert all(torch.equal(a, b) for a, b in zip(same, outs))
+
+
+@pytest.mark.parametrize("value", [1e-30, 1e-42, 1e19, 3e38])
+def test_grad_norm_of_large_and_small_values(P, value):
+    t = torch.full((100003,), value, device="cuda")
+    exact = float(t[0].double()) * math.sqrt(100003)
+    got = float(P.trimul_grad_norm([t]))
+    assert got == math.inf if exact > 3.4028235e38 else abs(got - exact) <= 64 * U * exact + 2.0**-150
+    b = torch.cat([torch.full((9,), 1e30, device="cuda"), torch.ones(50000, device="cuda")]).to(BF)
+    exact = 3 * float(b[0].double())
+    assert abs(float(P.trimul_grad_norm([b])) - exact) <= 64 * U * exact
+
+
+@pytest.mark.parametrize("bad,inf", [(math.nan, False), (math.inf, False), (math.nan, True), (-math.inf, True)])
+def test_grad_clip_leaves_what_is_not_finite(P, bad, inf):
+    g = rng_of(43)
+    ts = grads_of(g, [300, 20000, 17], [F32, BF])
+    ts[1][12345] = bad
+    keep = [t.clone() for t in ts]
+    n = float(P.trimul_grad_clip(ts, 1e-3, math.inf if inf else 2))
+    assert math.isnan(n) if math.isnan(bad) else n == math.inf
+    outs = [torch.zeros_like(t) for t in ts]
+    P.trimul_grad_clip(ts, 1e-3, math.inf if inf else 2, outs=outs)
+    for t, k, o in zip(ts, keep, outs):
+        view = torch.int32 if t.dtype == F32 else torch.int16
+        assert torch.equal(t.view(view), k.view(view)) and torch.equal(o.view(view), k.view(view))
+
+
+def test_grad_clip_to_zero_and_to_infinity(P):
+    ts = grads_of(rng_of(44), [1000], [F32])
+    keep = ts[0].clone()
+    P.trimul_grad_clip(ts, math.inf)
+    assert torch.equal(ts[0], keep)
+    P.trimul_grad_clip(ts, 0.0)
+    assert not ts[0].any()
+    assert float(P.trimul_grad_clip(ts, 1.0)) == 0.0
+
+
+def test_grad_clip_of_views_at_any_offset(P):
+    """Tensors that begin at any element of a buffer, source and destination alike or not; nothing between them moves."""
+    g = rng_of(45)
+    for dt in (F32, BF, F16):
+        flat, to = randn(g, 60000, dtype=dt), torch.full((60000,), 3.0, dtype=dt, device="cuda")
+        spans = [(1, 5), (7, 8), (13, 9011), (9030, 9030), (9031, 30000), (30002, 59999)]
+        outs = [(2, 6), (7, 8), (14, 9012), (9030, 9030), (9031, 30000), (30001, 59998)]
+        ts, os_ = [flat[a:b] for a, b in spans], [to[a:b] for a, b in outs]
+        before = flat.clone()
+        n = float(P.trimul_grad_clip(ts, 10.0, outs=os_))
+        c = np.float64(10.0) / (float(O.grad_norm([f64(t) for t in ts])) + 1e-6)
+        assert torch.equal(flat, before)
+        left = torch.ones(60000, dtype=torch.bool, device="cuda")
+        for (a, b), o, t in zip(outs, os_, ts):
+            left[a:b] = False
+            within(o, f64(t) * c, (HALF[dt] + 80 * U) * np.abs(f64(t) * c) + (2.0**-25 if dt == F16 else 0), "view")
+        assert (to[left] == 3.0).all() and n > 10
+
+
+def test_grad_clip_past_32_bits(P):
+    """2.2e9 elements in one tensor."""
+    n = (1 << 31) + 100_000_001
+    t = torch.zeros(n, dtype=BF, device="cuda")
+    t[0], t[n - 1], t[1 << 31] = 3.0, 4.0, 12.0
+    assert float(P.trimul_grad_clip([t], 1.3)) == 13.0
+    c = np.float32(np.float64(np.float32(1.3)) / (13 + 1e-6))
+    for at, v in ((0, 3.0), (n - 1, 4.0), (1 << 31, 12.0)):
+        assert float(t[at]) == float(torch.tensor(np.float32(v) * c).to(BF))
+
+
+# ------------------------------------------------------------------ streams, graphs, guard bands
+class Guarded:
+    """A tensor between two bands of a fixed pattern."""
+
+    def __init__(self, t):
+        n = t.numel() * t.element_size()
+        self.raw = torch.full((4096 + n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.t = self.raw[4096:4096 + n].view(t.dtype).view(t.shape)
+        self.t.copy_(t)
+
+    def intact(self):
+        n = self.raw.numel() - 8192
+        return bool((self.raw[:4096] == 0xA5).all()) and bool((self.raw[4096 + n:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("D,dt", [(8, BF), (136, F32), (256, BF)])
+def test_nothing_is_written_outside_the_outputs(P, D, dt):
+    g = rng_of(51)
+    r = P.RelPos("linear", 7)
+    for layout, shape in (("pair", (2, 19, 23, D)), ("heads", (2, D, 19, 23))):
+        qp, kp = Guarded(torch.arange(38, device="cuda").int().view(2, 19)), Guarded(torch.arange(46, device="cuda").int().view(2, 23))
+        t, out = Guarded(randn(g, 15, D)), Guarded(randn(g, *shape, dtype=dt))
+        dt_ = Guarded(torch.zeros(15, D, device="cuda"))
+        r.forward(t.t, qp.t, kp.t, base=out.t, out=out.t, layout=layout)
+        r.backward(out.t, qp.t, kp.t, layout=layout, dtable=dt_.t)
+        assert all(v.intact() for v in (qp, kp, t, out, dt_)), layout
+    x, u, gt = (Guarded(randn(g, 2, 19, 23, D, dtype=k)) for k in (dt, BF, BF))
+    m = Guarded(torch.ones(2, 19, 23, dtype=BF, device="cuda"))
+    p = {k: Guarded(randn(g, D)) for k in P.RESIDUAL_PARAMS}
+    pt = {k: v.t for k, v in p.items()}
+    kw = {"post_norm": "layer", "pre_norm": "layer", "gate": gt.t, "mask": m.t}
+    out, normed, dx, du, dg = (Guarded(torch.zeros(2, 19, 23, D, dtype=k, device="cuda")) for k in (dt, BF, dt, BF, BF))
+    gr = {k: Guarded(torch.zeros(D, device="cuda")) for k in p}
+    P.trimul_residual_forward(x.t, u.t, pt, out=out.t, normed=normed.t, **kw)
+    P.trimul_residual_backward(x.t, u.t, out.t, pt, dnormed=normed.t, dx=dx.t, du=du.t, dgate=dg.t,
+                               grads={k: v.t for k, v in gr.items()}, **kw)
+    assert all(v.intact() for v in (x, u, gt, m, out, normed, dx, du, dg, *p.values(), *gr.values()))
+
+
+def test_two_graphs_at_once(P):
+    """Each operator captured twice and the graphs replayed side by side on two streams, with new inputs, give what
+    the eager calls give."""
+    def make(seed):
+        g = rng_of(seed)
+        s = {"pos": torch.arange(200, device="cuda").int()[None], "r": P.RelPos("linear", 32),
+             "x": randn(g, 1, 200, 200, 64, dtype=BF), "u": randn(g, 1, 200, 200, 64, dtype=BF),
+             "dout": randn(g, 1, 200, 200, 64, dtype=BF), "p": {"post_gamma": 1 + randn(g, 64)}, "table": randn(g, 65, 64)}
+        return s
+
+    def step(s):
+        z = s["r"].forward(s["table"], s["pos"], base=s["x"])
+        out, _ = P.trimul_residual_forward(z, s["u"], s["p"], post_norm="rms")
+        b = P.trimul_residual_backward(z, s["u"], s["dout"], s["p"], post_norm="rms")
+        dt = s["r"].backward(b["dx"], s["pos"])
+        outs = [torch.empty_like(dt), torch.empty_like(b["grads"]["post_gamma"])]
+        n = P.trimul_grad_clip([dt, b["grads"]["post_gamma"]], 1.0, outs=outs)
+        return [z, out, b["dx"], b["du"], n, *outs]
+
+    states, graphs, results = [make(1), make(2)], [], []
+    for s in states:
+        step(s)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            results.append(step(s))
+        graphs.append(graph)
+    for seed in (5, 6):
+        for k, s in enumerate(states):
+            s["x"].copy_(randn(rng_of(10 * seed + k), *s["x"].shape, dtype=BF))
+        want = [step(s) for s in states]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in states]
+        for _ in range(20):
+            for graph, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(results, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_calls_on_another_stream(P):
+    """`stream` orders the call, and its outputs and workspace belong to it."""
+    g = rng_of(61)
+    s = torch.cuda.Stream()
+    x, u = randn(g, 1, 300, 300, 128, dtype=BF), randn(g, 1, 300, 300, 128, dtype=BF)
+    pos = torch.arange(300, device="cuda").int()[None]
+    r = P.RelPos("linear", 32)
+    torch.cuda.synchronize()
+    want = P.trimul_residual_backward(x, u, u, {}, post_norm="layer")["du"], r.backward(x, pos), P.trimul_grad_norm([x])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200000)
+        got = (P.trimul_residual_backward(x, u, u, {}, post_norm="layer", stream=s)["du"], r.backward(x, pos, stream=s),
+               P.trimul_grad_norm([x], stream=s))
+        junk = [torch.full((1, 300, 300, 128), 9.0, dtype=BF, device="cuda") for _ in range(3)]
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        torch.cuda.synchronize()
+        del junk
+
+
+# ------------------------------------------------------------------ a stack, as it is used
+def test_a_stack_and_its_training_step(P):
+    """relpos -> two blocks (a layer and its residual step) -> backward -> clip, against the fp64 definitions.
+
+    The layers' bounds hold here: 5e-3 relative (2-norm) for a layer's output, 1.5e-2 for its gradients; two layers and
+    the steps between them (bf16, 2^-8 each) are held to twice that."""
+    from co_folding_pair_gb300 import synthetic as S
+    from co_folding_pair_gb300 import trimul as T
+    from oracle import trimul_backward as OB
+    from oracle import trimul_oracle as OT
+
+    N, D = 24, 32
+    g = rng_of(71)
+    pos, group = positions(g, 1, N, 2, 0.0)
+    group[0, -3:] = -1
+    mask = ((group[0] >= 0)[:, None] & (group[0] >= 0)[None]).to(BF)[None].contiguous()
+    r = P.RelPos("linear", 8, groups=True)
+    table = randn(g, r.rows, D)
+    z_in, dout = randn(g, 1, N, N, D, dtype=BF), randn(g, 1, N, N, D, dtype=BF)
+    drop = ((torch.rand(1, 1, N, D, generator=g, device="cuda") > 0.25).float() / 0.75).to(BF)
+    params = [S.make_case(S.custom(1, N, D, D, seed=80 + k))[2] for k in range(2)]
+    dirs = ["outgoing", "incoming"]
+    res_p = [{"post_gamma": 1 + 0.1 * randn(g, D), "post_beta": 0.1 * randn(g, D), "channel": 0.5 + 0.1 * randn(g, D)} for _ in range(2)]
+    blocks = [P.PairBlock(T.TriMul(params[k], dirs[k]), P.Residual(res_p[k], post_norm="layer")) for k in range(2)]
+    z0 = r.forward(table, pos, q_group=group, base=z_in)
+    z1, _ = blocks[0].forward(z0, mask, drop)
+    z2, _ = blocks[1].forward(z1, mask, drop)
+    b2 = blocks[1].backward(z1, dout, mask, drop)
+    b1 = blocks[0].backward(z0, b2["dx"], mask, drop, dout2=b2["dz"])
+    dtable = r.backward(b1["dx"], pos, q_group=group)
+    r.backward(b1["dz"], pos, q_group=group, dtable=dtable, flags=P.FLAG_ACCUMULATE)
+    grads = {"table": dtable}
+    for k, b in enumerate((b1, b2)):
+        grads.update({f"{k}.{n}": v for part in ("layer_grads", "residual_grads") for n, v in b[part].items()})
+    raw = {k: f64(v) for k, v in grads.items()}
+    norm = P.trimul_grad_clip(grads, 1.0)
+
+    # the definitions
+    m64, drop64 = f64(mask), f64(drop)
+    bk = O.buckets("linear", 8, 17, True, pos.cpu().numpy(), pos.cpu().numpy(), group.cpu().numpy(), group.cpu().numpy())
+    zs, us, rp = [O.relpos_forward(f64(table), bk, f64(z_in))], [], [{k: f64(v) for k, v in q.items()} for q in res_p]
+    pn = [{k: v.double().numpy() for k, v in q.items()} for q in params]
+    for k in range(2):
+        us.append(OT.trimul_forward(zs[-1], m64, pn[k], dirs[k]))
+        zs.append(O.residual_forward(zs[-1], us[-1], rp[k], post="layer", gate=drop64, mask=m64)[0])
+    ref, d = {}, f64(dout)
+    for k in (1, 0):
+        dx, du, _, dp = O.residual_backward(zs[k], us[k], d, rp[k], post="layer", gate=drop64, mask=m64)
+        lay = OB.trimul_backward(zs[k], m64, pn[k], dirs[k], du)
+        ref.update({f"{k}.{n}": dp[n][0] for n in rp[k]})
+        ref.update({f"{k}.{n}": lay[n] for n in T.GRAD_NAMES})
+        d = dx + lay["dz"]
+    ref["table"] = O.relpos_backward(d, bk, r.rows)[0]
+
+    def rel(a, b):
+        return np.linalg.norm(a - b) / np.linalg.norm(b)
+
+    assert rel(f64(z2), zs[2]) < 1e-2
+    assert sorted(raw) == sorted(ref)
+    for k in ref:
+        assert rel(raw[k], ref[k]) < 3e-2, k
+    total = float(O.grad_norm(list(raw.values())))
+    assert abs(float(norm) - total) <= 64 * U * total
+    for k in raw:
+        within(grads[k], raw[k] / (total + 1e-6), 82 * U * np.abs(raw[k] / total), k)
