@@ -36,138 +36,529 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One thread per element of [B][H][I][J].
+template <typename T>
+struct Vec;  // 16 bytes of T
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void unpack(const uint4 v, float (&f)[8]) { unpack8(v, f); }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) { return pack8(f); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void unpack(const uint4 v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+// V buckets (16 bits each) that begin at word-aligned `ids` + V - m, from the two aligned groups of V around them.
+template <int V>
+__device__ __forceinline__ void shifted_ids(const uint16_t* ids, int m, uint32_t (&w)[V / 2]);
+template <>
+__device__ __forceinline__ void shifted_ids<8>(const uint16_t* ids, int m, uint32_t (&w)[4]) {
+  const uint4 hi = *reinterpret_cast<const uint4*>(ids + 8);
+  w[0] = hi.x, w[1] = hi.y, w[2] = hi.z, w[3] = hi.w;
+  if (m == 0) return;
+  const uint4 lo = *reinterpret_cast<const uint4*>(ids);
+  uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  // by whole words first, m / 2 of them, then by half a word
+  if (m & 4) {
+#pragma unroll
+    for (int i = 7; i >= 2; --i) x[i] = x[i - 2];
+  }
+  if (m & 2) {
+#pragma unroll
+    for (int i = 7; i >= 1; --i) x[i] = x[i - 1];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (m & 1) ? __funnelshift_l(x[i + 3], x[i + 4], 16) : x[i + 4];
+}
+template <>
+__device__ __forceinline__ void shifted_ids<4>(const uint16_t* ids, int m, uint32_t (&w)[2]) {
+  const uint2 hi = *reinterpret_cast<const uint2*>(ids + 4);
+  w[0] = hi.x, w[1] = hi.y;
+  if (m == 0) return;
+  const uint2 lo = *reinterpret_cast<const uint2*>(ids);
+  uint32_t x[4] = {lo.x, lo.y, hi.x, hi.y};
+  if (m & 2) {
+#pragma unroll
+    for (int i = 3; i >= 1; --i) x[i] = x[i - 1];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = (m & 1) ? __funnelshift_l(x[i + 1], x[i + 2], 16) : x[i + 2];
+}
+
+constexpr uint16_t kNoBucket = 0xffff;
+
+// The buckets of plane positions [f0 - V, f0 + n) of batch b, in order; kNoBucket outside the plane and for padding.
+__device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, long long f0, int n, int V, uint32_t plane,
+                                          uint16_t* ids) {
+  for (int i = threadIdx.x; i < n + V; i += blockDim.x) {
+    const long long f = f0 - V + i;
+    uint16_t k = kNoBucket;
+    if (f >= 0 && f < plane) {
+      uint32_t row, j;
+      a.by_J.divmod(static_cast<uint32_t>(f), row, j);
+      k = static_cast<uint16_t>(relpos_bucket(a, b * a.I + row, b * a.J + j));
+    }
+    ids[i] = k;
+  }
+}
+
+// HEADS layout.  A block goes over tiles of a plane [I][J] of 16 bytes a
+// thread: the buckets of a tile are worked out once, in shared memory, and
+// every head of the block looks its values up by them, in its column of the
+// table, in shared memory too.  Planes of odd sizes begin anywhere within 16
+// bytes: a head's tile then begins up to V - 1 elements early, on a boundary,
+// its buckets shifted alike, and only a plane's ends are written one by one.
+constexpr int kHeadThreads = 256;
+constexpr int kTableBytes = 64 * 1024;
+
 template <typename T, typename Tab>
-__global__ void __launch_bounds__(256)
-    k7_relpos_heads(RelposArgs a, const Tab* __restrict__ table, const T* base, T* out, long long n_out, FastDiv by_H) {
-  for (long long n = blockIdx.x * 256ll + threadIdx.x; n < n_out; n += gridDim.x * 256ll) {
-    const long long line = n / a.J;  // (b H + h) I + i
-    const uint32_t j = static_cast<uint32_t>(n - line * a.J);
-    const long long bh = line / a.I;
-    const uint32_t i = static_cast<uint32_t>(line - bh * a.I);
-    uint32_t b, h;
-    by_H.divmod(static_cast<uint32_t>(bh), b, h);
-    const int k = relpos_bucket(a, b * a.I + i, b * a.J + j);
-    float v = k >= 0 ? to_f32(table[static_cast<size_t>(k) * a.D + h]) : 0.f;
-    if (base) v += to_f32(base[n]);
-    out[n] = from_f32<T>(v);
+__global__ void __launch_bounds__(kHeadThreads)
+    k7_relpos_heads(RelposArgs a, const Tab* __restrict__ table, const T* base, T* out, uint32_t plane,
+                    FastDiv by_tiles, int heads) {
+  constexpr int V = Vec<T>::n, kTile = kHeadThreads * V;
+  extern __shared__ float tab[];  // [heads][rows]
+  __shared__ alignas(16) uint16_t ids[kTile + V];
+  const int h0 = blockIdx.y * heads, n_heads = min(heads, a.D - h0);
+  for (int n = threadIdx.x; n < a.rows * n_heads; n += kHeadThreads) {
+    const int r = n / n_heads, q = n - r * n_heads;
+    tab[q * a.rows + r] = to_f32(table[static_cast<size_t>(r) * a.D + h0 + q]);
+  }
+  for (uint32_t tile = blockIdx.x; tile < by_tiles.d * a.B; tile += gridDim.x) {
+    uint32_t b, t;
+    by_tiles.divmod(tile, b, t);
+    stage_ids(a, b, static_cast<long long>(t) * kTile, kTile, V, plane, ids);
+    __syncthreads();
+#pragma unroll 2
+    for (int q = 0; q < n_heads; ++q) {
+      const long long begin = (static_cast<long long>(b) * a.D + h0 + q) * plane;
+      const int m = static_cast<int>(begin % V);
+      const long long n = begin - m + static_cast<long long>(t) * kTile + threadIdx.x * V;
+      if (n >= begin + plane) continue;
+      uint32_t w[V / 2];
+      shifted_ids<V>(ids + threadIdx.x * V, m, w);
+      const float* const col = tab + q * a.rows;
+      float v[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const uint32_t k = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+        v[e] = k == kNoBucket ? 0.f : col[k];
+      }
+      if (n >= begin && n + V <= begin + plane) {
+        if (base) {
+          float z[V];
+          Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(base + n)), z);
+#pragma unroll
+          for (int e = 0; e < V; ++e) v[e] += z[e];
+        }
+        __stcs(reinterpret_cast<uint4*>(out + n), Vec<T>::pack(v));
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (n + e >= begin && n + e < begin + plane) out[n + e] = from_f32<T>(base ? v[e] + to_f32(base[n + e]) : v[e]);
+      }
+    }
+    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------ gradient
-// Each block adds up a range of pairs in shared memory, [rows][channels of the
-// block], and writes its sums; k7_relpos_sum adds the blocks' sums in order.
-constexpr int kSumBytes = 200 * 1024;  // shared memory for the sums
+// Sums are kept in shared memory and written to global memory once a block;
+// k7_relpos_sum adds the blocks' sums in order.  No atomics: every sum has one
+// owner, so results do not depend on the order in which warps run.
+//
+// What makes these sums cheap is that neighbours share a bucket: all pairs
+// farther than M, and in LOG buckets runs of near ones.  A run is added up in
+// registers and goes to shared memory when it ends.
+constexpr int kSumBytes = 200 * 1024;  // shared memory for a block's sums
 
-// One thread per channel; a block takes a slice of the channels and a range of pairs.
-template <typename T>
-__global__ void k7_relpos_grad_pair(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs) {
-  extern __shared__ float sums[];
-  const int W = blockDim.x, c = blockIdx.y * W + threadIdx.x;
-  for (int r = 0; r < a.rows; ++r) sums[r * W + threadIdx.x] = 0.f;
-  const uint32_t p0 = static_cast<uint32_t>(static_cast<unsigned long long>(pairs) * blockIdx.x / gridDim.x);
-  const uint32_t p1 = static_cast<uint32_t>(static_cast<unsigned long long>(pairs) * (blockIdx.x + 1) / gridDim.x);
-  if (c >= a.D) return;
-  int at = -1;
-  float run = 0.f;
-  for (uint32_t p = p0; p < p1; ++p) {
-    uint32_t row, j;
-    a.by_J.divmod(p, row, j);
-    const int k = relpos_bucket(a, row, a.by_I.div(row) * a.J + j);
-    if (k < 0) continue;
-    if (k != at) {
-      if (at >= 0) sums[at * W + threadIdx.x] += run;
-      at = k;
-      run = 0.f;
+// PAIR layout.  A warp has sums of its own, [rows][W channels], for one slice
+// of at most W channels.  G lanes (16 bytes each) share a pair, so the warp
+// takes 32 / G neighbouring pairs at a time, its slots; kSteps of these are
+// loaded together, and the next ones while these are added.  The buckets of
+// a batch are worked out once, one pair a lane, and handed round by shuffles.
+constexpr int kSteps = 8;
+
+template <typename T, int G>
+__global__ void __launch_bounds__(512)
+    k7_relpos_grad_pair(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs, int slice) {
+  constexpr int V = Vec<T>::n, W = G * V, P = 32 / G, kBatch = P * kSteps, kPerLane = (kBatch + 31) / 32;
+  extern __shared__ float4 smem4[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  const int slot = lane / G, c = (lane % G) * V;
+  float* const sums = reinterpret_cast<float*>(smem4) + static_cast<size_t>(warp) * a.rows * W;
+  for (int n = lane; n < a.rows * W / 4; n += 32) reinterpret_cast<float4*>(sums)[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncwarp();
+  // this block's channels, and its range of batches
+  const int c0 = blockIdx.y * slice, width = min(slice, a.D - c0);
+  const bool live = c < width;
+  const uint32_t batches = (pairs + kBatch - 1) / kBatch;
+  const uint32_t b0 = static_cast<uint32_t>(static_cast<unsigned long long>(batches) * blockIdx.x / gridDim.x);
+  const uint32_t b1 = static_cast<uint32_t>(static_cast<unsigned long long>(batches) * (blockIdx.x + 1) / gridDim.x);
+
+  uint4 next[kSteps];
+  int next_k[kPerLane];
+  auto load = [&](uint32_t batch) {
+    const uint32_t p0 = batch * kBatch;
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const uint32_t p = p0 + u * P + slot;
+      next[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && p < pairs) next[u] = __ldcs(reinterpret_cast<const uint4*>(dout + static_cast<size_t>(p) * a.D + c0 + c));
     }
-    run += to_f32(dout[static_cast<size_t>(p) * a.D + c]);
+#pragma unroll
+    for (int q = 0; q < kPerLane; ++q) {
+      const uint32_t p = p0 + q * 32 + lane;
+      next_k[q] = -1;
+      if (p < pairs && q * 32 + lane < kBatch) {
+        uint32_t row, j;
+        a.by_J.divmod(p, row, j);
+        next_k[q] = relpos_bucket(a, row, a.by_I.div(row) * a.J + j);
+      }
+    }
+  };
+
+  int at = -1;  // the bucket of this slot's run
+  float run[V] = {};
+  // the runs of the slots whose `end` is set go to shared memory; slots that
+  // share a bucket take turns
+  auto flush = [&](bool end) {
+    const unsigned same = __match_any_sync(0xffffffffu, end ? at : -1 - slot);
+    float4* const to = reinterpret_cast<float4*>(sums + at * W + c);
+    auto add = [&] {
+#pragma unroll
+      for (int q = 0; q < V / 4; ++q) {
+        float4 t = to[q];
+        t.x += run[4 * q], t.y += run[4 * q + 1], t.z += run[4 * q + 2], t.w += run[4 * q + 3];
+        to[q] = t;
+      }
+    };
+    if (__all_sync(0xffffffffu, __popc(same) <= G)) {
+      if (end) add();
+      __syncwarp();
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < P; ++k) {
+        if (end && slot == k) add();
+        __syncwarp();
+      }
+    }
+  };
+
+  uint32_t batch = b0 + warp;
+  if (batch < b1) load(batch);
+  for (; batch < b1; batch += warps) {
+    uint4 now[kSteps];
+    int k_of[kPerLane];
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) now[u] = next[u];
+#pragma unroll
+    for (int q = 0; q < kPerLane; ++q) k_of[q] = next_k[q];
+    if (batch + warps < b1) load(batch + warps);
+
+    const int k0 = __shfl_sync(0xffffffffu, at, 0);
+    bool one = at == k0 && k0 >= 0;  // the whole batch goes on with the run of all slots
+#pragma unroll
+    for (int q = 0; q < kPerLane; ++q) one = one && (k_of[q] == k0 || q * 32 + lane >= kBatch);
+    if (__all_sync(0xffffffffu, one)) {
+      float t[V] = {}, v[V];
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+        Vec<T>::unpack(now[u], v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) t[e] += v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) run[e] += t[e];
+      continue;
+    }
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const int k = __shfl_sync(0xffffffffu, k_of[u * P / 32], (u * P + slot) % 32);
+      const bool end = k >= 0 && at >= 0 && k != at;
+      if (__any_sync(0xffffffffu, end)) flush(end);
+      if (k >= 0) {
+        float v[V];
+        Vec<T>::unpack(now[u], v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) run[e] = (k == at ? run[e] : 0.f) + v[e];
+        at = k;
+      }
+    }
   }
-  if (at >= 0) sums[at * W + threadIdx.x] += run;
-  for (int r = 0; r < a.rows; ++r)
-    part[(static_cast<size_t>(blockIdx.x) * a.rows + r) * a.D + c] = sums[r * W + threadIdx.x];
+  flush(at >= 0);
+  __syncthreads();
+  const float* const all = reinterpret_cast<const float*>(smem4);
+  float* const out = part + static_cast<size_t>(blockIdx.x) * a.rows * a.D + c0;
+  for (int n = threadIdx.x; n < a.rows * W; n += blockDim.x) {
+    const int r = n / W, w = n % W;
+    if (w >= width) continue;
+    float t = 0.f;
+    for (int k = 0; k < warps; ++k) t += all[static_cast<size_t>(k) * a.rows * W + n];
+    out[static_cast<size_t>(r) * a.D + w] = t;
+  }
 }
 
-// One warp per head and range of pairs; every lane has its own column of sums.
+// HEADS layout.  A block goes over tiles of a plane [I][J]; the buckets of a
+// tile are worked out once, in shared memory, and every warp adds up one
+// head's part of the tile.  Each lane has sums of its own ([rows][32 lanes]),
+// 16 bytes of neighbouring elements at a time.  Planes of odd sizes begin
+// anywhere within 16 bytes: a head's tile then begins up to V - 1 elements
+// early, on a boundary, and its buckets are shifted alike.
+constexpr int kTileSteps = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(32)
-    k7_relpos_grad_heads(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs, FastDiv by_plane) {
-  extern __shared__ float sums[];
-  const int lane = threadIdx.x, h = blockIdx.y;
+struct HeadTile {
+  static constexpr int V = Vec<T>::n;
+  static constexpr int part = kTileSteps * 32 * V;  // elements of a warp's part of a tile
+};
+
+template <typename T>
+__global__ void __launch_bounds__(512)
+    k7_relpos_grad_heads(RelposArgs a, const T* __restrict__ dout, float* partial, uint32_t plane, FastDiv by_tiles,
+                         int heads) {
+  constexpr int V = Vec<T>::n, kPart = HeadTile<T>::part;
+  extern __shared__ float4 smem4[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  const int parts = warps / heads, tile_n = parts * kPart;
+  const int h = blockIdx.y * heads + warp % heads, my_part = warp / heads;
+  const bool live = h < a.D;
+  float* const sums = reinterpret_cast<float*>(smem4) + static_cast<size_t>(warp) * a.rows * 32;
+  uint16_t* const ids0 = reinterpret_cast<uint16_t*>(reinterpret_cast<float*>(smem4) + static_cast<size_t>(warps) * a.rows * 32);
   for (int r = 0; r < a.rows; ++r) sums[r * 32 + lane] = 0.f;
-  const uint32_t p0 = static_cast<uint32_t>(static_cast<unsigned long long>(pairs) * blockIdx.x / gridDim.x);
-  const uint32_t p1 = static_cast<uint32_t>(static_cast<unsigned long long>(pairs) * (blockIdx.x + 1) / gridDim.x);
-  for (uint32_t p = p0 + lane; p < p1; p += 32) {
-    uint32_t b, at, row, j;
-    by_plane.divmod(p, b, at);
-    a.by_J.divmod(p, row, j);
-    const int k = relpos_bucket(a, row, b * a.J + j);
-    if (k < 0) continue;
-    sums[k * 32 + lane] += to_f32(dout[(static_cast<size_t>(b) * a.D + h) * by_plane.d + at]);
+  const long long total = static_cast<long long>(a.B) * a.D * plane;
+  const uint32_t tiles = by_tiles.d * a.B;
+
+  uint4 next[kTileSteps];
+  auto load = [&](uint32_t tile) {
+    uint32_t b, t;
+    by_tiles.divmod(tile, b, t);
+    const long long base = (static_cast<long long>(b) * a.D + h) * plane;
+    const long long first = base - base % V + static_cast<long long>(t) * tile_n + my_part * kPart + lane * V;
+#pragma unroll
+    for (int u = 0; u < kTileSteps; ++u) {
+      const long long n = first + u * 32 * V;
+      next[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (!live || n >= base + plane) continue;
+      if (n + V <= total) {
+        next[u] = __ldcs(reinterpret_cast<const uint4*>(dout + n));
+      } else {  // the tensor's last elements, where they do not fill 16 bytes
+        alignas(16) T last[V] = {};
+        for (int e = 0; n + e < total; ++e) last[e] = dout[n + e];
+        next[u] = *reinterpret_cast<const uint4*>(last);
+      }
+    }
+  };
+
+  int at = -1;
+  float run = 0.f;
+  auto flush = [&] {
+    if (at >= 0) sums[at * 32 + lane] += run;
+  };
+  int turn = 0;
+  uint32_t tile = blockIdx.x;
+  if (tile < tiles) load(tile);
+  for (; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    uint32_t b, t;
+    by_tiles.divmod(tile, b, t);
+    uint16_t* const ids = ids0 + turn * (tile_n + V);
+    // two buffers: a warp that is still adding the last tile reads the other one
+    stage_ids(a, b, static_cast<long long>(t) * tile_n, tile_n, V, plane, ids);
+    __syncthreads();
+    uint4 now[kTileSteps];
+#pragma unroll
+    for (int u = 0; u < kTileSteps; ++u) now[u] = next[u];
+    if (tile + gridDim.x < tiles) load(tile + gridDim.x);
+    if (!live) continue;
+    const int m = static_cast<int>(((static_cast<long long>(b) * a.D + h) * plane) % V);
+#pragma unroll
+    for (int u = 0; u < kTileSteps; ++u) {
+      uint32_t w[V / 2];
+      shifted_ids<V>(ids + my_part * kPart + u * 32 * V + lane * V, m, w);
+      float v[V];
+      Vec<T>::unpack(now[u], v);
+      const uint32_t same = static_cast<uint32_t>(at) * 0x10001u;
+      bool one = at >= 0;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) one = one && w[i] == same;
+      if (one) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) s += v[e];
+        run += s;
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const int k = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+          if (k == kNoBucket) continue;
+          if (k != at) {
+            flush();
+            at = k;
+            run = 0.f;
+          }
+          run += v[e];
+        }
+      }
+    }
   }
+  flush();
   __syncwarp();
+  // the lanes' sums, added in a fixed order; then the parts' (in lane 0's column)
   for (int r = lane; r < a.rows; r += 32) {
     float t = 0.f;
     for (int l = 0; l < 32; ++l) t += sums[r * 32 + ((l + lane) & 31)];
-    part[(static_cast<size_t>(blockIdx.x) * a.rows + r) * a.D + h] = t;
+    sums[r * 32] = t;
+  }
+  __syncthreads();
+  for (int n = threadIdx.x; n < a.rows * heads; n += blockDim.x) {
+    const int r = n / heads, q = n % heads, head = blockIdx.y * heads + q;
+    if (head >= a.D) continue;
+    float t = 0.f;
+    for (int k = 0; k < parts; ++k)
+      t += reinterpret_cast<const float*>(smem4)[static_cast<size_t>(k * heads + q) * a.rows * 32 + r * 32];
+    partial[(static_cast<size_t>(blockIdx.x) * a.rows + r) * a.D + head] = t;
   }
 }
 
+// The blocks' sums: 32 columns a block, eight groups of parts side by side.
 __global__ void __launch_bounds__(256)
     k7_relpos_sum(const float* __restrict__ part, float* dtable, int n, int parts, int accumulate) {
-  const int e = blockIdx.x * 256 + threadIdx.x;
-  if (e >= n) return;
+  __shared__ float s[8][32];
+  const int e = blockIdx.x * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
   float t = 0.f;
-  for (int k = 0; k < parts; ++k) t += part[static_cast<size_t>(k) * n + e];
+  if (e < n) {
+#pragma unroll 8
+    for (int k = g; k < parts; k += 8) t += part[static_cast<size_t>(k) * n + e];
+  }
+  s[g][threadIdx.x % 32] = t;
+  __syncthreads();
+  if (g != 0 || e >= n) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) t += s[k][threadIdx.x];
   dtable[e] = accumulate ? dtable[e] + t : t;
 }
 
-// Ranges of pairs (blocks) of a gradient, and the channels of a block.
-void grad_split(int rows, int B, int I, int J, int D, trimul_layout layout, int num_sms, int* ranges, int* width) {
-  const long long pairs = static_cast<long long>(B) * I * J;
-  *width = layout == TRIMUL_LAYOUT_HEADS ? 1 : std::min(D, std::max(1, kSumBytes / (rows * 4)));
-  const int slices = (D + *width - 1) / *width;
-  *ranges = static_cast<int>(std::max<long long>(1, std::min<long long>(pairs / 64, std::max(1, 4 * num_sms / slices))));
+// How a gradient is split over blocks.
+struct GradSplit {
+  int warps, lanes, slice, slices, ranges, smem;
+};
+
+// PAIR: at least eight warps' sums have to fit an SM's shared memory for
+// enough loads to be in flight, so the slice is at most 64 channels and
+// narrower for long tables; slices are as even as 16-byte groups allow.
+template <typename T>
+GradSplit split_pair(int rows, long long pairs, int D, int num_sms) {
+  constexpr int V = Vec<T>::n;
+  GradSplit g;
+  int W = V;
+  while (W < D && W < 64 && rows * 2 * W * 4 * 8 <= kSumBytes) W *= 2;
+  g.lanes = W / V;
+  const int groups = D / V;  // of 16 bytes
+  g.slices = (groups + g.lanes - 1) / g.lanes;
+  g.slice = (groups + g.slices - 1) / g.slices * V;
+  g.slices = (D + g.slice - 1) / g.slice;
+  g.warps = std::min(16, kSumBytes / (rows * W * 4));
+  g.smem = g.warps * rows * W * 4;
+  const long long batches = (pairs + 32 / g.lanes * kSteps - 1) / (32 / g.lanes * kSteps);
+  g.ranges = static_cast<int>(std::max<long long>(1, std::min<long long>((batches + g.warps - 1) / g.warps, num_sms / g.slices)));
+  return g;
+}
+
+// HEADS: one warp a head, several for a head's parts of a tile where there are few heads.
+template <typename T>
+GradSplit split_heads(int rows, int B, long long plane, int H, int num_sms) {
+  constexpr int V = Vec<T>::n, kPart = HeadTile<T>::part;
+  GradSplit g;
+  constexpr int kMost = 220 * 1024, kIds = 2 * (kPart + V) * 2;  // two buffers of a part's buckets
+  const int own = rows * 32 * 4;
+  const int warps = std::max(1, std::min(16, (kMost - kIds) / own));
+  g.slices = (H + warps - 1) / warps;
+  g.lanes = (H + g.slices - 1) / g.slices;  // heads of a block
+  int parts = static_cast<int>(std::max<long long>(1, std::min<long long>(warps / g.lanes, (plane + kPart - 1) / kPart)));
+  while (parts > 1 && parts * (g.lanes * own + kIds) > kMost) --parts;
+  g.warps = g.lanes * parts;
+  g.slice = parts * kPart;
+  g.smem = g.warps * own + 2 * (g.slice + V) * 2;
+  const long long tiles = B * ((plane + V - 1 + g.slice - 1) / g.slice);
+  g.ranges = static_cast<int>(std::max<long long>(1, std::min<long long>(tiles, num_sms / g.slices)));
+  return g;
+}
+
+template <typename T>
+GradSplit split(int rows, int B, int I, int J, int D, trimul_layout layout, int num_sms) {
+  const long long plane = static_cast<long long>(I) * J;
+  return layout == TRIMUL_LAYOUT_PAIR ? split_pair<T>(rows, B * plane, D, num_sms)
+                                      : split_heads<T>(rows, B, plane, D, num_sms);
 }
 
 template <typename T, typename Tab>
 cudaError_t forward(const RelposArgs& a, const void* table, const void* base, void* out, trimul_layout layout,
                     int num_sms, cudaStream_t s) {
-  const long long elems = static_cast<long long>(a.B) * a.I * a.J * a.D;
-  const long long work = layout == TRIMUL_LAYOUT_PAIR ? elems / 8 : elems;
-  const int grid = static_cast<int>(std::min<long long>((work + 255) / 256, 8ll * num_sms));
-  if (layout == TRIMUL_LAYOUT_PAIR)
+  if (layout == TRIMUL_LAYOUT_PAIR) {
+    const long long work = static_cast<long long>(a.B) * a.I * a.J * (a.D / 8);
+    const int grid = static_cast<int>(std::min<long long>((work + 255) / 256, 8ll * num_sms));
     k7_relpos_pair<T, Tab><<<grid, 256, 0, s>>>(a, static_cast<const Tab*>(table), static_cast<const T*>(base),
                                                 static_cast<T*>(out), work, a.D / 8);
-  else
-    k7_relpos_heads<T, Tab><<<grid, 256, 0, s>>>(a, static_cast<const Tab*>(table), static_cast<const T*>(base),
-                                                 static_cast<T*>(out), work, FastDiv(a.D));
+    return cudaGetLastError();
+  }
+  constexpr int V = Vec<T>::n, kTile = kHeadThreads * V;
+  const uint32_t plane = static_cast<uint32_t>(a.I) * a.J;
+  const long long tiles = (static_cast<long long>(plane) + V - 1 + kTile - 1) / kTile;
+  // heads of a block: as many as have room for their columns of the table, fewer where that leaves SMs without work
+  const int most = std::min(a.D, kTableBytes / (a.rows * 4));
+  int groups = static_cast<int>(std::max<long long>((a.D + most - 1) / most,
+                                                    std::min<long long>(a.D, 4 * num_sms / (tiles * a.B))));
+  const int heads = (a.D + groups - 1) / groups;
+  groups = (a.D + heads - 1) / heads;
+  const int grid = static_cast<int>(std::min<long long>(tiles * a.B, std::max(1, 8 * num_sms / groups)));
+  cudaError_t e = cudaFuncSetAttribute(k7_relpos_heads<T, Tab>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableBytes);
+  if (e != cudaSuccess) return e;
+  k7_relpos_heads<T, Tab><<<dim3(grid, groups), kHeadThreads, heads * a.rows * 4, s>>>(
+      a, static_cast<const Tab*>(table), static_cast<const T*>(base), static_cast<T*>(out), plane,
+      FastDiv(static_cast<uint32_t>(tiles)), heads);
+  return cudaGetLastError();
+}
+
+template <typename T, int G>
+cudaError_t grad_pair(const RelposArgs& a, const T* dout, const GradSplit& g, float* ws, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(k7_relpos_grad_pair<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSumBytes);
+  if (e != cudaSuccess) return e;
+  k7_relpos_grad_pair<T, G><<<dim3(g.ranges, g.slices), g.warps * 32, g.smem, s>>>(
+      a, dout, ws, static_cast<uint32_t>(a.B) * a.I * a.J, g.slice);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t backward(const RelposArgs& a, const void* dout, trimul_layout layout, float* dtable, bool accumulate,
+cudaError_t backward(const RelposArgs& a, const void* grad, trimul_layout layout, float* dtable, bool accumulate,
                      float* ws, int num_sms, cudaStream_t s) {
-  int ranges, width;
-  grad_split(a.rows, a.B, a.I, a.J, a.D, layout, num_sms, &ranges, &width);
-  const uint32_t pairs = static_cast<uint32_t>(a.B) * a.I * a.J;
-  const dim3 grid(ranges, (a.D + width - 1) / width);
+  const GradSplit g = split<T>(a.rows, a.B, a.I, a.J, a.D, layout, num_sms);
+  const T* const dout = static_cast<const T*>(grad);
+  cudaError_t e = cudaSuccess;
   if (layout == TRIMUL_LAYOUT_PAIR) {
-    const int smem = a.rows * width * 4;
-    cudaError_t e = cudaFuncSetAttribute(k7_relpos_grad_pair<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSumBytes);
-    if (e != cudaSuccess) return e;
-    k7_relpos_grad_pair<T><<<grid, width, smem, s>>>(a, static_cast<const T*>(dout), ws, pairs);
+    switch (g.lanes) {
+      case 1: e = grad_pair<T, 1>(a, dout, g, ws, s); break;
+      case 2: e = grad_pair<T, 2>(a, dout, g, ws, s); break;
+      case 4: e = grad_pair<T, 4>(a, dout, g, ws, s); break;
+      case 8: e = grad_pair<T, 8>(a, dout, g, ws, s); break;
+      default: e = grad_pair<T, 16>(a, dout, g, ws, s); break;
+    }
   } else {
-    const int smem = a.rows * 32 * 4;
-    cudaError_t e = cudaFuncSetAttribute(k7_relpos_grad_heads<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kRelposMaxRows * 32 * 4);
+    e = cudaFuncSetAttribute(k7_relpos_grad_heads<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    k7_relpos_grad_heads<T><<<grid, 32, smem, s>>>(a, static_cast<const T*>(dout), ws, pairs,
-                                                   FastDiv(static_cast<uint32_t>(a.I) * a.J));
+    const uint32_t plane = static_cast<uint32_t>(a.I) * a.J;
+    const uint32_t tiles = static_cast<uint32_t>((plane + static_cast<long long>(Vec<T>::n) - 1 + g.slice - 1) / g.slice);
+    k7_relpos_grad_heads<T><<<dim3(g.ranges, g.slices), g.warps * 32, g.smem, s>>>(a, dout, ws, plane, FastDiv(tiles), g.lanes);
+    e = cudaGetLastError();
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int n = a.rows * a.D;
-  k7_relpos_sum<<<(n + 255) / 256, 256, 0, s>>>(ws, dtable, n, ranges, accumulate ? 1 : 0);
+  k7_relpos_sum<<<(n + 31) / 32, 256, 0, s>>>(ws, dtable, n, g.ranges, accumulate ? 1 : 0);
   return cudaGetLastError();
 }
 
@@ -183,9 +574,8 @@ cudaError_t launch_relpos_forward(const RelposArgs& a, const void* table, bool t
 }
 
 size_t relpos_backward_workspace(int rows, int B, int I, int J, int D, trimul_layout layout, bool f32, int num_sms) {
-  int ranges, width;
-  grad_split(rows, B, I, J, D, layout, num_sms, &ranges, &width);
-  return static_cast<size_t>(ranges) * rows * D * sizeof(float);
+  const GradSplit g = f32 ? split<float>(rows, B, I, J, D, layout, num_sms) : split<__nv_bfloat16>(rows, B, I, J, D, layout, num_sms);
+  return static_cast<size_t>(g.ranges) * rows * D * sizeof(float);
 }
 
 cudaError_t launch_relpos_backward(const RelposArgs& a, const void* dout, bool f32, trimul_layout layout,
