@@ -80,6 +80,43 @@ __device__ __forceinline__ void param8(const float* p, int c, bool live, float a
   }
 }
 
+// The rows of the next turns are on their way while one is worked on: every
+// thread copies its own 16 bytes of each tensor into a ring of its own in
+// shared memory and reads them back itself, so the ring needs no barrier, only
+// the thread's wait for its oldest copies.  Depth, not registers, sets the
+// bytes in flight.
+constexpr int kDepth = 4;
+
+__device__ __forceinline__ void copy16(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // until at most N groups are on their way
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's eight elements of T at ring slots [k], [k + 1] (fp32 only), kThreads apart.
+__device__ __forceinline__ void copy8(uint4* to, const __nv_bfloat16* from) { copy16(to, from); }
+__device__ __forceinline__ void copy8(uint4* to, const float* from) {
+  copy16(to, from);
+  copy16(to + kThreads, from + 4);
+}
+__device__ __forceinline__ void take8(const uint4* from, bool on, float (&f)[8], __nv_bfloat16) {
+  unpack8(on ? from[0] : make_uint4(0u, 0u, 0u, 0u), f);
+}
+__device__ __forceinline__ void take8(const uint4* from, bool on, float (&f)[8], float) {
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u), a = on ? from[0] : z, b = on ? from[kThreads] : z;
+  f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
+  f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
+}
+// Streaming stores: what is written is not read again here.
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&f)[8]) { __stcs(reinterpret_cast<uint4*>(p), pack8(f)); }
+__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+}
+
 // sigmoid(x) and 1 - sigmoid(x), each to fp32's relative precision (the
 // exponential's argument is never positive, so nothing overflows either).
 __device__ __forceinline__ float2 sigmoid2(float x) {
@@ -96,6 +133,8 @@ __device__ __forceinline__ const uint16_t* gate_row(const ResidualArgs& a, uint3
   return a.gate + at * a.p.D;
 }
 
+using bf = __nv_bfloat16;
+
 __device__ __forceinline__ float mask_of(const ResidualArgs& a, uint32_t pair) {
   return a.mask ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.mask)[pair]) : 1.f;
 }
@@ -105,111 +144,191 @@ __device__ __forceinline__ void zero8(float (&f)[8]) {
   for (int e = 0; e < 8; ++e) f[e] = 0.f;
 }
 
-using bf = __nv_bfloat16;
+template <typename T>
+constexpr int kSlots = sizeof(T) / 2;  // ring slots of eight elements
+
+// Ring slots of a stage.
+template <typename T>
+__host__ __device__ constexpr int forward_slots(bool gate) {
+  return kSlots<T> + 1 + (gate ? 1 : 0);
+}
+template <typename T>
+__host__ __device__ constexpr int backward_slots(bool gate, bool second, bool pre) {
+  return kSlots<T> * (second ? 3 : 2) + 1 + (gate ? 1 : 0) + (pre ? 1 : 0);
+}
 
 // G lanes share a row, eight channels each.
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) k8_residual_fwd(ResidualArgs a, uint32_t rows) {
+__global__ void __launch_bounds__(kThreads, 3) k8_residual_fwd(ResidualArgs a, uint32_t rows) {
+  extern __shared__ uint4 ring[];
+  constexpr uint32_t kRows = kThreads / G;
   const int c = (threadIdx.x % G) * 8;
   const bool live = c < a.p.D;
   const float d_f = static_cast<float>(a.p.D), inv_d = 1.0f / d_f;
-  float pg[8], pb[8], ng[8], nb[8], ch[8];
-  param8(a.p.post_gamma, c, live, 1.f, pg);
-  param8(a.p.post_beta, c, live, 0.f, pb);
+  // scale channel (gamma y^ + beta) = A y^ + B
+  float A[8], B[8], ng[8], nb[8];
+  {
+    float ch[8];
+    param8(a.p.post_gamma, c, live, 1.f, A);
+    param8(a.p.post_beta, c, live, 0.f, B);
+    param8(a.p.channel, c, live, 1.f, ch);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) A[e] *= a.p.scale * ch[e], B[e] *= a.p.scale * ch[e];
+  }
   param8(a.p.pre_gamma, c, live, 1.f, ng);
   param8(a.p.pre_beta, c, live, 0.f, nb);
-  param8(a.p.channel, c, live, 1.f, ch);
-  constexpr uint32_t kRows = kThreads / G;
+  const int slots = forward_slots<T>(a.gate);
+  const uint32_t step = gridDim.x * kRows, mine = blockIdx.x * kRows + threadIdx.x / G;
+  uint4* const own = ring + threadIdx.x;
+  // row `row` into stage `stage`; rows past the end close an empty group
+  auto fetch = [&](unsigned long long row, int stage) {
+    if (live && row < rows) {
+      const size_t at = static_cast<size_t>(row) * a.p.D + c;
+      uint4* const to = own + stage * slots * kThreads;
+      copy8(to, static_cast<const T*>(a.x) + at);
+      copy16(to + kSlots<T> * kThreads, a.u + at);
+      if (a.gate) copy16(to + (kSlots<T> + 1) * kThreads, gate_row(a, static_cast<uint32_t>(row)) + c);
+    }
+    copies_end();
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) fetch(mine + static_cast<unsigned long long>(k) * step, k);
+  int stage = 0;
+  float m_next = (a.mask && mine < rows) ? mask_of(a, mine) : 1.f;
   // every lane of a warp takes the same number of turns, for the shuffles
-  for (uint32_t base = blockIdx.x * kRows; base < rows; base += gridDim.x * kRows) {
-    const uint32_t row = base + threadIdx.x / G;
+  for (unsigned long long base = blockIdx.x * kRows; base < rows; base += step) {
+    const unsigned long long row = base + threadIdx.x / G;
     const bool on = live && row < rows;
     const size_t at = static_cast<size_t>(row) * a.p.D + c;
+    const float m = m_next;
+    if (a.mask && row + step < rows) m_next = mask_of(a, static_cast<uint32_t>(row + step));
+    fetch(row + (kDepth - 1ull) * step, (stage + kDepth - 1) % kDepth);
+    copies_wait<kDepth - 1>();
+    const uint4* const from = own + stage * slots * kThreads;
+    stage = (stage + 1) % kDepth;
     float x[8], y[8], g[8];
-    zero8(x), zero8(y), zero8(g);
-    float m = 1.f;
-    if (on) {
-      load8(static_cast<const T*>(a.x) + at, x);
-      load8(reinterpret_cast<const bf*>(a.u) + at, y);
-      if (a.gate) load8(reinterpret_cast<const bf*>(gate_row(a, row)) + c, g);
-      m = mask_of(a, row);
-    }
+    take8(from, on, x, T());
+    take8(from + kSlots<T> * kThreads, on, y, bf());
+    if (a.gate) take8(from + (kSlots<T> + 1) * kThreads, on, g, bf());
     if (a.p.post_norm != TRIMUL_NORM_NONE) normalise<G>(y, a.p.post_norm, d_f, inv_d, a.p.eps, live);
-    const float k = a.p.scale * m;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float w = k * ch[e];
+      float w = m;
       if (a.gate) w *= a.p.gate_sigmoid ? sigmoid2(g[e]).x : g[e];
-      if (m != 0.f) x[e] += w * (a.p.post_norm != TRIMUL_NORM_NONE ? y[e] * pg[e] + pb[e] : y[e]);
+      if (m != 0.f) x[e] += w * (y[e] * A[e] + B[e]);
     }
-    if (on) store8(static_cast<T*>(a.out) + at, x);
+    if (on) put8(static_cast<T*>(a.out) + at, x);
     if (a.normed) {
       if (!live) zero8(x);
       normalise<G>(x, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = m != 0.f ? x[e] * ng[e] + nb[e] : 0.f;
-      if (on) store8(reinterpret_cast<bf*>(a.normed) + at, x);
+      if (on) put8(reinterpret_cast<bf*>(a.normed) + at, x);
     }
   }
 }
 
+// Depth of the backward's ring: it has up to six tensors to read.
+constexpr int kBackDepth = 2;
+
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) k8_residual_bwd(ResidualArgs a, uint32_t rows) {
+__global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, uint32_t rows) {
+  extern __shared__ uint4 ring[];
+  __shared__ float4 par4[4][64];  // post_gamma, post_beta, pre_gamma, channel
+  constexpr uint32_t kRows = kThreads / G;
   const int c = (threadIdx.x % G) * 8;
   const bool live = c < a.p.D;
   const float d_f = static_cast<float>(a.p.D), inv_d = 1.0f / d_f;
   const bool post = a.p.post_norm != TRIMUL_NORM_NONE, pre = a.p.pre_norm != TRIMUL_NORM_NONE;
-  float pg[8], pb[8], ng[8], ch[8];
-  param8(a.p.post_gamma, c, live, 1.f, pg);
-  param8(a.p.post_beta, c, live, 0.f, pb);
-  param8(a.p.pre_gamma, c, live, 1.f, ng);
-  param8(a.p.channel, c, live, 1.f, ch);
+  {
+    const float* const from[4] = {a.p.post_gamma, a.p.post_beta, a.p.pre_gamma, a.p.channel};
+    for (int n = threadIdx.x; n < 4 * 256; n += kThreads) {
+      const int q = n / 256, e = n % 256;
+      reinterpret_cast<float*>(par4[q])[e] = e < a.p.D && from[q] ? from[q][e] : q == 1 ? 0.f : 1.f;
+    }
+    __syncthreads();
+  }
+  auto par = [&](int q, float (&f)[8]) { load8(reinterpret_cast<const float*>(par4[q]) + c, f); };
+  const int slots = backward_slots<T>(a.gate, a.dout2, pre);
+  const int at_u = kSlots<T> * (a.dout2 ? 3 : 2), at_g = at_u + 1, at_n = at_g + (a.gate ? 1 : 0);
+  const uint32_t step = gridDim.x * kRows, mine = blockIdx.x * kRows + threadIdx.x / G;
+  uint4* const own = ring + threadIdx.x;
+  auto fetch = [&](unsigned long long row, int stage) {
+    if (live && row < rows) {
+      const size_t at = static_cast<size_t>(row) * a.p.D + c;
+      uint4* const to = own + stage * slots * kThreads;
+      copy8(to, static_cast<const T*>(a.dout) + at);
+      copy8(to + kSlots<T> * kThreads, static_cast<const T*>(a.x) + at);
+      if (a.dout2) copy8(to + 2 * kSlots<T> * kThreads, static_cast<const T*>(a.dout2) + at);
+      copy16(to + at_u * kThreads, a.u + at);
+      if (a.gate) copy16(to + at_g * kThreads, gate_row(a, static_cast<uint32_t>(row)) + c);
+      if (pre) copy16(to + at_n * kThreads, a.dnormed + at);
+    }
+    copies_end();
+  };
+#pragma unroll
+  for (int k = 0; k < kBackDepth - 1; ++k) fetch(mine + static_cast<unsigned long long>(k) * step, k);
   float sums[RESIDUAL_SUMS][8] = {};
-  constexpr uint32_t kRows = kThreads / G;
-  for (uint32_t base = blockIdx.x * kRows; base < rows; base += gridDim.x * kRows) {
-    const uint32_t row = base + threadIdx.x / G;
+  int stage = 0;
+  float m_next = mine < rows ? mask_of(a, mine) : 0.f;
+  for (unsigned long long base = blockIdx.x * kRows; base < rows; base += step) {
+    const unsigned long long row = base + threadIdx.x / G;
     const bool on = live && row < rows;
     const size_t at = static_cast<size_t>(row) * a.p.D + c;
-    float x[8], yh[8], g[8], d[8], dn[8];
-    zero8(x), zero8(yh), zero8(g), zero8(d), zero8(dn);
-    float m = 0.f;
-    if (on) {
-      m = mask_of(a, row);
-      load8(static_cast<const T*>(a.dout) + at, d);
-      if (a.dout2) {
-        load8(static_cast<const T*>(a.dout2) + at, x);
+    const float m = on ? m_next : 0.f;
+    if (row + step < rows) m_next = mask_of(a, static_cast<uint32_t>(row + step));
+    fetch(row + (kBackDepth - 1ull) * step, (stage + kBackDepth - 1) % kBackDepth);
+    copies_wait<kBackDepth - 1>();
+    const uint4* const from = own + stage * slots * kThreads;
+    stage = (stage + 1) % kBackDepth;
+    const bool real = on && m != 0.f;  // padding: zeros, whatever the tensors hold
+    float x[8], yh[8], d[8], q[8];
+    take8(from, on, d, T());
+    if (a.dout2) {
+      take8(from + 2 * kSlots<T> * kThreads, on, x, T());
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] += x[e];
-      }
-      zero8(x);
-      if (m != 0.f) {  // padding: zeros, whatever these hold
-        load8(static_cast<const T*>(a.x) + at, x);
-        load8(reinterpret_cast<const bf*>(a.u) + at, yh);
-        if (a.gate) load8(reinterpret_cast<const bf*>(gate_row(a, row)) + c, g);
-        if (pre) load8(reinterpret_cast<const bf*>(a.dnormed) + at, dn);
-      }
+      for (int e = 0; e < 8; ++e) d[e] += x[e];
     }
+    take8(from + kSlots<T> * kThreads, real, x, T());
+    take8(from + at_u * kThreads, real, yh, bf());
     float pr = 0.f;
     if (post) pr = normalise<G>(yh, a.p.post_norm, d_f, inv_d, a.p.eps, live);
     const float k = a.p.scale * m;
-    float y[8], gv[8], gd[8];  // the gate's value and its derivative
+    float y[8], gv[8], gd[8], ch[8];  // the gate's value and its derivative
+    par(3, ch);
+    if (post) {
+      par(1, y), par(0, q);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = post ? yh[e] * pg[e] + pb[e] : yh[e];
-      const float2 sg = sigmoid2(g[e]);
-      gv[e] = !a.gate ? 1.f : a.p.gate_sigmoid ? sg.x : g[e];
-      gd[e] = a.p.gate_sigmoid ? sg.x * sg.y : 1.f;
+      for (int e = 0; e < 8; ++e) y[e] += yh[e] * q[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = yh[e];
+    }
+    if (a.gate) {
+      take8(from + at_g * kThreads, real, q, bf());
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 sg = sigmoid2(q[e]);
+        gv[e] = a.p.gate_sigmoid ? sg.x : q[e];
+        gd[e] = a.p.gate_sigmoid ? sg.x * sg.y : 1.f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gv[e] = gd[e] = 1.f;
     }
     if (pre) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] += k * ch[e] * gv[e] * y[e];
       if (!live) zero8(x);
       const float nr = normalise<G>(x, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
+      float dn[8];
+      take8(from + at_n * kThreads, real, dn, bf());
+      par(2, q);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         sums[2][e] += dn[e] * x[e];
         sums[3][e] += dn[e];
-        dn[e] *= ng[e];
+        dn[e] *= q[e];
       }
       normalise_grad<G>(dn, x, nr, a.p.pre_norm, inv_d);
       if (live) {
@@ -217,29 +336,30 @@ __global__ void __launch_bounds__(kThreads) k8_residual_bwd(ResidualArgs a, uint
         for (int e = 0; e < 8; ++e) d[e] += dn[e];
       }
     }
-    if (on) store8(static_cast<T*>(a.dx) + at, d);
+    if (on) put8(static_cast<T*>(a.dx) + at, d);
     // from here on d is w dX, and a padding pair's is 0
-    float dg[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float kd = m != 0.f ? k * d[e] : 0.f;
+      const float kd = real ? k * d[e] : 0.f;
       const float ky = kd * y[e];
       sums[4][e] += ky * gv[e];
-      dg[e] = ky * ch[e] * gd[e];
+      gd[e] *= ky * ch[e];
       d[e] = kd * ch[e] * gv[e];
       sums[0][e] += d[e] * yh[e];
       sums[1][e] += d[e];
     }
-    if (on && a.dgate) store8(reinterpret_cast<bf*>(a.dgate) + at, dg);
+    if (on && a.dgate) put8(reinterpret_cast<bf*>(a.dgate) + at, gd);
     if (post) {
+      par(0, q);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] *= pg[e];
+      for (int e = 0; e < 8; ++e) d[e] *= q[e];
       normalise_grad<G>(d, yh, pr, a.p.post_norm, inv_d);
     }
-    if (on) store8(reinterpret_cast<bf*>(a.du) + at, d);
+    if (on) put8(reinterpret_cast<bf*>(a.du) + at, d);
   }
   // the block's column sums, its rows added in order
   __shared__ float s[kRows][G * 8 + 1];
+#pragma unroll
   for (int q = 0; q < RESIDUAL_SUMS; ++q) {
     __syncthreads();
 #pragma unroll
@@ -253,14 +373,22 @@ __global__ void __launch_bounds__(kThreads) k8_residual_bwd(ResidualArgs a, uint
   }
 }
 
-// The blocks' column sums added in order.
+// The blocks' column sums: 32 columns a block, eight groups of parts side by side.
 __global__ void __launch_bounds__(256)
     k8_residual_sum(const float* __restrict__ part, trimul_residual_grads g, int D, int blocks) {
-  float* const out[RESIDUAL_SUMS] = {g.post_gamma, g.post_beta, g.pre_gamma, g.pre_beta, g.channel};
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= RESIDUAL_SUMS * D || !out[n / D]) return;
+  __shared__ float s[8][32];
+  const int n = blockIdx.x * 32 + threadIdx.x % 32, k0 = threadIdx.x / 32;
   float t = 0.f;
-  for (int k = 0; k < blocks; ++k) t += part[static_cast<size_t>(k) * RESIDUAL_SUMS * D + n];
+  if (n < RESIDUAL_SUMS * D) {
+#pragma unroll 8
+    for (int k = k0; k < blocks; k += 8) t += part[static_cast<size_t>(k) * RESIDUAL_SUMS * D + n];
+  }
+  s[k0][threadIdx.x % 32] = t;
+  __syncthreads();
+  float* const out[RESIDUAL_SUMS] = {g.post_gamma, g.post_beta, g.pre_gamma, g.pre_beta, g.channel};
+  if (k0 != 0 || n >= RESIDUAL_SUMS * D || !out[n / D]) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) t += s[k][threadIdx.x];
   out[n / D][n % D] = t;
 }
 
@@ -275,35 +403,45 @@ int blocks_for(int D, long long rows, int num_sms, int per_sm) {
   return static_cast<int>(std::min<long long>((rows + per_block - 1) / per_block, static_cast<long long>(per_sm) * num_sms));
 }
 
-template <typename T, int G>
-void forward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
-  k8_residual_fwd<T, G><<<blocks_for(a.p.D, rows, num_sms, 4), kThreads, 0, s>>>(a, rows);
+template <typename K>
+cudaError_t launch(K kernel, const ResidualArgs& a, uint32_t rows, int grid, int smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, smem, s>>>(a, rows);
+  return cudaGetLastError();
 }
 template <typename T, int G>
-void backward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
-  k8_residual_bwd<T, G><<<blocks_for(a.p.D, rows, num_sms, 2), kThreads, 0, s>>>(a, rows);
+cudaError_t forward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
+  return launch(k8_residual_fwd<T, G>, a, rows, blocks_for(a.p.D, rows, num_sms, 3),
+                kDepth * forward_slots<T>(a.gate) * kThreads * 16, s);
+}
+template <typename T, int G>
+cudaError_t backward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
+  return launch(k8_residual_bwd<T, G>, a, rows, blocks_for(a.p.D, rows, num_sms, 2),
+                kBackDepth * backward_slots<T>(a.gate, a.dout2, a.p.pre_norm != TRIMUL_NORM_NONE) * kThreads * 16, s);
 }
 
 #define BY_LANES(FN, T)                                                  \
   switch (lanes_of(a.p.D)) {                                             \
-    case 1: FN<T, 1>(a, rows, num_sms, s); break;                        \
-    case 2: FN<T, 2>(a, rows, num_sms, s); break;                        \
-    case 4: FN<T, 4>(a, rows, num_sms, s); break;                        \
-    case 8: FN<T, 8>(a, rows, num_sms, s); break;                        \
-    case 16: FN<T, 16>(a, rows, num_sms, s); break;                      \
-    default: FN<T, 32>(a, rows, num_sms, s); break;                      \
+    case 1: e = FN<T, 1>(a, rows, num_sms, s); break;                        \
+    case 2: e = FN<T, 2>(a, rows, num_sms, s); break;                        \
+    case 4: e = FN<T, 4>(a, rows, num_sms, s); break;                        \
+    case 8: e = FN<T, 8>(a, rows, num_sms, s); break;                        \
+    case 16: e = FN<T, 16>(a, rows, num_sms, s); break;                      \
+    default: e = FN<T, 32>(a, rows, num_sms, s); break;                      \
   }
 
 }  // namespace
 
 cudaError_t launch_residual_forward(const ResidualArgs& a, int num_sms, cudaStream_t s) {
   const uint32_t rows = static_cast<uint32_t>(a.B) * a.I * a.J;
+  cudaError_t e = cudaSuccess;
   if (a.p.stream_type == TRIMUL_F32) {
     BY_LANES(forward, float)
   } else {
     BY_LANES(forward, bf)
   }
-  return cudaGetLastError();
+  return e;
 }
 
 size_t residual_backward_workspace(int D, long long rows, int num_sms) {
@@ -312,15 +450,15 @@ size_t residual_backward_workspace(int D, long long rows, int num_sms) {
 
 cudaError_t launch_residual_backward(const ResidualArgs& a, int num_sms, cudaStream_t s) {
   const uint32_t rows = static_cast<uint32_t>(a.B) * a.I * a.J;
+  cudaError_t e = cudaSuccess;
   if (a.p.stream_type == TRIMUL_F32) {
     BY_LANES(backward, float)
   } else {
     BY_LANES(backward, bf)
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int n = RESIDUAL_SUMS * a.p.D;
-  k8_residual_sum<<<(n + 255) / 256, 256, 0, s>>>(a.part, a.g, a.p.D, blocks_for(a.p.D, rows, num_sms, 2));
+  k8_residual_sum<<<(n + 31) / 32, 256, 0, s>>>(a.part, a.g, a.p.D, blocks_for(a.p.D, rows, num_sms, 2));
   return cudaGetLastError();
 }
 
