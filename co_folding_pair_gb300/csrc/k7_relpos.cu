@@ -3,8 +3,8 @@
 //   out[b,i,j,:] = base[b,i,j,:] + table[bucket(q_pos[b,i] - k_pos[b,j])]
 //   dtable[n,:]  = sum of dout[b,i,j,:] over the pairs of bucket n
 //
-// The bucket of every distance within [-M, M] is a table of 16-bit numbers
-// made when the plan is made; farther distances have the bucket of -M or M.
+// Distances are clipped to [-M, M] (one-sided: [0, M]); LINEAR buckets are that,
+// LOG buckets a table of 16-bit numbers over it, made when the plan is made.
 // Both directions are one pass over B I J D elements (the forward writes them,
 // and reads them if there is a base; the gradient reads them), so both are
 // bound by memory.
@@ -42,6 +42,9 @@ template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int n = 8;
   static __device__ __forceinline__ void unpack(const uint4 v, float (&f)[8]) { unpack8(v, f); }
+  static __device__ __forceinline__ void unpack(const uint4 v, f2 (&f)[4]) {
+    f[0] = unpack_bf162(v.x), f[1] = unpack_bf162(v.y), f[2] = unpack_bf162(v.z), f[3] = unpack_bf162(v.w);
+  }
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) { return pack8(f); }
 };
 template <>
@@ -49,6 +52,9 @@ struct Vec<float> {
   static constexpr int n = 4;
   static __device__ __forceinline__ void unpack(const uint4 v, float (&f)[4]) {
     f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ void unpack(const uint4 v, f2 (&f)[2]) {
+    f[0] = pair2(__uint_as_float(v.x), __uint_as_float(v.y)), f[1] = pair2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
   static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
@@ -187,7 +193,7 @@ constexpr int kSteps = 8;
 
 template <typename T, int G>
 __global__ void __launch_bounds__(512)
-    k7_relpos_grad_pair(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs, int slice) {
+    k7_relpos_grad_pair(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs, int slice, int S) {
   constexpr int V = Vec<T>::n, W = G * V, P = 32 / G, kBatch = P * kSteps, kPerLane = (kBatch + 31) / 32;
   extern __shared__ float4 smem4[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
@@ -195,8 +201,8 @@ __global__ void __launch_bounds__(512)
   float* const sums = reinterpret_cast<float*>(smem4) + static_cast<size_t>(warp) * a.rows * W;
   for (int n = lane; n < a.rows * W / 4; n += 32) reinterpret_cast<float4*>(sums)[n] = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncwarp();
-  // this block's channels, and its range of batches
-  const int c0 = blockIdx.y * slice, width = min(slice, a.D - c0);
+  // this warp's channels, and its block's range of batches
+  const int c0 = (blockIdx.y * S + warp % S) * slice, width = min(slice, a.D - c0);
   const bool live = c < width;
   const uint32_t batches = (pairs + kBatch - 1) / kBatch;
   const uint32_t b0 = static_cast<uint32_t>(static_cast<unsigned long long>(batches) * blockIdx.x / gridDim.x);
@@ -225,18 +231,17 @@ __global__ void __launch_bounds__(512)
   };
 
   int at = -1;  // the bucket of this slot's run
-  float run[V] = {};
+  f2 run[V / 2] = {};
   // the runs of the slots whose `end` is set go to shared memory; slots that
   // share a bucket take turns
   auto flush = [&](bool end) {
     const unsigned same = __match_any_sync(0xffffffffu, end ? at : -1 - slot);
-    float4* const to = reinterpret_cast<float4*>(sums + at * W + c);
+    ulonglong2* const to = reinterpret_cast<ulonglong2*>(sums + at * W + c);
     auto add = [&] {
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
-        float4 t = to[q];
-        t.x += run[4 * q], t.y += run[4 * q + 1], t.z += run[4 * q + 2], t.w += run[4 * q + 3];
-        to[q] = t;
+        const ulonglong2 t = to[q];
+        to[q] = make_ulonglong2(add2(t.x, run[2 * q]), add2(t.y, run[2 * q + 1]));
       }
     };
     if (__all_sync(0xffffffffu, __popc(same) <= G)) {
@@ -251,31 +256,33 @@ __global__ void __launch_bounds__(512)
     }
   };
 
-  uint32_t batch = b0 + warp;
+  const int streams = warps / S;
+  uint32_t batch = b0 + warp / S;
   if (batch < b1) load(batch);
-  for (; batch < b1; batch += warps) {
+  for (; batch < b1; batch += streams) {
     uint4 now[kSteps];
     int k_of[kPerLane];
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) now[u] = next[u];
 #pragma unroll
     for (int q = 0; q < kPerLane; ++q) k_of[q] = next_k[q];
-    if (batch + warps < b1) load(batch + warps);
+    if (batch + streams < b1) load(batch + streams);
 
     const int k0 = __shfl_sync(0xffffffffu, at, 0);
     bool one = at == k0 && k0 >= 0;  // the whole batch goes on with the run of all slots
 #pragma unroll
     for (int q = 0; q < kPerLane; ++q) one = one && (k_of[q] == k0 || q * 32 + lane >= kBatch);
     if (__all_sync(0xffffffffu, one)) {
-      float t[V] = {}, v[V];
+      f2 t[V / 2], v[V / 2];
+      Vec<T>::unpack(now[0], t);
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
+      for (int u = 1; u < kSteps; ++u) {
         Vec<T>::unpack(now[u], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) t[e] += v[e];
+        for (int e = 0; e < V / 2; ++e) t[e] = add2(t[e], v[e]);
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) run[e] += t[e];
+      for (int e = 0; e < V / 2; ++e) run[e] = add2(run[e], t[e]);
       continue;
     }
 #pragma unroll
@@ -284,10 +291,10 @@ __global__ void __launch_bounds__(512)
       const bool end = k >= 0 && at >= 0 && k != at;
       if (__any_sync(0xffffffffu, end)) flush(end);
       if (k >= 0) {
-        float v[V];
+        f2 v[V / 2];
         Vec<T>::unpack(now[u], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) run[e] = (k == at ? run[e] : 0.f) + v[e];
+        for (int e = 0; e < V / 2; ++e) run[e] = k == at ? add2(run[e], v[e]) : v[e];
         at = k;
       }
     }
@@ -295,13 +302,14 @@ __global__ void __launch_bounds__(512)
   flush(at >= 0);
   __syncthreads();
   const float* const all = reinterpret_cast<const float*>(smem4);
-  float* const out = part + static_cast<size_t>(blockIdx.x) * a.rows * a.D + c0;
-  for (int n = threadIdx.x; n < a.rows * W; n += blockDim.x) {
-    const int r = n / W, w = n % W;
-    if (w >= width) continue;
+  float* const out = part + static_cast<size_t>(blockIdx.x) * a.rows * a.D;
+  for (int n = threadIdx.x; n < a.rows * W * S; n += blockDim.x) {
+    const int q = n / (a.rows * W), i = n - q * a.rows * W, r = i / W, w = i % W;
+    const int from = (blockIdx.y * S + q) * slice;
+    if (w >= min(slice, a.D - from)) continue;
     float t = 0.f;
-    for (int k = 0; k < warps; ++k) t += all[static_cast<size_t>(k) * a.rows * W + n];
-    out[static_cast<size_t>(r) * a.D + w] = t;
+    for (int k = 0; k < streams; ++k) t += all[static_cast<size_t>(k * S + q) * a.rows * W + i];
+    out[static_cast<size_t>(r) * a.D + from + w] = t;
   }
 }
 
@@ -447,6 +455,7 @@ __global__ void __launch_bounds__(256)
 // How a gradient is split over blocks.
 struct GradSplit {
   int warps, lanes, slice, slices, ranges, smem;
+  int S;  // PAIR: slices of a block
 };
 
 // PAIR: at least eight warps' sums have to fit an SM's shared memory for
@@ -464,9 +473,19 @@ GradSplit split_pair(int rows, long long pairs, int D, int num_sms) {
   g.slice = (groups + g.slices - 1) / g.slices * V;
   g.slices = (D + g.slice - 1) / g.slice;
   g.warps = std::min(16, kSumBytes / (rows * W * 4));
-  g.smem = g.warps * rows * W * 4;
+  g.S = 1;
   const long long batches = (pairs + 32 / g.lanes * kSteps - 1) / (32 / g.lanes * kSteps);
-  g.ranges = static_cast<int>(std::max<long long>(1, std::min<long long>((batches + g.warps - 1) / g.warps, num_sms / g.slices)));
+  // One block for all of a pair's slices reads whole rows, which DRAM serves
+  // better, but writes sums of all channels a block: worth it once a warp has
+  // some sixteen batches (2048^2 x 256: 479 us against 559; 256^2 x 128, with
+  // two batches a warp: 19.2 against 16.3).
+  if (g.slices <= g.warps && batches >= 16ll * (g.warps / g.slices) * num_sms) {
+    g.S = g.slices;
+    g.slices = 1;
+    g.warps = g.warps / g.S * g.S;
+  }
+  g.smem = g.warps * rows * W * 4;
+  g.ranges = static_cast<int>(std::max<long long>(1, std::min<long long>((batches + g.warps / g.S - 1) / (g.warps / g.S), num_sms / g.slices)));
   return g;
 }
 
@@ -530,7 +549,7 @@ cudaError_t grad_pair(const RelposArgs& a, const T* dout, const GradSplit& g, fl
   cudaError_t e = cudaFuncSetAttribute(k7_relpos_grad_pair<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSumBytes);
   if (e != cudaSuccess) return e;
   k7_relpos_grad_pair<T, G><<<dim3(g.ranges, g.slices), g.warps * 32, g.smem, s>>>(
-      a, dout, ws, static_cast<uint32_t>(a.B) * a.I * a.J, g.slice);
+      a, dout, ws, static_cast<uint32_t>(a.B) * a.I * a.J, g.slice, g.S);
   return cudaGetLastError();
 }
 

@@ -34,49 +34,41 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float sum8(const float (&v)[8]) {
-  return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-}
-
 // v -> its normalised value; returns r.  Lanes past D hold and keep zeros.
 // The mean is a true division: a row of one value has that value as its mean
 // exactly, and the product with 1 / D, off by half an ulp of the mean, would be
 // scaled by 1 / sqrt(eps) there.
 template <int G>
-__device__ __forceinline__ float normalise(float (&v)[8], int kind, float d, float inv_d, float eps, bool live) {
+__device__ __forceinline__ float normalise(F8& v, int kind, float d, float inv_d, float eps, bool live) {
   if (kind == TRIMUL_NORM_LAYER) {
-    const float mean = row_sum<G>(sum8(v)) / d;
+    const float mean = row_sum<G>(sum_of(v)) / d;
+    const f2 shift = both(live ? -mean : 0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = live ? v[e] - mean : 0.f;
+    for (int e = 0; e < 4; ++e) v.v[e] = add2(v.v[e], shift);
   }
-  float q[8];
+  const float r = rsqrtf(row_sum<G>(dot_of(v, v)) * inv_d + eps);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = v[e] * v[e];
-  const float r = rsqrtf(row_sum<G>(sum8(q)) * inv_d + eps);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] *= r;
+  for (int e = 0; e < 4; ++e) v.v[e] = mul2(v.v[e], both(r));
   return r;
 }
 
 // t (the gradient at the normalised value) -> the gradient at the norm's input.
 template <int G>
-__device__ __forceinline__ void normalise_grad(float (&t)[8], const float (&hat)[8], float r, int kind, float inv_d) {
-  float q[8];
+__device__ __forceinline__ void normalise_grad(F8& t, const F8& hat, float r, int kind, float inv_d) {
+  const float m2 = row_sum<G>(dot_of(t, hat)) * (-r * inv_d);
+  const float m1 = kind == TRIMUL_NORM_LAYER ? row_sum<G>(sum_of(t)) * (-r * inv_d) : 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = t[e] * hat[e];
-  const float m2 = row_sum<G>(sum8(q)) * inv_d;
-  const float m1 = kind == TRIMUL_NORM_LAYER ? row_sum<G>(sum8(t)) * inv_d : 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) t[e] = r * (t[e] - m1 - hat[e] * m2);
+  for (int e = 0; e < 4; ++e) t.v[e] = fma2(t.v[e], both(r), fma2(hat.v[e], both(m2), both(m1)));
 }
 
 // Eight of a parameter's values, or the value it has where it is absent.
-__device__ __forceinline__ void param8(const float* p, int c, bool live, float absent, float (&f)[8]) {
+__device__ __forceinline__ void param8(const float* p, int c, bool live, float absent, F8& f) {
   if (p && live) {
-    load8(p + c, f);
+    const float4 a = reinterpret_cast<const float4*>(p + c)[0], b = reinterpret_cast<const float4*>(p + c)[1];
+    f.v[0] = pair2(a.x, a.y), f.v[1] = pair2(a.z, a.w), f.v[2] = pair2(b.x, b.y), f.v[3] = pair2(b.z, b.w);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = absent;
+    for (int e = 0; e < 4; ++e) f.v[e] = both(absent);
   }
 }
 
@@ -102,26 +94,51 @@ __device__ __forceinline__ void copy8(uint4* to, const float* from) {
   copy16(to, from);
   copy16(to + kThreads, from + 4);
 }
-__device__ __forceinline__ void take8(const uint4* from, bool on, float (&f)[8], __nv_bfloat16) {
-  unpack8(on ? from[0] : make_uint4(0u, 0u, 0u, 0u), f);
+__device__ __forceinline__ F8 widen8(const uint4 v) {
+  return F8{{unpack_bf162(v.x), unpack_bf162(v.y), unpack_bf162(v.z), unpack_bf162(v.w)}};
 }
-__device__ __forceinline__ void take8(const uint4* from, bool on, float (&f)[8], float) {
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u), a = on ? from[0] : z, b = on ? from[kThreads] : z;
-  f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
-  f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
+__device__ __forceinline__ F8 take8(const uint4* from, bool on, __nv_bfloat16) {
+  return widen8(on ? from[0] : make_uint4(0u, 0u, 0u, 0u));
+}
+__device__ __forceinline__ F8 take8(const uint4* from, bool on, float) {
+  const ulonglong2 z = make_ulonglong2(0, 0);
+  const ulonglong2 a = on ? reinterpret_cast<const ulonglong2*>(from)[0] : z;
+  const ulonglong2 b = on ? reinterpret_cast<const ulonglong2*>(from)[kThreads] : z;
+  return F8{{a.x, a.y, b.x, b.y}};
 }
 // Streaming stores: what is written is not read again here.
-__device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&f)[8]) { __stcs(reinterpret_cast<uint4*>(p), pack8(f)); }
-__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const F8& f) {
+  __stcs(reinterpret_cast<uint4*>(p),
+         make_uint4(pack_bf162(f.v[0]), pack_bf162(f.v[1]), pack_bf162(f.v[2]), pack_bf162(f.v[3])));
+}
+__device__ __forceinline__ void put8(float* p, const F8& f) {
+  const float2 a = split2(f.v[0]), b = split2(f.v[1]), c = split2(f.v[2]), d = split2(f.v[3]);
+  __stcs(reinterpret_cast<float4*>(p), make_float4(a.x, a.y, b.x, b.y));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(c.x, c.y, d.x, d.y));
 }
 
+// 1 / x for x in [1, 2], to 1 ulp (the approximate instruction).
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // sigmoid(x) and 1 - sigmoid(x), each to fp32's relative precision (the
 // exponential's argument is never positive, so nothing overflows either).
 __device__ __forceinline__ float2 sigmoid2(float x) {
-  const float e = __expf(-fabsf(x)), big = __frcp_rn(1.0f + e);
-  return x >= 0.f ? make_float2(big, e * big) : make_float2(e * big, big);
+  const float e = __expf(-fabsf(x)), big = reciprocal(1.0f + e), small = e * big;
+  return x >= 0.f ? make_float2(big, small) : make_float2(small, big);
+}
+// The gate's values, in place; returns their derivatives.
+__device__ __forceinline__ F8 sigmoid8(F8& g) {
+  F8 d;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 x = split2(g.v[e]), a = sigmoid2(x.x), b = sigmoid2(x.y);
+    g.v[e] = pair2(a.x, b.x);
+    d.v[e] = pair2(a.x * a.y, b.x * b.y);
+  }
+  return d;
 }
 
 // The gate's eight values of a row (pair), as they are.
@@ -137,11 +154,6 @@ using bf = __nv_bfloat16;
 
 __device__ __forceinline__ float mask_of(const ResidualArgs& a, uint32_t pair) {
   return a.mask ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.mask)[pair]) : 1.f;
-}
-
-__device__ __forceinline__ void zero8(float (&f)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = 0.f;
 }
 
 template <typename T>
@@ -166,14 +178,18 @@ __global__ void __launch_bounds__(kThreads, 3) k8_residual_fwd(ResidualArgs a, u
   const bool live = c < a.p.D;
   const float d_f = static_cast<float>(a.p.D), inv_d = 1.0f / d_f;
   // scale channel (gamma y^ + beta) = A y^ + B
-  float A[8], B[8], ng[8], nb[8];
+  F8 A, B, ng, nb;
   {
-    float ch[8];
+    F8 ch;
     param8(a.p.post_gamma, c, live, 1.f, A);
     param8(a.p.post_beta, c, live, 0.f, B);
     param8(a.p.channel, c, live, 1.f, ch);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) A[e] *= a.p.scale * ch[e], B[e] *= a.p.scale * ch[e];
+    for (int e = 0; e < 4; ++e) {
+      ch.v[e] = mul2(ch.v[e], both(a.p.scale));
+      A.v[e] = mul2(A.v[e], ch.v[e]);
+      B.v[e] = mul2(B.v[e], ch.v[e]);
+    }
   }
   param8(a.p.pre_gamma, c, live, 1.f, ng);
   param8(a.p.pre_beta, c, live, 0.f, nb);
@@ -206,23 +222,29 @@ __global__ void __launch_bounds__(kThreads, 3) k8_residual_fwd(ResidualArgs a, u
     copies_wait<kDepth - 1>();
     const uint4* const from = own + stage * slots * kThreads;
     stage = (stage + 1) % kDepth;
-    float x[8], y[8], g[8];
-    take8(from, on, x, T());
-    take8(from + kSlots<T> * kThreads, on, y, bf());
-    if (a.gate) take8(from + (kSlots<T> + 1) * kThreads, on, g, bf());
+    F8 x = take8(from, on, T()), y = take8(from + kSlots<T> * kThreads, on, bf());
     if (a.p.post_norm != TRIMUL_NORM_NONE) normalise<G>(y, a.p.post_norm, d_f, inv_d, a.p.eps, live);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float w = m;
-      if (a.gate) w *= a.p.gate_sigmoid ? sigmoid2(g[e]).x : g[e];
-      if (m != 0.f) x[e] += w * (y[e] * A[e] + B[e]);
+    for (int e = 0; e < 4; ++e) y.v[e] = fma2(y.v[e], A.v[e], B.v[e]);
+    if (a.gate) {
+      F8 g = take8(from + (kSlots<T> + 1) * kThreads, on, bf());
+      if (a.p.gate_sigmoid) sigmoid8(g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y.v[e] = mul2(y.v[e], g.v[e]);
+    }
+    if (m != 0.f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.v[e] = fma2(y.v[e], both(m), x.v[e]);
     }
     if (on) put8(static_cast<T*>(a.out) + at, x);
     if (a.normed) {
-      if (!live) zero8(x);
       normalise<G>(x, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
+      if (m != 0.f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = m != 0.f ? x[e] * ng[e] + nb[e] : 0.f;
+        for (int e = 0; e < 4; ++e) x.v[e] = fma2(x.v[e], ng.v[e], nb.v[e]);
+      } else {
+        x = F8{};
+      }
       if (on) put8(reinterpret_cast<bf*>(a.normed) + at, x);
     }
   }
@@ -234,7 +256,8 @@ constexpr int kBackDepth = 2;
 template <typename T, int G>
 __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, uint32_t rows) {
   extern __shared__ uint4 ring[];
-  __shared__ float4 par4[4][64];  // post_gamma, post_beta, pre_gamma, channel
+  // post_gamma, post_beta, pre_gamma, channel: the low and the high four of each lane's eight
+  __shared__ float4 par4[4][2][32];
   constexpr uint32_t kRows = kThreads / G;
   const int c = (threadIdx.x % G) * 8;
   const bool live = c < a.p.D;
@@ -244,11 +267,15 @@ __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, u
     const float* const from[4] = {a.p.post_gamma, a.p.post_beta, a.p.pre_gamma, a.p.channel};
     for (int n = threadIdx.x; n < 4 * 256; n += kThreads) {
       const int q = n / 256, e = n % 256;
-      reinterpret_cast<float*>(par4[q])[e] = e < a.p.D && from[q] ? from[q][e] : q == 1 ? 0.f : 1.f;
+      reinterpret_cast<float*>(&par4[q][e / 4 % 2][e / 8])[e % 4] = e < a.p.D && from[q] ? from[q][e] : q == 1 ? 0.f : 1.f;
     }
     __syncthreads();
   }
-  auto par = [&](int q, float (&f)[8]) { load8(reinterpret_cast<const float*>(par4[q]) + c, f); };
+  auto par = [&](int q) {
+    const ulonglong2 lo = reinterpret_cast<const ulonglong2&>(par4[q][0][c / 8]);
+    const ulonglong2 hi = reinterpret_cast<const ulonglong2&>(par4[q][1][c / 8]);
+    return F8{{lo.x, lo.y, hi.x, hi.y}};
+  };
   const int slots = backward_slots<T>(a.gate, a.dout2, pre);
   const int at_u = kSlots<T> * (a.dout2 ? 3 : 2), at_g = at_u + 1, at_n = at_g + (a.gate ? 1 : 0);
   const uint32_t step = gridDim.x * kRows, mine = blockIdx.x * kRows + threadIdx.x / G;
@@ -258,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, u
       const size_t at = static_cast<size_t>(row) * a.p.D + c;
       uint4* const to = own + stage * slots * kThreads;
       copy8(to, static_cast<const T*>(a.dout) + at);
-      copy8(to + kSlots<T> * kThreads, static_cast<const T*>(a.x) + at);
+      if (pre) copy8(to + kSlots<T> * kThreads, static_cast<const T*>(a.x) + at);  // only X's statistics need x
       if (a.dout2) copy8(to + 2 * kSlots<T> * kThreads, static_cast<const T*>(a.dout2) + at);
       copy16(to + at_u * kThreads, a.u + at);
       if (a.gate) copy16(to + at_g * kThreads, gate_row(a, static_cast<uint32_t>(row)) + c);
@@ -268,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, u
   };
 #pragma unroll
   for (int k = 0; k < kBackDepth - 1; ++k) fetch(mine + static_cast<unsigned long long>(k) * step, k);
-  float sums[RESIDUAL_SUMS][8] = {};
+  F8 sums[RESIDUAL_SUMS] = {};
   int stage = 0;
   float m_next = mine < rows ? mask_of(a, mine) : 0.f;
   for (unsigned long long base = blockIdx.x * kRows; base < rows; base += step) {
@@ -282,77 +309,74 @@ __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, u
     const uint4* const from = own + stage * slots * kThreads;
     stage = (stage + 1) % kBackDepth;
     const bool real = on && m != 0.f;  // padding: zeros, whatever the tensors hold
-    float x[8], yh[8], d[8], q[8];
-    take8(from, on, d, T());
+    F8 d = take8(from, on, T());
     if (a.dout2) {
-      take8(from + 2 * kSlots<T> * kThreads, on, x, T());
+      const F8 t = take8(from + 2 * kSlots<T> * kThreads, on, T());
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] += x[e];
+      for (int e = 0; e < 4; ++e) d.v[e] = add2(d.v[e], t.v[e]);
     }
-    take8(from + kSlots<T> * kThreads, real, x, T());
-    take8(from + at_u * kThreads, real, yh, bf());
+    F8 yh = take8(from + at_u * kThreads, real, bf());
     float pr = 0.f;
     if (post) pr = normalise<G>(yh, a.p.post_norm, d_f, inv_d, a.p.eps, live);
-    const float k = a.p.scale * m;
-    float y[8], gv[8], gd[8], ch[8];  // the gate's value and its derivative
-    par(3, ch);
-    if (post) {
-      par(1, y), par(0, q);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] += yh[e] * q[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = yh[e];
-    }
+    F8 gv, gd;  // scale mask times the gate's value, and times its derivative
+    const f2 k = both(a.p.scale * m);
     if (a.gate) {
-      take8(from + at_g * kThreads, real, q, bf());
+      gv = take8(from + at_g * kThreads, real, bf());
+      if (a.p.gate_sigmoid) {
+        gd = sigmoid8(gv);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 sg = sigmoid2(q[e]);
-        gv[e] = a.p.gate_sigmoid ? sg.x : q[e];
-        gd[e] = a.p.gate_sigmoid ? sg.x * sg.y : 1.f;
+        for (int e = 0; e < 4; ++e) gd.v[e] = mul2(gd.v[e], k);
+      } else {
+        gd = F8{{k, k, k, k}};
       }
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) gv[e] = gd[e] = 1.f;
+      for (int e = 0; e < 4; ++e) gv.v[e] = mul2(gv.v[e], k);
+    } else {
+      gv = F8{{k, k, k, k}};
     }
     if (pre) {
+      F8 x = take8(from + kSlots<T> * kThreads, real, T());
+      const F8 pg = par(0), pb = par(1), ch = par(3), ng = par(2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] += k * ch[e] * gv[e] * y[e];
-      if (!live) zero8(x);
+      for (int e = 0; e < 4; ++e) {
+        const f2 y = post ? fma2(yh.v[e], pg.v[e], pb.v[e]) : yh.v[e];
+        x.v[e] = fma2(mul2(gv.v[e], ch.v[e]), y, x.v[e]);
+      }
       const float nr = normalise<G>(x, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
-      float dn[8];
-      take8(from + at_n * kThreads, real, dn, bf());
-      par(2, q);
+      F8 dn = take8(from + at_n * kThreads, real, bf());
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sums[2][e] += dn[e] * x[e];
-        sums[3][e] += dn[e];
-        dn[e] *= q[e];
+      for (int e = 0; e < 4; ++e) {
+        sums[2].v[e] = fma2(dn.v[e], x.v[e], sums[2].v[e]);
+        sums[3].v[e] = add2(dn.v[e], sums[3].v[e]);
+        dn.v[e] = mul2(dn.v[e], ng.v[e]);
       }
       normalise_grad<G>(dn, x, nr, a.p.pre_norm, inv_d);
-      if (live) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] += dn[e];
-      }
+      for (int e = 0; e < 4; ++e) d.v[e] = add2(d.v[e], dn.v[e]);
     }
     if (on) put8(static_cast<T*>(a.dx) + at, d);
-    // from here on d is w dX, and a padding pair's is 0
+    if (!real) d = F8{};  // a padding pair passes nothing on to what follows
+    const F8 pg = par(0), ch = par(3);
+    if (a.dgate || a.g.channel) {
+      const F8 pb = par(1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float kd = real ? k * d[e] : 0.f;
-      const float ky = kd * y[e];
-      sums[4][e] += ky * gv[e];
-      gd[e] *= ky * ch[e];
-      d[e] = kd * ch[e] * gv[e];
-      sums[0][e] += d[e] * yh[e];
-      sums[1][e] += d[e];
+      for (int e = 0; e < 4; ++e) {
+        const f2 y = post ? fma2(yh.v[e], pg.v[e], pb.v[e]) : yh.v[e];
+        const f2 dy = mul2(d.v[e], y);
+        sums[4].v[e] = fma2(dy, gv.v[e], sums[4].v[e]);
+        if (a.dgate) gd.v[e] = mul2(gd.v[e], mul2(dy, ch.v[e]));
+      }
+      if (on && a.dgate) put8(reinterpret_cast<bf*>(a.dgate) + at, gd);
     }
-    if (on && a.dgate) put8(reinterpret_cast<bf*>(a.dgate) + at, gd);
-    if (post) {
-      par(0, q);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] *= q[e];
+    for (int e = 0; e < 4; ++e) d.v[e] = mul2(d.v[e], mul2(gv.v[e], ch.v[e]));
+    if (post) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sums[0].v[e] = fma2(d.v[e], yh.v[e], sums[0].v[e]);
+        sums[1].v[e] = add2(d.v[e], sums[1].v[e]);
+        d.v[e] = mul2(d.v[e], pg.v[e]);
+      }
       normalise_grad<G>(d, yh, pr, a.p.post_norm, inv_d);
     }
     if (on) put8(reinterpret_cast<bf*>(a.du) + at, d);
@@ -363,7 +387,10 @@ __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, u
   for (int q = 0; q < RESIDUAL_SUMS; ++q) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[threadIdx.x / G][c + e] = sums[q][e];
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = split2(sums[q].v[e]);
+      s[threadIdx.x / G][c + 2 * e] = t.x, s[threadIdx.x / G][c + 2 * e + 1] = t.y;
+    }
     __syncthreads();
     for (int n = threadIdx.x; n < a.p.D; n += kThreads) {
       float t = 0.f;

@@ -39,6 +39,53 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
+// Two fp32 numbers in a register pair: the packed instructions do both with one
+// issue, which is what the row-wise kernels run short of.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 both(float v) { return pair2(v, v); }
+__device__ __forceinline__ float2 split2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Eight numbers, as pairs.
+struct F8 {
+  f2 v[4];
+};
+__device__ __forceinline__ f2 unpack_bf162(uint32_t w) { return pair2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t pack_bf162(f2 v) {
+  const float2 f = split2(v);
+  return pack_bf162(f.x, f.y);
+}
+__device__ __forceinline__ float sum_of(const F8& a) {
+  const float2 t = split2(add2(add2(a.v[0], a.v[1]), add2(a.v[2], a.v[3])));
+  return t.x + t.y;
+}
+__device__ __forceinline__ float dot_of(const F8& a, const F8& b) {
+  const float2 t = split2(fma2(a.v[3], b.v[3], fma2(a.v[2], b.v[2], fma2(a.v[1], b.v[1], mul2(a.v[0], b.v[0])))));
+  return t.x + t.y;
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -65,9 +112,9 @@ __device__ __forceinline__ int relpos_bucket(const RelposArgs& a, uint32_t qi, u
     if ((gq | gk) < 0) return -1;
     if (gq != gk) return a.rows - 1;
   }
-  long long d = static_cast<long long>(a.q_pos[qi]) - a.k_pos[kj];
-  d = d < -a.M ? -a.M : d > a.M ? a.M : d;
-  return a.lut[d + a.M];
+  const long long far = static_cast<long long>(a.q_pos[qi]) - a.k_pos[kj];
+  const int d = static_cast<int>(far < a.lo ? a.lo : far > a.M ? a.M : far) - a.lo;
+  return a.lut ? a.lut[d] : d;
 }
 
 }  // namespace trimul

@@ -36,8 +36,8 @@ constexpr int kRelposMaxDistance = 32768;
 constexpr int kRelposMaxRows = 1024;
 
 struct RelposArgs {
-  const int16_t* lut;  // [2M + 1]: the bucket of d + M, |d| <= M (farther distances have M's)
-  int M, rows;         // rows: of the table, the one for different groups (the last) among them
+  const int16_t* lut;  // [M - lo + 1]: the bucket of distance d, lo <= d <= M, at d - lo; null: d - lo itself
+  int lo, M, rows;     // distances below lo have lo's bucket; rows: of the table, the one for different groups (the last) among them
   const int32_t *q_pos, *k_pos, *q_group, *k_group;  // groups: both null, or neither
   int B, I, J, D;
   FastDiv by_I, by_J;

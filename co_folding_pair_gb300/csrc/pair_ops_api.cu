@@ -16,7 +16,7 @@ using namespace trimul;
 
 struct trimul_relpos_s {
   int device = 0;
-  int M = 0, rows = 0;
+  int lo = 0, M = 0, rows = 0;  // as in RelposArgs
   bool groups = false;
   int num_sms = 0;
   int16_t* lut = nullptr;
@@ -177,6 +177,7 @@ RelposArgs relpos_args(trimul_relpos r, const int32_t* q_pos, const int32_t* k_p
                        const int32_t* k_group, int B, int I, int J, int D) {
   RelposArgs a{};
   a.lut = r->lut;
+  a.lo = r->lo;
   a.M = r->M;
   a.rows = r->rows;
   a.q_pos = q_pos, a.k_pos = k_pos, a.q_group = q_group, a.k_group = k_group;
@@ -308,23 +309,23 @@ trimul_status trimul_relpos_create(trimul_relpos* out, const trimul_relpos_param
   TRY(device_sms(device, &sms));
   trimul_relpos r = nullptr;
   try {
-    std::vector<int16_t> lut(2 * M + 1);
-    if (p->kind == TRIMUL_BUCKETS_LINEAR) {
-      for (int d = -M; d <= M; ++d) lut[d + M] = static_cast<int16_t>(p->bidirectional ? d + M : d > 0 ? d : 0);
-    } else {
+    const int lo = p->bidirectional ? -M : 0;
+    std::vector<int16_t> lut;
+    if (p->kind == TRIMUL_BUCKETS_LOG) {
       const std::vector<int16_t> b = log_buckets(K, M);
-      for (int d = -M; d <= M; ++d)
-        lut[d + M] = d >= 0 ? b[d] : p->bidirectional ? static_cast<int16_t>(K + b[-d]) : b[0];
+      lut.resize(M - lo + 1);
+      for (int d = lo; d <= M; ++d) lut[d - lo] = d >= 0 ? b[d] : static_cast<int16_t>(K + b[-d]);
     }
     r = new trimul_relpos_s;
     r->device = device;
+    r->lo = lo;
     r->M = M;
     r->rows = rows;
     r->groups = p->groups != 0;
     r->num_sms = sms;
     DeviceScope scope;
     trimul_status st = scope.enter(device);
-    if (st == TRIMUL_OK) {
+    if (st == TRIMUL_OK && !lut.empty()) {
       cudaError_t e = cudaMalloc(&r->lut, lut.size() * sizeof(int16_t));
       if (e == cudaSuccess) e = cudaMemcpy(r->lut, lut.data(), lut.size() * sizeof(int16_t), cudaMemcpyHostToDevice);
       if (e != cudaSuccess) {
