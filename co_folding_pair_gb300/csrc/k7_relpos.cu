@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(512)
 // anywhere within 16 bytes: a head's tile then begins up to V - 1 elements
 // early, on a boundary, and its buckets are shifted alike.
 constexpr int kTileSteps = 8;
+constexpr int kHeadsBytes = 220 * 1024;  // shared memory for a block's sums and buckets
 
 template <typename T>
 struct HeadTile {
@@ -494,7 +495,7 @@ template <typename T>
 GradSplit split_heads(int rows, int B, long long plane, int H, int num_sms) {
   constexpr int V = Vec<T>::n, kPart = HeadTile<T>::part;
   GradSplit g;
-  constexpr int kMost = 220 * 1024, kIds = 2 * (kPart + V) * 2;  // two buffers of a part's buckets
+  constexpr int kMost = kHeadsBytes, kIds = 2 * (kPart + V) * 2;  // two buffers of a part's buckets
   const int own = rows * 32 * 4;
   const int warps = std::max(1, std::min(16, (kMost - kIds) / own));
   g.slices = (H + warps - 1) / warps;
@@ -536,7 +537,7 @@ cudaError_t forward(const RelposArgs& a, const void* table, const void* base, vo
   const int heads = (a.D + groups - 1) / groups;
   groups = (a.D + heads - 1) / heads;
   const int grid = static_cast<int>(std::min<long long>(tiles * a.B, std::max(1, 8 * num_sms / groups)));
-  cudaError_t e = cudaFuncSetAttribute(k7_relpos_heads<T, Tab>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTableBytes);
+  cudaError_t e = allow_smem<k7_relpos_heads<T, Tab>>(kTableBytes);
   if (e != cudaSuccess) return e;
   k7_relpos_heads<T, Tab><<<dim3(grid, groups), kHeadThreads, heads * a.rows * 4, s>>>(
       a, static_cast<const Tab*>(table), static_cast<const T*>(base), static_cast<T*>(out), plane,
@@ -546,7 +547,7 @@ cudaError_t forward(const RelposArgs& a, const void* table, const void* base, vo
 
 template <typename T, int G>
 cudaError_t grad_pair(const RelposArgs& a, const T* dout, const GradSplit& g, float* ws, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(k7_relpos_grad_pair<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSumBytes);
+  cudaError_t e = allow_smem<k7_relpos_grad_pair<T, G>>(kSumBytes);
   if (e != cudaSuccess) return e;
   k7_relpos_grad_pair<T, G><<<dim3(g.ranges, g.slices), g.warps * 32, g.smem, s>>>(
       a, dout, ws, static_cast<uint32_t>(a.B) * a.I * a.J, g.slice, g.S);
@@ -568,7 +569,7 @@ cudaError_t backward(const RelposArgs& a, const void* grad, trimul_layout layout
       default: e = grad_pair<T, 16>(a, dout, g, ws, s); break;
     }
   } else {
-    e = cudaFuncSetAttribute(k7_relpos_grad_heads<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    e = allow_smem<k7_relpos_grad_heads<T>>(kHeadsBytes);
     if (e != cudaSuccess) return e;
     const uint32_t plane = static_cast<uint32_t>(a.I) * a.J;
     const uint32_t tiles = static_cast<uint32_t>((plane + static_cast<long long>(Vec<T>::n) - 1 + g.slice - 1) / g.slice);

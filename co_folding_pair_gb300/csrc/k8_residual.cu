@@ -6,9 +6,11 @@
 // y, X and both norms' statistics again from x and u (so nothing is kept from
 // the forward, and X before its rounding is what the gradient is taken of), and
 //
-//   dX = dX' + Norm_pre'(dn),    dx = dX,   dy = w dX,   du = Norm_post'(dy),
-//   dgate = scale mask channel y dX G'(gate),   dchannel = sum scale mask G y dX,
-//   dgamma = sum (norm's gradient) (normalised value),   dbeta = sum (norm's gradient)
+//   dX = dX' + Norm_pre'(dn),    dx = dX,    q = scale mask G(gate) dX,
+//   du = Norm_post'(q channel),    dgate = scale mask G'(gate) dX (channel y),
+//   of the pre-norm: dgamma = sum dn X^, dbeta = sum dn, and of the rest, from
+//   S0 = sum q u^ and S1 = sum q alone,  dgamma = channel S0,  dbeta = channel S1,
+//   dchannel = gamma S0 + beta S1
 //
 // with, for v^ = (v - mean) r normalised and t = dv' gamma,
 //   Norm'(dv') = r (t - mean(t) - v^ mean(t v^))     (RMS: without the means of v and t).
@@ -17,6 +19,7 @@
 // in bf16 against some 20 to 60 operations, so both are bound by memory.
 // Rounding: each output is rounded once, from fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "pair_ops.cuh"
 
@@ -24,41 +27,81 @@ namespace trimul {
 
 namespace {
 
-constexpr int kThreads = 256;
-
-// Sum over the G lanes that share a row.
+// Sums over the G lanes that share a row: of one number, or of two at once.  In the
+// first step each half of the lanes takes over one of the numbers, and hands
+// its sum back in the last: log2 G + 1 shuffles for both instead of 2 log2 G.
 template <int G>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ void row_sums(float (&v)[1]) {
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = G / 2; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+}
+template <int G>
+__device__ __forceinline__ void row_sums(float (&v)[2]) {
+  if constexpr (G > 1) {
+    const bool up = threadIdx.x & (G / 2);
+    float keep = up ? v[1] : v[0];
+    keep += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], G / 2);
+#pragma unroll
+    for (int o = G / 4; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+    const float other = __shfl_xor_sync(0xffffffffu, keep, G / 2);
+    v[0] = up ? other : keep;
+    v[1] = up ? keep : other;
+  }
+}
+// 1 / sqrt(x) for x of normal size (eps keeps it from 0), to 2 ulp (the approximate instruction).
+__device__ __forceinline__ float inverse_root(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// v -> its normalised value; returns r.  Lanes past D hold and keep zeros.
-// The mean is a true division: a row of one value has that value as its mean
-// exactly, and the product with 1 / D, off by half an ulp of the mean, would be
-// scaled by 1 / sqrt(eps) there.
-template <int G>
-__device__ __forceinline__ float normalise(F8& v, int kind, float d, float inv_d, float eps, bool live) {
+// Each row of v -> its normalised value; scale[r] its factor.  Lanes past D hold
+// and keep zeros.  The mean has to be the sum over D exactly rounded: a row of
+// one value has that value as its mean, and half an ulp of the mean more would
+// be scaled by 1 / sqrt(eps) there.  So it is a division, unless 1 / D is a
+// number itself.
+template <int G, int R>
+__device__ __forceinline__ void normalise(F8 (&v)[R], float (&scale)[R], int kind, float d, float inv_d, float eps,
+                                          bool live) {
+  float t[R];
   if (kind == TRIMUL_NORM_LAYER) {
-    const float mean = row_sum<G>(sum_of(v)) / d;
-    const f2 shift = both(live ? -mean : 0.f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v.v[e] = add2(v.v[e], shift);
+    for (int r = 0; r < R; ++r) t[r] = sum_of(v[r]);
+    row_sums<G>(t);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float mean = (__float_as_uint(d) & 0x7fffffu) ? t[r] / d : t[r] * inv_d;
+      const f2 shift = both(live ? -mean : 0.f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[r].v[e] = add2(v[r].v[e], shift);
+    }
   }
-  const float r = rsqrtf(row_sum<G>(dot_of(v, v)) * inv_d + eps);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v.v[e] = mul2(v.v[e], both(r));
-  return r;
+  for (int r = 0; r < R; ++r) t[r] = dot_of(v[r], v[r]);
+  row_sums<G>(t);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    scale[r] = inverse_root(t[r] * inv_d + eps);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[r].v[e] = mul2(v[r].v[e], both(scale[r]));
+  }
 }
 
 // t (the gradient at the normalised value) -> the gradient at the norm's input.
 template <int G>
-__device__ __forceinline__ void normalise_grad(F8& t, const F8& hat, float r, int kind, float inv_d) {
-  const float m2 = row_sum<G>(dot_of(t, hat)) * (-r * inv_d);
-  const float m1 = kind == TRIMUL_NORM_LAYER ? row_sum<G>(sum_of(t)) * (-r * inv_d) : 0.f;
+__device__ __forceinline__ void normalise_grad(F8& t, const F8& hat, float scale, int kind, float inv_d) {
+  const float k = -scale * inv_d;
+  float m[2] = {dot_of(t, hat), 0.f};
+  if (kind == TRIMUL_NORM_LAYER) {
+    m[1] = sum_of(t);
+    row_sums<G>(m);
+  } else {
+    float one[1] = {m[0]};
+    row_sums<G>(one);
+    m[0] = one[0];
+  }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) t.v[e] = fma2(t.v[e], both(r), fma2(hat.v[e], both(m2), both(m1)));
+  for (int e = 0; e < 4; ++e) t.v[e] = fma2(t.v[e], both(scale), fma2(hat.v[e], both(m[0] * k), both(m[1] * k)));
 }
 
 // Eight of a parameter's values, or the value it has where it is absent.
@@ -72,12 +115,13 @@ __device__ __forceinline__ void param8(const float* p, int c, bool live, float a
   }
 }
 
-// The rows of the next turns are on their way while one is worked on: every
+// The rows of the next turns are on their way while some are worked on: every
 // thread copies its own 16 bytes of each tensor into a ring of its own in
 // shared memory and reads them back itself, so the ring needs no barrier, only
 // the thread's wait for its oldest copies.  Depth, not registers, sets the
-// bytes in flight.
-constexpr int kDepth = 4;
+// bytes in flight.  (The backward has up to six tensors to read.)
+constexpr int kForwardThreads = 256, kForwardBlocks = 2, kForwardDepth = 3;
+constexpr int kBackwardThreads = 256, kBackwardBlocks = 2, kBackwardDepth = 2;
 
 __device__ __forceinline__ void copy16(uint4* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
@@ -88,8 +132,12 @@ __device__ __forceinline__ void copies_wait() {  // until at most N groups are o
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's eight elements of T at ring slots [k], [k + 1] (fp32 only), kThreads apart.
-__device__ __forceinline__ void copy8(uint4* to, const __nv_bfloat16* from) { copy16(to, from); }
+// A thread's eight elements of T in ring slots kThreads apart, one slot (bf16) or two (fp32).
+template <int kThreads>
+__device__ __forceinline__ void copy8(uint4* to, const __nv_bfloat16* from) {
+  copy16(to, from);
+}
+template <int kThreads>
 __device__ __forceinline__ void copy8(uint4* to, const float* from) {
   copy16(to, from);
   copy16(to + kThreads, from + 4);
@@ -97,14 +145,22 @@ __device__ __forceinline__ void copy8(uint4* to, const float* from) {
 __device__ __forceinline__ F8 widen8(const uint4 v) {
   return F8{{unpack_bf162(v.x), unpack_bf162(v.y), unpack_bf162(v.z), unpack_bf162(v.w)}};
 }
+// The turns over whole blocks of rows without a mask need not look whether a
+// row is there; the others (kAsk) read zeros where it is not.
+template <bool kAsk, int kThreads>
 __device__ __forceinline__ F8 take8(const uint4* from, bool on, __nv_bfloat16) {
-  return widen8(on ? from[0] : make_uint4(0u, 0u, 0u, 0u));
+  return widen8(!kAsk || on ? from[0] : make_uint4(0u, 0u, 0u, 0u));
 }
+template <bool kAsk, int kThreads>
 __device__ __forceinline__ F8 take8(const uint4* from, bool on, float) {
   const ulonglong2 z = make_ulonglong2(0, 0);
-  const ulonglong2 a = on ? reinterpret_cast<const ulonglong2*>(from)[0] : z;
-  const ulonglong2 b = on ? reinterpret_cast<const ulonglong2*>(from)[kThreads] : z;
+  const ulonglong2 a = !kAsk || on ? reinterpret_cast<const ulonglong2*>(from)[0] : z;
+  const ulonglong2 b = !kAsk || on ? reinterpret_cast<const ulonglong2*>(from)[kThreads] : z;
   return F8{{a.x, a.y, b.x, b.y}};
+}
+// The slots of a lane past D, which nothing is copied to.
+__device__ __forceinline__ void clear_slots(uint4* own, int n, int threads) {
+  for (int k = 0; k < n; ++k) own[k * threads] = make_uint4(0u, 0u, 0u, 0u);
 }
 // Streaming stores: what is written is not read again here.
 __device__ __forceinline__ void put8(__nv_bfloat16* p, const F8& f) {
@@ -123,22 +179,42 @@ __device__ __forceinline__ float reciprocal(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// sigmoid(x) and 1 - sigmoid(x), each to fp32's relative precision (the
-// exponential's argument is never positive, so nothing overflows either).
-__device__ __forceinline__ float2 sigmoid2(float x) {
-  const float e = __expf(-fabsf(x)), big = reciprocal(1.0f + e), small = e * big;
-  return x >= 0.f ? make_float2(big, small) : make_float2(small, big);
+// A gate is kept as its value or, of a sigmoid, as one number that gives both
+// the value and its derivative to fp32's relative precision: with
+// e = exp(-|x|) (which cannot overflow) and small = e / (1 + e), the lesser of
+// sigmoid(x) and 1 - sigmoid(x), it is small for x < 0 and -small for x >= 0.
+__device__ __forceinline__ float sigmoid_code(float x) {
+  const float e = __expf(-fabsf(x)), small = e * reciprocal(1.0f + e);
+  return x >= 0.f ? -small : small;
 }
-// The gate's values, in place; returns their derivatives.
-__device__ __forceinline__ F8 sigmoid8(F8& g) {
-  F8 d;
+__device__ __forceinline__ void sigmoid_codes(F8& g) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 x = split2(g.v[e]), a = sigmoid2(x.x), b = sigmoid2(x.y);
-    g.v[e] = pair2(a.x, b.x);
-    d.v[e] = pair2(a.x * a.y, b.x * b.y);
+    const float2 x = split2(g.v[e]);
+    g.v[e] = pair2(sigmoid_code(x.x), sigmoid_code(x.y));
   }
-  return d;
+}
+__device__ __forceinline__ float sigmoid_value(float code) { return __float_as_int(code) < 0 ? 1.0f + code : code; }
+// The gate's values, and their derivatives (1 of a gate without sigmoid).
+__device__ __forceinline__ F8 gate_values(const F8& code, bool sigmoid) {
+  F8 v = code;
+  if (sigmoid) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = split2(code.v[e]);
+      v.v[e] = pair2(sigmoid_value(x.x), sigmoid_value(x.y));
+    }
+  }
+  return v;
+}
+__device__ __forceinline__ F8 gate_slopes(const F8& code) {
+  F8 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 x = split2(code.v[e]);
+    v.v[e] = pair2(fmaf(-fabsf(x.x), fabsf(x.x), fabsf(x.x)), fmaf(-fabsf(x.y), fabsf(x.y), fabsf(x.y)));
+  }
+  return v;
 }
 
 // The gate's eight values of a row (pair), as they are.
@@ -152,9 +228,13 @@ __device__ __forceinline__ const uint16_t* gate_row(const ResidualArgs& a, uint3
 
 using bf = __nv_bfloat16;
 
-__device__ __forceinline__ float mask_of(const ResidualArgs& a, uint32_t pair) {
-  return a.mask ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.mask)[pair]) : 1.f;
+// A pair's mask, as its bits: they are loaded a turn early, and not looked at before they are needed.
+constexpr uint32_t kOne = 0x3f80;
+__device__ __forceinline__ uint32_t mask_of(const ResidualArgs& a, uint32_t pair, uint32_t rows) {
+  return a.mask && pair < rows ? a.mask[pair] : kOne;
 }
+
+constexpr int kForwardRows = 2;  // R
 
 template <typename T>
 constexpr int kSlots = sizeof(T) / 2;  // ring slots of eight elements
@@ -169,10 +249,13 @@ __host__ __device__ constexpr int backward_slots(bool gate, bool second, bool pr
   return kSlots<T> * (second ? 3 : 2) + 1 + (gate ? 1 : 0) + (pre ? 1 : 0);
 }
 
-// G lanes share a row, eight channels each.
+// G lanes share a row, eight channels each.  A thread works on R rows at a
+// time: their chains of operations, shuffles above all, run side by side, and
+// their sums are reduced together.
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads, 3) k8_residual_fwd(ResidualArgs a, uint32_t rows) {
+__global__ void __launch_bounds__(kForwardThreads, kForwardBlocks) k8_residual_fwd(ResidualArgs a, uint32_t rows) {
   extern __shared__ uint4 ring[];
+  constexpr int kThreads = kForwardThreads, kDepth = kForwardDepth, R = kForwardRows;
   constexpr uint32_t kRows = kThreads / G;
   const int c = (threadIdx.x % G) * 8;
   const bool live = c < a.p.D;
@@ -194,83 +277,116 @@ __global__ void __launch_bounds__(kThreads, 3) k8_residual_fwd(ResidualArgs a, u
   param8(a.p.pre_gamma, c, live, 1.f, ng);
   param8(a.p.pre_beta, c, live, 0.f, nb);
   const int slots = forward_slots<T>(a.gate);
-  const uint32_t step = gridDim.x * kRows, mine = blockIdx.x * kRows + threadIdx.x / G;
+  const uint32_t step = gridDim.x * kRows * R;
   uint4* const own = ring + threadIdx.x;
-  // row `row` into stage `stage`; rows past the end close an empty group
-  auto fetch = [&](unsigned long long row, int stage) {
-    if (live && row < rows) {
-      const size_t at = static_cast<size_t>(row) * a.p.D + c;
-      uint4* const to = own + stage * slots * kThreads;
-      copy8(to, static_cast<const T*>(a.x) + at);
-      copy16(to + kSlots<T> * kThreads, a.u + at);
-      if (a.gate) copy16(to + (kSlots<T> + 1) * kThreads, gate_row(a, static_cast<uint32_t>(row)) + c);
+  if (!live) clear_slots(own, kDepth * R * slots, kThreads);
+  // rows are below 2^31 and steps below 2^20: sums of a few stay within 32 bits
+  uint32_t row = blockIdx.x * kRows * R + threadIdx.x / G;
+  size_t at = static_cast<size_t>(row) * a.p.D + c;
+  const size_t stride = static_cast<size_t>(step) * a.p.D, next = static_cast<size_t>(kRows) * a.p.D;
+  // the rows from `row`, at element `at`, on into stage `stage`; rows past the end are left out
+  auto fetch = [&](uint32_t row, size_t at, int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r, row += kRows, at += next) {
+      if (live && row < rows) {
+        uint4* const to = own + (stage * R + r) * slots * kThreads;
+        copy8<kThreads>(to, static_cast<const T*>(a.x) + at);
+        copy16(to + kSlots<T> * kThreads, a.u + at);
+        if (a.gate) copy16(to + (kSlots<T> + 1) * kThreads, gate_row(a, row) + c);
+      }
     }
     copies_end();
   };
 #pragma unroll
-  for (int k = 0; k < kDepth - 1; ++k) fetch(mine + static_cast<unsigned long long>(k) * step, k);
+  for (int k = 0; k < kDepth - 1; ++k) fetch(row + k * step, at + k * stride, k);
   int stage = 0;
-  float m_next = (a.mask && mine < rows) ? mask_of(a, mine) : 1.f;
-  // every lane of a warp takes the same number of turns, for the shuffles
-  for (unsigned long long base = blockIdx.x * kRows; base < rows; base += step) {
-    const unsigned long long row = base + threadIdx.x / G;
-    const bool on = live && row < rows;
-    const size_t at = static_cast<size_t>(row) * a.p.D + c;
-    const float m = m_next;
-    if (a.mask && row + step < rows) m_next = mask_of(a, static_cast<uint32_t>(row + step));
-    fetch(row + (kDepth - 1ull) * step, (stage + kDepth - 1) % kDepth);
+  uint32_t m_next[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) m_next[r] = mask_of(a, row + r * kRows, rows);
+  auto turn = [&](auto ask) {
+    constexpr bool kAsk = decltype(ask)::value;
+    bool on[R];
+    float m[R], unused[R];
+    F8 x[R], y[R];
+    fetch(row + (kDepth - 1) * step, at + (kDepth - 1) * stride, (stage + kDepth - 1) % kDepth);
     copies_wait<kDepth - 1>();
-    const uint4* const from = own + stage * slots * kThreads;
+    const uint4* const from = own + stage * R * slots * kThreads;
     stage = (stage + 1) % kDepth;
-    F8 x = take8(from, on, T()), y = take8(from + kSlots<T> * kThreads, on, bf());
-    if (a.p.post_norm != TRIMUL_NORM_NONE) normalise<G>(y, a.p.post_norm, d_f, inv_d, a.p.eps, live);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y.v[e] = fma2(y.v[e], A.v[e], B.v[e]);
-    if (a.gate) {
-      F8 g = take8(from + (kSlots<T> + 1) * kThreads, on, bf());
-      if (a.p.gate_sigmoid) sigmoid8(g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y.v[e] = mul2(y.v[e], g.v[e]);
+    for (int r = 0; r < R; ++r) {
+      const uint32_t mine = row + r * kRows;
+      on[r] = live && (!kAsk || mine < rows);
+      m[r] = kAsk ? bf16_lo(m_next[r]) : 1.f;
+      if (kAsk) m_next[r] = mask_of(a, mine + step, rows);
+      x[r] = take8<kAsk, kThreads>(from + r * slots * kThreads, on[r], T());
+      y[r] = take8<kAsk, kThreads>(from + (r * slots + kSlots<T>) * kThreads, on[r], bf());
     }
-    if (m != 0.f) {
+    if (a.p.post_norm != TRIMUL_NORM_NONE) normalise<G>(y, unused, a.p.post_norm, d_f, inv_d, a.p.eps, live);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x.v[e] = fma2(y.v[e], both(m), x.v[e]);
-    }
-    if (on) put8(static_cast<T*>(a.out) + at, x);
-    if (a.normed) {
-      normalise<G>(x, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
-      if (m != 0.f) {
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x.v[e] = fma2(x.v[e], ng.v[e], nb.v[e]);
-      } else {
-        x = F8{};
+      for (int e = 0; e < 4; ++e) y[r].v[e] = fma2(y[r].v[e], A.v[e], B.v[e]);
+      F8 g = {{both(m[r]), both(m[r]), both(m[r]), both(m[r])}};
+      if (a.gate) {
+        g = take8<kAsk, kThreads>(from + (r * slots + kSlots<T> + 1) * kThreads, on[r], bf());
+        if (a.p.gate_sigmoid) {
+          sigmoid_codes(g);
+          g = gate_values(g, true);
+        }
+        if (kAsk) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g.v[e] = mul2(g.v[e], both(m[r]));
+        }
       }
-      if (on) put8(reinterpret_cast<bf*>(a.normed) + at, x);
+      if (!kAsk || m[r] != 0.f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[r].v[e] = fma2(y[r].v[e], g.v[e], x[r].v[e]);
+      }
+      if (on[r]) put8(static_cast<T*>(a.out) + at + r * next, x[r]);
     }
+    if (a.normed) {
+      normalise<G>(x, unused, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[r].v[e] = fma2(x[r].v[e], ng.v[e], nb.v[e]);
+        if (kAsk && m[r] == 0.f) x[r] = F8{};
+        if (on[r]) put8(reinterpret_cast<bf*>(a.normed) + at + r * next, x[r]);
+      }
+    }
+    row += step;
+    at += stride;
+  };
+  // every lane of a warp takes the same number of turns, for the shuffles
+  for (uint32_t base = blockIdx.x * kRows * R; base < rows; base += step) {
+    if (a.mask || base + kRows * R > rows)
+      turn(std::true_type());
+    else
+      turn(std::false_type());
   }
 }
 
-// Depth of the backward's ring: it has up to six tensors to read.
-constexpr int kBackDepth = 2;
-
+// One row at a time here: the sums take the registers that a second one would need.
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, uint32_t rows) {
+__global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual_bwd(ResidualArgs a, uint32_t rows) {
   extern __shared__ uint4 ring[];
-  // post_gamma, post_beta, pre_gamma, channel: the low and the high four of each lane's eight
-  __shared__ float4 par4[4][2][32];
+  // channel post_gamma, channel post_beta, pre_gamma: the low and the high four of each lane's eight
+  __shared__ float4 par4[3][2][32];
+  constexpr int kThreads = kBackwardThreads, kDepth = kBackwardDepth;
   constexpr uint32_t kRows = kThreads / G;
   const int c = (threadIdx.x % G) * 8;
   const bool live = c < a.p.D;
   const float d_f = static_cast<float>(a.p.D), inv_d = 1.0f / d_f;
   const bool post = a.p.post_norm != TRIMUL_NORM_NONE, pre = a.p.pre_norm != TRIMUL_NORM_NONE;
-  {
-    const float* const from[4] = {a.p.post_gamma, a.p.post_beta, a.p.pre_gamma, a.p.channel};
-    for (int n = threadIdx.x; n < 4 * 256; n += kThreads) {
-      const int q = n / 256, e = n % 256;
-      reinterpret_cast<float*>(&par4[q][e / 4 % 2][e / 8])[e % 4] = e < a.p.D && from[q] ? from[q][e] : q == 1 ? 0.f : 1.f;
-    }
-    __syncthreads();
+  for (int n = threadIdx.x; n < 256; n += kThreads) {
+    const bool in = n < a.p.D;
+    const float ch = in && a.p.channel ? a.p.channel[n] : 1.f;
+    const float v[3] = {ch * (in && a.p.post_gamma ? a.p.post_gamma[n] : 1.f),
+                        ch * (in && a.p.post_beta ? a.p.post_beta[n] : 0.f), in && a.p.pre_gamma ? a.p.pre_gamma[n] : 1.f};
+#pragma unroll
+    for (int q = 0; q < 3; ++q) reinterpret_cast<float*>(&par4[q][n / 4 % 2][n / 8])[n % 4] = v[q];
   }
+  __syncthreads();
   auto par = [&](int q) {
     const ulonglong2 lo = reinterpret_cast<const ulonglong2&>(par4[q][0][c / 8]);
     const ulonglong2 hi = reinterpret_cast<const ulonglong2&>(par4[q][1][c / 8]);
@@ -278,108 +394,121 @@ __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, u
   };
   const int slots = backward_slots<T>(a.gate, a.dout2, pre);
   const int at_u = kSlots<T> * (a.dout2 ? 3 : 2), at_g = at_u + 1, at_n = at_g + (a.gate ? 1 : 0);
-  const uint32_t step = gridDim.x * kRows, mine = blockIdx.x * kRows + threadIdx.x / G;
+  const uint32_t step = gridDim.x * kRows;
   uint4* const own = ring + threadIdx.x;
-  auto fetch = [&](unsigned long long row, int stage) {
+  if (!live) clear_slots(own, kDepth * slots, kThreads);
+  uint32_t row = blockIdx.x * kRows + threadIdx.x / G;
+  size_t at = static_cast<size_t>(row) * a.p.D + c;
+  const size_t stride = static_cast<size_t>(step) * a.p.D;
+  auto fetch = [&](uint32_t row, size_t at, int stage) {
     if (live && row < rows) {
-      const size_t at = static_cast<size_t>(row) * a.p.D + c;
       uint4* const to = own + stage * slots * kThreads;
-      copy8(to, static_cast<const T*>(a.dout) + at);
-      if (pre) copy8(to + kSlots<T> * kThreads, static_cast<const T*>(a.x) + at);  // only X's statistics need x
-      if (a.dout2) copy8(to + 2 * kSlots<T> * kThreads, static_cast<const T*>(a.dout2) + at);
+      copy8<kThreads>(to, static_cast<const T*>(a.dout) + at);
+      if (pre) copy8<kThreads>(to + kSlots<T> * kThreads, static_cast<const T*>(a.x) + at);  // only X's statistics need x
+      if (a.dout2) copy8<kThreads>(to + 2 * kSlots<T> * kThreads, static_cast<const T*>(a.dout2) + at);
       copy16(to + at_u * kThreads, a.u + at);
-      if (a.gate) copy16(to + at_g * kThreads, gate_row(a, static_cast<uint32_t>(row)) + c);
+      if (a.gate) copy16(to + at_g * kThreads, gate_row(a, row) + c);
       if (pre) copy16(to + at_n * kThreads, a.dnormed + at);
     }
     copies_end();
   };
 #pragma unroll
-  for (int k = 0; k < kBackDepth - 1; ++k) fetch(mine + static_cast<unsigned long long>(k) * step, k);
+  for (int k = 0; k < kDepth - 1; ++k) fetch(row + k * step, at + k * stride, k);
   F8 sums[RESIDUAL_SUMS] = {};
   int stage = 0;
-  float m_next = mine < rows ? mask_of(a, mine) : 0.f;
-  for (unsigned long long base = blockIdx.x * kRows; base < rows; base += step) {
-    const unsigned long long row = base + threadIdx.x / G;
-    const bool on = live && row < rows;
-    const size_t at = static_cast<size_t>(row) * a.p.D + c;
-    const float m = on ? m_next : 0.f;
-    if (row + step < rows) m_next = mask_of(a, static_cast<uint32_t>(row + step));
-    fetch(row + (kBackDepth - 1ull) * step, (stage + kBackDepth - 1) % kBackDepth);
-    copies_wait<kBackDepth - 1>();
-    const uint4* const from = own + stage * slots * kThreads;
-    stage = (stage + 1) % kBackDepth;
+  uint32_t m_next = mask_of(a, row, rows);
+  auto turn = [&](auto ask) {
+    constexpr bool kAsk = decltype(ask)::value;
+    const bool on = live && (!kAsk || row < rows);
+    const float m = !kAsk ? 1.f : on ? bf16_lo(m_next) : 0.f;
+    if (kAsk) m_next = mask_of(a, row + step, rows);
     const bool real = on && m != 0.f;  // padding: zeros, whatever the tensors hold
-    F8 d = take8(from, on, T());
-    if (a.dout2) {
-      const F8 t = take8(from + 2 * kSlots<T> * kThreads, on, T());
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d.v[e] = add2(d.v[e], t.v[e]);
-    }
-    F8 yh = take8(from + at_u * kThreads, real, bf());
-    float pr = 0.f;
-    if (post) pr = normalise<G>(yh, a.p.post_norm, d_f, inv_d, a.p.eps, live);
-    F8 gv, gd;  // scale mask times the gate's value, and times its derivative
     const f2 k = both(a.p.scale * m);
+    fetch(row + (kDepth - 1) * step, at + (kDepth - 1) * stride, (stage + kDepth - 1) % kDepth);
+    copies_wait<kDepth - 1>();
+    const uint4* const from = own + stage * slots * kThreads;
+    stage = (stage + 1) % kDepth;
+    auto slot = [&](int n) { return from + n * kThreads; };
+    F8 yh[1] = {take8<kAsk, kThreads>(slot(at_u), real, bf())}, gate;
+    float post_r[1], pre_r[1];
+    if (post) normalise<G>(yh, post_r, a.p.post_norm, d_f, inv_d, a.p.eps, live);
     if (a.gate) {
-      gv = take8(from + at_g * kThreads, real, bf());
-      if (a.p.gate_sigmoid) {
-        gd = sigmoid8(gv);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) gd.v[e] = mul2(gd.v[e], k);
-      } else {
-        gd = F8{{k, k, k, k}};
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) gv.v[e] = mul2(gv.v[e], k);
-    } else {
-      gv = F8{{k, k, k, k}};
+      gate = take8<kAsk, kThreads>(slot(at_g), real, bf());
+      if (a.p.gate_sigmoid) sigmoid_codes(gate);
     }
+    F8 d = {};
     if (pre) {
-      F8 x = take8(from + kSlots<T> * kThreads, real, T());
-      const F8 pg = par(0), pb = par(1), ch = par(3), ng = par(2);
+      F8 x[1] = {take8<kAsk, kThreads>(slot(kSlots<T>), real, T())};
+      {
+        const F8 pg = par(0), pb = par(1);
+        F8 w = {{k, k, k, k}};
+        if (a.gate) {
+          w = gate_values(gate, a.p.gate_sigmoid);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w.v[e] = mul2(w.v[e], k);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[0].v[e] = fma2(w.v[e], fma2(yh[0].v[e], pg.v[e], pb.v[e]), x[0].v[e]);
+      }
+      normalise<G>(x, pre_r, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
+      const F8 ng = par(2);
+      d = take8<kAsk, kThreads>(slot(at_n), real, bf());
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const f2 y = post ? fma2(yh.v[e], pg.v[e], pb.v[e]) : yh.v[e];
-        x.v[e] = fma2(mul2(gv.v[e], ch.v[e]), y, x.v[e]);
+        sums[2].v[e] = fma2(d.v[e], x[0].v[e], sums[2].v[e]);
+        sums[3].v[e] = add2(d.v[e], sums[3].v[e]);
+        d.v[e] = mul2(d.v[e], ng.v[e]);
       }
-      const float nr = normalise<G>(x, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
-      F8 dn = take8(from + at_n * kThreads, real, bf());
+      normalise_grad<G>(d, x[0], pre_r[0], a.p.pre_norm, inv_d);
+    }
+    {
+      const F8 t = take8<kAsk, kThreads>(slot(0), on, T());
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sums[2].v[e] = fma2(dn.v[e], x.v[e], sums[2].v[e]);
-        sums[3].v[e] = add2(dn.v[e], sums[3].v[e]);
-        dn.v[e] = mul2(dn.v[e], ng.v[e]);
-      }
-      normalise_grad<G>(dn, x, nr, a.p.pre_norm, inv_d);
+      for (int e = 0; e < 4; ++e) d.v[e] = add2(t.v[e], d.v[e]);
+    }
+    if (a.dout2) {
+      const F8 t = take8<kAsk, kThreads>(slot(2 * kSlots<T>), on, T());
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d.v[e] = add2(d.v[e], dn.v[e]);
+      for (int e = 0; e < 4; ++e) d.v[e] = add2(t.v[e], d.v[e]);
     }
     if (on) put8(static_cast<T*>(a.dx) + at, d);
-    if (!real) d = F8{};  // a padding pair passes nothing on to what follows
-    const F8 pg = par(0), ch = par(3);
-    if (a.dgate || a.g.channel) {
+    if (kAsk && !real) d = F8{};  // a padding pair passes nothing on to what follows
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d.v[e] = mul2(d.v[e], k);
+    const F8 pg = par(0);
+    if (a.dgate) {
       const F8 pb = par(1);
+      F8 t;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f2 y = post ? fma2(yh.v[e], pg.v[e], pb.v[e]) : yh.v[e];
-        const f2 dy = mul2(d.v[e], y);
-        sums[4].v[e] = fma2(dy, gv.v[e], sums[4].v[e]);
-        if (a.dgate) gd.v[e] = mul2(gd.v[e], mul2(dy, ch.v[e]));
+      for (int e = 0; e < 4; ++e) t.v[e] = mul2(d.v[e], fma2(yh[0].v[e], pg.v[e], pb.v[e]));
+      if (a.p.gate_sigmoid) {
+        const F8 slope = gate_slopes(gate);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t.v[e] = mul2(t.v[e], slope.v[e]);
       }
-      if (on && a.dgate) put8(reinterpret_cast<bf*>(a.dgate) + at, gd);
+      if (on) put8(reinterpret_cast<bf*>(a.dgate) + at, t);
+    }
+    if (a.gate) {
+      const F8 w = gate_values(gate, a.p.gate_sigmoid);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d.v[e] = mul2(d.v[e], w.v[e]);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) d.v[e] = mul2(d.v[e], mul2(gv.v[e], ch.v[e]));
-    if (post) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sums[0].v[e] = fma2(d.v[e], yh.v[e], sums[0].v[e]);
-        sums[1].v[e] = add2(d.v[e], sums[1].v[e]);
-        d.v[e] = mul2(d.v[e], pg.v[e]);
-      }
-      normalise_grad<G>(d, yh, pr, a.p.post_norm, inv_d);
+    for (int e = 0; e < 4; ++e) {
+      sums[0].v[e] = fma2(d.v[e], yh[0].v[e], sums[0].v[e]);
+      sums[1].v[e] = add2(d.v[e], sums[1].v[e]);
+      d.v[e] = mul2(d.v[e], pg.v[e]);
     }
+    if (post) normalise_grad<G>(d, yh[0], post_r[0], a.p.post_norm, inv_d);
     if (on) put8(reinterpret_cast<bf*>(a.du) + at, d);
+    row += step;
+    at += stride;
+  };
+  for (uint32_t base = blockIdx.x * kRows; base < rows; base += step) {
+    if (a.mask || base + kRows > rows)
+      turn(std::true_type());
+    else
+      turn(std::false_type());
   }
   // the block's column sums, its rows added in order
   __shared__ float s[kRows][G * 8 + 1];
@@ -400,23 +529,35 @@ __global__ void __launch_bounds__(kThreads, 2) k8_residual_bwd(ResidualArgs a, u
   }
 }
 
-// The blocks' column sums: 32 columns a block, eight groups of parts side by side.
-__global__ void __launch_bounds__(256)
-    k8_residual_sum(const float* __restrict__ part, trimul_residual_grads g, int D, int blocks) {
-  __shared__ float s[8][32];
-  const int n = blockIdx.x * 32 + threadIdx.x % 32, k0 = threadIdx.x / 32;
-  float t = 0.f;
-  if (n < RESIDUAL_SUMS * D) {
+// The parameters' gradients from the blocks' column sums: 32 channels a block,
+// eight groups of parts side by side; blockIdx.y 0 for S0 and S1, 1 for the
+// pre-norm's two.
+__global__ void __launch_bounds__(256) k8_residual_sum(ResidualArgs a, int blocks) {
+  __shared__ float s[2][8][32];
+  const int lane = threadIdx.x % 32, n = blockIdx.x * 32 + lane, k0 = threadIdx.x / 32, D = a.p.D;
+  float t[2] = {};
+  if (n < D) {
 #pragma unroll 8
-    for (int k = k0; k < blocks; k += 8) t += part[static_cast<size_t>(k) * RESIDUAL_SUMS * D + n];
+    for (int k = k0; k < blocks; k += 8) {
+      const float* const p = a.part + (static_cast<size_t>(k) * RESIDUAL_SUMS + 2 * blockIdx.y) * D + n;
+      t[0] += p[0];
+      t[1] += p[D];
+    }
   }
-  s[k0][threadIdx.x % 32] = t;
+  s[0][k0][lane] = t[0], s[1][k0][lane] = t[1];
   __syncthreads();
-  float* const out[RESIDUAL_SUMS] = {g.post_gamma, g.post_beta, g.pre_gamma, g.pre_beta, g.channel};
-  if (k0 != 0 || n >= RESIDUAL_SUMS * D || !out[n / D]) return;
+  if (k0 != 0 || n >= D) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) t += s[k][threadIdx.x];
-  out[n / D][n % D] = t;
+  for (int k = 1; k < 8; ++k) t[0] += s[0][k][lane], t[1] += s[1][k][lane];
+  if (blockIdx.y == 1) {
+    if (a.g.pre_gamma) a.g.pre_gamma[n] = t[0];
+    if (a.g.pre_beta) a.g.pre_beta[n] = t[1];
+    return;
+  }
+  const float ch = a.p.channel ? a.p.channel[n] : 1.f;
+  if (a.g.post_gamma) a.g.post_gamma[n] = ch * t[0];
+  if (a.g.post_beta) a.g.post_beta[n] = ch * t[1];
+  if (a.g.channel) a.g.channel[n] = (a.p.post_gamma ? a.p.post_gamma[n] : 1.f) * t[0] + (a.p.post_beta ? a.p.post_beta[n] : 0.f) * t[1];
 }
 
 int lanes_of(int D) {
@@ -425,27 +566,30 @@ int lanes_of(int D) {
   return g;
 }
 
-int blocks_for(int D, long long rows, int num_sms, int per_sm) {
-  const int per_block = kThreads / lanes_of(D);
-  return static_cast<int>(std::min<long long>((rows + per_block - 1) / per_block, static_cast<long long>(per_sm) * num_sms));
+// Blocks of a launch over `rows` rows.
+int blocks_for(int D, long long rows, int threads, int R, int blocks) {
+  const int per_block = threads / lanes_of(D) * R;
+  return static_cast<int>(std::min<long long>((rows + per_block - 1) / per_block, blocks));
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const ResidualArgs& a, uint32_t rows, int grid, int smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename T, int G>
+cudaError_t forward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
+  constexpr int kStage = kForwardDepth * kForwardRows * kForwardThreads * 16;
+  cudaError_t e = allow_smem<k8_residual_fwd<T, G>>(forward_slots<T>(true) * kStage);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, smem, s>>>(a, rows);
+  const int grid = blocks_for(a.p.D, rows, kForwardThreads, kForwardRows, kForwardBlocks * num_sms);
+  k8_residual_fwd<T, G><<<grid, kForwardThreads, forward_slots<T>(a.gate) * kStage, s>>>(a, rows);
   return cudaGetLastError();
 }
 template <typename T, int G>
-cudaError_t forward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
-  return launch(k8_residual_fwd<T, G>, a, rows, blocks_for(a.p.D, rows, num_sms, 3),
-                kDepth * forward_slots<T>(a.gate) * kThreads * 16, s);
-}
-template <typename T, int G>
 cudaError_t backward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
-  return launch(k8_residual_bwd<T, G>, a, rows, blocks_for(a.p.D, rows, num_sms, 2),
-                kBackDepth * backward_slots<T>(a.gate, a.dout2, a.p.pre_norm != TRIMUL_NORM_NONE) * kThreads * 16, s);
+  constexpr int kStage = kBackwardDepth * kBackwardThreads * 16;
+  cudaError_t e = allow_smem<k8_residual_bwd<T, G>>(backward_slots<T>(true, true, true) * kStage);
+  if (e != cudaSuccess) return e;
+  const int grid = blocks_for(a.p.D, rows, kBackwardThreads, 1, kBackwardBlocks * num_sms);
+  const int slots = backward_slots<T>(a.gate, a.dout2, a.p.pre_norm != TRIMUL_NORM_NONE);
+  k8_residual_bwd<T, G><<<grid, kBackwardThreads, slots * kStage, s>>>(a, rows);
+  return cudaGetLastError();
 }
 
 #define BY_LANES(FN, T)                                                  \
@@ -472,7 +616,7 @@ cudaError_t launch_residual_forward(const ResidualArgs& a, int num_sms, cudaStre
 }
 
 size_t residual_backward_workspace(int D, long long rows, int num_sms) {
-  return static_cast<size_t>(blocks_for(D, rows, num_sms, 2)) * RESIDUAL_SUMS * D * sizeof(float);
+  return static_cast<size_t>(blocks_for(D, rows, kBackwardThreads, 1, kBackwardBlocks * num_sms)) * RESIDUAL_SUMS * D * sizeof(float);
 }
 
 cudaError_t launch_residual_backward(const ResidualArgs& a, int num_sms, cudaStream_t s) {
@@ -484,8 +628,8 @@ cudaError_t launch_residual_backward(const ResidualArgs& a, int num_sms, cudaStr
     BY_LANES(backward, bf)
   }
   if (e != cudaSuccess) return e;
-  const int n = RESIDUAL_SUMS * a.p.D;
-  k8_residual_sum<<<(n + 31) / 32, 256, 0, s>>>(a.part, a.g, a.p.D, blocks_for(a.p.D, rows, num_sms, 2));
+  k8_residual_sum<<<dim3((a.p.D + 31) / 32, 2), 256, 0, s>>>(
+      a, blocks_for(a.p.D, rows, kBackwardThreads, 1, kBackwardBlocks * num_sms));
   return cudaGetLastError();
 }
 

@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -30,6 +31,18 @@ struct FastDiv {
   }
 #endif
 };
+
+// Lets a kernel have `most` bytes of dynamic shared memory; asked for once a device.
+template <auto kKernel>
+cudaError_t allow_smem(int most) {
+  static std::atomic<uint64_t> done{0};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess || (device < 64 && (done.load() >> device & 1))) return e;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess && device < 64) done.fetch_or(1ull << device);
+  return e;
+}
 
 // ---------------------------------------------------------------- relative position bias
 constexpr int kRelposMaxDistance = 32768;
@@ -65,7 +78,7 @@ struct ResidualArgs {
   trimul_residual_grads g;
   float* part;        // [blocks][RESIDUAL_SUMS][D] column sums
 };
-constexpr int RESIDUAL_SUMS = 5;  // post_gamma, post_beta, pre_gamma, pre_beta, channel
+constexpr int RESIDUAL_SUMS = 4;  // S0 and S1 (k8_residual.cu), and the gradients of pre_gamma and pre_beta
 
 cudaError_t launch_residual_forward(const ResidualArgs& a, int num_sms, cudaStream_t s);
 size_t residual_backward_workspace(int D, long long rows, int num_sms);

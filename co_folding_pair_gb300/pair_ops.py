@@ -26,7 +26,7 @@ import torch
 
 from . import _lib
 from . import trimul as _T
-from .trimul import FLAG_CHECK, TrimulError, _check, _need, _stream, _vp
+from .trimul import FLAG_CHECK, TrimulError, _check
 
 FLAG_ACCUMULATE = 16  # trimul_relpos_backward only: add to dtable
 
@@ -34,7 +34,23 @@ _TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 _KINDS = {"linear": 0, "log": 1}
 _LAYOUTS = {"pair": 0, "heads": 1}
 _NORMS = {None: 0, "none": 0, "layer": 1, "rms": 2}
-_GATES = {"none": 0, "pair": 1, "row": 2, "col": 3}
+
+
+# The smallest calls take a few microseconds on the device, so what happens here
+# counts: a tensor that is as it should be is passed by four quick looks (_fits),
+# and only another one is looked at again for the message (_refuse).
+def _fits(t, dtype, shape, dev) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _refuse(t, dtype, shape, dev, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _one_of(table, value, name):
@@ -50,20 +66,27 @@ def _type(dtype, name, kinds=(torch.bfloat16, torch.float32)):
     return _TYPES[dtype]
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _cuda(t, name):
-    if t.device.type != "cuda":
+def _cuda(t, name) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
-    return t.device.index
+    return dev
 
 
-def _within(stream):
-    """Allocations inside belong to `stream`, so that the allocator gives them out again in its order."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(shape, dtype, device, stream):
+    """Uninitialised memory of `stream`, so that the allocator gives it out again in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _raw(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 # ------------------------------------------------------------------ relative position bias
@@ -96,23 +119,31 @@ def trimul_relpos_rows(r) -> int:
 
 
 def _positions(r, q_pos, k_pos, q_group, k_group):
-    k_pos = q_pos if k_pos is None else k_pos
-    if q_group is not None and k_group is None and k_pos is q_pos:
-        k_group = q_group
+    """B, I, J and the keys' positions and groups."""
+    if q_pos.dim() != 2:
+        raise ValueError(f"q_pos must be [B, length], got {tuple(q_pos.shape)}")
+    shape, dev = q_pos.shape, r.device
+    if not _fits(q_pos, torch.int32, shape, dev):
+        _refuse(q_pos, torch.int32, shape, dev, "q_pos")
+    B, I = shape
+    if k_pos is None or k_pos is q_pos:
+        k_pos, J = q_pos, I
+        if k_group is None:
+            k_group = q_group
+    else:
+        if k_pos.dim() != 2:
+            raise ValueError(f"k_pos must be [B, length], got {tuple(k_pos.shape)}")
+        J = k_pos.shape[1]
+        if not _fits(k_pos, torch.int32, (B, J), dev):
+            _refuse(k_pos, torch.int32, (B, J), dev, "k_pos")
     if (q_group is None) != (k_group is None):
         raise ValueError("give both q_group and k_group, or neither")
-    for t, name, like in ((q_pos, "q_pos", None), (k_pos, "k_pos", None), (q_group, "q_group", q_pos),
-                          (k_group, "k_group", k_pos)):
-        if t is None:
-            continue
-        _need(t, torch.int32, name, r.device)
-        if t.dim() != 2:
-            raise ValueError(f"{name} must be [B, length], got {tuple(t.shape)}")
-        if like is not None:
-            _shape(t, like.shape, name)
-    if k_pos.shape[0] != q_pos.shape[0]:
-        raise ValueError(f"q_pos and k_pos must have the same B, got {q_pos.shape[0]} and {k_pos.shape[0]}")
-    return k_pos, k_group
+    if q_group is not None:
+        if not _fits(q_group, torch.int32, shape, dev):
+            _refuse(q_group, torch.int32, shape, dev, "q_group")
+        if k_group is not q_group and not _fits(k_group, torch.int32, (B, J), dev):
+            _refuse(k_group, torch.int32, (B, J), dev, "k_group")
+    return B, I, J, k_pos, k_group
 
 
 def trimul_relpos_forward(r: RelPosPlan, table, q_pos, k_pos=None, q_group=None, k_group=None, base=None,
@@ -122,26 +153,25 @@ def trimul_relpos_forward(r: RelPosPlan, table, q_pos, k_pos=None, q_group=None,
     table: [rows, D] bf16 or float32; q_pos, q_group: int32 [B, I]; k_pos, k_group: int32 [B, J] (default: the
     queries'); base, if given, sets the type of the result (else `dtype`); `out` may be `base`."""
     lay = _one_of(_LAYOUTS, layout, "layout")
-    k_pos, k_group = _positions(r, q_pos, k_pos, q_group, k_group)
-    _need(table, table.dtype, "table", r.device)
+    B, I, J, k_pos, k_group = _positions(r, q_pos, k_pos, q_group, k_group)
     tt = _type(table.dtype, "table")
     if table.dim() != 2 or table.shape[0] != r.rows:
         raise ValueError(f"table must be [{r.rows}, D], got {tuple(table.shape)}")
-    (B, I), J, D = q_pos.shape, k_pos.shape[1], table.shape[1]
+    D = table.shape[1]
+    if not _fits(table, table.dtype, (r.rows, D), r.device):
+        _refuse(table, table.dtype, (r.rows, D), r.device, "table")
     shape = (B, I, J, D) if lay == 0 else (B, D, I, J)
     dtype = dtype if base is None else base.dtype
     ot = _type(dtype, "dtype" if base is None else "base")
-    if base is not None:
-        _need(base, dtype, "base", r.device)
-        _shape(base, shape, "base")
+    if base is not None and not _fits(base, dtype, shape, r.device):
+        _refuse(base, dtype, shape, r.device, "base")
     if out is None:
-        with _within(stream):
-            out = torch.empty(shape, dtype=dtype, device=q_pos.device)
-    else:
-        _need(out, dtype, "out", r.device)
-        _shape(out, shape, "out")
-    _check(_lib.load().trimul_relpos_forward(r.ptr, _vp(table), tt, _vp(q_pos), _vp(k_pos), _vp(q_group), _vp(k_group),
-                                             _vp(base), B, I, J, D, lay, _vp(out), ot, _stream(stream, r.device), flags))
+        out = _empty(shape, dtype, q_pos.device, stream)
+    elif not _fits(out, dtype, shape, r.device):
+        _refuse(out, dtype, shape, r.device, "out")
+    _check(_lib.load().trimul_relpos_forward(r.ptr, table.data_ptr(), tt, q_pos.data_ptr(), k_pos.data_ptr(),
+                                             _ptr(q_group), _ptr(k_group), _ptr(base), B, I, J, D, lay, out.data_ptr(),
+                                             ot, _raw(stream, r.device), flags))
     return out
 
 
@@ -150,24 +180,24 @@ def trimul_relpos_backward(r: RelPosPlan, dout, q_pos, k_pos=None, q_group=None,
     """The table's gradient, float32 [rows, D], from dout [B, I, J, D] or [B, D, I, J] (bf16 or float32); with
     FLAG_ACCUMULATE it is added to `dtable`."""
     lay = _one_of(_LAYOUTS, layout, "layout")
-    k_pos, k_group = _positions(r, q_pos, k_pos, q_group, k_group)
-    _need(dout, dout.dtype, "dout", r.device)
+    B, I, J, k_pos, k_group = _positions(r, q_pos, k_pos, q_group, k_group)
     ot = _type(dout.dtype, "dout")
-    (B, I), J = q_pos.shape, k_pos.shape[1]
     D = dout.shape[-1 if lay == 0 else 1] if dout.dim() == 4 else 0
-    _shape(dout, (B, I, J, D) if lay == 0 else (B, D, I, J), "dout")
-    if dtable is None and flags & FLAG_ACCUMULATE:
-        raise ValueError("FLAG_ACCUMULATE needs dtable")
+    shape = (B, I, J, D) if lay == 0 else (B, D, I, J)
+    if not _fits(dout, dout.dtype, shape, r.device):
+        _refuse(dout, dout.dtype, shape, r.device, "dout")
     lib = _lib.load()
     need = lib.trimul_relpos_backward_workspace_bytes(r.ptr, B, I, J, D, lay, ot)
-    with _within(stream):
-        if dtable is None:
-            dtable = torch.empty((r.rows, D), dtype=torch.float32, device=dout.device)
-        ws = torch.empty(need, dtype=torch.uint8, device=dout.device)
-    _need(dtable, torch.float32, "dtable", r.device)
-    _shape(dtable, (r.rows, D), "dtable")
-    _check(lib.trimul_relpos_backward(r.ptr, _vp(dout), ot, _vp(q_pos), _vp(k_pos), _vp(q_group), _vp(k_group), B, I, J,
-                                      D, lay, _vp(dtable), _vp(ws), need, _stream(stream, r.device), flags))
+    if dtable is None:
+        if flags & FLAG_ACCUMULATE:
+            raise ValueError("FLAG_ACCUMULATE needs dtable")
+        dtable = _empty((r.rows, D), torch.float32, dout.device, stream)
+    elif not _fits(dtable, torch.float32, (r.rows, D), r.device):
+        _refuse(dtable, torch.float32, (r.rows, D), r.device, "dtable")
+    ws = _empty(need, torch.uint8, dout.device, stream)
+    _check(lib.trimul_relpos_backward(r.ptr, dout.data_ptr(), ot, q_pos.data_ptr(), k_pos.data_ptr(), _ptr(q_group),
+                                      _ptr(k_group), B, I, J, D, lay, dtable.data_ptr(), ws.data_ptr(), need,
+                                      _raw(stream, r.device), flags))
     return dtable
 
 
@@ -206,36 +236,39 @@ RESIDUAL_PARAMS = _lib.RESIDUAL_GRAD_FIELDS  # post_gamma, post_beta, pre_gamma,
 
 
 def _residual(x, u, params, post_norm, pre_norm, gate, gate_sigmoid, mask, scale, eps):
-    """The C parameter block of a call, its checks, and the gate's kind."""
+    """The C parameter block of a call, its checks, the device and the gate's kind."""
     dev = _cuda(x, "x")
-    _need(x, x.dtype, "x", dev)
     if x.dim() != 4:
         raise ValueError(f"x must be [B, I, J, D], got {tuple(x.shape)}")
-    B, I, J, D = x.shape
-    _need(u, torch.bfloat16, "u", dev)
-    _shape(u, x.shape, "u")
-    kind = "none"
+    shape, bf = x.shape, torch.bfloat16
+    B, I, J, D = shape
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if not _fits(u, bf, shape, dev):
+        _refuse(u, bf, shape, dev, "u")
+    kind = 0  # trimul_gate
     if gate is not None:
-        _need(gate, torch.bfloat16, "gate", dev)
-        kinds = {(B, I, J, D): "pair", (B, 1, J, D): "row", (B, I, 1, D): "col"}
-        kinds[(B, I, J, D)] = "pair"  # where I or J is 1
-        if tuple(gate.shape) not in kinds:
-            raise ValueError(f"gate must be one of {list(kinds)}, got {tuple(gate.shape)}")
-        kind = kinds[tuple(gate.shape)]
-    if mask is not None:
-        _need(mask, torch.bfloat16, "mask", dev)
-        _shape(mask, (B, I, J), "mask")
-    p = _lib.ResidualParams()
-    p.D, p.stream_type = D, _type(x.dtype, "x")
-    p.post_norm, p.pre_norm = _one_of(_NORMS, post_norm, "post_norm"), _one_of(_NORMS, pre_norm, "pre_norm")
+        if gate.shape == shape:  # where I or J is 1, too
+            kind = 1
+        elif gate.shape == (B, 1, J, D):
+            kind = 2
+        elif gate.shape == (B, I, 1, D):
+            kind = 3
+        else:
+            raise ValueError(f"gate must be one of {[(B, I, J, D), (B, 1, J, D), (B, I, 1, D)]}, got {tuple(gate.shape)}")
+        if not _fits(gate, bf, gate.shape, dev):
+            _refuse(gate, bf, gate.shape, dev, "gate")
+    if mask is not None and not _fits(mask, bf, (B, I, J), dev):
+        _refuse(mask, bf, (B, I, J), dev, "mask")
+    at = dict.fromkeys(RESIDUAL_PARAMS)
     for k, v in params.items():
-        if k not in RESIDUAL_PARAMS:
+        if k not in at:
             raise ValueError(f"unknown parameter {k!r}: {list(RESIDUAL_PARAMS)} are taken")
-        _need(v, torch.float32, k, dev)
-        _shape(v, (D,), k)
-        setattr(p, k, v.data_ptr())
-    p.gate, p.gate_sigmoid = _GATES[kind], int(bool(gate_sigmoid))
-    p.scale, p.eps = float(scale), float(eps)
+        if not _fits(v, torch.float32, (D,), dev):
+            _refuse(v, torch.float32, (D,), dev, k)
+        at[k] = v.data_ptr()
+    p = _lib.ResidualParams(D, _type(x.dtype, "x"), _one_of(_NORMS, post_norm, "post_norm"),
+                            _one_of(_NORMS, pre_norm, "pre_norm"), *at.values(), kind, 1 if gate_sigmoid else 0, scale, eps)
     return p, dev, kind
 
 
@@ -247,18 +280,18 @@ def trimul_residual_forward(x, u, params=None, post_norm=None, pre_norm=None, ga
     pre_gamma, pre_beta, channel), any of them absent; norms: "layer", "rms" or None; gate: bf16 [B, I, J, D],
     [B, 1, J, D] or [B, I, 1, D]; mask: bf16 [B, I, J].  out may be x."""
     p, dev, _ = _residual(x, u, params or {}, post_norm, pre_norm, gate, gate_sigmoid, mask, scale, eps)
-    B, I, J, D = x.shape
-    with _within(stream):
-        out = torch.empty_like(x) if out is None else out
-        if normed is None and p.pre_norm:
-            normed = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    _need(out, x.dtype, "out", dev)
-    _shape(out, x.shape, "out")
+    shape = x.shape
+    if out is None:
+        out = _empty(shape, x.dtype, x.device, stream)
+    elif not _fits(out, x.dtype, shape, dev):
+        _refuse(out, x.dtype, shape, dev, "out")
     if normed is not None:
-        _need(normed, torch.bfloat16, "normed", dev)
-        _shape(normed, x.shape, "normed")
-    _check(_lib.load().trimul_residual_forward(ctypes.byref(p), _vp(x), _vp(u), _vp(gate), _vp(mask), B, I, J, _vp(out),
-                                               _vp(normed), dev, _stream(stream, dev), flags))
+        if not _fits(normed, torch.bfloat16, shape, dev):
+            _refuse(normed, torch.bfloat16, shape, dev, "normed")
+    elif p.pre_norm:
+        normed = _empty(shape, torch.bfloat16, x.device, stream)
+    _check(_lib.load().trimul_residual_forward(p, x.data_ptr(), u.data_ptr(), _ptr(gate), _ptr(mask), *shape[:3],
+                                               out.data_ptr(), _ptr(normed), dev, _raw(stream, dev), flags))
     return out, normed
 
 
@@ -272,36 +305,31 @@ def trimul_residual_backward(x, u, dout, params=None, post_norm=None, pre_norm=N
     only the names in it are computed)."""
     params = params or {}
     p, dev, kind = _residual(x, u, params, post_norm, pre_norm, gate, gate_sigmoid, mask, scale, eps)
-    B, I, J, D = x.shape
-    bf = torch.bfloat16
-    for t, name, dt in ((dout, "dout", x.dtype), (dout2, "dout2", x.dtype), (dnormed, "dnormed", bf)):
-        if t is not None:
-            _need(t, dt, name, dev)
-            _shape(t, x.shape, name)
+    shape, xt, bf = x.shape, x.dtype, torch.bfloat16
+    for t, name, dt in ((dout, "dout", xt), (dout2, "dout2", xt), (dnormed, "dnormed", bf), (dx, "dx", xt), (du, "du", bf),
+                        (dgate, "dgate", bf)):
+        if t is not None and not _fits(t, dt, shape, dev):
+            _refuse(t, dt, shape, dev, name)
+    D, device = shape[3], x.device
     lib = _lib.load()
-    need = lib.trimul_residual_backward_workspace_bytes(ctypes.byref(p), B, I, J)
-    with _within(stream):
-        dx = torch.empty_like(x) if dx is None else dx
-        du = torch.empty_like(u) if du is None else du
-        if dgate is None and kind == "pair":
-            dgate = torch.empty_like(gate)
-        if grads is None:
-            grads = {k: torch.empty(D, dtype=torch.float32, device=x.device) for k in params}
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    g = _lib.ResidualGrads()
-    for k, v in grads.items():
-        if k not in RESIDUAL_PARAMS:
-            raise ValueError(f"unknown parameter {k!r}: {list(RESIDUAL_PARAMS)} are taken")
-        _need(v, torch.float32, k, dev)
-        _shape(v, (D,), k)
-        setattr(g, k, v.data_ptr())
-    for t, name, dt in ((dx, "dx", x.dtype), (du, "du", bf), (dgate, "dgate", bf)):
-        if t is not None:
-            _need(t, dt, name, dev)
-            _shape(t, x.shape, name)
-    _check(lib.trimul_residual_backward(ctypes.byref(p), _vp(x), _vp(u), _vp(gate), _vp(mask), _vp(dout), _vp(dout2),
-                                        _vp(dnormed), B, I, J, _vp(dx), _vp(du), _vp(dgate), ctypes.byref(g), _vp(ws),
-                                        need, dev, _stream(stream, dev), flags))
+    need = lib.trimul_residual_backward_workspace_bytes(p, *shape[:3])
+    dx = _empty(shape, xt, device, stream) if dx is None else dx
+    du = _empty(shape, bf, device, stream) if du is None else du
+    if dgate is None and kind == 1:
+        dgate = _empty(shape, bf, device, stream)
+    if grads is None:
+        grads = dict(zip(params, _empty((len(params), D), torch.float32, device, stream).unbind())) if params else {}
+    else:
+        for k, v in grads.items():
+            if k not in RESIDUAL_PARAMS:
+                raise ValueError(f"unknown parameter {k!r}: {list(RESIDUAL_PARAMS)} are taken")
+            if not _fits(v, torch.float32, (D,), dev):
+                _refuse(v, torch.float32, (D,), dev, k)
+    ws = _empty(need, torch.uint8, device, stream)
+    g = _lib.ResidualGrads(*[_ptr(grads.get(k)) for k in RESIDUAL_PARAMS])
+    _check(lib.trimul_residual_backward(p, x.data_ptr(), u.data_ptr(), _ptr(gate), _ptr(mask), dout.data_ptr(),
+                                        _ptr(dout2), _ptr(dnormed), *shape[:3], dx.data_ptr(), du.data_ptr(), _ptr(dgate),
+                                        g, ws.data_ptr(), need, dev, _raw(stream, dev), flags))
     return {"dx": dx, "du": du, "dgate": dgate, "grads": grads}
 
 
@@ -333,28 +361,27 @@ class GradSet:
             raise ValueError(f"{len(outs)} outs for {len(tensors)} tensors")
         self.tensors, self.outs = tensors, outs
         self.device = _cuda(tensors[0], "tensors[0]") if tensors else torch.cuda.current_device()
+        self.torch_device = torch.device("cuda", self.device)
         self.table = (_lib.GradTensor * len(tensors))()
         for k, (t, o) in enumerate(zip(tensors, outs)):
             kind = _type(t.dtype, f"tensors[{k}]", tuple(_TYPES))
-            _need(t, t.dtype, f"tensors[{k}]", self.device)
-            if o is not t:
-                _need(o, t.dtype, f"outs[{k}]", self.device)
-                _shape(o, t.shape, f"outs[{k}]")
+            if not _fits(t, t.dtype, t.shape, self.device):
+                _refuse(t, t.dtype, t.shape, self.device, f"tensors[{k}]")
+            if o is not t and not _fits(o, t.dtype, t.shape, self.device):
+                _refuse(o, t.dtype, t.shape, self.device, f"outs[{k}]")
             self.table[k] = _lib.GradTensor(t.data_ptr(), o.data_ptr(), t.numel(), kind)
         self.workspace_bytes = _lib.load().trimul_grad_workspace_bytes(len(tensors))
 
     def _call(self, name, norm_type, norm, stream, flags, *first):
         if norm_type not in (2, math.inf):
             raise ValueError(f"norm_type must be 2 or infinity, got {norm_type}")
-        with _within(stream):
-            dev = torch.device("cuda", self.device)
-            norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
-            ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=dev)
-        _need(norm, torch.float32, "norm", self.device)
-        if norm.numel() != 1:
-            raise ValueError("norm must have one element")
-        _check(getattr(_lib.load(), name)(self.table, len(self.table), *first, int(norm_type == math.inf), _vp(norm),
-                                          _vp(ws), self.workspace_bytes, self.device, _stream(stream, self.device), flags))
+        if norm is None:
+            norm = _empty((), torch.float32, self.torch_device, stream)
+        elif norm.numel() != 1 or not _fits(norm, torch.float32, norm.shape, self.device):
+            raise ValueError(f"norm must be one float32 on cuda:{self.device}")
+        ws = _empty(self.workspace_bytes, torch.uint8, self.torch_device, stream)
+        _check(getattr(_lib.load(), name)(self.table, len(self.table), *first, 0 if norm_type == 2 else 1, norm.data_ptr(),
+                                          ws.data_ptr(), self.workspace_bytes, self.device, _raw(stream, self.device), flags))
         return norm
 
     def norm(self, norm_type=2.0, norm=None, stream=None, flags: int = 0):
@@ -387,16 +414,18 @@ class PairBlock:
     def __init__(self, layer: _T.TriMul, residual: Residual):
         self.layer, self.residual = layer, residual
 
+    def _layer(self, z, mask, stream):
+        return self.layer(z, mask, out=_empty(z.shape, z.dtype, z.device, stream), stream=stream)
+
     def forward(self, z, mask=None, gate=None, stream=None):
-        with _within(stream):
-            u = self.layer(z, mask, stream=stream)
-        return self.residual.forward(z, u, gate=gate, mask=mask, stream=stream)
+        return self.residual.forward(z, self._layer(z, mask, stream), gate=gate, mask=mask, stream=stream)
 
     def backward(self, z, dout, mask=None, gate=None, dnormed=None, dout2=None, stream=None):
-        """(dx, dz, ...): the gradient of z is dx + dz, its parts along the stream and through the layer.  Give both to
-        the block below as dout and dout2: it adds them in 32 bits, in the pass that reads them."""
-        with _within(stream):
-            u = self.layer(z, mask, stream=stream)
-            r = self.residual.backward(z, u, dout, dnormed=dnormed, dout2=dout2, gate=gate, mask=mask, stream=stream)
+        """{"dx", "dz", "dgate", "layer_grads", "residual_grads"}: the gradient of z is dx + dz, its parts along the
+        stream and through the layer.  Give both to the block below as dout and dout2: it adds them in 32 bits, in the
+        pass that reads them."""
+        u = self._layer(z, mask, stream)
+        r = self.residual.backward(z, u, dout, dnormed=dnormed, dout2=dout2, gate=gate, mask=mask, stream=stream)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             dz, grads = _T.trimul_backward(self.layer.handle, z, mask, r["du"], self.layer.direction, stream=stream)
         return {"dx": r["dx"], "dz": dz, "dgate": r["dgate"], "layer_grads": grads, "residual_grads": r["grads"]}
