@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(512)
     k7_relpos_grad_pair(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs, int slice, int S) {
   constexpr int V = Vec<T>::n, W = G * V, P = 32 / G, kBatch = P * kSteps, kPerLane = (kBatch + 31) / 32;
   extern __shared__ float4 smem4[];
+  let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const int slot = lane / G, c = (lane % G) * V;
   float* const sums = reinterpret_cast<float*>(smem4) + static_cast<size_t>(warp) * a.rows * W;
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(512)
                          int heads) {
   constexpr int V = Vec<T>::n, kPart = HeadTile<T>::part;
   extern __shared__ float4 smem4[];
+  let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const int parts = warps / heads, tile_n = parts * kPart;
   const int h = blockIdx.y * heads + warp % heads, my_part = warp / heads;
@@ -441,6 +443,7 @@ __global__ void __launch_bounds__(256)
   __shared__ float s[8][32];
   const int e = blockIdx.x * 32 + threadIdx.x % 32, g = threadIdx.x / 32;
   float t = 0.f;
+  after_previous();
   if (e < n) {
 #pragma unroll 8
     for (int k = g; k < parts; k += 8) t += part[static_cast<size_t>(k) * n + e];
@@ -578,8 +581,7 @@ cudaError_t backward(const RelposArgs& a, const void* grad, trimul_layout layout
   }
   if (e != cudaSuccess) return e;
   const int n = a.rows * a.D;
-  k7_relpos_sum<<<(n + 31) / 32, 256, 0, s>>>(ws, dtable, n, g.ranges, accumulate ? 1 : 0);
-  return cudaGetLastError();
+  return launch_early(k7_relpos_sum, (n + 31) / 32, 256, s, ws, dtable, n, g.ranges, accumulate);
 }
 
 }  // namespace

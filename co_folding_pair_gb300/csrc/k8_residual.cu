@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
   extern __shared__ uint4 ring[];
   // channel post_gamma, channel post_beta, pre_gamma: the low and the high four of each lane's eight
   __shared__ float4 par4[3][2][32];
+  let_next_begin();
   constexpr int kThreads = kBackwardThreads, kDepth = kBackwardDepth;
   constexpr uint32_t kRows = kThreads / G;
   const int c = (threadIdx.x % G) * 8;
@@ -536,6 +537,7 @@ __global__ void __launch_bounds__(256) k8_residual_sum(ResidualArgs a, int block
   __shared__ float s[2][8][32];
   const int lane = threadIdx.x % 32, n = blockIdx.x * 32 + lane, k0 = threadIdx.x / 32, D = a.p.D;
   float t[2] = {};
+  after_previous();
   if (n < D) {
 #pragma unroll 8
     for (int k = k0; k < blocks; k += 8) {
@@ -628,9 +630,8 @@ cudaError_t launch_residual_backward(const ResidualArgs& a, int num_sms, cudaStr
     BY_LANES(backward, bf)
   }
   if (e != cudaSuccess) return e;
-  k8_residual_sum<<<dim3((a.p.D + 31) / 32, 2), 256, 0, s>>>(
-      a, blocks_for(a.p.D, rows, kBackwardThreads, 1, kBackwardBlocks * num_sms));
-  return cudaGetLastError();
+  return launch_early(k8_residual_sum, dim3((a.p.D + 31) / 32, 2), 256, s, a,
+                      blocks_for(a.p.D, rows, kBackwardThreads, 1, kBackwardBlocks * num_sms));
 }
 
 }  // namespace trimul

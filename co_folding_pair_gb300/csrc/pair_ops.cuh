@@ -12,6 +12,10 @@
 
 namespace trimul {
 
+// The two ends of an early launch (launch_early).
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Eight consecutive elements as fp32: one 16-byte access for bf16, two for fp32.
 __device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};

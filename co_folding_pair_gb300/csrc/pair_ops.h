@@ -44,6 +44,24 @@ cudaError_t allow_smem(int most) {
   return e;
 }
 
+// Launches a kernel whose blocks may be set up while the one before it in the
+// stream still runs (programmatic dependent launch).  The kernel waits
+// (after_previous) before it reads what that one writes; that one says with
+// let_next_begin that all its blocks have begun.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = threads;
+  c.stream = s;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<Params>(args)...);
+}
+
 // ---------------------------------------------------------------- relative position bias
 constexpr int kRelposMaxDistance = 32768;
 constexpr int kRelposMaxRows = 1024;

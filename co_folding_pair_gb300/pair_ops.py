@@ -318,7 +318,7 @@ def trimul_residual_backward(x, u, dout, params=None, post_norm=None, pre_norm=N
     if dgate is None and kind == 1:
         dgate = _empty(shape, bf, device, stream)
     if grads is None:
-        grads = dict(zip(params, _empty((len(params), D), torch.float32, device, stream).unbind())) if params else {}
+        grads = {k: _empty(D, torch.float32, device, stream) for k in params}
     else:
         for k, v in grads.items():
             if k not in RESIDUAL_PARAMS:
