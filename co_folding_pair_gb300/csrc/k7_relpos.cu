@@ -98,29 +98,50 @@ __device__ __forceinline__ void shifted_ids<4>(const uint16_t* ids, int m, uint3
   for (int i = 0; i < 2; ++i) w[i] = (m & 1) ? __funnelshift_l(x[i + 1], x[i + 2], 16) : x[i + 2];
 }
 
-constexpr uint16_t kNoBucket = 0xffff;
-
-// The buckets of plane positions [f0 - V, f0 + n) of batch b, in order; kNoBucket outside the plane and for padding.
-__device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, long long f0, int n, int V, uint32_t plane,
-                                          uint16_t* ids) {
-  for (int i = threadIdx.x; i < n + V; i += blockDim.x) {
-    const long long f = f0 - V + i;
-    uint16_t k = kNoBucket;
-    if (f >= 0 && f < plane) {
-      uint32_t row, j;
-      a.by_J.divmod(static_cast<uint32_t>(f), row, j);
-      k = static_cast<uint16_t>(relpos_bucket(a, b * a.I + row, b * a.J + j));
+// The buckets of plane positions [f0 - V, f0 + 32 V n) of batch b, in order:
+// a tile of n segments, 16 bytes of elements a lane each.  `none` stands for
+// what has no bucket: padding, and positions outside the plane.  Where all of a
+// segment, early ones of a shifted plane among them, is in one bucket, as most
+// are, whole[segment] is that bucket, else kMixed.
+constexpr uint32_t kMixed = 0xffffffff;
+template <int V>
+__device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, long long f0, int n, uint32_t plane,
+                                          uint16_t none, uint16_t* ids, uint32_t* whole) {
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  for (int seg = threadIdx.x / 32; seg < n; seg += warps) {
+    RelposPair pair[V + 1];
+#pragma unroll
+    for (int q = 0; q <= V; ++q) {
+      const long long f = f0 - V + (seg * V + q) * 32 + lane;
+      pair[q].none();
+      if (f >= 0 && f < plane && (q < V || lane < V)) {
+        uint32_t row, j;
+        a.by_J.divmod(static_cast<uint32_t>(f), row, j);
+        pair[q].load(a, b * a.I + row, b * a.J + j);
+      }
     }
-    ids[i] = k;
+    uint32_t first = 0;
+    bool same = true;
+#pragma unroll
+    for (int q = 0; q <= V; ++q) {
+      const int k = pair[q].bucket(a);
+      const uint32_t id = k < 0 ? none : k;
+      if (q == 0) first = __shfl_sync(0xffffffffu, id, 0);
+      same = same && (id == first || (q == V && lane >= V));
+      if (q < V || (seg == n - 1 && lane < V)) ids[(seg * V + q) * 32 + lane] = static_cast<uint16_t>(id);
+    }
+    same = __all_sync(0xffffffffu, same);
+    if (lane == 0) whole[seg] = same ? first : kMixed;
   }
 }
 
 // HEADS layout.  A block goes over tiles of a plane [I][J] of 16 bytes a
 // thread: the buckets of a tile are worked out once, in shared memory, and
 // every head of the block looks its values up by them, in its column of the
-// table, in shared memory too.  Planes of odd sizes begin anywhere within 16
-// bytes: a head's tile then begins up to V - 1 elements early, on a boundary,
-// its buckets shifted alike, and only a plane's ends are written one by one.
+// table, in shared memory too; a segment of one bucket takes one look.  Planes
+// of odd sizes begin anywhere within 16 bytes: a head's tile then begins up to
+// V - 1 elements early, on a boundary, its buckets shifted alike, and only a
+// plane's ends are written one by one.
 constexpr int kHeadThreads = 256;
 constexpr int kTableBytes = 64 * 1024;
 
@@ -128,49 +149,60 @@ template <typename T, typename Tab>
 __global__ void __launch_bounds__(kHeadThreads)
     k7_relpos_heads(RelposArgs a, const Tab* __restrict__ table, const T* base, T* out, uint32_t plane,
                     FastDiv by_tiles, int heads) {
-  constexpr int V = Vec<T>::n, kTile = kHeadThreads * V;
-  extern __shared__ float tab[];  // [heads][rows]
-  __shared__ alignas(16) uint16_t ids[kTile + V];
-  const int h0 = blockIdx.y * heads, n_heads = min(heads, a.D - h0);
-  for (int n = threadIdx.x; n < a.rows * n_heads; n += kHeadThreads) {
+  constexpr int V = Vec<T>::n, kTile = kHeadThreads * V, kSegments = kHeadThreads / 32;
+  extern __shared__ float tab[];  // [heads][rows + 1], the last of each 0
+  __shared__ alignas(16) uint16_t ids[2][kTile + V];
+  __shared__ uint32_t whole[2][kSegments];
+  const int h0 = blockIdx.y * heads, n_heads = min(heads, a.D - h0), rows = a.rows + 1;
+  const uint16_t none = static_cast<uint16_t>(a.rows);
+  for (int n = threadIdx.x; n < rows * n_heads; n += kHeadThreads) {
     const int r = n / n_heads, q = n - r * n_heads;
-    tab[q * a.rows + r] = to_f32(table[static_cast<size_t>(r) * a.D + h0 + q]);
+    tab[q * rows + r] = r < a.rows ? to_f32(table[static_cast<size_t>(r) * a.D + h0 + q]) : 0.f;
   }
-  for (uint32_t tile = blockIdx.x; tile < by_tiles.d * a.B; tile += gridDim.x) {
+  int turn = 0;
+  for (uint32_t tile = blockIdx.x; tile < by_tiles.d * a.B; tile += gridDim.x, turn ^= 1) {
     uint32_t b, t;
     by_tiles.divmod(tile, b, t);
-    stage_ids(a, b, static_cast<long long>(t) * kTile, kTile, V, plane, ids);
+    // two buffers: a warp that still works on the last tile reads the other one
+    stage_ids<V>(a, b, static_cast<long long>(t) * kTile, kSegments, plane, none, ids[turn], whole[turn]);
     __syncthreads();
+    const uint32_t one = whole[turn][threadIdx.x / 32];
+    const uint32_t first = t * kTile + threadIdx.x * V;
+    const long long begin0 = (static_cast<long long>(b) * a.D + h0) * plane;
+    int m = static_cast<int>(begin0 % V);
+    const int m_step = static_cast<int>(plane % V);
+    const T* z0 = base + begin0;
+    T* o0 = out + begin0;
+    const float* col = tab;
 #pragma unroll 2
-    for (int q = 0; q < n_heads; ++q) {
-      const long long begin = (static_cast<long long>(b) * a.D + h0 + q) * plane;
-      const int m = static_cast<int>(begin % V);
-      const long long n = begin - m + static_cast<long long>(t) * kTile + threadIdx.x * V;
-      if (n >= begin + plane) continue;
-      uint32_t w[V / 2];
-      shifted_ids<V>(ids + threadIdx.x * V, m, w);
-      const float* const col = tab + q * a.rows;
+    for (int q = 0; q < n_heads; ++q, m = (m + m_step) % V, z0 += plane, o0 += plane, col += rows) {
+      const int n = static_cast<int>(first) - m;  // the position in the plane of the first of V elements
+      if (n >= static_cast<int>(plane)) continue;
       float v[V];
+      if (one != kMixed) {
+        v[0] = col[one];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t k = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-        v[e] = k == kNoBucket ? 0.f : col[k];
+        for (int e = 1; e < V; ++e) v[e] = v[0];
+      } else {
+        uint32_t w[V / 2];
+        shifted_ids<V>(ids[turn] + threadIdx.x * V, m, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = col[(e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu];
       }
-      if (n >= begin && n + V <= begin + plane) {
+      if (n >= 0 && n <= static_cast<int>(plane) - V) {
         if (base) {
           float z[V];
-          Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(base + n)), z);
+          Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z0 + n)), z);
 #pragma unroll
           for (int e = 0; e < V; ++e) v[e] += z[e];
         }
-        __stcs(reinterpret_cast<uint4*>(out + n), Vec<T>::pack(v));
+        __stcs(reinterpret_cast<uint4*>(o0 + n), Vec<T>::pack(v));
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          if (n + e >= begin && n + e < begin + plane) out[n + e] = from_f32<T>(base ? v[e] + to_f32(base[n + e]) : v[e]);
+          if (n + e >= 0 && n + e < static_cast<int>(plane)) o0[n + e] = from_f32<T>(base ? v[e] + to_f32(z0[n + e]) : v[e]);
       }
     }
-    __syncthreads();
   }
 }
 
@@ -186,15 +218,22 @@ constexpr int kSumBytes = 200 * 1024;  // shared memory for a block's sums
 
 // PAIR layout.  A warp has sums of its own, [rows][W channels], for one slice
 // of at most W channels.  G lanes (16 bytes each) share a pair, so the warp
-// takes 32 / G neighbouring pairs at a time, its slots; kSteps of these are
-// loaded together, and the next ones while these are added.  The buckets of
-// a batch are worked out once, one pair a lane, and handed round by shuffles.
+// takes 32 / G neighbouring pairs at a time, its slots, and kSteps of these
+// make a batch.  kBuffers batches are in registers or on their way, which is
+// what DRAM's latency asks of the twelve warps that have room for their sums.
+// A batch of one bucket is added up in registers, and joins the run of batches
+// before it, as does a step of one bucket in a mixed batch; the pairs of other
+// steps go to shared memory at once.  The buckets are worked out one pair a
+// lane and handed round by shuffles.
 constexpr int kSteps = 8;
+// Warps of a block: few lanes a pair means many pairs a lane, and registers for them.
+constexpr int pair_warps(int G) { return G >= 8 ? 12 : G == 4 ? 16 : 8; }
 
 template <typename T, int G>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(pair_warps(G) * 32)
     k7_relpos_grad_pair(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs, int slice, int S) {
   constexpr int V = Vec<T>::n, W = G * V, P = 32 / G, kBatch = P * kSteps, kPerLane = (kBatch + 31) / 32;
+  constexpr int kBuffers = G >= 8 ? 3 : 2;
   extern __shared__ float4 smem4[];
   let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
@@ -208,120 +247,151 @@ __global__ void __launch_bounds__(512)
   const uint32_t batches = (pairs + kBatch - 1) / kBatch;
   const uint32_t b0 = static_cast<uint32_t>(static_cast<unsigned long long>(batches) * blockIdx.x / gridDim.x);
   const uint32_t b1 = static_cast<uint32_t>(static_cast<unsigned long long>(batches) * (blockIdx.x + 1) / gridDim.x);
+  const int streams = warps / S;
 
-  uint4 next[kSteps];
-  int next_k[kPerLane];
-  auto load = [&](uint32_t batch) {
+  uint4 buf[kBuffers][kSteps];
+  RelposPair pos[kBuffers][kPerLane];
+  // lanes past the slice read its first channels, into columns that nobody looks at
+  const T* const mine = dout + c0 + (live ? c : 0);
+  auto load = [&](uint32_t batch, uint4 (&to)[kSteps], RelposPair (&at)[kPerLane]) {
+    if (batch >= b1) return;
     const uint32_t p0 = batch * kBatch;
+    if (p0 + kBatch <= pairs) {
+      const T* from = mine + static_cast<size_t>(p0 + slot) * a.D;
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const uint32_t p = p0 + u * P + slot;
-      next[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && p < pairs) next[u] = __ldcs(reinterpret_cast<const uint4*>(dout + static_cast<size_t>(p) * a.D + c0 + c));
+      for (int u = 0; u < kSteps; ++u, from += P * a.D) to[u] = __ldcs(reinterpret_cast<const uint4*>(from));
+    } else {  // pairs past the end: the last one, without a bucket
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+        to[u] = *reinterpret_cast<const uint4*>(mine + static_cast<size_t>(min(p0 + u * P + slot, pairs - 1)) * a.D);
     }
 #pragma unroll
     for (int q = 0; q < kPerLane; ++q) {
-      const uint32_t p = p0 + q * 32 + lane;
-      next_k[q] = -1;
-      if (p < pairs && q * 32 + lane < kBatch) {
+      const uint32_t p = p0 + (q * 32 + lane) % kBatch;
+      at[q].none();
+      if (p < pairs) {
         uint32_t row, j;
         a.by_J.divmod(p, row, j);
-        next_k[q] = relpos_bucket(a, row, a.by_I.div(row) * a.J + j);
+        at[q].load(a, row, a.by_I.div(row) * a.J + j);
       }
     }
   };
-
-  int at = -1;  // the bucket of this slot's run
-  f2 run[V / 2] = {};
-  // the runs of the slots whose `end` is set go to shared memory; slots that
-  // share a bucket take turns
-  auto flush = [&](bool end) {
-    const unsigned same = __match_any_sync(0xffffffffu, end ? at : -1 - slot);
-    ulonglong2* const to = reinterpret_cast<ulonglong2*>(sums + at * W + c);
-    auto add = [&] {
+  // v joins the sums of bucket k, for the slots that say `on`
+  auto add = [&](int k, const f2 (&v)[V / 2], bool on) {
+    ulonglong2* const to = reinterpret_cast<ulonglong2*>(sums + k * W + c);
+    if (on) {
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
         const ulonglong2 t = to[q];
-        to[q] = make_ulonglong2(add2(t.x, run[2 * q]), add2(t.y, run[2 * q + 1]));
-      }
-    };
-    if (__all_sync(0xffffffffu, __popc(same) <= G)) {
-      if (end) add();
-      __syncwarp();
-    } else {
-#pragma unroll 1
-      for (int k = 0; k < P; ++k) {
-        if (end && slot == k) add();
-        __syncwarp();
+        to[q] = make_ulonglong2(add2(t.x, v[2 * q]), add2(t.y, v[2 * q + 1]));
       }
     }
+    __syncwarp();
   };
-
-  const int streams = warps / S;
-  uint32_t batch = b0 + warp / S;
-  if (batch < b1) load(batch);
-  for (; batch < b1; batch += streams) {
-    uint4 now[kSteps];
+  int at = -1;  // the bucket of the run of batches
+  f2 run[V / 2] = {};
+  auto flush = [&] {
+    if (at < 0) return;
+#pragma unroll 1
+    for (int k = 0; k < P; ++k) add(at, run, slot == k);
+  };
+  auto join = [&](int k, const f2 (&v)[V / 2]) {  // k and what it leads to is the same in all lanes
+    if (k != at) {
+      flush();
+      at = k;
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) run[e] = v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) run[e] = add2(run[e], v[e]);
+    }
+  };
+  auto take = [&](const uint4 (&from)[kSteps], const RelposPair (&pair)[kPerLane]) {
     int k_of[kPerLane];
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) now[u] = next[u];
+    for (int q = 0; q < kPerLane; ++q) k_of[q] = pair[q].bucket(a);
+    const int k0 = __shfl_sync(0xffffffffu, k_of[0], 0);
+    bool one = k0 >= 0;
 #pragma unroll
-    for (int q = 0; q < kPerLane; ++q) k_of[q] = next_k[q];
-    if (batch + streams < b1) load(batch + streams);
-
-    const int k0 = __shfl_sync(0xffffffffu, at, 0);
-    bool one = at == k0 && k0 >= 0;  // the whole batch goes on with the run of all slots
-#pragma unroll
-    for (int q = 0; q < kPerLane; ++q) one = one && (k_of[q] == k0 || q * 32 + lane >= kBatch);
+    for (int q = 0; q < kPerLane; ++q) one = one && k_of[q] == k0;
+    f2 v[V / 2];
     if (__all_sync(0xffffffffu, one)) {
-      f2 t[V / 2], v[V / 2];
-      Vec<T>::unpack(now[0], t);
+      f2 t[V / 2];
+      Vec<T>::unpack(from[0], t);
 #pragma unroll
       for (int u = 1; u < kSteps; ++u) {
-        Vec<T>::unpack(now[u], v);
+        Vec<T>::unpack(from[u], v);
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) t[e] = add2(t[e], v[e]);
       }
+      join(k0, t);
+      return;
+    }
+    // pairs that share their step's bucket with another pair, and with all the others
+    constexpr unsigned step = P == 32 ? 0xffffffffu : (1u << (P % 32)) - 1;
+    unsigned some[kPerLane], all[kPerLane];
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) run[e] = add2(run[e], t[e]);
-      continue;
+    for (int q = 0; q < kPerLane; ++q) {
+      const unsigned like = (__match_any_sync(0xffffffffu, k_of[q]) >> (lane / P * P)) & step;
+      some[q] = __ballot_sync(0xffffffffu, __popc(like) > 1 && k_of[q] >= 0);
+      all[q] = __ballot_sync(0xffffffffu, like == step && k_of[q] >= 0);
     }
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
       const int k = __shfl_sync(0xffffffffu, k_of[u * P / 32], (u * P + slot) % 32);
-      const bool end = k >= 0 && at >= 0 && k != at;
-      if (__any_sync(0xffffffffu, end)) flush(end);
-      if (k >= 0) {
-        f2 v[V / 2];
-        Vec<T>::unpack(now[u], v);
+      Vec<T>::unpack(from[u], v);
+      const int at_bit = u * P % 32;
+      if ((all[u * P / 32] >> at_bit) & 1) {
+        join(k, v);
+      } else if (some[u * P / 32] & (step << at_bit)) {
+#pragma unroll 1
+        for (int q = 0; q < P; ++q) add(k, v, slot == q && k >= 0);
+      } else {
+        add(k, v, k >= 0);
+      }
+    }
+  };
+
+  uint32_t batch = b0 + warp / S;
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) run[e] = k == at ? add2(run[e], v[e]) : v[e];
-        at = k;
+  for (int q = 0; q < kBuffers; ++q) load(batch + q * streams, buf[q], pos[q]);
+  while (batch < b1) {
+#pragma unroll
+    for (int q = 0; q < kBuffers; ++q) {
+      if (batch < b1) {
+        take(buf[q], pos[q]);
+        load(batch + kBuffers * streams, buf[q], pos[q]);
+        batch += streams;
       }
     }
   }
-  flush(at >= 0);
+  flush();
   __syncthreads();
   const float* const all = reinterpret_cast<const float*>(smem4);
   float* const out = part + static_cast<size_t>(blockIdx.x) * a.rows * a.D;
-  for (int n = threadIdx.x; n < a.rows * W * S; n += blockDim.x) {
-    const int q = n / (a.rows * W), i = n - q * a.rows * W, r = i / W, w = i % W;
-    const int from = (blockIdx.y * S + q) * slice;
-    if (w >= min(slice, a.D - from)) continue;
-    float t = 0.f;
-    for (int k = 0; k < streams; ++k) t += all[static_cast<size_t>(k * S + q) * a.rows * W + i];
-    out[static_cast<size_t>(r) * a.D + from + w] = t;
+  for (int q = 0; q < S; ++q) {
+    const int from = (blockIdx.y * S + q) * slice, n_here = min(slice, a.D - from);
+    for (int n = threadIdx.x; n < a.rows * W / 4; n += blockDim.x) {
+      const int r = n * 4 / W, w = n * 4 % W;
+      if (w >= n_here) continue;
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < streams; ++k) {
+        const float4 v = reinterpret_cast<const float4*>(all + static_cast<size_t>(k * S + q) * a.rows * W)[n];
+        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+      }
+      *reinterpret_cast<float4*>(out + static_cast<size_t>(r) * a.D + from + w) = t;
+    }
   }
 }
 
 // HEADS layout.  A block goes over tiles of a plane [I][J]; the buckets of a
 // tile are worked out once, in shared memory, and every warp adds up one
-// head's part of the tile.  Each lane has sums of its own ([rows][32 lanes]),
-// 16 bytes of neighbouring elements at a time.  Planes of odd sizes begin
-// anywhere within 16 bytes: a head's tile then begins up to V - 1 elements
-// early, on a boundary, and its buckets are shifted alike.
+// head's part of the tile.  Each lane has sums of its own ([rows + 1][32
+// lanes], the last row for what has no bucket), 16 bytes of neighbouring
+// elements at a time.  Planes of odd sizes as in the forward.
 constexpr int kTileSteps = 8;
-constexpr int kHeadsBytes = 220 * 1024;  // shared memory for a block's sums and buckets
+constexpr int kHeadsBytes = 218 * 1024;  // shared memory for a block's sums and buckets
 
 template <typename T>
 struct HeadTile {
@@ -337,41 +407,45 @@ __global__ void __launch_bounds__(512)
   extern __shared__ float4 smem4[];
   let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-  const int parts = warps / heads, tile_n = parts * kPart;
+  const int parts = warps / heads, tile_n = parts * kPart, own = (a.rows + 1) * 32;
   const int h = blockIdx.y * heads + warp % heads, my_part = warp / heads;
   const bool live = h < a.D;
-  float* const sums = reinterpret_cast<float*>(smem4) + static_cast<size_t>(warp) * a.rows * 32;
-  uint16_t* const ids0 = reinterpret_cast<uint16_t*>(reinterpret_cast<float*>(smem4) + static_cast<size_t>(warps) * a.rows * 32);
-  for (int r = 0; r < a.rows; ++r) sums[r * 32 + lane] = 0.f;
-  const long long total = static_cast<long long>(a.B) * a.D * plane;
+  float* const sums = reinterpret_cast<float*>(smem4) + static_cast<size_t>(warp) * own;
+  uint16_t* const ids0 = reinterpret_cast<uint16_t*>(reinterpret_cast<float*>(smem4) + static_cast<size_t>(warps) * own);
+  __shared__ uint32_t whole0[2][16 * kTileSteps];
+  for (int r = 0; r <= a.rows; ++r) sums[r * 32 + lane] = 0.f;
   const uint32_t tiles = by_tiles.d * a.B;
+  const uint16_t none = static_cast<uint16_t>(a.rows);
 
+  // elements from the boundary at or before the plane (b, h)'s first one
+  auto boundary = [&](uint32_t b) { return static_cast<int>((static_cast<long long>(b) * a.D + h) * plane % V); };
   uint4 next[kTileSteps];
   auto load = [&](uint32_t tile) {
     uint32_t b, t;
     by_tiles.divmod(tile, b, t);
-    const long long base = (static_cast<long long>(b) * a.D + h) * plane;
-    const long long first = base - base % V + static_cast<long long>(t) * tile_n + my_part * kPart + lane * V;
+    const int m = boundary(b);
+    const T* const from = dout + ((static_cast<long long>(b) * a.D + h) * plane - m);
+    const uint32_t first = t * tile_n + my_part * kPart + lane * V, end = plane + m;
+    // what lies behind a plane is the next one, but for the tensor's last, whose last group may be part of 16 bytes
+    const uint32_t whole = b == static_cast<uint32_t>(a.B) - 1 && h == a.D - 1 ? end : end + V - 1;
 #pragma unroll
     for (int u = 0; u < kTileSteps; ++u) {
-      const long long n = first + u * 32 * V;
+      const uint32_t n = first + u * 32 * V;
       next[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (!live || n >= base + plane) continue;
-      if (n + V <= total) {
-        next[u] = __ldcs(reinterpret_cast<const uint4*>(dout + n));
-      } else {  // the tensor's last elements, where they do not fill 16 bytes
+      if (!live || n >= end) continue;
+      if (n + V <= whole) {
+        next[u] = __ldcs(reinterpret_cast<const uint4*>(from + n));
+      } else {
         alignas(16) T last[V] = {};
-        for (int e = 0; n + e < total; ++e) last[e] = dout[n + e];
+        for (int e = 0; e < V; ++e)
+          if (n + e < end) last[e] = from[n + e];
         next[u] = *reinterpret_cast<const uint4*>(last);
       }
     }
   };
 
-  int at = -1;
+  uint32_t at = none;
   float run = 0.f;
-  auto flush = [&] {
-    if (at >= 0) sums[at * 32 + lane] += run;
-  };
   int turn = 0;
   uint32_t tile = blockIdx.x;
   if (tile < tiles) load(tile);
@@ -380,36 +454,39 @@ __global__ void __launch_bounds__(512)
     by_tiles.divmod(tile, b, t);
     uint16_t* const ids = ids0 + turn * (tile_n + V);
     // two buffers: a warp that is still adding the last tile reads the other one
-    stage_ids(a, b, static_cast<long long>(t) * tile_n, tile_n, V, plane, ids);
+    stage_ids<V>(a, b, static_cast<long long>(t) * tile_n, parts * kTileSteps, plane, none, ids, whole0[turn]);
     __syncthreads();
     uint4 now[kTileSteps];
 #pragma unroll
     for (int u = 0; u < kTileSteps; ++u) now[u] = next[u];
     if (tile + gridDim.x < tiles) load(tile + gridDim.x);
     if (!live) continue;
-    const int m = static_cast<int>(((static_cast<long long>(b) * a.D + h) * plane) % V);
+    const int m = boundary(b);
 #pragma unroll
     for (int u = 0; u < kTileSteps; ++u) {
-      uint32_t w[V / 2];
-      shifted_ids<V>(ids + my_part * kPart + u * 32 * V + lane * V, m, w);
-      float v[V];
-      Vec<T>::unpack(now[u], v);
-      const uint32_t same = static_cast<uint32_t>(at) * 0x10001u;
-      bool one = at >= 0;
+      const uint32_t one = whole0[turn][my_part * kTileSteps + u];
+      if (one != kMixed) {  // of the whole warp's elements
+        f2 v[V / 2];
+        Vec<T>::unpack(now[u], v);
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) one = one && w[i] == same;
-      if (one) {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) s += v[e];
-        run += s;
+        for (int i = 1; i < V / 2; ++i) v[0] = add2(v[0], v[i]);
+        const float2 s = split2(v[0]);
+        if (one != at) {
+          sums[at * 32 + lane] += run;
+          at = one;
+          run = 0.f;
+        }
+        run += s.x + s.y;
       } else {
+        uint32_t w[V / 2];
+        shifted_ids<V>(ids + my_part * kPart + u * 32 * V + lane * V, m, w);
+        float v[V];
+        Vec<T>::unpack(now[u], v);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const int k = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-          if (k == kNoBucket) continue;
+          const uint32_t k = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
           if (k != at) {
-            flush();
+            sums[at * 32 + lane] += run;
             at = k;
             run = 0.f;
           }
@@ -418,9 +495,9 @@ __global__ void __launch_bounds__(512)
       }
     }
   }
-  flush();
+  sums[at * 32 + lane] += run;
   __syncwarp();
-  // the lanes' sums, added in a fixed order; then the parts' (in lane 0's column)
+  // the lanes' sums, added in a fixed order into lane 0's column; then the parts'
   for (int r = lane; r < a.rows; r += 32) {
     float t = 0.f;
     for (int l = 0; l < 32; ++l) t += sums[r * 32 + ((l + lane) & 31)];
@@ -432,7 +509,7 @@ __global__ void __launch_bounds__(512)
     if (head >= a.D) continue;
     float t = 0.f;
     for (int k = 0; k < parts; ++k)
-      t += reinterpret_cast<const float*>(smem4)[static_cast<size_t>(k * heads + q) * a.rows * 32 + r * 32];
+      t += reinterpret_cast<const float*>(smem4)[static_cast<size_t>(k * heads + q) * own + r * 32];
     partial[(static_cast<size_t>(blockIdx.x) * a.rows + r) * a.D + head] = t;
   }
 }
@@ -476,7 +553,7 @@ GradSplit split_pair(int rows, long long pairs, int D, int num_sms) {
   g.slices = (groups + g.lanes - 1) / g.lanes;
   g.slice = (groups + g.slices - 1) / g.slices * V;
   g.slices = (D + g.slice - 1) / g.slice;
-  g.warps = std::min(16, kSumBytes / (rows * W * 4));
+  g.warps = std::min(pair_warps(g.lanes), kSumBytes / (rows * W * 4));
   g.S = 1;
   const long long batches = (pairs + 32 / g.lanes * kSteps - 1) / (32 / g.lanes * kSteps);
   // One block for all of a pair's slices reads whole rows, which DRAM serves
@@ -499,7 +576,7 @@ GradSplit split_heads(int rows, int B, long long plane, int H, int num_sms) {
   constexpr int V = Vec<T>::n, kPart = HeadTile<T>::part;
   GradSplit g;
   constexpr int kMost = kHeadsBytes, kIds = 2 * (kPart + V) * 2;  // two buffers of a part's buckets
-  const int own = rows * 32 * 4;
+  const int own = (rows + 1) * 32 * 4;
   const int warps = std::max(1, std::min(16, (kMost - kIds) / own));
   g.slices = (H + warps - 1) / warps;
   g.lanes = (H + g.slices - 1) / g.slices;  // heads of a block
@@ -534,7 +611,7 @@ cudaError_t forward(const RelposArgs& a, const void* table, const void* base, vo
   const uint32_t plane = static_cast<uint32_t>(a.I) * a.J;
   const long long tiles = (static_cast<long long>(plane) + V - 1 + kTile - 1) / kTile;
   // heads of a block: as many as have room for their columns of the table, fewer where that leaves SMs without work
-  const int most = std::min(a.D, kTableBytes / (a.rows * 4));
+  const int most = std::min(a.D, kTableBytes / ((a.rows + 1) * 4));
   int groups = static_cast<int>(std::max<long long>((a.D + most - 1) / most,
                                                     std::min<long long>(a.D, 4 * num_sms / (tiles * a.B))));
   const int heads = (a.D + groups - 1) / groups;
@@ -542,7 +619,7 @@ cudaError_t forward(const RelposArgs& a, const void* table, const void* base, vo
   const int grid = static_cast<int>(std::min<long long>(tiles * a.B, std::max(1, 8 * num_sms / groups)));
   cudaError_t e = allow_smem<k7_relpos_heads<T, Tab>>(kTableBytes);
   if (e != cudaSuccess) return e;
-  k7_relpos_heads<T, Tab><<<dim3(grid, groups), kHeadThreads, heads * a.rows * 4, s>>>(
+  k7_relpos_heads<T, Tab><<<dim3(grid, groups), kHeadThreads, heads * (a.rows + 1) * 4, s>>>(
       a, static_cast<const Tab*>(table), static_cast<const T*>(base), static_cast<T*>(out), plane,
       FastDiv(static_cast<uint32_t>(tiles)), heads);
   return cudaGetLastError();

@@ -108,17 +108,26 @@ __device__ __forceinline__ __half from_f32<__half>(float v) {
   return __float2half_rn(v);
 }
 
-// The table row of positions (b, i), (b, j), given as indexes into the position
-// arrays; -1 for padding.
-__device__ __forceinline__ int relpos_bucket(const RelposArgs& a, uint32_t qi, uint32_t kj) {
-  if (a.q_group) {
-    const int gq = a.q_group[qi], gk = a.k_group[kj];
-    if ((gq | gk) < 0) return -1;
-    if (gq != gk) return a.rows - 1;
+// What the bucket of a pair is worked out from: loaded first, and looked at later.
+struct RelposPair {
+  int q, k, gq, gk;
+  __device__ __forceinline__ void load(const RelposArgs& a, uint32_t qi, uint32_t kj) {
+    q = a.q_pos[qi], k = a.k_pos[kj], gq = gk = 0;
+    if (a.q_group) gq = a.q_group[qi], gk = a.k_group[kj];
   }
-  const long long far = static_cast<long long>(a.q_pos[qi]) - a.k_pos[kj];
-  const int d = static_cast<int>(far < a.lo ? a.lo : far > a.M ? a.M : far) - a.lo;
-  return a.lut ? a.lut[d] : d;
+  __device__ __forceinline__ void none() { q = k = 0, gq = gk = -1; }
+  // The table row; -1 for padding, and for none.
+  __device__ __forceinline__ int bucket(const RelposArgs& a) const {
+    const long long far = static_cast<long long>(q) - k;
+    const int d = static_cast<int>(far < a.lo ? a.lo : far > a.M ? a.M : far) - a.lo;
+    const int row = a.lut ? a.lut[d] : d;
+    return (gq | gk) < 0 ? -1 : gq != gk ? a.rows - 1 : row;
+  }
+};
+__device__ __forceinline__ int relpos_bucket(const RelposArgs& a, uint32_t qi, uint32_t kj) {
+  RelposPair p;
+  p.load(a, qi, kj);
+  return p.bucket(a);
 }
 
 }  // namespace trimul
