@@ -214,7 +214,11 @@ __global__ void __launch_bounds__(kHeadThreads)
 // What makes these sums cheap is that neighbours share a bucket: all pairs
 // farther than M, and in LOG buckets runs of near ones.  A run is added up in
 // registers and goes to shared memory when it ends.
-constexpr int kSumBytes = 200 * 1024;  // shared memory for a block's sums
+// Shared memory for a block's sums.  With the 1 KB that every block has besides
+// it is one of the sizes that an SM can split its 256 KB by, and leaves 60 KB
+// for L1, through which the loads on their way go: the next size leaves 28 KB,
+// and cost the pair gradient a fifth (2048^2 x 256 with 66 rows: 415 us to 340).
+constexpr int kSumBytes = 195 * 1024;
 
 // PAIR layout.  A warp has sums of its own, [rows][W channels], for one slice
 // of at most W channels.  G lanes (16 bytes each) share a pair, so the warp
@@ -327,14 +331,17 @@ __global__ void __launch_bounds__(pair_warps(G) * 32)
       join(k0, t);
       return;
     }
-    // pairs that share their step's bucket with another pair, and with all the others
+    // Pairs that share their step's bucket take turns, by their rank among
+    // these (in bits 16 on); steps of one bucket join the run.
     constexpr unsigned step = P == 32 ? 0xffffffffu : (1u << (P % 32)) - 1;
     unsigned some[kPerLane], all[kPerLane];
 #pragma unroll
     for (int q = 0; q < kPerLane; ++q) {
       const unsigned like = (__match_any_sync(0xffffffffu, k_of[q]) >> (lane / P * P)) & step;
-      some[q] = __ballot_sync(0xffffffffu, __popc(like) > 1 && k_of[q] >= 0);
+      const int rank = __popc(like & ((1u << (lane % P)) - 1));
+      some[q] = __ballot_sync(0xffffffffu, rank > 0 && k_of[q] >= 0);
       all[q] = __ballot_sync(0xffffffffu, like == step && k_of[q] >= 0);
+      if (k_of[q] >= 0) k_of[q] |= rank << 16;
     }
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
@@ -342,10 +349,10 @@ __global__ void __launch_bounds__(pair_warps(G) * 32)
       Vec<T>::unpack(from[u], v);
       const int at_bit = u * P % 32;
       if ((all[u * P / 32] >> at_bit) & 1) {
-        join(k, v);
+        join(k & 0xffff, v);
       } else if (some[u * P / 32] & (step << at_bit)) {
 #pragma unroll 1
-        for (int q = 0; q < P; ++q) add(k, v, slot == q && k >= 0);
+        for (int turn = 0; __any_sync(0xffffffffu, k >> 16 >= turn); ++turn) add(k & 0xffff, v, k >> 16 == turn);
       } else {
         add(k, v, k >= 0);
       }
@@ -539,15 +546,18 @@ struct GradSplit {
   int S;  // PAIR: slices of a block
 };
 
-// PAIR: at least eight warps' sums have to fit an SM's shared memory for
-// enough loads to be in flight, so the slice is at most 64 channels and
-// narrower for long tables; slices are as even as 16-byte groups allow.
+// PAIR: a warp's slice is 64 channels where these divide D and twelve warps'
+// sums have room, else 32: sixteen warps, and more pairs that meet in a bucket
+// (1024^2 x 256, us: 65 rows 101 to 100, LOG 32 rows 117 to 138, 66 rows 128
+// to 114; 2048^2 x 96: 170 to 141).  Narrower for long tables, whose sums
+// leave room for few warps.  Slices are as even as 16-byte groups allow.
 template <typename T>
 GradSplit split_pair(int rows, long long pairs, int D, int num_sms) {
   constexpr int V = Vec<T>::n;
   GradSplit g;
   int W = V;
-  while (W < D && W < 64 && rows * 2 * W * 4 * 8 <= kSumBytes) W *= 2;
+  while (W < D && W < 32 && rows * 2 * W * 4 * 6 <= kSumBytes) W *= 2;
+  if (D % 64 == 0 && rows * 64 * 4 * pair_warps(64 / V) <= kSumBytes) W = 64;
   g.lanes = W / V;
   const int groups = D / V;  // of 16 bytes
   g.slices = (groups + g.lanes - 1) / g.lanes;
@@ -558,8 +568,8 @@ GradSplit split_pair(int rows, long long pairs, int D, int num_sms) {
   const long long batches = (pairs + 32 / g.lanes * kSteps - 1) / (32 / g.lanes * kSteps);
   // One block for all of a pair's slices reads whole rows, which DRAM serves
   // better, but writes sums of all channels a block: worth it once a warp has
-  // some sixteen batches (2048^2 x 256: 479 us against 559; 256^2 x 128, with
-  // two batches a warp: 19.2 against 16.3).
+  // some sixteen batches (when written, 2048^2 x 256: 479 us against 559; 256^2
+  // x 128, with two batches a warp: 19.2 against 16.3).
   if (g.slices <= g.warps && batches >= 16ll * (g.warps / g.slices) * num_sms) {
     g.S = g.slices;
     g.slices = 1;
