@@ -223,21 +223,20 @@ constexpr int kSumBytes = 195 * 1024;
 // PAIR layout.  A warp has sums of its own, [rows][W channels], for one slice
 // of at most W channels.  G lanes (16 bytes each) share a pair, so the warp
 // takes 32 / G neighbouring pairs at a time, its slots, and kSteps of these
-// make a batch.  kBuffers batches are in registers or on their way, which is
-// what DRAM's latency asks of the twelve warps that have room for their sums.
+// make a batch.  One batch is worked on while the next one is on its way.
 // A batch of one bucket is added up in registers, and joins the run of batches
 // before it, as does a step of one bucket in a mixed batch; the pairs of other
 // steps go to shared memory at once.  The buckets are worked out one pair a
 // lane and handed round by shuffles.
 constexpr int kSteps = 8;
 // Warps of a block: few lanes a pair means many pairs a lane, and registers for them.
-constexpr int pair_warps(int G) { return G >= 8 ? 12 : G == 4 ? 16 : 8; }
+constexpr int pair_warps(int G) { return G >= 4 ? 16 : 8; }
 
 template <typename T, int G>
 __global__ void __launch_bounds__(pair_warps(G) * 32)
     k7_relpos_grad_pair(RelposArgs a, const T* __restrict__ dout, float* part, uint32_t pairs, int slice, int S) {
   constexpr int V = Vec<T>::n, W = G * V, P = 32 / G, kBatch = P * kSteps, kPerLane = (kBatch + 31) / 32;
-  constexpr int kBuffers = G >= 8 ? 3 : 2;
+  constexpr int kBuffers = 2;
   extern __shared__ float4 smem4[];
   let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
@@ -546,10 +545,10 @@ struct GradSplit {
   int S;  // PAIR: slices of a block
 };
 
-// PAIR: a warp's slice is 64 channels where these divide D and twelve warps'
-// sums have room, else 32: sixteen warps, and more pairs that meet in a bucket
-// (1024^2 x 256, us: 65 rows 101 to 100, LOG 32 rows 117 to 138, 66 rows 128
-// to 114; 2048^2 x 96: 170 to 141).  Narrower for long tables, whose sums
+// PAIR: a warp's slice is 64 channels where these divide D and ten warps' sums
+// have room, else 32: more warps, and more pairs that meet in a bucket
+// (1024^2 x 256, us, 64 to 32: 65 rows 101 to 100, LOG 32 rows 99 to 138, 66
+// rows with eight warps 128 to 114; 2048^2 x 96: 170 to 141).  Narrower for long tables, whose sums
 // leave room for few warps.  Slices are as even as 16-byte groups allow.
 template <typename T>
 GradSplit split_pair(int rows, long long pairs, int D, int num_sms) {
@@ -557,7 +556,8 @@ GradSplit split_pair(int rows, long long pairs, int D, int num_sms) {
   GradSplit g;
   int W = V;
   while (W < D && W < 32 && rows * 2 * W * 4 * 6 <= kSumBytes) W *= 2;
-  if (D % 64 == 0 && rows * 64 * 4 * pair_warps(64 / V) <= kSumBytes) W = 64;
+  const int fit64 = std::min(pair_warps(64 / V), kSumBytes / (rows * 64 * 4));
+  if (D % 64 == 0 && fit64 / (D / 64) * (D / 64) >= 10) W = 64;
   g.lanes = W / V;
   const int groups = D / V;  // of 16 bytes
   g.slices = (groups + g.lanes - 1) / g.lanes;

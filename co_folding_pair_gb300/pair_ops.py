@@ -60,10 +60,12 @@ def _one_of(table, value, name):
         raise ValueError(f"{name} must be one of {[k for k in table if k is not None]}, got {value!r}") from None
 
 
-def _type(dtype, name, kinds=(torch.bfloat16, torch.float32)):
-    if dtype not in kinds:
-        raise TypeError(f"{name} must be one of {list(kinds)}, got {dtype}")
-    return _TYPES[dtype]
+def _type(dtype, name, most=1) -> int:
+    """The number of an element type: bf16 or float32, or (most 2) float16."""
+    kind = _TYPES.get(dtype, 3)
+    if kind > most:
+        raise TypeError(f"{name} must be one of {[k for k, v in _TYPES.items() if v <= most]}, got {dtype}")
+    return kind
 
 
 def _cuda(t, name) -> int:
@@ -154,12 +156,13 @@ def trimul_relpos_forward(r: RelPosPlan, table, q_pos, k_pos=None, q_group=None,
     queries'); base, if given, sets the type of the result (else `dtype`); `out` may be `base`."""
     lay = _one_of(_LAYOUTS, layout, "layout")
     B, I, J, k_pos, k_group = _positions(r, q_pos, k_pos, q_group, k_group)
-    tt = _type(table.dtype, "table")
+    kind = table.dtype
+    tt = _type(kind, "table")
     if table.dim() != 2 or table.shape[0] != r.rows:
         raise ValueError(f"table must be [{r.rows}, D], got {tuple(table.shape)}")
     D = table.shape[1]
-    if not _fits(table, table.dtype, (r.rows, D), r.device):
-        _refuse(table, table.dtype, (r.rows, D), r.device, "table")
+    if not _fits(table, kind, (r.rows, D), r.device):
+        _refuse(table, kind, (r.rows, D), r.device, "table")
     shape = (B, I, J, D) if lay == 0 else (B, D, I, J)
     dtype = dtype if base is None else base.dtype
     ot = _type(dtype, "dtype" if base is None else "base")
@@ -214,11 +217,13 @@ class RelPos:
         self.plan = trimul_relpos_create(kind, max_distance, num_buckets, bidirectional, groups, device)
         self.rows = self.plan.rows
 
-    def forward(self, table, q_pos, k_pos=None, **kw):
-        return trimul_relpos_forward(self.plan, table, q_pos, k_pos, **kw)
+    def forward(self, table, q_pos, k_pos=None, q_group=None, k_group=None, base=None, layout="pair",
+                dtype=torch.bfloat16, out=None, stream=None, flags: int = 0):
+        return trimul_relpos_forward(self.plan, table, q_pos, k_pos, q_group, k_group, base, layout, dtype, out, stream, flags)
 
-    def backward(self, dout, q_pos, k_pos=None, **kw):
-        return trimul_relpos_backward(self.plan, dout, q_pos, k_pos, **kw)
+    def backward(self, dout, q_pos, k_pos=None, q_group=None, k_group=None, layout="pair", dtable=None, stream=None,
+                 flags: int = 0):
+        return trimul_relpos_backward(self.plan, dout, q_pos, k_pos, q_group, k_group, layout, dtable, stream, flags)
 
     def free(self):
         trimul_relpos_destroy(self.plan)
@@ -260,15 +265,24 @@ def _residual(x, u, params, post_norm, pre_norm, gate, gate_sigmoid, mask, scale
             _refuse(gate, bf, gate.shape, dev, "gate")
     if mask is not None and not _fits(mask, bf, (B, I, J), dev):
         _refuse(mask, bf, (B, I, J), dev, "mask")
-    at = dict.fromkeys(RESIDUAL_PARAMS)
-    for k, v in params.items():
-        if k not in at:
+    at = []
+    for k in RESIDUAL_PARAMS:
+        v = params.get(k)
+        if v is None:
+            at.append(None)
+        else:
+            if not _fits(v, torch.float32, (D,), dev):
+                _refuse(v, torch.float32, (D,), dev, k)
+            at.append(v.data_ptr())
+    for k in params:
+        if k not in RESIDUAL_PARAMS:
             raise ValueError(f"unknown parameter {k!r}: {list(RESIDUAL_PARAMS)} are taken")
-        if not _fits(v, torch.float32, (D,), dev):
-            _refuse(v, torch.float32, (D,), dev, k)
-        at[k] = v.data_ptr()
-    p = _lib.ResidualParams(D, _type(x.dtype, "x"), _one_of(_NORMS, post_norm, "post_norm"),
-                            _one_of(_NORMS, pre_norm, "pre_norm"), *at.values(), kind, 1 if gate_sigmoid else 0, scale, eps)
+    xt = _type(x.dtype, "x")
+    post, pre = _NORMS.get(post_norm), _NORMS.get(pre_norm)
+    if post is None or pre is None:
+        _one_of(_NORMS, post_norm, "post_norm")
+        _one_of(_NORMS, pre_norm, "pre_norm")
+    p = _lib.ResidualParams(D, xt, post, pre, *at, kind, 1 if gate_sigmoid else 0, scale, eps)
     return p, dev, kind
 
 
@@ -338,13 +352,17 @@ class Residual:
 
     def __init__(self, params=None, post_norm=None, pre_norm=None, gate_sigmoid=False, scale=1.0, eps=1e-5):
         self.params = dict(params or {})
-        self.kw = {"post_norm": post_norm, "pre_norm": pre_norm, "gate_sigmoid": gate_sigmoid, "scale": scale, "eps": eps}
+        self.post_norm, self.pre_norm = post_norm, pre_norm
+        self.gate_sigmoid, self.scale, self.eps = gate_sigmoid, scale, eps
 
-    def forward(self, x, u, **kw):
-        return trimul_residual_forward(x, u, self.params, **self.kw, **kw)
+    def forward(self, x, u, gate=None, mask=None, out=None, normed=None, stream=None, flags: int = 0):
+        return trimul_residual_forward(x, u, self.params, self.post_norm, self.pre_norm, gate, self.gate_sigmoid, mask,
+                                       self.scale, self.eps, out, normed, stream, flags)
 
-    def backward(self, x, u, dout, **kw):
-        return trimul_residual_backward(x, u, dout, self.params, **self.kw, **kw)
+    def backward(self, x, u, dout, dnormed=None, gate=None, mask=None, dout2=None, dx=None, du=None, dgate=None,
+                 grads=None, stream=None, flags: int = 0):
+        return trimul_residual_backward(x, u, dout, self.params, self.post_norm, self.pre_norm, gate, self.gate_sigmoid,
+                                        mask, self.scale, self.eps, dnormed, dout2, dx, du, dgate, grads, stream, flags)
 
 
 # ------------------------------------------------------------------ gradient norm and clipping
@@ -364,7 +382,7 @@ class GradSet:
         self.torch_device = torch.device("cuda", self.device)
         self.table = (_lib.GradTensor * len(tensors))()
         for k, (t, o) in enumerate(zip(tensors, outs)):
-            kind = _type(t.dtype, f"tensors[{k}]", tuple(_TYPES))
+            kind = _type(t.dtype, f"tensors[{k}]", 2)
             if not _fits(t, t.dtype, t.shape, self.device):
                 _refuse(t, t.dtype, t.shape, self.device, f"tensors[{k}]")
             if o is not t and not _fits(o, t.dtype, t.shape, self.device):

@@ -174,6 +174,43 @@ def test_relpos_scattered_positions(P):
             within(r.backward(dout, pos, layout=layout), ref, 1024 * U * mag, layout)
 
 
+@pytest.mark.parametrize("layout,D,dt", [("heads", 6, BF), ("heads", 20, BF), ("heads", 6, F32), ("pair", 40, BF), ("pair", 16, F32)])
+def test_relpos_gradient_keeps_what_is_not_finite_apart(P, layout, D, dt):
+    """An infinity or NaN reaches its own bucket and channel; all others are as without it."""
+    g = rng_of(12)
+    r = P.RelPos("linear", 20)
+    pos = torch.arange(77, device="cuda").int().repeat(2, 1).contiguous()
+    d = randn(g, *((2, 77, 77, D) if layout == "pair" else (2, D, 77, 77)), dtype=dt)
+    b = O.buckets("linear", 20, 41, True, pos.cpu().numpy(), pos.cpu().numpy())
+    ref, mag = O.relpos_backward(f64(d), b, 41, layout)
+    view = d if layout == "pair" else d.permute(0, 2, 3, 1)
+    view[0, 40, 33, 2] = math.inf    # bucket 27
+    view[1, 3, 70, D - 1] = math.nan  # bucket 0
+    view[1, 76, 76, 0] = -math.inf   # bucket 20
+    got = f64(r.backward(d, pos, layout=layout))
+    assert got[27, 2] == math.inf and math.isnan(got[0, D - 1]) and got[20, 0] == -math.inf
+    for at in ((27, 2), (0, D - 1), (20, 0)):
+        got[at] = ref[at]
+    assert (np.abs(got - ref) <= 1024 * U * mag).all()
+
+
+@pytest.mark.parametrize("layout", ["pair", "heads"])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_relpos_gradient_of_one_sign(P, layout, dt):
+    """A million values of one size in one bucket: no rounding goes one way only.
+
+    The sums of 1.5 and of 2^20 times it are exact in fp32 in any order; 1 + 2^-7 times up to 2^20 needs 28 bits, so
+    a chain of additions rounds (up or down) by at most half an ulp each: held to 128 U of the sum."""
+    r = P.RelPos("linear", 1)
+    pos = torch.zeros(1, 1024, dtype=torch.int32, device="cuda")
+    shape = (1, 1024, 1024, 8) if layout == "pair" else (1, 8, 1024, 1024)
+    for v in (1.5, 1 + 2.0**-7):
+        got = f64(r.backward(torch.full(shape, v, dtype=dt, device="cuda"), pos, layout=layout))
+        ref = np.zeros((3, 8))
+        ref[1] = v * 2.0**20
+        assert (np.abs(got - ref) <= (0 if v == 1.5 else 128 * U * ref)).all()
+
+
 def test_relpos_is_its_gradients_adjoint(P):
     """sum dout (forward(T + E) - forward(T)) = sum dtable E: the forward is linear, with small whole numbers exact."""
     g = rng_of(9)
