@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
     else
       turn(std::false_type());
   }
+  if (!a.part) return;  // no parameter's gradient is wanted
   // the block's column sums, its rows added in order
   __shared__ float s[kRows][G * 8 + 1];
 #pragma unroll
@@ -531,35 +532,46 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
 }
 
 // The parameters' gradients from the blocks' column sums: 32 channels a block,
-// eight groups of parts side by side; blockIdx.y 0 for S0 and S1, 1 for the
+// 32 groups of parts side by side; blockIdx.y 0 for S0 and S1, 1 for the
 // pre-norm's two.
-__global__ void __launch_bounds__(256) k8_residual_sum(ResidualArgs a, int blocks) {
-  __shared__ float s[2][8][32];
-  const int lane = threadIdx.x % 32, n = blockIdx.x * 32 + lane, k0 = threadIdx.x / 32, D = a.p.D;
-  float t[2] = {};
+__global__ void __launch_bounds__(1024) k8_residual_sum(ResidualArgs a, int blocks) {
+  __shared__ float2 s[32][33];
+  const int lane = threadIdx.x % 32, group = threadIdx.x / 32, D = a.p.D;
+  int n = blockIdx.x * 32 + lane;
+  float2 t = make_float2(0.f, 0.f);
   after_previous();
   if (n < D) {
-#pragma unroll 8
-    for (int k = k0; k < blocks; k += 8) {
+#pragma unroll 4
+    for (int k = group; k < blocks; k += 32) {
       const float* const p = a.part + (static_cast<size_t>(k) * RESIDUAL_SUMS + 2 * blockIdx.y) * D + n;
-      t[0] += p[0];
-      t[1] += p[D];
+      t.x += p[0];
+      t.y += p[D];
     }
   }
-  s[0][k0][lane] = t[0], s[1][k0][lane] = t[1];
+  s[group][lane] = t;
   __syncthreads();
-  if (k0 != 0 || n >= D) return;
+  // a warp a channel from here on
+  t = s[lane][group];
 #pragma unroll
-  for (int k = 1; k < 8; ++k) t[0] += s[0][k][lane], t[1] += s[1][k][lane];
+  for (int o = 16; o > 0; o >>= 1) {
+    t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+    t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+  }
+  n = blockIdx.x * 32 + group;
+  if (lane != 0 || n >= D) return;
   if (blockIdx.y == 1) {
-    if (a.g.pre_gamma) a.g.pre_gamma[n] = t[0];
-    if (a.g.pre_beta) a.g.pre_beta[n] = t[1];
+    if (a.g.pre_gamma) a.g.pre_gamma[n] = t.x;
+    if (a.g.pre_beta) a.g.pre_beta[n] = t.y;
     return;
   }
   const float ch = a.p.channel ? a.p.channel[n] : 1.f;
-  if (a.g.post_gamma) a.g.post_gamma[n] = ch * t[0];
-  if (a.g.post_beta) a.g.post_beta[n] = ch * t[1];
-  if (a.g.channel) a.g.channel[n] = (a.p.post_gamma ? a.p.post_gamma[n] : 1.f) * t[0] + (a.p.post_beta ? a.p.post_beta[n] : 0.f) * t[1];
+  if (a.g.post_gamma) a.g.post_gamma[n] = ch * t.x;
+  if (a.g.post_beta) a.g.post_beta[n] = ch * t.y;
+  if (a.g.channel) a.g.channel[n] = (a.p.post_gamma ? a.p.post_gamma[n] : 1.f) * t.x + (a.p.post_beta ? a.p.post_beta[n] : 0.f) * t.y;
+}
+
+bool any_sum(const trimul_residual_grads& g) {
+  return g.post_gamma || g.post_beta || g.pre_gamma || g.pre_beta || g.channel;
 }
 
 int lanes_of(int D) {
@@ -586,11 +598,13 @@ cudaError_t forward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStrea
 template <typename T, int G>
 cudaError_t backward(const ResidualArgs& a, uint32_t rows, int num_sms, cudaStream_t s) {
   constexpr int kStage = kBackwardDepth * kBackwardThreads * 16;
+  ResidualArgs b = a;
+  if (!any_sum(a.g)) b.part = nullptr;
   cudaError_t e = allow_smem<k8_residual_bwd<T, G>>(backward_slots<T>(true, true, true) * kStage);
   if (e != cudaSuccess) return e;
   const int grid = blocks_for(a.p.D, rows, kBackwardThreads, 1, kBackwardBlocks * num_sms);
   const int slots = backward_slots<T>(a.gate, a.dout2, a.p.pre_norm != TRIMUL_NORM_NONE);
-  k8_residual_bwd<T, G><<<grid, kBackwardThreads, slots * kStage, s>>>(a, rows);
+  k8_residual_bwd<T, G><<<grid, kBackwardThreads, slots * kStage, s>>>(b, rows);
   return cudaGetLastError();
 }
 
@@ -629,8 +643,8 @@ cudaError_t launch_residual_backward(const ResidualArgs& a, int num_sms, cudaStr
   } else {
     BY_LANES(backward, bf)
   }
-  if (e != cudaSuccess) return e;
-  return launch_early(k8_residual_sum, dim3((a.p.D + 31) / 32, 2), 256, s, a,
+  if (e != cudaSuccess || !any_sum(a.g)) return e;
+  return launch_early(k8_residual_sum, dim3((a.p.D + 31) / 32, 2), 1024, s, a,
                       blocks_for(a.p.D, rows, kBackwardThreads, 1, kBackwardBlocks * num_sms));
 }
 
