@@ -132,33 +132,47 @@ __device__ __forceinline__ void copies_wait() {  // until at most N groups are o
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's eight elements of T in ring slots kThreads apart, one slot (bf16) or two (fp32).
-template <int kThreads>
-__device__ __forceinline__ void copy8(uint4* to, const __nv_bfloat16* from) {
-  copy16(to, from);
+// Eight elements a lane of a row of D, in ring slots kThreads apart: one slot
+// (bf16), which the lane copies and reads itself, or two (fp32).  There, the
+// lanes of a row copy its 16-byte groups in order, the first G of them to the
+// first slot and the others to the second, so that every instruction reads
+// whole sectors; a lane's two groups are copied by others, and the warp has to
+// meet before they are read, and before they are written again (meet).
+template <int kThreads, int G>
+__device__ __forceinline__ void copy8(uint4* to, const __nv_bfloat16* row, int D) {
+  const int i = threadIdx.x % G;
+  copy16(to, row + i * 8);
 }
-template <int kThreads>
-__device__ __forceinline__ void copy8(uint4* to, const float* from) {
-  copy16(to, from);
-  copy16(to + kThreads, from + 4);
+template <int kThreads, int G>
+__device__ __forceinline__ void copy8(uint4* to, const float* row, int D) {
+  const int i = threadIdx.x % G;
+  if (i * 4 < D) copy16(to, row + i * 4);
+  if ((G + i) * 4 < D) copy16(to + kThreads, row + (G + i) * 4);
+}
+template <typename T>
+__device__ __forceinline__ void meet() {
+  if (sizeof(T) == 4) __syncwarp();
 }
 __device__ __forceinline__ F8 widen8(const uint4 v) {
   return F8{{unpack_bf162(v.x), unpack_bf162(v.y), unpack_bf162(v.z), unpack_bf162(v.w)}};
 }
 // The turns over whole blocks of rows without a mask need not look whether a
 // row is there; the others (kAsk) read zeros where it is not.
-template <bool kAsk, int kThreads>
+template <bool kAsk, int kThreads, int G>
 __device__ __forceinline__ F8 take8(const uint4* from, bool on, __nv_bfloat16) {
   return widen8(!kAsk || on ? from[0] : make_uint4(0u, 0u, 0u, 0u));
 }
-template <bool kAsk, int kThreads>
+template <bool kAsk, int kThreads, int G>
 __device__ __forceinline__ F8 take8(const uint4* from, bool on, float) {
+  const int i = threadIdx.x % G;
+  auto group = [&](int p) { return reinterpret_cast<const ulonglong2*>(from - i + p % G + p / G * kThreads)[0]; };
   const ulonglong2 z = make_ulonglong2(0, 0);
-  const ulonglong2 a = !kAsk || on ? reinterpret_cast<const ulonglong2*>(from)[0] : z;
-  const ulonglong2 b = !kAsk || on ? reinterpret_cast<const ulonglong2*>(from)[kThreads] : z;
+  const ulonglong2 a = !kAsk || on ? group(2 * i) : z;
+  const ulonglong2 b = !kAsk || on ? group(2 * i + 1) : z;
   return F8{{a.x, a.y, b.x, b.y}};
 }
-// The slots of a lane past D, which nothing is copied to.
+
+// Slots that nothing is copied to hold zeros.
 __device__ __forceinline__ void clear_slots(uint4* own, int n, int threads) {
   for (int k = 0; k < n; ++k) own[k * threads] = make_uint4(0u, 0u, 0u, 0u);
 }
@@ -279,7 +293,7 @@ __global__ void __launch_bounds__(kForwardThreads, kForwardBlocks) k8_residual_f
   const int slots = forward_slots<T>(a.gate);
   const uint32_t step = gridDim.x * kRows * R;
   uint4* const own = ring + threadIdx.x;
-  if (!live) clear_slots(own, kDepth * R * slots, kThreads);
+  if (!live || sizeof(T) == 4) clear_slots(own, kDepth * R * slots, kThreads);
   // rows are below 2^31 and steps below 2^20: sums of a few stay within 32 bits
   uint32_t row = blockIdx.x * kRows * R + threadIdx.x / G;
   size_t at = static_cast<size_t>(row) * a.p.D + c;
@@ -288,11 +302,13 @@ __global__ void __launch_bounds__(kForwardThreads, kForwardBlocks) k8_residual_f
   auto fetch = [&](uint32_t row, size_t at, int stage) {
 #pragma unroll
     for (int r = 0; r < R; ++r, row += kRows, at += next) {
-      if (live && row < rows) {
+      if (row < rows) {
         uint4* const to = own + (stage * R + r) * slots * kThreads;
-        copy8<kThreads>(to, static_cast<const T*>(a.x) + at);
-        copy16(to + kSlots<T> * kThreads, a.u + at);
-        if (a.gate) copy16(to + (kSlots<T> + 1) * kThreads, gate_row(a, row) + c);
+        if (live || sizeof(T) == 4) copy8<kThreads, G>(to, static_cast<const T*>(a.x) + (at - c), a.p.D);
+        if (live) {
+          copy16(to + kSlots<T> * kThreads, a.u + at);
+          if (a.gate) copy16(to + (kSlots<T> + 1) * kThreads, gate_row(a, row) + c);
+        }
       }
     }
     copies_end();
@@ -308,8 +324,10 @@ __global__ void __launch_bounds__(kForwardThreads, kForwardBlocks) k8_residual_f
     bool on[R];
     float m[R], unused[R];
     F8 x[R], y[R];
+    meet<T>();
     fetch(row + (kDepth - 1) * step, at + (kDepth - 1) * stride, (stage + kDepth - 1) % kDepth);
     copies_wait<kDepth - 1>();
+    meet<T>();
     const uint4* const from = own + stage * R * slots * kThreads;
     stage = (stage + 1) % kDepth;
 #pragma unroll
@@ -318,8 +336,8 @@ __global__ void __launch_bounds__(kForwardThreads, kForwardBlocks) k8_residual_f
       on[r] = live && (!kAsk || mine < rows);
       m[r] = kAsk ? bf16_lo(m_next[r]) : 1.f;
       if (kAsk) m_next[r] = mask_of(a, mine + step, rows);
-      x[r] = take8<kAsk, kThreads>(from + r * slots * kThreads, on[r], T());
-      y[r] = take8<kAsk, kThreads>(from + (r * slots + kSlots<T>) * kThreads, on[r], bf());
+      x[r] = take8<kAsk, kThreads, G>(from + r * slots * kThreads, on[r], T());
+      y[r] = take8<kAsk, kThreads, G>(from + (r * slots + kSlots<T>) * kThreads, on[r], bf());
     }
     if (a.p.post_norm != TRIMUL_NORM_NONE) normalise<G>(y, unused, a.p.post_norm, d_f, inv_d, a.p.eps, live);
 #pragma unroll
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(kForwardThreads, kForwardBlocks) k8_residual_f
       for (int e = 0; e < 4; ++e) y[r].v[e] = fma2(y[r].v[e], A.v[e], B.v[e]);
       F8 g = {{both(m[r]), both(m[r]), both(m[r]), both(m[r])}};
       if (a.gate) {
-        g = take8<kAsk, kThreads>(from + (r * slots + kSlots<T> + 1) * kThreads, on[r], bf());
+        g = take8<kAsk, kThreads, G>(from + (r * slots + kSlots<T> + 1) * kThreads, on[r], bf());
         if (a.p.gate_sigmoid) {
           sigmoid_codes(g);
           g = gate_values(g, true);
@@ -397,19 +415,25 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
   const int at_u = kSlots<T> * (a.dout2 ? 3 : 2), at_g = at_u + 1, at_n = at_g + (a.gate ? 1 : 0);
   const uint32_t step = gridDim.x * kRows;
   uint4* const own = ring + threadIdx.x;
-  if (!live) clear_slots(own, kDepth * slots, kThreads);
+  if (!live || sizeof(T) == 4) clear_slots(own, kDepth * slots, kThreads);
   uint32_t row = blockIdx.x * kRows + threadIdx.x / G;
   size_t at = static_cast<size_t>(row) * a.p.D + c;
   const size_t stride = static_cast<size_t>(step) * a.p.D;
   auto fetch = [&](uint32_t row, size_t at, int stage) {
-    if (live && row < rows) {
+    if (row < rows) {
       uint4* const to = own + stage * slots * kThreads;
-      copy8<kThreads>(to, static_cast<const T*>(a.dout) + at);
-      if (pre) copy8<kThreads>(to + kSlots<T> * kThreads, static_cast<const T*>(a.x) + at);  // only X's statistics need x
-      if (a.dout2) copy8<kThreads>(to + 2 * kSlots<T> * kThreads, static_cast<const T*>(a.dout2) + at);
-      copy16(to + at_u * kThreads, a.u + at);
-      if (a.gate) copy16(to + at_g * kThreads, gate_row(a, row) + c);
-      if (pre) copy16(to + at_n * kThreads, a.dnormed + at);
+      if (live || sizeof(T) == 4) {
+        const size_t first = at - c;
+        copy8<kThreads, G>(to, static_cast<const T*>(a.dout) + first, a.p.D);
+        // only X's statistics need x
+        if (pre) copy8<kThreads, G>(to + kSlots<T> * kThreads, static_cast<const T*>(a.x) + first, a.p.D);
+        if (a.dout2) copy8<kThreads, G>(to + 2 * kSlots<T> * kThreads, static_cast<const T*>(a.dout2) + first, a.p.D);
+      }
+      if (live) {
+        copy16(to + at_u * kThreads, a.u + at);
+        if (a.gate) copy16(to + at_g * kThreads, gate_row(a, row) + c);
+        if (pre) copy16(to + at_n * kThreads, a.dnormed + at);
+      }
     }
     copies_end();
   };
@@ -425,21 +449,23 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
     if (kAsk) m_next = mask_of(a, row + step, rows);
     const bool real = on && m != 0.f;  // padding: zeros, whatever the tensors hold
     const f2 k = both(a.p.scale * m);
+    meet<T>();
     fetch(row + (kDepth - 1) * step, at + (kDepth - 1) * stride, (stage + kDepth - 1) % kDepth);
     copies_wait<kDepth - 1>();
+    meet<T>();
     const uint4* const from = own + stage * slots * kThreads;
     stage = (stage + 1) % kDepth;
     auto slot = [&](int n) { return from + n * kThreads; };
-    F8 yh[1] = {take8<kAsk, kThreads>(slot(at_u), real, bf())}, gate;
+    F8 yh[1] = {take8<kAsk, kThreads, G>(slot(at_u), real, bf())}, gate;
     float post_r[1], pre_r[1];
     if (post) normalise<G>(yh, post_r, a.p.post_norm, d_f, inv_d, a.p.eps, live);
     if (a.gate) {
-      gate = take8<kAsk, kThreads>(slot(at_g), real, bf());
+      gate = take8<kAsk, kThreads, G>(slot(at_g), real, bf());
       if (a.p.gate_sigmoid) sigmoid_codes(gate);
     }
     F8 d = {};
     if (pre) {
-      F8 x[1] = {take8<kAsk, kThreads>(slot(kSlots<T>), real, T())};
+      F8 x[1] = {take8<kAsk, kThreads, G>(slot(kSlots<T>), real, T())};
       {
         const F8 pg = par(0), pb = par(1);
         F8 w = {{k, k, k, k}};
@@ -453,7 +479,7 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
       }
       normalise<G>(x, pre_r, a.p.pre_norm, d_f, inv_d, a.p.eps, live);
       const F8 ng = par(2);
-      d = take8<kAsk, kThreads>(slot(at_n), real, bf());
+      d = take8<kAsk, kThreads, G>(slot(at_n), real, bf());
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         sums[2].v[e] = fma2(d.v[e], x[0].v[e], sums[2].v[e]);
@@ -463,12 +489,12 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
       normalise_grad<G>(d, x[0], pre_r[0], a.p.pre_norm, inv_d);
     }
     {
-      const F8 t = take8<kAsk, kThreads>(slot(0), on, T());
+      const F8 t = take8<kAsk, kThreads, G>(slot(0), on, T());
 #pragma unroll
       for (int e = 0; e < 4; ++e) d.v[e] = add2(t.v[e], d.v[e]);
     }
     if (a.dout2) {
-      const F8 t = take8<kAsk, kThreads>(slot(2 * kSlots<T>), on, T());
+      const F8 t = take8<kAsk, kThreads, G>(slot(2 * kSlots<T>), on, T());
 #pragma unroll
       for (int e = 0; e < 4; ++e) d.v[e] = add2(t.v[e], d.v[e]);
     }
