@@ -140,41 +140,41 @@ __device__ __forceinline__ void shifted_ids<4>(const uint16_t* ids, int m, uint3
 
 // The buckets of plane positions [f0 - V, f0 + 32 V n) of batch b, in order:
 // a tile of n segments, 16 bytes of elements a lane each.  `none` stands for
-// what has no bucket: padding, and positions outside the plane.  Where all of a
-// segment, early ones of a shifted plane among them, is in one bucket, as most
-// are, whole[segment] is that bucket, else kMixed.
+// what has no bucket: padding, and positions outside the plane.  The warps take
+// pieces of 32 H positions, H = V or half of it.  Where all of a piece, early
+// ones of a shifted plane among them, is in one bucket, as most are,
+// whole[piece] is that bucket, else kMixed.
 constexpr uint32_t kMixed = 0xffffffff;
-template <int V>
-__device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, long long f0, int n, uint32_t plane,
+template <int V, int H>
+__device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, uint32_t f0, int n, uint32_t plane,
                                           uint16_t none, uint16_t* ids, uint32_t* whole) {
-  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
-  for (int seg = threadIdx.x / 32; seg < n; seg += warps) {
-    RelposPair pair[V + 1];
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32, pieces = n * (V / H);
+  for (int piece = threadIdx.x / 32; piece < pieces; piece += warps) {
+    RelposPair pair[H + 1];
 #pragma unroll
-    for (int q = 0; q <= V; ++q) {
-      const long long f = f0 - V + (seg * V + q) * 32 + lane;
+    for (int q = 0; q <= H; ++q) {
+      const uint32_t f = f0 - V + (piece * H + q) * 32 + lane;  // what is before the plane comes out beyond its end
       pair[q].none();
-      if (f >= 0 && f < plane && (q < V || lane < V)) {
+      if (f < plane && (q < H || lane < V)) {
         uint32_t row, j;
-        a.by_J.divmod(static_cast<uint32_t>(f), row, j);
+        a.by_J.divmod(f, row, j);
         pair[q].load(a, b * a.I + row, b * a.J + j);
       }
     }
     uint32_t first = 0;
     bool same = true;
 #pragma unroll
-    for (int q = 0; q <= V; ++q) {
+    for (int q = 0; q <= H; ++q) {
       const int k = pair[q].bucket(a);
       const uint32_t id = k < 0 ? none : k;
       if (q == 0) first = __shfl_sync(0xffffffffu, id, 0);
-      same = same && (id == first || (q == V && lane >= V));
-      if (q < V || (seg == n - 1 && lane < V)) ids[(seg * V + q) * 32 + lane] = static_cast<uint16_t>(id);
+      same = same && (id == first || (q == H && lane >= V));
+      if (q < H || (piece == pieces - 1 && lane < V)) ids[(piece * H + q) * 32 + lane] = static_cast<uint16_t>(id);
     }
     same = __all_sync(0xffffffffu, same);
-    if (lane == 0) whole[seg] = same ? first : kMixed;
+    if (lane == 0) whole[piece] = same ? first : kMixed;
   }
 }
-
 // HEADS layout.  A block goes over tiles of a plane [I][J] of 16 bytes a
 // thread: the buckets of a tile are worked out once, in shared memory, and
 // every head of the block looks its values up by them, in its column of the
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kHeadThreads)
     uint32_t b, t;
     by_tiles.divmod(tile, b, t);
     // two buffers: a warp that still works on the last tile reads the other one
-    stage_ids<V>(a, b, static_cast<long long>(t) * kTile, kSegments, plane, none, ids[turn], whole[turn]);
+    stage_ids<V, V>(a, b, t * kTile, kSegments, plane, none, ids[turn], whole[turn]);
     __syncthreads();
     const uint32_t one = whole[turn][threadIdx.x / 32];
     const uint32_t first = t * kTile + threadIdx.x * V;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(512)
   const bool live = h < a.D;
   float* const sums = reinterpret_cast<float*>(smem4) + static_cast<size_t>(warp) * own;
   uint16_t* const ids0 = reinterpret_cast<uint16_t*>(reinterpret_cast<float*>(smem4) + static_cast<size_t>(warps) * own);
-  __shared__ uint32_t whole0[2][16 * kTileSteps];
+  __shared__ alignas(8) uint32_t whole0[2][2 * 16 * kTileSteps];
   for (int r = 0; r <= a.rows; ++r) sums[r * 32 + lane] = 0.f;
   const uint32_t tiles = by_tiles.d * a.B;
   const uint16_t none = static_cast<uint16_t>(a.rows);
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(512)
     by_tiles.divmod(tile, b, t);
     uint16_t* const ids = ids0 + turn * (tile_n + V);
     // two buffers: a warp that is still adding the last tile reads the other one
-    stage_ids<V>(a, b, static_cast<long long>(t) * tile_n, parts * kTileSteps, plane, none, ids, whole0[turn]);
+    stage_ids<V, V / 2>(a, b, t * tile_n, parts * kTileSteps, plane, none, ids, whole0[turn]);
     __syncthreads();
     uint4 now[kTileSteps];
 #pragma unroll
@@ -510,7 +510,8 @@ __global__ void __launch_bounds__(512)
     const int m = boundary(b);
 #pragma unroll
     for (int u = 0; u < kTileSteps; ++u) {
-      const uint32_t one = whole0[turn][my_part * kTileSteps + u];
+      const uint2 halves = reinterpret_cast<const uint2*>(whole0[turn])[my_part * kTileSteps + u];
+      const uint32_t one = halves.x == halves.y ? halves.x : kMixed;
       if (one != kMixed) {  // of the whole warp's elements
         f2 v[V / 2];
         Vec<T>::unpack(now[u], v);
@@ -529,15 +530,7 @@ __global__ void __launch_bounds__(512)
         float v[V];
         Vec<T>::unpack(now[u], v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const uint32_t k = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
-          if (k != at) {
-            sums[at * 32 + lane] += run;
-            at = k;
-            run = 0.f;
-          }
-          run += v[e];
-        }
+        for (int e = 0; e < V; ++e) sums[((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu) * 32 + lane] += v[e];
       }
     }
   }
