@@ -22,6 +22,7 @@ import contextlib
 import ctypes
 import math
 
+import numpy as np
 import torch
 
 from . import _lib
@@ -369,8 +370,9 @@ class Residual:
 class GradSet:
     """A list (or dict) of gradients whose norm is taken together: norm() and clip().
 
-    The tensors (and `outs`, buffers of the same shapes and types for clipped copies; default: in place) are kept,
-    and read at each call.  bf16, float16 and float32 may be mixed; all on one device, contiguous, not overlapping."""
+    `outs`: buffers of the same shapes and types for clipped copies (default: in place).  A set stands for the memory
+    that its tensors have when it is made, keeps it, and reads it at each call.  bf16, float16 and float32 may be mixed;
+    all on one device, contiguous, not overlapping."""
 
     def __init__(self, tensors, outs=None):
         tensors = list(tensors.values() if isinstance(tensors, dict) else tensors)
@@ -378,16 +380,29 @@ class GradSet:
         if len(outs) != len(tensors):
             raise ValueError(f"{len(outs)} outs for {len(tensors)} tensors")
         self.tensors, self.outs = tensors, outs
+        self._memory = [t.untyped_storage() for t in tensors] + ([] if outs is tensors else [o.untyped_storage() for o in outs])
         self.device = _cuda(tensors[0], "tensors[0]") if tensors else torch.cuda.current_device()
         self.torch_device = torch.device("cuda", self.device)
-        self.table = (_lib.GradTensor * len(tensors))()
-        for k, (t, o) in enumerate(zip(tensors, outs)):
-            kind = _type(t.dtype, f"tensors[{k}]", 2)
-            if not _fits(t, t.dtype, t.shape, self.device):
-                _refuse(t, t.dtype, t.shape, self.device, f"tensors[{k}]")
-            if o is not t and not _fits(o, t.dtype, t.shape, self.device):
-                _refuse(o, t.dtype, t.shape, self.device, f"outs[{k}]")
-            self.table[k] = _lib.GradTensor(t.data_ptr(), o.data_ptr(), t.numel(), kind)
+        data, numel = [t.data_ptr() for t in tensors], [t.numel() for t in tensors]
+        kinds = [_TYPES.get(t.dtype, 3) for t in tensors]
+        fine = max(kinds, default=0) < 3 and all(t.get_device() == self.device and t.is_contiguous() for t in tensors)
+        if outs is tensors:
+            to = data
+        else:
+            to = [o.data_ptr() for o in outs]
+            fine = fine and all(o.dtype is t.dtype and o.shape == t.shape and o.get_device() == self.device
+                                and o.is_contiguous() for t, o in zip(tensors, outs))
+        if not fine:
+            for k, (t, o) in enumerate(zip(tensors, outs)):
+                _type(t.dtype, f"tensors[{k}]", 2)
+                for v, name in ((t, "tensors"), (o, "outs")):
+                    if not _fits(v, t.dtype, t.shape, self.device):
+                        _refuse(v, t.dtype, t.shape, self.device, f"{name}[{k}]")
+        # one row of numbers for each tensor, as _lib.GradTensor lays them out
+        rows = np.zeros((len(tensors), 4), dtype=np.int64)
+        if tensors:
+            rows[:, 0], rows[:, 1], rows[:, 2], rows[:, 3] = data, to, numel, kinds
+        self.table = (_lib.GradTensor * len(tensors)).from_buffer(rows) if tensors else (_lib.GradTensor * 0)()
         self.workspace_bytes = _lib.load().trimul_grad_workspace_bytes(len(tensors))
 
     def _call(self, name, norm_type, norm, stream, flags, *first):
