@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(512)
 
   // elements from the boundary at or before the plane (b, h)'s first one
   auto boundary = [&](uint32_t b) { return static_cast<int>((static_cast<long long>(b) * a.D + h) * plane % V); };
-  uint4 next[kTileSteps];
+  uint4 buf[kTileSteps];
   auto load = [&](uint32_t tile) {
     uint32_t b, t;
     by_tiles.divmod(tile, b, t);
@@ -477,15 +477,15 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
     for (int u = 0; u < kTileSteps; ++u) {
       const uint32_t n = first + u * 32 * V;
-      next[u] = make_uint4(0u, 0u, 0u, 0u);
+      buf[u] = make_uint4(0u, 0u, 0u, 0u);
       if (!live || n >= end) continue;
       if (n + V <= whole) {
-        next[u] = __ldcs(reinterpret_cast<const uint4*>(from + n));
+        buf[u] = __ldcs(reinterpret_cast<const uint4*>(from + n));
       } else {
         alignas(16) T last[V] = {};
         for (int e = 0; e < V; ++e)
           if (n + e < end) last[e] = from[n + e];
-        next[u] = *reinterpret_cast<const uint4*>(last);
+        buf[u] = *reinterpret_cast<const uint4*>(last);
       }
     }
   };
@@ -493,19 +493,14 @@ __global__ void __launch_bounds__(512)
   uint32_t at = none;
   float run = 0.f;
   int turn = 0;
-  uint32_t tile = blockIdx.x;
-  if (tile < tiles) load(tile);
-  for (; tile < tiles; tile += gridDim.x, turn ^= 1) {
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
     uint32_t b, t;
     by_tiles.divmod(tile, b, t);
+    load(tile);  // on its way while the buckets are worked out
     uint16_t* const ids = ids0 + turn * (tile_n + V);
     // two buffers: a warp that is still adding the last tile reads the other one
     stage_ids<V, V / 2>(a, b, t * tile_n, parts * kTileSteps, plane, none, ids, whole0[turn]);
     __syncthreads();
-    uint4 now[kTileSteps];
-#pragma unroll
-    for (int u = 0; u < kTileSteps; ++u) now[u] = next[u];
-    if (tile + gridDim.x < tiles) load(tile + gridDim.x);
     if (!live) continue;
     const int m = boundary(b);
 #pragma unroll
@@ -514,7 +509,7 @@ __global__ void __launch_bounds__(512)
       const uint32_t one = halves.x == halves.y ? halves.x : kMixed;
       if (one != kMixed) {  // of the whole warp's elements
         f2 v[V / 2];
-        Vec<T>::unpack(now[u], v);
+        Vec<T>::unpack(buf[u], v);
 #pragma unroll
         for (int i = 1; i < V / 2; ++i) v[0] = add2(v[0], v[i]);
         const float2 s = split2(v[0]);
@@ -528,7 +523,7 @@ __global__ void __launch_bounds__(512)
         uint32_t w[V / 2];
         shifted_ids<V>(ids + my_part * kPart + u * 32 * V + lane * V, m, w);
         float v[V];
-        Vec<T>::unpack(now[u], v);
+        Vec<T>::unpack(buf[u], v);
 #pragma unroll
         for (int e = 0; e < V; ++e) sums[((e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu) * 32 + lane] += v[e];
       }
