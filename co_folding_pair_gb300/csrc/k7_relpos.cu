@@ -175,13 +175,16 @@ __device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, uint3
     if (lane == 0) whole[piece] = same ? first : kMixed;
   }
 }
+
 // HEADS layout.  A block goes over tiles of a plane [I][J] of 16 bytes a
 // thread: the buckets of a tile are worked out once, in shared memory, and
 // every head of the block looks its values up by them, in its column of the
 // table, in shared memory too; a segment of one bucket takes one look.  Planes
 // of odd sizes begin anywhere within 16 bytes: a head's tile then begins up to
 // V - 1 elements early, on a boundary, its buckets shifted alike, and only a
-// plane's ends are written one by one.
+// plane's ends are written one by one.  4 x 8 x 515 x 1030 fp32: 16.3 us, 4.2
+// TB/s written, which is what a fill reaches; bf16 is bound by the look-ups (2 x
+// 16 x 1000^2: 18.5 us, 3.5 TB/s).
 constexpr int kHeadThreads = 256;
 constexpr int kTableBytes = 64 * 1024;
 
@@ -254,6 +257,7 @@ __global__ void __launch_bounds__(kHeadThreads)
 // What makes these sums cheap is that neighbours share a bucket: all pairs
 // farther than M, and in LOG buckets runs of near ones.  A run is added up in
 // registers and goes to shared memory when it ends.
+
 // Shared memory for a block's sums.  With the 1 KB that every block has besides
 // it is one of the sizes that an SM can split its 256 KB by, and leaves 60 KB
 // for L1, through which the loads on their way go: the next size leaves 28 KB,
@@ -267,7 +271,10 @@ constexpr int kSumBytes = 195 * 1024;
 // A batch of one bucket is added up in registers, and joins the run of batches
 // before it, as does a step of one bucket in a mixed batch; the pairs of other
 // steps go to shared memory at once.  The buckets are worked out one pair a
-// lane and handed round by shuffles.
+// lane and handed round by shuffles.  2048^2 x 256 with four chains: 369 us, 5.8
+// TB/s, bound by DRAM; 256^2 x 128: 12.5 us, most of it the sums' way through
+// shared and global memory.  Every pair in a bucket of its own choosing, the
+// worst there is, takes three times as long.
 constexpr int kSteps = 8;
 // Warps of a block: few lanes a pair means many pairs a lane, and registers for them.
 constexpr int pair_warps(int G) { return G >= 4 ? 16 : 8; }
@@ -435,7 +442,12 @@ __global__ void __launch_bounds__(pair_warps(G) * 32)
 // tile are worked out once, in shared memory, and every warp adds up one
 // head's part of the tile.  Each lane has sums of its own ([rows + 1][32
 // lanes], the last row for what has no bucket), 16 bytes of neighbouring
-// elements at a time.  Planes of odd sizes as in the forward.
+// elements at a time; a segment of one bucket joins a run in registers, the
+// elements of others go to shared memory at once.  Planes of odd sizes as in the
+// forward.  2 x 16 x 1001^2 bf16: 28.8 us, 2.2 TB/s; bound by the instructions
+// around each tile (its buckets, loads and the meeting of the warps), which take
+// as long for any pattern of buckets.  (The same sums as a product with tiles of
+// ones on the tensor cores took 24 to 29 us here and more for few heads.)
 constexpr int kTileSteps = 8;
 constexpr int kHeadsBytes = 218 * 1024;  // shared memory for a block's sums and buckets
 

@@ -194,7 +194,7 @@ trimul_status check_residual(const trimul_residual_params* p, const uint16_t* ga
   TRY(check_pairs(B, I, J));
   if (p->stream_type != TRIMUL_BF16 && p->stream_type != TRIMUL_F32)
     return fail(TRIMUL_ERR_INVALID_ARG, "stream_type must be BF16 or F32");
-  if (!(p->eps > 0.0f) || !std::isfinite(p->eps)) return fail(TRIMUL_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (!std::isnormal(p->eps) || p->eps < 0.0f) return fail(TRIMUL_ERR_INVALID_ARG, "eps must be a normal number > 0");
   if (!std::isfinite(p->scale)) return fail(TRIMUL_ERR_INVALID_ARG, "scale must be finite");
   const struct {
     trimul_norm kind;
@@ -254,11 +254,13 @@ ResidualArgs residual_args(const trimul_residual_params* p, const void* x, const
 // ------------------------------------------------------------------ gradients
 size_t type_bytes(trimul_dtype t) { return t == TRIMUL_F32 ? 4 : 2; }
 
-trimul_status check_tensors(const trimul_grad_tensor* t, int n, trimul_norm_kind kind, const float* norm, bool out) {
+trimul_status check_tensors(const trimul_grad_tensor* t, int n, trimul_norm_kind kind, const float* norm,
+                            const void* ws, size_t ws_bytes, bool out) {
   if (n < 0) return fail(TRIMUL_ERR_INVALID_ARG, "n (%d) must be >= 0", n);
   if (n > 0 && !t) return fail(TRIMUL_ERR_INVALID_ARG, "tensors is null");
   if (kind != TRIMUL_NORM_L2 && kind != TRIMUL_NORM_INF) return fail(TRIMUL_ERR_INVALID_ARG, "unknown norm %d", static_cast<int>(kind));
   if (!norm || !aligned(norm, 4)) return fail(TRIMUL_ERR_INVALID_ARG, "norm is null or not 4-byte aligned");
+  if (overlap(norm, 4, ws, ws_bytes)) return fail(TRIMUL_ERR_INVALID_ARG, "norm overlaps the workspace");
   for (int k = 0; k < n; ++k) {
     if (t[k].numel < 0) return fail(TRIMUL_ERR_SHAPE, "tensor %d: numel (%lld) must be >= 0", k, static_cast<long long>(t[k].numel));
     if (t[k].numel >= (1ll << 42)) return fail(TRIMUL_ERR_SHAPE, "tensor %d: numel (%lld) is too large", k, static_cast<long long>(t[k].numel));
@@ -267,6 +269,9 @@ trimul_status check_tensors(const trimul_grad_tensor* t, int n, trimul_norm_kind
     if (t[k].numel == 0) continue;
     const size_t w = type_bytes(t[k].type);
     if (!t[k].data || !aligned(t[k].data, w)) return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: data is null or not aligned to its type", k);
+    for (const void* q : {t[k].data, out ? static_cast<const void*>(t[k].out) : nullptr})
+      if (overlap(norm, 4, q, t[k].numel * w) || overlap(ws, ws_bytes, q, t[k].numel * w))
+        return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d overlaps norm or the workspace", k);
     if (!out) continue;
     if (!t[k].out || !aligned(t[k].out, w)) return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: out is null or not aligned to its type", k);
     if (t[k].out != t[k].data && overlap(t[k].out, t[k].numel * w, t[k].data, t[k].numel * w))
@@ -511,8 +516,9 @@ size_t trimul_grad_workspace_bytes(int n) { return n < 0 ? 0 : grad_workspace(n,
 trimul_status trimul_grad_norm(const trimul_grad_tensor* tensors, int n, trimul_norm_kind kind, float* norm,
                                void* workspace, size_t workspace_bytes, int device, void* stream, unsigned flags) {
   TRY(check_flags(flags, TRIMUL_FLAG_CHECK));
-  TRY(check_tensors(tensors, n, kind, norm, false));
-  TRY(check_workspace(workspace, workspace_bytes, trimul_grad_workspace_bytes(n), 16));
+  const size_t need = trimul_grad_workspace_bytes(n);
+  TRY(check_tensors(tensors, n, kind, norm, workspace, need, false));
+  TRY(check_workspace(workspace, workspace_bytes, need, 16));
   int sms = 0;
   TRY(device_sms(device, &sms));
   DeviceScope scope;
@@ -526,8 +532,9 @@ trimul_status trimul_grad_clip(const trimul_grad_tensor* tensors, int n, float m
                                unsigned flags) {
   TRY(check_flags(flags, TRIMUL_FLAG_CHECK));
   if (!(max_norm >= 0.0f)) return fail(TRIMUL_ERR_INVALID_ARG, "max_norm must be >= 0");
-  TRY(check_tensors(tensors, n, kind, norm, true));
-  TRY(check_workspace(workspace, workspace_bytes, trimul_grad_workspace_bytes(n), 16));
+  const size_t need = trimul_grad_workspace_bytes(n);
+  TRY(check_tensors(tensors, n, kind, norm, workspace, need, true));
+  TRY(check_workspace(workspace, workspace_bytes, need, 16));
   int sms = 0;
   TRY(device_sms(device, &sms));
   DeviceScope scope;

@@ -456,7 +456,7 @@ typedef struct {
   trimul_gate gate;
   int gate_sigmoid;                 /* nonzero: the gate holds logits */
   float scale;                      /* finite */
-  float eps;                        /* finite, > 0 */
+  float eps;                        /* > 0, and no subnormal number */
 } trimul_residual_params;           /* the pointers are DEVICE pointers, read by the kernels */
 
 /*
@@ -524,7 +524,7 @@ trimul_status trimul_grad_norm(const trimul_grad_tensor* tensors, int n, trimul_
  * The norm, and out = the tensors scaled by min(1, max_norm / (norm + 1e-6)) (max_norm >= 0; infinity: norm alone,
  * nothing scaled), in 32 bits with one rounding to the tensor's type.  A norm that is not finite leaves the values as
  * they are (out-of-place: copied), so that the caller can look at the norm and skip its step.  No two tensors may
- * overlap.
+ * overlap (that is not checked).
  */
 trimul_status trimul_grad_clip(const trimul_grad_tensor* tensors, int n, float max_norm, trimul_norm_kind kind,
                                float* norm, void* workspace, size_t workspace_bytes, int device, void* stream,

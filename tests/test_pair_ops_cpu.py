@@ -71,6 +71,8 @@ def forward(lib, p, **kw):
     ({}, {"I": 50000, "J": 50000}, SHAPE, "2^31 pairs"),
     ({"stream_type": 2}, {}, INVALID, "stream_type"),
     ({"eps": 0.0}, {}, INVALID, "eps"),
+    ({"eps": 1e-40}, {}, INVALID, "eps"),
+    ({"eps": -1e-5}, {}, INVALID, "eps"),
     ({"scale": float("inf")}, {}, INVALID, "scale"),
     ({"post_norm": 3}, {}, INVALID, "unknown post_norm"),
     ({"post_norm": 0, "post_gamma": 5 * A}, {}, INVALID, "post_norm is NONE"),
@@ -144,6 +146,10 @@ def test_residual_backward_refused(lib, fields, call, grads, text):
     ((A, A, 8, 1), {"kind": 2}, INVALID, "unknown norm"),
     ((A, A, 8, 1), {"norm": None}, INVALID, "norm is null"),
     ((A, A, 8, 1), {"bytes": 8}, INVALID, "are needed"),
+    ((A, A, A, 1), {"norm": A + 64}, INVALID, "overlaps norm"),
+    ((A, 4 * A, 8, 1), {"norm": 4 * A + 16}, INVALID, "overlaps norm"),
+    ((A, 5 * A, 8, 1), {}, INVALID, "overlaps norm or the workspace"),
+    ((A, A, 8, 1), {"norm": 5 * A + 32}, INVALID, "norm overlaps"),
     ((A, A, 8, 1), {"n": -1}, INVALID, "n (-1)"),
     ((A, A, 8, 1), {"flags": 2}, INVALID, "flags 0x2"),
 ])
