@@ -146,11 +146,10 @@ __device__ __forceinline__ void shifted_ids<4>(const uint16_t* ids, int m, uint3
 // whole[piece] is that bucket, else kMixed.
 constexpr uint32_t kMixed = 0xffffffff;
 template <int V, int H>
-__device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, uint32_t f0, int n, uint32_t plane,
-                                          uint16_t none, uint16_t* ids, uint32_t* whole) {
-  const int lane = threadIdx.x % 32, warps = blockDim.x / 32, pieces = n * (V / H);
-  for (int piece = threadIdx.x / 32; piece < pieces; piece += warps) {
-    RelposPair pair[H + 1];
+struct Piece {
+  RelposPair pair[H + 1];
+  __device__ __forceinline__ void load(const RelposArgs& a, uint32_t b, uint32_t f0, int piece, uint32_t plane) {
+    const int lane = threadIdx.x % 32;
 #pragma unroll
     for (int q = 0; q <= H; ++q) {
       const uint32_t f = f0 - V + (piece * H + q) * 32 + lane;  // what is before the plane comes out beyond its end
@@ -161,6 +160,10 @@ __device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, uint3
         pair[q].load(a, b * a.I + row, b * a.J + j);
       }
     }
+  }
+  __device__ __forceinline__ void finish(const RelposArgs& a, int piece, int pieces, uint16_t none, uint16_t* ids,
+                                         uint32_t* whole) const {
+    const int lane = threadIdx.x % 32;
     uint32_t first = 0;
     bool same = true;
 #pragma unroll
@@ -174,7 +177,7 @@ __device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, uint3
     same = __all_sync(0xffffffffu, same);
     if (lane == 0) whole[piece] = same ? first : kMixed;
   }
-}
+};
 
 // HEADS layout.  A block goes over tiles of a plane [I][J] of 16 bytes a
 // thread: the buckets of a tile are worked out once, in shared memory, and
@@ -182,9 +185,9 @@ __device__ __forceinline__ void stage_ids(const RelposArgs& a, uint32_t b, uint3
 // table, in shared memory too; a segment of one bucket takes one look.  Planes
 // of odd sizes begin anywhere within 16 bytes: a head's tile then begins up to
 // V - 1 elements early, on a boundary, its buckets shifted alike, and only a
-// plane's ends are written one by one.  4 x 8 x 515 x 1030 fp32: 16.3 us, 4.2
+// plane's ends are written one by one.  4 x 8 x 515 x 1030 fp32: 15.6 us, 4.4
 // TB/s written, which is what a fill reaches; bf16 is bound by the look-ups (2 x
-// 16 x 1000^2: 18.5 us, 3.5 TB/s).
+// 16 x 1000^2: 17.1 us, 3.7 TB/s).
 constexpr int kHeadThreads = 256;
 constexpr int kTableBytes = 64 * 1024;
 
@@ -207,7 +210,9 @@ __global__ void __launch_bounds__(kHeadThreads)
     uint32_t b, t;
     by_tiles.divmod(tile, b, t);
     // two buffers: a warp that still works on the last tile reads the other one
-    stage_ids<V, V>(a, b, t * kTile, kSegments, plane, none, ids[turn], whole[turn]);
+    Piece<V, V> piece;  // one a warp
+    piece.load(a, b, t * kTile, threadIdx.x / 32, plane);
+    piece.finish(a, threadIdx.x / 32, kSegments, none, ids[turn], whole[turn]);
     __syncthreads();
     const uint32_t one = whole[turn][threadIdx.x / 32];
     const uint32_t first = t * kTile + threadIdx.x * V;
@@ -511,7 +516,11 @@ __global__ void __launch_bounds__(512)
     load(tile);  // on its way while the buckets are worked out
     uint16_t* const ids = ids0 + turn * (tile_n + V);
     // two buffers: a warp that is still adding the last tile reads the other one
-    stage_ids<V, V / 2>(a, b, t * tile_n, parts * kTileSteps, plane, none, ids, whole0[turn]);
+    for (int k = warp; k < 2 * parts * kTileSteps; k += warps) {
+      Piece<V, V / 2> piece;
+      piece.load(a, b, t * tile_n, k, plane);
+      piece.finish(a, k, 2 * parts * kTileSteps, none, ids, whole0[turn]);
+    }
     __syncthreads();
     if (!live) continue;
     const int m = boundary(b);
