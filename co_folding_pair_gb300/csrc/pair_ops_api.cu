@@ -416,7 +416,7 @@ trimul_status trimul_relpos_backward(trimul_relpos r, const void* dout, trimul_d
 
 trimul_status trimul_relpos_destroy(trimul_relpos r) {
   if (!r) return TRIMUL_OK;
-  {
+  if (r->lut) {
     DeviceScope scope;
     TRY(scope.enter(r->device));
     cudaDeviceSynchronize();

@@ -76,6 +76,14 @@ def _cuda(t, name) -> int:
     return dev
 
 
+def _device(device) -> int:
+    """The number of a device: the current one where none, or "cuda" without a number, is given."""
+    at = torch.device("cuda" if device is None else device)
+    if at.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {device}")
+    return torch.cuda.current_device() if at.index is None else at.index
+
+
 def _empty(shape, dtype, device, stream):
     """Uninitialised memory of `stream`, so that the allocator gives it out again in that stream's order."""
     if stream is None:
@@ -108,7 +116,7 @@ def trimul_relpos_create(kind="linear", max_distance=32, num_buckets=None, bidir
     lib = _lib.load()
     p = _lib.RelposParams(_one_of(_KINDS, kind, "kind"), int(max_distance), int(num_buckets or 0),
                           int(bool(bidirectional)), int(bool(groups)))
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    dev = _device(device)
     out = ctypes.c_void_p()
     _check(lib.trimul_relpos_create(ctypes.byref(out), ctypes.byref(p), dev))
     return RelPosPlan(out, trimul_relpos_rows(out), dev)
@@ -367,12 +375,28 @@ class Residual:
 
 
 # ------------------------------------------------------------------ gradient norm and clipping
+def _shared(data, out, size):
+    """(k, i): the output i (out[i], size[i] bytes) lies over the tensor k or its output; None if none does but over its own."""
+    some = np.flatnonzero(size)
+    by = some[np.argsort(out[some], kind="stable")]
+    begin, end = out[by], out[by] + size[by]
+    bad = np.flatnonzero(end[:-1] > begin[1:])
+    if bad.size:
+        return int(by[bad[0]]), int(by[bad[0] + 1])
+    # the outputs are apart, so the last one that begins before a tensor's end is the one that reaches furthest
+    at = np.searchsorted(begin, data[some] + size[some]) - 1
+    own = (by[at] == some) & (out[some] == data[some])
+    bad = np.flatnonzero((at >= 0) & (end[at] > data[some]) & ~own)
+    return (int(some[bad[0]]), int(by[at[bad[0]]])) if bad.size else None
+
+
 class GradSet:
     """A list (or dict) of gradients whose norm is taken together: norm() and clip().
 
     `outs`: buffers of the same shapes and types for clipped copies (default: in place).  A set stands for the memory
     that its tensors have when it is made, keeps it, and reads it at each call.  bf16, float16 and float32 may be mixed;
-    all on one device, contiguous, not overlapping."""
+    all on one device, contiguous.  clip() refuses a set with an output over another's memory, such as one tensor given
+    twice."""
 
     def __init__(self, tensors, outs=None):
         tensors = list(tensors.values() if isinstance(tensors, dict) else tensors)
@@ -403,6 +427,7 @@ class GradSet:
         if tensors:
             rows[:, 0], rows[:, 1], rows[:, 2], rows[:, 3] = data, to, numel, kinds
         self.table = (_lib.GradTensor * len(tensors)).from_buffer(rows) if tensors else (_lib.GradTensor * 0)()
+        self._rows, self._apart = rows, False
         self.workspace_bytes = _lib.load().trimul_grad_workspace_bytes(len(tensors))
 
     def _call(self, name, norm_type, norm, stream, flags, *first):
@@ -424,6 +449,12 @@ class GradSet:
     def clip(self, max_norm, norm_type=2.0, norm=None, stream=None, flags: int = 0):
         """Scale the gradients by min(1, max_norm / (norm + 1e-6)); returns the norm before it.  A norm that is not
         finite leaves them as they are."""
+        if not self._apart:  # looked at once: the set's memory stays what it is
+            data, out, numel, kinds = self._rows.T
+            both = _shared(data, out, numel * np.where(kinds == _TYPES[torch.float32], 4, 2))
+            if both:
+                raise ValueError(f"outs[{both[1]}] overlaps tensors[{both[0]}] or its output")
+            self._apart = True
         return self._call("trimul_grad_clip", norm_type, norm, stream, flags, float(max_norm))
 
 

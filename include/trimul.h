@@ -421,7 +421,7 @@ trimul_status trimul_relpos_backward(trimul_relpos r, const void* dout, trimul_d
                                      int I, int J, int D, trimul_layout layout, float* dtable, void* workspace,
                                      size_t workspace_bytes, void* stream, unsigned flags);
 
-/* Release the plan's device memory.  Synchronises the device.  NULL is accepted. */
+/* Release the plan.  One with LOG buckets has device memory, and synchronises the device.  NULL is accepted. */
 trimul_status trimul_relpos_destroy(trimul_relpos r);
 
 /* ---------------------------------------------------------------- residual step

@@ -521,6 +521,17 @@ def test_grad_clip(P, sizes, kinds, inf):
         assert all(torch.equal(a, b) for a, b in zip(same, outs))
 
 
+def test_clip_refuses_memory_that_is_shared(P):
+    t = torch.ones(1024, device="cuda")
+    for ts, outs in (([t, t], None), ([t, t[512:]], None), ([t[:512], t[512:]], [t[512:], torch.empty_like(t[:512])])):
+        s = P.GradSet(ts, outs)
+        with pytest.raises(ValueError, match="overlaps"):
+            s.clip(1.0)
+        assert float(s.norm()) == pytest.approx(sum(v.numel() for v in ts) ** 0.5, rel=64 * U)
+    assert bool((t == 1).all())
+    P.GradSet([t, t], [torch.empty_like(t), torch.empty_like(t)]).clip(1.0)
+
+
 @pytest.mark.parametrize("value", [1e-30, 1e-42, 1e19, 3e38])
 def test_grad_norm_of_large_and_small_values(P, value):
     t = torch.full((100003,), value, device="cuda")

@@ -174,3 +174,30 @@ def test_binding_refusals():
         P.trimul_relpos_create("cubic")
     with pytest.raises(ValueError, match="post_norm must be one of"):
         P._one_of(P._NORMS, "batch", "post_norm")
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta"])
+def test_plans_are_on_cuda_devices(device):
+    with pytest.raises(ValueError, match="CUDA device"):
+        P._device(device)
+    assert P._device("cuda:3") == 3
+
+
+@pytest.mark.parametrize("data,out,size,want", [
+    ([100, 200, 300], [100, 200, 300], [100, 100, 50], None),         # in place, end to end
+    ([300, 100, 200], [300, 100, 200], [50, 100, 100], None),         # in any order
+    ([100, 100], [100, 100], [64, 64], (0, 1)),                       # one tensor twice
+    ([100, 150], [100, 150], [64, 8], (0, 1)),                        # a part of it
+    ([100, 100], [100, 100], [64, 0], None),                          # nothing of it
+    ([100, 200], [500, 564], [64, 64], None),                         # out of place
+    ([100, 100], [500, 564], [64, 64], None),                         # read twice, written apart
+    ([100, 200], [200, 500], [64, 64], (1, 0)),                       # an output over another tensor
+    ([100, 200], [500, 140], [64, 64], (0, 1)),
+    ([100, 200], [100, 150], [64, 64], (0, 1)),
+    ([100, 200], [100, 220], [64, 64], (1, 1)),                       # partly over its own
+    ([], [], [], None),
+    ([100], [100], [0], None),
+])
+def test_clipped_tensors_are_apart(data, out, size, want):
+    import numpy as np
+    assert P._shared(*[np.array(v, dtype=np.int64) for v in (data, out, size)]) == want
