@@ -94,13 +94,16 @@ __device__ __forceinline__ void normalise(F8 (&v)[R], float (&scale)[R], int kin
 }
 
 // t (the gradient at the normalised value) -> the gradient at the norm's input.
+// Lanes past D hold and keep zeros here too: the mean of t is not for them, as
+// the next norm's gradient would sum it.
 template <int G>
-__device__ __forceinline__ void normalise_grad(F8& t, const F8& hat, float scale, int kind, float inv_d) {
+__device__ __forceinline__ void normalise_grad(F8& t, const F8& hat, float scale, int kind, float inv_d, bool live) {
   const float k = -scale * inv_d;
   float m[2] = {dot_of(t, hat), 0.f};
   if (kind == TRIMUL_NORM_LAYER) {
     m[1] = sum_of(t);
     row_sums<G>(m);
+    if (!live) m[1] = 0.f;
   } else {
     float one[1] = {m[0]};
     row_sums<G>(one);
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
         sums[3].v[e] = add2(d.v[e], sums[3].v[e]);
         d.v[e] = mul2(d.v[e], ng.v[e]);
       }
-      normalise_grad<G>(d, x[0], pre_r[0], a.p.pre_norm, inv_d);
+      normalise_grad<G>(d, x[0], pre_r[0], a.p.pre_norm, inv_d, live);
     }
     {
       const F8 t = take8<kAsk, kThreads, G>(slot(0), on, T());
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(kBackwardThreads, kBackwardBlocks) k8_residual
       sums[1].v[e] = add2(d.v[e], sums[1].v[e]);
       d.v[e] = mul2(d.v[e], pg.v[e]);
     }
-    if (post) normalise_grad<G>(d, yh[0], post_r[0], a.p.post_norm, inv_d);
+    if (post) normalise_grad<G>(d, yh[0], post_r[0], a.p.post_norm, inv_d, live);
     if (on) put8(reinterpret_cast<bf*>(a.du) + at, d);
     row += step;
     at += stride;
