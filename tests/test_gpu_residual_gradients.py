@@ -4,13 +4,15 @@ Widths that leave lanes of a row idle (all but the powers of two), with and
 without a mask, over whole blocks of rows and a rest.
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import pair_ops_oracle as O
 from tests import _residual as R
-from tests.test_gpu_pair_ops import f64, randn, residual_case, rng_of, spoil
+from tests.test_gpu_pair_ops import RESIDUAL, f64, randn, residual_case, rng_of, spoil
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -55,3 +57,44 @@ IDLE = [(1, 11, 13, D, stream, "layer", "layer", gate, gate is not None, D == 96
 @pytest.mark.parametrize("case", IDLE, ids=lambda c: f"{c[3]}-{'fp32' if c[4] == F32 else 'bf16'}-{c[7]}")
 def test_widths_with_idle_lanes(P, case):
     held(P, case, 51)
+
+
+@pytest.mark.parametrize("post", [None, "layer", "rms"])
+@pytest.mark.parametrize("pre", [None, "layer", "rms"])
+@pytest.mark.parametrize("D", [16, 24, 56, 136, 256])
+@pytest.mark.parametrize("masked", [False, True])
+def test_every_pair_of_norms(P, post, pre, D, masked):
+    for stream in (BF, F32):
+        held(P, (2, 9, 17, D, stream, post, pre, "pair", masked, True, masked, True), 61, second=masked)
+
+
+@pytest.mark.parametrize("second", [False, True])
+@pytest.mark.parametrize("case", RESIDUAL, ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}x{c[3]}-{c[5]}-{c[6]}-{c[7]}")
+def test_the_cases_of_the_elementwise_test(P, case, second):
+    if case[:3] == (1, 1, 1):
+        case = (1, 1, 2) + case[3:]  # two pairs
+    held(P, case, 22, second)
+
+
+def test_pre_norm_parameters_against_differences(P):
+    """normed is linear in pre_gamma and pre_beta, so a difference over any step is the derivative, but for rounding.
+
+    A value of normed is rounded to bf16, by a number of root mean square at most 2^-8 / sqrt(3) of it; with values and
+    weights near 1 the sum over n = 11520 of them is off by some 2^-8 / sqrt(3) 1.2 sqrt(n) = 0.29, the difference of
+    two by 0.41, and over 2 h = 2 by 0.21: eight times that is 0.016 sqrt(n)."""
+    g = rng_of(32)
+    x, u = randn(g, 1, 10, 12, 96), randn(g, 1, 10, 12, 96, dtype=BF)
+    for pre in ("layer", "rms"):
+        p = {"post_gamma": 1 + 0.1 * randn(g, 96), "pre_gamma": 1 + 0.1 * randn(g, 96)}
+        if pre == "layer":
+            p["pre_beta"] = 0.1 * randn(g, 96)
+        dn = randn(g, *x.shape, dtype=BF)
+        kw = {"post_norm": "rms", "pre_norm": pre, "scale": 0.75}
+        got = P.trimul_residual_backward(x, u, torch.zeros_like(x), p, dnormed=dn, **kw)["grads"]
+        for k in ("pre_gamma", "pre_beta"):
+            if k not in p:
+                continue
+            e = randn(g, 96)
+            up, down = (float((P.trimul_residual_forward(x, u, {**p, k: p[k] + h * e}, **kw)[1].double() * dn.double()).sum())
+                        for h in (1.0, -1.0))
+            assert abs((up - down) / 2 - float((got[k].double() * e).sum())) < 0.016 * math.sqrt(x.numel()), (pre, k)
