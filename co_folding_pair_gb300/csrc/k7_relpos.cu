@@ -480,28 +480,27 @@ __global__ void __launch_bounds__(512)
   const uint32_t tiles = by_tiles.d * a.B;
   const uint16_t none = static_cast<uint16_t>(a.rows);
 
-  // elements from the boundary at or before the plane (b, h)'s first one
-  auto boundary = [&](uint32_t b) { return static_cast<int>((static_cast<long long>(b) * a.D + h) * plane % V); };
+  auto plane_of = [&](uint32_t b) {
+    return HeadPlane((static_cast<long long>(b) * a.D + h) * plane, plane, static_cast<long long>(a.B) * a.D * plane, V);
+  };
   uint4 buf[kTileSteps];
   auto load = [&](uint32_t tile) {
     uint32_t b, t;
     by_tiles.divmod(tile, b, t);
-    const int m = boundary(b);
-    const T* const from = dout + ((static_cast<long long>(b) * a.D + h) * plane - m);
-    const uint32_t first = t * tile_n + my_part * kPart + lane * V, end = plane + m;
-    // what lies behind a plane is the next one, but for the tensor's last, whose last group may be part of 16 bytes
-    const uint32_t whole = b == static_cast<uint32_t>(a.B) - 1 && h == a.D - 1 ? end : end + V - 1;
+    const HeadPlane p = plane_of(b);
+    const T* const from = dout + p.at;
+    const uint32_t first = t * tile_n + my_part * kPart + lane * V;
 #pragma unroll
     for (int u = 0; u < kTileSteps; ++u) {
       const uint32_t n = first + u * 32 * V;
       buf[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (!live || n >= end) continue;
-      if (n + V <= whole) {
+      if (!live || n >= p.end) continue;
+      if (n + V <= p.whole) {
         buf[u] = __ldcs(reinterpret_cast<const uint4*>(from + n));
       } else {
         alignas(16) T last[V] = {};
         for (int e = 0; e < V; ++e)
-          if (n + e < end) last[e] = from[n + e];
+          if (n + e < p.end) last[e] = from[n + e];
         buf[u] = *reinterpret_cast<const uint4*>(last);
       }
     }
@@ -523,7 +522,7 @@ __global__ void __launch_bounds__(512)
     }
     __syncthreads();
     if (!live) continue;
-    const int m = boundary(b);
+    const int m = plane_of(b).early;
 #pragma unroll
     for (int u = 0; u < kTileSteps; ++u) {
       const uint2 halves = reinterpret_cast<const uint2*>(whole0[turn])[my_part * kTileSteps + u];

@@ -74,6 +74,23 @@ struct RelposArgs {
   FastDiv by_I, by_J;
 };
 
+// HEADS layout: a plane of `n` elements, the first of them `begin` into a tensor
+// of `total`, as groups of V elements (16 bytes) on the tensor's 16-byte
+// boundaries.  A group takes in what lies before and behind the plane, other
+// planes, but nothing past the tensor: behind small planes that is soon.
+struct HeadPlane {
+  long long at;         // the boundary at or before the plane's first element
+  uint32_t early;       // elements from there to it
+  uint32_t end, whole;  // from `at` on: past the plane's last element; a group at k < end is all in the tensor if k + V <= whole
+  __host__ __device__ HeadPlane(long long begin, uint32_t n, long long total, int V) {
+    early = static_cast<uint32_t>(begin % V);
+    at = begin - early;
+    end = early + n;
+    const long long left = total - at;
+    whole = left < static_cast<long long>(end) + V - 1 ? static_cast<uint32_t>(left) : end + V - 1;
+  }
+};
+
 cudaError_t launch_relpos_forward(const RelposArgs& a, const void* table, bool table_f32, const void* base, void* out,
                                   bool f32, trimul_layout layout, int num_sms, cudaStream_t s);
 size_t relpos_backward_workspace(int rows, int B, int I, int J, int D, trimul_layout layout, bool f32, int num_sms);

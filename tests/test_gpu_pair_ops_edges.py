@@ -1,0 +1,31 @@
+"""The operators around the layer at the ends of their ranges, on a GB300."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def P():
+    from co_folding_pair_gb300 import pair_ops
+    return pair_ops
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_head_planes_smaller_than_a_group(P, dt):
+    """Planes of one to nine elements, several of them within 16 bytes; small whole numbers, so sums are exact."""
+    r = P.RelPos("linear", 3)
+    for I, J in [(1, 1), (1, 2), (3, 1), (2, 2), (1, 5), (2, 3), (7, 1), (2, 4), (3, 3)]:
+        for B in (1, 2, 3):
+            for D in (1, 2, 3, 5, 9):
+                qp = torch.arange(B * I, device="cuda").int().view(B, I) % 5
+                kp = torch.arange(B * J, device="cuda").int().view(B, J) % 7
+                b = (qp[:, :, None] - kp[:, None, :]).clamp(-3, 3).long() + 3
+                dout = (torch.arange(B * D * I * J, device="cuda") % 9 - 4).view(B, D, I, J).to(dt)
+                want = torch.zeros(7, D, device="cuda").index_add_(0, b.reshape(-1), dout.float().permute(0, 2, 3, 1).reshape(-1, D))
+                assert torch.equal(r.backward(dout, qp, kp, layout="heads"), want), (B, I, J, D)
+                table = torch.arange(7 * D, device="cuda").float().view(7, D)
+                got = r.forward(table, qp, kp, base=dout, layout="heads")
+                assert torch.equal(got.float(), dout.float() + table[b].permute(0, 3, 1, 2)), (B, I, J, D)
