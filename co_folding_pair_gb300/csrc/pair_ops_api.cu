@@ -333,6 +333,8 @@ trimul_status trimul_relpos_create(trimul_relpos* out, const trimul_relpos_param
     if (st == TRIMUL_OK && !lut.empty()) {
       cudaError_t e = cudaMalloc(&r->lut, lut.size() * sizeof(int16_t));
       if (e == cudaSuccess) e = cudaMemcpy(r->lut, lut.data(), lut.size() * sizeof(int16_t), cudaMemcpyHostToDevice);
+      // a copy from pageable memory may return before it is done, and streams that do not block on stream 0 would not wait
+      if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
       if (e != cudaSuccess) {
         cudaGetLastError();
         st = cuda_fail(e, "relpos plan");

@@ -29,3 +29,20 @@ def test_head_planes_smaller_than_a_group(P, dt):
                 table = torch.arange(7 * D, device="cuda").float().view(7, D)
                 got = r.forward(table, qp, kp, base=dout, layout="heads")
                 assert torch.equal(got.float(), dout.float() + table[b].permute(0, 3, 1, 2)), (B, I, J, D)
+
+
+def test_a_log_plan_is_ready_for_any_stream(P):
+    """A plan used at once on a stream that does not wait for the one that its table was copied on."""
+    pos = torch.arange(-3000, 3001, device="cuda").int()[None]
+    zero = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    table = torch.arange(1024, dtype=F32, device="cuda")[:, None].repeat(1, 8)
+    want = P.RelPos("log", 32768, 1024).forward(table, pos, zero, dtype=F32)
+    torch.cuda.synchronize()
+    assert want[0, :, 0, 0].unique().numel() > 700
+    stream = torch.cuda.Stream()
+    for _ in range(5):
+        plan = P.RelPos("log", 32768, 1024)
+        got = plan.forward(table, pos, zero, dtype=F32, stream=stream)
+        stream.synchronize()
+        assert torch.equal(got, want)
+        plan.free()

@@ -4,6 +4,8 @@ import os
 import shutil
 import subprocess
 
+import pytest
+
 from co_folding_pair_gb300 import _lib
 
 
@@ -49,3 +51,63 @@ def test_head_planes_are_read_within_their_tensor(tmp_path):
     """A group of 16 bytes is read whole if, and only if, all of it is in the tensor, planes smaller than a group
     among others."""
     assert "groups" in compiled(tmp_path, PLANES)
+
+
+# A CUDA runtime that only writes down what it is called for, so that the entry points' host code runs without a GPU.
+RUNTIME = r"""
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include "api_status.h"
+#include "pair_ops.h"
+
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { return *d = 0, cudaSuccess; }
+cudaError_t cudaSetDevice(int) { return cudaSuccess; }
+cudaError_t cudaGetDeviceCount(int* n) { return *n = 1, cudaSuccess; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr a, int) {
+  return *v = a == cudaDevAttrComputeCapabilityMajor ? 10 : a == cudaDevAttrComputeCapabilityMinor ? 3 : 152, cudaSuccess;
+}
+cudaError_t cudaMalloc(void** p, size_t n) { return std::puts("malloc"), *p = std::malloc(n), cudaSuccess; }
+cudaError_t cudaFree(void* p) { return std::puts("free"), std::free(p), cudaSuccess; }
+cudaError_t cudaMemcpy(void*, const void*, size_t, cudaMemcpyKind) { return std::puts("copy"), cudaSuccess; }
+cudaError_t cudaDeviceSynchronize() { return std::puts("synchronize device"), cudaSuccess; }
+cudaError_t cudaStreamSynchronize(cudaStream_t s) { return std::printf("synchronize %s\n", s ? "a stream" : "stream 0"), cudaSuccess; }
+cudaError_t cudaGetLastError() { return cudaSuccess; }
+}
+namespace trimul {
+trimul_status fail(trimul_status s, const char* fmt, ...) {
+  std::va_list a;
+  va_start(a, fmt), std::vprintf(fmt, a), va_end(a);
+  return std::puts(""), s;
+}
+trimul_status cuda_fail(cudaError_t, const char* what) { return std::puts(what), TRIMUL_ERR_CUDA; }
+cudaError_t launch_relpos_forward(const RelposArgs&, const void*, bool, const void*, void*, bool, trimul_layout, int, cudaStream_t) { return std::puts("forward"), cudaSuccess; }
+size_t relpos_backward_workspace(int, int, int, int, int, trimul_layout, bool, int) { return 64; }
+cudaError_t launch_relpos_backward(const RelposArgs&, const void*, bool, trimul_layout, float*, bool, float*, int, cudaStream_t) { return std::puts("backward"), cudaSuccess; }
+cudaError_t launch_residual_forward(const ResidualArgs&, int, cudaStream_t) { return cudaSuccess; }
+size_t residual_backward_workspace(int, long long, int) { return 64; }
+cudaError_t launch_residual_backward(const ResidualArgs&, int, cudaStream_t) { return cudaSuccess; }
+size_t grad_workspace(int, int) { return 64; }
+cudaError_t launch_grad_norm(const trimul_grad_tensor*, int, trimul_norm_kind, float*, void*, bool, float, int, cudaStream_t) { return cudaSuccess; }
+}  // namespace trimul
+"""
+
+
+@pytest.mark.parametrize("kind,buckets,want", [
+    (0, 0, ["made", "gone"]),
+    (1, 32, ["malloc", "copy", "synchronize stream 0", "made", "synchronize device", "free", "gone"]),
+])
+def test_a_plan_is_made_once_its_table_has_arrived(tmp_path, kind, buckets, want):
+    """A copy from pageable memory may return before its data is on the device, and other streams do not wait for it."""
+    main = RUNTIME + r"""
+int main() {
+  const trimul_relpos_params p{static_cast<trimul_bucket_kind>(KIND), 128, BUCKETS, 1, 0};
+  trimul_relpos r = nullptr;
+  if (trimul_relpos_create(&r, &p, 0) != TRIMUL_OK) return 1;
+  std::puts("made");
+  if (trimul_relpos_destroy(r) != TRIMUL_OK) return 1;
+  std::puts("gone");
+}
+""".replace("KIND", str(kind)).replace("BUCKETS", str(buckets))
+    assert compiled(tmp_path, main, "pair_ops_api.cu").split("\n")[:-1] == want
