@@ -1101,6 +1101,8 @@ trimul_status trimul_create(trimul_handle* out, const trimul_params* p, int devi
   if (e == cudaSuccess) e = cudaMemcpy(h->colc, colc.data(), colc.size() * 4, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(h->in_bias, in_bias.data(), in_bias.size() * 4, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 16);
+  // copies from pageable memory may return before they are done, and streams that do not block on stream 0 would not wait
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) {
     trimul_destroy(h);
     return cuda_fail(e, "handle allocation");
