@@ -369,8 +369,10 @@ trimul_status trimul_relpos_forward(trimul_relpos r, const void* table, trimul_d
   TRY(check_relpos(r, q_pos, k_pos, q_group, k_group, B, I, J, D, layout, type));
   if (table_type != TRIMUL_BF16 && table_type != TRIMUL_F32) return fail(TRIMUL_ERR_INVALID_ARG, "table_type must be BF16 or F32");
   if (!table || !out) return fail(TRIMUL_ERR_INVALID_ARG, "table or out is null");
-  if (!aligned(table, 16) || !aligned(base, 16) || !aligned(out, 16))
-    return fail(TRIMUL_ERR_INVALID_ARG, "table, base and out must be 16-byte aligned");
+  if (!aligned(base, 16) || !aligned(out, 16)) return fail(TRIMUL_ERR_INVALID_ARG, "base and out must be 16-byte aligned");
+  // PAIR reads the table's rows 16 bytes at a time, HEADS its elements one by one
+  const size_t at = layout == TRIMUL_LAYOUT_PAIR ? 16 : type_bytes(table_type);
+  if (!aligned(table, at)) return fail(TRIMUL_ERR_INVALID_ARG, "table must be %zu-byte aligned", at);
   const size_t bytes = static_cast<size_t>(B) * I * J * D * type_bytes(type);
   const size_t nq = static_cast<size_t>(B) * I * 4, nk = static_cast<size_t>(B) * J * 4;
   const Buffer in[] = {{base, bytes, "base"}, {table, r->rows * static_cast<size_t>(D) * type_bytes(table_type), "table"},
@@ -399,7 +401,8 @@ trimul_status trimul_relpos_backward(trimul_relpos r, const void* dout, trimul_d
   TRY(check_flags(flags, TRIMUL_FLAG_CHECK | TRIMUL_FLAG_ACCUMULATE));
   TRY(check_relpos(r, q_pos, k_pos, q_group, k_group, B, I, J, D, layout, type));
   if (!dout || !dtable) return fail(TRIMUL_ERR_INVALID_ARG, "dout or dtable is null");
-  if (!aligned(dout, 16) || !aligned(dtable, 16)) return fail(TRIMUL_ERR_INVALID_ARG, "dout and dtable must be 16-byte aligned");
+  if (!aligned(dout, 16)) return fail(TRIMUL_ERR_INVALID_ARG, "dout must be 16-byte aligned");
+  if (!aligned(dtable, 4)) return fail(TRIMUL_ERR_INVALID_ARG, "dtable must be 4-byte aligned");
   const size_t need = relpos_backward_workspace(r->rows, B, I, J, D, layout, type == TRIMUL_F32, r->num_sms);
   TRY(check_workspace(workspace, workspace_bytes, need, 16));
   const size_t nq = static_cast<size_t>(B) * I * 4, nk = static_cast<size_t>(B) * J * 4;

@@ -400,7 +400,8 @@ int trimul_relpos_rows(trimul_relpos r);
  * out = base + table[bucket] (base NULL: 0).  table: [rows][D] of table_type (BF16 or F32); q_pos, q_group:
  * int32 [B][I]; k_pos, k_group: int32 [B][J] (the groups: both NULL, or both given to a plan made with
  * `groups`); base, out: `type` (BF16 or F32) in `layout`; out may be base itself, and overlaps nothing else.
- * The sum is taken in 32 bits and rounded once.  B, I, J >= 1 and B I J < 2^31.
+ * The sum is taken in 32 bits and rounded once.  B, I, J >= 1 and B I J < 2^31.  In the HEADS layout the table need
+ * only be aligned to its elements.
  */
 trimul_status trimul_relpos_forward(trimul_relpos r, const void* table, trimul_dtype table_type, const int32_t* q_pos,
                                     const int32_t* k_pos, const int32_t* q_group, const int32_t* k_group,
@@ -412,8 +413,8 @@ size_t trimul_relpos_backward_workspace_bytes(trimul_relpos r, int B, int I, int
                                               trimul_dtype type);
 
 /*
- * The table's gradient: dtable[n][c] = the sum of dout over the pairs of bucket n (f32 [rows][D]; overwritten,
- * or added to with TRIMUL_FLAG_ACCUMULATE).  dout: `type` in `layout`.  The sums are fp32 in a fixed order: the
+ * The table's gradient: dtable[n][c] = the sum of dout over the pairs of bucket n (f32 [rows][D], 4-byte aligned;
+ * overwritten, or added to with TRIMUL_FLAG_ACCUMULATE).  dout: `type` in `layout`.  The sums are fp32 in a fixed order: the
  * result is deterministic.  (The gradient of base is dout itself.)
  */
 trimul_status trimul_relpos_backward(trimul_relpos r, const void* dout, trimul_dtype type, const int32_t* q_pos,

@@ -46,3 +46,26 @@ def test_a_log_plan_is_ready_for_any_stream(P):
         stream.synchronize()
         assert torch.equal(got, want)
         plan.free()
+
+
+@pytest.mark.parametrize("layout", ["pair", "heads"])
+def test_tables_and_their_gradients_within_flat_buffers(P, layout):
+    """dtable at any float, and the head layout's table at any element: as parts of one buffer of parameters."""
+    r = P.RelPos("linear", 4)
+    pos = torch.arange(37, device="cuda").int()[None]
+    dout = torch.randn(*((1, 37, 37, 24) if layout == "pair" else (1, 24, 37, 37)), device="cuda")
+    want = r.backward(dout, pos, layout=layout)
+    flat = torch.full((4 * 220,), 7.0, device="cuda")
+    for at in (1, 222, 443, 660):
+        part = flat[at:at + 216].view(9, 24)
+        r.backward(dout, pos, layout=layout, dtable=part)
+        assert torch.equal(part, want)
+        r.backward(dout, pos, layout=layout, dtable=part, flags=P.FLAG_ACCUMULATE)
+        assert torch.equal(part, 2 * want)
+        assert (flat[at + 216:at + 220] == 7.0).all() and flat[at - 1] == 7.0
+    if layout == "heads":
+        for dt in (BF, F32):
+            flat = torch.randn(300, device="cuda").to(dt)
+            for at in (1, 2, 3, 5):
+                part = flat[at:at + 216].view(9, 24)
+                assert torch.equal(r.forward(part, pos, layout=layout, dtype=dt), r.forward(part.clone(), pos, layout=layout, dtype=dt))

@@ -111,3 +111,38 @@ int main() {
 }
 """.replace("KIND", str(kind)).replace("BUCKETS", str(buckets))
     assert compiled(tmp_path, main, "pair_ops_api.cu").split("\n")[:-1] == want
+
+
+def test_alignment_is_asked_for_where_it_is_needed(tmp_path):
+    """dtable is written, and the HEADS layout's table read, one element at a time; all else 16 bytes at a time."""
+    main = RUNTIME + r"""
+int main() {
+  const trimul_relpos_params p{TRIMUL_BUCKETS_LINEAR, 4, 0, 1, 0};
+  trimul_relpos r = nullptr;
+  if (trimul_relpos_create(&r, &p, 0) != TRIMUL_OK) return 1;
+  auto at = [](long mb, long off) { return reinterpret_cast<char*>((mb << 20) + off); };
+  const int32_t* const pos = reinterpret_cast<int32_t*>(at(1, 4));
+  auto forward = [&](trimul_layout lay, long table, trimul_dtype type, long out) {
+    return trimul_relpos_forward(r, at(2, table), type, pos, pos, nullptr, nullptr, nullptr, 1, 8, 8, 16, lay, at(3, out), TRIMUL_BF16, nullptr, 0);
+  };
+  auto backward = [&](trimul_layout lay, long dout, long dtable) {
+    return trimul_relpos_backward(r, at(2, dout), TRIMUL_BF16, pos, pos, nullptr, nullptr, 1, 8, 8, 16, lay,
+                                  reinterpret_cast<float*>(at(3, dtable)), at(4, 0), 64, nullptr, 0);
+  };
+  const trimul_layout P = TRIMUL_LAYOUT_PAIR, H = TRIMUL_LAYOUT_HEADS;
+  std::printf("%d %d %d\n", forward(P, 16, TRIMUL_BF16, 16), forward(H, 2, TRIMUL_BF16, 16), forward(H, 4, TRIMUL_F32, 16));
+  std::printf("%d %d %d\n", backward(P, 16, 4), backward(H, 16, 12), backward(P, 0, 0));
+  std::puts("refused");
+  std::printf("%d %d %d %d\n", forward(P, 8, TRIMUL_F32, 16), forward(H, 2, TRIMUL_F32, 16), forward(H, 1, TRIMUL_BF16, 16), forward(H, 0, TRIMUL_F32, 8));
+  std::printf("%d %d %d\n", backward(P, 8, 0), backward(H, 2, 0), backward(P, 0, 2));
+  return trimul_relpos_destroy(r) != TRIMUL_OK;
+}
+"""
+    fine, refused = compiled(tmp_path, main, "pair_ops_api.cu").split("refused\n")
+    assert sorted(fine.split()) == sorted(["0"] * 6 + ["forward"] * 3 + ["backward"] * 3)
+    lines = refused.strip().split("\n")
+    assert [v for v in lines if v[0].isdigit()] == ["1 1 1 1", "1 1 1"]
+    assert sorted(v for v in lines if not v[0].isdigit()) == sorted(
+        ["table must be 16-byte aligned", "table must be 4-byte aligned", "table must be 2-byte aligned",
+         "base and out must be 16-byte aligned", "dout must be 16-byte aligned", "dout must be 16-byte aligned",
+         "dtable must be 4-byte aligned"])
