@@ -480,9 +480,7 @@ __global__ void __launch_bounds__(512)
   const uint32_t tiles = by_tiles.d * a.B;
   const uint16_t none = static_cast<uint16_t>(a.rows);
 
-  auto plane_of = [&](uint32_t b) {
-    return HeadPlane((static_cast<long long>(b) * a.D + h) * plane, plane, static_cast<long long>(a.B) * a.D * plane, V);
-  };
+  auto plane_of = [&](uint32_t b) { return HeadPlane(b, h, a.B, a.D, plane, V); };
   uint4 buf[kTileSteps];
   auto load = [&](uint32_t tile) {
     uint32_t b, t;

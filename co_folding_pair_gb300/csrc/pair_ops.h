@@ -74,20 +74,24 @@ struct RelposArgs {
   FastDiv by_I, by_J;
 };
 
-// HEADS layout: a plane of `n` elements, the first of them `begin` into a tensor
-// of `total`, as groups of V elements (16 bytes) on the tensor's 16-byte
-// boundaries.  A group takes in what lies before and behind the plane, other
-// planes, but nothing past the tensor: behind small planes that is soon.
+// HEADS layout [B][H][n]: head h's plane of batch b, as groups of V elements (16
+// bytes) on the tensor's 16-byte boundaries.  A group takes in what lies before
+// and behind the plane, other planes, but nothing past the tensor: behind small
+// planes that is soon.
 struct HeadPlane {
   long long at;         // the boundary at or before the plane's first element
   uint32_t early;       // elements from there to it
   uint32_t end, whole;  // from `at` on: past the plane's last element; a group at k < end is all in the tensor if k + V <= whole
-  __host__ __device__ HeadPlane(long long begin, uint32_t n, long long total, int V) {
+  __host__ __device__ HeadPlane(uint32_t b, int h, int B, int H, uint32_t n, int V) {
+    const long long begin = (static_cast<long long>(b) * H + h) * n;
     early = static_cast<uint32_t>(begin % V);
     at = begin - early;
     end = early + n;
-    const long long left = total - at;
-    whole = left < static_cast<long long>(end) + V - 1 ? static_cast<uint32_t>(left) : end + V - 1;
+    // elements behind the plane, where they are less than the V - 1 that a group may reach past it
+    const uint32_t most = V - 1, batches = B - 1 - b;
+    const uint32_t planes = (batches < most ? batches : most) * H + (H - 1 - h);
+    const uint32_t behind = (planes < most ? planes : most) * (n < most ? n : most);
+    whole = end + (behind < most ? behind : most);
   }
 };
 

@@ -31,9 +31,9 @@ int main() {
   long long looked = 0;
   for (int V : {4, 8})
     for (uint32_t n : {1u, 2u, 3u, 4u, 5u, 6u, 7u, 8u, 9u, 15u, 16u, 17u, 1000u, 2147483647u})
-      for (long long planes = 1; planes <= 20; ++planes)
-        for (long long q = 0; q < planes; ++q) {
-          const HeadPlane p(q * n, n, planes * n, V);
+      for (int B : {1, 2, 3, 5, 9, 20}) for (int H : {1, 2, 3, 4, 7, 8, 9, 256})
+        for (long long q = 0, planes = B * H; q < planes; ++q) {
+          const HeadPlane p(static_cast<uint32_t>(q / H), static_cast<int>(q % H), B, H, n, V);
           if (p.at % V || p.at + p.early != q * n || p.early >= static_cast<uint32_t>(V) || p.end != p.early + n) return 1;
           // the first groups and the last ones
           for (uint32_t k = 0; k < p.end; k = k < 64 || k + 256 > p.end ? k + V : p.end / V * V - 64) {
