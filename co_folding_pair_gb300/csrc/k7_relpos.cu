@@ -222,10 +222,12 @@ __global__ void __launch_bounds__(kHeadThreads)
     const T* z0 = base + begin0;
     T* o0 = out + begin0;
     const float* col = tab;
+    const uint32_t whole_ends = plane < V ? 0u : plane - V + 1;  // all V of those that begin before it are in the plane
 #pragma unroll 2
     for (int q = 0; q < n_heads; ++q, m = (m + m_step) % V, z0 += plane, o0 += plane, col += rows) {
-      const int n = static_cast<int>(first) - m;  // the position in the plane of the first of V elements
-      if (n >= static_cast<int>(plane)) continue;
+      // the position in the plane of the first of V elements; what is before the plane is beyond its end without a sign
+      const uint32_t n = first - m;
+      if (first >= plane + m) continue;
       float v[V];
       if (one != kMixed) {
         v[0] = col[one];
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kHeadThreads)
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = col[(e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xffffu];
       }
-      if (n >= 0 && n <= static_cast<int>(plane) - V) {
+      if (n < whole_ends) {
         if (base) {
           float z[V];
           Vec<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z0 + n)), z);
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kHeadThreads)
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
-          if (n + e >= 0 && n + e < static_cast<int>(plane)) o0[n + e] = from_f32<T>(base ? v[e] + to_f32(z0[n + e]) : v[e]);
+          if (n + e < plane) o0[n + e] = from_f32<T>(base ? v[e] + to_f32(z0[n + e]) : v[e]);
       }
     }
   }

@@ -69,3 +69,26 @@ def test_tables_and_their_gradients_within_flat_buffers(P, layout):
             for at in (1, 2, 3, 5):
                 part = flat[at:at + 216].view(9, 24)
                 assert torch.equal(r.forward(part, pos, layout=layout, dtype=dt), r.forward(part.clone(), pos, layout=layout, dtype=dt))
+
+
+@pytest.mark.parametrize("layout,D,dt", [("heads", 2, BF), ("heads", 2, F32), ("pair", 8, BF)])
+def test_the_most_pairs(P, layout, D, dt):
+    """One query and 2^31 - 1 keys: positions in a plane reach past 31 bits where a tile, or a plane's early elements,
+    go past its end."""
+    n = 2**31 - 1
+    r = P.RelPos("linear", 32)
+    qp, kp = torch.full((1, 1), n - 6, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    table = torch.randn(65, D, device="cuda").to(dt)
+    out = r.forward(table, qp, kp, layout=layout, dtype=dt)
+    view = out.view(D, n) if layout == "heads" else out.view(n, D).t()
+    last = 100
+    b = ((n - 6) - torch.arange(n - last, n, device="cuda")).clamp(-32, 32) + 32
+    assert torch.equal(view[:, n - last:], table[b].t())
+    for c in range(D):
+        assert not (view[c, :n - last] != table[64, c]).any()
+    out.zero_()
+    for j, v in ((n - 1, 1.0), (n - 6, 2.0), (0, 4.0)):
+        view[:, j] = v
+    want = torch.zeros(65, D, device="cuda")
+    want[27], want[32], want[64] = 1.0, 2.0, 4.0
+    assert torch.equal(r.backward(out, qp, kp, layout=layout), want)
