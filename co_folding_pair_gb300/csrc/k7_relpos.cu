@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256)
   constexpr int V = Vec<T>::n;
   const uint32_t at_once = blockDim.x / per_pair, c = threadIdx.x % per_pair;
   const uint32_t step = gridDim.x * at_once * kUnroll;
-  // (pairs are below 2^31 and steps below 2^20)
+  // (pairs are below 2^31, and a step is at most 8 x 1024 of them an SM: p0 stays within 32 bits)
   for (uint32_t p0 = blockIdx.x * at_once * kUnroll + threadIdx.x / per_pair; p0 < pairs; p0 += step) {
     uint4 z[kUnroll];
     RelposPair at[kUnroll];

@@ -203,9 +203,12 @@ __device__ __forceinline__ float reciprocal(float x) {
   return r;
 }
 // A gate is kept as its value or, of a sigmoid, as one number that gives both
-// the value and its derivative to fp32's relative precision: with
-// e = exp(-|x|) (which cannot overflow) and small = e / (1 + e), the lesser of
-// sigmoid(x) and 1 - sigmoid(x), it is small for x < 0 and -small for x >= 0.
+// the value and its derivative: with e = exp(-|x|) (which cannot overflow) and
+// small = e / (1 + e), the lesser of sigmoid(x) and 1 - sigmoid(x), it is small
+// for x < 0 and -small for x >= 0.  The fast exponential is off by up to 2 +
+// 1.173 |x| ulp, and small with it, by some 3 more: 2^-18 of it at x = -20, when
+// it is 2e-9 itself.  Below the least normal number (x < -87.3) it is 0.  1 -
+// small, the value for x >= 0, has fp32's precision.
 __device__ __forceinline__ float sigmoid_code(float x) {
   const float e = __expf(-fabsf(x)), small = e * reciprocal(1.0f + e);
   return x >= 0.f ? -small : small;

@@ -16,6 +16,7 @@ from tests.test_gpu_pair_ops import RESIDUAL, f64, randn, residual_case, rng_of,
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
+U = 2.0**-24
 
 
 @pytest.fixture(scope="module")
@@ -98,3 +99,23 @@ def test_pre_norm_parameters_against_differences(P):
             up, down = (float((P.trimul_residual_forward(x, u, {**p, k: p[k] + h * e}, **kw)[1].double() * dn.double()).sum())
                         for h in (1.0, -1.0))
             assert abs((up - down) / 2 - float((got[k].double() * e).sum())) < 0.016 * math.sqrt(x.numel()), (pre, k)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_sigmoid_gates_of_large_logits(P, sign):
+    """The gate alone (x = 0, u = 1): exp(-|x|) is off by at most 2 + 1.173 |x| ulp (the fast exponential's documented
+    bound), the sum, reciprocal and product by 3 more; an ulp is at most 2^-23 of a value.  Results below the smallest
+    normal number are 0.  1 - small has fp32's precision whatever small's."""
+    logits = (sign * torch.linspace(0.0, 100.0, 2048, device="cuda")).to(BF).view(1, 16, 16, 8)
+    x, u = torch.zeros(1, 16, 16, 8, device="cuda"), torch.ones(1, 16, 16, 8, dtype=BF, device="cuda")
+    t = f64(logits)
+    e = np.exp(-np.abs(t))
+    small = e / (1 + e)
+    ref = small if sign < 0 else 1 - small
+    steps = 5 + 1.173 * np.abs(t)
+    out = f64(P.trimul_residual_forward(x, u, gate=logits, gate_sigmoid=True)[0])
+    assert (np.abs(out - ref) <= steps * 2.0**-23 * small + U * ref + 2.0**-126).all()
+    # dgate = u small (1 - small), whichever the sign, rounded to bf16
+    got = f64(P.trimul_residual_backward(x, u, torch.ones_like(x), gate=logits, gate_sigmoid=True)["dgate"])
+    slope = small * (1 - small)
+    assert (np.abs(got - slope) <= (2.0**-8 + (steps + 2) * 2.0**-23) * slope + 2.0**-126).all()
