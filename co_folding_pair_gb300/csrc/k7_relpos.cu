@@ -185,9 +185,11 @@ struct Piece {
 // table, in shared memory too; a segment of one bucket takes one look.  Planes
 // of odd sizes begin anywhere within 16 bytes: a head's tile then begins up to
 // V - 1 elements early, on a boundary, its buckets shifted alike, and only a
-// plane's ends are written one by one.  4 x 8 x 515 x 1030 fp32: 15.6 us, 4.4
-// TB/s written, which is what a fill reaches; bf16 is bound by the look-ups (2 x
-// 16 x 1000^2: 17.1 us, 3.7 TB/s).
+// plane's ends are written one by one.  4 x 8 x 515 x 1030 fp32: 15.4 us, 4.4
+// TB/s; bf16, 2 x 16 x 1000^2: 16.9 us, 3.8 TB/s.  Both outputs fit L2, and DRAM
+// is idle: what bounds them is the issue of the look-ups' instructions (three
+// quarters of the slots in fp32, 0.71 in bf16) and the last, partial wave of blocks
+// (1.3 waves).
 constexpr int kHeadThreads = 256;
 constexpr int kTableBytes = 64 * 1024;
 
@@ -268,7 +270,8 @@ __global__ void __launch_bounds__(kHeadThreads)
 // Shared memory for a block's sums.  With the 1 KB that every block has besides
 // it is one of the sizes that an SM can split its 256 KB by, and leaves 60 KB
 // for L1, through which the loads on their way go: the next size leaves 28 KB,
-// and cost the pair gradient a fifth (2048^2 x 256 with 66 rows: 415 us to 340).
+// and cost the pair gradient a fifth of its rate when the two were compared
+// (2048^2 x 256 with 66 rows: 415 us to 340, before the present order of its sums).
 constexpr int kSumBytes = 195 * 1024;
 
 // PAIR layout.  A warp has sums of its own, [rows][W channels], for one slice
@@ -278,8 +281,8 @@ constexpr int kSumBytes = 195 * 1024;
 // A batch of one bucket is added up in registers, and joins the run of batches
 // before it, as does a step of one bucket in a mixed batch; the pairs of other
 // steps go to shared memory at once.  The buckets are worked out one pair a
-// lane and handed round by shuffles.  2048^2 x 256 with four chains: 369 us, 5.8
-// TB/s, bound by DRAM; 256^2 x 128: 12.5 us, most of it the sums' way through
+// lane and handed round by shuffles.  2048^2 x 256 with four chains: 370 us, 5.8
+// TB/s, bound by DRAM; 256^2 x 128: 12.7 us, most of it the sums' way through
 // shared and global memory.  Every pair in a bucket of its own choosing, the
 // worst there is, takes three times as long.
 constexpr int kSteps = 8;

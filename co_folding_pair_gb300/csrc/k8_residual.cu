@@ -17,11 +17,12 @@
 //
 // Each is one pass over the rows: 8 (forward) to 14 (backward) bytes an element
 // in bf16 against some 20 to 60 operations, so both should be bound by memory.
-// The forward is (2048^2 x 256 bf16, both norms, a gate a row: 1.43 ms, 6.0
+// The forward is (2048^2 x 256 bf16, both norms, a gate a row: 1.42 ms, 6.0
 // TB/s), and the backward with an fp32 stream (1024^2 x 256, both norms, a gate a
 // pair: 0.87 ms, 6.8 TB/s).  In bf16 with two layer norms the backward is bound
-// by its instructions and their latency (1024^2 x 128: 0.33 ms, 0.73 of the
-// floor; with RMS norms 0.25 ms, 0.96).  Widths a little above a power of two
+// by its instructions and their latency (1024^2 x 128: 0.28 ms, 0.85 of the
+// floor, with a gate a row and a channel scale 0.33 ms, 0.72; with RMS norms
+// 0.25 ms, 0.96).  Widths a little above a power of two
 // leave lanes idle (136: 15 of 32), and that much of the rate.
 // Rounding: each output is rounded once, from fp32.
 #include <algorithm>

@@ -220,7 +220,10 @@ def trimul_relpos_destroy(r: RelPosPlan):
 
 
 class RelPos:
-    """A bucketed relative position bias: construct -> forward / backward -> free."""
+    """A bucketed relative position bias: construct -> forward / backward -> free.
+
+    "log" buckets have device memory: making them waits for their copy, and free (or the object's end) for the device,
+    so neither belongs into the capture of a graph."""
 
     def __init__(self, kind="linear", max_distance=32, num_buckets=None, bidirectional=True, groups=False, device=None):
         self.plan = trimul_relpos_create(kind, max_distance, num_buckets, bidirectional, groups, device)
@@ -394,8 +397,9 @@ class GradSet:
     """A list (or dict) of gradients whose norm is taken together: norm() and clip().
 
     `outs`: buffers of the same shapes and types for clipped copies (default: in place).  A set stands for the memory
-    that its tensors have when it is made, keeps it, and reads it at each call.  bf16, float16 and float32 may be mixed;
-    all on one device, contiguous.  clip() refuses a set with an output over another's memory, such as one tensor given
+    that its tensors have when it is made, keeps it, and reads it at each call: gradients that are new tensors each step
+    (trimul_backward without `grads`, zero_grad with set_to_none) need a new set each step, as one that is kept goes on
+    with the old memory.  bf16, float16 and float32 may be mixed; all on one device, contiguous.  clip() refuses a set with an output over another's memory, such as one tensor given
     twice."""
 
     def __init__(self, tensors, outs=None):

@@ -344,7 +344,8 @@ int trimul_kernels_per_forward_host(trimul_handle h, int B, int N);
  * where it needs one, from the caller, so calls on different streams (or
  * captured graphs) that have workspaces and outputs of their own may run at
  * once.  They allocate nothing and do not wait on the host (TRIMUL_FLAG_CHECK
- * aside), so every call may be captured in a CUDA graph.  Tensors are dense
+ * aside), so every call may be captured in a CUDA graph; making and releasing a
+ * relpos plan, which may allocate and wait, is done outside one.  Tensors are dense
  * with 16-byte aligned base addresses unless said otherwise, and the calling
  * thread's current device is left as it was.
  * ====================================================================== */
