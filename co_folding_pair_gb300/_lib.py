@@ -147,6 +147,31 @@ class GradTensor(ctypes.Structure):
     ]
 
 
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("param", "copy", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("numel", ctypes.c_int64),
+        ("weight_decay", ctypes.c_float),
+        ("param_type", ctypes.c_int),
+        ("copy_type", ctypes.c_int),
+        ("grad_type", ctypes.c_int),
+    ]
+
+
+class AdamwParams(ctypes.Structure):
+    _fields_ = [
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_float),
+        ("lr", ctypes.c_float),
+        ("lr_device", ctypes.c_void_p),
+        ("norm", ctypes.c_void_p),
+        ("max_norm", ctypes.c_float),
+        ("states", ctypes.c_int),
+        ("rounding", ctypes.c_int),
+        ("seed", ctypes.c_uint32),
+    ]
+
+
 # Exported entry points: name -> (restype, argtypes).  Mirrors include/trimul.h.
 _VP, _I, _U, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
 SIGNATURES = {
@@ -182,6 +207,7 @@ SIGNATURES = {
     "trimul_grad_workspace_bytes": (_S, [_I]),
     "trimul_grad_norm": (_I, [ctypes.POINTER(GradTensor), _I, _I, _VP, _VP, _S, _I, _VP, _U]),
     "trimul_grad_clip": (_I, [ctypes.POINTER(GradTensor), _I, ctypes.c_float, _I, _VP, _VP, _S, _I, _VP, _U]),
+    "trimul_adamw_step": (_I, [ctypes.POINTER(AdamwParams), ctypes.POINTER(AdamwTensor), _I, _VP, _I, _VP, _U]),
 }
 
 

@@ -1,0 +1,421 @@
+// k10_adamw.cu -- one AdamW step over many tensors.
+//
+//   g = c grad,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = p - lr wd p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// with c = min(1, max_norm / (norm + 1e-6)) where the gradients' norm is given:
+// the factor is applied here, so that clipping needs no pass of its own.  A
+// norm that is not finite makes the step nothing at all.
+//
+// One pass: every element of p, grad, m and v is read once and p, m, v and the
+// copy are written once.  Bound by memory.  A thread has four neighbours, a
+// warp 128: the 8-bit states' blocks, whose largest magnitudes two warp-wide
+// reductions give.
+//
+// 8-bit states hold m and r = sqrt(v) as e4m3 with an fp32 scale for each
+// block.  r and not v, because eight bits of e4m3 span 2^17 and a block's
+// gradients, squared, would not fit.  At b2 = 0.999 a step changes r by less
+// than a thousandth, and a code is an eighth: rounded to nearest, r would keep
+// its code until |g| is some eleven times r.  Rounded at random, it moves as
+// far as it should on average.
+//
+// A code is one of two neighbours, and an ulp in what is rounded can decide
+// which.  So all that leads to a code is rounded operation by operation (the _rn
+// intrinsics are not fused): the states are those of plain fp32 arithmetic, bit
+// for bit.  What leads to the parameter alone may be approximate.
+//
+// The random bits are a hash of the seed, the step, the tensor's number and
+// the element's, the PCG hash of Jarzynski and Olano, "Hash Functions for GPU
+// Rendering" (2020): nothing is kept for them, and a step can be repeated.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda_fp8.h>
+
+#include "pair_ops.cuh"
+#include "step_ops.h"
+
+namespace trimul {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kEach = 4;                   // neighbours of a thread
+constexpr int kChunk = kThreads * kEach;   // elements of a block's turn
+constexpr int kBlocksPerSm = 5, kMostBlocks = 1024;
+constexpr int kTableSmall = 64, kTableMax = 384;  // tensors of one launch
+static_assert(32 * kEach == TRIMUL_STATE_BLOCK, "a warp has one block of the 8-bit states");
+
+enum : uint8_t { PARAM_BF16 = 1, GRAD_SHIFT = 1, COPY_SHIFT = 3, WIDE = 32 };  // of Table::kind
+
+// The tensors of a launch, in its parameters.
+template <int N>
+struct Table {
+  int n;
+  uint32_t chunks;
+  void* param[N];
+  void* copy[N];
+  const void* grad[N];
+  void* m[N];
+  void* v[N];
+  float* m_scale[N];
+  float* v_scale[N];
+  long long numel[N];
+  float decay[N];
+  uint32_t index[N];                // the tensor's number in the call
+  uint32_t chunk[N + 1];            // each tensor's first chunk, and the number of all
+  uint16_t begin[kMostBlocks + 1];  // the tensor of each run's first chunk
+  uint8_t kind[N];
+};
+
+struct Hyper {
+  float b1, not_b1, b2, not_b2, log_b1, log_b2, eps, lr;
+  const float* lr_device;
+  const float* norm;
+  float max_norm;
+  uint32_t seed;
+  int stochastic;
+};
+static_assert(sizeof(Table<kTableMax>) + sizeof(Hyper) + 64 <= 32764, "the table and the other arguments fit a launch's parameters");
+
+struct Entry {
+  void *param, *copy;
+  const void* grad;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  long long numel;
+  float decay;
+  uint32_t chunk, key;
+  int kind;
+};
+
+__device__ __forceinline__ uint32_t hash(uint32_t x) {
+  x = x * 747796405u + 2891336453u;
+  x = ((x >> ((x >> 28) + 4)) ^ x) * 277803737u;
+  return (x >> 22) ^ x;
+}
+
+// ------------------------------------------------------------------ four neighbours
+// Elements i .. i + 3 of a tensor of n; `wide`: in one access where they are all there.
+__device__ __forceinline__ void load4(const void* p, int type, long long i, long long n, bool wide, float (&f)[4]) {
+  if (wide && i + 4 <= n) {
+    if (type == TRIMUL_F32) {
+      const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+      if (type == TRIMUL_BF16) {
+        f[0] = bf16_lo(q.x), f[1] = bf16_hi(q.x), f[2] = bf16_lo(q.y), f[3] = bf16_hi(q.y);
+      } else {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&q.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
+        f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[e] = 0.f;
+    if (i + e < n)
+      f[e] = type == TRIMUL_F32    ? static_cast<const float*>(p)[i + e]
+             : type == TRIMUL_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i + e])
+                                   : __half2float(static_cast<const __half*>(p)[i + e]);
+  }
+}
+__device__ __forceinline__ void store4(void* p, int type, long long i, long long n, bool wide, const float (&f)[4]) {
+  if (wide && i + 4 <= n) {
+    if (type == TRIMUL_F32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+          type == TRIMUL_BF16 ? make_uint2(pack_bf162(f[0], f[1]), pack_bf162(f[2], f[3]))
+                              : make_uint2(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (i + e >= n) continue;
+    if (type == TRIMUL_F32)
+      static_cast<float*>(p)[i + e] = f[e];
+    else if (type == TRIMUL_BF16)
+      static_cast<__nv_bfloat16*>(p)[i + e] = __float2bfloat16_rn(f[e]);
+    else
+      static_cast<__half*>(p)[i + e] = __float2half_rn(f[e]);
+  }
+}
+
+// ------------------------------------------------------------------ 8-bit states
+__device__ __forceinline__ void unpack_codes(uint32_t w, float scale, float (&f)[4]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * e)), __NV_E4M3);
+    const float2 v = __half22float2(__half2(h));
+    f[2 * e] = __fmul_rn(v.x, scale), f[2 * e + 1] = __fmul_rn(v.y, scale);
+  }
+}
+__device__ __forceinline__ uint32_t pack_codes(const float (&f)[4]) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
+// The largest magnitude of a warp's 128 numbers (a NaN's bits are above infinity's).
+__device__ __forceinline__ float warp_largest(const float (&f)[4]) {
+  unsigned top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+}
+
+// x / scale as a number that e4m3 has: one of the two neighbours, the upper one
+// with the probability of x's place between them (to 16 bits).  Below 2^-6,
+// where the codes are evenly spaced, they are as far apart as just above it, so
+// 2^-6 is added for the rounding.
+__device__ __forceinline__ float at_random(float x, uint32_t bits16) {
+  const float a = fabsf(x);
+  const float base = a < 0x1p-6f ? 0x1p-6f : 0.f;
+  const uint32_t t = (__float_as_uint(a + base) + (bits16 << 4)) & 0xfff00000u;
+  return copysignf(fminf(__uint_as_float(t) - base, 448.f), x);
+}
+
+// A warp's block as codes; returns its scale.  `least`: what is above zero keeps a code above zero.
+__device__ __forceinline__ float quantize(const float (&f)[4], const uint32_t (&bits)[4], int shift, bool stochastic,
+                                          bool least, uint32_t& codes) {
+  const float scale = __fmul_rn(fmaxf(warp_largest(f), 0x1p-90f), 1.f / 448.f);
+  const float inv = __frcp_rn(scale);
+  float q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    q[e] = __fmul_rn(f[e], inv);
+    if (stochastic) q[e] = at_random(q[e], bits[e] >> shift & 0xffffu);
+    if (least && f[e] > 0.f) q[e] = fmaxf(q[e], 0x1p-9f);
+  }
+  codes = pack_codes(q);
+  return scale;
+}
+
+// ------------------------------------------------------------------ the step
+__device__ __forceinline__ float root(float x) {  // within 2 ulp
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// What all elements of a step have in common.
+struct Step {
+  bool run;
+  float clip, lr, rate, over_c2;  // rate: lr / (1 - b1^t)
+  uint32_t key;
+};
+__device__ __forceinline__ Step step_of(const Hyper& h, int count) {
+  Step s;
+  s.run = true, s.clip = 1.f;
+  if (h.norm) {
+    const float norm = *h.norm, share = __fmul_rn(h.max_norm, __frcp_rn(__fadd_rn(norm, 1e-6f)));
+    s.run = norm - norm == 0.f;
+    s.clip = share < 1.f ? share : 1.f;
+  }
+  const float t = static_cast<float>(count + 1);
+  s.lr = h.lr_device ? *h.lr_device : h.lr;
+  // 1 - b^t without the cancellation of early steps
+  s.rate = s.lr / -expm1f(t * h.log_b1);
+  s.over_c2 = 1.f / -expm1f(t * h.log_b2);
+  s.key = hash(static_cast<uint32_t>(count + 1) + hash(h.seed));
+  return s;
+}
+
+template <int N>
+__device__ __forceinline__ Entry entry(const Table<N>& tab, int k, const Step& s) {
+  return Entry{tab.param[k],   tab.copy[k],  tab.grad[k],  tab.m[k],     tab.v[k],
+               tab.m_scale[k], tab.v_scale[k], tab.numel[k], tab.decay[k], tab.chunk[k],
+               hash(tab.index[k] + s.key), tab.kind[k]};
+}
+
+template <bool k8>
+__device__ __forceinline__ void step_chunk(const Entry& t, uint32_t chunk, const Hyper& h, const Step& s) {
+  const long long i = static_cast<long long>(chunk - t.chunk) * kChunk + threadIdx.x * kEach;
+  const long long block = i / TRIMUL_STATE_BLOCK;  // the same for a warp
+  if (block * TRIMUL_STATE_BLOCK >= t.numel) return;
+  const bool wide = t.kind & WIDE, stochastic = h.stochastic;
+  const int ptype = t.kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32;
+  const int copy = t.kind >> COPY_SHIFT & 3;
+  float p[4], g[4], m[4], v[4];
+  if (k8) {
+    uint32_t mc = 0, vc = 0;
+    const bool whole = i + 4 <= t.numel;
+    if (whole) {
+      mc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i);
+      vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < t.numel) {
+          mc |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.m)[i + e]) << (8 * e);
+          vc |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.v)[i + e]) << (8 * e);
+        }
+    }
+    const float ms = t.m_scale[block], vs = t.v_scale[block];
+    load4(t.param, ptype, i, t.numel, wide, p);
+    load4(t.grad, t.kind >> GRAD_SHIFT & 3, i, t.numel, wide, g);
+    unpack_codes(mc, ms, m);
+    unpack_codes(vc, vs, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(v[e], v[e]);
+  } else {
+    load4(t.m, TRIMUL_F32, i, t.numel, true, m);
+    load4(t.v, TRIMUL_F32, i, t.numel, true, v);
+    load4(t.param, ptype, i, t.numel, wide, p);
+    load4(t.grad, t.kind >> GRAD_SHIFT & 3, i, t.numel, wide, g);
+  }
+  const float keep = 1.f - s.lr * t.decay;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float ge = __fmul_rn(g[e], s.clip);
+    m[e] = __fadd_rn(__fmul_rn(h.b1, m[e]), __fmul_rn(h.not_b1, ge));
+    v[e] = __fadd_rn(__fmul_rn(h.b2, v[e]), __fmul_rn(__fmul_rn(h.not_b2, ge), ge));
+    p[e] = p[e] * keep - s.rate * m[e] / (root(v[e] * s.over_c2) + h.eps);
+  }
+  uint32_t bits[4] = {0, 0, 0, 0};
+  if (stochastic && (k8 || ptype == TRIMUL_BF16)) {
+    const uint32_t key = hash(t.key + static_cast<uint32_t>(i >> 32));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bits[e] = hash(key ^ (static_cast<uint32_t>(i) + e));
+  }
+  if (copy) store4(t.copy, copy == 1 ? TRIMUL_BF16 : TRIMUL_F16, i, t.numel, wide, p);
+  if (ptype == TRIMUL_BF16 && stochastic) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (fabsf(p[e]) < INFINITY) p[e] = __uint_as_float((__float_as_uint(p[e]) + (hash(bits[e]) & 0xffffu)) & 0xffff0000u);
+  }
+  store4(t.param, ptype, i, t.numel, wide, p);
+  if (k8) {
+    uint32_t mc, vc;
+    const float ms = quantize(m, bits, 0, stochastic, false, mc);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __fsqrt_rn(v[e]);
+    const float vs = quantize(v, bits, 16, stochastic, true, vc);
+    if (i + 4 <= t.numel) {
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i) = mc;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i) = vc;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < t.numel) {
+          static_cast<uint8_t*>(t.m)[i + e] = static_cast<uint8_t>(mc >> (8 * e));
+          static_cast<uint8_t*>(t.v)[i + e] = static_cast<uint8_t>(vc >> (8 * e));
+        }
+    }
+    if (threadIdx.x % 32 == 0) t.m_scale[block] = ms, t.v_scale[block] = vs;
+  } else {
+    store4(t.m, TRIMUL_F32, i, t.numel, true, m);
+    store4(t.v, TRIMUL_F32, i, t.numel, true, v);
+  }
+}
+
+__host__ __device__ __forceinline__ uint32_t run_begin(uint32_t chunks, uint32_t block, uint32_t blocks) {
+  return static_cast<uint32_t>(static_cast<unsigned long long>(chunks) * block / blocks);
+}
+
+// count: {steps taken, blocks of the last launch that are done}.  Every block
+// reads the steps before it says that it is done, and the last one of the last
+// launch counts the step.
+template <bool k8, int N>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    k10_adamw(const __grid_constant__ Table<N> tab, const __grid_constant__ Hyper h, int* count, int last_launch) {
+  const Step s = step_of(h, *static_cast<volatile int*>(count));
+  if (s.run) {
+    const uint32_t c0 = run_begin(tab.chunks, blockIdx.x, gridDim.x), c1 = run_begin(tab.chunks, blockIdx.x + 1, gridDim.x);
+    if (c0 < c1) {
+      int k = tab.begin[blockIdx.x];
+      Entry t = entry(tab, k, s);
+      uint32_t end = tab.chunk[k + 1];
+      for (uint32_t chunk = c0; chunk < c1; ++chunk) {
+        if (chunk >= end) {
+          t = entry(tab, ++k, s);
+          end = tab.chunk[k + 1];
+        }
+        step_chunk<k8>(t, chunk, h, s);
+      }
+    }
+  }
+  if (!last_launch) return;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(count + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+      count[1] = 0;
+      if (s.run) count[0] += 1;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+template <int N>
+int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int num_sms) {
+  tab.n = 0;
+  tab.chunks = 0;
+  for (; k < n && tab.n < N; ++k) {
+    if (t[k].numel == 0) continue;
+    const int q = tab.n++;
+    tab.param[q] = t[k].param;
+    tab.copy[q] = t[k].copy;
+    tab.grad[q] = t[k].grad;
+    tab.m[q] = t[k].m;
+    tab.v[q] = t[k].v;
+    tab.m_scale[q] = t[k].m_scale;
+    tab.v_scale[q] = t[k].v_scale;
+    tab.numel[q] = t[k].numel;
+    tab.decay[q] = t[k].weight_decay;
+    tab.index[q] = static_cast<uint32_t>(k);
+    const int copy = !t[k].copy ? 0 : t[k].copy_type == TRIMUL_BF16 ? 1 : 2;
+    const bool wide = aligned_to(t[k].param, t[k].param_type == TRIMUL_F32 ? 16 : 8) &&
+                      aligned_to(t[k].grad, t[k].grad_type == TRIMUL_F32 ? 16 : 8) && (!copy || aligned_to(t[k].copy, 8));
+    tab.kind[q] = static_cast<uint8_t>((t[k].param_type == TRIMUL_BF16 ? PARAM_BF16 : 0) | t[k].grad_type << GRAD_SHIFT |
+                                       copy << COPY_SHIFT | (wide ? WIDE : 0));
+    tab.chunk[q] = tab.chunks;
+    tab.chunks += static_cast<uint32_t>((t[k].numel + kChunk - 1) / kChunk);
+  }
+  tab.chunk[tab.n] = tab.chunks;
+  const int most = std::min(kMostBlocks, kBlocksPerSm * num_sms);
+  const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(tab.chunks, most)));
+  int at = 0;
+  for (int block = 0; block <= grid; ++block) {
+    const uint32_t first = run_begin(tab.chunks, block, grid);
+    while (at + 1 < tab.n && tab.chunk[at + 1] <= first) ++at;
+    tab.begin[block] = static_cast<uint16_t>(at);
+  }
+  return grid;
+}
+
+template <bool k8, int N>
+cudaError_t run(const Hyper& h, const trimul_adamw_tensor* t, int n, int32_t* count, int num_sms, cudaStream_t s) {
+  Table<N> tab;
+  int k = 0;
+  do {
+    const int grid = fill(tab, t, n, k, num_sms);
+    k10_adamw<k8, N><<<grid, kThreads, 0, s>>>(tab, h, count, k >= n);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  } while (k < n);
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const trimul_adamw_params& p, const trimul_adamw_tensor* t, int n, int32_t* count, int num_sms,
+                         cudaStream_t s) {
+  Hyper h{};
+  h.b1 = static_cast<float>(p.beta1), h.not_b1 = static_cast<float>(1.0 - p.beta1);
+  h.b2 = static_cast<float>(p.beta2), h.not_b2 = static_cast<float>(1.0 - p.beta2);
+  h.log_b1 = static_cast<float>(std::log(p.beta1)), h.log_b2 = static_cast<float>(std::log(p.beta2));
+  h.eps = p.eps, h.lr = p.lr, h.lr_device = p.lr_device;
+  h.norm = p.norm, h.max_norm = p.max_norm;
+  h.seed = p.seed, h.stochastic = p.rounding == TRIMUL_ROUND_STOCHASTIC;
+  if (p.states == TRIMUL_STATES_E4M3)
+    return n <= kTableSmall ? run<true, kTableSmall>(h, t, n, count, num_sms, s) : run<true, kTableMax>(h, t, n, count, num_sms, s);
+  return n <= kTableSmall ? run<false, kTableSmall>(h, t, n, count, num_sms, s) : run<false, kTableMax>(h, t, n, count, num_sms, s);
+}
+
+}  // namespace trimul

@@ -1,0 +1,144 @@
+"""Python binding of the operators that end a training step (include/trimul.h): argument marshalling
+only.
+
+  AdamW    one step over many tensors, with states in 32 bits or in 8, which clips by the norm of a
+           GradSet in the same pass
+
+The class wraps the C entry point as those of ``pair_ops`` wrap theirs: calls take ``stream`` (default:
+the current one), do not wait on the host and may be captured; without the library or an sm_103 device
+they raise.
+"""
+
+from __future__ import annotations
+
+
+import numpy as np
+import torch
+
+from . import _lib
+from .pair_ops import _TYPES, GradSet, _cuda, _fits, _one_of, _raw, _refuse, _shared, _type
+from .trimul import FLAG_CHECK, _check  # noqa: F401
+
+_STATES = {"float32": 0, "8bit": 1}
+_ROUNDING = {"nearest": 0, "stochastic": 1}
+BLOCK = 128  # neighbours that share a scale in the 8-bit states
+_BYTES = np.array([2, 4, 2], dtype=np.int64)  # of _TYPES
+
+
+def _listed(v, n, name):
+    """A value for each of n tensors, from one for all, a list or a dict."""
+    if isinstance(v, dict):
+        v = list(v.values())
+    if not isinstance(v, (list, tuple)):
+        return [v] * n
+    if len(v) != n:
+        raise ValueError(f"{len(v)} {name} for {n} params")
+    return list(v)
+
+
+class AdamW:
+    """AdamW (decoupled weight decay) over a list (or dict) of parameters: step(grads).
+
+    params: float32 or bf16, updated in place; copies: for each parameter a bf16 or float16 tensor of its shape that
+    gets the new value rounded to nearest, or None (default: none); weight_decay: one number, or one for each
+    parameter.  states: "float32", or "8bit" for e4m3 codes with a scale for each 128 neighbours.  rounding: how bf16
+    parameters and 8-bit states are rounded, "stochastic" (at random, by a hash of `seed`, the step and the element)
+    or "nearest".
+
+    `state` has the states of all parameters behind one another, each from a multiple of 128 on (`starts`): "m", "v" and
+    "count", the steps taken (int32, on the device), and with "8bit" "m_scale" and "v_scale" by blocks, "v" then being
+    the codes of v's root.  A checkpoint keeps these tensors, and goes on by copying into them.  The object stands for
+    the memory that its tensors have when it is made, and keeps it.  No parameter or copy may lie over another one, nor a
+    gradient over any of them."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, states="float32", copies=None,
+                 rounding="stochastic", seed=0):
+        params = list(params.values() if isinstance(params, dict) else params)
+        n = len(params)
+        copies = _listed(copies, n, "copies")
+        decay = _listed(weight_decay, n, "weight_decay")
+        self.params, self.copies, self.lr = params, copies, lr
+        self.device = _cuda(params[0], "params[0]") if params else torch.cuda.current_device()
+        for k, (p, c) in enumerate(zip(params, copies)):
+            _type(p.dtype, f"params[{k}]")
+            if not _fits(p, p.dtype, p.shape, self.device):
+                _refuse(p, p.dtype, p.shape, self.device, f"params[{k}]")
+            if c is None:
+                continue
+            if c.dtype not in (torch.bfloat16, torch.float16):
+                raise TypeError(f"copies[{k}] must be bf16 or float16, got {c.dtype}")
+            if not _fits(c, c.dtype, p.shape, self.device):
+                _refuse(c, c.dtype, p.shape, self.device, f"copies[{k}]")
+        self._memory = [t.untyped_storage() for t in params + copies if t is not None]
+        self.eight = _one_of(_STATES, states, "states") == 1
+        numel = np.array([p.numel() for p in params], dtype=np.int64)
+        padded = -(-numel // BLOCK) * BLOCK
+        starts = np.concatenate([[0], np.cumsum(padded)])
+        total, dev = int(starts[-1]), torch.device("cuda", self.device)
+        self.starts = [int(v) for v in starts[:-1]]
+        self._count = torch.zeros(2, dtype=torch.int32, device=dev)
+        kind = torch.float8_e4m3fn if self.eight else torch.float32
+        self.state = {k: torch.zeros(total, dtype=kind, device=dev) for k in "mv"}
+        if self.eight:
+            self.state.update({k + "_scale": torch.zeros(total // BLOCK, dtype=torch.float32, device=dev) for k in "mv"})
+        self.state["count"] = self._count[0]
+        # one row of numbers for each tensor, as _lib.AdamwTensor lays them out
+        rows = np.zeros(n, dtype=np.dtype([("param", "<i8"), ("copy", "<i8"), ("grad", "<i8"), ("m", "<i8"), ("v", "<i8"),
+                                           ("m_scale", "<i8"), ("v_scale", "<i8"), ("numel", "<i8"), ("weight_decay", "<f4"),
+                                           ("param_type", "<i4"), ("copy_type", "<i4"), ("grad_type", "<i4")]))
+        rows["param"] = [p.data_ptr() for p in params]
+        rows["copy"] = [0 if c is None else c.data_ptr() for c in copies]
+        rows["numel"], rows["weight_decay"] = numel, decay
+        rows["param_type"] = [_TYPES[p.dtype] for p in params]
+        rows["copy_type"] = [0 if c is None else _TYPES[c.dtype] for c in copies]
+        for k in "mv":
+            rows[k] = self.state[k].data_ptr() + starts[:-1] * (1 if self.eight else 4)
+            if self.eight:
+                rows[k + "_scale"] = self.state[k + "_scale"].data_ptr() + starts[:-1] // BLOCK * 4
+        at = np.concatenate([rows["param"], rows["copy"]])
+        both = _shared(at, at, np.concatenate([numel * _BYTES[rows["param_type"]], np.where(rows["copy"] != 0, 2 * numel, 0)]))
+        if both:
+            names = [f"{'params' if k < n else 'copies'}[{k % n}]" for k in both]
+            raise ValueError(f"{names[1]} overlaps {names[0]}")
+        self._rows = rows
+        self.table = (_lib.AdamwTensor * n).from_buffer(rows) if n else (_lib.AdamwTensor * 0)()
+        self._p = _lib.AdamwParams(beta1=betas[0], beta2=betas[1], eps=eps, lr=0.0, states=int(self.eight),
+                                   rounding=_one_of(_ROUNDING, rounding, "rounding"), seed=seed & 0xFFFFFFFF)
+
+    def step(self, grads, lr=None, norm=None, max_norm=None, stream=None, flags: int = 0):
+        """One step with `grads` (a GradSet, a list or a dict, in the parameters' order; bf16, float16 or float32).
+
+        lr: for this step and the later ones, a number or a float32 tensor on the device, which a captured step reads
+        each time; norm (GradSet.norm's, on the device) and max_norm: clip by it in the same pass; a norm that is not
+        finite makes the step nothing."""
+        if not isinstance(grads, GradSet):
+            grads = GradSet(grads)
+        rows, p = self._rows, self._p
+        if len(grads.tensors) != len(rows):
+            raise ValueError(f"{len(grads.tensors)} grads for {len(rows)} params")
+        if len(rows):
+            data, _, numel, kinds = grads._rows.T
+            if not np.array_equal(numel, rows["numel"]):
+                k = int(np.flatnonzero(numel != rows["numel"])[0])
+                raise ValueError(f"grads[{k}] must be {tuple(self.params[k].shape)}, got {tuple(grads.tensors[k].shape)}")
+            if grads.device != self.device:
+                raise ValueError(f"grads must be on cuda:{self.device}, got cuda:{grads.device}")
+            rows["grad"], rows["grad_type"] = data, kinds
+        if lr is not None:
+            self.lr = lr
+        if (norm is None) != (max_norm is None):
+            raise ValueError("give both norm and max_norm, or neither")
+        p.norm, p.max_norm = self._one(norm, "norm"), 0.0 if max_norm is None else max_norm
+        if isinstance(self.lr, torch.Tensor):
+            p.lr, p.lr_device = 0.0, self._one(self.lr, "lr")
+        else:
+            p.lr, p.lr_device = self.lr, None
+        _check(_lib.load().trimul_adamw_step(p, self.table, len(rows), self._count.data_ptr(), self.device,
+                                             _raw(stream, self.device), flags))
+
+    def _one(self, t, name):
+        if t is None:
+            return None
+        if t.dtype != torch.float32 or t.numel() != 1 or t.get_device() != self.device:
+            raise ValueError(f"{name} must be one float32 on cuda:{self.device}")
+        return t.data_ptr()

@@ -532,6 +532,73 @@ trimul_status trimul_grad_clip(const trimul_grad_tensor* tensors, int n, float m
                                float* norm, void* workspace, size_t workspace_bytes, int device, void* stream,
                                unsigned flags);
 
+/* ---------------------------------------------------------------- AdamW
+ * One step of AdamW (decoupled weight decay) over n tensors, t = count + 1:
+ *
+ *   g = c grad                                   c: 1, or min(1, max_norm / (norm + 1e-6)) where `norm` is given
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ *
+ * in 32 bits, in one pass over the tensors: with the norm of trimul_grad_norm
+ * the gradients are clipped as trimul_grad_clip clips them, without a pass of
+ * its own.  Where that norm is not finite, the step is nothing: parameters,
+ * copies, states and count stay as they are.
+ *
+ * States in 8 bits (TRIMUL_STATES_E4M3): m, and r = sqrt(v), are held as e4m3
+ * codes with an f32 scale for each 128 neighbours of a tensor (the last block
+ * may have fewer).  A block with a value that is not finite is not finite
+ * afterwards, all of it.
+ *
+ *   scale = max(max |x|, 2^-90) / 448,   code = e4m3(x / scale),   r's code at least 2^-9 where r > 0
+ *
+ * What is kept in fewer than 32 bits from step to step, 8-bit states and bf16
+ * parameters, is rounded to the nearest number, or at random to one of its two
+ * neighbours (TRIMUL_ROUND_STOCHASTIC): each with a probability that makes the
+ * mean the value, to 16 bits.  The random bits are a hash of the seed, t, the
+ * tensor's place in `tensors` and the element's in the tensor, so a step gives
+ * the same bits each time, on any stream.
+ */
+#define TRIMUL_STATE_BLOCK 128
+
+typedef enum { TRIMUL_STATES_F32 = 0, TRIMUL_STATES_E4M3 = 1 } trimul_states;
+typedef enum { TRIMUL_ROUND_NEAREST = 0, TRIMUL_ROUND_STOCHASTIC = 1 } trimul_rounding;
+
+typedef struct {
+  void* param;                      /* DEVICE, F32 or BF16, aligned to its element, overwritten */
+  void* copy;                       /* the new value rounded to nearest, BF16 or F16; NULL: not wanted */
+  const void* grad;                 /* F32, BF16 or F16 */
+  void* m;                          /* 16-byte aligned: f32 [numel], or e4m3 codes [numel] */
+  void* v;                          /* likewise: v as f32, or the codes of its root */
+  float* m_scale;                   /* E4M3: f32 [ceil(numel / 128)], 4-byte aligned; F32: not looked at */
+  float* v_scale;
+  int64_t numel;                    /* >= 0; the pointers may be NULL where it is 0 */
+  float weight_decay;               /* finite, >= 0 */
+  trimul_dtype param_type;
+  trimul_dtype copy_type;
+  trimul_dtype grad_type;
+} trimul_adamw_tensor;
+
+typedef struct {
+  double beta1, beta2;              /* in [0, 1) */
+  float eps;                        /* > 0, and no subnormal number */
+  float lr;                         /* finite; not looked at where lr_device is given */
+  const float* lr_device;           /* DEVICE f32[1], read by the kernels (a captured step's learning rate); NULL: lr */
+  const float* norm;                /* DEVICE f32[1]: the gradients' norm; NULL: no clipping */
+  float max_norm;                   /* >= 0; not looked at without norm */
+  trimul_states states;
+  trimul_rounding rounding;
+  uint32_t seed;
+} trimul_adamw_params;
+
+/*
+ * `tensors` and `p` are HOST memory, read during the call.  count: DEVICE int32[2], the steps taken so far (the call adds
+ * one) and a word for the kernels, 0 at first and between calls; steps of one count are ordered by the caller.  No output (param, copy,
+ * states, count) may overlap anything else; within one entry of `tensors` that is checked, between two it is not.
+ */
+trimul_status trimul_adamw_step(const trimul_adamw_params* p, const trimul_adamw_tensor* tensors, int n, int32_t* count,
+                                int device, void* stream, unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif
