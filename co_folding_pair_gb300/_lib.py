@@ -208,6 +208,12 @@ SIGNATURES = {
     "trimul_grad_norm": (_I, [ctypes.POINTER(GradTensor), _I, _I, _VP, _VP, _S, _I, _VP, _U]),
     "trimul_grad_clip": (_I, [ctypes.POINTER(GradTensor), _I, ctypes.c_float, _I, _VP, _VP, _S, _I, _VP, _U]),
     "trimul_adamw_step": (_I, [ctypes.POINTER(AdamwParams), ctypes.POINTER(AdamwTensor), _I, _VP, _I, _VP, _U]),
+    "trimul_linear8_packed_bytes": (_S, [_I, _I]),
+    "trimul_linear8_pack": (_I, [_VP, _I, _I, _I, _VP, _S, _I, _VP, _U]),
+    "trimul_linear8_forward_workspace_bytes": (_S, [ctypes.c_int64, _I, _I]),
+    "trimul_linear8_forward": (_I, [_VP, _VP, _VP, ctypes.c_int64, _I, _I, _VP, _VP, _S, _I, _VP, _U]),
+    "trimul_linear8_backward_workspace_bytes": (_S, [ctypes.c_int64, _I, _I]),
+    "trimul_linear8_backward": (_I, [_VP, _VP, _VP, ctypes.c_int64, _I, _I, _VP, _VP, _VP, _VP, _S, _I, _VP, _U]),
 }
 
 

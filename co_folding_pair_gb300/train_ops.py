@@ -3,8 +3,10 @@ only.
 
   AdamW    one step over many tensors, with states in 32 bits or in 8, which clips by the norm of a
            GradSet in the same pass
+  Linear8  a linear layer whose operands are 8-bit floating point with a power of two for each block
+           of 128, and its gradients
 
-The class wraps the C entry point as those of ``pair_ops`` wrap theirs: calls take ``stream`` (default:
+The functions keep the C names; the classes wrap them as those of ``pair_ops`` do: calls take ``stream`` (default:
 the current one), do not wait on the host and may be captured; without the library or an sm_103 device
 they raise.
 """
@@ -16,8 +18,8 @@ import numpy as np
 import torch
 
 from . import _lib
-from .pair_ops import _TYPES, GradSet, _cuda, _fits, _one_of, _raw, _refuse, _shared, _type
-from .trimul import FLAG_CHECK, _check  # noqa: F401
+from .pair_ops import _TYPES, GradSet, _cuda, _empty, _fits, _one_of, _ptr, _raw, _refuse, _shared, _type
+from .trimul import FLAG_CHECK, FLAG_INJECT_STALL, _check  # noqa: F401
 
 _STATES = {"float32": 0, "8bit": 1}
 _ROUNDING = {"nearest": 0, "stochastic": 1}
@@ -142,3 +144,121 @@ class AdamW:
         if t.dtype != torch.float32 or t.numel() != 1 or t.get_device() != self.device:
             raise ValueError(f"{name} must be one float32 on cuda:{self.device}")
         return t.data_ptr()
+
+
+# ------------------------------------------------------------------ linear layer in 8 bits
+def _rows(x, width, dev, name):
+    """The rows of a bf16 tensor [..., width]."""
+    if x.dim() < 1 or x.shape[-1] != width:
+        raise ValueError(f"{name} must be [..., {width}], got {tuple(x.shape)}")
+    if not _fits(x, torch.bfloat16, x.shape, dev):
+        _refuse(x, torch.bfloat16, x.shape, dev, name)
+    return x.numel() // width
+
+
+def trimul_linear8_pack(weight, packed=None, stream=None, flags: int = 0):
+    """The weight [N, K] (bf16 or float32) as the calls below read it, a uint8 tensor; written to `packed` if that is given."""
+    dev = _cuda(weight, "weight")
+    kind = _type(weight.dtype, "weight")
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [N, K], got {tuple(weight.shape)}")
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    N, K = weight.shape
+    lib = _lib.load()
+    need = lib.trimul_linear8_packed_bytes(N, K)
+    if packed is None:
+        packed = _empty(need, torch.uint8, weight.device, stream)
+    elif not _fits(packed, torch.uint8, (need,), dev):
+        _refuse(packed, torch.uint8, (need,), dev, "packed")
+    _check(lib.trimul_linear8_pack(weight.data_ptr(), kind, N, K, packed.data_ptr(), need, dev, _raw(stream, dev), flags))
+    return packed
+
+
+def trimul_linear8_forward(packed, N, K, x, bias=None, out=None, stream=None, flags: int = 0):
+    """x W^T + bias: bf16 [..., N] for bf16 x [..., K]; bias: float32 [N]."""
+    dev = _cuda(packed, "packed")
+    lib = _lib.load()
+    _packed(lib, packed, N, K, dev)
+    rows = _rows(x, K, dev, "x")
+    if bias is not None and not _fits(bias, torch.float32, (N,), dev):
+        _refuse(bias, torch.float32, (N,), dev, "bias")
+    shape = (*x.shape[:-1], N)
+    if out is None:
+        out = _empty(shape, torch.bfloat16, x.device, stream)
+    elif not _fits(out, torch.bfloat16, shape, dev):
+        _refuse(out, torch.bfloat16, shape, dev, "out")
+    need = lib.trimul_linear8_forward_workspace_bytes(rows, N, K)
+    ws = _empty(need, torch.uint8, x.device, stream)
+    _check(lib.trimul_linear8_forward(packed.data_ptr(), _ptr(bias), x.data_ptr(), rows, N, K, out.data_ptr(), ws.data_ptr(), need,
+                                      dev, _raw(stream, dev), flags))
+    return out
+
+
+def trimul_linear8_backward(packed, N, K, x, dy, dx=None, dw=None, dbias=None, want=("dx", "dw", "dbias"), stream=None,
+                            flags: int = 0):
+    """{"dx", "dw", "dbias"} for dy (bf16 [..., N]) with respect to the output: bf16 like x, float32 [N, K] and [N]; those that
+    `want` does not name are None."""
+    dev = _cuda(packed, "packed")
+    lib = _lib.load()
+    _packed(lib, packed, N, K, dev)
+    rows = _rows(x, K, dev, "x")
+    if _rows(dy, N, dev, "dy") != rows or dy.shape[:-1] != x.shape[:-1]:
+        raise ValueError(f"dy must be {(*x.shape[:-1], N)}, got {tuple(dy.shape)}")
+    for k in want:
+        if k not in ("dx", "dw", "dbias"):
+            raise ValueError(f"unknown gradient {k!r}: dx, dw and dbias are given")
+    got = {}
+    for name, t, dtype, shape in (("dx", dx, torch.bfloat16, x.shape), ("dw", dw, torch.float32, (N, K)), ("dbias", dbias, torch.float32, (N,))):
+        if name not in want:
+            got[name] = None
+        elif t is None:
+            got[name] = _empty(shape, dtype, x.device, stream)
+        else:
+            if not _fits(t, dtype, shape, dev):
+                _refuse(t, dtype, shape, dev, name)
+            got[name] = t
+    need = lib.trimul_linear8_backward_workspace_bytes(rows, N, K)
+    ws = _empty(need, torch.uint8, x.device, stream)
+    _check(lib.trimul_linear8_backward(packed.data_ptr(), x.data_ptr(), dy.data_ptr(), rows, N, K, _ptr(got["dx"]), _ptr(got["dw"]),
+                                       _ptr(got["dbias"]), ws.data_ptr(), need, dev, _raw(stream, dev), flags))
+    return got
+
+
+def _packed(lib, packed, N, K, dev):
+    need = lib.trimul_linear8_packed_bytes(N, K)
+    if need == 0:
+        raise ValueError(f"N ({N}) and K ({K}) must be multiples of 8 in [8, 65536]")
+    if not _fits(packed, torch.uint8, (need,), dev):
+        _refuse(packed, torch.uint8, (need,), dev, "packed")
+
+
+class Linear8:
+    """A linear layer in 8 bits: forward(x) and backward(x, dy).
+
+    The weight [N, K] (bf16 or float32) is rounded to 8 bits when the object is made, and again by pack(weight) after
+    each change of it, such as an optimiser's step; the object keeps the 8-bit form, not the weight.  bias: float32 [N],
+    read at each call."""
+
+    def __init__(self, weight, bias=None):
+        self.packed = trimul_linear8_pack(weight)
+        self.N, self.K = weight.shape
+        self.bias = bias
+        if bias is not None and not _fits(bias, torch.float32, (self.N,), weight.get_device()):
+            _refuse(bias, torch.float32, (self.N,), weight.get_device(), "bias")
+
+    def pack(self, weight, stream=None, flags: int = 0):
+        if tuple(weight.shape) != (self.N, self.K):
+            raise ValueError(f"weight must be {(self.N, self.K)}, got {tuple(weight.shape)}")
+        trimul_linear8_pack(weight, self.packed, stream, flags)
+
+    def forward(self, x, out=None, stream=None, flags: int = 0):
+        return trimul_linear8_forward(self.packed, self.N, self.K, x, self.bias, out, stream, flags)
+
+    __call__ = forward
+
+    def backward(self, x, dy, dx=None, dw=None, dbias=None, want=None, stream=None, flags: int = 0):
+        """{"dx", "dw", "dbias"}; dbias is None for a layer without bias, and what `want` does not name."""
+        if want is None:
+            want = ("dx", "dw", "dbias") if self.bias is not None else ("dx", "dw")
+        return trimul_linear8_backward(self.packed, self.N, self.K, x, dy, dx, dw, dbias, want, stream, flags)

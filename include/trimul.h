@@ -599,6 +599,52 @@ typedef struct {
 trimul_status trimul_adamw_step(const trimul_adamw_params* p, const trimul_adamw_tensor* tensors, int n, int32_t* count,
                                 int device, void* stream, unsigned flags);
 
+/* ---------------------------------------------------------------- linear layer in 8 bits
+ * y = x W^T + bias over rows of K channels (a transition's projections), and its
+ * gradients, on the 8-bit tensor cores.  Every operand is rounded to e4m3 with a
+ * power of two for each block of 128 along what the product sums over:
+ *
+ *   Q(v) of a block: codes e4m3(v 2^-e) to nearest, times 2^e, for the least e >= -126 with max |v| <= 448 2^e
+ *   y     = bf16(Qrow(x) Qblk(W)^T + bias)       Qrow: 128 channels of a row     Qblk: 128 x 128 of W
+ *   dx    = bf16(Qrow(dy) Qblk(W))
+ *   dW    = Qcol(dy)^T Qcol(x)                   Qcol: 128 rows of a channel
+ *   dbias = the sum of dy over the rows          (not rounded to 8 bits)
+ *
+ * Sums are in 32 bits; those over rows are cut into parts of 4096 on the tensor
+ * cores, which are added in a fixed order.  A number that is not finite becomes NaN,
+ * in every output that it takes part in, and leaves its block's power to the others.  As the
+ * TRIMUL_FLAG_FP8 path, this is less accurate than 16 bits: some 3e-2 of an
+ * output's norm for operands of normal distribution.
+ *
+ * N and K are multiples of 8 in [8, 65536], 0 <= rows < 2^31 - 256.  The caller
+ * keeps the weight as codes (trimul_linear8_pack after each change of it) and gives
+ * the workspaces, both 256-byte aligned.
+ */
+
+/* Bytes that a packed weight takes (0 for sizes that are refused). */
+size_t trimul_linear8_packed_bytes(int N, int K);
+
+/* packed = Qblk(W), as the forward and the backward read it.  W: `type` (BF16 or F32) [N][K] as nn.Linear's, aligned to its
+ * element. */
+trimul_status trimul_linear8_pack(const void* W, trimul_dtype type, int N, int K, void* packed, size_t packed_bytes, int device,
+                                  void* stream, unsigned flags);
+
+size_t trimul_linear8_forward_workspace_bytes(int64_t rows, int N, int K);
+
+/* x: bf16 [rows][K]; y: bf16 [rows][N]; bias: f32 [N] or NULL.  TRIMUL_FLAG_CHECK and TRIMUL_FLAG_INJECT_STALL as for
+ * trimul_forward. */
+trimul_status trimul_linear8_forward(const void* packed, const float* bias, const uint16_t* x, int64_t rows, int N, int K,
+                                     uint16_t* y, void* workspace, size_t workspace_bytes, int device, void* stream,
+                                     unsigned flags);
+
+size_t trimul_linear8_backward_workspace_bytes(int64_t rows, int N, int K);
+
+/* The gradients for dy (bf16 [rows][N]): dx bf16 [rows][K], dW f32 [N][K], dbias f32 [N]; NULL: not wanted.  x and packed are the
+ * forward's.  No output may overlap an input or another output. */
+trimul_status trimul_linear8_backward(const void* packed, const uint16_t* x, const uint16_t* dy, int64_t rows, int N, int K,
+                                      uint16_t* dx, float* dW, float* dbias, void* workspace, size_t workspace_bytes, int device,
+                                      void* stream, unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif

@@ -77,3 +77,44 @@ def scales(x):
 
 def dequantized(codes, scale):
     return codes * np.repeat(scale, BLOCK)[: len(codes)]
+
+
+# ------------------------------------------------------------------ linear layer in 8 bits
+def quantized(v, axes):
+    """Q(v) for blocks along `axes` of an array, what is not finite as NaN."""
+    fine = np.isfinite(v)
+    a = np.where(fine, np.abs(v), 0.0).max(axis=axes, keepdims=True)
+    e = np.maximum(np.ceil(np.log2(np.maximum(a, 2.0**-200) / 448)), -126)  # (a quotient that is a power of two is exact)
+    return np.where(fine, e4m3(np.where(fine, v, 0.0) * 2.0**-e) * 2.0**e, np.nan)
+
+
+def _tiles(x, down, along):
+    R, C = x.shape
+    return np.pad(x, ((0, -R % down), (0, -C % along))).reshape(-(-R // down), down, -(-C // along), along)
+
+
+def by_rows(x):
+    return quantized(_tiles(x, 1, BLOCK), 3).reshape(x.shape[0], -1)[:, : x.shape[1]]
+
+
+def by_columns(x):
+    return quantized(_tiles(x, BLOCK, 1), 1).reshape(-1, x.shape[1])[: x.shape[0]]
+
+
+def by_blocks(w):
+    N, K = w.shape
+    return quantized(_tiles(w, BLOCK, BLOCK), (1, 3)).reshape(N + -N % BLOCK, -1)[:N, :K]
+
+
+def linear8(x, w, bias=None):
+    """y before its rounding, and the sums of the products' magnitudes."""
+    q, p = by_rows(x), by_blocks(w)
+    y = q @ p.T
+    return (y if bias is None else y + bias), np.abs(q) @ np.abs(p).T
+
+
+def linear8_backward(x, w, dy):
+    """dx (before its rounding), dW, dbias, each with its products' magnitudes."""
+    r, p = by_rows(dy), by_blocks(w)
+    c, d = by_columns(dy), by_columns(x)
+    return (r @ p, np.abs(r) @ np.abs(p)), (c.T @ d, np.abs(c).T @ np.abs(d)), (dy.sum(0), np.abs(dy).sum(0))

@@ -45,3 +45,40 @@ def test_adamw_is_torchs():
         opt.step()
         p, m, v, *_ = O.adamw(p, g, m, v, k, 1e-2, (0.8, 0.95), 1e-6, 0.1)
         assert np.allclose(t.detach().numpy(), p, rtol=1e-13, atol=1e-14)
+
+
+def test_quantized_by_another_statement():
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((70, 300)) * np.exp(rng.standard_normal((70, 300)))
+    q = O.by_rows(x)
+    for r in range(70):
+        for b in range(0, 300, 128):
+            v = x[r, b:b + 128]
+            e = -126
+            while np.abs(v).max() > 448 * 2.0**e:
+                e += 1
+            assert (q[r, b:b + 128] == O.e4m3(v * 2.0**-e) * 2.0**e).all()
+    assert (O.by_columns(x) == O.by_rows(x.T).T).all()
+    w = rng.standard_normal((130, 140))
+    p = O.by_blocks(w)
+    assert (O.by_blocks(w.T) == p.T).all() and np.abs(p - w).max() <= 2.0**-4 * np.abs(w).max()
+    assert (O.quantized(np.array([448.0, -3.0]), 0) == [448, -3]).all() and (O.quantized(np.array([449.0, 9.0]), 0) == [448, 9]).all()
+    assert (O.quantized(np.zeros(4), 0) == 0).all()
+    bad = O.quantized(np.array([np.inf, 1.0625, np.nan, 2.0]), 0)
+    assert np.isnan(bad[[0, 2]]).all() and (bad[[1, 3]] == O.quantized(np.array([1.0625, 2.0]), 0)).all()
+
+
+def test_linear8_gradients_are_the_products_derivatives():
+    """With operands that 8 bits hold, rounding changes nothing and dx, dW, dbias are those of x W^T + b."""
+    rng = np.random.default_rng(2)
+    x, w, dy = (rng.integers(-8, 9, s).astype(np.float64) for s in ((40, 24), (16, 24), (40, 16)))
+    b = np.ones(16)
+    (dx, _), (dw, _), (db, _) = O.linear8_backward(x, w, dy)
+    f = lambda x, w, b: float((O.linear8(x, w, b)[0] * dy).sum())  # noqa: E731
+    assert (O.linear8(x, w, b)[0] == x @ w.T + b).all()
+    for t, d in ((x, dx), (w, dw), (b, db)):
+        for i in range(0, t.size, 37):
+            u = t.copy()
+            u.flat[i] += 1 if u.flat[i] < 8 else -1
+            args = [u if s is t else s for s in (x, w, b)]
+            assert f(*args) - f(x, w, b) == (u.flat[i] - t.flat[i]) * d.flat[i]

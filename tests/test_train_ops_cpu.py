@@ -80,3 +80,77 @@ def test_binding_refusals():
         P.AdamW([torch.zeros(8)])
     with pytest.raises(ValueError, match="2 copies for 1 params"):
         P.AdamW([torch.zeros(8)], copies=[None, None])
+
+
+FWD = {"packed": A, "bias": None, "x": 2 * A, "rows": 64, "N": 128, "K": 128, "y": 3 * A, "ws": 4 * A, "bytes": A, "flags": 0}
+
+
+@pytest.mark.parametrize("call,want,text", [
+    ({"N": 12}, SHAPE, "N (12)"),
+    ({"K": 0}, SHAPE, "K (0)"),
+    ({"K": 65544}, SHAPE, "K (65544)"),
+    ({"rows": -1}, SHAPE, "rows (-1)"),
+    ({"rows": 1 << 31}, SHAPE, "rows (2147483648)"),
+    ({"packed": None}, INVALID, "packed is null"),
+    ({"packed": A + 16}, INVALID, "256-byte aligned"),
+    ({"bias": 5 * A + 4}, INVALID, "bias must be"),
+    ({"x": None}, INVALID, "x or y is null"),
+    ({"x": 2 * A + 2}, INVALID, "not 16-byte aligned"),
+    ({"y": 3 * A + 8}, INVALID, "not 16-byte aligned"),
+    ({"y": 2 * A}, INVALID, "y overlaps x"),
+    ({"y": A + 256}, INVALID, "y overlaps packed"),
+    ({"ws": 3 * A + 1024}, INVALID, "workspace overlaps y"),
+    ({"bias": 4 * A}, INVALID, "workspace overlaps bias"),
+    ({"bytes": 1000}, INVALID, "are needed"),
+    ({"ws": None}, INVALID, "are needed"),
+    ({"ws": 4 * A + 16}, INVALID, "256-byte aligned"),
+    ({"flags": 16}, INVALID, "flags 0x10"),
+])
+def test_linear8_forward_refused(lib, call, want, text):
+    a = {**FWD, **call}
+    refused(lib, lib.trimul_linear8_forward(a["packed"], a["bias"], a["x"], a["rows"], a["N"], a["K"], a["y"], a["ws"], a["bytes"], 0,
+                                            None, a["flags"]), want, text)
+
+
+BWD = {**FWD, "dy": 5 * A, "dx": 6 * A, "dw": 7 * A, "db": 8 * A, "bytes": 1 << 30, "ws": 16 * A}
+
+
+@pytest.mark.parametrize("call,want,text", [
+    ({"N": 4}, SHAPE, "N (4)"),
+    ({"dy": None}, INVALID, "x or dy is null"),
+    ({"dx": 6 * A + 8}, INVALID, "not 16-byte aligned"),
+    ({"dw": 7 * A + 4}, INVALID, "dW and dbias must be"),
+    ({"db": 8 * A + 4}, INVALID, "dW and dbias must be"),
+    ({"dx": 5 * A}, INVALID, "dx overlaps dy"),
+    ({"dw": 2 * A}, INVALID, "dW overlaps x"),
+    ({"db": 7 * A + 64}, INVALID, "dbias overlaps dW"),
+    ({"ws": 8 * A}, INVALID, "workspace overlaps dbias"),
+    ({"bytes": 1000}, INVALID, "are needed"),
+    ({"flags": 4}, INVALID, "flags 0x4"),
+])
+def test_linear8_backward_refused(lib, call, want, text):
+    a = {**BWD, **call}
+    refused(lib, lib.trimul_linear8_backward(a["packed"], a["x"], a["dy"], a["rows"], a["N"], a["K"], a["dx"], a["dw"], a["db"], a["ws"],
+                                             a["bytes"], 0, None, a["flags"]), want, text)
+
+
+@pytest.mark.parametrize("call,want,text", [
+    ({"type": 2}, INVALID, "type must be"),
+    ({"W": None}, INVALID, "W is null"),
+    ({"W": A + 2}, INVALID, "W is null or not aligned"),
+    ({"packed": 2 * A + 16}, INVALID, "256-byte aligned"),
+    ({"bytes": 100}, INVALID, "are needed"),
+    ({"packed": A + 256}, INVALID, "packed overlaps W"),
+    ({"N": 20}, SHAPE, "N (20)"),
+])
+def test_linear8_pack_refused(lib, call, want, text):
+    a = {"W": A, "type": 1, "N": 128, "K": 128, "packed": 2 * A, "bytes": A, **call}
+    refused(lib, lib.trimul_linear8_pack(a["W"], a["type"], a["N"], a["K"], a["packed"], a["bytes"], 0, None, 0), want, text)
+
+
+def test_linear8_sizes(lib):
+    assert lib.trimul_linear8_packed_bytes(12, 8) == 0
+    assert lib.trimul_linear8_forward_workspace_bytes(-1, 8, 8) == 0
+    assert lib.trimul_linear8_backward_workspace_bytes(8, 8, 7) == 0
+    # codes [N][K] in rows of whole 16 bytes and the scales' tiles, both ways
+    assert lib.trimul_linear8_packed_bytes(128, 24) == (128 * 32 + 512) + (24 * 128 + 512)
