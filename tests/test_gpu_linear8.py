@@ -203,7 +203,7 @@ def test_linear8_in_a_graph_and_on_streams(P):
         with torch.cuda.graph(graph):
             lin.pack(w)
             y, g = lin(x), lin.backward(x, dy)
-        passes.append((x, w, dy, graph, y, g))
+        passes.append((x, w, dy, graph, y, g, lin))  # (the layer's memory is the graph's)
     streams = [torch.cuda.Stream() for _ in range(2)]
     for k, (x, w, dy, *_) in enumerate(passes):
         fresh = inputs(rng_of(50 + k), rows, K, N)
@@ -215,7 +215,7 @@ def test_linear8_in_a_graph_and_on_streams(P):
             with torch.cuda.stream(s):
                 p[3].replay()
     torch.cuda.synchronize()
-    for x, w, dy, _, y, g in passes:
+    for x, w, dy, _, y, g, _ in passes:
         check_forward(y, x, w, None)
         check_backward(g, x, w, dy)
     x, w, dy = (torch.zeros_like(t) for t in passes[0][:3])
