@@ -45,218 +45,256 @@ __device__ __forceinline__ uint32_t finite16x2(uint32_t w) {
 // Infinity as NaN.
 __device__ __forceinline__ float no_infinity(float v) { return fmaf(v, 0.f, v); }
 
-// Eight numbers as codes.
-__device__ __forceinline__ uint2 codes8(const uint4& v, float inv, bool all_finite) {
-  float f[8];
-  unpack8(v, f);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = (all_finite ? f[e] : no_infinity(f[e])) * inv;
-  return make_uint2(codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7]));
+// Two numbers, a register of bf16, as codes: times `inv`, one for each.
+__device__ __forceinline__ uint32_t codes_of(uint32_t w, f2 inv, bool all_finite) {
+  f2 v = unpack_bf162(w);
+  if (!all_finite) v = fma2(v, both(0.f), v);  // infinity as NaN
+  const float2 f = split2(mul2(v, inv));
+  return codes2(f.x, f.y);
+}
+__device__ __forceinline__ uint2 codes_of(const uint4& v, const f2 (&inv)[4], bool all_finite) {
+  return make_uint2(codes_of(v.x, inv[0], all_finite) | codes_of(v.y, inv[1], all_finite) << 16,
+                    codes_of(v.z, inv[2], all_finite) | codes_of(v.w, inv[3], all_finite) << 16);
+}
+__device__ __forceinline__ uint2 codes_of(const uint4& v, float inv, bool all_finite) {
+  const f2 i = both(inv);
+  const f2 four[4] = {i, i, i, i};
+  return codes_of(v, four, all_finite);
 }
 
-// The largest magnitude, bf16 bits, of the eight numbers of each of 16 lanes, of all of these; where one is not
-// finite, `all_finite` is false and the largest is of the others.
-__device__ __forceinline__ uint32_t largest_of_16(const uint4& v, bool& all_finite) {
-  auto over_lanes = [](uint32_t m) {
-    m = max(m & 0xffffu, m >> 16);
+__device__ __forceinline__ uint32_t max_of(const uint4& v) { return max16x2(max16x2(v.x, v.y), max16x2(v.z, v.w)); }
+__device__ __forceinline__ uint4 magnitudes(const uint4& v) {
+  return make_uint4(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
+}
+__device__ __forceinline__ uint4 finite(const uint4& v) {
+  return make_uint4(finite16x2(v.x), finite16x2(v.y), finite16x2(v.z), finite16x2(v.w));
+}
+
+// The larger half of what kLanes neighbouring lanes have.
+template <int kLanes>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t m) {
+  m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
-  };
-  const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
-  uint32_t m = over_lanes(max16x2(max16x2(w[0], w[1]), max16x2(w[2], w[3])));
-  all_finite = m < 0x7f80u;
-  if (__any_sync(0xffffffffu, !all_finite))  // rare
-    m = over_lanes(max16x2(max16x2(finite16x2(w[0]), finite16x2(w[1])), max16x2(finite16x2(w[2]), finite16x2(w[3]))));
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
 // ------------------------------------------------------------------ rows
-// Sixteen lanes have a block of 128 in one 16-byte load each; their turns run along the rows.
-constexpr int kTurns = 4;  // loads of a thread that are on their way together
-__global__ void __launch_bounds__(kThreads) k11_rows(const uint16_t* __restrict__ x, Operand8 o, long long items, uint32_t per_row,
-                                                      uint8_t* __restrict__ out, int* status) {
+// Eight lanes have a block of 128: two 16-byte loads each, 64 columns apart.  A
+// thread block has whole rows, so that the place of a block among them is a
+// 32-bit division.
+constexpr int kGroup = 8;                       // lanes of a block of 128
+constexpr int kPerTurn = kThreads / kGroup;
+constexpr int kTurns = 2;                       // blocks of a thread that are on their way together
+__global__ void __launch_bounds__(kThreads, 6)
+    k11_rows(const uint16_t* __restrict__ x, long long rows, int depth, uint32_t ld, uint32_t groups, FastDiv per_row,
+             uint8_t* __restrict__ out, uint8_t* __restrict__ scales, int* status) {
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
-  uint8_t* const scales = out + o.scales_at();
-  const int lane = threadIdx.x % 16;
-  const long long step = static_cast<long long>(gridDim.x) * (kThreads / 16);
-  const long long first = static_cast<long long>(blockIdx.x) * (kThreads / 16) + threadIdx.x / 16;
-  // (a warp's two halves go through the turns together: the shuffles need all lanes)
-  const long long turns = (items + step * kTurns - 1) / (step * kTurns);
-  for (long long t = 0; t < turns; ++t) {
-    uint4 v[kTurns];
+  const long long r0 = rows * blockIdx.x / gridDim.x, r1 = rows * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t items = static_cast<uint32_t>(r1 - r0) * per_row.d;
+  const uint16_t* const from = x + r0 * depth;
+  uint8_t* const to = out + r0 * ld;
+  const int lane = threadIdx.x % kGroup;
+  for (uint32_t at = 0; at < items; at += kPerTurn * kTurns) {  // (all lanes of a warp: the shuffles need them)
+    uint4 v[kTurns][2];
+    uint32_t row[kTurns], block[kTurns];
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
-      const long long item = first + (t * kTurns + u) * step;
-      v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (item < items) {
-        const long long row = item / per_row, col = (item - row * per_row) * L8_BLOCK + lane * 8;
-        if (col < o.depth) v[u] = __ldcs(reinterpret_cast<const uint4*>(x + row * o.depth + col));
+      const uint32_t item = at + u * kPerTurn + threadIdx.x / kGroup;
+      per_row.divmod(item, row[u], block[u]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t col = block[u] * L8_BLOCK + h * 64 + lane * 8;
+        v[u][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (item < items && col < depth) v[u][h] = __ldcs(reinterpret_cast<const uint4*>(from + static_cast<size_t>(row[u]) * depth + col));
       }
     }
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
-      const long long item = first + (t * kTurns + u) * step;
-      bool fine;
-      const uint32_t byte = scale_byte(largest_of_16(v[u], fine) << 16);
-      if (item >= items) continue;
-      const long long row = item / per_row, block = item - row * per_row, col = block * L8_BLOCK + lane * 8;
-      if (col < o.depth) *reinterpret_cast<uint2*>(out + row * o.ld() + col) = codes8(v[u], over_scale(byte), fine);
-      if (lane == 0) scales[o.scale_at(row, block)] = static_cast<uint8_t>(byte);
+      uint32_t top = over_lanes<kGroup>(max16x2(max_of(magnitudes(v[u][0])), max_of(magnitudes(v[u][1]))));
+      const bool fine = top < 0x7f80u;
+      if (__any_sync(0xffffffffu, !fine))  // rare
+        top = over_lanes<kGroup>(max16x2(max_of(finite(v[u][0])), max_of(finite(v[u][1]))));
+      const uint32_t byte = scale_byte(top << 16);
+      if (at + u * kPerTurn + threadIdx.x / kGroup >= items) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t col = block[u] * L8_BLOCK + h * 64 + lane * 8;
+        if (col < depth) *reinterpret_cast<uint2*>(to + static_cast<size_t>(row[u]) * ld + col) = codes_of(v[u][h], over_scale(byte), fine);
+      }
+      if (lane == 0) scales[l8_scale_at(r0 + row[u], block[u], groups)] = static_cast<uint8_t>(byte);
     }
   }
 }
 
 // ------------------------------------------------------------------ columns
-// A block takes 128 x 128 tiles below one another.  Rows come in as above (and
-// leave as row-wise codes); the tile waits in shared memory, rows 272 bytes
-// apart so that a warp's 32 words of one row, and its eight 16-byte stores, lie
-// in different banks.  A thread then has two columns of 32 rows: 32 codes a
-// column are a whole sector of the transposed output.
+// A thread block takes 128 x 128 tiles below one another.  Sixteen lanes have a
+// row's 128 columns, eight each, and sixteen groups of lanes have eight rows
+// each: a thread keeps its 8 x 8 numbers in registers, the columns' largest
+// magnitudes are taken over its rows, over the warp's two groups and, through
+// shared memory, over the warps; then the codes leave the way the numbers came.
 constexpr int kSide = 128;
-constexpr int kRowBytes = kSide * 2 + 16;
+constexpr int kWarps = kThreads / 32;
 
 template <bool kRows, bool kSums>
-__global__ void __launch_bounds__(kThreads)
-    k11_columns(const uint16_t* __restrict__ x, long long rows, int cols, uint8_t* __restrict__ out,
-                uint8_t* __restrict__ by_rows, float* __restrict__ part, int parts, int* status) {
+__global__ void __launch_bounds__(kThreads, kSums ? 2 : 3)
+    k11_columns(const uint16_t* __restrict__ x, long long rows, int cols, uint32_t ld, uint32_t groups, uint8_t* __restrict__ out,
+                uint8_t* __restrict__ scales, uint32_t row_groups, uint8_t* __restrict__ by_rows, uint8_t* __restrict__ row_scales,
+                float* __restrict__ part, int parts, int* status) {
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && status) *status = 0;
-  __shared__ alignas(16) uint8_t tile[kSide * kRowBytes];
-  __shared__ uint32_t tops[4][kSide / 2];
-  const Operand8 oc{cols, rows}, orow{rows, cols};
-  uint8_t* const scales = out + oc.scales_at();
-  uint8_t* const row_scales = kRows ? by_rows + orow.scales_at() : nullptr;
-  const int c0 = blockIdx.x * kSide, lane16 = threadIdx.x % 16;
-  const int word = threadIdx.x % 64, quarter = threadIdx.x / 64;  // columns 2 word and 2 word + 1, rows 32 quarter ..
+  __shared__ uint4 tops[2][kWarps][16];
+  __shared__ float sums[kSums ? kWarps : 1][kSums ? kSide : 1];
+  const int lane16 = threadIdx.x % 16, warp = threadIdx.x / 32, group = threadIdx.x / 16;
+  const int col = blockIdx.x * kSide + lane16 * 8;
+  const bool inside = col < cols;  // of a multiple of eight: all eight or none
   const long long tiles = l8_blocks(rows);
-  float sum[2] = {0.f, 0.f};
-  for (long long rt = blockIdx.y; rt < tiles; rt += parts) {
-    const long long r0 = rt * kSide;
-    const int col = c0 + lane16 * 8;
+  f2 sum[4] = {};
+  int turn = 0;
+  for (long long rt = blockIdx.y; rt < tiles; rt += parts, turn ^= 1) {
+    const long long r0 = rt * kSide + group;  // rows 16 apart
+    uint4 v[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = (h * 4 + u) * 16 + threadIdx.x / 16;
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r0 + r < rows && col < cols) v[u] = __ldcs(reinterpret_cast<const uint4*>(x + (r0 + r) * cols + col));
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = (h * 4 + u) * 16 + threadIdx.x / 16;
-        *reinterpret_cast<uint4*>(tile + r * kRowBytes + lane16 * 16) = v[u];
-        if (kRows) {
-          bool fine;
-          const uint32_t byte = scale_byte(largest_of_16(v[u], fine) << 16);
-          if (r0 + r < rows) {
-            if (col < cols) *reinterpret_cast<uint2*>(by_rows + (r0 + r) * orow.ld() + col) = codes8(v[u], over_scale(byte), fine);
-            if (lane16 == 0) row_scales[orow.scale_at(r0 + r, blockIdx.x)] = static_cast<uint8_t>(byte);
-          }
-        }
-      }
+    for (int u = 0; u < 8; ++u) {
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (inside && r0 + u * 16 < rows) v[u] = __ldcs(reinterpret_cast<const uint4*>(x + (r0 + u * 16) * cols + col));
     }
-    __syncthreads();
-    uint32_t w[32];
-    uint32_t top = 0;
+    uint4 top = make_uint4(0u, 0u, 0u, 0u);
+    auto join = [](uint4& a, const uint4& b) {
+      a.x = max16x2(a.x, b.x), a.y = max16x2(a.y, b.y), a.z = max16x2(a.z, b.z), a.w = max16x2(a.w, b.w);
+    };
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      w[r] = *reinterpret_cast<const uint32_t*>(tile + (quarter * 32 + r) * kRowBytes + word * 4);
-      top = max16x2(top, w[r] & 0x7fff7fffu);
-    }
-    const bool fine = (top & 0xffffu) < 0x7f80u && top < 0x7f800000u;
+    for (int u = 0; u < 8; ++u) join(top, magnitudes(v[u]));
+    const uint32_t all = max_of(top);
+    const bool fine = (all & 0xffffu) < 0x7f80u && all < 0x7f800000u;
     if (!fine) {  // rare
-      top = 0;
+      top = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int r = 0; r < 32; ++r) top = max16x2(top, finite16x2(w[r]));
+      for (int u = 0; u < 8; ++u) join(top, finite(v[u]));
     }
+    join(top, make_uint4(__shfl_xor_sync(0xffffffffu, top.x, 16), __shfl_xor_sync(0xffffffffu, top.y, 16),
+                         __shfl_xor_sync(0xffffffffu, top.z, 16), __shfl_xor_sync(0xffffffffu, top.w, 16)));
+    if (threadIdx.x % 32 < 16) tops[turn][warp][lane16] = top;
     if (kSums) {
 #pragma unroll
-      for (int r = 0; r < 32; ++r) sum[0] += bf16_lo(w[r]), sum[1] += bf16_hi(w[r]);
+      for (int u = 0; u < 8; ++u) {
+        sum[0] = add2(sum[0], unpack_bf162(v[u].x)), sum[1] = add2(sum[1], unpack_bf162(v[u].y));
+        sum[2] = add2(sum[2], unpack_bf162(v[u].z)), sum[3] = add2(sum[3], unpack_bf162(v[u].w));
+      }
     }
-    tops[quarter][word] = top;
-    __syncthreads();
-    top = max16x2(max16x2(tops[0][word], tops[1][word]), max16x2(tops[2][word], tops[3][word]));
-    const uint32_t byte[2] = {scale_byte(top << 16), scale_byte(top & 0xffff0000u)};
-    const long long rq = r0 + quarter * 32;
+    if (kRows) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = c0 + 2 * word + e;
-      if (c >= cols) continue;
-      const float inv = over_scale(byte[e]);
-      uint32_t q[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[i] = e ? bf16_hi(w[4 * k + i]) : bf16_lo(w[4 * k + i]);
-          f[i] = (fine ? f[i] : no_infinity(f[i])) * inv;
+      for (int u = 0; u < 8; ++u) {
+        uint32_t most = over_lanes<16>(max_of(magnitudes(v[u])));
+        const bool row_fine = most < 0x7f80u;
+        if (__any_sync(0xffffffffu, !row_fine)) most = over_lanes<16>(max_of(finite(v[u])));  // rare
+        const uint32_t byte = scale_byte(most << 16);
+        const long long r = r0 + u * 16;
+        if (r < rows) {
+          if (inside) *reinterpret_cast<uint2*>(by_rows + r * ld + col) = codes_of(v[u], over_scale(byte), row_fine);
+          if (lane16 == 0) row_scales[l8_scale_at(r, blockIdx.x, row_groups)] = static_cast<uint8_t>(byte);
         }
-        q[k] = codes4(f[0], f[1], f[2], f[3]);
       }
-      uint8_t* const to = out + c * oc.ld() + rq;
-      if (rq + 32 <= oc.ld()) {  // (zeros behind the last row)
-        reinterpret_cast<uint4*>(to)[0] = make_uint4(q[0], q[1], q[2], q[3]);
-        reinterpret_cast<uint4*>(to)[1] = make_uint4(q[4], q[5], q[6], q[7]);
-      } else if (rq + 16 <= oc.ld()) {
-        reinterpret_cast<uint4*>(to)[0] = make_uint4(q[0], q[1], q[2], q[3]);
-      }
-      if (quarter == 0) scales[oc.scale_at(c, rt)] = static_cast<uint8_t>(byte[e]);
     }
-    // the next tile's rows come where this one's have been read (before the second meeting), its largest ones after its own first meeting
+    __syncthreads();  // (the other half of `tops` is written next: one meeting a tile is enough)
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) join(top, tops[turn][q][lane16]);
+    const uint32_t word[4] = {top.x, top.y, top.z, top.w};
+    f2 inv[4];
+    uint32_t byte[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      byte[2 * e] = scale_byte(word[e] << 16), byte[2 * e + 1] = scale_byte(word[e] & 0xffff0000u);
+      inv[e] = pair2(over_scale(byte[2 * e]), over_scale(byte[2 * e + 1]));
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (inside && r0 + u * 16 < rows) *reinterpret_cast<uint2*>(out + (r0 + u * 16) * ld + col) = codes_of(v[u], inv, fine);
+    if (group < 8 && inside) {  // group g stores column g's byte of the lane's eight
+      uint32_t mine = byte[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) mine = group == e ? byte[e] : mine;
+      scales[l8_scale_at(col + group, rt, groups)] = static_cast<uint8_t>(mine);
+    }
   }
-  if (kSums) {
+  if (kSums) {  // in a fixed order: a thread's rows, the warp's two groups, the warps, then the blocks (k11_join)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = split2(sum[e]);
+      const float lo = f.x + __shfl_xor_sync(0xffffffffu, f.x, 16), hi = f.y + __shfl_xor_sync(0xffffffffu, f.y, 16);
+      if (threadIdx.x % 32 < 16) sums[warp][lane16 * 8 + 2 * e] = lo, sums[warp][lane16 * 8 + 2 * e + 1] = hi;
+    }
     __syncthreads();
-    float2* const s = reinterpret_cast<float2*>(tile);
-    s[quarter * 64 + word] = make_float2(sum[0], sum[1]);
-    __syncthreads();
-    if (quarter == 0 && c0 + 2 * word < cols) {
-      const float2 a = s[word], b = s[64 + word], c = s[128 + word], d = s[192 + word];
-      *reinterpret_cast<float2*>(part + static_cast<size_t>(blockIdx.y) * cols + c0 + 2 * word) =
-          make_float2((a.x + b.x) + (c.x + d.x), (a.y + b.y) + (c.y + d.y));
+    if (threadIdx.x < kSide && blockIdx.x * kSide + threadIdx.x < cols) {
+      float t = 0.f;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) t += sums[q][threadIdx.x];
+      part[static_cast<size_t>(blockIdx.y) * cols + blockIdx.x * kSide + threadIdx.x] = t;
     }
   }
 }
 
 // ------------------------------------------------------------------ weights
-// One 128 x 128 block of W a thread block, as the operands [N][K] and [K][N].
+// One 128 x 128 block of W a thread block, 8 x 8 numbers a thread as above.
+__device__ __forceinline__ void load8(const float* p, bool wide, float (&f)[8]) {
+  if (wide) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = p[e];
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, bool wide, float (&f)[8]) {
+  if (wide) {
+    unpack8(*reinterpret_cast<const uint4*>(p), f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __bfloat162float(p[e]);
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k11_weight(const T* __restrict__ w, int N, int K, uint8_t* __restrict__ out, uint8_t* __restrict__ out_t) {
-  __shared__ uint8_t tile[kSide][kSide + 4];
-  __shared__ uint32_t tops[kThreads / 32];
-  const Operand8 o{N, K}, ot{K, N};
-  const int n0 = blockIdx.y * kSide, k0 = blockIdx.x * kSide;
-  const int k = k0 + threadIdx.x % 128, half = threadIdx.x / 128;
-  float v[64];
+__global__ void __launch_bounds__(kThreads) k11_weight(const T* __restrict__ w, int N, int K, uint32_t ld, uint32_t groups, uint32_t groups_mn,
+                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                        uint8_t* __restrict__ scales_mn) {
+  __shared__ uint32_t tops[kWarps];
+  const int lane16 = threadIdx.x % 16, group = threadIdx.x / 16;
+  const int k = blockIdx.x * kSide + lane16 * 8, n0 = blockIdx.y * kSide + group;
+  const bool wide = reinterpret_cast<uintptr_t>(w) % 16 == 0;
+  float v[8][8];
   uint32_t top = 0;
 #pragma unroll
-  for (int r = 0; r < 64; ++r) {
-    const int n = n0 + half * 64 + r;
-    v[r] = n < N && k < K ? to_f32(w[static_cast<size_t>(n) * K + k]) : 0.f;
-    const uint32_t bits = __float_as_uint(v[r]) & 0x7fffffffu;
-    if (bits < 0x7f800000u) top = max(top, bits);
-    v[r] = no_infinity(v[r]);
+  for (int u = 0; u < 8; ++u) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+    if (n0 + u * 16 < N && k < K) load8(w + static_cast<size_t>(n0 + u * 16) * K + k, wide, v[u]);
   }
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t bits = __float_as_uint(v[u][e]) & 0x7fffffffu;
+      top = max(top, bits < 0x7f800000u ? bits : 0u);
+    }
   top = __reduce_max_sync(0xffffffffu, top);
   if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
   __syncthreads();
-  for (int q = 0; q < kThreads / 32; ++q) top = max(top, tops[q]);
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) top = max(top, tops[q]);
   const uint32_t byte = scale_byte(top);
   const float inv = over_scale(byte);
 #pragma unroll
-  for (int r = 0; r < 64; ++r)
-    tile[half * 64 + r][threadIdx.x % 128] = static_cast<uint8_t>(__nv_cvt_float_to_fp8(v[r] * inv, __NV_SATFINITE, __NV_E4M3));
-  __syncthreads();
-  for (int i = threadIdx.x; i < kSide * kSide; i += kThreads) {
-    const int a = i / kSide, b = i % kSide;
-    if (n0 + a < N && k0 + b < K) out[static_cast<size_t>(n0 + a) * o.ld() + k0 + b] = tile[a][b];
-    if (k0 + a < K && n0 + b < N) out_t[static_cast<size_t>(k0 + a) * ot.ld() + n0 + b] = tile[b][a];
+  for (int u = 0; u < 8; ++u) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = no_infinity(v[u][e]) * inv;
+    if (n0 + u * 16 < N && k < K)
+      *reinterpret_cast<uint2*>(codes + static_cast<size_t>(n0 + u * 16) * ld + k) = make_uint2(codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7]));
   }
   if (threadIdx.x < kSide) {
-    const int n = n0 + threadIdx.x, kk = k0 + threadIdx.x;
-    if (n < N) out[o.scales_at() + o.scale_at(n, blockIdx.x)] = static_cast<uint8_t>(byte);
-    if (kk < K) out_t[ot.scales_at() + ot.scale_at(kk, blockIdx.y)] = static_cast<uint8_t>(byte);
+    const int n = blockIdx.y * kSide + threadIdx.x, kk = blockIdx.x * kSide + threadIdx.x;
+    if (n < N) scales[l8_scale_at(n, blockIdx.x, groups)] = static_cast<uint8_t>(byte);
+    if (kk < K) scales_mn[l8_scale_at(kk, blockIdx.y, groups_mn)] = static_cast<uint8_t>(byte);
   }
 }
 
@@ -272,36 +310,42 @@ __global__ void __launch_bounds__(kThreads) k11_join(const float* __restrict__ p
 }  // namespace
 
 cudaError_t launch_quantize_rows(const uint16_t* x, long long rows, int depth, uint8_t* out, int* status, int num_sms, cudaStream_t s) {
-  const Operand8 o{rows, depth};
+  const Operand8 o{rows, depth, false};
   const uint32_t per_row = static_cast<uint32_t>(l8_blocks(depth));
-  const long long items = rows * per_row, per_block = kThreads / 16 * kTurns;
-  const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>((items + per_block - 1) / per_block, 8ll * num_sms)));
-  k11_rows<<<grid, kThreads, 0, s>>>(x, o, items, per_row, out, status);
+  const long long turns = (rows * per_row + kPerTurn * kTurns - 1) / (kPerTurn * kTurns);
+  const int grid = static_cast<int>(std::min<long long>(rows, std::min<long long>(turns, 6ll * num_sms)));
+  k11_rows<<<grid, kThreads, 0, s>>>(x, rows, depth, static_cast<uint32_t>(o.ld()), static_cast<uint32_t>(o.groups()), FastDiv(per_row), out,
+                                     out + o.scales_at(), status);
   return cudaGetLastError();
 }
 
 int quantize_columns_parts(long long rows, int cols, int num_sms) {
   const long long across = l8_blocks(cols);
-  return static_cast<int>(std::max<long long>(1, std::min<long long>(l8_blocks(rows), 4ll * num_sms / across)));
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(l8_blocks(rows), 3ll * num_sms / across)));
 }
 
 cudaError_t launch_quantize_columns(const uint16_t* x, long long rows, int cols, uint8_t* out, uint8_t* by_rows,
                                     float* column_sums, float* part, int* status, int num_sms, cudaStream_t s) {
+  const Operand8 c{cols, rows, true}, r{rows, cols, false};
   const int parts = quantize_columns_parts(rows, cols, num_sms);
   const dim3 grid(static_cast<unsigned>(l8_blocks(cols)), parts);
   auto kernel = by_rows ? (column_sums ? k11_columns<true, true> : k11_columns<true, false>)
                         : (column_sums ? k11_columns<false, true> : k11_columns<false, false>);
-  kernel<<<grid, kThreads, 0, s>>>(x, rows, cols, out, by_rows, part, parts, status);
+  kernel<<<grid, kThreads, 0, s>>>(x, rows, cols, static_cast<uint32_t>(c.ld()), static_cast<uint32_t>(c.groups()), out, out + c.scales_at(),
+                                   static_cast<uint32_t>(r.groups()), by_rows, by_rows ? by_rows + r.scales_at() : nullptr, part, parts, status);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess && column_sums ? launch_join(part, parts, cols, column_sums, s) : e;
 }
 
-cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_t* out, uint8_t* out_t, cudaStream_t s) {
+cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_t* codes, uint8_t* scales, uint8_t* scales_mn,
+                                   cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(l8_blocks(K)), static_cast<unsigned>(l8_blocks(N)));
+  const Operand8 o{N, K, false}, t{K, N, true};
+  const uint32_t ld = static_cast<uint32_t>(o.ld()), g = static_cast<uint32_t>(o.groups()), gt = static_cast<uint32_t>(t.groups());
   if (f32)
-    k11_weight<<<grid, kThreads, 0, s>>>(static_cast<const float*>(w), N, K, out, out_t);
+    k11_weight<<<grid, kThreads, 0, s>>>(static_cast<const float*>(w), N, K, ld, g, gt, codes, scales, scales_mn);
   else
-    k11_weight<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(w), N, K, out, out_t);
+    k11_weight<<<grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(w), N, K, ld, g, gt, codes, scales, scales_mn);
   return cudaGetLastError();
 }
 

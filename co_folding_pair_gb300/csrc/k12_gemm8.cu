@@ -55,8 +55,8 @@ static_assert(ACC_STEP + L8_TILE <= SCALE_COLS && SCALE_COLS + SCALE_SETS * SCAL
 
 constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + BAR_BYTES;
 
-// Instruction descriptor of kind::mxf8f6f4: E4M3 A and B (format 0), K-major,
-// N >> 3 at bit 17, ue8m0 scales (bit 23), M >> 4 at bit 24; the byte of B's
+// Instruction descriptor of kind::mxf8f6f4: E4M3 A and B (format 0), the
+// operands' majors (bits 15 and 16: 1 for depth by depth), N >> 3 at bit 17, ue8m0 scales (bit 23), M >> 4 at bit 24; the byte of B's
 // and A's scale words at bits 4 and 29.
 constexpr uint32_t kIdesc = ((L8_TILE >> 3) << 17) | (1u << 23) | ((L8_TILE >> 4) << 24);
 
@@ -204,8 +204,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t fb = mapa_shared(full0 + 8 * stage, 0);
           const bool scales = b % 4 == 0 || b == w.b0;
           if (leader) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * (2 * CODE_BYTES + (scales ? 3 * L8_SCALE_TILE : 0)));
-          tma_load_2d_pair(sa, &maps.a, fb, b * L8_BLOCK, ra);
-          tma_load_2d_pair(sb, &maps.b, fb, b * L8_BLOCK, rb);
+          const int d = b * L8_BLOCK;
+          tma_load_2d_pair(sa, &maps.a, fb, p.a_mn ? ra : d, p.a_mn ? d : ra);
+          tma_load_2d_pair(sb, &maps.b, fb, p.b_mn ? rb : d, p.b_mn ? d : rb);
           if (scales) {
             const int g = b / 4, b1 = w.tn * 2 + 1;
             tma_load_2d_pair(sa + A_SCALES, &maps.a_scale, fb, 0, (at < a_tiles ? at : 0) * groups + g);
@@ -234,7 +235,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
     if (lane == 0 && leader) {
-      const uint64_t adesc0 = sdesc_sw128(base, 16, 1024), bdesc0 = sdesc_sw128(base + CODE_BYTES, 16, 1024);
+      // row by row: 128 rows of 128 bytes of depth, 32 bytes a step.  Depth by
+      // depth: 128 lines of 128 rows, eight lines 1024 bytes, 32 lines a step (a
+      // CTA's 128 rows are one line, so the offset between lines' parts is not used)
+      const uint64_t adesc0 = sdesc_sw128(base, p.a_mn ? CODE_BYTES : 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(base + CODE_BYTES, p.b_mn ? CODE_BYTES : 16, 1024);
+      const uint32_t astep = p.a_mn ? 32 * 128 >> 4 : 32 >> 4, bstep = p.b_mn ? 32 * 128 >> 4 : 32 >> 4;
+      const uint32_t majors = static_cast<uint32_t>(p.a_mn) << 15 | static_cast<uint32_t>(p.b_mn) << 16;
       const uint64_t as0 = sdesc_scales(base + A_SCALES), bs0 = sdesc_scales(base + B_SCALES);
       int stage = 0, acc = 0;
       uint32_t phase = 0, aphase = 0, ophase = 1, set = 0;
@@ -263,10 +270,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             copy_scales_pair(sf + 4, bs0 + soff);
             copy_scales_pair(sf + 8, bs0 + soff + (L8_SCALE_TILE >> 4));
           }
-          const uint32_t idesc = kIdesc | static_cast<uint32_t>(b % 4) << 4 | static_cast<uint32_t>(b % 4) << 29;
+          const uint32_t idesc = kIdesc | majors | static_cast<uint32_t>(b % 4) << 4 | static_cast<uint32_t>(b % 4) << 29;
 #pragma unroll
           for (int kk = 0; kk < L8_BLOCK / 32; ++kk)
-            mma_block_scaled_pair(d_tmem, adesc0 + soff + kk * (32 >> 4), bdesc0 + soff + kk * (32 >> 4), idesc, sf, sf + 4,
+            mma_block_scaled_pair(d_tmem, adesc0 + soff + kk * astep, bdesc0 + soff + kk * bstep, idesc, sf, sf + 4,
                                   (b != w.b0 || kk != 0) ? 1u : 0u);
           mma_commit_pair(empty0 + 8 * stage, 0x3);
           if (++stage == STAGES) {

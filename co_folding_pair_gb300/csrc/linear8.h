@@ -1,12 +1,15 @@
 // linear8.h -- operands in 8 bits with a power of two for each block of 128,
 // and launchers of the linear layer in 8 bits (internal).
 //
-// An operand of the product is a matrix [rows][depth] of e4m3 codes, `depth`
+// An operand of the product is a matrix of rows x depth e4m3 codes, `depth`
 // being what the product sums over, with one scale for each row and 128 of
-// depth.  A scale is a power of two, held as its biased exponent in a byte
-// (ue8m0).  The scales lie as the tensor cores take them: tiles of 512 bytes
-// for 128 rows and four blocks of depth, row r's byte of block b at
-// (r % 32) 16 + (r / 32) 4 + b in tile [row / 128][block / 4].
+// depth.  The codes lie row by row ([rows][depth]) or depth by depth
+// ([depth][rows], `mn`): the tensor cores take both, so that a tensor's codes
+// are written the way that the tensor itself lies.  A scale is a power of two,
+// held as its biased exponent in a byte (ue8m0).  The scales lie as the tensor
+// cores take them: tiles of 512 bytes for 128 rows and four blocks of depth, row
+// r's byte of block b at (r % 32) 16 + (r % 128) / 32 4 + b % 4 in tile
+// [r / 128][b / 4].
 #pragma once
 
 #include <cuda.h>
@@ -23,38 +26,39 @@ constexpr int L8_TILE = 256;         // rows and columns of a product's tile (a 
 
 __host__ __device__ constexpr long long l8_blocks(long long n) { return (n + L8_BLOCK - 1) / L8_BLOCK; }
 
-// Sizes of one operand in memory.
+// One operand in memory: codes, then scales, each from a multiple of 256 bytes on.
 struct Operand8 {
   long long rows, depth;
-  __host__ __device__ long long ld() const { return (depth + 15) / 16 * 16; }  // bytes from row to row
+  bool mn;
+  __host__ __device__ long long ld() const { return ((mn ? rows : depth) + 15) / 16 * 16; }  // bytes from line to line
   __host__ __device__ long long groups() const { return (l8_blocks(depth) + 3) / 4; }
-  __host__ __device__ size_t code_bytes() const { return static_cast<size_t>(rows) * ld(); }
-  __host__ __device__ size_t scale_bytes() const { return static_cast<size_t>(l8_blocks(rows)) * groups() * L8_SCALE_TILE; }
-  // codes, then scales, each from a multiple of 256 bytes on
+  __host__ __device__ size_t code_bytes() const { return static_cast<size_t>(mn ? depth : rows) * ld(); }
+  __host__ __device__ size_t scale_bytes() const { return (static_cast<size_t>(l8_blocks(rows)) * groups() * L8_SCALE_TILE + 255) / 256 * 256; }
   __host__ __device__ size_t scales_at() const { return (code_bytes() + 255) / 256 * 256; }
-  __host__ __device__ size_t bytes() const { return scales_at() + (scale_bytes() + 255) / 256 * 256; }
-#ifdef __CUDACC__
-  __device__ __forceinline__ size_t scale_at(long long row, long long block) const {
-    return (static_cast<size_t>(row / 128) * groups() + block / 4) * L8_SCALE_TILE + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
-  }
-#endif
+  __host__ __device__ size_t bytes() const { return scales_at() + scale_bytes(); }
 };
+// Where a row's byte of a block is among the scales, `groups` of them a row of tiles.
+__host__ __device__ __forceinline__ size_t l8_scale_at(long long row, long long block, long long groups) {
+  return (static_cast<size_t>(row / 128) * groups + block / 4) * L8_SCALE_TILE + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
+}
 
 // ---------------------------------------------------------------- rounding to 8 bits (k11_quantize8.cu)
 // Each clears the word `status` (or null) for the product behind it.
-// bf16 [rows][depth], a scale for each row and 128 columns.
+// bf16 [rows][depth], a scale for each row and 128 columns: the operand {rows, depth}.
 cudaError_t launch_quantize_rows(const uint16_t* x, long long rows, int depth, uint8_t* out, int* status, int num_sms, cudaStream_t s);
-// bf16 [rows][cols] as the operand [cols][rows], a scale for each column and 128 rows; with by_rows (or null) also as
+// bf16 [rows][cols], a scale for each column and 128 rows: the operand {cols, rows, mn}; with by_rows (or null) also as
 // launch_quantize_rows, and with column_sums (or null) the sums of the columns, f32 [cols], by way of `part`.
 int quantize_columns_parts(long long rows, int cols, int num_sms);
 cudaError_t launch_quantize_columns(const uint16_t* x, long long rows, int cols, uint8_t* out, uint8_t* by_rows,
                                     float* column_sums, float* part, int* status, int num_sms, cudaStream_t s);
-// A weight [N][K], a scale for each 128 x 128: as the operands [N][K] and [K][N].
-cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_t* out, uint8_t* out_t, cudaStream_t s);
+// A weight [N][K], a scale for each 128 x 128: codes [N][K], which are the operands {N, K} and {K, N, mn}, and the scales of both.
+cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_t* codes, uint8_t* scales, uint8_t* scales_mn,
+                                   cudaStream_t s);
 
 // ---------------------------------------------------------------- products (k12_gemm8.cu)
 struct Gemm8Args {
   int M, N;
+  int a_mn, b_mn;        // how the operands lie
   int blocks;            // of 128 depth in all
   int chunk;             // blocks that one accumulation takes
   int per_z, n_z;        // blocks of a slice of the depth, and the slices

@@ -41,20 +41,20 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Two-dimensional maps: codes (boxes of 128 rows x 128 bytes, zeros past the
-// operand's rows and depth) and scales (boxes of one tile).
-trimul_status operand_maps(CUtensorMap* codes, CUtensorMap* scales, const uint8_t* at, const Operand8& o) {
+// Two-dimensional maps: codes (boxes of 128 rows x 128 of depth, zeros past the
+// operand's) and scales (boxes of one tile).
+trimul_status operand_maps(CUtensorMap* codes, CUtensorMap* scales, const Operand8& o, const uint8_t* at, const uint8_t* scales_at) {
   EncodeTiled fn = encode_tiled();
   if (!fn) return fail(TRIMUL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint32_t one[2] = {1, 1};
-  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(o.depth), static_cast<cuuint64_t>(o.rows)}, stride[1] = {static_cast<cuuint64_t>(o.ld())};
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(o.mn ? o.rows : o.depth), static_cast<cuuint64_t>(o.mn ? o.depth : o.rows)}, stride[1] = {static_cast<cuuint64_t>(o.ld())};
   const cuuint32_t box[2] = {L8_BLOCK, 128};
   CUresult r = fn(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(at), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r == CUDA_SUCCESS) {
     const cuuint64_t sdim[2] = {L8_SCALE_TILE / 4, static_cast<cuuint64_t>(l8_blocks(o.rows) * o.groups())}, sstride[1] = {L8_SCALE_TILE};
     const cuuint32_t sbox[2] = {L8_SCALE_TILE / 4, 1};
-    r = fn(scales, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<uint8_t*>(at) + o.scales_at(), sdim, sstride, sbox, one,
+    r = fn(scales, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<uint8_t*>(scales_at), sdim, sstride, sbox, one,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
   if (r != CUDA_SUCCESS) return fail(TRIMUL_ERR_CUDA, "tensor map of an 8-bit operand rejected (CUresult %d)", static_cast<int>(r));
@@ -81,11 +81,20 @@ void slices(int M, int N, int blocks, int pairs, int* per_z, int* n_z) {
   *n_z = (blocks + *per_z - 1) / *per_z;
 }
 
-trimul_status run_gemm(const uint8_t* a, const Operand8& ao, const uint8_t* b, const Operand8& bo, void* c, bool f32,
-                       const float* bias, int per_z, int n_z, int* status, int pairs, cudaStream_t s, unsigned flags) {
+// An operand and where its codes and scales are.
+struct Placed8 {
+  Operand8 o;
+  const uint8_t *codes, *scales;
+  Placed8(const Operand8& op, const uint8_t* at) : o(op), codes(at), scales(at + op.scales_at()) {}
+  Placed8(const Operand8& op, const uint8_t* at, const uint8_t* scales_at) : o(op), codes(at), scales(scales_at) {}
+};
+
+trimul_status run_gemm(const Placed8& a, const Placed8& b, void* c, bool f32, const float* bias, int per_z, int n_z, int* status,
+                       int pairs, cudaStream_t s, unsigned flags) {
   Gemm8Args p{};
-  p.M = static_cast<int>(ao.rows), p.N = static_cast<int>(bo.rows);
-  p.blocks = static_cast<int>(l8_blocks(ao.depth));
+  p.M = static_cast<int>(a.o.rows), p.N = static_cast<int>(b.o.rows);
+  p.a_mn = a.o.mn, p.b_mn = b.o.mn;
+  p.blocks = static_cast<int>(l8_blocks(a.o.depth));
   p.per_z = per_z ? per_z : p.blocks;
   p.n_z = n_z;
   p.chunk = f32 ? kChunk : p.per_z;
@@ -94,8 +103,8 @@ trimul_status run_gemm(const uint8_t* a, const Operand8& ao, const uint8_t* b, c
   p.timeout_ns = flags & TRIMUL_FLAG_INJECT_STALL ? kStallTimeoutNs : kTimeoutNs;
   p.stall = flags & TRIMUL_FLAG_INJECT_STALL;
   Gemm8Maps m;
-  TRY(operand_maps(&m.a, &m.a_scale, a, ao));
-  TRY(operand_maps(&m.b, &m.b_scale, b, bo));
+  TRY(operand_maps(&m.a, &m.a_scale, a.o, a.codes, a.scales));
+  TRY(operand_maps(&m.b, &m.b_scale, b.o, b.codes, b.scales));
   TRY_CUDA(launch_gemm8(p, m, f32, pairs, s), "8-bit product launch");
   return TRIMUL_OK;
 }
@@ -121,18 +130,18 @@ trimul_status check_rows(int64_t rows) {
   return TRIMUL_OK;
 }
 
-// Offsets in a packed weight: the operand [N][K], then [K][N].
+// A packed weight: codes [N][K], the scales of the operand {N, K}, then those of {K, N}.
 struct Packed {
   Operand8 w, wt;
-  size_t wt_at, bytes;
-  Packed(int N, int K) : w{N, K}, wt{K, N}, wt_at(w.bytes()), bytes(wt_at + wt.bytes()) {}
+  size_t wt_scales_at, bytes;
+  Packed(int N, int K) : w{N, K, false}, wt{K, N, true}, wt_scales_at(w.bytes()), bytes(wt_scales_at + wt.scale_bytes()) {}
 };
 
 // Offsets in a backward's workspace.
 struct Backward8 {
   Operand8 dy_rows, dy_cols, x_cols;
   size_t dy_rows_at, dy_cols_at, x_cols_at, slices_at, sums_at, bytes;
-  Backward8(int64_t rows, int N, int K) : dy_rows{rows, N}, dy_cols{N, rows}, x_cols{K, rows} {
+  Backward8(int64_t rows, int N, int K) : dy_rows{rows, N, false}, dy_cols{N, rows, true}, x_cols{K, rows, true} {
     int per_z, n_z;
     slices(N, K, static_cast<int>(l8_blocks(rows)), kMostPairs, &per_z, &n_z);
     dy_rows_at = kStatusBytes;
@@ -168,12 +177,12 @@ trimul_status trimul_linear8_pack(const void* W, trimul_dtype type, int N, int K
   TRY(scope.enter(device));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* const to = static_cast<uint8_t*>(packed);
-  return finish(launch_quantize_weight(W, type == TRIMUL_F32, N, K, to, to + l.wt_at, s), s, flags, "weight quantisation launch");
+  return finish(launch_quantize_weight(W, type == TRIMUL_F32, N, K, to, to + l.w.scales_at(), to + l.wt_scales_at, s), s, flags, "weight quantisation launch");
 }
 
 size_t trimul_linear8_forward_workspace_bytes(int64_t rows, int N, int K) {
   if (check_widths(N, K) != TRIMUL_OK || check_rows(rows) != TRIMUL_OK) return 0;
-  return kStatusBytes + Operand8{rows, K}.bytes();
+  return kStatusBytes + Operand8{rows, K, false}.bytes();
 }
 
 trimul_status trimul_linear8_forward(const void* packed, const float* bias, const uint16_t* x, int64_t rows, int N, int K,
@@ -201,7 +210,7 @@ trimul_status trimul_linear8_forward(const void* packed, const float* bias, cons
   int* const status = static_cast<int*>(workspace);
   uint8_t* const codes = static_cast<uint8_t*>(workspace) + kStatusBytes;
   TRY_CUDA(launch_quantize_rows(x, rows, K, codes, status, sms, s), "quantisation launch");
-  TRY(run_gemm(codes, Operand8{rows, K}, static_cast<const uint8_t*>(packed), l.w, y, false, bias, 0, 1, status, pairs_of(device, sms), s, flags));
+  TRY(run_gemm(Placed8(Operand8{rows, K, false}, codes), Placed8(l.w, static_cast<const uint8_t*>(packed)), y, false, bias, 0, 1, status, pairs_of(device, sms), s, flags));
   return finish8(status, s, flags);
 }
 
@@ -250,13 +259,13 @@ trimul_status trimul_linear8_backward(const void* packed, const uint16_t* x, con
                                      reinterpret_cast<float*>(ws + b.sums_at), status, sms, s), "quantisation launch");
   else if (dx)
     TRY_CUDA(launch_quantize_rows(dy, rows, N, ws + b.dy_rows_at, status, sms, s), "quantisation launch");
-  if (dx) TRY(run_gemm(ws + b.dy_rows_at, b.dy_rows, pk + l.wt_at, l.wt, dx, false, nullptr, 0, 1, status, pairs, s, flags));
+  if (dx) TRY(run_gemm(Placed8(b.dy_rows, ws + b.dy_rows_at), Placed8(l.wt, pk, pk + l.wt_scales_at), dx, false, nullptr, 0, 1, status, pairs, s, flags));
   if (dW) {
     TRY_CUDA(launch_quantize_columns(x, rows, K, ws + b.x_cols_at, nullptr, nullptr, nullptr, nullptr, sms, s), "quantisation launch");
     int per_z, n_z;
     slices(N, K, static_cast<int>(l8_blocks(rows)), pairs, &per_z, &n_z);
     float* const part = n_z == 1 ? dW : reinterpret_cast<float*>(ws + b.slices_at);
-    TRY(run_gemm(ws + b.dy_cols_at, b.dy_cols, ws + b.x_cols_at, b.x_cols, part, true, nullptr, per_z, n_z, status, pairs, s, flags));
+    TRY(run_gemm(Placed8(b.dy_cols, ws + b.dy_cols_at), Placed8(b.x_cols, ws + b.x_cols_at), part, true, nullptr, per_z, n_z, status, pairs, s, flags));
     if (n_z > 1) TRY_CUDA(launch_join(part, n_z, static_cast<long long>(N) * K, dW, s), "join launch");
   }
   if (!dx && !dW && !dbias) return finish(cudaSuccess, s, flags, "linear8 backward");

@@ -152,5 +152,5 @@ def test_linear8_sizes(lib):
     assert lib.trimul_linear8_packed_bytes(12, 8) == 0
     assert lib.trimul_linear8_forward_workspace_bytes(-1, 8, 8) == 0
     assert lib.trimul_linear8_backward_workspace_bytes(8, 8, 7) == 0
-    # codes [N][K] in rows of whole 16 bytes and the scales' tiles, both ways
-    assert lib.trimul_linear8_packed_bytes(128, 24) == (128 * 32 + 512) + (24 * 128 + 512)
+    # codes [N][K] in rows of whole 16 bytes, and the tiles of scales for both of its uses
+    assert lib.trimul_linear8_packed_bytes(128, 24) == 128 * 32 + 512 + 512
