@@ -40,13 +40,19 @@ namespace trimul {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEach = 4;                   // neighbours of a thread
-constexpr int kChunk = kThreads * kEach;   // elements of a block's turn
-constexpr int kBlocksPerSm = 5, kMostBlocks = 1024;
+constexpr int kEach = 4;                             // neighbours of a thread
+constexpr int kParts = 2;                            // such fours of a thread that are on their way together
+constexpr int kStride = kThreads * kEach;            // elements from one to the next
+constexpr int kChunk = kStride * kParts;             // elements of a block's turn
+constexpr int blocks_per_sm(bool k8) { return k8 ? 3 : 4; }  // what the registers allow without spills
+constexpr int kMostBlocks = 1024;
 constexpr int kTableSmall = 64, kTableMax = 384;  // tensors of one launch
 static_assert(32 * kEach == TRIMUL_STATE_BLOCK, "a warp has one block of the 8-bit states");
 
 enum : uint8_t { PARAM_BF16 = 1, GRAD_SHIFT = 1, COPY_SHIFT = 3, WIDE = 32 };  // of Table::kind
+
+constexpr int kF32 = TRIMUL_F32 << GRAD_SHIFT | WIDE, kF32Copy = kF32 | 1 << COPY_SHIFT;  // fp32 with fp32 gradients, and a bf16 copy
+constexpr int kBf16 = PARAM_BF16 | TRIMUL_BF16 << GRAD_SHIFT | WIDE;
 
 // The tensors of a launch, in its parameters.
 template <int N>
@@ -96,34 +102,43 @@ __device__ __forceinline__ uint32_t hash(uint32_t x) {
 }
 
 // ------------------------------------------------------------------ four neighbours
-// Elements i .. i + 3 of a tensor of n; `wide`: in one access where they are all there.
-__device__ __forceinline__ void load4(const void* p, int type, long long i, long long n, bool wide, float (&f)[4]) {
-  if (wide && i + 4 <= n) {
-    if (type == TRIMUL_F32) {
-      const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
-    } else {
-      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-      if (type == TRIMUL_BF16) {
-        f[0] = bf16_lo(q.x), f[1] = bf16_hi(q.x), f[2] = bf16_lo(q.y), f[3] = bf16_hi(q.y);
-      } else {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&q.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&q.y));
-        f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
-      }
+// Elements i .. i + 3 of a tensor of n as they lie there, 16 bytes or 8; `wide`: in one access, all of them there.  Nothing
+// is made of them yet: the loads of all tensors are to be on their way together.
+__device__ __forceinline__ uint4 load4(const void* p, int type, long long i, long long n, bool wide) {
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  if (type == TRIMUL_F32) {
+    const uint32_t* const q = static_cast<const uint32_t*>(p) + i;
+    if (wide) return *reinterpret_cast<const uint4*>(q);
+    if (i < n) r.x = q[0];
+    if (i + 1 < n) r.y = q[1];
+    if (i + 2 < n) r.z = q[2];
+    if (i + 3 < n) r.w = q[3];
+  } else {
+    const uint16_t* const q = static_cast<const uint16_t*>(p) + i;
+    if (wide) {
+      const uint2 w = *reinterpret_cast<const uint2*>(q);
+      r.x = w.x, r.y = w.y;
+      return r;
     }
-    return;
+    if (i < n) r.x = q[0];
+    if (i + 1 < n) r.x |= static_cast<uint32_t>(q[1]) << 16;
+    if (i + 2 < n) r.y = q[2];
+    if (i + 3 < n) r.y |= static_cast<uint32_t>(q[3]) << 16;
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[e] = 0.f;
-    if (i + e < n)
-      f[e] = type == TRIMUL_F32    ? static_cast<const float*>(p)[i + e]
-             : type == TRIMUL_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i + e])
-                                   : __half2float(static_cast<const __half*>(p)[i + e]);
+  return r;
+}
+__device__ __forceinline__ void unpack4(const uint4& r, int type, float (&f)[4]) {
+  if (type == TRIMUL_F32) {
+    f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
+  } else if (type == TRIMUL_BF16) {
+    f[0] = bf16_lo(r.x), f[1] = bf16_hi(r.x), f[2] = bf16_lo(r.y), f[3] = bf16_hi(r.y);
+  } else {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
   }
 }
 __device__ __forceinline__ void store4(void* p, int type, long long i, long long n, bool wide, const float (&f)[4]) {
-  if (wide && i + 4 <= n) {
+  if (wide) {
     if (type == TRIMUL_F32)
       *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
     else
@@ -143,7 +158,50 @@ __device__ __forceinline__ void store4(void* p, int type, long long i, long long
       static_cast<__half*>(p)[i + e] = __float2half_rn(f[e]);
   }
 }
+// The same for codes, four bytes.
+__device__ __forceinline__ uint32_t load_codes(const void* p, long long i, long long n, bool whole) {
+  if (whole) return *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + i);
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) w |= static_cast<uint32_t>(static_cast<const uint8_t*>(p)[i + e]) << (8 * e);
+  return w;
+}
+__device__ __forceinline__ void store_codes(void* p, long long i, long long n, bool whole, uint32_t w) {
+  if (whole) {
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + i) = w;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) static_cast<uint8_t*>(p)[i + e] = static_cast<uint8_t>(w >> (8 * e));
+}
 
+// ------------------------------------------------------------------ roots and reciprocals
+__device__ __forceinline__ float root_approx(float x) {  // within 2 ulp
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {  // of a normal number, within 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The root of x in [2^-60, inf), rounded to nearest: Newton's step from an approximation, with the remainder x - r^2
+// exact in the fused product (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  Compared
+// with the correctly rounded root for every x.
+__device__ __forceinline__ float root(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  const float r = x * y;
+  return fmaf(fmaf(-r, r, x), 0.5f * y, r);
+}
+// 1 / x for x in [2^-100, 2^100], rounded to nearest: likewise.
+__device__ __forceinline__ float reciprocal_rn(float x) {
+  const float y = reciprocal(x);
+  return fmaf(fmaf(-x, y, 1.f), y, y);
+}
 // ------------------------------------------------------------------ 8-bit states
 __device__ __forceinline__ void unpack_codes(uint32_t w, float scale, float (&f)[4]) {
 #pragma unroll
@@ -159,52 +217,75 @@ __device__ __forceinline__ uint32_t pack_codes(const float (&f)[4]) {
   return lo | hi << 16;
 }
 
+__device__ __forceinline__ float least_of(const float (&f)[4]) { return fminf(fminf(fabsf(f[0]), fabsf(f[1])), fminf(fabsf(f[2]), fabsf(f[3]))); }
+
 // The largest magnitude of a warp's 128 numbers (a NaN's bits are above infinity's).
 __device__ __forceinline__ float warp_largest(const float (&f)[4]) {
-  unsigned top = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  auto larger = [](float a, float b) {  // NaN if one is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  };
+  const float top = larger(larger(fabsf(f[0]), fabsf(f[1])), larger(fabsf(f[2]), fabsf(f[3])));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
 // x / scale as a number that e4m3 has: one of the two neighbours, the upper one
-// with the probability of x's place between them (to 16 bits).  Below 2^-6,
-// where the codes are evenly spaced, they are as far apart as just above it, so
-// 2^-6 is added for the rounding.
-__device__ __forceinline__ float at_random(float x, uint32_t bits16) {
-  const float a = fabsf(x);
-  const float base = a < 0x1p-6f ? 0x1p-6f : 0.f;
-  const uint32_t t = (__float_as_uint(a + base) + (bits16 << 4)) & 0xfff00000u;
-  return copysignf(fminf(__uint_as_float(t) - base, 448.f), x);
+// with the probability of x's place between them (`bits`: 16, times 2^4).  From
+// 2^-6 on the sum's carry out of what is cut off decides (past 448 the
+// conversion saturates); below, where the codes are evenly spaced, they are as
+// far apart as just above, so 2^-6 is added for the rounding.
+__device__ __forceinline__ float at_random(float x, uint32_t bits) { return __uint_as_float((__float_as_uint(x) + bits) & 0xfff00000u); }
+__device__ __forceinline__ float at_random_low(float x, uint32_t bits) {
+  const float a = fabsf(x), base = a < 0x1p-6f ? 0x1p-6f : 0.f;
+  return copysignf(at_random(a + base, bits) - base, x);
 }
 
-// A warp's block as codes; returns its scale.  `least`: what is above zero keeps a code above zero.
-__device__ __forceinline__ float quantize(const float (&f)[4], const uint32_t (&bits)[4], int shift, bool stochastic,
-                                          bool least, uint32_t& codes) {
+// A warp's block as codes; returns its scale.  kRoot: of roots, none negative, the random bits from the hashes' upper halves, and
+// what is above zero keeps a code above zero.
+template <bool kRoot>
+__device__ __forceinline__ float quantize(const float (&f)[4], const uint32_t (&hashes)[4], bool stochastic, uint32_t& codes) {
   const float scale = __fmul_rn(fmaxf(warp_largest(f), 0x1p-90f), 1.f / 448.f);
-  const float inv = __frcp_rn(scale);
+  const float inv = scale < 0x1p100f ? reciprocal_rn(scale) : __frcp_rn(scale);
   float q[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    q[e] = __fmul_rn(f[e], inv);
-    if (stochastic) q[e] = at_random(q[e], bits[e] >> shift & 0xffffu);
-    if (least && f[e] > 0.f) q[e] = fmaxf(q[e], 0x1p-9f);
+  for (int e = 0; e < 4; ++e) q[e] = __fmul_rn(f[e], inv);
+  const bool low = __any_sync(0xffffffffu, !(least_of(q) >= 0x1p-6f));  // few blocks have such small numbers
+  if (stochastic) {
+    uint32_t bits[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bits[e] = kRoot ? hashes[e] >> 12 & 0xffff0u : hashes[e] << 4 & 0xffff0u;
+    if (!low) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = at_random(q[e], bits[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = at_random_low(q[e], bits[e]);
+    }
+  }
+  if (kRoot && low) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = f[e] > 0.f ? fmaxf(q[e], 0x1p-9f) : q[e];
   }
   codes = pack_codes(q);
   return scale;
 }
 
 // ------------------------------------------------------------------ the step
-__device__ __forceinline__ float root(float x) {  // within 2 ulp
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+__device__ __forceinline__ void roots(const float (&x)[4], float (&r)[4]) {
+  if (__all_sync(0xffffffffu, least_of(x) >= 0x1p-60f && x[0] + x[1] + (x[2] + x[3]) < INFINITY)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = root(x[e]);
+  } else {  // few blocks: the remainder would fall below fp32's range
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = __fsqrt_rn(x[e]);
+  }
 }
 
 // What all elements of a step have in common.
 struct Step {
   bool run;
-  float clip, lr, rate, over_c2;  // rate: lr / (1 - b1^t)
+  float clip, lr, rate, over_root_c2;  // rate: lr / (1 - b1^t)
   uint32_t key;
 };
 __device__ __forceinline__ Step step_of(const Hyper& h, int count) {
@@ -219,7 +300,7 @@ __device__ __forceinline__ Step step_of(const Hyper& h, int count) {
   s.lr = h.lr_device ? *h.lr_device : h.lr;
   // 1 - b^t without the cancellation of early steps
   s.rate = s.lr / -expm1f(t * h.log_b1);
-  s.over_c2 = 1.f / -expm1f(t * h.log_b2);
+  s.over_root_c2 = 1.f / sqrtf(-expm1f(t * h.log_b2));
   s.key = hash(static_cast<uint32_t>(count + 1) + hash(h.seed));
   return s;
 }
@@ -231,84 +312,85 @@ __device__ __forceinline__ Entry entry(const Table<N>& tab, int k, const Step& s
                hash(tab.index[k] + s.key), tab.kind[k]};
 }
 
-template <bool k8>
+// kKind: the tensor's kind, or -1 for one that is known only here.
+template <bool k8, int kKind>
 __device__ __forceinline__ void step_chunk(const Entry& t, uint32_t chunk, const Hyper& h, const Step& s) {
-  const long long i = static_cast<long long>(chunk - t.chunk) * kChunk + threadIdx.x * kEach;
-  const long long block = i / TRIMUL_STATE_BLOCK;  // the same for a warp
-  if (block * TRIMUL_STATE_BLOCK >= t.numel) return;
-  const bool wide = t.kind & WIDE, stochastic = h.stochastic;
-  const int ptype = t.kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32;
-  const int copy = t.kind >> COPY_SHIFT & 3;
-  float p[4], g[4], m[4], v[4];
-  if (k8) {
-    uint32_t mc = 0, vc = 0;
-    const bool whole = i + 4 <= t.numel;
-    if (whole) {
-      mc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i);
-      vc = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i);
+  const long long first = static_cast<long long>(chunk - t.chunk) * kChunk + threadIdx.x * kEach;
+  const bool stochastic = h.stochastic;
+  const int kind = kKind < 0 ? t.kind : kKind;
+  const int ptype = kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32;
+  const int copy = kind >> COPY_SHIFT & 3;
+  const int gtype = kind >> GRAD_SHIFT & 3;
+  uint4 pr[kParts], gr[kParts], mr[kParts], vr[kParts];  // as they lie in memory; 8-bit states: .x the codes, .y the scale
+#pragma unroll
+  for (int u = 0; u < kParts; ++u) {
+    const long long i = first + u * kStride;
+    const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
+    pr[u] = load4(t.param, ptype, i, t.numel, wide);
+    gr[u] = load4(t.grad, gtype, i, t.numel, wide);
+    if (k8) {
+      const long long block = i / TRIMUL_STATE_BLOCK;  // the same for a warp
+      const bool any = block * TRIMUL_STATE_BLOCK < t.numel;
+      mr[u].x = load_codes(t.m, i, t.numel, whole), vr[u].x = load_codes(t.v, i, t.numel, whole);
+      mr[u].y = any ? __float_as_uint(t.m_scale[block]) : 0u, vr[u].y = any ? __float_as_uint(t.v_scale[block]) : 0u;
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < t.numel) {
-          mc |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.m)[i + e]) << (8 * e);
-          vc |= static_cast<uint32_t>(static_cast<const uint8_t*>(t.v)[i + e]) << (8 * e);
-        }
+      mr[u] = load4(t.m, TRIMUL_F32, i, t.numel, whole), vr[u] = load4(t.v, TRIMUL_F32, i, t.numel, whole);
     }
-    const float ms = t.m_scale[block], vs = t.v_scale[block];
-    load4(t.param, ptype, i, t.numel, wide, p);
-    load4(t.grad, t.kind >> GRAD_SHIFT & 3, i, t.numel, wide, g);
-    unpack_codes(mc, ms, m);
-    unpack_codes(vc, vs, v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(v[e], v[e]);
-  } else {
-    load4(t.m, TRIMUL_F32, i, t.numel, true, m);
-    load4(t.v, TRIMUL_F32, i, t.numel, true, v);
-    load4(t.param, ptype, i, t.numel, wide, p);
-    load4(t.grad, t.kind >> GRAD_SHIFT & 3, i, t.numel, wide, g);
   }
   const float keep = 1.f - s.lr * t.decay;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float ge = __fmul_rn(g[e], s.clip);
-    m[e] = __fadd_rn(__fmul_rn(h.b1, m[e]), __fmul_rn(h.not_b1, ge));
-    v[e] = __fadd_rn(__fmul_rn(h.b2, v[e]), __fmul_rn(__fmul_rn(h.not_b2, ge), ge));
-    p[e] = p[e] * keep - s.rate * m[e] / (root(v[e] * s.over_c2) + h.eps);
-  }
-  uint32_t bits[4] = {0, 0, 0, 0};
-  if (stochastic && (k8 || ptype == TRIMUL_BF16)) {
-    const uint32_t key = hash(t.key + static_cast<uint32_t>(i >> 32));
+  for (int u = 0; u < kParts; ++u) {
+    const long long i = first + u * kStride;
+    const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
+    if (i / TRIMUL_STATE_BLOCK * TRIMUL_STATE_BLOCK >= t.numel) return;  // the same for a warp
+    float p[4], g[4], m[4], v[4], r[4];
+    unpack4(pr[u], ptype, p), unpack4(gr[u], gtype, g);
+    if (k8) {
+      unpack_codes(mr[u].x, __uint_as_float(mr[u].y), m), unpack_codes(vr[u].x, __uint_as_float(vr[u].y), v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bits[e] = hash(key ^ (static_cast<uint32_t>(i) + e));
-  }
-  if (copy) store4(t.copy, copy == 1 ? TRIMUL_BF16 : TRIMUL_F16, i, t.numel, wide, p);
-  if (ptype == TRIMUL_BF16 && stochastic) {
+      for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(v[e], v[e]);
+    } else {
+      unpack4(mr[u], TRIMUL_F32, m), unpack4(vr[u], TRIMUL_F32, v);
+    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (fabsf(p[e]) < INFINITY) p[e] = __uint_as_float((__float_as_uint(p[e]) + (hash(bits[e]) & 0xffffu)) & 0xffff0000u);
-  }
-  store4(t.param, ptype, i, t.numel, wide, p);
-  if (k8) {
-    uint32_t mc, vc;
-    const float ms = quantize(m, bits, 0, stochastic, false, mc);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __fsqrt_rn(v[e]);
-    const float vs = quantize(v, bits, 16, stochastic, true, vc);
-    if (i + 4 <= t.numel) {
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i) = mc;
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i) = vc;
+    for (int e = 0; e < 4; ++e) {
+      const float ge = __fmul_rn(g[e], s.clip);
+      m[e] = __fadd_rn(__fmul_rn(h.b1, m[e]), __fmul_rn(h.not_b1, ge));
+      v[e] = __fadd_rn(__fmul_rn(h.b2, v[e]), __fmul_rn(__fmul_rn(h.not_b2, ge), ge));
+    }
+    if (k8) {
+      roots(v, r);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < t.numel) {
-          static_cast<uint8_t*>(t.m)[i + e] = static_cast<uint8_t>(mc >> (8 * e));
-          static_cast<uint8_t*>(t.v)[i + e] = static_cast<uint8_t>(vc >> (8 * e));
-        }
+      for (int e = 0; e < 4; ++e) r[e] = root_approx(v[e]);
     }
-    if (threadIdx.x % 32 == 0) t.m_scale[block] = ms, t.v_scale[block] = vs;
-  } else {
-    store4(t.m, TRIMUL_F32, i, t.numel, true, m);
-    store4(t.v, TRIMUL_F32, i, t.numel, true, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = fmaf(-(s.rate * m[e]), reciprocal(fmaf(r[e], s.over_root_c2, h.eps)), p[e] * keep);
+    uint32_t hashes[4] = {0, 0, 0, 0};
+    if (stochastic && (k8 || ptype == TRIMUL_BF16)) {
+      const uint32_t key = hash(t.key + static_cast<uint32_t>(i >> 32)) ^ static_cast<uint32_t>(i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hashes[e] = hash(key ^ e);  // (i is a multiple of four)
+    }
+    if (copy) store4(t.copy, copy == 1 ? TRIMUL_BF16 : TRIMUL_F16, i, t.numel, wide, p);
+    if (ptype == TRIMUL_BF16 && stochastic) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (fabsf(p[e]) < INFINITY) p[e] = __uint_as_float((__float_as_uint(p[e]) + (hash(hashes[e]) & 0xffffu)) & 0xffff0000u);
+    }
+    store4(t.param, ptype, i, t.numel, wide, p);
+    if (k8) {
+      const long long block = i / TRIMUL_STATE_BLOCK;
+      uint32_t codes;
+      const float m_scale = quantize<false>(m, hashes, stochastic, codes);
+      store_codes(t.m, i, t.numel, whole, codes);
+      const float v_scale = quantize<true>(r, hashes, stochastic, codes);
+      store_codes(t.v, i, t.numel, whole, codes);
+      if (threadIdx.x % 32 == 0) t.m_scale[block] = m_scale, t.v_scale[block] = v_scale;
+    } else {
+      store4(t.m, TRIMUL_F32, i, t.numel, whole, m);
+      store4(t.v, TRIMUL_F32, i, t.numel, whole, v);
+    }
   }
 }
 
@@ -318,10 +400,13 @@ __host__ __device__ __forceinline__ uint32_t run_begin(uint32_t chunks, uint32_t
 
 // count: {steps taken, blocks of the last launch that are done}.  Every block
 // reads the steps before it says that it is done, and the last one of the last
-// launch counts the step.
+// launch counts the step.  The launches of a step begin early, each in what room the
+// one before leaves (their tensors are others), and wait for it before they end, so that what
+// comes behind the last one comes behind all.
 template <bool k8, int N>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(k8))
     k10_adamw(const __grid_constant__ Table<N> tab, const __grid_constant__ Hyper h, int* count, int last_launch) {
+  let_next_begin();
   const Step s = step_of(h, *static_cast<volatile int*>(count));
   if (s.run) {
     const uint32_t c0 = run_begin(tab.chunks, blockIdx.x, gridDim.x), c1 = run_begin(tab.chunks, blockIdx.x + 1, gridDim.x);
@@ -334,10 +419,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           t = entry(tab, ++k, s);
           end = tab.chunk[k + 1];
         }
-        step_chunk<k8>(t, chunk, h, s);
+        // what most programs have gets code without questions about types
+        if (t.kind == kF32Copy)
+          step_chunk<k8, kF32Copy>(t, chunk, h, s);
+        else if (t.kind == kF32)
+          step_chunk<k8, kF32>(t, chunk, h, s);
+        else if (t.kind == kBf16)
+          step_chunk<k8, kBf16>(t, chunk, h, s);
+        else
+          step_chunk<k8, -1>(t, chunk, h, s);
       }
     }
   }
+  after_previous();
   if (!last_launch) return;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -353,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 template <int N>
-int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int num_sms) {
+int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int blocks) {
   tab.n = 0;
   tab.chunks = 0;
   for (; k < n && tab.n < N; ++k) {
@@ -378,7 +472,7 @@ int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int num_sms
     tab.chunks += static_cast<uint32_t>((t[k].numel + kChunk - 1) / kChunk);
   }
   tab.chunk[tab.n] = tab.chunks;
-  const int most = std::min(kMostBlocks, kBlocksPerSm * num_sms);
+  const int most = std::min(kMostBlocks, blocks);
   const int grid = static_cast<int>(std::max<long long>(1, std::min<long long>(tab.chunks, most)));
   int at = 0;
   for (int block = 0; block <= grid; ++block) {
@@ -393,12 +487,17 @@ template <bool k8, int N>
 cudaError_t run(const Hyper& h, const trimul_adamw_tensor* t, int n, int32_t* count, int num_sms, cudaStream_t s) {
   Table<N> tab;
   int k = 0;
-  do {
-    const int grid = fill(tab, t, n, k, num_sms);
-    k10_adamw<k8, N><<<grid, kThreads, 0, s>>>(tab, h, count, k >= n);
-    const cudaError_t e = cudaGetLastError();
+  for (bool first = true; first || k < n; first = false) {
+    const int grid = fill(tab, t, n, k, blocks_per_sm(k8) * num_sms);
+    cudaError_t e = cudaSuccess;
+    if (first) {  // behind all that was before the call
+      k10_adamw<k8, N><<<grid, kThreads, 0, s>>>(tab, h, count, k >= n);
+      e = cudaGetLastError();
+    } else {
+      e = launch_early(k10_adamw<k8, N>, dim3(grid), kThreads, s, tab, h, count, k >= n);
+    }
     if (e != cudaSuccess) return e;
-  } while (k < n);
+  }
   return cudaSuccess;
 }
 

@@ -228,6 +228,20 @@ def test_adamw_8bit_states_at_their_ends(P):
     assert (v[:128] == 0).all() and (v[128:256] > 0).all() and (v[384:] == 448).all()
 
 
+@pytest.mark.parametrize("states", ["float32", "8bit"])
+def test_adamw_of_tiny_gradients(P, states):
+    """Squares below fp32's normal range, with an eps smaller than their roots: the step is still lr's size."""
+    g = torch.tensor([1e-18, -3e-19, 2e-17, 1e-15], device="cuda").repeat(64)
+    p = torch.zeros(256, device="cuda")
+    opt = P.AdamW([p], lr=1.0, weight_decay=0.0, states=states, betas=(0.9, 0.999), eps=1e-30, rounding="nearest")
+    opt.step([g])
+    g64 = f64(g)
+    v = (g64 * g64 * 1e-3).astype(np.float32).astype(np.float64)  # subnormal: in steps of 2^-149
+    want = -(0.1 * g64 / 0.1) / (np.sqrt(v / 1e-3) + 1e-30)
+    # a subnormal v is off by 2 steps of 2^-149, its root by half that share
+    within(p, want, (2.0**-149 / v + 64 * U) * np.abs(want), "p")
+
+
 def test_adamw_random_rounding_is_fair(P):
     """The mean over many elements is the value: a code's place is uniform, so its variance is at most step^2 / 4 and
     the mean of n is within 5 step / (2 sqrt n) (5 deviations), the bits' grid adding step 2^-16."""
