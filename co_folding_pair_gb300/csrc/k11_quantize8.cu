@@ -9,75 +9,16 @@
 // Bound by memory: bf16 is read once; the codes are half of it, and where both
 // forms of a gradient are wanted (rows for dx, columns for dW) one read makes
 // both.
-#include <cuda_fp8.h>
-
 #include <algorithm>
 
 #include "linear8.h"
-#include "pair_ops.cuh"
+#include "quantize8.cuh"
 
 namespace trimul {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-// The larger ones of two pairs of 16-bit numbers.
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
-// The scale's byte for a largest magnitude, its fp32 bits (finite): 0.875 2^(e + 9) is the last value that 2^e covers.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
-  const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u);
-  return static_cast<uint32_t>(e > 1 ? e : 1);
-}
-__device__ __forceinline__ float over_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-
-__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) { return codes2(a, b) | codes2(c, d) << 16; }
-
-// Magnitudes of two bf16 numbers, zero for those that are not finite.
-__device__ __forceinline__ uint32_t finite16x2(uint32_t w) {
-  const uint32_t a = w & 0x7fff7fffu;
-  return ((a & 0xffffu) >= 0x7f80u ? 0u : a & 0xffffu) | (a >= 0x7f800000u ? 0u : a & 0xffff0000u);
-}
-// Infinity as NaN.
-__device__ __forceinline__ float no_infinity(float v) { return fmaf(v, 0.f, v); }
-
-// Two numbers, a register of bf16, as codes: times `inv`, one for each.
-__device__ __forceinline__ uint32_t codes_of(uint32_t w, f2 inv, bool all_finite) {
-  f2 v = unpack_bf162(w);
-  if (!all_finite) v = fma2(v, both(0.f), v);  // infinity as NaN
-  const float2 f = split2(mul2(v, inv));
-  return codes2(f.x, f.y);
-}
-__device__ __forceinline__ uint2 codes_of(const uint4& v, const f2 (&inv)[4], bool all_finite) {
-  return make_uint2(codes_of(v.x, inv[0], all_finite) | codes_of(v.y, inv[1], all_finite) << 16,
-                    codes_of(v.z, inv[2], all_finite) | codes_of(v.w, inv[3], all_finite) << 16);
-}
-__device__ __forceinline__ uint2 codes_of(const uint4& v, float inv, bool all_finite) {
-  const f2 i = both(inv);
-  const f2 four[4] = {i, i, i, i};
-  return codes_of(v, four, all_finite);
-}
-
-__device__ __forceinline__ uint32_t max_of(const uint4& v) { return max16x2(max16x2(v.x, v.y), max16x2(v.z, v.w)); }
-__device__ __forceinline__ uint4 magnitudes(const uint4& v) {
-  return make_uint4(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
-}
-__device__ __forceinline__ uint4 finite(const uint4& v) {
-  return make_uint4(finite16x2(v.x), finite16x2(v.y), finite16x2(v.z), finite16x2(v.w));
-}
-
-// The larger half of what kLanes neighbouring lanes have.
-template <int kLanes>
-__device__ __forceinline__ uint32_t over_lanes(uint32_t m) {
-  m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
-}
 
 // ------------------------------------------------------------------ rows
 // Eight lanes have a block of 128: two 16-byte loads each, 64 columns apart.  A
@@ -111,7 +52,7 @@ __global__ void __launch_bounds__(kThreads, 6)
     }
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
-      uint32_t top = over_lanes<kGroup>(max16x2(max_of(magnitudes(v[u][0])), max_of(magnitudes(v[u][1]))));
+      uint32_t top = over_lanes<kGroup>(max_magnitude(v[u][0], v[u][1]));
       const bool fine = top < 0x7f80u;
       if (__any_sync(0xffffffffu, !fine))  // rare
         top = over_lanes<kGroup>(max16x2(max_of(finite(v[u][0])), max_of(finite(v[u][1]))));
@@ -158,12 +99,14 @@ __global__ void __launch_bounds__(kThreads, kSums ? 2 : 3)
       v[u] = make_uint4(0u, 0u, 0u, 0u);
       if (inside && r0 + u * 16 < rows) v[u] = __ldcs(reinterpret_cast<const uint4*>(x + (r0 + u * 16) * cols + col));
     }
-    uint4 top = make_uint4(0u, 0u, 0u, 0u);
+    uint4 top = v[0];
     auto join = [](uint4& a, const uint4& b) {
       a.x = max16x2(a.x, b.x), a.y = max16x2(a.y, b.y), a.z = max16x2(a.z, b.z), a.w = max16x2(a.w, b.w);
     };
 #pragma unroll
-    for (int u = 0; u < 8; ++u) join(top, magnitudes(v[u]));
+    for (int u = 1; u < 8; ++u)
+      top = make_uint4(max_signed(top.x, v[u].x), max_signed(top.y, v[u].y), max_signed(top.z, v[u].z), max_signed(top.w, v[u].w));
+    top = magnitudes(top);
     const uint32_t all = max_of(top);
     const bool fine = (all & 0xffffu) < 0x7f80u && all < 0x7f800000u;
     if (!fine) {  // rare
@@ -183,15 +126,24 @@ __global__ void __launch_bounds__(kThreads, kSums ? 2 : 3)
     }
     if (kRows) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        uint32_t most = over_lanes<16>(max_of(magnitudes(v[u])));
-        const bool row_fine = most < 0x7f80u;
-        if (__any_sync(0xffffffffu, !row_fine)) most = over_lanes<16>(max_of(finite(v[u])));  // rare
-        const uint32_t byte = scale_byte(most << 16);
-        const long long r = r0 + u * 16;
-        if (r < rows) {
-          if (inside) *reinterpret_cast<uint2*>(by_rows + r * ld + col) = codes_of(v[u], over_scale(byte), row_fine);
-          if (lane16 == 0) row_scales[l8_scale_at(r, blockIdx.x, row_groups)] = static_cast<uint8_t>(byte);
+      for (int u = 0; u < 8; u += 2) {  // two rows' largest in a register
+        auto over_rows = [&](uint32_t a, uint32_t b) {
+          uint32_t two = max16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) two = max16x2(two, __shfl_xor_sync(0xffffffffu, two, o));
+          return two;
+        };
+        uint32_t two = over_rows(max_signed(v[u]) & 0x7fff7fffu, max_signed(v[u + 1]) & 0x7fff7fffu);
+        const bool row_fine[2] = {(two & 0xffffu) < 0x7f80u, two < 0x7f800000u};
+        if (__any_sync(0xffffffffu, !(row_fine[0] && row_fine[1]))) two = over_rows(max_of(finite(v[u])), max_of(finite(v[u + 1])));  // rare
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t byte = scale_byte(h ? two & 0xffff0000u : two << 16);
+          const long long r = r0 + (u + h) * 16;
+          if (r < rows) {
+            if (inside) *reinterpret_cast<uint2*>(by_rows + r * ld + col) = codes_of(v[u + h], over_scale(byte), row_fine[h]);
+            if (lane16 == 0) row_scales[l8_scale_at(r, blockIdx.x, row_groups)] = static_cast<uint8_t>(byte);
+          }
         }
       }
     }
@@ -299,12 +251,12 @@ __global__ void __launch_bounds__(kThreads) k11_weight(const T* __restrict__ w, 
 }
 
 // ------------------------------------------------------------------ sums of slices
-__global__ void __launch_bounds__(kThreads) k11_join(const float* __restrict__ part, int n_z, long long n, float* __restrict__ out) {
+__global__ void __launch_bounds__(kThreads) k11_join(const float* __restrict__ part, int n_z, long long n, int cols, float* __restrict__ out) {
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= n) return;
   float s = 0.f;
   for (int z = 0; z < n_z; ++z) s += part[z * n + i];
-  out[i] = s;
+  out[cols ? i % cols * (n / cols) + i / cols : i] = s;
 }
 
 }  // namespace
@@ -334,7 +286,7 @@ cudaError_t launch_quantize_columns(const uint16_t* x, long long rows, int cols,
   kernel<<<grid, kThreads, 0, s>>>(x, rows, cols, static_cast<uint32_t>(c.ld()), static_cast<uint32_t>(c.groups()), out, out + c.scales_at(),
                                    static_cast<uint32_t>(r.groups()), by_rows, by_rows ? by_rows + r.scales_at() : nullptr, part, parts, status);
   cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess && column_sums ? launch_join(part, parts, cols, column_sums, s) : e;
+  return e == cudaSuccess && column_sums ? launch_join(part, parts, cols, 0, column_sums, s) : e;
 }
 
 cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_t* codes, uint8_t* scales, uint8_t* scales_mn,
@@ -349,8 +301,8 @@ cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_
   return cudaGetLastError();
 }
 
-cudaError_t launch_join(const float* part, int n_z, long long n, float* out, cudaStream_t s) {
-  k11_join<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(part, n_z, n, out);
+cudaError_t launch_join(const float* part, int n_z, long long n, int cols, float* out, cudaStream_t s) {
+  k11_join<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(part, n_z, n, cols, out);
   return cudaGetLastError();
 }
 

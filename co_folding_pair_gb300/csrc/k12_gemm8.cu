@@ -32,8 +32,7 @@
 // the accumulations in registers, because the tensor cores' own additions
 // truncate, which over thousands of them in a row drifts.  Slices of the depth
 // (n_z) give the pairs work where there are few tiles.
-#include "linear8.h"
-#include "sm103_ptx.cuh"
+#include "gemm8.cuh"
 
 namespace trimul {
 
@@ -55,85 +54,6 @@ static_assert(ACC_STEP + L8_TILE <= SCALE_COLS && SCALE_COLS + SCALE_SETS * SCAL
 
 constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + BAR_BYTES;
 
-// Instruction descriptor of kind::mxf8f6f4: E4M3 A and B (format 0), the
-// operands' majors (bits 15 and 16: 1 for depth by depth), N >> 3 at bit 17, ue8m0 scales (bit 23), M >> 4 at bit 24; the byte of B's
-// and A's scale words at bits 4 and 29.
-constexpr uint32_t kIdesc = ((L8_TILE >> 3) << 17) | (1u << 23) | ((L8_TILE >> 4) << 24);
-
-__device__ __forceinline__ void mma_block_scaled_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                      uint32_t a_scale, uint32_t b_scale, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
-      : "memory");
-}
-
-// 32 rows of 16 bytes from shared memory to four TMEM columns, in each quadrant of lanes, in both CTAs.
-__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sdesc) : "memory");
-}
-
-// Shared-memory descriptor without swizzle: groups of eight 16-byte rows, 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(128 >> 4) << 32 | 1ull << 46;
-}
-
-// 8 x 8 chunks of 16 bytes inside each group of 8 lanes: lane 8a + b holds
-// chunks of its row, and afterwards chunk b of rows 8a .. 8a + 7.
-__device__ __forceinline__ void transpose8(uint4 (&R)[8], uint32_t gb) {
-#pragma unroll
-  for (int k = 4; k >= 1; k >>= 1) {
-    const bool upper = (gb & k) != 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j & k) continue;
-      const uint4 lo = R[j], hi = R[j | k];
-      const uint4 send = upper ? lo : hi;
-      uint4 recv;
-      recv.x = __shfl_xor_sync(0xffffffffu, send.x, k);
-      recv.y = __shfl_xor_sync(0xffffffffu, send.y, k);
-      recv.z = __shfl_xor_sync(0xffffffffu, send.z, k);
-      recv.w = __shfl_xor_sync(0xffffffffu, send.w, k);
-      R[j] = upper ? recv : lo;
-      R[j | k] = upper ? hi : recv;
-    }
-  }
-}
-
-// One accumulation: blocks [b0, b1) of a tile.  A pair's tiles, each with its
-// accumulations, in turn; all warps walk them alike.
-struct Walk {
-  const Gemm8Args& p;
-  long long tile, step, total;
-  int z, tm, tn, b0, b1, z_end;
-  __device__ __forceinline__ Walk(const Gemm8Args& a, int first, int pairs)
-      : p(a), tile(first), step(pairs), total(static_cast<long long>(a.tiles_m) * a.tiles_n * a.n_z) {
-    if (more()) begin();
-  }
-  __device__ __forceinline__ bool more() const { return tile < total; }
-  __device__ __forceinline__ void begin() {
-    const long long per_z = static_cast<long long>(p.tiles_m) * p.tiles_n;
-    z = static_cast<int>(tile / per_z);
-    const int rem = static_cast<int>(tile - z * per_z);
-    tm = rem / p.tiles_n, tn = rem - tm * p.tiles_n;
-    b0 = z * p.per_z;
-    z_end = min(b0 + p.per_z, p.blocks);
-    b1 = min(b0 + p.chunk, z_end);
-  }
-  __device__ __forceinline__ bool first() const { return b0 == z * p.per_z; }
-  __device__ __forceinline__ bool last() const { return b1 == z_end; }
-  __device__ __forceinline__ void next() {
-    if (!last()) {
-      b0 = b1;
-      b1 = min(b0 + p.chunk, z_end);
-    } else {
-      tile += step;
-      if (more()) begin();
-    }
-  }
-};
 }  // namespace
 
 template <bool kF32>
@@ -270,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             copy_scales_pair(sf + 4, bs0 + soff);
             copy_scales_pair(sf + 8, bs0 + soff + (L8_SCALE_TILE >> 4));
           }
-          const uint32_t idesc = kIdesc | majors | static_cast<uint32_t>(b % 4) << 4 | static_cast<uint32_t>(b % 4) << 29;
+          const uint32_t idesc = kIdesc8 | majors | static_cast<uint32_t>(b % 4) << 4 | static_cast<uint32_t>(b % 4) << 29;
 #pragma unroll
           for (int kk = 0; kk < L8_BLOCK / 32; ++kk)
             mma_block_scaled_pair(d_tmem, adesc0 + soff + kk * astep, bdesc0 + soff + kk * bstep, idesc, sf, sf + 4,
@@ -322,8 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t r[32];
-          tmem_ld32(t_addr + h * 32, r);
-          tmem_ld_wait();
+          tmem_read32(t_addr + h * 32, r);
           if (p.bias) {
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
@@ -355,8 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t r[32];
-          tmem_ld32(t_addr + h * 32, r);
-          tmem_ld_wait();
+          tmem_read32(t_addr + h * 32, r);
           if (w.first()) {
 #pragma unroll
             for (int v = 0; v < 32; ++v) sum[h * 32 + v] = __uint_as_float(r[v]);

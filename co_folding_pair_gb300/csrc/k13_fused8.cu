@@ -1,0 +1,575 @@
+// k13_fused8.cu -- the product in 8 bits (k12_gemm8.cu) with one operand taken
+// as bf16 and rounded on its way to the tensor cores, so that its codes never
+// reach memory.
+//
+//   by rows (kCols false)    C[m][n] = Q(t)[m][:] . B[n][:]     t: bf16 [M][depth], 128 of a row share a power: y and dx
+//   by columns (kCols true)  C[m][n] = Q(t)[:][m] . B[n][:]     t: bf16 [depth][M], 128 of a column share a power: dW
+//
+// A pair stack's layers are narrow (K of 1024 at most) and have millions of
+// rows: bf16 in, bf16 out bounds them, and a pass of its own for the codes would
+// write and read half of the input again.  The price is that a tile of t is
+// rounded once for every 256 columns of C (from L2: a pair takes a row of tiles
+// in turn).
+//
+// Two CTAs of a cluster have 128 rows of A each and one tile of B between them:
+// each loads half of it (TMA) for both.  Unlike k12_gemm8.cu each multiplies by
+// itself (M = 128, N = 256, cta_group::1): as one pair, the odd CTA's codes had to be made
+// known to the even CTA by a release at cluster scope for every block, which takes
+// about as long as rounding it (550 to 860 us at 2^20 rows of 1024 to 256, whichever warps did it).
+//
+// Per CTA, 19 warps: 0 loads B and 18 the CTA's tile of t, 1 issues the
+// multiplications, 2..9 are the epilogue and 10..17 round.  A tile of t waits as bf16
+// in a ring of its own.  Eight lanes take a row's 128 numbers (by columns, sixteen
+// lanes eight each), and the codes go to shared memory as TMA would have put them
+// there, with the block's powers beside them; a proxy fence makes them visible to the
+// tensor cores.  (The rounding warps load nothing from global memory themselves: with
+// the next block's loads on their way in registers each fence waited for those.)
+//
+// TMEM as in k12_gemm8.cu; A's powers are copied for each block (eight sets of four
+// columns, more than the ring is deep: a set's readers are done when it is written
+// again), B's for each group of four.
+//
+// fp32 output: an accumulation takes `chunk` blocks, and the epilogue adds it to
+// what it has written before.  Each element has one thread, whichever accumulator
+// it is in: the order is fixed, and no thread reads what another one wrote.
+#include "gemm8.cuh"
+#include "quantize8.cuh"
+
+namespace trimul {
+
+namespace {
+constexpr int ROWS = 128;
+constexpr int STAGES = 3, RAW_SLOTS = 2;
+constexpr uint32_t CODE_BYTES = ROWS * L8_BLOCK;
+constexpr uint32_t A_SCALES = 3 * CODE_BYTES, B_SCALES = A_SCALES + L8_SCALE_TILE;  // 128 rows of A, 256 of B
+constexpr uint32_t STAGE_BYTES = 50 * 1024;
+constexpr uint32_t RAW_HALF = 128 * 128, RAW_BYTES = 2 * RAW_HALF;  // 128 rows of 64 bf16 numbers, twice
+constexpr uint32_t BAR_BYTES = 512;
+constexpr uint32_t TOPS_BYTES = 2 * 8 * 16 * 16;  // by columns: the warps' largest magnitudes, two turns of them
+constexpr uint32_t TMEM_COLS = 512, ACC_STEP = 192;
+constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 3;
+constexpr int EPI_WARPS = 8, ROUND_WARPS = 8;
+constexpr int EPI0 = 2, ROUND0 = EPI0 + EPI_WARPS, RAW = ROUND0 + ROUND_WARPS, THREADS = 32 * (RAW + 1);
+static_assert(A_SETS > STAGES + 1, "a set's readers are done when it is written again");
+static_assert(A_COLS + 4 * A_SETS <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
+constexpr uint32_t RAW0 = STAGES * STAGE_BYTES, BARS = RAW0 + RAW_SLOTS * RAW_BYTES;
+constexpr size_t kSmem = 1024 + BARS + BAR_BYTES + TOPS_BYTES;
+constexpr uint32_t SITE_ROUND = 0x500;
+constexpr uint32_t kIdesc128 = (kIdesc8 & ~(0x1Fu << 24)) | ((ROWS >> 4) << 24);
+
+__device__ __forceinline__ void mma_block_scaled(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t a_scale,
+                                                 uint32_t b_scale, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sdesc) : "memory");
+}
+// Arrive once at the offset `bar` in both CTAs when what this thread has issued is done.
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// A box to the same place in both CTAs, its bytes counted on the barrier at the same place in each.
+__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_shared8(uint32_t at, uint2 v) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
+
+// A thread's 64 numbers of a block.
+struct Numbers {
+  uint4 v[8];
+};
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+// 16 bytes of a row of a tile of t: `chunk` of the row's sixteen (128-byte swizzle, 64 numbers a half).
+__device__ __forceinline__ uint4 raw16(uint32_t slot, int row, int chunk) {
+  return ld_shared16(slot + (chunk >> 3) * RAW_HALF + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+// ---- by rows: lane `lane8` of row group `group` (0..31) has numbers 8 lane8 .. + 7 and 64 + 8 lane8 .. of rows group +
+// 32 u: v[2 u] and v[2 u + 1]; `left`: of the block's 128, those before the row's end (the others are not loaded)
+__device__ __forceinline__ void load_rows(Numbers& x, uint32_t slot, int left, int group, int lane8) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x.v[2 * u + h] = make_uint4(0u, 0u, 0u, 0u);
+      if (64 * h + 8 * lane8 < left) x.v[2 * u + h] = raw16(slot, group + 32 * u, 8 * h + lane8);
+    }
+}
+__device__ __forceinline__ void round_rows(const Numbers& x, uint32_t codes, uint32_t scales, int group, int lane8) {
+  uint32_t m[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) m[u] = max_magnitude(x.v[2 * u], x.v[2 * u + 1]);
+  // two rows' largest in a word, over the row's eight lanes
+  auto over_row = [&](uint32_t (&top)[4]) {
+    uint32_t two[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      two[k] = max16x2(__byte_perm(top[2 * k], top[2 * k + 1], 0x5410), __byte_perm(top[2 * k], top[2 * k + 1], 0x7632));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      two[0] = max16x2(two[0], __shfl_xor_sync(0xffffffffu, two[0], o));
+      two[1] = max16x2(two[1], __shfl_xor_sync(0xffffffffu, two[1], o));
+    }
+    top[0] = two[0] & 0xffffu, top[1] = two[0] >> 16, top[2] = two[1] & 0xffffu, top[3] = two[1] >> 16;
+  };
+  over_row(m);
+  bool fine[4], all = true;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) fine[u] = m[u] < 0x7f80u, all = all && fine[u];
+  if (!__all_sync(0xffffffffu, all)) {  // rare
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m[u] = max16x2(max_of(finite(x.v[2 * u])), max_of(finite(x.v[2 * u + 1])));
+    over_row(m);
+  }
+  uint32_t byte[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    byte[u] = scale_byte(m[u] << 16);
+    const float inv = over_scale(byte[u]);
+    const uint2 a = codes_of(x.v[2 * u], inv, fine[u]), b = codes_of(x.v[2 * u + 1], inv, fine[u]);
+    const int row = group + 32 * u;
+    st_shared8(codes + row * 128 + (((lane8 >> 1) ^ (row & 7)) << 4) + (lane8 & 1) * 8, a);
+    st_shared8(codes + row * 128 + (((4 + (lane8 >> 1)) ^ (row & 7)) << 4) + (lane8 & 1) * 8, b);
+  }
+  if (lane8 == 0) st_shared16(scales + group * 16, byte[0], byte[1], byte[2], byte[3]);
+}
+
+// ---- by columns: lane `lane16` of row group `group` (0..15) has columns 8 lane16 .. + 7 of rows group + 16 u: v[u]; `left`: of
+// the tile's 128 columns, those before the last
+__device__ __forceinline__ void load_cols(Numbers& x, uint32_t slot, int left, int group, int lane16) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    x.v[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (8 * lane16 < left) x.v[u] = raw16(slot, group + 16 * u, lane16);
+  }
+}
+__device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uint32_t scales, uint4* tops, int warp, int group, int lane16) {
+  auto join = [](uint4& a, const uint4& b) {
+    a.x = max16x2(a.x, b.x), a.y = max16x2(a.y, b.y), a.z = max16x2(a.z, b.z), a.w = max16x2(a.w, b.w);
+  };
+  auto larger = [](uint4& a, const uint4& b) {
+    a.x = max_signed(a.x, b.x), a.y = max_signed(a.y, b.y), a.z = max_signed(a.z, b.z), a.w = max_signed(a.w, b.w);
+  };
+  uint4 top = x.v[0];
+#pragma unroll
+  for (int u = 1; u < 8; ++u) larger(top, x.v[u]);
+  top = magnitudes(top);
+  const uint32_t all = max_of(top);
+  const bool fine = (all & 0xffffu) < 0x7f80u && all < 0x7f800000u;
+  if (!fine) {  // rare
+    top = finite(x.v[0]);
+#pragma unroll
+    for (int u = 1; u < 8; ++u) join(top, finite(x.v[u]));
+  }
+  join(top, make_uint4(__shfl_xor_sync(0xffffffffu, top.x, 16), __shfl_xor_sync(0xffffffffu, top.y, 16),
+                       __shfl_xor_sync(0xffffffffu, top.z, 16), __shfl_xor_sync(0xffffffffu, top.w, 16)));
+  if (threadIdx.x % 32 < 16) tops[warp * 16 + lane16] = top;
+  named_bar_sync(1, 32 * ROUND_WARPS);  // (the next block has the other half of `tops`)
+#pragma unroll
+  for (int q = 0; q < ROUND_WARPS; ++q) join(top, tops[q * 16 + lane16]);
+  const uint32_t word[4] = {top.x, top.y, top.z, top.w};
+  uint32_t byte[8];
+  f2 inv[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    byte[2 * e] = scale_byte(word[e] << 16), byte[2 * e + 1] = scale_byte(word[e] & 0xffff0000u);
+    inv[e] = pair2(over_scale(byte[2 * e]), over_scale(byte[2 * e + 1]));
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int row = group + 16 * u;
+    st_shared8(codes + row * 128 + (((lane16 >> 1) ^ (row & 7)) << 4) + (lane16 & 1) * 8, codes_of(x.v[u], inv, fine));
+  }
+  if (group < 8) {  // group g has column g of the lane's eight
+    uint32_t mine = byte[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) mine = group == e ? byte[e] : mine;
+    const int c = lane16 * 8 + group;
+    st_shared4(scales + (c % 32) * 16 + (c / 32) * 4, mine);
+  }
+}
+}  // namespace
+
+template <bool kCols>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
+               const __grid_constant__ CUtensorMap tm_b_scale, const Fused8Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const uint32_t bars = base + BARS;
+  // bfull[STAGES] afull[STAGES] empty[STAGES] rfull[RAW_SLOTS] rempty[RAW_SLOTS] tfull[2] tempty[2] over drain, then the TMEM
+  // base word
+  const uint32_t bfull0 = bars, afull0 = bfull0 + 8 * STAGES, empty0 = afull0 + 8 * STAGES;
+  const uint32_t rfull0 = empty0 + 8 * STAGES, rempty0 = rfull0 + 8 * RAW_SLOTS;
+  const uint32_t tfull0 = rempty0 + 8 * RAW_SLOTS, tempty0 = tfull0 + 16, over = tempty0 + 16, drain = over + 8;
+  const uint32_t tmem_slot = drain + 8;
+  volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base));
+  uint4* const tops = reinterpret_cast<uint4*>(base_ptr + BARS + BAR_BYTES);
+
+  const KStatus st{p.g.status, p.g.timeout_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  // a first kernel has nobody before it to clear the status word: the first block does, and no other looks at it sooner
+  // than a millisecond into a wait
+  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.g.status = 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bfull0 + 8 * s, 1);            // one expect_tx arrival; bytes that both CTAs load
+      mbar_init(afull0 + 8 * s, ROUND_WARPS);
+      mbar_init(empty0 + 8 * s, 2);            // one commit of each CTA: B's tile is written for both
+    }
+    for (int r = 0; r < RAW_SLOTS; ++r) {
+      mbar_init(rfull0 + 8 * r, 1);  // one expect_tx arrival
+      mbar_init(rempty0 + 8 * r, ROUND_WARPS);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, EPI_WARPS);
+    }
+    mbar_init(over, 4);  // the warps that have read the columns that overlap
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot_ptr;
+  Walk w(p.g, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1));
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer of B: this CTA's half, for both
+    if (lane == 0 && !p.g.stall) {
+      tma_prefetch_desc(&tm_b);
+      tma_prefetch_desc(&tm_b_scale);
+      const int groups = (p.g.blocks + 3) / 4, b_tiles = (p.g.N + ROWS - 1) / ROWS;
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (; w.more() && ok; w.next()) {
+        const int bt = w.tn * 2 + static_cast<int>(rank);
+        const int rb = bt < b_tiles ? bt * ROWS : 0;  // (a box wholly past N loads row 0)
+        for (int b = w.b0; b < w.b1; ++b) {
+          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, st, SITE_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + stage * STAGE_BYTES;
+          const uint32_t fb = bfull0 + 8 * stage;
+          const bool scales = b % 4 == 0 || b == w.b0;
+          mbar_arrive_expect_tx(fb, 2 * (CODE_BYTES + (scales ? L8_SCALE_TILE : 0)));
+          const int d = b * L8_BLOCK;
+          tma_load_2d_both(sa + CODE_BYTES * (1 + rank), &tm_b, fb, p.g.b_mn ? rb : d, p.g.b_mn ? d : rb);
+          if (scales) tma_load_2d_both(sa + B_SCALES + rank * L8_SCALE_TILE, &tm_b_scale, fb, 0, (bt < b_tiles ? bt : 0) * groups + b / 4);
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {  // the copies on their way land before the CTA goes away
+        int s = stage;
+        uint32_t ph = phase;
+        for (long long i = 0; i < issued && i < STAGES; ++i) {
+          if (--s < 0) {
+            s = STAGES - 1;
+            ph ^= 1u;
+          }
+          mbar_wait_drain(bfull0 + 8 * s, ph, p.g.timeout_ns);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t adesc0 = sdesc_sw128(base, kCols ? CODE_BYTES : 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(base + CODE_BYTES, p.g.b_mn ? CODE_BYTES : 16, 1024);
+      const uint64_t as0 = sdesc_scales(base + A_SCALES), bs0 = sdesc_scales(base + B_SCALES);
+      const uint32_t astep = kCols ? 32 * 128 >> 4 : 32 >> 4, bstep = p.g.b_mn ? 32 * 128 >> 4 : 32 >> 4;
+      const uint32_t majors = static_cast<uint32_t>(kCols) << 15 | static_cast<uint32_t>(p.g.b_mn) << 16;
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, aphase = 0, ophase = 1, a_set = 0, b_set = 0;
+      bool ok = true;
+      for (; w.more() && ok; w.next()) {
+        if (!mbar_wait(tempty0 + 8 * acc, aphase ^ 1u, st, SITE_MMA) || !mbar_wait(over, ophase, st, SITE_MMA)) {
+          ok = false;
+          break;
+        }
+        ophase ^= 1u;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * ACC_STEP;
+        uint32_t sfb = 0;
+        for (int b = w.b0; b < w.b1; ++b) {
+          if (!mbar_wait(bfull0 + 8 * stage, phase, st, SITE_MMA) || !mbar_wait(afull0 + 8 * stage, phase, st, SITE_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t soff = (stage * STAGE_BYTES) >> 4;
+          const uint32_t sfa = tmem_base + A_COLS + a_set * 4;
+          if (++a_set == A_SETS) a_set = 0;
+          copy_scales(sfa, as0 + soff);
+          if (b % 4 == 0 || b == w.b0) {
+            sfb = tmem_base + B_COLS + b_set * 8;
+            if (++b_set == B_SETS) b_set = 0;
+            copy_scales(sfb, bs0 + soff);
+            copy_scales(sfb + 4, bs0 + soff + (L8_SCALE_TILE >> 4));
+          }
+          const uint32_t idesc = kIdesc128 | majors | static_cast<uint32_t>(b % 4) << 4;  // A's power is the first byte of its word
+#pragma unroll
+          for (int kk = 0; kk < L8_BLOCK / 32; ++kk)
+            mma_block_scaled(d_tmem, adesc0 + soff + kk * astep, bdesc0 + soff + kk * bstep, idesc, sfa, sfb,
+                                  (b != w.b0 || kk != 0) ? 1u : 0u);
+          mma_commit_both(empty0 + 8 * stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit(tfull0 + 8 * acc);
+        if (++acc == 2) {
+          acc = 0;
+          aphase ^= 1u;
+        }
+      }
+      if (!ok) {
+        mma_commit(drain);
+        mbar_wait_drain(drain, 0, p.g.timeout_ns);
+      }
+    }
+  } else if (warp < ROUND0) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;               // TMEM lane quadrant of this warp
+    const int sub = (warp - EPI0) >> 2;   // 0: the outer two of the 64-column blocks, 1: the inner two
+    const uint32_t gb = lane & 7, ga = lane >> 3;
+    int acc = 0;
+    uint32_t aphase = 0;
+    bool ok = true;
+    for (; w.more() && ok; w.next()) {
+      ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * acc, aphase, st, SITE_EPI));
+      if (!ok) break;
+      tc_fence_after();
+      const int row0 = w.tm * L8_TILE + static_cast<int>(rank) * ROWS + q * 32 + static_cast<int>(ga) * 8;
+#pragma unroll 1
+      for (int turn = 0; turn < 2; ++turn) {
+        const int cb = (turn ^ acc) ? sub : 3 - sub;  // the shared columns are the last block's of accumulator 0, the first's of 1
+        const bool shared = sub == 0 && turn == 0;
+        const int c0 = w.tn * L8_TILE + cb * 64;
+        const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * ACC_STEP + cb * 64;
+        auto hand_back = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (shared) mbar_arrive(over);
+            if (turn == 1) mbar_arrive(tempty0 + 8 * acc);
+          }
+        };
+        if constexpr (!kCols) {
+          uint4 R[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_read32(t_addr + h * 32, r);
+            if (p.g.bias) {
+#pragma unroll
+              for (int v = 0; v < 8; ++v) {
+                const int col = c0 + h * 32 + v * 4;
+                const float4 b = col < p.g.N ? *reinterpret_cast<const float4*>(p.g.bias + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+                r[4 * v] = __float_as_uint(__uint_as_float(r[4 * v]) + b.x);
+                r[4 * v + 1] = __float_as_uint(__uint_as_float(r[4 * v + 1]) + b.y);
+                r[4 * v + 2] = __float_as_uint(__uint_as_float(r[4 * v + 2]) + b.z);
+                r[4 * v + 3] = __float_as_uint(__uint_as_float(r[4 * v + 3]) + b.w);
+              }
+            }
+            auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf162(__uint_as_float(lo), __uint_as_float(hi)); };
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              R[h * 4 + v] = make_uint4(pack(r[v * 8 + 0], r[v * 8 + 1]), pack(r[v * 8 + 2], r[v * 8 + 3]),
+                                        pack(r[v * 8 + 4], r[v * 8 + 5]), pack(r[v * 8 + 6], r[v * 8 + 7]));
+          }
+          hand_back();
+          transpose8(R, gb);
+          const int col = c0 + static_cast<int>(gb) * 8;
+          if (col < p.g.N) {  // N is a multiple of 8: a chunk is all in or all out
+#pragma unroll
+            for (int s8 = 0; s8 < 8; ++s8) {
+              const int row = row0 + s8;
+              if (row < p.g.M) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.g.c) + static_cast<size_t>(row) * p.g.N + col) = R[s8];
+            }
+          }
+        } else {
+          float* const cz = static_cast<float*>(p.g.c) + static_cast<size_t>(w.z) * p.g.M * p.g.N;
+          const bool add = !w.first();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 32 columns: 8 chunks of 4 fp32
+            uint4 R[8];
+            {
+              uint32_t r[32];
+              tmem_read32(t_addr + h * 32, r);
+#pragma unroll
+              for (int v = 0; v < 8; ++v) R[v] = make_uint4(r[v * 4], r[v * 4 + 1], r[v * 4 + 2], r[v * 4 + 3]);
+            }
+            if (h == 1) hand_back();
+            transpose8(R, gb);
+            const int col = c0 + h * 32 + static_cast<int>(gb) * 4;
+            if (col < p.g.N) {
+#pragma unroll
+              for (int s8 = 0; s8 < 8; ++s8) {
+                const int row = row0 + s8;
+                if (row >= p.g.M) continue;
+                float4* const to = reinterpret_cast<float4*>(cz + static_cast<size_t>(row) * p.g.N + col);
+                float4 v = make_float4(__uint_as_float(R[s8].x), __uint_as_float(R[s8].y), __uint_as_float(R[s8].z), __uint_as_float(R[s8].w));
+                if (add) {
+                  const float4 o = *to;
+                  v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                }
+                *to = v;
+              }
+            }
+          }
+        }
+      }
+      if (++acc == 2) {
+        acc = 0;
+        aphase ^= 1u;
+      }
+    }
+  } else if (warp < RAW) {
+    // ------------------------------------------------------------ rounding of A
+    const int t = threadIdx.x - 32 * ROUND0;
+    const int lanes = kCols ? t % 16 : t % 8, group = kCols ? t / 16 : t / 8;
+    int stage = 0, slot = 0, turn = 0;
+    uint32_t phase = 0, rphase = 0;
+    bool ok = true;
+    for (; w.more() && ok; w.next()) {
+      const long long c0 = (static_cast<long long>(w.tm) * 2 + rank) * ROWS;
+      for (int b = w.b0; b < w.b1; ++b, turn ^= 1) {
+        ok = __all_sync(0xffffffffu, mbar_wait(rfull0 + 8 * slot, rphase, st, SITE_ROUND) &&
+                                         mbar_wait(empty0 + 8 * stage, phase ^ 1u, st, SITE_ROUND));
+        if (kCols) ok = named_bar_and(2, 32 * ROUND_WARPS, ok);  // they meet in round_cols: all of them, or none
+        if (!ok) break;
+        const uint32_t sr = base + RAW0 + slot * RAW_BYTES, sa = base + stage * STAGE_BYTES;
+        Numbers x;
+        if (kCols) {
+          const long long left = p.g.M - c0;
+          load_cols(x, sr, left < ROWS ? static_cast<int>(left) : ROWS, group, lanes);
+        } else {
+          const long long left = p.depth - static_cast<long long>(b) * L8_BLOCK;
+          load_rows(x, sr, left < L8_BLOCK ? static_cast<int>(left) : L8_BLOCK, group, lanes);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rempty0 + 8 * slot);
+        if (kCols)
+          round_cols(x, sa, sa + A_SCALES, tops + turn * (ROUND_WARPS * 16), t / 32, group, lanes);
+        else
+          round_rows(x, sa, sa + A_SCALES, group, lanes);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(afull0 + 8 * stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++slot == RAW_SLOTS) {
+          slot = 0;
+          rphase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ producer of t
+    if (lane == 0 && !p.g.stall) {
+      tma_prefetch_desc(&tm_t);
+      int slot = 0;
+      uint32_t rphase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (; w.more() && ok; w.next()) {
+        // (a box wholly past t may not complete its bytes: rows of C past M take those of row 0, and a half that has nothing
+        // is not loaded)
+        long long c0 = (static_cast<long long>(w.tm) * 2 + rank) * ROWS;
+        if (c0 >= p.g.M) c0 = 0;
+        for (int b = w.b0; b < w.b1; ++b) {
+          if (!mbar_wait(rempty0 + 8 * slot, rphase ^ 1u, st, SITE_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          const int d = b * L8_BLOCK, x = kCols ? static_cast<int>(c0) : d, y = kCols ? d : static_cast<int>(c0);
+          const int halves = x + 64 < (kCols ? p.g.M : p.depth) ? 2 : 1;
+          const uint32_t sr = base + RAW0 + slot * RAW_BYTES;
+          mbar_arrive_expect_tx(rfull0 + 8 * slot, halves * RAW_HALF);
+          tma_load_2d(sr, &tm_t, rfull0 + 8 * slot, x, y);
+          if (halves == 2) tma_load_2d(sr + RAW_HALF, &tm_t, rfull0 + 8 * slot, x + 64, y);
+          ++issued;
+          if (++slot == RAW_SLOTS) {
+            slot = 0;
+            rphase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {  // the copies on their way land before the CTA goes away
+        int r = slot;
+        uint32_t ph = rphase;
+        for (long long i = 0; i < issued && i < RAW_SLOTS; ++i) {
+          if (--r < 0) {
+            r = RAW_SLOTS - 1;
+            ph ^= 1u;
+          }
+          mbar_wait_drain(rfull0 + 8 * r, ph, p.g.timeout_ns);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while the other may still write to it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+cudaError_t launch_fused8(const Fused8Args& a, const CUtensorMap& t, const CUtensorMap& b, const CUtensorMap& b_scale, bool cols, int pairs, cudaStream_t s) {
+  auto kernel = cols ? k13_fused8<true> : k13_fused8<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+  if (e != cudaSuccess) return e;
+  const long long tiles = static_cast<long long>(a.g.tiles_m) * a.g.tiles_n * a.g.n_z;
+  const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+  kernel<<<grid, THREADS, kSmem, s>>>(t, b, b_scale, a);
+  return cudaGetLastError();
+}
+
+}  // namespace trimul

@@ -43,7 +43,7 @@ __host__ __device__ __forceinline__ size_t l8_scale_at(long long row, long long 
 }
 
 // ---------------------------------------------------------------- rounding to 8 bits (k11_quantize8.cu)
-// Each clears the word `status` (or null) for the product behind it.
+// Each clears the word `status` (or null) for the products behind it.
 // bf16 [rows][depth], a scale for each row and 128 columns: the operand {rows, depth}.
 cudaError_t launch_quantize_rows(const uint16_t* x, long long rows, int depth, uint8_t* out, int* status, int num_sms, cudaStream_t s);
 // bf16 [rows][cols], a scale for each column and 128 rows: the operand {cols, rows, mn}; with by_rows (or null) also as
@@ -72,9 +72,17 @@ struct Gemm8Args {
 struct Gemm8Maps {
   CUtensorMap a, b, a_scale, b_scale;
 };
+// The same with A as bf16 that is rounded on its way (k13_fused8.cu): by rows from t [M][depth] to bf16, or by columns from
+// t [depth][M] to f32 slices, whose accumulations begin at multiples of g.chunk.
+struct Fused8Args {
+  Gemm8Args g;
+  long long depth;
+  int clear;             // clear the status word first
+};
+cudaError_t launch_fused8(const Fused8Args& a, const CUtensorMap& t, const CUtensorMap& b, const CUtensorMap& b_scale, bool cols, int pairs, cudaStream_t s);
 int gemm8_max_pairs(int num_sms);
 cudaError_t launch_gemm8(const Gemm8Args& a, const Gemm8Maps& m, bool f32, int pairs, cudaStream_t s);
-// out = the sum of n_z slices of n floats.
-cudaError_t launch_join(const float* part, int n_z, long long n, float* out, cudaStream_t s);
+// out = the sum of n_z slices of n floats; cols > 0: of matrices [n / cols][cols], transposed.
+cudaError_t launch_join(const float* part, int n_z, long long n, int cols, float* out, cudaStream_t s);
 
 }  // namespace trimul

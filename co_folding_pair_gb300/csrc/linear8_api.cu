@@ -20,6 +20,7 @@ namespace {
 constexpr int kMostWidth = 65536;
 constexpr int kMostPairs = 128, kMostSms = 256;  // what workspaces are sized for
 constexpr int kChunk = 32;                       // blocks of 128 rows that a weight gradient's accumulation takes
+constexpr int kFusedTiles = 1;                   // 256-wide tiles of the other operand up to which rounding on the way is faster (k13_fused8.cu)
 constexpr unsigned long long kTimeoutNs = 4000000000ull, kStallTimeoutNs = 200000000ull;
 constexpr size_t kStatusBytes = 256;
 
@@ -58,6 +59,18 @@ trimul_status operand_maps(CUtensorMap* codes, CUtensorMap* scales, const Operan
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
   if (r != CUDA_SUCCESS) return fail(TRIMUL_ERR_CUDA, "tensor map of an 8-bit operand rejected (CUresult %d)", static_cast<int>(r));
+  return TRIMUL_OK;
+}
+
+// bf16 [rows][cols] in boxes of 128 rows and 64 columns, zeros past the end.
+trimul_status bf16_map(CUtensorMap* m, const uint16_t* at, long long cols, long long rows) {
+  EncodeTiled fn = encode_tiled();
+  if (!fn) return fail(TRIMUL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint32_t one[2] = {1, 1}, box[2] = {64, 128};
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)}, stride[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(at), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TRIMUL_ERR_CUDA, "tensor map of a bf16 operand rejected (CUresult %d)", static_cast<int>(r));
   return TRIMUL_OK;
 }
 
@@ -109,6 +122,29 @@ trimul_status run_gemm(const Placed8& a, const Placed8& b, void* c, bool f32, co
   return TRIMUL_OK;
 }
 
+// C = Q(t) b^T with t, bf16, rounded on its way: by rows (t [M][depth], bf16 C) or by columns (t [depth][M], f32 slices).
+trimul_status run_fused(const uint16_t* from, long long M, long long depth, bool cols, const Placed8& b, void* c, const float* bias,
+                        int per_z, int n_z, int* status, bool clear, int pairs, cudaStream_t s, unsigned flags) {
+  Fused8Args p{};
+  p.clear = clear;
+  p.depth = depth;
+  p.g.M = static_cast<int>(M), p.g.N = static_cast<int>(b.o.rows);
+  p.g.b_mn = b.o.mn;
+  p.g.blocks = static_cast<int>(l8_blocks(depth));
+  p.g.per_z = per_z ? per_z : p.g.blocks;
+  p.g.n_z = n_z;
+  p.g.chunk = cols ? kChunk : p.g.per_z;
+  p.g.tiles_m = tiles_of(p.g.M), p.g.tiles_n = tiles_of(p.g.N);
+  p.g.c = c, p.g.bias = bias, p.g.status = status;
+  p.g.timeout_ns = flags & TRIMUL_FLAG_INJECT_STALL ? kStallTimeoutNs : kTimeoutNs;
+  p.g.stall = flags & TRIMUL_FLAG_INJECT_STALL;
+  CUtensorMap t, codes, scales;
+  TRY(bf16_map(&t, from, cols ? M : depth, cols ? depth : M));
+  TRY(operand_maps(&codes, &scales, b.o, b.codes, b.scales));
+  TRY_CUDA(launch_fused8(p, t, codes, scales, cols, pairs, s), "8-bit product launch");
+  return TRIMUL_OK;
+}
+
 trimul_status finish8(const int* status, cudaStream_t s, unsigned flags) {
   if (!(flags & TRIMUL_FLAG_CHECK)) return TRIMUL_OK;
   TRY_CUDA(cudaStreamSynchronize(s), "stream synchronize");
@@ -137,17 +173,23 @@ struct Packed {
   Packed(int N, int K) : w{N, K, false}, wt{K, N, true}, wt_scales_at(w.bytes()), bytes(wt_scales_at + wt.scale_bytes()) {}
 };
 
-// Offsets in a backward's workspace.
+// How a backward goes about it, and the offsets in its workspace.
 struct Backward8 {
+  bool dx_fused, dw_fused, dw_swapped;  // dw_swapped: x is A, and the slices are of dW^T
   Operand8 dy_rows, dy_cols, x_cols;
   size_t dy_rows_at, dy_cols_at, x_cols_at, slices_at, sums_at, bytes;
-  Backward8(int64_t rows, int N, int K) : dy_rows{rows, N, false}, dy_cols{N, rows, true}, x_cols{K, rows, true} {
+  Backward8(int64_t rows, int N, int K, bool want_dbias) : dy_rows{rows, N, false}, dy_cols{N, rows, true}, x_cols{K, rows, true} {
+    dx_fused = tiles_of(K) <= kFusedTiles;
+    // the wider one is rounded on its way; dbias comes from the pass over dy that rounds it by columns
+    dw_swapped = K >= N || want_dbias;
+    dw_fused = tiles_of(dw_swapped ? N : K) <= kFusedTiles;
+    if (!dw_fused) dw_swapped = false;
     int per_z, n_z;
     slices(N, K, static_cast<int>(l8_blocks(rows)), kMostPairs, &per_z, &n_z);
     dy_rows_at = kStatusBytes;
-    dy_cols_at = dy_rows_at + dy_rows.bytes();
-    x_cols_at = dy_cols_at + dy_cols.bytes();
-    slices_at = x_cols_at + x_cols.bytes();
+    dy_cols_at = dy_rows_at + (dx_fused ? 0 : dy_rows.bytes());
+    x_cols_at = dy_cols_at + (dw_fused && !dw_swapped ? 0 : dy_cols.bytes());
+    slices_at = x_cols_at + (dw_fused && dw_swapped ? 0 : x_cols.bytes());
     // (as many slices as kMostPairs allow, whatever rounding makes of fewer)
     sums_at = slices_at + up256(static_cast<size_t>(std::max(n_z, kMostPairs / (tiles_of(N) * tiles_of(K)))) * N * K * 4);
     bytes = sums_at + up256(static_cast<size_t>(quantize_columns_parts(rows, N, kMostSms)) * N * 4);
@@ -182,7 +224,7 @@ trimul_status trimul_linear8_pack(const void* W, trimul_dtype type, int N, int K
 
 size_t trimul_linear8_forward_workspace_bytes(int64_t rows, int N, int K) {
   if (check_widths(N, K) != TRIMUL_OK || check_rows(rows) != TRIMUL_OK) return 0;
-  return kStatusBytes + Operand8{rows, K, false}.bytes();
+  return kStatusBytes + (tiles_of(N) <= kFusedTiles ? 0 : Operand8{rows, K, false}.bytes());
 }
 
 trimul_status trimul_linear8_forward(const void* packed, const float* bias, const uint16_t* x, int64_t rows, int N, int K,
@@ -208,15 +250,21 @@ trimul_status trimul_linear8_forward(const void* packed, const float* bias, cons
   TRY(scope.enter(device));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* const status = static_cast<int*>(workspace);
-  uint8_t* const codes = static_cast<uint8_t*>(workspace) + kStatusBytes;
-  TRY_CUDA(launch_quantize_rows(x, rows, K, codes, status, sms, s), "quantisation launch");
-  TRY(run_gemm(Placed8(Operand8{rows, K, false}, codes), Placed8(l.w, static_cast<const uint8_t*>(packed)), y, false, bias, 0, 1, status, pairs_of(device, sms), s, flags));
+  const Placed8 w(l.w, static_cast<const uint8_t*>(packed));
+  const int pairs = pairs_of(device, sms);
+  if (tiles_of(N) <= kFusedTiles) {
+    TRY(run_fused(x, rows, K, false, w, y, bias, 0, 1, status, true, pairs, s, flags));
+  } else {
+    uint8_t* const codes = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    TRY_CUDA(launch_quantize_rows(x, rows, K, codes, status, sms, s), "quantisation launch");
+    TRY(run_gemm(Placed8(Operand8{rows, K, false}, codes), w, y, false, bias, 0, 1, status, pairs, s, flags));
+  }
   return finish8(status, s, flags);
 }
 
 size_t trimul_linear8_backward_workspace_bytes(int64_t rows, int N, int K) {
   if (check_widths(N, K) != TRIMUL_OK || check_rows(rows) != TRIMUL_OK) return 0;
-  return Backward8(rows, N, K).bytes;
+  return std::max(Backward8(rows, N, K, false).bytes, Backward8(rows, N, K, true).bytes);
 }
 
 trimul_status trimul_linear8_backward(const void* packed, const uint16_t* x, const uint16_t* dy, int64_t rows, int N, int K,
@@ -249,24 +297,40 @@ trimul_status trimul_linear8_backward(const void* packed, const uint16_t* x, con
     if (dbias) TRY_CUDA(cudaMemsetAsync(dbias, 0, bb, s), "dbias");
     return finish(cudaSuccess, s, flags, "linear8 backward");
   }
-  const Backward8 b(rows, N, K);
+  const Backward8 b(rows, N, K, dbias != nullptr);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   int* const status = static_cast<int*>(workspace);
   const uint8_t* const pk = static_cast<const uint8_t*>(packed);
   const int pairs = pairs_of(device, sms);
-  if (dW || dbias)
-    TRY_CUDA(launch_quantize_columns(dy, rows, N, ws + b.dy_cols_at, dx ? ws + b.dy_rows_at : nullptr, dbias,
-                                     reinterpret_cast<float*>(ws + b.sums_at), status, sms, s), "quantisation launch");
-  else if (dx)
-    TRY_CUDA(launch_quantize_rows(dy, rows, N, ws + b.dy_rows_at, status, sms, s), "quantisation launch");
-  if (dx) TRY(run_gemm(Placed8(b.dy_rows, ws + b.dy_rows_at), Placed8(l.wt, pk, pk + l.wt_scales_at), dx, false, nullptr, 0, 1, status, pairs, s, flags));
+  const Placed8 w(l.wt, pk, pk + l.wt_scales_at), dy_rows(b.dy_rows, ws + b.dy_rows_at), dy_cols(b.dy_cols, ws + b.dy_cols_at),
+      x_cols(b.x_cols, ws + b.x_cols_at);
+  const bool codes_of_dy = dbias || (dW && !(b.dw_fused && !b.dw_swapped));  // by columns
+  uint8_t* const rows_of_dy = dx && !b.dx_fused ? ws + b.dy_rows_at : nullptr;
+  if (codes_of_dy)
+    TRY_CUDA(launch_quantize_columns(dy, rows, N, ws + b.dy_cols_at, rows_of_dy, dbias, reinterpret_cast<float*>(ws + b.sums_at), status, sms, s),
+             "quantisation launch");
+  else if (rows_of_dy)
+    TRY_CUDA(launch_quantize_rows(dy, rows, N, rows_of_dy, status, sms, s), "quantisation launch");
+  if (dx) {
+    if (b.dx_fused)
+      TRY(run_fused(dy, rows, N, false, w, dx, nullptr, 0, 1, status, !codes_of_dy, pairs, s, flags));
+    else
+      TRY(run_gemm(dy_rows, w, dx, false, nullptr, 0, 1, status, pairs, s, flags));
+  }
   if (dW) {
-    TRY_CUDA(launch_quantize_columns(x, rows, K, ws + b.x_cols_at, nullptr, nullptr, nullptr, nullptr, sms, s), "quantisation launch");
     int per_z, n_z;
     slices(N, K, static_cast<int>(l8_blocks(rows)), pairs, &per_z, &n_z);
-    float* const part = n_z == 1 ? dW : reinterpret_cast<float*>(ws + b.slices_at);
-    TRY(run_gemm(Placed8(b.dy_cols, ws + b.dy_cols_at), Placed8(b.x_cols, ws + b.x_cols_at), part, true, nullptr, per_z, n_z, status, pairs, s, flags));
-    if (n_z > 1) TRY_CUDA(launch_join(part, n_z, static_cast<long long>(N) * K, dW, s), "join launch");
+    float* const part = n_z == 1 && !b.dw_swapped ? dW : reinterpret_cast<float*>(ws + b.slices_at);
+    if (!b.dw_fused || !b.dw_swapped)
+      TRY_CUDA(launch_quantize_columns(x, rows, K, ws + b.x_cols_at, nullptr, nullptr, nullptr, dx || codes_of_dy ? nullptr : status, sms, s),
+               "quantisation launch");
+    if (!b.dw_fused)
+      TRY(run_gemm(dy_cols, x_cols, part, true, nullptr, per_z, n_z, status, pairs, s, flags));
+    else if (b.dw_swapped)
+      TRY(run_fused(x, K, rows, true, dy_cols, part, nullptr, per_z, n_z, status, false, pairs, s, flags));
+    else
+      TRY(run_fused(dy, N, rows, true, x_cols, part, nullptr, per_z, n_z, status, false, pairs, s, flags));
+    if (part != dW) TRY_CUDA(launch_join(part, n_z, static_cast<long long>(N) * K, b.dw_swapped ? N : 0, dW, s), "join launch");
   }
   if (!dx && !dW && !dbias) return finish(cudaSuccess, s, flags, "linear8 backward");
   return finish8(status, s, flags);

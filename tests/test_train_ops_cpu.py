@@ -101,9 +101,11 @@ FWD = {"packed": A, "bias": None, "x": 2 * A, "rows": 64, "N": 128, "K": 128, "y
     ({"y": A + 256}, INVALID, "y overlaps packed"),
     ({"ws": 3 * A + 1024}, INVALID, "workspace overlaps y"),
     ({"bias": 4 * A}, INVALID, "workspace overlaps bias"),
-    ({"bytes": 1000}, INVALID, "are needed"),
+    ({"bias": 3 * A + 64}, INVALID, "y overlaps bias"),
+    ({"bytes": 100}, INVALID, "are needed"),
     ({"ws": None}, INVALID, "are needed"),
     ({"ws": 4 * A + 16}, INVALID, "256-byte aligned"),
+    ({"N": 2048, "bytes": 4096}, INVALID, "are needed"),
     ({"flags": 16}, INVALID, "flags 0x10"),
 ])
 def test_linear8_forward_refused(lib, call, want, text):
@@ -125,7 +127,7 @@ BWD = {**FWD, "dy": 5 * A, "dx": 6 * A, "dw": 7 * A, "db": 8 * A, "bytes": 1 << 
     ({"dw": 2 * A}, INVALID, "dW overlaps x"),
     ({"db": 7 * A + 64}, INVALID, "dbias overlaps dW"),
     ({"ws": 8 * A}, INVALID, "workspace overlaps dbias"),
-    ({"bytes": 1000}, INVALID, "are needed"),
+    ({"bytes": 100}, INVALID, "are needed"),
     ({"flags": 4}, INVALID, "flags 0x4"),
 ])
 def test_linear8_backward_refused(lib, call, want, text):
