@@ -17,8 +17,8 @@
 // known to the even CTA by a release at cluster scope for every block, which takes
 // about as long as rounding it (550 to 860 us at 2^20 rows of 1024 to 256, whichever warps did it).
 //
-// Per CTA, 19 warps: 0 loads B and 18 the CTA's tile of t, 1 issues the
-// multiplications, 2..9 are the epilogue and 10..17 round.  A tile of t waits as bf16
+// Per CTA, 27 warps: 0 loads B and 26 the CTA's tile of t, 1 issues the
+// multiplications, 2..9 are the epilogue and 10..25 round, in two teams.  A tile of t waits as bf16
 // in a ring of its own.  Eight lanes take a row's 128 numbers (by columns, sixteen
 // lanes eight each), and the codes go to shared memory as TMA would have put them
 // there, with the block's powers beside them; a proxy fence makes them visible to the
@@ -45,10 +45,10 @@ constexpr uint32_t A_SCALES = 3 * CODE_BYTES, B_SCALES = A_SCALES + L8_SCALE_TIL
 constexpr uint32_t STAGE_BYTES = 50 * 1024;
 constexpr uint32_t RAW_HALF = 128 * 128, RAW_BYTES = 2 * RAW_HALF;  // 128 rows of 64 bf16 numbers, twice
 constexpr uint32_t BAR_BYTES = 512;
-constexpr uint32_t TOPS_BYTES = 2 * 8 * 16 * 16;  // by columns: the warps' largest magnitudes, two turns of them
+constexpr uint32_t TOPS_BYTES = 2 * 8 * 16 * 16;  // by columns: the largest magnitudes that each warp of a team has found
 constexpr uint32_t TMEM_COLS = 512, ACC_STEP = 192;
 constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 3;
-constexpr int EPI_WARPS = 8, ROUND_WARPS = 8;
+constexpr int EPI_WARPS = 8, TEAMS = 2, TEAM_WARPS = 8, ROUND_WARPS = TEAMS * TEAM_WARPS;
 constexpr int EPI0 = 2, ROUND0 = EPI0 + EPI_WARPS, RAW = ROUND0 + ROUND_WARPS, THREADS = 32 * (RAW + 1);
 static_assert(A_SETS > STAGES + 1, "a set's readers are done when it is written again");
 static_assert(A_COLS + 4 * A_SETS <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
@@ -118,7 +118,8 @@ __device__ __forceinline__ void load_rows(Numbers& x, uint32_t slot, int left, i
       if (64 * h + 8 * lane8 < left) x.v[2 * u + h] = raw16(slot, group + 32 * u, 8 * h + lane8);
     }
 }
-__device__ __forceinline__ void round_rows(const Numbers& x, uint32_t codes, uint32_t scales, int group, int lane8) {
+template <typename Release>
+__device__ __forceinline__ void round_rows(const Numbers& x, uint32_t codes, uint32_t scales, int group, int lane8, Release release) {
   uint32_t m[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) m[u] = max_magnitude(x.v[2 * u], x.v[2 * u + 1]);
@@ -136,6 +137,7 @@ __device__ __forceinline__ void round_rows(const Numbers& x, uint32_t codes, uin
     top[0] = two[0] & 0xffffu, top[1] = two[0] >> 16, top[2] = two[1] & 0xffffu, top[3] = two[1] >> 16;
   };
   over_row(m);
+  release();
   bool fine[4], all = true;
 #pragma unroll
   for (int u = 0; u < 4; ++u) fine[u] = m[u] < 0x7f80u, all = all && fine[u];
@@ -166,7 +168,9 @@ __device__ __forceinline__ void load_cols(Numbers& x, uint32_t slot, int left, i
     if (8 * lane16 < left) x.v[u] = raw16(slot, group + 16 * u, lane16);
   }
 }
-__device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uint32_t scales, uint4* tops, int warp, int group, int lane16) {
+template <typename Release>
+__device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uint32_t scales, uint4* tops, int team, int warp, int group,
+                                           int lane16, Release release) {
   auto join = [](uint4& a, const uint4& b) {
     a.x = max16x2(a.x, b.x), a.y = max16x2(a.y, b.y), a.z = max16x2(a.z, b.z), a.w = max16x2(a.w, b.w);
   };
@@ -187,9 +191,10 @@ __device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uin
   join(top, make_uint4(__shfl_xor_sync(0xffffffffu, top.x, 16), __shfl_xor_sync(0xffffffffu, top.y, 16),
                        __shfl_xor_sync(0xffffffffu, top.z, 16), __shfl_xor_sync(0xffffffffu, top.w, 16)));
   if (threadIdx.x % 32 < 16) tops[warp * 16 + lane16] = top;
-  named_bar_sync(1, 32 * ROUND_WARPS);  // (the next block has the other half of `tops`)
+  release();
+  named_bar_sync(1 + team, 32 * TEAM_WARPS);
 #pragma unroll
-  for (int q = 0; q < ROUND_WARPS; ++q) join(top, tops[q * 16 + lane16]);
+  for (int q = 0; q < TEAM_WARPS; ++q) join(top, tops[q * 16 + lane16]);
   const uint32_t word[4] = {top.x, top.y, top.z, top.w};
   uint32_t byte[8];
   f2 inv[4];
@@ -241,12 +246,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bfull0 + 8 * s, 1);            // one expect_tx arrival; bytes that both CTAs load
-      mbar_init(afull0 + 8 * s, ROUND_WARPS);
+      mbar_init(afull0 + 8 * s, TEAM_WARPS);
       mbar_init(empty0 + 8 * s, 2);            // one commit of each CTA: B's tile is written for both
     }
     for (int r = 0; r < RAW_SLOTS; ++r) {
       mbar_init(rfull0 + 8 * r, 1);  // one expect_tx arrival
-      mbar_init(rempty0 + 8 * r, ROUND_WARPS);
+      mbar_init(rempty0 + 8 * r, TEAM_WARPS);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
@@ -468,36 +473,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp < RAW) {
     // ------------------------------------------------------------ rounding of A
-    const int t = threadIdx.x - 32 * ROUND0;
+    // the teams take the blocks in turns: one block's way through shared memory, the maxima and the conversions is long, and the
+    // other team's instructions fill it
+    const int team = (warp - ROUND0) / TEAM_WARPS, t = threadIdx.x - 32 * (ROUND0 + team * TEAM_WARPS);
     const int lanes = kCols ? t % 16 : t % 8, group = kCols ? t / 16 : t / 8;
     int stage = 0, slot = 0, turn = 0;
     uint32_t phase = 0, rphase = 0;
     bool ok = true;
     for (; w.more() && ok; w.next()) {
       const long long c0 = (static_cast<long long>(w.tm) * 2 + rank) * ROWS;
-      for (int b = w.b0; b < w.b1; ++b, turn ^= 1) {
-        ok = __all_sync(0xffffffffu, mbar_wait(rfull0 + 8 * slot, rphase, st, SITE_ROUND) &&
-                                         mbar_wait(empty0 + 8 * stage, phase ^ 1u, st, SITE_ROUND));
-        if (kCols) ok = named_bar_and(2, 32 * ROUND_WARPS, ok);  // they meet in round_cols: all of them, or none
-        if (!ok) break;
-        const uint32_t sr = base + RAW0 + slot * RAW_BYTES, sa = base + stage * STAGE_BYTES;
-        Numbers x;
-        if (kCols) {
-          const long long left = p.g.M - c0;
-          load_cols(x, sr, left < ROWS ? static_cast<int>(left) : ROWS, group, lanes);
-        } else {
-          const long long left = p.depth - static_cast<long long>(b) * L8_BLOCK;
-          load_rows(x, sr, left < L8_BLOCK ? static_cast<int>(left) : L8_BLOCK, group, lanes);
+      for (int b = w.b0; b < w.b1; ++b) {
+        if (turn == team) {
+          ok = __all_sync(0xffffffffu, mbar_wait(rfull0 + 8 * slot, rphase, st, SITE_ROUND) &&
+                                           mbar_wait(empty0 + 8 * stage, phase ^ 1u, st, SITE_ROUND));
+          // by columns they meet in round_cols: all of the team, or none (and none has still to read the last block's `tops`)
+          if (kCols) ok = named_bar_and(1 + TEAMS + team, 32 * TEAM_WARPS, ok);
+          if (!ok) break;
+          const uint32_t sr = base + RAW0 + slot * RAW_BYTES, sa = base + stage * STAGE_BYTES;
+          Numbers x;
+          if (kCols) {
+            const long long left = p.g.M - c0;
+            load_cols(x, sr, left < ROWS ? static_cast<int>(left) : ROWS, group, lanes);
+          } else {
+            const long long left = p.depth - static_cast<long long>(b) * L8_BLOCK;
+            load_rows(x, sr, left < L8_BLOCK ? static_cast<int>(left) : L8_BLOCK, group, lanes);
+          }
+          // The slot is free once the numbers are here, not once their loads have been issued: it is given back behind the
+          // maxima, which need all of them.  (Given back right behind the loads, by columns one pass in two hundred took some
+          // numbers from the next block's copy.)
+          auto release = [&] {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(rempty0 + 8 * slot);
+          };
+          if (kCols)
+            round_cols(x, sa, sa + A_SCALES, tops + team * (TEAM_WARPS * 16), team, t / 32, group, lanes, release);
+          else
+            round_rows(x, sa, sa + A_SCALES, group, lanes, release);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(afull0 + 8 * stage);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(rempty0 + 8 * slot);
-        if (kCols)
-          round_cols(x, sa, sa + A_SCALES, tops + turn * (ROUND_WARPS * 16), t / 32, group, lanes);
-        else
-          round_rows(x, sa, sa + A_SCALES, group, lanes);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(afull0 + 8 * stage);
+        if (++turn == TEAMS) turn = 0;
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;

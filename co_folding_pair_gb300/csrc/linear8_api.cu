@@ -20,7 +20,9 @@ namespace {
 constexpr int kMostWidth = 65536;
 constexpr int kMostPairs = 128, kMostSms = 256;  // what workspaces are sized for
 constexpr int kChunk = 32;                       // blocks of 128 rows that a weight gradient's accumulation takes
-constexpr int kFusedTiles = 1;                   // 256-wide tiles of the other operand up to which rounding on the way is faster (k13_fused8.cu)
+// 256-wide tiles of the other operand up to which rounding on the way (k13_fused8.cu) is faster than a pass of its own: each tile
+// rounds again.  Rows (2^20 of them, us): one tile 175 to 280, two (2^19 rows) 264 to 287, four 634 to 560; columns: one 737 to 933, two 457 to 406.
+constexpr int kFusedRows = 2, kFusedColumns = 1;
 constexpr unsigned long long kTimeoutNs = 4000000000ull, kStallTimeoutNs = 200000000ull;
 constexpr size_t kStatusBytes = 256;
 
@@ -179,10 +181,10 @@ struct Backward8 {
   Operand8 dy_rows, dy_cols, x_cols;
   size_t dy_rows_at, dy_cols_at, x_cols_at, slices_at, sums_at, bytes;
   Backward8(int64_t rows, int N, int K, bool want_dbias) : dy_rows{rows, N, false}, dy_cols{N, rows, true}, x_cols{K, rows, true} {
-    dx_fused = tiles_of(K) <= kFusedTiles;
+    dx_fused = tiles_of(K) <= kFusedRows;
     // the wider one is rounded on its way; dbias comes from the pass over dy that rounds it by columns
     dw_swapped = K >= N || want_dbias;
-    dw_fused = tiles_of(dw_swapped ? N : K) <= kFusedTiles;
+    dw_fused = tiles_of(dw_swapped ? N : K) <= kFusedColumns;
     if (!dw_fused) dw_swapped = false;
     int per_z, n_z;
     slices(N, K, static_cast<int>(l8_blocks(rows)), kMostPairs, &per_z, &n_z);
@@ -224,7 +226,7 @@ trimul_status trimul_linear8_pack(const void* W, trimul_dtype type, int N, int K
 
 size_t trimul_linear8_forward_workspace_bytes(int64_t rows, int N, int K) {
   if (check_widths(N, K) != TRIMUL_OK || check_rows(rows) != TRIMUL_OK) return 0;
-  return kStatusBytes + (tiles_of(N) <= kFusedTiles ? 0 : Operand8{rows, K, false}.bytes());
+  return kStatusBytes + (tiles_of(N) <= kFusedRows ? 0 : Operand8{rows, K, false}.bytes());
 }
 
 trimul_status trimul_linear8_forward(const void* packed, const float* bias, const uint16_t* x, int64_t rows, int N, int K,
@@ -252,7 +254,7 @@ trimul_status trimul_linear8_forward(const void* packed, const float* bias, cons
   int* const status = static_cast<int*>(workspace);
   const Placed8 w(l.w, static_cast<const uint8_t*>(packed));
   const int pairs = pairs_of(device, sms);
-  if (tiles_of(N) <= kFusedTiles) {
+  if (tiles_of(N) <= kFusedRows) {
     TRY(run_fused(x, rows, K, false, w, y, bias, 0, 1, status, true, pairs, s, flags));
   } else {
     uint8_t* const codes = static_cast<uint8_t*>(workspace) + kStatusBytes;

@@ -125,6 +125,19 @@ def test_linear8_repeats(P):
     assert torch.equal(lin(x[1000:1300].contiguous()), y[1000:1300])
 
 
+@pytest.mark.parametrize("K,N", [(264, 136), (256, 264), (128, 520), (1024, 256)])
+def test_linear8_repeats_many_times(P, K, N):
+    """Rings that are reused thousands of times, at full speed: every pass gives the first one's bits."""
+    x, w, dy = inputs(rng_of(K), 1 << 18, K, N)
+    lin = P.Linear8(w)
+    y, g = lin(x), lin.backward(x, dy)
+    off = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        h = lin.backward(x, dy)
+        off += (lin(x) != y).sum() + (h["dx"] != g["dx"]).sum() + (h["dw"] != g["dw"]).sum()
+    assert int(off) == 0
+
+
 def test_linear8_no_rows(P):
     w = randn(rng_of(5), 16, 24, dtype=BF)
     lin = P.Linear8(w, torch.ones(16, device="cuda"))
