@@ -148,12 +148,11 @@ class GradTensor(ctypes.Structure):
 
 
 class AdamwTensor(ctypes.Structure):
-    _fields_ = [(name, ctypes.c_void_p) for name in ("param", "copy", "grad", "m", "v", "m_scale", "v_scale")] + [
+    _fields_ = [(name, ctypes.c_void_p) for name in ("param", "copy", "m", "v", "m_scale", "v_scale")] + [
         ("numel", ctypes.c_int64),
         ("weight_decay", ctypes.c_float),
         ("param_type", ctypes.c_int),
         ("copy_type", ctypes.c_int),
-        ("grad_type", ctypes.c_int),
     ]
 
 
@@ -207,7 +206,7 @@ SIGNATURES = {
     "trimul_grad_workspace_bytes": (_S, [_I]),
     "trimul_grad_norm": (_I, [ctypes.POINTER(GradTensor), _I, _I, _VP, _VP, _S, _I, _VP, _U]),
     "trimul_grad_clip": (_I, [ctypes.POINTER(GradTensor), _I, ctypes.c_float, _I, _VP, _VP, _S, _I, _VP, _U]),
-    "trimul_adamw_step": (_I, [ctypes.POINTER(AdamwParams), ctypes.POINTER(AdamwTensor), _I, _VP, _I, _VP, _U]),
+    "trimul_adamw_step": (_I, [ctypes.POINTER(AdamwParams), ctypes.POINTER(AdamwTensor), ctypes.POINTER(GradTensor), _I, _VP, _I, _VP, _U]),
     "trimul_linear8_packed_bytes": (_S, [_I, _I]),
     "trimul_linear8_pack": (_I, [_VP, _I, _I, _I, _VP, _S, _I, _VP, _U]),
     "trimul_linear8_forward_workspace_bytes": (_S, [ctypes.c_int64, _I, _I]),

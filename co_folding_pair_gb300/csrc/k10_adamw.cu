@@ -91,7 +91,7 @@ struct Entry {
   float *m_scale, *v_scale;
   long long numel;
   float decay;
-  uint32_t chunk, key;
+  uint32_t chunk, index;
   int kind;
 };
 
@@ -284,13 +284,13 @@ __device__ __forceinline__ void roots(const float (&x)[4], float (&r)[4]) {
 
 // What all elements of a step have in common.
 struct Step {
-  bool run;
+  bool known, run;
   float clip, lr, rate, over_root_c2;  // rate: lr / (1 - b1^t)
   uint32_t key;
 };
 __device__ __forceinline__ Step step_of(const Hyper& h, int count) {
   Step s;
-  s.run = true, s.clip = 1.f;
+  s.known = s.run = true, s.clip = 1.f;
   if (h.norm) {
     const float norm = *h.norm, share = __fmul_rn(h.max_norm, __frcp_rn(__fadd_rn(norm, 1e-6f)));
     s.run = norm - norm == 0.f;
@@ -306,15 +306,16 @@ __device__ __forceinline__ Step step_of(const Hyper& h, int count) {
 }
 
 template <int N>
-__device__ __forceinline__ Entry entry(const Table<N>& tab, int k, const Step& s) {
+__device__ __forceinline__ Entry entry(const Table<N>& tab, int k) {
   return Entry{tab.param[k],   tab.copy[k],  tab.grad[k],  tab.m[k],     tab.v[k],
                tab.m_scale[k], tab.v_scale[k], tab.numel[k], tab.decay[k], tab.chunk[k],
-               hash(tab.index[k] + s.key), tab.kind[k]};
+               tab.index[k],   tab.kind[k]};
 }
 
 // kKind: the tensor's kind, or -1 for one that is known only here.
+// `s` is worked out behind the first chunk's loads: what it is made of comes from memory as well.
 template <bool k8, int kKind>
-__device__ __forceinline__ void step_chunk(const Entry& t, uint32_t chunk, const Hyper& h, const Step& s) {
+__device__ __forceinline__ void step_chunk(const Entry& t, uint32_t chunk, const Hyper& h, const int* count, Step& s) {
   const long long first = static_cast<long long>(chunk - t.chunk) * kChunk + threadIdx.x * kEach;
   const bool stochastic = h.stochastic;
   const int kind = kKind < 0 ? t.kind : kKind;
@@ -337,7 +338,10 @@ __device__ __forceinline__ void step_chunk(const Entry& t, uint32_t chunk, const
       mr[u] = load4(t.m, TRIMUL_F32, i, t.numel, whole), vr[u] = load4(t.v, TRIMUL_F32, i, t.numel, whole);
     }
   }
+  if (!s.known) s = step_of(h, *const_cast<const volatile int*>(count));
+  if (!s.run) return;
   const float keep = 1.f - s.lr * t.decay;
+  const uint32_t tensor_key = hash(t.index + s.key);
 #pragma unroll
   for (int u = 0; u < kParts; ++u) {
     const long long i = first + u * kStride;
@@ -368,7 +372,7 @@ __device__ __forceinline__ void step_chunk(const Entry& t, uint32_t chunk, const
     for (int e = 0; e < 4; ++e) p[e] = fmaf(-(s.rate * m[e]), reciprocal(fmaf(r[e], s.over_root_c2, h.eps)), p[e] * keep);
     uint32_t hashes[4] = {0, 0, 0, 0};
     if (stochastic && (k8 || ptype == TRIMUL_BF16)) {
-      const uint32_t key = hash(t.key + static_cast<uint32_t>(i >> 32)) ^ static_cast<uint32_t>(i);
+      const uint32_t key = hash(tensor_key + static_cast<uint32_t>(i >> 32)) ^ static_cast<uint32_t>(i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) hashes[e] = hash(key ^ e);  // (i is a multiple of four)
     }
@@ -407,35 +411,36 @@ template <bool k8, int N>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(k8))
     k10_adamw(const __grid_constant__ Table<N> tab, const __grid_constant__ Hyper h, int* count, int last_launch) {
   let_next_begin();
-  const Step s = step_of(h, *static_cast<volatile int*>(count));
-  if (s.run) {
-    const uint32_t c0 = run_begin(tab.chunks, blockIdx.x, gridDim.x), c1 = run_begin(tab.chunks, blockIdx.x + 1, gridDim.x);
-    if (c0 < c1) {
-      int k = tab.begin[blockIdx.x];
-      Entry t = entry(tab, k, s);
-      uint32_t end = tab.chunk[k + 1];
-      for (uint32_t chunk = c0; chunk < c1; ++chunk) {
-        if (chunk >= end) {
-          t = entry(tab, ++k, s);
-          end = tab.chunk[k + 1];
-        }
-        // what most programs have gets code without questions about types
-        if (t.kind == kF32Copy)
-          step_chunk<k8, kF32Copy>(t, chunk, h, s);
-        else if (t.kind == kF32)
-          step_chunk<k8, kF32>(t, chunk, h, s);
-        else if (t.kind == kBf16)
-          step_chunk<k8, kBf16>(t, chunk, h, s);
-        else
-          step_chunk<k8, -1>(t, chunk, h, s);
+  Step s;
+  s.known = false;
+  const uint32_t c0 = run_begin(tab.chunks, blockIdx.x, gridDim.x), c1 = run_begin(tab.chunks, blockIdx.x + 1, gridDim.x);
+  if (c0 < c1) {
+    int k = tab.begin[blockIdx.x];
+    Entry t = entry(tab, k);
+    uint32_t end = tab.chunk[k + 1];
+    for (uint32_t chunk = c0; chunk < c1; ++chunk) {
+      if (chunk >= end) {
+        t = entry(tab, ++k);
+        end = tab.chunk[k + 1];
       }
+      // what most programs have gets code without questions about types
+      if (t.kind == kF32Copy)
+        step_chunk<k8, kF32Copy>(t, chunk, h, count, s);
+      else if (t.kind == kF32)
+        step_chunk<k8, kF32>(t, chunk, h, count, s);
+      else if (t.kind == kBf16)
+        step_chunk<k8, kBf16>(t, chunk, h, count, s);
+      else
+        step_chunk<k8, -1>(t, chunk, h, count, s);
+      if (!s.run) break;
     }
+  } else {
+    s = step_of(h, *static_cast<volatile int*>(count));
   }
   after_previous();
   if (!last_launch) return;
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
     if (atomicAdd(count + 1, 1) == static_cast<int>(gridDim.x) - 1) {
       count[1] = 0;
       if (s.run) count[0] += 1;
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(k8))
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 template <int N>
-int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int blocks) {
+int fill(Table<N>& tab, const trimul_adamw_tensor* t, const trimul_grad_tensor* g, int n, int& k, int blocks) {
   tab.n = 0;
   tab.chunks = 0;
   for (; k < n && tab.n < N; ++k) {
@@ -455,7 +460,7 @@ int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int blocks)
     const int q = tab.n++;
     tab.param[q] = t[k].param;
     tab.copy[q] = t[k].copy;
-    tab.grad[q] = t[k].grad;
+    tab.grad[q] = g[k].data;
     tab.m[q] = t[k].m;
     tab.v[q] = t[k].v;
     tab.m_scale[q] = t[k].m_scale;
@@ -465,8 +470,8 @@ int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int blocks)
     tab.index[q] = static_cast<uint32_t>(k);
     const int copy = !t[k].copy ? 0 : t[k].copy_type == TRIMUL_BF16 ? 1 : 2;
     const bool wide = aligned_to(t[k].param, t[k].param_type == TRIMUL_F32 ? 16 : 8) &&
-                      aligned_to(t[k].grad, t[k].grad_type == TRIMUL_F32 ? 16 : 8) && (!copy || aligned_to(t[k].copy, 8));
-    tab.kind[q] = static_cast<uint8_t>((t[k].param_type == TRIMUL_BF16 ? PARAM_BF16 : 0) | t[k].grad_type << GRAD_SHIFT |
+                      aligned_to(g[k].data, g[k].type == TRIMUL_F32 ? 16 : 8) && (!copy || aligned_to(t[k].copy, 8));
+    tab.kind[q] = static_cast<uint8_t>((t[k].param_type == TRIMUL_BF16 ? PARAM_BF16 : 0) | g[k].type << GRAD_SHIFT |
                                        copy << COPY_SHIFT | (wide ? WIDE : 0));
     tab.chunk[q] = tab.chunks;
     tab.chunks += static_cast<uint32_t>((t[k].numel + kChunk - 1) / kChunk);
@@ -484,11 +489,11 @@ int fill(Table<N>& tab, const trimul_adamw_tensor* t, int n, int& k, int blocks)
 }
 
 template <bool k8, int N>
-cudaError_t run(const Hyper& h, const trimul_adamw_tensor* t, int n, int32_t* count, int num_sms, cudaStream_t s) {
+cudaError_t run(const Hyper& h, const trimul_adamw_tensor* t, const trimul_grad_tensor* g, int n, int32_t* count, int num_sms, cudaStream_t s) {
   Table<N> tab;
   int k = 0;
   for (bool first = true; first || k < n; first = false) {
-    const int grid = fill(tab, t, n, k, blocks_per_sm(k8) * num_sms);
+    const int grid = fill(tab, t, g, n, k, blocks_per_sm(k8) * num_sms);
     cudaError_t e = cudaSuccess;
     if (first) {  // behind all that was before the call
       k10_adamw<k8, N><<<grid, kThreads, 0, s>>>(tab, h, count, k >= n);
@@ -503,8 +508,8 @@ cudaError_t run(const Hyper& h, const trimul_adamw_tensor* t, int n, int32_t* co
 
 }  // namespace
 
-cudaError_t launch_adamw(const trimul_adamw_params& p, const trimul_adamw_tensor* t, int n, int32_t* count, int num_sms,
-                         cudaStream_t s) {
+cudaError_t launch_adamw(const trimul_adamw_params& p, const trimul_adamw_tensor* t, const trimul_grad_tensor* g, int n, int32_t* count,
+                         int num_sms, cudaStream_t s) {
   Hyper h{};
   h.b1 = static_cast<float>(p.beta1), h.not_b1 = static_cast<float>(1.0 - p.beta1);
   h.b2 = static_cast<float>(p.beta2), h.not_b2 = static_cast<float>(1.0 - p.beta2);
@@ -513,8 +518,8 @@ cudaError_t launch_adamw(const trimul_adamw_params& p, const trimul_adamw_tensor
   h.norm = p.norm, h.max_norm = p.max_norm;
   h.seed = p.seed, h.stochastic = p.rounding == TRIMUL_ROUND_STOCHASTIC;
   if (p.states == TRIMUL_STATES_E4M3)
-    return n <= kTableSmall ? run<true, kTableSmall>(h, t, n, count, num_sms, s) : run<true, kTableMax>(h, t, n, count, num_sms, s);
-  return n <= kTableSmall ? run<false, kTableSmall>(h, t, n, count, num_sms, s) : run<false, kTableMax>(h, t, n, count, num_sms, s);
+    return n <= kTableSmall ? run<true, kTableSmall>(h, t, g, n, count, num_sms, s) : run<true, kTableMax>(h, t, g, n, count, num_sms, s);
+  return n <= kTableSmall ? run<false, kTableSmall>(h, t, g, n, count, num_sms, s) : run<false, kTableMax>(h, t, g, n, count, num_sms, s);
 }
 
 }  // namespace trimul

@@ -12,7 +12,7 @@
 namespace trimul {
 
 // ---------------------------------------------------------------- AdamW
-cudaError_t launch_adamw(const trimul_adamw_params& p, const trimul_adamw_tensor* t, int n, int32_t* count, int num_sms,
-                         cudaStream_t s);
+cudaError_t launch_adamw(const trimul_adamw_params& p, const trimul_adamw_tensor* t, const trimul_grad_tensor* g, int n, int32_t* count,
+                         int num_sms, cudaStream_t s);
 
 }  // namespace trimul

@@ -15,10 +15,11 @@ using namespace trimul;
 namespace {
 
 // ------------------------------------------------------------------ AdamW
-trimul_status check_adamw(const trimul_adamw_params* p, int n, const trimul_adamw_tensor* t, const int32_t* count) {
+trimul_status check_adamw(const trimul_adamw_params* p, int n, const trimul_adamw_tensor* t, const trimul_grad_tensor* g,
+                          const int32_t* count) {
   if (!p) return fail(TRIMUL_ERR_INVALID_ARG, "params is null");
   if (n < 0) return fail(TRIMUL_ERR_INVALID_ARG, "n (%d) must be >= 0", n);
-  if (n > 0 && !t) return fail(TRIMUL_ERR_INVALID_ARG, "tensors is null");
+  if (n > 0 && (!t || !g)) return fail(TRIMUL_ERR_INVALID_ARG, "tensors or grads is null");
   if (!(p->beta1 >= 0.0 && p->beta1 < 1.0) || !(p->beta2 >= 0.0 && p->beta2 < 1.0))
     return fail(TRIMUL_ERR_INVALID_ARG, "beta1 (%g) and beta2 (%g) must be in [0, 1)", p->beta1, p->beta2);
   if (!std::isnormal(p->eps) || p->eps < 0.0f) return fail(TRIMUL_ERR_INVALID_ARG, "eps must be a normal number > 0");
@@ -41,8 +42,10 @@ trimul_status check_adamw(const trimul_adamw_params* p, int n, const trimul_adam
       return fail(TRIMUL_ERR_SHAPE, "tensor %d: numel (%lld) is too large", k, static_cast<long long>(a.numel));
     if (a.param_type != TRIMUL_F32 && a.param_type != TRIMUL_BF16)
       return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: param_type must be BF16 or F32", k);
-    if (a.grad_type != TRIMUL_F32 && a.grad_type != TRIMUL_BF16 && a.grad_type != TRIMUL_F16)
-      return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: unknown grad_type %d", k, static_cast<int>(a.grad_type));
+    if (g[k].numel != a.numel)
+      return fail(TRIMUL_ERR_SHAPE, "tensor %d: its gradient has %lld elements, not %lld", k, static_cast<long long>(g[k].numel), static_cast<long long>(a.numel));
+    if (g[k].type != TRIMUL_F32 && g[k].type != TRIMUL_BF16 && g[k].type != TRIMUL_F16)
+      return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: unknown type %d of its gradient", k, static_cast<int>(g[k].type));
     if (a.copy && a.copy_type != TRIMUL_BF16 && a.copy_type != TRIMUL_F16)
       return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: copy_type must be BF16 or F16", k);
     if (!std::isfinite(a.weight_decay) || a.weight_decay < 0.0f)
@@ -52,7 +55,7 @@ trimul_status check_adamw(const trimul_adamw_params* p, int n, const trimul_adam
     const size_t scales = codes ? (num + TRIMUL_STATE_BLOCK - 1) / TRIMUL_STATE_BLOCK * 4 : 0;
     if (!a.param || !aligned(a.param, type_bytes(a.param_type)))
       return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: param is null or not aligned to its type", k);
-    if (!a.grad || !aligned(a.grad, type_bytes(a.grad_type)))
+    if (!g[k].data || !aligned(g[k].data, type_bytes(g[k].type)))
       return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: grad is null or not aligned to its type", k);
     if (!aligned(a.copy, 2)) return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: copy is not aligned to its type", k);
     if (!a.m || !a.v || !aligned(a.m, 16) || !aligned(a.v, 16))
@@ -62,13 +65,13 @@ trimul_status check_adamw(const trimul_adamw_params* p, int n, const trimul_adam
     const Buffer all_of[] = {{a.param, num * type_bytes(a.param_type), "param"}, {a.copy, num * 2, "copy"},
                              {a.m, state, "m"}, {a.v, state, "v"}, {codes ? a.m_scale : nullptr, scales, "m_scale"},
                              {codes ? a.v_scale : nullptr, scales, "v_scale"}, {count, 8, "count"},
-                             {a.grad, num * type_bytes(a.grad_type), "grad"}, {p->norm, 4, "norm"}, {p->lr_device, 4, "lr_device"}};
+                             {g[k].data, num * type_bytes(g[k].type), "grad"}, {p->norm, 4, "norm"}, {p->lr_device, 4, "lr_device"}};
     constexpr int kOutputs = 6;  // of these; what comes behind is read (count: seen to above)
     for (int x = 0; x < kOutputs; ++x)
       for (int y = x + 1; y < 10; ++y)
         if (overlap(all_of[x].p, all_of[x].bytes, all_of[y].p, all_of[y].bytes))
           return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: %s overlaps %s", k, all_of[x].name, all_of[y].name);
-    if (overlap(count, 8, a.grad, num * type_bytes(a.grad_type))) return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: count overlaps grad", k);
+    if (overlap(count, 8, g[k].data, num * type_bytes(g[k].type))) return fail(TRIMUL_ERR_INVALID_ARG, "tensor %d: count overlaps grad", k);
   }
   return TRIMUL_OK;
 }
@@ -77,16 +80,16 @@ trimul_status check_adamw(const trimul_adamw_params* p, int n, const trimul_adam
 
 extern "C" {
 
-trimul_status trimul_adamw_step(const trimul_adamw_params* p, const trimul_adamw_tensor* tensors, int n, int32_t* count,
-                                int device, void* stream, unsigned flags) {
+trimul_status trimul_adamw_step(const trimul_adamw_params* p, const trimul_adamw_tensor* tensors, const trimul_grad_tensor* grads,
+                                int n, int32_t* count, int device, void* stream, unsigned flags) {
   TRY(check_flags(flags, TRIMUL_FLAG_CHECK));
-  TRY(check_adamw(p, n, tensors, count));
+  TRY(check_adamw(p, n, tensors, grads, count));
   int sms = 0;
   TRY(device_sms(device, &sms));
   DeviceScope scope;
   TRY(scope.enter(device));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return finish(launch_adamw(*p, tensors, n, count, sms, s), s, flags, "AdamW launch");
+  return finish(launch_adamw(*p, tensors, grads, n, count, sms, s), s, flags, "AdamW launch");
 }
 
 }  // extern "C"

@@ -83,11 +83,11 @@ class AdamW:
         self.state = {k: torch.zeros(total, dtype=kind, device=dev) for k in "mv"}
         if self.eight:
             self.state.update({k + "_scale": torch.zeros(total // BLOCK, dtype=torch.float32, device=dev) for k in "mv"})
-        self.state["count"] = self._count[0]
+        self.state["count"], self._count_at = self._count[0], self._count.data_ptr()
         # one row of numbers for each tensor, as _lib.AdamwTensor lays them out
-        rows = np.zeros(n, dtype=np.dtype([("param", "<i8"), ("copy", "<i8"), ("grad", "<i8"), ("m", "<i8"), ("v", "<i8"),
+        rows = np.zeros(n, dtype=np.dtype([("param", "<i8"), ("copy", "<i8"), ("m", "<i8"), ("v", "<i8"),
                                            ("m_scale", "<i8"), ("v_scale", "<i8"), ("numel", "<i8"), ("weight_decay", "<f4"),
-                                           ("param_type", "<i4"), ("copy_type", "<i4"), ("grad_type", "<i4")]))
+                                           ("param_type", "<i4"), ("copy_type", "<i4")], align=True))
         rows["param"] = [p.data_ptr() for p in params]
         rows["copy"] = [0 if c is None else c.data_ptr() for c in copies]
         rows["numel"], rows["weight_decay"] = numel, decay
@@ -102,7 +102,6 @@ class AdamW:
         if both:
             names = [f"{'params' if k < n else 'copies'}[{k % n}]" for k in both]
             raise ValueError(f"{names[1]} overlaps {names[0]}")
-        self._rows = rows
         self.table = (_lib.AdamwTensor * n).from_buffer(rows) if n else (_lib.AdamwTensor * 0)()
         self._p = _lib.AdamwParams(beta1=betas[0], beta2=betas[1], eps=eps, lr=0.0, states=int(self.eight),
                                    rounding=_one_of(_ROUNDING, rounding, "rounding"), seed=seed & 0xFFFFFFFF)
@@ -115,17 +114,11 @@ class AdamW:
         finite makes the step nothing."""
         if not isinstance(grads, GradSet):
             grads = GradSet(grads)
-        rows, p = self._rows, self._p
-        if len(grads.tensors) != len(rows):
-            raise ValueError(f"{len(grads.tensors)} grads for {len(rows)} params")
-        if len(rows):
-            data, _, numel, kinds = grads._rows.T
-            if not np.array_equal(numel, rows["numel"]):
-                k = int(np.flatnonzero(numel != rows["numel"])[0])
-                raise ValueError(f"grads[{k}] must be {tuple(self.params[k].shape)}, got {tuple(grads.tensors[k].shape)}")
-            if grads.device != self.device:
-                raise ValueError(f"grads must be on cuda:{self.device}, got cuda:{grads.device}")
-            rows["grad"], rows["grad_type"] = data, kinds
+        p = self._p
+        if len(grads.table) != len(self.table):
+            raise ValueError(f"{len(grads.table)} grads for {len(self.table)} params")
+        if grads.device != self.device and len(self.table):
+            raise ValueError(f"grads must be on cuda:{self.device}, got cuda:{grads.device}")
         if lr is not None:
             self.lr = lr
         if (norm is None) != (max_norm is None):
@@ -135,7 +128,7 @@ class AdamW:
             p.lr, p.lr_device = 0.0, self._one(self.lr, "lr")
         else:
             p.lr, p.lr_device = self.lr, None
-        _check(_lib.load().trimul_adamw_step(p, self.table, len(rows), self._count.data_ptr(), self.device,
+        _check(_lib.load().trimul_adamw_step(p, self.table, grads.table, len(self.table), self._count_at, self.device,
                                              _raw(stream, self.device), flags))
 
     def _one(self, t, name):
@@ -177,17 +170,20 @@ def trimul_linear8_pack(weight, packed=None, stream=None, flags: int = 0):
 
 def trimul_linear8_forward(packed, N, K, x, bias=None, out=None, stream=None, flags: int = 0):
     """x W^T + bias: bf16 [..., N] for bf16 x [..., K]; bias: float32 [N]."""
-    dev = _cuda(packed, "packed")
-    lib = _lib.load()
-    _packed(lib, packed, N, K, dev)
-    rows = _rows(x, K, dev, "x")
+    dev = _packed(packed, N, K)
     if bias is not None and not _fits(bias, torch.float32, (N,), dev):
         _refuse(bias, torch.float32, (N,), dev, "bias")
+    return _forward(packed, N, K, dev, x, bias, out, stream, flags)
+
+
+def _forward(packed, N, K, dev, x, bias, out, stream, flags):  # packed and bias have been looked at
+    rows = _rows(x, K, dev, "x")
     shape = (*x.shape[:-1], N)
     if out is None:
         out = _empty(shape, torch.bfloat16, x.device, stream)
     elif not _fits(out, torch.bfloat16, shape, dev):
         _refuse(out, torch.bfloat16, shape, dev, "out")
+    lib = _lib.load()
     need = lib.trimul_linear8_forward_workspace_bytes(rows, N, K)
     ws = _empty(need, torch.uint8, x.device, stream)
     _check(lib.trimul_linear8_forward(packed.data_ptr(), _ptr(bias), x.data_ptr(), rows, N, K, out.data_ptr(), ws.data_ptr(), need,
@@ -199,9 +195,10 @@ def trimul_linear8_backward(packed, N, K, x, dy, dx=None, dw=None, dbias=None, w
                             flags: int = 0):
     """{"dx", "dw", "dbias"} for dy (bf16 [..., N]) with respect to the output: bf16 like x, float32 [N, K] and [N]; those that
     `want` does not name are None."""
-    dev = _cuda(packed, "packed")
-    lib = _lib.load()
-    _packed(lib, packed, N, K, dev)
+    return _backward(packed, N, K, _packed(packed, N, K), x, dy, dx, dw, dbias, want, stream, flags)
+
+
+def _backward(packed, N, K, dev, x, dy, dx, dw, dbias, want, stream, flags):  # packed has been looked at
     rows = _rows(x, K, dev, "x")
     if _rows(dy, N, dev, "dy") != rows or dy.shape[:-1] != x.shape[:-1]:
         raise ValueError(f"dy must be {(*x.shape[:-1], N)}, got {tuple(dy.shape)}")
@@ -218,6 +215,7 @@ def trimul_linear8_backward(packed, N, K, x, dy, dx=None, dw=None, dbias=None, w
             if not _fits(t, dtype, shape, dev):
                 _refuse(t, dtype, shape, dev, name)
             got[name] = t
+    lib = _lib.load()
     need = lib.trimul_linear8_backward_workspace_bytes(rows, N, K)
     ws = _empty(need, torch.uint8, x.device, stream)
     _check(lib.trimul_linear8_backward(packed.data_ptr(), x.data_ptr(), dy.data_ptr(), rows, N, K, _ptr(got["dx"]), _ptr(got["dw"]),
@@ -225,12 +223,15 @@ def trimul_linear8_backward(packed, N, K, x, dy, dx=None, dw=None, dbias=None, w
     return got
 
 
-def _packed(lib, packed, N, K, dev):
-    need = lib.trimul_linear8_packed_bytes(N, K)
+def _packed(packed, N, K) -> int:
+    """The device of a packed weight of these sizes."""
+    dev = _cuda(packed, "packed")
+    need = _lib.load().trimul_linear8_packed_bytes(N, K)
     if need == 0:
         raise ValueError(f"N ({N}) and K ({K}) must be multiples of 8 in [8, 65536]")
     if not _fits(packed, torch.uint8, (need,), dev):
         _refuse(packed, torch.uint8, (need,), dev, "packed")
+    return dev
 
 
 class Linear8:
@@ -243,9 +244,10 @@ class Linear8:
     def __init__(self, weight, bias=None):
         self.packed = trimul_linear8_pack(weight)
         self.N, self.K = weight.shape
+        self.device = weight.get_device()
+        if bias is not None and not _fits(bias, torch.float32, (self.N,), self.device):
+            _refuse(bias, torch.float32, (self.N,), self.device, "bias")
         self.bias = bias
-        if bias is not None and not _fits(bias, torch.float32, (self.N,), weight.get_device()):
-            _refuse(bias, torch.float32, (self.N,), weight.get_device(), "bias")
 
     def pack(self, weight, stream=None, flags: int = 0):
         if tuple(weight.shape) != (self.N, self.K):
@@ -253,7 +255,7 @@ class Linear8:
         trimul_linear8_pack(weight, self.packed, stream, flags)
 
     def forward(self, x, out=None, stream=None, flags: int = 0):
-        return trimul_linear8_forward(self.packed, self.N, self.K, x, self.bias, out, stream, flags)
+        return _forward(self.packed, self.N, self.K, self.device, x, self.bias, out, stream, flags)
 
     __call__ = forward
 
@@ -261,4 +263,4 @@ class Linear8:
         """{"dx", "dw", "dbias"}; dbias is None for a layer without bias, and what `want` does not name."""
         if want is None:
             want = ("dx", "dw", "dbias") if self.bias is not None else ("dx", "dw")
-        return trimul_linear8_backward(self.packed, self.N, self.K, x, dy, dx, dw, dbias, want, stream, flags)
+        return _backward(self.packed, self.N, self.K, self.device, x, dy, dx, dw, dbias, want, stream, flags)

@@ -567,7 +567,6 @@ typedef enum { TRIMUL_ROUND_NEAREST = 0, TRIMUL_ROUND_STOCHASTIC = 1 } trimul_ro
 typedef struct {
   void* param;                      /* DEVICE, F32 or BF16, aligned to its element, overwritten */
   void* copy;                       /* the new value rounded to nearest, BF16 or F16; NULL: not wanted */
-  const void* grad;                 /* F32, BF16 or F16 */
   void* m;                          /* 16-byte aligned: f32 [numel], or e4m3 codes [numel] */
   void* v;                          /* likewise: v as f32, or the codes of its root */
   float* m_scale;                   /* E4M3: f32 [ceil(numel / 128)], 4-byte aligned; F32: not looked at */
@@ -576,7 +575,6 @@ typedef struct {
   float weight_decay;               /* finite, >= 0 */
   trimul_dtype param_type;
   trimul_dtype copy_type;
-  trimul_dtype grad_type;
 } trimul_adamw_tensor;
 
 typedef struct {
@@ -592,12 +590,13 @@ typedef struct {
 } trimul_adamw_params;
 
 /*
- * `tensors` and `p` are HOST memory, read during the call.  count: DEVICE int32[2], the steps taken so far (the call adds
+ * grads: the gradients in the same order, as trimul_grad_norm takes them (`out` is not looked at), of the tensors' sizes.
+ * `p`, `tensors` and `grads` are HOST memory, read during the call.  count: DEVICE int32[2], the steps taken so far (the call adds
  * one) and a word for the kernels, 0 at first and between calls; steps of one count are ordered by the caller.  No output (param, copy,
- * states, count) may overlap anything else; within one entry of `tensors` that is checked, between two it is not.
+ * states, count) may overlap anything else; within one tensor and its gradient that is checked, between two it is not.
  */
-trimul_status trimul_adamw_step(const trimul_adamw_params* p, const trimul_adamw_tensor* tensors, int n, int32_t* count,
-                                int device, void* stream, unsigned flags);
+trimul_status trimul_adamw_step(const trimul_adamw_params* p, const trimul_adamw_tensor* tensors, const trimul_grad_tensor* grads,
+                                int n, int32_t* count, int device, void* stream, unsigned flags);
 
 /* ---------------------------------------------------------------- linear layer in 8 bits
  * y = x W^T + bias over rows of K channels (a transition's projections), and its

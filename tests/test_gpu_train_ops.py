@@ -372,7 +372,7 @@ def test_adamw_refusals(P, R):
     opt = P.AdamW([x])
     with pytest.raises(ValueError, match="2 grads for 1 params"):
         opt.step([y, y])
-    with pytest.raises(ValueError, match=r"grads\[0\] must be"):
+    with pytest.raises(Exception, match="its gradient has 8 elements, not 64"):
         opt.step([y[:8]])
     with pytest.raises(ValueError, match="both norm and max_norm"):
         opt.step([y], norm=torch.ones((), device="cuda"))

@@ -17,29 +17,30 @@ def refused(lib, status, want, text):
     assert text in lib.trimul_last_error().decode()
 
 
-TENSOR = {"param": A, "grad": 2 * A, "m": 3 * A, "v": 4 * A, "m_scale": 5 * A, "v_scale": 6 * A, "numel": 256, "param_type": 1,
-          "grad_type": 1}
+TENSOR = {"param": A, "m": 3 * A, "v": 4 * A, "m_scale": 5 * A, "v_scale": 6 * A, "numel": 256, "param_type": 1}
+GRAD = {"data": 2 * A, "numel": 256, "type": 1}
 PARAMS = {"beta1": 0.9, "beta2": 0.999, "eps": 1e-8, "lr": 1e-3, "states": 1}
 
 
 @pytest.mark.parametrize("tensor,params,call,want,text", [
-    ({"numel": -1}, {}, {}, SHAPE, "numel (-1)"),
-    ({"numel": 1 << 40}, {}, {}, SHAPE, "too large"),
+    ({"numel": -1}, {}, {"grad": {"numel": -1}}, SHAPE, "numel (-1)"),
+    ({"numel": 1 << 40}, {}, {"grad": {"numel": 1 << 40}}, SHAPE, "too large"),
     ({"param_type": 2}, {}, {}, INVALID, "param_type must be"),
-    ({"grad_type": 3}, {}, {}, INVALID, "unknown grad_type 3"),
+    ({}, {}, {"grad": {"type": 3}}, INVALID, "unknown type 3 of its gradient"),
+    ({}, {}, {"grad": {"numel": 255}}, SHAPE, "its gradient has 255 elements, not 256"),
     ({"copy": 7 * A, "copy_type": 1}, {}, {}, INVALID, "copy_type must be"),
     ({"weight_decay": -0.1}, {}, {}, INVALID, "weight_decay"),
     ({"weight_decay": float("nan")}, {}, {}, INVALID, "weight_decay"),
     ({"param": None}, {}, {}, INVALID, "param is null"),
     ({"param": A + 2}, {}, {}, INVALID, "param is null or not aligned"),
-    ({"grad": None}, {}, {}, INVALID, "grad is null"),
-    ({"grad": 2 * A + 1, "grad_type": 0}, {}, {}, INVALID, "grad is null or not aligned"),
+    ({}, {}, {"grad": {"data": None}}, INVALID, "grad is null"),
+    ({}, {}, {"grad": {"data": 2 * A + 1, "type": 0}}, INVALID, "grad is null or not aligned"),
     ({"copy": 7 * A + 1}, {}, {}, INVALID, "copy is not aligned"),
     ({"m": 3 * A + 8}, {}, {}, INVALID, "m or v is null"),
     ({"v": None}, {}, {}, INVALID, "m or v is null"),
     ({"m_scale": None}, {}, {}, INVALID, "m_scale or v_scale is null"),
     ({"v_scale": 6 * A + 2}, {}, {}, INVALID, "m_scale or v_scale is null"),
-    ({"grad": A + 512}, {}, {}, INVALID, "param overlaps grad"),
+    ({}, {}, {"grad": {"data": A + 512}}, INVALID, "param overlaps grad"),
     ({"v": 3 * A + 128}, {}, {}, INVALID, "m overlaps v"),
     ({"v_scale": 5 * A + 4}, {}, {}, INVALID, "m_scale overlaps v_scale"),
     ({"copy": A + 1000}, {}, {}, INVALID, "param overlaps copy"),
@@ -47,7 +48,7 @@ PARAMS = {"beta1": 0.9, "beta2": 0.999, "eps": 1e-8, "lr": 1e-3, "states": 1}
     ({}, {"norm": A + 4}, {}, INVALID, "param overlaps norm"),
     ({}, {"lr_device": 4 * A}, {}, INVALID, "v overlaps lr_device"),
     ({}, {"norm": 8 * A + 4}, {}, INVALID, "count overlaps"),
-    ({"grad": 8 * A}, {}, {}, INVALID, "count overlaps grad"),
+    ({}, {}, {"grad": {"data": 8 * A}}, INVALID, "count overlaps grad"),
     ({}, {"beta1": 1.0}, {}, INVALID, "beta1"),
     ({}, {"beta2": -0.1}, {}, INVALID, "beta1"),
     ({}, {"beta2": float("nan")}, {}, INVALID, "beta1"),
@@ -65,14 +66,15 @@ PARAMS = {"beta1": 0.9, "beta2": 0.999, "eps": 1e-8, "lr": 1e-3, "states": 1}
 def test_adamw_refused(lib, tensor, params, call, want, text):
     t = (_lib.AdamwTensor * 1)(_lib.AdamwTensor(**{**TENSOR, **tensor}))
     p = _lib.AdamwParams(**{**PARAMS, **params})
-    c = {"n": 1, "count": 8 * A, "flags": 0, **call}
-    refused(lib, lib.trimul_adamw_step(ctypes.byref(p), t, c["n"], c["count"], 0, None, c["flags"]), want, text)
+    c = {"n": 1, "count": 8 * A, "flags": 0, "grad": {}, **call}
+    g = (_lib.GradTensor * 1)(_lib.GradTensor(**{**GRAD, **c["grad"]}))
+    refused(lib, lib.trimul_adamw_step(ctypes.byref(p), t, g, c["n"], c["count"], 0, None, c["flags"]), want, text)
 
 
 def test_adamw_null_arguments(lib):
     p = _lib.AdamwParams(**PARAMS)
-    refused(lib, lib.trimul_adamw_step(None, None, 0, A, 0, None, 0), INVALID, "params is null")
-    refused(lib, lib.trimul_adamw_step(ctypes.byref(p), None, 1, A, 0, None, 0), INVALID, "tensors is null")
+    refused(lib, lib.trimul_adamw_step(None, None, None, 0, A, 0, None, 0), INVALID, "params is null")
+    refused(lib, lib.trimul_adamw_step(ctypes.byref(p), None, None, 1, A, 0, None, 0), INVALID, "tensors or grads is null")
 
 
 def test_binding_refusals():
