@@ -69,36 +69,48 @@ __device__ __forceinline__ void transpose8(uint4 (&R)[8], uint32_t gb) {
   }
 }
 
-// One accumulation: blocks [b0, b1) of a tile.  A pair's tiles, each with its
-// accumulations, in turn; all warps walk them alike.
+// One accumulation: blocks [b0, b1) of a tile.  A pair takes runs of p.run tiles
+// beside one another, each tile with its accumulations, in turn; all warps walk them alike.
 struct Walk {
   const Gemm8Args& p;
-  long long tile, step, total;
-  int z, tm, tn, b0, b1, z_end;
-  __device__ __forceinline__ Walk(const Gemm8Args& a, int first, int pairs)
-      : p(a), tile(first), step(pairs), total(static_cast<long long>(a.tiles_m) * a.tiles_n * a.n_z) {
+  uint32_t at, step, total;  // of runs: fewer than 2^31, for rows and columns below 2^31 and 2^16
+  int runs, z, tm, tn, tn_end, b0, b1, z_end;
+  __device__ __forceinline__ Walk(const Gemm8Args& a, uint32_t first, uint32_t pairs)
+      : p(a), at(first), step(pairs), runs((a.tiles_n + a.run - 1) / a.run) {
+    total = static_cast<uint32_t>(a.tiles_m) * runs * a.n_z;
     if (more()) begin();
   }
-  __device__ __forceinline__ bool more() const { return tile < total; }
+  __device__ __forceinline__ bool more() const { return at < total; }
   __device__ __forceinline__ void begin() {
-    const long long per_z = static_cast<long long>(p.tiles_m) * p.tiles_n;
-    z = static_cast<int>(tile / per_z);
-    const int rem = static_cast<int>(tile - z * per_z);
-    tm = rem / p.tiles_n, tn = rem - tm * p.tiles_n;
+    const uint32_t per_z = static_cast<uint32_t>(p.tiles_m) * runs;
+    z = static_cast<int>(at / per_z);
+    const uint32_t rem = at - z * per_z;
+    tm = static_cast<int>(rem / runs), tn = static_cast<int>(rem - tm * runs) * p.run;
+    tn_end = min(tn + p.run, p.tiles_n);
+    z_end = min((z + 1) * p.per_z, p.blocks);
+    begin_tile();
+  }
+  __device__ __forceinline__ void begin_tile() {
     b0 = z * p.per_z;
-    z_end = min(b0 + p.per_z, p.blocks);
     b1 = min(b0 + p.chunk, z_end);
   }
   __device__ __forceinline__ bool first() const { return b0 == z * p.per_z; }
   __device__ __forceinline__ bool last() const { return b1 == z_end; }
+  __device__ __forceinline__ bool last_tile() const { return tn + 1 == tn_end; }
   __device__ __forceinline__ void next() {
     if (!last()) {
       b0 = b1;
       b1 = min(b0 + p.chunk, z_end);
+    } else if (!last_tile()) {
+      ++tn;
+      begin_tile();
     } else {
-      tile += step;
-      if (more()) begin();
+      next_run();
     }
+  }
+  __device__ __forceinline__ void next_run() {
+    at += step;
+    if (more()) begin();
   }
 };
 }  // namespace trimul

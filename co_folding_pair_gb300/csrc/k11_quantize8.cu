@@ -251,25 +251,28 @@ __global__ void __launch_bounds__(kThreads) k11_weight(const T* __restrict__ w, 
 }
 
 // ------------------------------------------------------------------ sums of slices
-// A thread block has 32 sums, eight threads each: a thread adds every eighth slice,
-// and the eight are added in order.  (With a thread for each sum the loads of a hundred
-// slices came one after the other: 13 us for 512 sums.)
-constexpr int kJoinThreads = 8;
+// kEach threads a sum: each adds every kEach-th slice, and they are added in order.
+// Few sums of many slices take eight (with one, the loads of a hundred slices come one after the other: 13 us for
+// 512 sums, 5.4 with eight); many take one (262144 sums of 76 slices: 8 us, with eight 18.6).
+template <int kEach>
 __global__ void __launch_bounds__(kThreads) k11_join(const float* __restrict__ part, int n_z, long long n, int cols, float* __restrict__ out) {
-  __shared__ float sums[kJoinThreads][32];
-  const int lane = threadIdx.x % 32, q = threadIdx.x / 32;
-  const long long i = static_cast<long long>(blockIdx.x) * 32 + lane;
+  constexpr int kSums = kThreads / kEach;
+  __shared__ float sums[kEach][kSums];
+  const int lane = threadIdx.x % kSums, q = threadIdx.x / kSums;
+  const long long i = static_cast<long long>(blockIdx.x) * kSums + lane;
   float s = 0.f;
   if (i < n) {
-#pragma unroll 4
-    for (int z = q; z < n_z; z += kJoinThreads) s += part[z * n + i];
+#pragma unroll 8
+    for (int z = q; z < n_z; z += kEach) s += part[z * n + i];
   }
-  sums[q][lane] = s;
-  __syncthreads();
-  if (q != 0 || i >= n) return;
+  if (kEach > 1) {
+    sums[q][lane] = s;
+    __syncthreads();
+    if (q != 0) return;
 #pragma unroll
-  for (int k = 1; k < kJoinThreads; ++k) s += sums[k][lane];
-  out[cols ? i % cols * (n / cols) + i / cols : i] = s;
+    for (int k = 1; k < kEach; ++k) s += sums[k][lane];
+  }
+  if (i < n) out[cols ? i % cols * (n / cols) + i / cols : i] = s;
 }
 
 }  // namespace
@@ -315,7 +318,10 @@ cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_
 }
 
 cudaError_t launch_join(const float* part, int n_z, long long n, int cols, float* out, cudaStream_t s) {
-  k11_join<<<static_cast<unsigned>((n + 31) / 32), kThreads, 0, s>>>(part, n_z, n, cols, out);
+  if (n < 16384)
+    k11_join<8><<<static_cast<unsigned>((n + 31) / 32), kThreads, 0, s>>>(part, n_z, n, cols, out);
+  else
+    k11_join<1><<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(part, n_z, n, cols, out);
   return cudaGetLastError();
 }
 

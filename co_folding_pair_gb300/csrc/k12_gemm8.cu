@@ -96,7 +96,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot_ptr;
-  Walk w(p, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1));
+  Walk w(p, blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)

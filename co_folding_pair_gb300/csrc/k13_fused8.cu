@@ -39,10 +39,10 @@ namespace trimul {
 
 namespace {
 constexpr int ROWS = 128;
-constexpr int STAGES = 3, RAW_SLOTS = 2;
+constexpr int A_SLOTS = 3, B_STAGES = 3, RAW_SLOTS = 2;
+static_assert(A_SLOTS == B_STAGES && FUSED8_RUN_BLOCKS <= A_SLOTS, "a run's codes wait in their slots");
 constexpr uint32_t CODE_BYTES = ROWS * L8_BLOCK;
-constexpr uint32_t A_SCALES = 3 * CODE_BYTES, B_SCALES = A_SCALES + L8_SCALE_TILE;  // 128 rows of A, 256 of B
-constexpr uint32_t STAGE_BYTES = 50 * 1024;
+constexpr uint32_t B_BYTES = 2 * CODE_BYTES;  // 256 rows of B
 constexpr uint32_t RAW_HALF = 128 * 128, RAW_BYTES = 2 * RAW_HALF;  // 128 rows of 64 bf16 numbers, twice
 constexpr uint32_t BAR_BYTES = 512;
 constexpr uint32_t TOPS_BYTES = 2 * 8 * 16 * 16;  // by columns: the largest magnitudes that each warp of a team has found
@@ -50,10 +50,18 @@ constexpr uint32_t TMEM_COLS = 512, ACC_STEP = 192;
 constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 3;
 constexpr int EPI_WARPS = 8, TEAMS = 2, TEAM_WARPS = 8, ROUND_WARPS = TEAMS * TEAM_WARPS;
 constexpr int EPI0 = 2, ROUND0 = EPI0 + EPI_WARPS, RAW = ROUND0 + ROUND_WARPS, THREADS = 32 * (RAW + 1);
-static_assert(A_SETS > STAGES + 1, "a set's readers are done when it is written again");
+// A team waits for its own blocks alone.  A wait that has skipped a use of its barrier would take the phase before for the one it
+// wants, and pass at once.  So a slot of t is always the same team's.  With three slots of codes a team comes to a slot every
+// second use; what it skipped (the multiplications of the block six before its own) was done when it was last let on, by those of the block five before.
+static_assert(RAW_SLOTS % TEAMS == 0, "a slot of t is always the same team's");
+static_assert(TEAMS == 2 && (A_SLOTS == 3 || A_SLOTS % 2 == 0), "a team knows its slot's phase");
+static_assert(A_SETS > B_STAGES + 1 && B_STAGES <= 3, "a set's readers are done when it is written again");
 static_assert(A_COLS + 4 * A_SETS <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
-constexpr uint32_t RAW0 = STAGES * STAGE_BYTES, BARS = RAW0 + RAW_SLOTS * RAW_BYTES;
+// rings: A's codes, B's codes, tiles of t, A's and B's scales
+constexpr uint32_t B0 = A_SLOTS * CODE_BYTES, RAW0 = B0 + B_STAGES * B_BYTES, AS0 = RAW0 + RAW_SLOTS * RAW_BYTES;
+constexpr uint32_t BS0 = AS0 + A_SLOTS * L8_SCALE_TILE, BARS = BS0 + B_STAGES * 2 * L8_SCALE_TILE;
 constexpr size_t kSmem = 1024 + BARS + BAR_BYTES + TOPS_BYTES;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
 constexpr uint32_t SITE_ROUND = 0x500;
 constexpr uint32_t kIdesc128 = (kIdesc8 & ~(0x1Fu << 24)) | ((ROWS >> 4) << 24);
 
@@ -218,7 +226,9 @@ __device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uin
 }
 }  // namespace
 
-template <bool kCols>
+// kRuns (by rows only): a run's tiles take the same codes of A, which wait in their slots until the last tile has had them.
+// Else a slot of A's codes goes with a stage of B's, and is free when that is.
+template <bool kCols, bool kRuns>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_b_scale, const Fused8Args p) {
@@ -227,10 +237,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
   const uint32_t bars = base + BARS;
-  // bfull[STAGES] afull[STAGES] empty[STAGES] rfull[RAW_SLOTS] rempty[RAW_SLOTS] tfull[2] tempty[2] over drain, then the TMEM
-  // base word
-  const uint32_t bfull0 = bars, afull0 = bfull0 + 8 * STAGES, empty0 = afull0 + 8 * STAGES;
-  const uint32_t rfull0 = empty0 + 8 * STAGES, rempty0 = rfull0 + 8 * RAW_SLOTS;
+  // bfull bempty [B_STAGES] afull aempty [A_SLOTS] rfull rempty [RAW_SLOTS] tfull tempty [2] over drain, then the TMEM base word
+  const uint32_t bfull0 = bars, bempty0 = bfull0 + 8 * B_STAGES, afull0 = bempty0 + 8 * B_STAGES, aempty0 = kRuns ? afull0 + 8 * A_SLOTS : bempty0;
+  const uint32_t rfull0 = afull0 + 16 * A_SLOTS, rempty0 = rfull0 + 8 * RAW_SLOTS;
   const uint32_t tfull0 = rempty0 + 8 * RAW_SLOTS, tempty0 = tfull0 + 16, over = tempty0 + 16, drain = over + 8;
   const uint32_t tmem_slot = drain + 8;
   volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base));
@@ -244,10 +253,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // than a millisecond into a wait
   if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.g.status = 0;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < B_STAGES; ++s) {
       mbar_init(bfull0 + 8 * s, 1);            // one expect_tx arrival; bytes that both CTAs load
+      mbar_init(bempty0 + 8 * s, 2);           // one commit of each CTA: B's tile is written for both
+    }
+    for (int s = 0; s < A_SLOTS; ++s) {
       mbar_init(afull0 + 8 * s, TEAM_WARPS);
-      mbar_init(empty0 + 8 * s, 2);            // one commit of each CTA: B's tile is written for both
+      if (kRuns) mbar_init(aempty0 + 8 * s, 1);  // one commit
     }
     for (int r = 0; r < RAW_SLOTS; ++r) {
       mbar_init(rfull0 + 8 * r, 1);  // one expect_tx arrival
@@ -269,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot_ptr;
-  Walk w(p.g, static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1));
+  Walk w(p.g, blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer of B: this CTA's half, for both
@@ -285,19 +297,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int bt = w.tn * 2 + static_cast<int>(rank);
         const int rb = bt < b_tiles ? bt * ROWS : 0;  // (a box wholly past N loads row 0)
         for (int b = w.b0; b < w.b1; ++b) {
-          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, st, SITE_PRODUCER)) {
+          if (!mbar_wait(bempty0 + 8 * stage, phase ^ 1u, st, SITE_PRODUCER)) {
             ok = false;
             break;
           }
-          const uint32_t sa = base + stage * STAGE_BYTES;
           const uint32_t fb = bfull0 + 8 * stage;
           const bool scales = b % 4 == 0 || b == w.b0;
           mbar_arrive_expect_tx(fb, 2 * (CODE_BYTES + (scales ? L8_SCALE_TILE : 0)));
           const int d = b * L8_BLOCK;
-          tma_load_2d_both(sa + CODE_BYTES * (1 + rank), &tm_b, fb, p.g.b_mn ? rb : d, p.g.b_mn ? d : rb);
-          if (scales) tma_load_2d_both(sa + B_SCALES + rank * L8_SCALE_TILE, &tm_b_scale, fb, 0, (bt < b_tiles ? bt : 0) * groups + b / 4);
+          tma_load_2d_both(base + B0 + stage * B_BYTES + rank * CODE_BYTES, &tm_b, fb, p.g.b_mn ? rb : d, p.g.b_mn ? d : rb);
+          if (scales)
+            tma_load_2d_both(base + BS0 + (2 * stage + rank) * L8_SCALE_TILE, &tm_b_scale, fb, 0, (bt < b_tiles ? bt : 0) * groups + b / 4);
           ++issued;
-          if (++stage == STAGES) {
+          if (++stage == B_STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -306,9 +318,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!ok) {  // the copies on their way land before the CTA goes away
         int s = stage;
         uint32_t ph = phase;
-        for (long long i = 0; i < issued && i < STAGES; ++i) {
+        for (long long i = 0; i < issued && i < B_STAGES; ++i) {
           if (--s < 0) {
-            s = STAGES - 1;
+            s = B_STAGES - 1;
             ph ^= 1u;
           }
           mbar_wait_drain(bfull0 + 8 * s, ph, p.g.timeout_ns);
@@ -319,12 +331,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint64_t adesc0 = sdesc_sw128(base, kCols ? CODE_BYTES : 16, 1024);
-      const uint64_t bdesc0 = sdesc_sw128(base + CODE_BYTES, p.g.b_mn ? CODE_BYTES : 16, 1024);
-      const uint64_t as0 = sdesc_scales(base + A_SCALES), bs0 = sdesc_scales(base + B_SCALES);
+      const uint64_t bdesc0 = sdesc_sw128(base + B0, p.g.b_mn ? CODE_BYTES : 16, 1024);
+      const uint64_t as0 = sdesc_scales(base + AS0), bs0 = sdesc_scales(base + BS0);
       const uint32_t astep = kCols ? 32 * 128 >> 4 : 32 >> 4, bstep = p.g.b_mn ? 32 * 128 >> 4 : 32 >> 4;
       const uint32_t majors = static_cast<uint32_t>(kCols) << 15 | static_cast<uint32_t>(p.g.b_mn) << 16;
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, aphase = 0, ophase = 1, a_set = 0, b_set = 0;
+      int stage = 0, acc = 0, slot = 0, run_slot = 0;
+      uint32_t phase = 0, sphase = 0, run_phase = 0, aphase = 0, ophase = 1, a_set = 0, b_set = 0;
       bool ok = true;
       for (; w.more() && ok; w.next()) {
         if (!mbar_wait(tempty0 + 8 * acc, aphase ^ 1u, st, SITE_MMA) || !mbar_wait(over, ophase, st, SITE_MMA)) {
@@ -335,35 +347,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * ACC_STEP;
         uint32_t sfb = 0;
+        if (kRuns) slot = run_slot, sphase = run_phase;  // each tile of a run begins at its first slot
+        const bool give_back = kRuns && w.last_tile();
         for (int b = w.b0; b < w.b1; ++b) {
-          if (!mbar_wait(bfull0 + 8 * stage, phase, st, SITE_MMA) || !mbar_wait(afull0 + 8 * stage, phase, st, SITE_MMA)) {
+          if (!mbar_wait(bfull0 + 8 * stage, phase, st, SITE_MMA) || !mbar_wait(afull0 + 8 * slot, sphase, st, SITE_MMA)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t soff = (stage * STAGE_BYTES) >> 4;
+          const uint32_t aoff = (slot * CODE_BYTES) >> 4, boff = (stage * B_BYTES) >> 4;
           const uint32_t sfa = tmem_base + A_COLS + a_set * 4;
           if (++a_set == A_SETS) a_set = 0;
-          copy_scales(sfa, as0 + soff);
+          copy_scales(sfa, as0 + slot * (L8_SCALE_TILE >> 4));
           if (b % 4 == 0 || b == w.b0) {
             sfb = tmem_base + B_COLS + b_set * 8;
             if (++b_set == B_SETS) b_set = 0;
-            copy_scales(sfb, bs0 + soff);
-            copy_scales(sfb + 4, bs0 + soff + (L8_SCALE_TILE >> 4));
+            copy_scales(sfb, bs0 + 2 * stage * (L8_SCALE_TILE >> 4));
+            copy_scales(sfb + 4, bs0 + (2 * stage + 1) * (L8_SCALE_TILE >> 4));
           }
           const uint32_t idesc = kIdesc128 | majors | static_cast<uint32_t>(b % 4) << 4;  // A's power is the first byte of its word
 #pragma unroll
           for (int kk = 0; kk < L8_BLOCK / 32; ++kk)
-            mma_block_scaled(d_tmem, adesc0 + soff + kk * astep, bdesc0 + soff + kk * bstep, idesc, sfa, sfb,
+            mma_block_scaled(d_tmem, adesc0 + aoff + kk * astep, bdesc0 + boff + kk * bstep, idesc, sfa, sfb,
                                   (b != w.b0 || kk != 0) ? 1u : 0u);
-          mma_commit_both(empty0 + 8 * stage);
-          if (++stage == STAGES) {
+          mma_commit_both(bempty0 + 8 * stage);
+          if (give_back) mma_commit(aempty0 + 8 * slot);
+          if (++stage == B_STAGES) {
             stage = 0;
             phase ^= 1u;
+          }
+          if (++slot == A_SLOTS) {
+            slot = 0;
+            sphase ^= 1u;
           }
         }
         if (!ok) break;
         mma_commit(tfull0 + 8 * acc);
+        if (give_back) run_slot = slot, run_phase = sphase;
         if (++acc == 2) {
           acc = 0;
           aphase ^= 1u;
@@ -477,19 +497,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // other team's instructions fill it
     const int team = (warp - ROUND0) / TEAM_WARPS, t = threadIdx.x - 32 * (ROUND0 + team * TEAM_WARPS);
     const int lanes = kCols ? t % 16 : t % 8, group = kCols ? t / 16 : t / 8;
-    int stage = 0, slot = 0, turn = 0;
-    uint32_t phase = 0, rphase = 0;
+    int slot = 0, raw_slot = 0, turn = 0;
+    uint32_t sphase = 0, rphase = 0;
     bool ok = true;
-    for (; w.more() && ok; w.next()) {
+    for (; w.more() && ok; kRuns ? w.next_run() : w.next()) {
       const long long c0 = (static_cast<long long>(w.tm) * 2 + rank) * ROWS;
       for (int b = w.b0; b < w.b1; ++b) {
         if (turn == team) {
-          ok = __all_sync(0xffffffffu, mbar_wait(rfull0 + 8 * slot, rphase, st, SITE_ROUND) &&
-                                           mbar_wait(empty0 + 8 * stage, phase ^ 1u, st, SITE_ROUND));
+          ok = __all_sync(0xffffffffu, mbar_wait(rfull0 + 8 * raw_slot, rphase, st, SITE_ROUND) &&
+                                           mbar_wait(aempty0 + 8 * slot, sphase ^ 1u, st, SITE_ROUND));
           // by columns they meet in round_cols: all of the team, or none (and none has still to read the last block's `tops`)
           if (kCols) ok = named_bar_and(1 + TEAMS + team, 32 * TEAM_WARPS, ok);
           if (!ok) break;
-          const uint32_t sr = base + RAW0 + slot * RAW_BYTES, sa = base + stage * STAGE_BYTES;
+          const uint32_t sr = base + RAW0 + raw_slot * RAW_BYTES, sa = base + slot * CODE_BYTES, ss = base + AS0 + slot * L8_SCALE_TILE;
           Numbers x;
           if (kCols) {
             const long long left = p.g.M - c0;
@@ -503,23 +523,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           // numbers from the next block's copy.)
           auto release = [&] {
             __syncwarp();
-            if (lane == 0) mbar_arrive(rempty0 + 8 * slot);
+            if (lane == 0) mbar_arrive(rempty0 + 8 * raw_slot);
           };
           if (kCols)
-            round_cols(x, sa, sa + A_SCALES, tops + team * (TEAM_WARPS * 16), team, t / 32, group, lanes, release);
+            round_cols(x, sa, ss, tops + team * (TEAM_WARPS * 16), team, t / 32, group, lanes, release);
           else
-            round_rows(x, sa, sa + A_SCALES, group, lanes, release);
+            round_rows(x, sa, ss, group, lanes, release);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(afull0 + 8 * stage);
+          if (lane == 0) mbar_arrive(afull0 + 8 * slot);
         }
         if (++turn == TEAMS) turn = 0;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (++slot == RAW_SLOTS) {
+        if (++slot == A_SLOTS) {
           slot = 0;
+          sphase ^= 1u;
+        }
+        if (++raw_slot == RAW_SLOTS) {
+          raw_slot = 0;
           rphase ^= 1u;
         }
       }
@@ -532,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       uint32_t rphase = 0;
       long long issued = 0;
       bool ok = true;
-      for (; w.more() && ok; w.next()) {
+      for (; w.more() && ok; kRuns ? w.next_run() : w.next()) {
         // (a box wholly past t may not complete its bytes: rows of C past M take those of row 0, and a half that has nothing
         // is not loaded)
         long long c0 = (static_cast<long long>(w.tm) * 2 + rank) * ROWS;
@@ -579,11 +599,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 cudaError_t launch_fused8(const Fused8Args& a, const CUtensorMap& t, const CUtensorMap& b, const CUtensorMap& b_scale, bool cols, int pairs, cudaStream_t s) {
-  auto kernel = cols ? k13_fused8<true> : k13_fused8<false>;
+  auto kernel = cols ? k13_fused8<true, false> : a.g.run > 1 ? k13_fused8<false, true> : k13_fused8<false, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
-  const long long tiles = static_cast<long long>(a.g.tiles_m) * a.g.tiles_n * a.g.n_z;
-  const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+  const long long runs = static_cast<long long>(a.g.tiles_m) * ((a.g.tiles_n + a.g.run - 1) / a.g.run) * a.g.n_z;
+  const int grid = 2 * static_cast<int>(runs < pairs ? runs : pairs);
   kernel<<<grid, THREADS, kSmem, s>>>(t, b, b_scale, a);
   return cudaGetLastError();
 }

@@ -63,6 +63,7 @@ struct Gemm8Args {
   int chunk;             // blocks that one accumulation takes
   int per_z, n_z;        // blocks of a slice of the depth, and the slices
   int tiles_m, tiles_n;
+  int run;               // tiles beside one another that a pair takes in turn
   void* c;               // bf16 [M][N], or f32 [n_z][M][N]
   const float* bias;     // f32 [N] or null (bf16 output)
   int* status;
@@ -73,7 +74,8 @@ struct Gemm8Maps {
   CUtensorMap a, b, a_scale, b_scale;
 };
 // The same with A as bf16 that is rounded on its way (k13_fused8.cu): by rows from t [M][depth] to bf16, or by columns from
-// t [depth][M] to f32 slices, whose accumulations begin at multiples of g.chunk.
+// t [depth][M] to f32 slices.  By rows with g.run > 1 a run's tiles share the codes, rounded once: at most FUSED8_RUN_BLOCKS blocks.
+constexpr int FUSED8_RUN_BLOCKS = 3;
 struct Fused8Args {
   Gemm8Args g;
   long long depth;

@@ -114,6 +114,7 @@ trimul_status run_gemm(const Placed8& a, const Placed8& b, void* c, bool f32, co
   p.n_z = n_z;
   p.chunk = f32 ? kChunk : p.per_z;
   p.tiles_m = tiles_of(p.M), p.tiles_n = tiles_of(p.N);
+  p.run = 1;
   p.c = c, p.bias = bias, p.status = status;
   p.timeout_ns = flags & TRIMUL_FLAG_INJECT_STALL ? kStallTimeoutNs : kTimeoutNs;
   p.stall = flags & TRIMUL_FLAG_INJECT_STALL;
@@ -122,6 +123,13 @@ trimul_status run_gemm(const Placed8& a, const Placed8& b, void* c, bool f32, co
   TRY(operand_maps(&m.b, &m.b_scale, b.o, b.codes, b.scales));
   TRY_CUDA(launch_gemm8(p, m, f32, pairs, s), "8-bit product launch");
   return TRIMUL_OK;
+}
+
+// Whether a row of tiles can share its codes in a fused product by rows: they fit, and there are rows enough for all pairs.
+bool runs_of_tiles(long long M, int blocks, int pairs) { return blocks <= FUSED8_RUN_BLOCKS && M >= 2ll * L8_TILE * pairs; }
+// Whether a product by rows rounds on its way (asked for without a device too, for the workspaces: kMostPairs there, at least as many as any has).
+bool fused_rows(long long M, int N, int depth) {
+  return tiles_of(N) <= kFusedRows || runs_of_tiles(M, static_cast<int>(l8_blocks(depth)), kMostPairs);
 }
 
 // C = Q(t) b^T with t, bf16, rounded on its way: by rows (t [M][depth], bf16 C) or by columns (t [depth][M], f32 slices).
@@ -137,6 +145,7 @@ trimul_status run_fused(const uint16_t* from, long long M, long long depth, bool
   p.g.n_z = n_z;
   p.g.chunk = cols ? kChunk : p.g.per_z;
   p.g.tiles_m = tiles_of(p.g.M), p.g.tiles_n = tiles_of(p.g.N);
+  p.g.run = !cols && runs_of_tiles(p.g.M, p.g.blocks, pairs) ? p.g.tiles_n : 1;
   p.g.c = c, p.g.bias = bias, p.g.status = status;
   p.g.timeout_ns = flags & TRIMUL_FLAG_INJECT_STALL ? kStallTimeoutNs : kTimeoutNs;
   p.g.stall = flags & TRIMUL_FLAG_INJECT_STALL;
@@ -181,7 +190,7 @@ struct Backward8 {
   Operand8 dy_rows, dy_cols, x_cols;
   size_t dy_rows_at, dy_cols_at, x_cols_at, slices_at, sums_at, bytes;
   Backward8(int64_t rows, int N, int K, bool want_dbias) : dy_rows{rows, N, false}, dy_cols{N, rows, true}, x_cols{K, rows, true} {
-    dx_fused = tiles_of(K) <= kFusedRows;
+    dx_fused = fused_rows(rows, K, N);
     // the wider one is rounded on its way; dbias comes from the pass over dy that rounds it by columns
     dw_swapped = K >= N || want_dbias;
     dw_fused = tiles_of(dw_swapped ? N : K) <= kFusedColumns;
@@ -226,7 +235,7 @@ trimul_status trimul_linear8_pack(const void* W, trimul_dtype type, int N, int K
 
 size_t trimul_linear8_forward_workspace_bytes(int64_t rows, int N, int K) {
   if (check_widths(N, K) != TRIMUL_OK || check_rows(rows) != TRIMUL_OK) return 0;
-  return kStatusBytes + (tiles_of(N) <= kFusedRows ? 0 : Operand8{rows, K, false}.bytes());
+  return kStatusBytes + (fused_rows(rows, N, K) ? 0 : Operand8{rows, K, false}.bytes());
 }
 
 trimul_status trimul_linear8_forward(const void* packed, const float* bias, const uint16_t* x, int64_t rows, int N, int K,
@@ -254,7 +263,7 @@ trimul_status trimul_linear8_forward(const void* packed, const float* bias, cons
   int* const status = static_cast<int*>(workspace);
   const Placed8 w(l.w, static_cast<const uint8_t*>(packed));
   const int pairs = pairs_of(device, sms);
-  if (tiles_of(N) <= kFusedRows) {
+  if (fused_rows(rows, N, K)) {
     TRY(run_fused(x, rows, K, false, w, y, bias, 0, 1, status, true, pairs, s, flags));
   } else {
     uint8_t* const codes = static_cast<uint8_t*>(workspace) + kStatusBytes;
