@@ -3,6 +3,7 @@
 #pragma once
 
 #include "linear8.h"
+#include "pair_ops.cuh"
 #include "sm103_ptx.cuh"
 
 namespace trimul {
@@ -66,6 +67,49 @@ __device__ __forceinline__ void transpose8(uint4 (&R)[8], uint32_t gb) {
       R[j] = upper ? recv : lo;
       R[j | k] = upper ? hi : recv;
     }
+  }
+}
+
+// The same for 4 x 4 chunks inside each group of 4 lanes.
+__device__ __forceinline__ void transpose4(uint4 (&R)[4], uint32_t lane4) {
+#pragma unroll
+  for (int k = 2; k >= 1; k >>= 1) {
+    const bool upper = (lane4 & k) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & k) continue;
+      const uint4 lo = R[j], hi = R[j | k];
+      const uint4 send = upper ? lo : hi;
+      uint4 recv;
+      recv.x = __shfl_xor_sync(0xffffffffu, send.x, k);
+      recv.y = __shfl_xor_sync(0xffffffffu, send.y, k);
+      recv.z = __shfl_xor_sync(0xffffffffu, send.z, k);
+      recv.w = __shfl_xor_sync(0xffffffffu, send.w, k);
+      R[j] = upper ? recv : lo;
+      R[j | k] = upper ? hi : recv;
+    }
+  }
+}
+
+// The bias is added from shared memory: read from global memory where it is added,
+// sixteen times a block of columns, the loads' latency made the epilogue twice as long
+// (2^20 rows of 256 to 1024: 954 us against 463 without a bias, 538 this way).  A warp's 64 columns of it:
+__device__ __forceinline__ void stage_bias(float* to, const float* bias, int c0, int N, int lane) {
+  const int col = c0 + 2 * lane;  // N is even
+  *reinterpret_cast<float2*>(to + 2 * lane) = col < N ? *reinterpret_cast<const float2*>(bias + col) : make_float2(0.f, 0.f);
+}
+// Adds kCount of them to a row's columns.
+template <int kCount>
+__device__ __forceinline__ void add_bias(uint32_t (&r)[kCount], const float* from) {
+  auto two = [](uint32_t& lo, uint32_t& hi, float a, float b) {
+    const float2 s = split2(add2(pair2(__uint_as_float(lo), __uint_as_float(hi)), pair2(a, b)));
+    lo = __float_as_uint(s.x), hi = __float_as_uint(s.y);
+  };
+#pragma unroll
+  for (int v = 0; v < kCount / 4; ++v) {
+    const float4 b = reinterpret_cast<const float4*>(from)[v];
+    two(r[4 * v], r[4 * v + 1], b.x, b.y);
+    two(r[4 * v + 2], r[4 * v + 3], b.z, b.w);
   }
 }
 

@@ -52,7 +52,8 @@ constexpr int THREADS = 64 + 32 * EPI_WARPS;
 static_assert(B_SCALES + 2 * L8_SCALE_TILE <= STAGE_BYTES, "the scales fit the stage");
 static_assert(ACC_STEP + L8_TILE <= SCALE_COLS && SCALE_COLS + SCALE_SETS * SCALE_SET <= TMEM_COLS, "TMEM");
 
-constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + BAR_BYTES;
+constexpr uint32_t BIAS_BYTES = EPI_WARPS * 64 * 4;
+constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + BAR_BYTES + BIAS_BYTES;
 
 }  // namespace
 
@@ -221,7 +222,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int acc = 0;
     uint32_t aphase = 0;
     float sum[kF32 ? 64 : 1];
+    float* const bias_at = reinterpret_cast<float*>(base_ptr + STAGES * STAGE_BYTES + BAR_BYTES) + (warp - 2) * 64;
     for (; w.more(); w.next()) {
+      if (!kF32 && p.bias) {
+        __syncwarp();  // the last tile's have been read
+        stage_bias(bias_at, p.bias, w.tn * L8_TILE + cb * 64, p.N, lane);
+        __syncwarp();
+      }
       const bool ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * acc, aphase, st, SITE_EPI));
       if (!ok) break;
       tc_fence_after();
@@ -243,17 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int h = 0; h < 2; ++h) {
           uint32_t r[32];
           tmem_read32(t_addr + h * 32, r);
-          if (p.bias) {
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const int col = c0 + h * 32 + v * 4;
-              const float4 b = col < p.N ? *reinterpret_cast<const float4*>(p.bias + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-              r[4 * v] = __float_as_uint(__uint_as_float(r[4 * v]) + b.x);
-              r[4 * v + 1] = __float_as_uint(__uint_as_float(r[4 * v + 1]) + b.y);
-              r[4 * v + 2] = __float_as_uint(__uint_as_float(r[4 * v + 2]) + b.z);
-              r[4 * v + 3] = __float_as_uint(__uint_as_float(r[4 * v + 3]) + b.w);
-            }
-          }
+          if (p.bias) add_bias(r, bias_at + h * 32);
           auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf162(__uint_as_float(lo), __uint_as_float(hi)); };
 #pragma unroll
           for (int v = 0; v < 4; ++v)

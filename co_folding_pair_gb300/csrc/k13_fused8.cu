@@ -45,7 +45,8 @@ constexpr uint32_t CODE_BYTES = ROWS * L8_BLOCK;
 constexpr uint32_t B_BYTES = 2 * CODE_BYTES;  // 256 rows of B
 constexpr uint32_t RAW_HALF = 128 * 128, RAW_BYTES = 2 * RAW_HALF;  // 128 rows of 64 bf16 numbers, twice
 constexpr uint32_t BAR_BYTES = 512;
-constexpr uint32_t TOPS_BYTES = 2 * 8 * 16 * 16;  // by columns: the largest magnitudes that each warp of a team has found
+constexpr uint32_t TOPS_BYTES = 8192;  // by columns: the largest magnitudes that each warp of a team has found; by rows: the bias
+constexpr int ALL_BIAS = TOPS_BYTES / 4;  // up to so many outputs it is all there; past that each epilogue warp has that of its tile
 constexpr uint32_t TMEM_COLS = 512, ACC_STEP = 192;
 constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 3;
 constexpr int EPI_WARPS = 8, TEAMS = 2, TEAM_WARPS = 8, ROUND_WARPS = TEAMS * TEAM_WARPS;
@@ -60,6 +61,7 @@ static_assert(A_COLS + 4 * A_SETS <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS,
 // rings: A's codes, B's codes, tiles of t, A's and B's scales
 constexpr uint32_t B0 = A_SLOTS * CODE_BYTES, RAW0 = B0 + B_STAGES * B_BYTES, AS0 = RAW0 + RAW_SLOTS * RAW_BYTES;
 constexpr uint32_t BS0 = AS0 + A_SLOTS * L8_SCALE_TILE, BARS = BS0 + B_STAGES * 2 * L8_SCALE_TILE;
+static_assert(TEAMS * TEAM_WARPS * 16 * 16 <= TOPS_BYTES && EPI_WARPS * 2 * 64 * 4 <= TOPS_BYTES, "the magnitudes, or the bias, fit");
 constexpr size_t kSmem = 1024 + BARS + BAR_BYTES + TOPS_BYTES;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 constexpr uint32_t SITE_ROUND = 0x500;
@@ -228,7 +230,7 @@ __device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uin
 
 // kRuns (by rows only): a run's tiles take the same codes of A, which wait in their slots until the last tile has had them.
 // Else a slot of A's codes goes with a stage of B's, and is free when that is.
-template <bool kCols, bool kRuns>
+template <bool kCols, bool kRuns, bool kBias>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_b_scale, const Fused8Args p) {
@@ -276,6 +278,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
+  }
+  float* const bias_at = reinterpret_cast<float*>(tops);
+  const bool all_bias = kBias && p.g.N <= ALL_BIAS;
+  if (all_bias) {
+    for (int i = threadIdx.x; i < ALL_BIAS; i += THREADS) bias_at[i] = i < p.g.N ? p.g.bias[i] : 0.f;
   }
   tc_fence_before();
   cluster_sync_all();
@@ -403,6 +410,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t aphase = 0;
     bool ok = true;
     for (; w.more() && ok; w.next()) {
+      if (kBias && !all_bias) {
+        __syncwarp();  // the last tile's have been read
+#pragma unroll
+        for (int turn = 0; turn < 2; ++turn)
+          stage_bias(bias_at + (2 * (warp - EPI0) + turn) * 64, p.g.bias, w.tn * L8_TILE + ((turn ^ acc) ? sub : 3 - sub) * 64, p.g.N, lane);
+        __syncwarp();
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * acc, aphase, st, SITE_EPI));
       if (!ok) break;
       tc_fence_after();
@@ -422,36 +436,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
         };
         if constexpr (!kCols) {
-          uint4 R[8];
+          // 32 columns at a time, and four rows' chunks among four lanes: few registers, as the rounding warps leave few
+          const float* const bias = bias_at + (all_bias ? c0 : (2 * (warp - EPI0) + turn) * 64);
+          const int row4 = w.tm * L8_TILE + static_cast<int>(rank) * ROWS + q * 32 + (lane & ~3);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
-            tmem_read32(t_addr + h * 32, r);
-            if (p.g.bias) {
+            uint4 R[4];
+            {
+              uint32_t r[32];
+              tmem_read32(t_addr + h * 32, r);
+              if (h == 1) hand_back();
+              if (kBias) add_bias(r, bias + h * 32);
+              auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf162(__uint_as_float(lo), __uint_as_float(hi)); };
 #pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                const int col = c0 + h * 32 + v * 4;
-                const float4 b = col < p.g.N ? *reinterpret_cast<const float4*>(p.g.bias + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-                r[4 * v] = __float_as_uint(__uint_as_float(r[4 * v]) + b.x);
-                r[4 * v + 1] = __float_as_uint(__uint_as_float(r[4 * v + 1]) + b.y);
-                r[4 * v + 2] = __float_as_uint(__uint_as_float(r[4 * v + 2]) + b.z);
-                r[4 * v + 3] = __float_as_uint(__uint_as_float(r[4 * v + 3]) + b.w);
-              }
+              for (int v = 0; v < 4; ++v)
+                R[v] = make_uint4(pack(r[v * 8 + 0], r[v * 8 + 1]), pack(r[v * 8 + 2], r[v * 8 + 3]), pack(r[v * 8 + 4], r[v * 8 + 5]),
+                                  pack(r[v * 8 + 6], r[v * 8 + 7]));
             }
-            auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf162(__uint_as_float(lo), __uint_as_float(hi)); };
+            transpose4(R, lane & 3);
+            const int col = c0 + h * 32 + (lane & 3) * 8;
+            if (col < p.g.N) {  // N is a multiple of 8: a chunk is all in or all out
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              R[h * 4 + v] = make_uint4(pack(r[v * 8 + 0], r[v * 8 + 1]), pack(r[v * 8 + 2], r[v * 8 + 3]),
-                                        pack(r[v * 8 + 4], r[v * 8 + 5]), pack(r[v * 8 + 6], r[v * 8 + 7]));
-          }
-          hand_back();
-          transpose8(R, gb);
-          const int col = c0 + static_cast<int>(gb) * 8;
-          if (col < p.g.N) {  // N is a multiple of 8: a chunk is all in or all out
-#pragma unroll
-            for (int s8 = 0; s8 < 8; ++s8) {
-              const int row = row0 + s8;
-              if (row < p.g.M) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.g.c) + static_cast<size_t>(row) * p.g.N + col) = R[s8];
+              for (int s4 = 0; s4 < 4; ++s4) {
+                const int row = row4 + s4;
+                if (row < p.g.M) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.g.c) + static_cast<size_t>(row) * p.g.N + col) = R[s4];
+              }
             }
           }
         } else {
@@ -599,7 +608,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 cudaError_t launch_fused8(const Fused8Args& a, const CUtensorMap& t, const CUtensorMap& b, const CUtensorMap& b_scale, bool cols, int pairs, cudaStream_t s) {
-  auto kernel = cols ? k13_fused8<true, false> : a.g.run > 1 ? k13_fused8<false, true> : k13_fused8<false, false>;
+  auto kernel = cols ? k13_fused8<true, false, false>
+                : a.g.run > 1 ? (a.g.bias ? k13_fused8<false, true, true> : k13_fused8<false, true, false>)
+                              : (a.g.bias ? k13_fused8<false, false, true> : k13_fused8<false, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
   if (e != cudaSuccess) return e;
   const long long runs = static_cast<long long>(a.g.tiles_m) * ((a.g.tiles_n + a.g.run - 1) / a.g.run) * a.g.n_z;
