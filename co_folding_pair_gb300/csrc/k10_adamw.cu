@@ -40,11 +40,10 @@ namespace trimul {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEach = 4;                             // neighbours of a thread
-constexpr int kParts = 2;                            // such fours of a thread that are on their way together
-constexpr int kStride = kThreads * kEach;            // elements from one to the next
-constexpr int kChunk = kStride * kParts;             // elements of a block's turn
-constexpr int blocks_per_sm(bool k8) { return k8 ? 3 : 4; }  // what the registers allow without spills
+constexpr int kEach = 4;                    // neighbours of a thread
+constexpr int kPart = kThreads * kEach;     // elements of a block
+constexpr int parts(bool k8) { return k8 ? 2 : 1; }  // of a chunk, which is a block's turn
+constexpr int kBlocksPerSm = 3;             // what the registers allow
 constexpr int kMostBlocks = 1024;
 constexpr int kTableSmall = 64, kTableMax = 384;  // tensors of one launch
 static_assert(32 * kEach == TRIMUL_STATE_BLOCK, "a warp has one block of the 8-bit states");
@@ -284,13 +283,13 @@ __device__ __forceinline__ void roots(const float (&x)[4], float (&r)[4]) {
 
 // What all elements of a step have in common.
 struct Step {
-  bool known, run;
+  bool run;
   float clip, lr, rate, over_root_c2;  // rate: lr / (1 - b1^t)
   uint32_t key;
 };
 __device__ __forceinline__ Step step_of(const Hyper& h, int count) {
   Step s;
-  s.known = s.run = true, s.clip = 1.f;
+  s.run = true, s.clip = 1.f;
   if (h.norm) {
     const float norm = *h.norm, share = __fmul_rn(h.max_norm, __frcp_rn(__fadd_rn(norm, 1e-6f)));
     s.run = norm - norm == 0.f;
@@ -312,91 +311,172 @@ __device__ __forceinline__ Entry entry(const Table<N>& tab, int k) {
                tab.index[k],   tab.kind[k]};
 }
 
+// A thread's numbers of a chunk as they lie in memory; of 8-bit states m.x and v.x are codes, m.y and v.y scales.
+struct Raw {
+  uint4 p, g, m, v;
+};
+template <bool k8>
+__device__ __forceinline__ long long place(const Entry& t, uint32_t chunk) {
+  return static_cast<long long>(chunk - t.chunk) * (kPart * parts(k8)) + threadIdx.x * kEach;
+}
+
 // kKind: the tensor's kind, or -1 for one that is known only here.
-// `s` is worked out behind the first chunk's loads: what it is made of comes from memory as well.
 template <bool k8, int kKind>
-__device__ __forceinline__ void step_chunk(const Entry& t, uint32_t chunk, const Hyper& h, const int* count, Step& s) {
-  const long long first = static_cast<long long>(chunk - t.chunk) * kChunk + threadIdx.x * kEach;
-  const bool stochastic = h.stochastic;
+__device__ __forceinline__ void load_part(const Entry& t, long long i, Raw& x) {
   const int kind = kKind < 0 ? t.kind : kKind;
-  const int ptype = kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32;
-  const int copy = kind >> COPY_SHIFT & 3;
-  const int gtype = kind >> GRAD_SHIFT & 3;
-  uint4 pr[kParts], gr[kParts], mr[kParts], vr[kParts];  // as they lie in memory; 8-bit states: .x the codes, .y the scale
-#pragma unroll
-  for (int u = 0; u < kParts; ++u) {
-    const long long i = first + u * kStride;
-    const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
-    pr[u] = load4(t.param, ptype, i, t.numel, wide);
-    gr[u] = load4(t.grad, gtype, i, t.numel, wide);
-    if (k8) {
-      const long long block = i / TRIMUL_STATE_BLOCK;  // the same for a warp
-      const bool any = block * TRIMUL_STATE_BLOCK < t.numel;
-      mr[u].x = load_codes(t.m, i, t.numel, whole), vr[u].x = load_codes(t.v, i, t.numel, whole);
-      mr[u].y = any ? __float_as_uint(t.m_scale[block]) : 0u, vr[u].y = any ? __float_as_uint(t.v_scale[block]) : 0u;
-    } else {
-      mr[u] = load4(t.m, TRIMUL_F32, i, t.numel, whole), vr[u] = load4(t.v, TRIMUL_F32, i, t.numel, whole);
-    }
-  }
-  if (!s.known) s = step_of(h, *const_cast<const volatile int*>(count));
-  if (!s.run) return;
-  const float keep = 1.f - s.lr * t.decay;
-  const uint32_t tensor_key = hash(t.index + s.key);
-#pragma unroll
-  for (int u = 0; u < kParts; ++u) {
-    const long long i = first + u * kStride;
-    const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
-    if (i / TRIMUL_STATE_BLOCK * TRIMUL_STATE_BLOCK >= t.numel) return;  // the same for a warp
-    float p[4], g[4], m[4], v[4], r[4];
-    unpack4(pr[u], ptype, p), unpack4(gr[u], gtype, g);
-    if (k8) {
-      unpack_codes(mr[u].x, __uint_as_float(mr[u].y), m), unpack_codes(vr[u].x, __uint_as_float(vr[u].y), v);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(v[e], v[e]);
-    } else {
-      unpack4(mr[u], TRIMUL_F32, m), unpack4(vr[u], TRIMUL_F32, v);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float ge = __fmul_rn(g[e], s.clip);
-      m[e] = __fadd_rn(__fmul_rn(h.b1, m[e]), __fmul_rn(h.not_b1, ge));
-      v[e] = __fadd_rn(__fmul_rn(h.b2, v[e]), __fmul_rn(__fmul_rn(h.not_b2, ge), ge));
-    }
-    if (k8) {
-      roots(v, r);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = root_approx(v[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = fmaf(-(s.rate * m[e]), reciprocal(fmaf(r[e], s.over_root_c2, h.eps)), p[e] * keep);
-    uint32_t hashes[4] = {0, 0, 0, 0};
-    if (stochastic && (k8 || ptype == TRIMUL_BF16)) {
-      const uint32_t key = hash(tensor_key + static_cast<uint32_t>(i >> 32)) ^ static_cast<uint32_t>(i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) hashes[e] = hash(key ^ e);  // (i is a multiple of four)
-    }
-    if (copy) store4(t.copy, copy == 1 ? TRIMUL_BF16 : TRIMUL_F16, i, t.numel, wide, p);
-    if (ptype == TRIMUL_BF16 && stochastic) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (fabsf(p[e]) < INFINITY) p[e] = __uint_as_float((__float_as_uint(p[e]) + (hash(hashes[e]) & 0xffffu)) & 0xffff0000u);
-    }
-    store4(t.param, ptype, i, t.numel, wide, p);
-    if (k8) {
-      const long long block = i / TRIMUL_STATE_BLOCK;
-      uint32_t codes;
-      const float m_scale = quantize<false>(m, hashes, stochastic, codes);
-      store_codes(t.m, i, t.numel, whole, codes);
-      const float v_scale = quantize<true>(r, hashes, stochastic, codes);
-      store_codes(t.v, i, t.numel, whole, codes);
-      if (threadIdx.x % 32 == 0) t.m_scale[block] = m_scale, t.v_scale[block] = v_scale;
-    } else {
-      store4(t.m, TRIMUL_F32, i, t.numel, whole, m);
-      store4(t.v, TRIMUL_F32, i, t.numel, whole, v);
-    }
+  const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
+  x.p = load4(t.param, kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32, i, t.numel, wide);
+  x.g = load4(t.grad, kind >> GRAD_SHIFT & 3, i, t.numel, wide);
+  if (k8) {
+    const long long block = i / TRIMUL_STATE_BLOCK;  // the same for a warp
+    const bool any = block * TRIMUL_STATE_BLOCK < t.numel;
+    x.m.x = load_codes(t.m, i, t.numel, whole), x.v.x = load_codes(t.v, i, t.numel, whole);
+    x.m.y = any ? __float_as_uint(t.m_scale[block]) : 0u, x.v.y = any ? __float_as_uint(t.v_scale[block]) : 0u;
+  } else {
+    x.m = load4(t.m, TRIMUL_F32, i, t.numel, whole), x.v = load4(t.v, TRIMUL_F32, i, t.numel, whole);
   }
 }
+
+template <bool k8, int kKind>
+__device__ __forceinline__ void step_part(const Entry& t, long long i, const Raw& x, const Hyper& h, const Step& s) {
+  const int kind = kKind < 0 ? t.kind : kKind;
+  const int ptype = kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32, gtype = kind >> GRAD_SHIFT & 3, copy = kind >> COPY_SHIFT & 3;
+  const bool stochastic = h.stochastic;
+  const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
+  if (i / TRIMUL_STATE_BLOCK * TRIMUL_STATE_BLOCK >= t.numel) return;  // the same for a warp
+  float p[4], g[4], m[4], v[4], r[4];
+  unpack4(x.p, ptype, p), unpack4(x.g, gtype, g);
+  if (k8) {
+    unpack_codes(x.m.x, __uint_as_float(x.m.y), m), unpack_codes(x.v.x, __uint_as_float(x.v.y), v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(v[e], v[e]);
+  } else {
+    unpack4(x.m, TRIMUL_F32, m), unpack4(x.v, TRIMUL_F32, v);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float ge = __fmul_rn(g[e], s.clip);
+    m[e] = __fadd_rn(__fmul_rn(h.b1, m[e]), __fmul_rn(h.not_b1, ge));
+    v[e] = __fadd_rn(__fmul_rn(h.b2, v[e]), __fmul_rn(__fmul_rn(h.not_b2, ge), ge));
+  }
+  if (k8) {
+    roots(v, r);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = root_approx(v[e]);
+  }
+  const float keep = 1.f - s.lr * t.decay;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = fmaf(-(s.rate * m[e]), reciprocal(fmaf(r[e], s.over_root_c2, h.eps)), p[e] * keep);
+  uint32_t hashes[4] = {0, 0, 0, 0};
+  if (stochastic && (k8 || ptype == TRIMUL_BF16)) {
+    const uint32_t key = hash(hash(t.index + s.key) + static_cast<uint32_t>(i >> 32)) ^ static_cast<uint32_t>(i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) hashes[e] = hash(key ^ e);  // (i is a multiple of four)
+  }
+  if (copy) store4(t.copy, copy == 1 ? TRIMUL_BF16 : TRIMUL_F16, i, t.numel, wide, p);
+  if (ptype == TRIMUL_BF16 && stochastic) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (fabsf(p[e]) < INFINITY) p[e] = __uint_as_float((__float_as_uint(p[e]) + (hash(hashes[e]) & 0xffffu)) & 0xffff0000u);
+  }
+  store4(t.param, ptype, i, t.numel, wide, p);
+  if (k8) {
+    const long long block = i / TRIMUL_STATE_BLOCK;
+    uint32_t codes;
+    const float m_scale = quantize<false>(m, hashes, stochastic, codes);
+    store_codes(t.m, i, t.numel, whole, codes);
+    const float v_scale = quantize<true>(r, hashes, stochastic, codes);
+    store_codes(t.v, i, t.numel, whole, codes);
+    if (threadIdx.x % 32 == 0) t.m_scale[block] = m_scale, t.v_scale[block] = v_scale;
+  } else {
+    store4(t.m, TRIMUL_F32, i, t.numel, whole, m);
+    store4(t.v, TRIMUL_F32, i, t.numel, whole, v);
+  }
+}
+
+// What most programs have gets code without questions about types.
+#define TRIMUL_BY_KIND(kind, f)      \
+  do {                               \
+    if ((kind) == kF32Copy)          \
+      f(kF32Copy);                   \
+    else if ((kind) == kF32)         \
+      f(kF32);                       \
+    else if ((kind) == kBf16)        \
+      f(kBf16);                      \
+    else                             \
+      f(-1);                         \
+  } while (0)
+
+// fp32 states: a chunk is on its way while the one before is worked on (179 us for the 96 layers' tensors where
+// loading two fours of a chunk together and then working on them takes 185).
+template <int N>
+__device__ __forceinline__ Step run_f32(const Table<N>& tab, const Hyper& h, const int* count, uint32_t c0, uint32_t c1) {
+  int k = tab.begin[blockIdx.x];
+  Entry t = entry(tab, k);
+  uint32_t end = tab.chunk[k + 1];
+  Raw x;
+  auto load = [&](const Entry& t, uint32_t chunk) {
+#define TRIMUL_LOAD(kKind) load_part<false, kKind>(t, place<false>(t, chunk), x)
+    TRIMUL_BY_KIND(t.kind, TRIMUL_LOAD);
+#undef TRIMUL_LOAD
+  };
+  if (c0 < c1) load(t, c0);
+  const Step s = step_of(h, *const_cast<const volatile int*>(count));  // behind the loads: it is made of what lies in memory as well
+  for (uint32_t chunk = c0; chunk < c1 && s.run; ++chunk) {
+    const Raw y = x;
+    const bool other = chunk + 1 >= end;  // the next chunk is another tensor's
+    if (chunk + 1 < c1) {
+      if (other)
+        load(entry(tab, k + 1), chunk + 1);
+      else
+        load(t, chunk + 1);
+    }
+#define TRIMUL_STEP(kKind) step_part<false, kKind>(t, place<false>(t, chunk), y, h, s)
+    TRIMUL_BY_KIND(t.kind, TRIMUL_STEP);
+#undef TRIMUL_STEP
+    if (other && chunk + 1 < c1) {
+      t = entry(tab, ++k);
+      end = tab.chunk[k + 1];
+    }
+  }
+  return s;
+}
+
+// 8-bit states: two fours of a thread are on their way together and then worked on.  The arithmetic is what takes the time; the
+// order above is 2% faster in long tensors and slower, 28 us for 23, in many of some ten thousand bf16 elements.
+template <int kKind>
+__device__ __forceinline__ void step_8bit(const Entry& t, uint32_t chunk, const Hyper& h, const int* count, bool& known, Step& s) {
+  const long long i = place<true>(t, chunk);
+  Raw x[parts(true)];
+#pragma unroll
+  for (int u = 0; u < parts(true); ++u) load_part<true, kKind>(t, i + u * kPart, x[u]);
+  if (!known) s = step_of(h, *const_cast<const volatile int*>(count)), known = true;
+  if (!s.run) return;
+#pragma unroll
+  for (int u = 0; u < parts(true); ++u) step_part<true, kKind>(t, i + u * kPart, x[u], h, s);
+}
+template <int N>
+__device__ __forceinline__ Step run_8bit(const Table<N>& tab, const Hyper& h, const int* count, uint32_t c0, uint32_t c1) {
+  Step s;
+  if (c0 >= c1) return step_of(h, *const_cast<const volatile int*>(count));
+  int k = tab.begin[blockIdx.x];
+  Entry t = entry(tab, k);
+  uint32_t end = tab.chunk[k + 1];
+  bool known = false;
+  for (uint32_t chunk = c0; chunk < c1; ++chunk) {
+    if (chunk >= end) {
+      t = entry(tab, ++k);
+      end = tab.chunk[k + 1];
+    }
+#define TRIMUL_STEP(kKind) step_8bit<kKind>(t, chunk, h, count, known, s)
+    TRIMUL_BY_KIND(t.kind, TRIMUL_STEP);
+#undef TRIMUL_STEP
+    if (!s.run) break;
+  }
+  return s;
+}
+#undef TRIMUL_BY_KIND
 
 __host__ __device__ __forceinline__ uint32_t run_begin(uint32_t chunks, uint32_t block, uint32_t blocks) {
   return static_cast<uint32_t>(static_cast<unsigned long long>(chunks) * block / blocks);
@@ -408,35 +488,15 @@ __host__ __device__ __forceinline__ uint32_t run_begin(uint32_t chunks, uint32_t
 // one before leaves (their tensors are others), and wait for it before they end, so that what
 // comes behind the last one comes behind all.
 template <bool k8, int N>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(k8))
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     k10_adamw(const __grid_constant__ Table<N> tab, const __grid_constant__ Hyper h, int* count, int last_launch) {
   let_next_begin();
-  Step s;
-  s.known = false;
   const uint32_t c0 = run_begin(tab.chunks, blockIdx.x, gridDim.x), c1 = run_begin(tab.chunks, blockIdx.x + 1, gridDim.x);
-  if (c0 < c1) {
-    int k = tab.begin[blockIdx.x];
-    Entry t = entry(tab, k);
-    uint32_t end = tab.chunk[k + 1];
-    for (uint32_t chunk = c0; chunk < c1; ++chunk) {
-      if (chunk >= end) {
-        t = entry(tab, ++k);
-        end = tab.chunk[k + 1];
-      }
-      // what most programs have gets code without questions about types
-      if (t.kind == kF32Copy)
-        step_chunk<k8, kF32Copy>(t, chunk, h, count, s);
-      else if (t.kind == kF32)
-        step_chunk<k8, kF32>(t, chunk, h, count, s);
-      else if (t.kind == kBf16)
-        step_chunk<k8, kBf16>(t, chunk, h, count, s);
-      else
-        step_chunk<k8, -1>(t, chunk, h, count, s);
-      if (!s.run) break;
-    }
-  } else {
-    s = step_of(h, *static_cast<volatile int*>(count));
-  }
+  Step s;
+  if constexpr (k8)
+    s = run_8bit(tab, h, count, c0, c1);
+  else
+    s = run_f32(tab, h, count, c0, c1);
   after_previous();
   if (!last_launch) return;
   __syncthreads();
@@ -451,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(k8))
 // ------------------------------------------------------------------ launches
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-template <int N>
+template <bool k8, int N>
 int fill(Table<N>& tab, const trimul_adamw_tensor* t, const trimul_grad_tensor* g, int n, int& k, int blocks) {
   tab.n = 0;
   tab.chunks = 0;
@@ -474,6 +534,7 @@ int fill(Table<N>& tab, const trimul_adamw_tensor* t, const trimul_grad_tensor* 
     tab.kind[q] = static_cast<uint8_t>((t[k].param_type == TRIMUL_BF16 ? PARAM_BF16 : 0) | g[k].type << GRAD_SHIFT |
                                        copy << COPY_SHIFT | (wide ? WIDE : 0));
     tab.chunk[q] = tab.chunks;
+    constexpr int kChunk = kPart * parts(k8);
     tab.chunks += static_cast<uint32_t>((t[k].numel + kChunk - 1) / kChunk);
   }
   tab.chunk[tab.n] = tab.chunks;
@@ -493,7 +554,7 @@ cudaError_t run(const Hyper& h, const trimul_adamw_tensor* t, const trimul_grad_
   Table<N> tab;
   int k = 0;
   for (bool first = true; first || k < n; first = false) {
-    const int grid = fill(tab, t, g, n, k, blocks_per_sm(k8) * num_sms);
+    const int grid = fill<k8>(tab, t, g, n, k, kBlocksPerSm * num_sms);
     cudaError_t e = cudaSuccess;
     if (first) {  // behind all that was before the call
       k10_adamw<k8, N><<<grid, kThreads, 0, s>>>(tab, h, count, k >= n);
