@@ -19,8 +19,8 @@
 //
 // Per CTA, 27 warps: 0 loads B and 26 the CTA's tile of t, 1 issues the
 // multiplications, 2..9 are the epilogue and 10..25 round, in two teams.  A tile of t waits as bf16
-// in a ring of its own.  Eight lanes take a row's 128 numbers (by columns, sixteen
-// lanes eight each), and the codes go to shared memory as TMA would have put them
+// in a ring of its own.  Eight lanes take a row's 128 numbers (by columns, a warp sixteen
+// columns), and the codes go to shared memory as TMA would have put them
 // there, with the block's powers beside them; a proxy fence makes them visible to the
 // tensor cores.  (The rounding warps load nothing from global memory themselves: with
 // the next block's loads on their way in registers each fence waited for those.)
@@ -45,8 +45,8 @@ constexpr uint32_t CODE_BYTES = ROWS * L8_BLOCK;
 constexpr uint32_t B_BYTES = 2 * CODE_BYTES;  // 256 rows of B
 constexpr uint32_t RAW_HALF = 128 * 128, RAW_BYTES = 2 * RAW_HALF;  // 128 rows of 64 bf16 numbers, twice
 constexpr uint32_t BAR_BYTES = 512;
-constexpr uint32_t TOPS_BYTES = 8192;  // by columns: the largest magnitudes that each warp of a team has found; by rows: the bias
-constexpr int ALL_BIAS = TOPS_BYTES / 4;  // up to so many outputs it is all there; past that each epilogue warp has that of its tile
+constexpr uint32_t BIAS_BYTES = 8192;
+constexpr int ALL_BIAS = BIAS_BYTES / 4;  // up to so many outputs it is all there; past that each epilogue warp has that of its tile
 constexpr uint32_t TMEM_COLS = 512, ACC_STEP = 192;
 constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 3;
 constexpr int EPI_WARPS = 8, TEAMS = 2, TEAM_WARPS = 8, ROUND_WARPS = TEAMS * TEAM_WARPS;
@@ -61,8 +61,8 @@ static_assert(A_COLS + 4 * A_SETS <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS,
 // rings: A's codes, B's codes, tiles of t, A's and B's scales
 constexpr uint32_t B0 = A_SLOTS * CODE_BYTES, RAW0 = B0 + B_STAGES * B_BYTES, AS0 = RAW0 + RAW_SLOTS * RAW_BYTES;
 constexpr uint32_t BS0 = AS0 + A_SLOTS * L8_SCALE_TILE, BARS = BS0 + B_STAGES * 2 * L8_SCALE_TILE;
-static_assert(TEAMS * TEAM_WARPS * 16 * 16 <= TOPS_BYTES && EPI_WARPS * 2 * 64 * 4 <= TOPS_BYTES, "the magnitudes, or the bias, fit");
-constexpr size_t kSmem = 1024 + BARS + BAR_BYTES + TOPS_BYTES;
+static_assert(EPI_WARPS * 2 * 64 * 4 <= BIAS_BYTES, "the bias fits");
+constexpr size_t kSmem = 1024 + BARS + BAR_BYTES + BIAS_BYTES;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 constexpr uint32_t SITE_ROUND = 0x500;
 constexpr uint32_t kIdesc128 = (kIdesc8 & ~(0x1Fu << 24)) | ((ROWS >> 4) << 24);
@@ -169,18 +169,18 @@ __device__ __forceinline__ void round_rows(const Numbers& x, uint32_t codes, uin
   if (lane8 == 0) st_shared16(scales + group * 16, byte[0], byte[1], byte[2], byte[3]);
 }
 
-// ---- by columns: lane `lane16` of row group `group` (0..15) has columns 8 lane16 .. + 7 of rows group + 16 u: v[u]; `left`: of
-// the tile's 128 columns, those before the last
-__device__ __forceinline__ void load_cols(Numbers& x, uint32_t slot, int left, int group, int lane16) {
+// ---- by columns: warp `warp` of the team has columns 16 warp .. + 15, a lane the eight of its `chunk` (2 warp or 2 warp + 1) in
+// rows `row0` + 16 u: v[u]; eight neighbouring lanes eight rows of a chunk, so that no two meet in a bank.  A column's
+// numbers are all in one warp: no other is waited for.  `left`: of the tile's 128 columns, those before the last
+__device__ __forceinline__ void load_cols(Numbers& x, uint32_t slot, int left, int row0, int chunk) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     x.v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (8 * lane16 < left) x.v[u] = raw16(slot, group + 16 * u, lane16);
+    if (8 * chunk < left) x.v[u] = raw16(slot, row0 + 16 * u, chunk);
   }
 }
 template <typename Release>
-__device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uint32_t scales, uint4* tops, int team, int warp, int group,
-                                           int lane16, Release release) {
+__device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uint32_t scales, int lane, int row0, int chunk, Release release) {
   auto join = [](uint4& a, const uint4& b) {
     a.x = max16x2(a.x, b.x), a.y = max16x2(a.y, b.y), a.z = max16x2(a.z, b.z), a.w = max16x2(a.w, b.w);
   };
@@ -198,32 +198,35 @@ __device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uin
 #pragma unroll
     for (int u = 1; u < 8; ++u) join(top, finite(x.v[u]));
   }
-  join(top, make_uint4(__shfl_xor_sync(0xffffffffu, top.x, 16), __shfl_xor_sync(0xffffffffu, top.y, 16),
-                       __shfl_xor_sync(0xffffffffu, top.z, 16), __shfl_xor_sync(0xffffffffu, top.w, 16)));
-  if (threadIdx.x % 32 < 16) tops[warp * 16 + lane16] = top;
+  // Over the sixteen lanes of a chunk (all of a lane's bits but 8): by bit 16 a lane keeps two of its four words and gets the
+  // other lane's, by bit 4 one of the two.  Then each lane has two columns, whose powers it works out, and the way back
+  // brings those of all eight.
+  const bool hi2 = lane & 16, hi1 = lane & 4;
+  auto other = [](uint32_t v, int bit) { return __shfl_xor_sync(0xffffffffu, v, bit); };
+  const uint32_t t0 = max16x2(hi2 ? top.z : top.x, other(hi2 ? top.x : top.z, 16));
+  const uint32_t t1 = max16x2(hi2 ? top.w : top.y, other(hi2 ? top.y : top.w, 16));
+  uint32_t m = max16x2(hi1 ? t1 : t0, other(hi1 ? t0 : t1, 4));
+  m = max16x2(m, other(m, 2));
+  m = max16x2(m, other(m, 1));
   release();
-  named_bar_sync(1 + team, 32 * TEAM_WARPS);
-#pragma unroll
-  for (int q = 0; q < TEAM_WARPS; ++q) join(top, tops[q * 16 + lane16]);
-  const uint32_t word[4] = {top.x, top.y, top.z, top.w};
-  uint32_t byte[8];
+  const uint32_t two = scale_byte(m << 16) | scale_byte(m & 0xffff0000u) << 8;
+  const uint32_t two1 = other(two, 4);
+  const uint32_t four = __byte_perm(two, two1, hi1 ? 0x1054 : 0x5410), four1 = other(four, 16);
+  const uint32_t lo = hi2 ? four1 : four, hi = hi2 ? four : four1;  // the bytes of columns 0 .. 3 and 4 .. 7
   f2 inv[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    byte[2 * e] = scale_byte(word[e] << 16), byte[2 * e + 1] = scale_byte(word[e] & 0xffff0000u);
-    inv[e] = pair2(over_scale(byte[2 * e]), over_scale(byte[2 * e + 1]));
+    const uint32_t w = e < 2 ? lo : hi, at = 16 * (e & 1);
+    inv[e] = pair2(over_scale(w >> at & 0xffu), over_scale(w >> (at + 8) & 0xffu));
   }
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const int row = group + 16 * u;
-    st_shared8(codes + row * 128 + (((lane16 >> 1) ^ (row & 7)) << 4) + (lane16 & 1) * 8, codes_of(x.v[u], inv, fine));
+    const int row = row0 + 16 * u;
+    st_shared8(codes + row * 128 + (((chunk >> 1) ^ (row & 7)) << 4) + (chunk & 1) * 8, codes_of(x.v[u], inv, fine));
   }
-  if (group < 8) {  // group g has column g of the lane's eight
-    uint32_t mine = byte[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) mine = group == e ? byte[e] : mine;
-    const int c = lane16 * 8 + group;
-    st_shared4(scales + (c % 32) * 16 + (c / 32) * 4, mine);
+  if (!(lane & 2)) {  // a lane's two columns, by bit 1
+    const int c = chunk * 8 + 4 * hi2 + 2 * hi1 + (lane & 1);
+    st_shared4(scales + (c % 32) * 16 + (c / 32) * 4, two >> (8 * (lane & 1)) & 0xffu);
   }
 }
 }  // namespace
@@ -245,7 +248,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t tfull0 = rempty0 + 8 * RAW_SLOTS, tempty0 = tfull0 + 16, over = tempty0 + 16, drain = over + 8;
   const uint32_t tmem_slot = drain + 8;
   volatile uint32_t* tmem_slot_ptr = reinterpret_cast<volatile uint32_t*>(base_ptr + (tmem_slot - base));
-  uint4* const tops = reinterpret_cast<uint4*>(base_ptr + BARS + BAR_BYTES);
 
   const KStatus st{p.g.status, p.g.timeout_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -279,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
-  float* const bias_at = reinterpret_cast<float*>(tops);
+  float* const bias_at = reinterpret_cast<float*>(base_ptr + BARS + BAR_BYTES);
   const bool all_bias = kBias && p.g.N <= ALL_BIAS;
   if (all_bias) {
     for (int i = threadIdx.x; i < ALL_BIAS; i += THREADS) bias_at[i] = i < p.g.N ? p.g.bias[i] : 0.f;
@@ -505,7 +507,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // the teams take the blocks in turns: one block's way through shared memory, the maxima and the conversions is long, and the
     // other team's instructions fill it
     const int team = (warp - ROUND0) / TEAM_WARPS, t = threadIdx.x - 32 * (ROUND0 + team * TEAM_WARPS);
-    const int lanes = kCols ? t % 16 : t % 8, group = kCols ? t / 16 : t / 8;
+    // by columns: the chunk and the first row
+    const int lanes = kCols ? t / 32 * 2 + (lane >> 3 & 1) : t % 8, group = kCols ? (lane & 7) + (lane >> 4) * 8 : t / 8;
     int slot = 0, raw_slot = 0, turn = 0;
     uint32_t sphase = 0, rphase = 0;
     bool ok = true;
@@ -515,8 +518,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (turn == team) {
           ok = __all_sync(0xffffffffu, mbar_wait(rfull0 + 8 * raw_slot, rphase, st, SITE_ROUND) &&
                                            mbar_wait(aempty0 + 8 * slot, sphase ^ 1u, st, SITE_ROUND));
-          // by columns they meet in round_cols: all of the team, or none (and none has still to read the last block's `tops`)
-          if (kCols) ok = named_bar_and(1 + TEAMS + team, 32 * TEAM_WARPS, ok);
           if (!ok) break;
           const uint32_t sr = base + RAW0 + raw_slot * RAW_BYTES, sa = base + slot * CODE_BYTES, ss = base + AS0 + slot * L8_SCALE_TILE;
           Numbers x;
@@ -535,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(rempty0 + 8 * raw_slot);
           };
           if (kCols)
-            round_cols(x, sa, ss, tops + team * (TEAM_WARPS * 16), team, t / 32, group, lanes, release);
+            round_cols(x, sa, ss, lane, group, lanes, release);
           else
             round_rows(x, sa, ss, group, lanes, release);
           fence_proxy_async_smem();
