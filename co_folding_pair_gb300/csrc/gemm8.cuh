@@ -93,7 +93,7 @@ __device__ __forceinline__ void transpose4(uint4 (&R)[4], uint32_t lane4) {
 
 // The bias is added from shared memory: read from global memory where it is added,
 // sixteen times a block of columns, the loads' latency made the epilogue twice as long
-// (2^20 rows of 256 to 1024: 954 us against 463 without a bias, 538 this way).  A warp's 64 columns of it:
+// (2^20 rows of 256 to 1024: 954 us against 463 without a bias).  A warp's 64 columns of it:
 __device__ __forceinline__ void stage_bias(float* to, const float* bias, int c0, int N, int lane) {
   const int col = c0 + 2 * lane;  // N is even
   *reinterpret_cast<float2*>(to + 2 * lane) = col < N ? *reinterpret_cast<const float2*>(bias + col) : make_float2(0.f, 0.f);

@@ -8,8 +8,7 @@
 // A pair stack's layers are narrow (K of 1024 at most) and have millions of
 // rows: bf16 in, bf16 out bounds them, and a pass of its own for the codes would
 // write and read half of the input again.  The price is that a tile of t is
-// rounded once for every 256 columns of C (from L2: a pair takes a row of tiles
-// in turn).
+// rounded once for every 256 columns of C, unless it has few blocks (below).
 //
 // Two CTAs of a cluster have 128 rows of A each and one tile of B between them:
 // each loads half of it (TMA) for both.  Unlike k12_gemm8.cu each multiplies by
@@ -17,8 +16,8 @@
 // known to the even CTA by a release at cluster scope for every block, which takes
 // about as long as rounding it (550 to 860 us at 2^20 rows of 1024 to 256, whichever warps did it).
 //
-// Per CTA, 27 warps: 0 loads B and 26 the CTA's tile of t, 1 issues the
-// multiplications, 2..9 are the epilogue and 10..25 round, in two teams.  A tile of t waits as bf16
+// Per CTA: warp 0 loads B and the last one the CTA's tile of t, 1 issues the
+// multiplications, 2..9 are the epilogue, and the others round, in teams of eight.  A tile of t waits as bf16
 // in a ring of its own.  Eight lanes take a row's 128 numbers (by columns, a warp sixteen
 // columns), and the codes go to shared memory as TMA would have put them
 // there, with the block's powers beside them; a proxy fence makes them visible to the
@@ -39,34 +38,47 @@ namespace trimul {
 
 namespace {
 constexpr int ROWS = 128;
-constexpr int A_SLOTS = 3, B_STAGES = 3, RAW_SLOTS = 2;
-// Blocks of t that are asked for in L2 ahead of their turn, as two tiles are too little on its way: 1024 to 256 channels 454 us without,
-// 414 with two (and with four, but then 256 to 256 takes 198 for 166).  Where a run's tiles share the codes it does not help: 446 us become 503.
+// Blocks of t that are asked for in L2 ahead of their turn, as the tiles that are on their way are too few: 2^20 rows of 1024 to 256
+// channels 454 us without, 414 with two (and with four, but then 256 to 256 takes 198 for 166).  Where a run's tiles share the
+// codes it does not help: 446 us became 503.
 constexpr int AHEAD = 2;
-static_assert(A_SLOTS == B_STAGES && FUSED8_RUN_BLOCKS <= A_SLOTS, "a run's codes wait in their slots");
 constexpr uint32_t CODE_BYTES = ROWS * L8_BLOCK;
 constexpr uint32_t B_BYTES = 2 * CODE_BYTES;  // 256 rows of B
 constexpr uint32_t RAW_HALF = 128 * 128, RAW_BYTES = 2 * RAW_HALF;  // 128 rows of 64 bf16 numbers, twice
+constexpr uint32_t OUT_BYTES = 32 * 128;  // of an epilogue warp: 32 rows of 64 bf16 numbers
 constexpr uint32_t BAR_BYTES = 512;
 constexpr uint32_t BIAS_BYTES = 8192;
 constexpr int ALL_BIAS = BIAS_BYTES / 4;  // up to so many outputs it is all there; past that each epilogue warp has that of its tile
 constexpr uint32_t TMEM_COLS = 512, ACC_STEP = 192;
-constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 3;
-constexpr int EPI_WARPS = 8, TEAMS = 2, TEAM_WARPS = 8, ROUND_WARPS = TEAMS * TEAM_WARPS;
-constexpr int EPI0 = 2, ROUND0 = EPI0 + EPI_WARPS, RAW = ROUND0 + ROUND_WARPS, THREADS = 32 * (RAW + 1);
-// A team waits for its own blocks alone.  A wait that has skipped a use of its barrier would take the phase before for the one it
-// wants, and pass at once.  So a slot of t is always the same team's.  With three slots of codes a team comes to a slot every
-// second use; what it skipped (the multiplications of the block six before its own) was done when it was last let on, by those of the block five before.
-static_assert(RAW_SLOTS % TEAMS == 0, "a slot of t is always the same team's");
-static_assert(TEAMS == 2 && (A_SLOTS == 3 || A_SLOTS % 2 == 0), "a team knows its slot's phase");
-static_assert(A_SETS > B_STAGES + 1 && B_STAGES <= 3, "a set's readers are done when it is written again");
-static_assert(A_COLS + 4 * A_SETS <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
-// rings: A's codes, B's codes, tiles of t, A's and B's scales
-constexpr uint32_t B0 = A_SLOTS * CODE_BYTES, RAW0 = B0 + B_STAGES * B_BYTES, AS0 = RAW0 + RAW_SLOTS * RAW_BYTES;
-constexpr uint32_t BS0 = AS0 + A_SLOTS * L8_SCALE_TILE, BARS = BS0 + B_STAGES * 2 * L8_SCALE_TILE;
-static_assert(EPI_WARPS * 2 * 64 * 4 <= BIAS_BYTES, "the bias fits");
-constexpr size_t kSmem = 1024 + BARS + BAR_BYTES + BIAS_BYTES;
-static_assert(kSmem <= 232448, "shared memory of a CTA");
+constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 4;
+constexpr uint32_t A_COLS_END = A_COLS + 4 * A_SETS;
+static_assert(A_COLS_END <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
+constexpr int EPI0 = 2, TEAM_WARPS = 8;
+// How the warps and the shared memory are shared out.  kFew: by rows, with few blocks of depth (FUSED8_FEW_BLOCKS).  There the
+// way out counts: a tile goes by way of shared memory and TMA.  (Turned in registers by shuffles and stored by the warps, 2^20 rows of
+// 256 to 1024 channels take 455 us and with a bias 531; this way 440 and 443.  128 to 128: 119 and 145, now 94 and 102.)
+// The room is a tile of t's, one team is enough for what is left to round, and the warps have more registers.
+// Else rounding has two teams: with one, or with one tile of t on its way, it falls behind.
+template <bool kFew>
+struct Plan {
+  static constexpr int A_SLOTS = 3, B_STAGES = 3, RAW_SLOTS = kFew ? 1 : 2;
+  static constexpr int EPI_WARPS = 8, TEAMS = kFew ? 1 : 2;
+  static constexpr int ROUND0 = EPI0 + EPI_WARPS, RAW = ROUND0 + TEAMS * TEAM_WARPS, THREADS = 32 * (RAW + 1);
+  // rings: A's codes, B's codes, tiles of t, what is on its way out, A's and B's scales
+  static constexpr uint32_t B0 = A_SLOTS * CODE_BYTES, RAW0 = B0 + B_STAGES * B_BYTES, OUT0 = RAW0 + RAW_SLOTS * RAW_BYTES;
+  static constexpr uint32_t AS0 = OUT0 + (kFew ? EPI_WARPS * OUT_BYTES : 0);
+  static constexpr uint32_t BS0 = AS0 + A_SLOTS * L8_SCALE_TILE, BARS = BS0 + B_STAGES * 2 * L8_SCALE_TILE;
+  static constexpr size_t SMEM = 1024 + BARS + BAR_BYTES + BIAS_BYTES;
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static_assert(8 * (2 * B_STAGES + 2 * A_SLOTS + 2 * RAW_SLOTS + 6) + 4 <= BAR_BYTES && 16 * 64 * 4 <= BIAS_BYTES, "the barriers and the bias fit");
+  static_assert(kFew ? FUSED8_FEW_BLOCKS <= A_SLOTS : A_SLOTS == B_STAGES, "a run's codes wait in their slots, or go with a stage of B's");
+  static_assert(A_SETS > B_STAGES + 1 && B_STAGES <= B_SETS, "a set's readers are done when it is written again");
+  // A team waits for its own blocks alone.  A wait that has skipped a use of its barrier would take the phase before for the one it
+  // wants, and pass at once.  So a slot of t is always the same team's.  With three slots of codes and two teams a team comes to a slot every
+  // second use; what it skipped (the multiplications of the block six before its own) was done when it was last let on, by those of the block five before.
+  static_assert(RAW_SLOTS % TEAMS == 0, "a slot of t is always the same team's");
+  static_assert(TEAMS == 1 || (TEAMS == 2 && (A_SLOTS == 3 || A_SLOTS % 2 == 0)), "a team knows its slot's phase");
+};
 constexpr uint32_t SITE_ROUND = 0x500;
 constexpr uint32_t kIdesc128 = (kIdesc8 & ~(0x1Fu << 24)) | ((ROWS >> 4) << 24);
 
@@ -97,6 +109,11 @@ __device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(c0),
+               "r"(c1)
+               : "memory");
+}
 // A box into L2 alone.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int c0, int c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1) : "memory");
@@ -239,19 +256,23 @@ __device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uin
 }
 }  // namespace
 
-// kRuns (by rows only): a run's tiles take the same codes of A, which wait in their slots until the last tile has had them.
+// kFew (by rows only): a run's tiles take the same codes of A, which wait in their slots until the last tile has had them.
 // Else a slot of A's codes goes with a stage of B's, and is free when that is.
-template <bool kCols, bool kRuns, bool kBias>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+template <bool kCols, bool kFew, bool kBias>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS, 1)
     k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
-               const __grid_constant__ CUtensorMap tm_b_scale, const Fused8Args p) {
+               const __grid_constant__ CUtensorMap tm_b_scale, const __grid_constant__ CUtensorMap tm_c, const Fused8Args p) {
+  using P = Plan<kFew>;
+  constexpr int A_SLOTS = P::A_SLOTS, B_STAGES = P::B_STAGES, RAW_SLOTS = P::RAW_SLOTS, EPI_WARPS = P::EPI_WARPS, TEAMS = P::TEAMS, ROUND0 = P::ROUND0, RAW = P::RAW;
+  constexpr uint32_t B0 = P::B0, RAW0 = P::RAW0, AS0 = P::AS0, BS0 = P::BS0, BARS = P::BARS;
+  constexpr int TURNS = 16 / EPI_WARPS;  // 64-column blocks of a warp
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
   const uint32_t bars = base + BARS;
   // bfull bempty [B_STAGES] afull aempty [A_SLOTS] rfull rempty [RAW_SLOTS] tfull tempty [2] over drain, then the TMEM base word
-  const uint32_t bfull0 = bars, bempty0 = bfull0 + 8 * B_STAGES, afull0 = bempty0 + 8 * B_STAGES, aempty0 = kRuns ? afull0 + 8 * A_SLOTS : bempty0;
+  const uint32_t bfull0 = bars, bempty0 = bfull0 + 8 * B_STAGES, afull0 = bempty0 + 8 * B_STAGES, aempty0 = kFew ? afull0 + 8 * A_SLOTS : bempty0;
   const uint32_t rfull0 = afull0 + 16 * A_SLOTS, rempty0 = rfull0 + 8 * RAW_SLOTS;
   const uint32_t tfull0 = rempty0 + 8 * RAW_SLOTS, tempty0 = tfull0 + 16, over = tempty0 + 16, drain = over + 8;
   const uint32_t tmem_slot = drain + 8;
@@ -271,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int s = 0; s < A_SLOTS; ++s) {
       mbar_init(afull0 + 8 * s, TEAM_WARPS);
-      if (kRuns) mbar_init(aempty0 + 8 * s, 1);  // one commit
+      if (kFew) mbar_init(aempty0 + 8 * s, 1);  // one commit
     }
     for (int r = 0; r < RAW_SLOTS; ++r) {
       mbar_init(rfull0 + 8 * r, 1);  // one expect_tx arrival
@@ -292,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   float* const bias_at = reinterpret_cast<float*>(base_ptr + BARS + BAR_BYTES);
   const bool all_bias = kBias && p.g.N <= ALL_BIAS;
   if (all_bias) {
-    for (int i = threadIdx.x; i < ALL_BIAS; i += THREADS) bias_at[i] = i < p.g.N ? p.g.bias[i] : 0.f;
+    for (int i = threadIdx.x; i < ALL_BIAS; i += P::THREADS) bias_at[i] = i < p.g.N ? p.g.bias[i] : 0.f;
   }
   tc_fence_before();
   cluster_sync_all();
@@ -364,8 +385,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * ACC_STEP;
         uint32_t sfb = 0;
-        if (kRuns) slot = run_slot, sphase = run_phase;  // each tile of a run begins at its first slot
-        const bool give_back = kRuns && w.last_tile();
+        if (kFew) slot = run_slot, sphase = run_phase;  // each tile of a run begins at its first slot
+        const bool give_back = kFew && w.last_tile();
         for (int b = w.b0; b < w.b1; ++b) {
           if (!mbar_wait(bfull0 + 8 * stage, phase, st, SITE_MMA) || !mbar_wait(afull0 + 8 * slot, sphase, st, SITE_MMA)) {
             ok = false;
@@ -414,7 +435,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp < ROUND0) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;               // TMEM lane quadrant of this warp
-    const int sub = (warp - EPI0) >> 2;   // 0: the outer two of the 64-column blocks, 1: the inner two
+    // which of the four 64-column blocks: with two a warp, 0 the outer two and 1 the inner two (an element has one thread, whichever
+    // accumulator it is in)
+    const int sub = (warp - EPI0) >> 2;
+    auto block_of = [&](int turn, int acc) { return TURNS == 1 ? sub : (turn ^ acc) ? sub : 3 - sub; };
     const uint32_t gb = lane & 7, ga = lane >> 3;
     int acc = 0;
     uint32_t aphase = 0;
@@ -423,8 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (kBias && !all_bias) {
         __syncwarp();  // the last tile's have been read
 #pragma unroll
-        for (int turn = 0; turn < 2; ++turn)
-          stage_bias(bias_at + (2 * (warp - EPI0) + turn) * 64, p.g.bias, w.tn * L8_TILE + ((turn ^ acc) ? sub : 3 - sub) * 64, p.g.N, lane);
+        for (int turn = 0; turn < TURNS; ++turn)
+          stage_bias(bias_at + (TURNS * (warp - EPI0) + turn) * 64, p.g.bias, w.tn * L8_TILE + block_of(turn, acc) * 64, p.g.N, lane);
         __syncwarp();
       }
       ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * acc, aphase, st, SITE_EPI));
@@ -432,9 +456,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const int row0 = w.tm * L8_TILE + static_cast<int>(rank) * ROWS + q * 32 + static_cast<int>(ga) * 8;
 #pragma unroll 1
-      for (int turn = 0; turn < 2; ++turn) {
-        const int cb = (turn ^ acc) ? sub : 3 - sub;  // the shared columns are the last block's of accumulator 0, the first's of 1
-        const bool shared = sub == 0 && turn == 0;
+      for (int turn = 0; turn < TURNS; ++turn) {
+        const int cb = block_of(turn, acc);
+        const bool shared = cb == (acc ? 0 : 3);  // the columns that both accumulators have
         const int c0 = w.tn * L8_TILE + cb * 64;
         const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * ACC_STEP + cb * 64;
         auto hand_back = [&] {
@@ -442,12 +466,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             if (shared) mbar_arrive(over);
-            if (turn == 1) mbar_arrive(tempty0 + 8 * acc);
+            if (turn == TURNS - 1) mbar_arrive(tempty0 + 8 * acc);
           }
         };
-        if constexpr (!kCols) {
+        if constexpr (kFew) {
+          // by way of shared memory, row by row as the tile's map has them (128-byte swizzle); TMA writes what lies in C
+          const float* const bias = bias_at + (all_bias ? c0 : (TURNS * (warp - EPI0) + turn) * 64);
+          const uint32_t out = base + P::OUT0 + (warp - EPI0) * OUT_BYTES;
+          const int row = w.tm * L8_TILE + static_cast<int>(rank) * ROWS + q * 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_read32(t_addr + h * 32, r);
+            if (h == 1) hand_back();
+            if (kBias) add_bias(r, bias + h * 32);
+            if (h == 0) {
+              if (lane == 0) tma_store_wait_read<0>();  // the last one has been read
+              __syncwarp();
+            }
+            auto pack = [](uint32_t lo, uint32_t hi) { return pack_bf162(__uint_as_float(lo), __uint_as_float(hi)); };
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              st_shared16(out + lane * 128 + (((4 * h + v) ^ gb) << 4), pack(r[v * 8 + 0], r[v * 8 + 1]), pack(r[v * 8 + 2], r[v * 8 + 3]),
+                          pack(r[v * 8 + 4], r[v * 8 + 5]), pack(r[v * 8 + 6], r[v * 8 + 7]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row < p.g.M && c0 < p.g.N) {
+            tma_store_2d(&tm_c, out, c0, row);
+            tma_store_commit();
+          }
+        } else if constexpr (!kCols) {
           // 32 columns at a time, and four rows' chunks among four lanes: few registers, as the rounding warps leave few
-          const float* const bias = bias_at + (all_bias ? c0 : (2 * (warp - EPI0) + turn) * 64);
+          const float* const bias = bias_at + (all_bias ? c0 : (TURNS * (warp - EPI0) + turn) * 64);
           const int row4 = w.tm * L8_TILE + static_cast<int>(rank) * ROWS + q * 32 + (lane & ~3);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -510,6 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         aphase ^= 1u;
       }
     }
+    if (kFew && lane == 0) tma_store_wait_all();
   } else if (warp < RAW) {
     // ------------------------------------------------------------ rounding of A
     // the teams take the blocks in turns: one block's way through shared memory, the maxima and the conversions is long, and the
@@ -520,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int slot = 0, raw_slot = 0, turn = 0;
     uint32_t sphase = 0, rphase = 0;
     bool ok = true;
-    for (; w.more() && ok; kRuns ? w.next_run() : w.next()) {
+    for (; w.more() && ok; kFew ? w.next_run() : w.next()) {
       const long long c0 = (static_cast<long long>(w.tm) * 2 + rank) * ROWS;
       for (int b = w.b0; b < w.b1; ++b) {
         if (turn == team) {
@@ -581,12 +633,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int d = b * L8_BLOCK, x = kCols ? static_cast<int>(c0) : d;
         return Box{x, kCols ? d : static_cast<int>(c0), x + 64 < (kCols ? p.g.M : p.depth) ? 2 : 1};
       };
-      auto next = [](Walk& v) { kRuns ? v.next_run() : v.next(); };
-      Walk far = w;  // AHEAD blocks before
+      auto next = [](Walk& v) { kFew ? v.next_run() : v.next(); };
+      const int ahead = p.g.run > 1 ? 0 : AHEAD;
+      Walk far = w;
       int far_b = far.b0;
       for (; w.more() && ok; next(w)) {
         for (int b = w.b0; b < w.b1; ++b) {
-          for (; !kRuns && lead < AHEAD && far.more(); ++lead) {
+          for (; lead < ahead && far.more(); ++lead) {
             const Box f = box(far, far_b);
             tma_prefetch_2d(&tm_t, f.x, f.y);
             if (f.halves == 2) tma_prefetch_2d(&tm_t, f.x + 64, f.y);
@@ -595,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               far_b = far.b0;
             }
           }
-          if (!kRuns) --lead;
+          if (ahead) --lead;
           if (!mbar_wait(rempty0 + 8 * slot, rphase ^ 1u, st, SITE_PRODUCER)) {
             ok = false;
             break;
@@ -635,15 +688,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-cudaError_t launch_fused8(const Fused8Args& a, const CUtensorMap& t, const CUtensorMap& b, const CUtensorMap& b_scale, bool cols, int pairs, cudaStream_t s) {
+cudaError_t launch_fused8(const Fused8Args& a, const Fused8Maps& m, bool cols, int pairs, cudaStream_t s) {
+  const bool few = !cols && a.g.blocks <= FUSED8_FEW_BLOCKS;
   auto kernel = cols ? k13_fused8<true, false, false>
-                : a.g.run > 1 ? (a.g.bias ? k13_fused8<false, true, true> : k13_fused8<false, true, false>)
-                              : (a.g.bias ? k13_fused8<false, false, true> : k13_fused8<false, false, false>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+                : few ? (a.g.bias ? k13_fused8<false, true, true> : k13_fused8<false, true, false>)
+                      : (a.g.bias ? k13_fused8<false, false, true> : k13_fused8<false, false, false>);
+  const size_t smem = few ? Plan<true>::SMEM : Plan<false>::SMEM;
+  const int threads = few ? Plan<true>::THREADS : Plan<false>::THREADS;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const long long runs = static_cast<long long>(a.g.tiles_m) * ((a.g.tiles_n + a.g.run - 1) / a.g.run) * a.g.n_z;
   const int grid = 2 * static_cast<int>(runs < pairs ? runs : pairs);
-  kernel<<<grid, THREADS, kSmem, s>>>(t, b, b_scale, a);
+  kernel<<<grid, threads, smem, s>>>(m.t, m.b, m.b_scale, m.c, a);
   return cudaGetLastError();
 }
 

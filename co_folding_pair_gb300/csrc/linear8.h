@@ -74,14 +74,18 @@ struct Gemm8Maps {
   CUtensorMap a, b, a_scale, b_scale;
 };
 // The same with A as bf16 that is rounded on its way (k13_fused8.cu): by rows from t [M][depth] to bf16, or by columns from
-// t [depth][M] to f32 slices.  By rows with g.run > 1 a run's tiles share the codes, rounded once: at most FUSED8_RUN_BLOCKS blocks.
-constexpr int FUSED8_RUN_BLOCKS = 3;
+// t [depth][M] to f32 slices.  By rows of at most FUSED8_FEW_BLOCKS blocks, C is written by way of its map `c` (boxes of 32 rows and
+// 64 columns), and with g.run > 1 a run's tiles share the codes, rounded once.
+constexpr int FUSED8_FEW_BLOCKS = 3;
 struct Fused8Args {
   Gemm8Args g;
   long long depth;
   int clear;             // clear the status word first
 };
-cudaError_t launch_fused8(const Fused8Args& a, const CUtensorMap& t, const CUtensorMap& b, const CUtensorMap& b_scale, bool cols, int pairs, cudaStream_t s);
+struct Fused8Maps {
+  CUtensorMap t, b, b_scale, c;
+};
+cudaError_t launch_fused8(const Fused8Args& a, const Fused8Maps& m, bool cols, int pairs, cudaStream_t s);
 int gemm8_max_pairs(int num_sms);
 cudaError_t launch_gemm8(const Gemm8Args& a, const Gemm8Maps& m, bool f32, int pairs, cudaStream_t s);
 // out = the sum of n_z slices of n floats; cols > 0: of matrices [n / cols][cols], transposed.

@@ -64,11 +64,11 @@ trimul_status operand_maps(CUtensorMap* codes, CUtensorMap* scales, const Operan
   return TRIMUL_OK;
 }
 
-// bf16 [rows][cols] in boxes of 128 rows and 64 columns, zeros past the end.
-trimul_status bf16_map(CUtensorMap* m, const uint16_t* at, long long cols, long long rows) {
+// bf16 [rows][cols] in boxes of `box_rows` rows and 64 columns; past the end zeros are read and nothing is written.
+trimul_status bf16_map(CUtensorMap* m, const uint16_t* at, long long cols, long long rows, unsigned box_rows) {
   EncodeTiled fn = encode_tiled();
   if (!fn) return fail(TRIMUL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint32_t one[2] = {1, 1}, box[2] = {64, 128};
+  const cuuint32_t one[2] = {1, 1}, box[2] = {64, box_rows};
   const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)}, stride[1] = {static_cast<cuuint64_t>(cols) * 2};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(at), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -126,7 +126,7 @@ trimul_status run_gemm(const Placed8& a, const Placed8& b, void* c, bool f32, co
 }
 
 // Whether a row of tiles can share its codes in a fused product by rows: they fit, and there are rows enough for all pairs.
-bool runs_of_tiles(long long M, int blocks, int pairs) { return blocks <= FUSED8_RUN_BLOCKS && M >= 2ll * L8_TILE * pairs; }
+bool runs_of_tiles(long long M, int blocks, int pairs) { return blocks <= FUSED8_FEW_BLOCKS && M >= 2ll * L8_TILE * pairs; }
 // Whether a product by rows rounds on its way (asked for without a device too, for the workspaces: kMostPairs there, at least as many as any has).
 bool fused_rows(long long M, int N, int depth) {
   return tiles_of(N) <= kFusedRows || runs_of_tiles(M, static_cast<int>(l8_blocks(depth)), kMostPairs);
@@ -149,10 +149,14 @@ trimul_status run_fused(const uint16_t* from, long long M, long long depth, bool
   p.g.c = c, p.g.bias = bias, p.g.status = status;
   p.g.timeout_ns = flags & TRIMUL_FLAG_INJECT_STALL ? kStallTimeoutNs : kTimeoutNs;
   p.g.stall = flags & TRIMUL_FLAG_INJECT_STALL;
-  CUtensorMap t, codes, scales;
-  TRY(bf16_map(&t, from, cols ? M : depth, cols ? depth : M));
-  TRY(operand_maps(&codes, &scales, b.o, b.codes, b.scales));
-  TRY_CUDA(launch_fused8(p, t, codes, scales, cols, pairs, s), "8-bit product launch");
+  Fused8Maps m;
+  TRY(bf16_map(&m.t, from, cols ? M : depth, cols ? depth : M, 128));
+  TRY(operand_maps(&m.b, &m.b_scale, b.o, b.codes, b.scales));
+  if (cols)
+    m.c = m.t;  // not used
+  else
+    TRY(bf16_map(&m.c, static_cast<const uint16_t*>(c), b.o.rows, M, 32));
+  TRY_CUDA(launch_fused8(p, m, cols, pairs, s), "8-bit product launch");
   return TRIMUL_OK;
 }
 
