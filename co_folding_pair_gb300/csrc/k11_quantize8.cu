@@ -255,24 +255,53 @@ __global__ void __launch_bounds__(kThreads) k11_weight(const T* __restrict__ w, 
 // Few sums of many slices take eight (with one, the loads of a hundred slices come one after the other: 13 us for
 // 512 sums, 5.4 with eight); many take one (262144 sums of 76 slices: 8 us, with eight 18.6).
 template <int kEach>
-__global__ void __launch_bounds__(kThreads) k11_join(const float* __restrict__ part, int n_z, long long n, int cols, float* __restrict__ out) {
+__device__ __forceinline__ void join(const Join8& a, long long block, float* sums) {
   constexpr int kSums = kThreads / kEach;
-  __shared__ float sums[kEach][kSums];
   const int lane = threadIdx.x % kSums, q = threadIdx.x / kSums;
-  const long long i = static_cast<long long>(blockIdx.x) * kSums + lane;
+  const long long i = block * kSums + lane;
   float s = 0.f;
-  if (i < n) {
+  if (i < a.n) {
 #pragma unroll 8
-    for (int z = q; z < n_z; z += kEach) s += part[z * n + i];
+    for (int z = q; z < a.n_z; z += kEach) s += a.part[z * a.n + i];
   }
   if (kEach > 1) {
-    sums[q][lane] = s;
+    sums[q * kSums + lane] = s;
     __syncthreads();
     if (q != 0) return;
 #pragma unroll
-    for (int k = 1; k < kEach; ++k) s += sums[k][lane];
+    for (int k = 1; k < kEach; ++k) s += sums[k * kSums + lane];
   }
-  if (i < n) out[cols ? i % cols * (n / cols) + i / cols : i] = s;
+  if (i < a.n) a.out[a.cols ? i % a.cols * (a.n / a.cols) + i / a.cols : i] = s;
+}
+template <int kEach>
+__global__ void __launch_bounds__(kThreads) k11_join(const Join8 a, const Join8 few, unsigned blocks_a) {
+  __shared__ float sums[kThreads];
+  if (blockIdx.x < blocks_a)
+    join<kEach>(a, blockIdx.x, sums);
+  else
+    join<8>(few, blockIdx.x - blocks_a, sums);
+}
+
+// ------------------------------------------------------------------ sums of columns, as k13_fused8.cu takes them
+__global__ void __launch_bounds__(kThreads) k11_sums(const uint16_t* __restrict__ t, long long rows, int cols, int per_z,
+                                                     float* __restrict__ out, int* __restrict__ status) {
+  if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+  const int lane = threadIdx.x % 32, z = blockIdx.y / 2, odd = blockIdx.y % 2;
+  const int c = blockIdx.x * kSide + 8 * (threadIdx.x / 32 * 2 + (lane >> 3 & 1));
+  const long long blocks = l8_blocks(rows), end = min(static_cast<long long>(z + 1) * per_z, blocks);
+  f2 sums[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+  for (long long b = static_cast<long long>(z) * per_z + odd; b < end; b += 2) {
+    uint4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const long long row = b * kSide + (lane & 7) + (lane >> 4) * 8 + 16 * u;
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows && c < cols) v[u] = *reinterpret_cast<const uint4*>(t + row * cols + c);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) add_row(sums, v[u]);
+  }
+  join_columns(sums, out + static_cast<long long>(blockIdx.y) * cols + c, c < cols);
 }
 
 }  // namespace
@@ -302,7 +331,7 @@ cudaError_t launch_quantize_columns(const uint16_t* x, long long rows, int cols,
   kernel<<<grid, kThreads, 0, s>>>(x, rows, cols, static_cast<uint32_t>(c.ld()), static_cast<uint32_t>(c.groups()), out, out + c.scales_at(),
                                    static_cast<uint32_t>(r.groups()), by_rows, by_rows ? by_rows + r.scales_at() : nullptr, part, parts, status);
   cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess && column_sums ? launch_join(part, parts, cols, 0, column_sums, s) : e;
+  return e == cudaSuccess && column_sums ? launch_join(Join8{}, Join8{part, parts, cols, 0, column_sums}, s) : e;
 }
 
 cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_t* codes, uint8_t* scales, uint8_t* scales_mn,
@@ -317,11 +346,20 @@ cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_
   return cudaGetLastError();
 }
 
-cudaError_t launch_join(const float* part, int n_z, long long n, int cols, float* out, cudaStream_t s) {
-  if (n < 16384)
-    k11_join<8><<<static_cast<unsigned>((n + 31) / 32), kThreads, 0, s>>>(part, n_z, n, cols, out);
-  else
-    k11_join<1><<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(part, n_z, n, cols, out);
+cudaError_t launch_join(const Join8& a, const Join8& few, cudaStream_t s) {
+  const unsigned blocks_few = static_cast<unsigned>((few.n + 31) / 32);
+  if (a.n < 16384) {
+    const unsigned blocks = static_cast<unsigned>((a.n + 31) / 32);
+    k11_join<8><<<blocks + blocks_few, kThreads, 0, s>>>(a, few, blocks);
+  } else {
+    const unsigned blocks = static_cast<unsigned>((a.n + kThreads - 1) / kThreads);
+    k11_join<1><<<blocks + blocks_few, kThreads, 0, s>>>(a, few, blocks);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_column_sums(const uint16_t* t, long long rows, int cols, int per_z, int n_z, float* sums, int* status, cudaStream_t s) {
+  k11_sums<<<dim3(static_cast<unsigned>(l8_blocks(cols)), 2 * n_z), kThreads, 0, s>>>(t, rows, cols, per_z, sums, status);
   return cudaGetLastError();
 }
 

@@ -204,8 +204,9 @@ __device__ __forceinline__ void load_cols(Numbers& x, uint32_t slot, int left, i
     if (8 * chunk < left) x.v[u] = raw16(slot, row0 + 16 * u, chunk);
   }
 }
-template <typename Release>
-__device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uint32_t scales, int lane, int row0, int chunk, Release release) {
+template <bool kSums, typename Release>
+__device__ __forceinline__ void round_cols(const Numbers& x, f2 (&sums)[4], uint32_t codes, uint32_t scales, int lane, int row0, int chunk,
+                                           Release release) {
   auto join = [](uint4& a, const uint4& b) {
     a.x = max16x2(a.x, b.x), a.y = max16x2(a.y, b.y), a.z = max16x2(a.z, b.z), a.w = max16x2(a.w, b.w);
   };
@@ -247,6 +248,7 @@ __device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uin
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const int row = row0 + 16 * u;
+    if (kSums) add_row(sums, x.v[u]);
     st_shared8(codes + row * 128 + (((chunk >> 1) ^ (row & 7)) << 4) + (chunk & 1) * 8, codes_of(x.v[u], inv, fine));
   }
   if (!(lane & 2)) {  // a lane's two columns, by bit 1
@@ -258,7 +260,9 @@ __device__ __forceinline__ void round_cols(const Numbers& x, uint32_t codes, uin
 
 // kFew (by rows only): a run's tiles take the same codes of A, which wait in their slots until the last tile has had them.
 // Else a slot of A's codes goes with a stage of B's, and is free when that is.
-template <bool kCols, bool kFew, bool kBias>
+// kMore: with a bias; by columns, with the sums of t's columns (dbias), which the rounding warps take as they pass: a lane adds its
+// eight rows of each of its team's blocks, the sixteen lanes of a column are joined, and every slice leaves two sums.
+template <bool kCols, bool kFew, bool kMore>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS, 1)
     k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_b_scale, const __grid_constant__ CUtensorMap tm_c, const Fused8Args p) {
@@ -266,6 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
   constexpr int A_SLOTS = P::A_SLOTS, B_STAGES = P::B_STAGES, RAW_SLOTS = P::RAW_SLOTS, EPI_WARPS = P::EPI_WARPS, TEAMS = P::TEAMS, ROUND0 = P::ROUND0, RAW = P::RAW;
   constexpr uint32_t B0 = P::B0, RAW0 = P::RAW0, AS0 = P::AS0, BS0 = P::BS0, BARS = P::BARS;
   constexpr int TURNS = 16 / EPI_WARPS;  // 64-column blocks of a warp
+  constexpr bool kBias = kMore && !kCols, kSums = kMore && kCols;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -572,6 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
     int slot = 0, raw_slot = 0, turn = 0;
     uint32_t sphase = 0, rphase = 0;
     bool ok = true;
+    f2 sums[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+    int first_turn = 0;
     for (; w.more() && ok; kFew ? w.next_run() : w.next()) {
       const long long c0 = (static_cast<long long>(w.tm) * 2 + rank) * ROWS;
       for (int b = w.b0; b < w.b1; ++b) {
@@ -596,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
             if (lane == 0) mbar_arrive(rempty0 + 8 * raw_slot);
           };
           if (kCols)
-            round_cols(x, sa, ss, lane, group, lanes, release);
+            round_cols<kSums>(x, sums, sa, ss, lane, group, lanes, release);
           else
             round_rows(x, sa, ss, group, lanes, release);
           fence_proxy_async_smem();
@@ -612,6 +619,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
           raw_slot = 0;
           rphase ^= 1u;
         }
+      }
+      if (kSums && ok && w.last()) {  // a slice's end: the sums of every other of its blocks, from the first or the second on
+        const int odd = team ^ first_turn;
+        const long long c = c0 + 8 * lanes;
+        join_columns(sums, p.sums + (static_cast<long long>(w.z) * TEAMS + odd) * p.g.M + c, c < p.g.M);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sums[e] = both(0.f);
+        first_turn = turn;
       }
     }
   } else {
@@ -690,7 +705,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
 
 cudaError_t launch_fused8(const Fused8Args& a, const Fused8Maps& m, bool cols, int pairs, cudaStream_t s) {
   const bool few = !cols && a.g.blocks <= FUSED8_FEW_BLOCKS;
-  auto kernel = cols ? k13_fused8<true, false, false>
+  auto kernel = cols  ? (a.sums ? k13_fused8<true, false, true> : k13_fused8<true, false, false>)
                 : few ? (a.g.bias ? k13_fused8<false, true, true> : k13_fused8<false, true, false>)
                       : (a.g.bias ? k13_fused8<false, false, true> : k13_fused8<false, false, false>);
   const size_t smem = few ? Plan<true>::SMEM : Plan<false>::SMEM;

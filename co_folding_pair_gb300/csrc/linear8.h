@@ -81,6 +81,7 @@ struct Fused8Args {
   Gemm8Args g;
   long long depth;
   int clear;             // clear the status word first
+  float* sums;           // by columns: [2 g.n_z][M], whose sum is that of t's columns; or null.  One tile of N
 };
 struct Fused8Maps {
   CUtensorMap t, b, b_scale, c;
@@ -88,7 +89,17 @@ struct Fused8Maps {
 cudaError_t launch_fused8(const Fused8Args& a, const Fused8Maps& m, bool cols, int pairs, cudaStream_t s);
 int gemm8_max_pairs(int num_sms);
 cudaError_t launch_gemm8(const Gemm8Args& a, const Gemm8Maps& m, bool f32, int pairs, cudaStream_t s);
+// The same sums without the product, bit for bit: of t [rows][cols], slices of per_z blocks of 128 rows.
+cudaError_t launch_column_sums(const uint16_t* t, long long rows, int cols, int per_z, int n_z, float* sums, int* status, cudaStream_t s);
 // out = the sum of n_z slices of n floats; cols > 0: of matrices [n / cols][cols], transposed.
-cudaError_t launch_join(const float* part, int n_z, long long n, int cols, float* out, cudaStream_t s);
+struct Join8 {
+  const float* part;
+  int n_z;
+  long long n;
+  int cols;
+  float* out;
+};
+// Two of them in one launch, either of them of nothing; `few`: of few sums.
+cudaError_t launch_join(const Join8& a, const Join8& few, cudaStream_t s);
 
 }  // namespace trimul

@@ -21,7 +21,8 @@ constexpr int kMostWidth = 65536;
 constexpr int kMostPairs = 128, kMostSms = 256;  // what workspaces are sized for
 constexpr int kChunk = 32;                       // blocks of 128 rows that a weight gradient's accumulation takes
 // 256-wide tiles of the other operand up to which rounding on the way (k13_fused8.cu) is faster than a pass of its own: each tile
-// rounds again.  Rows (2^20 of them, us): one tile 175 to 280, two (2^19 rows) 264 to 287, four 634 to 560; columns: one 737 to 933, two 457 to 406.
+// rounds again.  Rows (2^20 of them, us): one tile 175 to 280, two (2^19 rows) 264 to 287, four 634 to 560; columns: one 737 to 933, two
+// 457 to 406.  (With dbias 2^20 rows of 256 to 1024 channels took 1184 when its sums still asked for a pass over dy, and take 668.)
 constexpr int kFusedRows = 2, kFusedColumns = 1;
 constexpr unsigned long long kTimeoutNs = 4000000000ull, kStallTimeoutNs = 200000000ull;
 constexpr size_t kStatusBytes = 256;
@@ -134,9 +135,10 @@ bool fused_rows(long long M, int N, int depth) {
 
 // C = Q(t) b^T with t, bf16, rounded on its way: by rows (t [M][depth], bf16 C) or by columns (t [depth][M], f32 slices).
 trimul_status run_fused(const uint16_t* from, long long M, long long depth, bool cols, const Placed8& b, void* c, const float* bias,
-                        int per_z, int n_z, int* status, bool clear, int pairs, cudaStream_t s, unsigned flags) {
+                        float* sums, int per_z, int n_z, int* status, bool clear, int pairs, cudaStream_t s, unsigned flags) {
   Fused8Args p{};
   p.clear = clear;
+  p.sums = sums;
   p.depth = depth;
   p.g.M = static_cast<int>(M), p.g.N = static_cast<int>(b.o.rows);
   p.g.b_mn = b.o.mn;
@@ -191,14 +193,16 @@ struct Packed {
 // How a backward goes about it, and the offsets in its workspace.
 struct Backward8 {
   bool dx_fused, dw_fused, dw_swapped;  // dw_swapped: x is A, and the slices are of dW^T
+  bool sums_alone;  // dbias does not come from the pass over dy that rounds it by columns, as there is none
   Operand8 dy_rows, dy_cols, x_cols;
   size_t dy_rows_at, dy_cols_at, x_cols_at, slices_at, sums_at, bytes;
-  Backward8(int64_t rows, int N, int K, bool want_dbias) : dy_rows{rows, N, false}, dy_cols{N, rows, true}, x_cols{K, rows, true} {
+  Backward8(int64_t rows, int N, int K) : dy_rows{rows, N, false}, dy_cols{N, rows, true}, x_cols{K, rows, true} {
     dx_fused = fused_rows(rows, K, N);
-    // the wider one is rounded on its way; dbias comes from the pass over dy that rounds it by columns
-    dw_swapped = K >= N || want_dbias;
+    // the wider one is rounded on its way
+    dw_swapped = K >= N;
     dw_fused = tiles_of(dw_swapped ? N : K) <= kFusedColumns;
     if (!dw_fused) dw_swapped = false;
+    sums_alone = dw_fused && !dw_swapped;
     int per_z, n_z;
     slices(N, K, static_cast<int>(l8_blocks(rows)), kMostPairs, &per_z, &n_z);
     dy_rows_at = kStatusBytes;
@@ -206,8 +210,9 @@ struct Backward8 {
     x_cols_at = dy_cols_at + (dw_fused && !dw_swapped ? 0 : dy_cols.bytes());
     slices_at = x_cols_at + (dw_fused && dw_swapped ? 0 : x_cols.bytes());
     // (as many slices as kMostPairs allow, whatever rounding makes of fewer)
-    sums_at = slices_at + up256(static_cast<size_t>(std::max(n_z, kMostPairs / (tiles_of(N) * tiles_of(K)))) * N * K * 4);
-    bytes = sums_at + up256(static_cast<size_t>(quantize_columns_parts(rows, N, kMostSms)) * N * 4);
+    const int most_z = std::max(n_z, kMostPairs / (tiles_of(N) * tiles_of(K)));
+    sums_at = slices_at + up256(static_cast<size_t>(most_z) * N * K * 4);
+    bytes = sums_at + up256(static_cast<size_t>(sums_alone ? 2 * most_z : quantize_columns_parts(rows, N, kMostSms)) * N * 4);
   }
 };
 
@@ -268,7 +273,7 @@ trimul_status trimul_linear8_forward(const void* packed, const float* bias, cons
   const Placed8 w(l.w, static_cast<const uint8_t*>(packed));
   const int pairs = pairs_of(device, sms);
   if (fused_rows(rows, N, K)) {
-    TRY(run_fused(x, rows, K, false, w, y, bias, 0, 1, status, true, pairs, s, flags));
+    TRY(run_fused(x, rows, K, false, w, y, bias, nullptr, 0, 1, status, true, pairs, s, flags));
   } else {
     uint8_t* const codes = static_cast<uint8_t*>(workspace) + kStatusBytes;
     TRY_CUDA(launch_quantize_rows(x, rows, K, codes, status, sms, s), "quantisation launch");
@@ -279,7 +284,7 @@ trimul_status trimul_linear8_forward(const void* packed, const float* bias, cons
 
 size_t trimul_linear8_backward_workspace_bytes(int64_t rows, int N, int K) {
   if (check_widths(N, K) != TRIMUL_OK || check_rows(rows) != TRIMUL_OK) return 0;
-  return std::max(Backward8(rows, N, K, false).bytes, Backward8(rows, N, K, true).bytes);
+  return Backward8(rows, N, K).bytes;
 }
 
 trimul_status trimul_linear8_backward(const void* packed, const uint16_t* x, const uint16_t* dy, int64_t rows, int N, int K,
@@ -312,41 +317,47 @@ trimul_status trimul_linear8_backward(const void* packed, const uint16_t* x, con
     if (dbias) TRY_CUDA(cudaMemsetAsync(dbias, 0, bb, s), "dbias");
     return finish(cudaSuccess, s, flags, "linear8 backward");
   }
-  const Backward8 b(rows, N, K, dbias != nullptr);
+  const Backward8 b(rows, N, K);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   int* const status = static_cast<int*>(workspace);
   const uint8_t* const pk = static_cast<const uint8_t*>(packed);
   const int pairs = pairs_of(device, sms);
   const Placed8 w(l.wt, pk, pk + l.wt_scales_at), dy_rows(b.dy_rows, ws + b.dy_rows_at), dy_cols(b.dy_cols, ws + b.dy_cols_at),
       x_cols(b.x_cols, ws + b.x_cols_at);
-  const bool codes_of_dy = dbias || (dW && !(b.dw_fused && !b.dw_swapped));  // by columns
+  const bool codes_of_dy = (dbias || dW) && !b.sums_alone;  // by columns
+  float* const sums = reinterpret_cast<float*>(ws + b.sums_at);
   uint8_t* const rows_of_dy = dx && !b.dx_fused ? ws + b.dy_rows_at : nullptr;
   if (codes_of_dy)
-    TRY_CUDA(launch_quantize_columns(dy, rows, N, ws + b.dy_cols_at, rows_of_dy, dbias, reinterpret_cast<float*>(ws + b.sums_at), status, sms, s),
+    TRY_CUDA(launch_quantize_columns(dy, rows, N, ws + b.dy_cols_at, rows_of_dy, dbias, sums, status, sms, s),
              "quantisation launch");
   else if (rows_of_dy)
     TRY_CUDA(launch_quantize_rows(dy, rows, N, rows_of_dy, status, sms, s), "quantisation launch");
   if (dx) {
     if (b.dx_fused)
-      TRY(run_fused(dy, rows, N, false, w, dx, nullptr, 0, 1, status, !codes_of_dy, pairs, s, flags));
+      TRY(run_fused(dy, rows, N, false, w, dx, nullptr, nullptr, 0, 1, status, !codes_of_dy, pairs, s, flags));
     else
       TRY(run_gemm(dy_rows, w, dx, false, nullptr, 0, 1, status, pairs, s, flags));
   }
+  int per_z, n_z;
+  slices(N, K, static_cast<int>(l8_blocks(rows)), pairs, &per_z, &n_z);
+  const Join8 of_sums = dbias && b.sums_alone ? Join8{sums, 2 * n_z, N, 0, dbias} : Join8{};
+  Join8 of_dw{};
   if (dW) {
-    int per_z, n_z;
-    slices(N, K, static_cast<int>(l8_blocks(rows)), pairs, &per_z, &n_z);
     float* const part = n_z == 1 && !b.dw_swapped ? dW : reinterpret_cast<float*>(ws + b.slices_at);
-    if (!b.dw_fused || !b.dw_swapped)
+    if (part != dW) of_dw = Join8{part, n_z, static_cast<long long>(N) * K, b.dw_swapped ? N : 0, dW};
+    if (!b.dw_swapped)
       TRY_CUDA(launch_quantize_columns(x, rows, K, ws + b.x_cols_at, nullptr, nullptr, nullptr, dx || codes_of_dy ? nullptr : status, sms, s),
                "quantisation launch");
     if (!b.dw_fused)
       TRY(run_gemm(dy_cols, x_cols, part, true, nullptr, per_z, n_z, status, pairs, s, flags));
     else if (b.dw_swapped)
-      TRY(run_fused(x, K, rows, true, dy_cols, part, nullptr, per_z, n_z, status, false, pairs, s, flags));
+      TRY(run_fused(x, K, rows, true, dy_cols, part, nullptr, nullptr, per_z, n_z, status, false, pairs, s, flags));
     else
-      TRY(run_fused(dy, N, rows, true, x_cols, part, nullptr, per_z, n_z, status, false, pairs, s, flags));
-    if (part != dW) TRY_CUDA(launch_join(part, n_z, static_cast<long long>(N) * K, b.dw_swapped ? N : 0, dW, s), "join launch");
+      TRY(run_fused(dy, N, rows, true, x_cols, part, nullptr, of_sums.out ? sums : nullptr, per_z, n_z, status, false, pairs, s, flags));
+  } else if (of_sums.out) {
+    TRY_CUDA(launch_column_sums(dy, rows, N, per_z, n_z, sums, dx ? nullptr : status, s), "column sum launch");
   }
+  if (of_dw.out || of_sums.out) TRY_CUDA(launch_join(of_dw, of_sums, s), "join launch");
   if (!dx && !dW && !dbias) return finish(cudaSuccess, s, flags, "linear8 backward");
   return finish8(status, s, flags);
 }

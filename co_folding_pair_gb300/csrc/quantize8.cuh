@@ -67,6 +67,29 @@ __device__ __forceinline__ uint4 finite(const uint4& v) {
   return make_uint4(finite16x2(v.x), finite16x2(v.y), finite16x2(v.z), finite16x2(v.w));
 }
 
+// Adds a row's eight numbers to the sums of their columns.
+__device__ __forceinline__ void add_row(f2 (&sums)[4], const uint4& v) {
+  sums[0] = add2(sums[0], unpack_bf162(v.x)), sums[1] = add2(sums[1], unpack_bf162(v.y));
+  sums[2] = add2(sums[2], unpack_bf162(v.z)), sums[3] = add2(sums[3], unpack_bf162(v.w));
+}
+// Their sums over the sixteen lanes that have the same columns (all of a lane's bits but 8), written by one of them.
+__device__ __forceinline__ void join_columns(const f2 (&sums)[4], float* to, bool any) {
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 two = split2(sums[e]);
+    v[2 * e] = two.x, v[2 * e + 1] = two.y;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], k < 3 ? 1 << k : 16);
+  if (any && (threadIdx.x & 0x17) == 0) {
+    reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // The larger half of what kLanes neighbouring lanes have.
 template <int kLanes>
 __device__ __forceinline__ uint32_t over_lanes(uint32_t m) {

@@ -138,6 +138,21 @@ def test_linear8_repeats_many_times(P, K, N):
     assert int(off) == 0
 
 
+@pytest.mark.parametrize("rows,K,N", [(70001, 128, 520), (300, 8, 19976), (129, 64, 136), (1, 8, 16), (513, 256, 1000)])
+def test_linear8_bias_gradient_alone_and_together(P, rows, K, N):
+    """Where dy is rounded on its way to dW, its columns are added there; dbias alone has the same bits.  19976 outputs are
+    more tiles than there are pairs of processors, with an odd number of blocks each."""
+    x, w, dy = inputs(rng_of(rows + N), rows, K, N)
+    lin = P.Linear8(w, torch.zeros(N, device="cuda"))
+    every = lin.backward(x, dy, flags=P.FLAG_CHECK)
+    check_backward(every, x, w, dy)
+    for want in (("dbias",), ("dx", "dbias"), ("dw", "dbias")):
+        part = lin.backward(x, dy, want=want, flags=P.FLAG_CHECK)
+        assert all(torch.equal(part[k], every[k]) for k in want)
+    again = lin.backward(x, dy)
+    assert all(torch.equal(again[k], every[k]) for k in again)
+
+
 def test_linear8_no_rows(P):
     w = randn(rng_of(5), 16, 24, dtype=BF)
     lin = P.Linear8(w, torch.ones(16, device="cuda"))
