@@ -211,7 +211,7 @@ struct Backward8 {
     slices_at = x_cols_at + (dw_fused && dw_swapped ? 0 : x_cols.bytes());
     // (as many slices as kMostPairs allow, whatever rounding makes of fewer)
     const int most_z = std::max(n_z, kMostPairs / (tiles_of(N) * tiles_of(K)));
-    sums_at = slices_at + up256(static_cast<size_t>(most_z) * N * K * 4);
+    sums_at = slices_at + (most_z == 1 && !dw_swapped ? 0 : up256(static_cast<size_t>(most_z) * N * K * 4));  // (one slice is dW itself)
     bytes = sums_at + up256(static_cast<size_t>(sums_alone ? 2 * most_z : quantize_columns_parts(rows, N, kMostSms)) * N * 4);
   }
 };

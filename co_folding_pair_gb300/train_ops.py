@@ -50,7 +50,8 @@ class AdamW:
     `state` has the states of all parameters behind one another, each from a multiple of 128 on (`starts`): "m", "v" and
     "count", the steps taken (int32, on the device), and with "8bit" "m_scale" and "v_scale" by blocks, "v" then being
     the codes of v's root.  A checkpoint keeps these tensors, and goes on by copying into them.  The object stands for
-    the memory that its tensors have when it is made, and keeps it.  No parameter or copy may lie over another one, nor a
+    the memory that its tensors have when it is made, and keeps it.  Steps of one object are one after the other: on several
+    streams, or as graphs that are replayed, the caller sees to it.  No parameter or copy may lie over another one, nor a
     gradient over any of them."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, states="float32", copies=None,
@@ -208,6 +209,8 @@ def _backward(packed, N, K, dev, x, dy, dx, dw, dbias, want, stream, flags):  # 
     got = {}
     for name, t, dtype, shape in (("dx", dx, torch.bfloat16, x.shape), ("dw", dw, torch.float32, (N, K)), ("dbias", dbias, torch.float32, (N,))):
         if name not in want:
+            if t is not None:
+                raise ValueError(f"{name} is given but not among what is wanted, {tuple(want)}")
             got[name] = None
         elif t is None:
             got[name] = _empty(shape, dtype, x.device, stream)
@@ -260,7 +263,8 @@ class Linear8:
     __call__ = forward
 
     def backward(self, x, dy, dx=None, dw=None, dbias=None, want=None, stream=None, flags: int = 0):
-        """{"dx", "dw", "dbias"}; dbias is None for a layer without bias, and what `want` does not name."""
+        """{"dx", "dw", "dbias"}; dbias is None for a layer without bias (unless `want` names it), and so is what `want` does
+        not name."""
         if want is None:
             want = ("dx", "dw", "dbias") if self.bias is not None else ("dx", "dw")
         return _backward(self.packed, self.N, self.K, self.device, x, dy, dx, dw, dbias, want, stream, flags)

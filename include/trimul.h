@@ -630,7 +630,7 @@ trimul_status trimul_linear8_pack(const void* W, trimul_dtype type, int N, int K
 
 size_t trimul_linear8_forward_workspace_bytes(int64_t rows, int N, int K);
 
-/* x: bf16 [rows][K]; y: bf16 [rows][N]; bias: f32 [N] or NULL.  TRIMUL_FLAG_CHECK and TRIMUL_FLAG_INJECT_STALL as for
+/* x: bf16 [rows][K]; y: bf16 [rows][N]; bias: f32 [N] or NULL; all 16-byte aligned.  TRIMUL_FLAG_CHECK and TRIMUL_FLAG_INJECT_STALL as for
  * trimul_forward. */
 trimul_status trimul_linear8_forward(const void* packed, const float* bias, const uint16_t* x, int64_t rows, int N, int K,
                                      uint16_t* y, void* workspace, size_t workspace_bytes, int device, void* stream,
@@ -638,8 +638,8 @@ trimul_status trimul_linear8_forward(const void* packed, const float* bias, cons
 
 size_t trimul_linear8_backward_workspace_bytes(int64_t rows, int N, int K);
 
-/* The gradients for dy (bf16 [rows][N]): dx bf16 [rows][K], dW f32 [N][K], dbias f32 [N]; NULL: not wanted.  x and packed are the
- * forward's.  No output may overlap an input or another output. */
+/* The gradients for dy (bf16 [rows][N]): dx bf16 [rows][K], dW f32 [N][K], dbias f32 [N]; NULL: not wanted; all
+ * 16-byte aligned.  x and packed are the forward's.  No output may overlap an input or another output. */
 trimul_status trimul_linear8_backward(const void* packed, const uint16_t* x, const uint16_t* dy, int64_t rows, int N, int K,
                                       uint16_t* dx, float* dW, float* dbias, void* workspace, size_t workspace_bytes, int device,
                                       void* stream, unsigned flags);

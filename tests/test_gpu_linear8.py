@@ -348,3 +348,17 @@ def test_linear8_refusals(P):
         lin.backward(x, dy, dx=x)
     with pytest.raises(Exception, match="16-byte aligned"):
         lin(torch.zeros(32 * 24 + 1, dtype=BF, device="cuda")[1:].view(32, 24))
+
+
+def test_linear8_refuses_a_buffer_for_what_is_not_wanted(P):
+    """It would be left as it is."""
+    g = rng_of(12)
+    x, w, dy = inputs(g, 32, 24, 16)
+    lin, db = P.Linear8(w), torch.empty(16, device="cuda")
+    with pytest.raises(ValueError, match="dbias is given but not among"):
+        lin.backward(x, dy, dbias=db)
+    with pytest.raises(ValueError, match="dw is given but not among"):
+        lin.backward(x, dy, dw=torch.empty(16, 24, device="cuda"), want=("dx",))
+    got = lin.backward(x, dy, dbias=db, want=("dbias",))
+    assert got["dbias"] is db and got["dx"] is None and got["dw"] is None
+    check_backward(got, x, w, dy)

@@ -156,5 +156,7 @@ def test_linear8_sizes(lib):
     assert lib.trimul_linear8_packed_bytes(12, 8) == 0
     assert lib.trimul_linear8_forward_workspace_bytes(-1, 8, 8) == 0
     assert lib.trimul_linear8_backward_workspace_bytes(8, 8, 7) == 0
+    # a wide layer has tiles enough for every pair of processors: dW is summed where it is wanted, not in slices
+    assert lib.trimul_linear8_backward_workspace_bytes(128, 16384, 16384) < 64 << 20
     # codes [N][K] in rows of whole 16 bytes, and the tiles of scales for both of its uses
     assert lib.trimul_linear8_packed_bytes(128, 24) == 128 * 32 + 512 + 512
