@@ -30,6 +30,7 @@ constexpr int kTurns = 2;                       // blocks of a thread that are o
 __global__ void __launch_bounds__(kThreads, 6)
     k11_rows(const uint16_t* __restrict__ x, long long rows, int depth, uint32_t ld, uint32_t groups, FastDiv per_row,
              uint8_t* __restrict__ out, uint8_t* __restrict__ scales, int* status) {
+  let_next_begin();
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   const long long r0 = rows * blockIdx.x / gridDim.x, r1 = rows * (blockIdx.x + 1) / gridDim.x;
   const uint32_t items = static_cast<uint32_t>(r1 - r0) * per_row.d;
@@ -82,6 +83,8 @@ __global__ void __launch_bounds__(kThreads, kSums ? 2 : 3)
     k11_columns(const uint16_t* __restrict__ x, long long rows, int cols, uint32_t ld, uint32_t groups, uint8_t* __restrict__ out,
                 uint8_t* __restrict__ scales, uint32_t row_groups, uint8_t* __restrict__ by_rows, uint8_t* __restrict__ row_scales,
                 float* __restrict__ part, int parts, int* status) {
+  let_next_begin();
+  after_previous();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && status) *status = 0;
   __shared__ uint4 tops[2][kWarps][16];
   __shared__ float sums[kSums ? kWarps : 1][kSums ? kSide : 1];
@@ -276,6 +279,7 @@ __device__ __forceinline__ void join(const Join8& a, long long block, float* sum
 template <int kEach>
 __global__ void __launch_bounds__(kThreads) k11_join(const Join8 a, const Join8 few, unsigned blocks_a) {
   __shared__ float sums[kThreads];
+  after_previous();
   if (blockIdx.x < blocks_a)
     join<kEach>(a, blockIdx.x, sums);
   else
@@ -285,6 +289,8 @@ __global__ void __launch_bounds__(kThreads) k11_join(const Join8 a, const Join8 
 // ------------------------------------------------------------------ sums of columns, as k13_fused8.cu takes them
 __global__ void __launch_bounds__(kThreads) k11_sums(const uint16_t* __restrict__ t, long long rows, int cols, int per_z,
                                                      float* __restrict__ out, int* __restrict__ status) {
+  let_next_begin();
+  after_previous();
   if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
   const int lane = threadIdx.x % 32, z = blockIdx.y / 2, odd = blockIdx.y % 2;
   const int c = blockIdx.x * kSide + 8 * (threadIdx.x / 32 * 2 + (lane >> 3 & 1));
@@ -328,9 +334,9 @@ cudaError_t launch_quantize_columns(const uint16_t* x, long long rows, int cols,
   const dim3 grid(static_cast<unsigned>(l8_blocks(cols)), parts);
   auto kernel = by_rows ? (column_sums ? k11_columns<true, true> : k11_columns<true, false>)
                         : (column_sums ? k11_columns<false, true> : k11_columns<false, false>);
-  kernel<<<grid, kThreads, 0, s>>>(x, rows, cols, static_cast<uint32_t>(c.ld()), static_cast<uint32_t>(c.groups()), out, out + c.scales_at(),
-                                   static_cast<uint32_t>(r.groups()), by_rows, by_rows ? by_rows + r.scales_at() : nullptr, part, parts, status);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch8(kernel, grid, kThreads, 0, status == nullptr, s, x, rows, cols, static_cast<uint32_t>(c.ld()),
+                                static_cast<uint32_t>(c.groups()), out, out + c.scales_at(), static_cast<uint32_t>(r.groups()), by_rows,
+                                by_rows ? by_rows + r.scales_at() : nullptr, part, parts, status);
   return e == cudaSuccess && column_sums ? launch_join(Join8{}, Join8{part, parts, cols, 0, column_sums}, s) : e;
 }
 
@@ -348,19 +354,14 @@ cudaError_t launch_quantize_weight(const void* w, bool f32, int N, int K, uint8_
 
 cudaError_t launch_join(const Join8& a, const Join8& few, cudaStream_t s) {
   const unsigned blocks_few = static_cast<unsigned>((few.n + 31) / 32);
-  if (a.n < 16384) {
-    const unsigned blocks = static_cast<unsigned>((a.n + 31) / 32);
-    k11_join<8><<<blocks + blocks_few, kThreads, 0, s>>>(a, few, blocks);
-  } else {
-    const unsigned blocks = static_cast<unsigned>((a.n + kThreads - 1) / kThreads);
-    k11_join<1><<<blocks + blocks_few, kThreads, 0, s>>>(a, few, blocks);
-  }
-  return cudaGetLastError();
+  const bool short_one = a.n < 16384;
+  const unsigned blocks = static_cast<unsigned>(short_one ? (a.n + 31) / 32 : (a.n + kThreads - 1) / kThreads);
+  return launch8(short_one ? k11_join<8> : k11_join<1>, blocks + blocks_few, kThreads, 0, true, s, a, few, blocks);
 }
 
 cudaError_t launch_column_sums(const uint16_t* t, long long rows, int cols, int per_z, int n_z, float* sums, int* status, cudaStream_t s) {
-  k11_sums<<<dim3(static_cast<unsigned>(l8_blocks(cols)), 2 * n_z), kThreads, 0, s>>>(t, rows, cols, per_z, sums, status);
-  return cudaGetLastError();
+  return launch8(k11_sums, dim3(static_cast<unsigned>(l8_blocks(cols)), 2 * n_z), kThreads, 0, status == nullptr, s, t, rows, cols, per_z,
+                 sums, status);
 }
 
 }  // namespace trimul

@@ -60,6 +60,7 @@ constexpr size_t kSmem = 1024 + STAGES * STAGE_BYTES + BAR_BYTES + BIAS_BYTES;
 template <bool kF32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k12_gemm8(const __grid_constant__ Gemm8Maps maps, const Gemm8Args p) {
+  let_next_begin();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -96,6 +97,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
+  after_previous();
   const uint32_t tmem_base = *tmem_slot_ptr;
   Walk w(p, blockIdx.x >> 1, gridDim.x >> 1);
 
@@ -324,8 +326,7 @@ cudaError_t launch_gemm8(const Gemm8Args& a, const Gemm8Maps& m, bool f32, int p
   if (e != cudaSuccess) return e;
   const long long tiles = static_cast<long long>(a.tiles_m) * a.tiles_n * a.n_z;
   const int grid = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
-  kernel<<<grid, THREADS, kSmem, s>>>(m, a);
-  return cudaGetLastError();
+  return launch8(kernel, grid, THREADS, kSmem, true, s, m, a);
 }
 
 int gemm8_max_pairs(int num_sms) {

@@ -271,6 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
   constexpr uint32_t B0 = P::B0, RAW0 = P::RAW0, AS0 = P::AS0, BS0 = P::BS0, BARS = P::BARS;
   constexpr int TURNS = 16 / EPI_WARPS;  // 64-column blocks of a warp
   constexpr bool kBias = kMore && !kCols, kSums = kMore && kCols;
+  let_next_begin();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -323,6 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
+  after_previous();  // (the bias is older than the call)
   const uint32_t tmem_base = *tmem_slot_ptr;
   Walk w(p.g, blockIdx.x >> 1, gridDim.x >> 1);
 
@@ -714,8 +716,7 @@ cudaError_t launch_fused8(const Fused8Args& a, const Fused8Maps& m, bool cols, i
   if (e != cudaSuccess) return e;
   const long long runs = static_cast<long long>(a.g.tiles_m) * ((a.g.tiles_n + a.g.run - 1) / a.g.run) * a.g.n_z;
   const int grid = 2 * static_cast<int>(runs < pairs ? runs : pairs);
-  kernel<<<grid, threads, smem, s>>>(m.t, m.b, m.b_scale, m.c, a);
-  return cudaGetLastError();
+  return launch8(kernel, grid, threads, smem, !a.clear, s, m.t, m.b, m.b_scale, m.c, a);
 }
 
 }  // namespace trimul

@@ -42,8 +42,26 @@ __host__ __device__ __forceinline__ size_t l8_scale_at(long long row, long long 
   return (static_cast<size_t>(row / 128) * groups + block / 4) * L8_SCALE_TILE + (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4;
 }
 
+// A launch; `early`: it may begin while the kernel before it in the stream runs, whose results it waits for by itself (after_previous).
+// The kernels of a call follow one another so, which hides a launch's latency and a kernel's preparations; the first one, which
+// clears the status word, comes behind all that was before the call.
+template <typename... Params, typename... Args>
+cudaError_t launch8(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, bool early, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = threads;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<Params>(args)...);
+}
+
 // ---------------------------------------------------------------- rounding to 8 bits (k11_quantize8.cu)
-// Each clears the word `status` (or null) for the products behind it.
+// Each clears the word `status` for the products behind it; null: it is not a call's first kernel.
 // bf16 [rows][depth], a scale for each row and 128 columns: the operand {rows, depth}.
 cudaError_t launch_quantize_rows(const uint16_t* x, long long rows, int depth, uint8_t* out, int* status, int num_sms, cudaStream_t s);
 // bf16 [rows][cols], a scale for each column and 128 rows: the operand {cols, rows, mn}; with by_rows (or null) also as
