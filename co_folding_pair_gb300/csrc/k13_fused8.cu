@@ -30,7 +30,9 @@
 //
 // fp32 output: an accumulation takes `chunk` blocks, and the epilogue adds it to
 // what it has written before.  Each element has one thread, whichever accumulator
-// it is in: the order is fixed, and no thread reads what another one wrote.
+// it is in, whose additions to it come in its program's order: the order is fixed.
+// They are done in L2 (red): with a load, an addition and a store the warps waited for the
+// loads, and dW of 2^20 rows of 1024 to 256 channels took 649 us for 569.
 #include "gemm8.cuh"
 #include "quantize8.cuh"
 
@@ -117,6 +119,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src,
 // A box into L2 alone.
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* m, int c0, int c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1) : "memory");
+}
+
+// Adds four fp32 numbers to those at `to`, on their way through L2.
+__device__ __forceinline__ void add_to(float* to, const uint4& v) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)),
+               "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w))
+               : "memory");
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -551,13 +560,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
               for (int s8 = 0; s8 < 8; ++s8) {
                 const int row = row0 + s8;
                 if (row >= p.g.M) continue;
-                float4* const to = reinterpret_cast<float4*>(cz + static_cast<size_t>(row) * p.g.N + col);
-                float4 v = make_float4(__uint_as_float(R[s8].x), __uint_as_float(R[s8].y), __uint_as_float(R[s8].z), __uint_as_float(R[s8].w));
-                if (add) {
-                  const float4 o = *to;
-                  v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-                }
-                *to = v;
+                float* const to = cz + static_cast<size_t>(row) * p.g.N + col;
+                if (add)
+                  add_to(to, R[s8]);
+                else
+                  *reinterpret_cast<uint4*>(to) = R[s8];
               }
             }
           }
