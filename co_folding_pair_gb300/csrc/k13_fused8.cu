@@ -632,7 +632,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
       if (kSums && ok && w.last()) {  // a slice's end: the sums of every other of its blocks, from the first or the second on
         const int odd = team ^ first_turn;
         const long long c = c0 + 8 * lanes;
-        join_columns(sums, p.sums + (static_cast<long long>(w.z) * TEAMS + odd) * p.g.M + c, c < p.g.M);
+        if (w.tn == 0) join_columns(sums, p.sums + (static_cast<long long>(w.z) * TEAMS + odd) * p.g.M + c, c < p.g.M);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sums[e] = both(0.f);
         first_turn = turn;

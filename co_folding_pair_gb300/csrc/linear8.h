@@ -99,7 +99,7 @@ struct Fused8Args {
   Gemm8Args g;
   long long depth;
   int clear;             // clear the status word first
-  float* sums;           // by columns: [2 g.n_z][M], whose sum is that of t's columns; or null.  One tile of N
+  float* sums;           // by columns: [2 g.n_z][M], whose sum is that of t's columns; or null
 };
 struct Fused8Maps {
   CUtensorMap t, b, b_scale, c;

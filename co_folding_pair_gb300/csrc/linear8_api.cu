@@ -21,9 +21,9 @@ constexpr int kMostWidth = 65536;
 constexpr int kMostPairs = 128, kMostSms = 256;  // what workspaces are sized for
 constexpr int kChunk = 32;                       // blocks of 128 rows that a weight gradient's accumulation takes
 // 256-wide tiles of the other operand up to which rounding on the way (k13_fused8.cu) is faster than a pass of its own: each tile
-// rounds again.  Rows (2^20 of them, us): one tile 175 to 280, two (2^19 rows) 264 to 287, four 634 to 560; columns: one 737 to 933, two
-// 457 to 406.  (With dbias 2^20 rows of 256 to 1024 channels took 1184 when its sums still asked for a pass over dy, and take 668.)
-constexpr int kFusedRows = 2, kFusedColumns = 1;
+// rounds again.  us: by rows 2^20 of 256 to 256 channels (one tile) 165 to 280, 2^19 of 512 to 512 (two) 253 to 287, 2^18 of 1024 to 768
+// (three) 321 to 303; by columns 2^20 of 1024 to 256 569 to 933, 2^19 of 512 to 512 346 to 400, 2^18 of 1024 to 1024 (four) 601 to 491.
+constexpr int kFusedRows = 2, kFusedColumns = 2;
 constexpr unsigned long long kTimeoutNs = 4000000000ull, kStallTimeoutNs = 200000000ull;
 constexpr size_t kStatusBytes = 256;
 

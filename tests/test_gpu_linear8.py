@@ -138,7 +138,8 @@ def test_linear8_repeats_many_times(P, K, N):
     assert int(off) == 0
 
 
-@pytest.mark.parametrize("rows,K,N", [(70001, 128, 520), (300, 8, 19976), (129, 64, 136), (1, 8, 16), (513, 256, 1000)])
+@pytest.mark.parametrize("rows,K,N", [(70001, 128, 520), (300, 8, 19976), (129, 64, 136), (1, 8, 16), (513, 256, 1000),
+                                      (5000, 304, 1000), (4097, 512, 264)])
 def test_linear8_bias_gradient_alone_and_together(P, rows, K, N):
     """Where dy is rounded on its way to dW, its columns are added there; dbias alone has the same bits.  19976 outputs are
     more tiles than there are pairs of processors, with an odd number of blocks each."""
