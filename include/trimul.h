@@ -338,9 +338,9 @@ int trimul_kernels_per_forward_host(trimul_handle h, int B, int N);
  * Operators around the layer
  *
  * A pair stack starts from a position signal, adds each layer's output back
- * into its residual stream, and takes an optimiser step from the layers'
- * gradients.  Three operators cover these steps; each enqueues its kernels on
- * `stream`, keeps nothing from one call to the next and takes its workspace,
+ * into its residual stream, passes it through transitions (linear layers) and
+ * takes an optimiser step from all gradients.  The operators below cover these
+ * steps; each enqueues its kernels on `stream`, keeps nothing from one call to the next and takes its workspace,
  * where it needs one, from the caller, so calls on different streams (or
  * captured graphs) that have workspaces and outputs of their own may run at
  * once.  They allocate nothing and do not wait on the host (TRIMUL_FLAG_CHECK
