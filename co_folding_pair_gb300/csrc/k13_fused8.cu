@@ -58,7 +58,7 @@ static_assert(A_COLS_END <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
 constexpr int EPI0 = 2, TEAM_WARPS = 8;
 // How the warps and the shared memory are shared out.  kFew: by rows, with few blocks of depth (FUSED8_FEW_BLOCKS).  There the
 // way out counts: a tile goes by way of shared memory and TMA.  (Turned in registers by shuffles and stored by the warps, 2^20 rows of
-// 256 to 1024 channels take 455 us and with a bias 531; this way 440 and 443.  128 to 128: 119 and 145, now 94 and 102.)
+// 256 to 1024 channels take 455 us and with a bias 531; this way 440 and 443.  128 to 128: 119 and 145, now 91 and 93.)
 // The room is a tile of t's, one team is enough for what is left to round, and the warps have more registers.
 // Else rounding has two teams: with one, or with one tile of t on its way, it falls behind.
 template <bool kFew>
@@ -486,6 +486,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
           }
         };
         if constexpr (kFew) {
+          if (c0 >= p.g.N) {  // nothing of C
+            hand_back();
+            continue;
+          }
           // by way of shared memory, row by row as the tile's map has them (128-byte swizzle); TMA writes what lies in C
           const float* const bias = bias_at + (all_bias ? c0 : (TURNS * (warp - EPI0) + turn) * 64);
           const uint32_t out = base + P::OUT0 + (warp - EPI0) * OUT_BYTES;
@@ -508,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && row < p.g.M && c0 < p.g.N) {
+          if (lane == 0 && row < p.g.M) {
             tma_store_2d(&tm_c, out, c0, row);
             tma_store_commit();
           }
