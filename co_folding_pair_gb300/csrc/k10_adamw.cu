@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kEach = 4;                    // neighbours of a thread
-constexpr int kPart = kThreads * kEach;     // elements of a block
+constexpr int kPart = kThreads * kEach;     // elements that a block takes at once
 constexpr int parts(bool k8) { return k8 ? 2 : 1; }  // of a chunk, which is a block's turn
 constexpr int kBlocksPerSm = 3;             // what the registers allow
 constexpr int kMostBlocks = 1024;
@@ -240,44 +240,73 @@ __device__ __forceinline__ float at_random_low(float x, uint32_t bits) {
   return copysignf(at_random(a + base, bits) - base, x);
 }
 
-// A warp's block as codes; returns its scale.  kRoot: of roots, none negative, the random bits from the hashes' upper halves, and
-// what is above zero keeps a code above zero.
-template <bool kRoot>
-__device__ __forceinline__ float quantize(const float (&f)[4], const uint32_t (&hashes)[4], bool stochastic, uint32_t& codes) {
-  const float scale = __fmul_rn(fmaxf(warp_largest(f), 0x1p-90f), 1.f / 448.f);
-  const float inv = scale < 0x1p100f ? reciprocal_rn(scale) : __frcp_rn(scale);
-  float q[4];
+// A warp's blocks as codes with their scales; the first kParts are of m, the others of roots: none negative, the random bits from
+// the hashes' upper halves, and what is above zero keeps a code above zero.  Few blocks have what takes longer (numbers below the evenly
+// spaced codes, scales past the reciprocal's range), so it is asked once for all.  A lane that is not `inside` is not asked.
+template <int kParts>
+__device__ __forceinline__ void quantize(const float (&f)[2 * kParts][4], const bool (&inside)[kParts], const uint32_t (&hashes)[kParts][4], bool stochastic,
+                                         float (&scale)[2 * kParts], uint32_t (&codes)[2 * kParts]) {
+  float inv[2 * kParts];
+  bool normal = true, low = false;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) q[e] = __fmul_rn(f[e], inv);
-  const bool low = __any_sync(0xffffffffu, !(least_of(q) >= 0x1p-6f));  // few blocks have such small numbers
-  if (stochastic) {
-    uint32_t bits[4];
+  for (int k = 0; k < 2 * kParts; ++k) {
+    scale[k] = __fmul_rn(fmaxf(warp_largest(f[k]), 0x1p-90f), 1.f / 448.f);
+    inv[k] = reciprocal_rn(scale[k]);
+    normal = normal && scale[k] < 0x1p100f;
+  }
+  if (!normal) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bits[e] = kRoot ? hashes[e] >> 12 & 0xffff0u : hashes[e] << 4 & 0xffff0u;
-    if (!low) {
+    for (int k = 0; k < 2 * kParts; ++k) inv[k] = __frcp_rn(scale[k]);
+  }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = at_random(q[e], bits[e]);
-    } else {
+  for (int k = 0; k < 2 * kParts; ++k) low = low || (inside[k % kParts] && !(__fmul_rn(least_of(f[k]), inv[k]) >= 0x1p-6f));
+  low = __any_sync(0xffffffffu, low);
+  auto bits = [&](int k, int e) {
+    const uint32_t h = hashes[k % kParts][e];
+    return k < kParts ? h << 4 & 0xffff0u : h >> 12 & 0xffff0u;
+  };
+  if (!low) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = at_random_low(q[e], bits[e]);
+    for (int k = 0; k < 2 * kParts; ++k) {
+      float q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        q[e] = __fmul_rn(f[k][e], inv[k]);
+        if (stochastic) q[e] = at_random(q[e], bits(k, e));
+      }
+      codes[k] = pack_codes(q);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2 * kParts; ++k) {
+      float q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        q[e] = __fmul_rn(f[k][e], inv[k]);
+        if (stochastic) q[e] = at_random_low(q[e], bits(k, e));
+        if (k >= kParts && f[k][e] > 0.f) q[e] = fmaxf(q[e], 0x1p-9f);
+      }
+      codes[k] = pack_codes(q);
     }
   }
-  if (kRoot && low) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = f[e] > 0.f ? fmaxf(q[e], 0x1p-9f) : q[e];
-  }
-  codes = pack_codes(q);
-  return scale;
 }
 
 // ------------------------------------------------------------------ the step
-__device__ __forceinline__ void roots(const float (&x)[4], float (&r)[4]) {
-  if (__all_sync(0xffffffffu, least_of(x) >= 0x1p-60f && x[0] + x[1] + (x[2] + x[3]) < INFINITY)) {
+template <int kParts>
+__device__ __forceinline__ void roots(const float (&x)[kParts][4], float (&r)[2 * kParts][4]) {  // to r[kParts] ..
+  bool usual = true;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = root(x[e]);
+  for (int u = 0; u < kParts; ++u) usual = usual && least_of(x[u]) >= 0x1p-60f && x[u][0] + x[u][1] + (x[u][2] + x[u][3]) < INFINITY;
+  if (__all_sync(0xffffffffu, usual)) {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[kParts + u][e] = root(x[u][e]);
   } else {  // few blocks: the remainder would fall below fp32's range
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = __fsqrt_rn(x[e]);
+    for (int u = 0; u < kParts; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[kParts + u][e] = __fsqrt_rn(x[u][e]);
   }
 }
 
@@ -315,21 +344,22 @@ __device__ __forceinline__ Entry entry(const Table<N>& tab, int k) {
 struct Raw {
   uint4 p, g, m, v;
 };
+// The first of them: a warp has whole blocks, `parts` beside one another, so that at a tensor's end few warps have less to do.
 template <bool k8>
 __device__ __forceinline__ long long place(const Entry& t, uint32_t chunk) {
-  return static_cast<long long>(chunk - t.chunk) * (kPart * parts(k8)) + threadIdx.x * kEach;
+  return static_cast<long long>(chunk - t.chunk) * (kPart * parts(k8)) + threadIdx.x / 32 * (TRIMUL_STATE_BLOCK * parts(k8)) + threadIdx.x % 32 * kEach;
 }
 
-// kKind: the tensor's kind, or -1 for one that is known only here.
+// kKind: the tensor's kind, or -1 for one that is known only here.  sure: all four are the tensor's, and aligned.
 template <bool k8, int kKind>
-__device__ __forceinline__ void load_part(const Entry& t, long long i, Raw& x) {
+__device__ __forceinline__ void load_part(const Entry& t, long long i, bool sure, Raw& x) {
   const int kind = kKind < 0 ? t.kind : kKind;
-  const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
+  const bool whole = sure || i + 4 <= t.numel, wide = sure || (whole && kind & WIDE);
   x.p = load4(t.param, kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32, i, t.numel, wide);
   x.g = load4(t.grad, kind >> GRAD_SHIFT & 3, i, t.numel, wide);
   if (k8) {
     const long long block = i / TRIMUL_STATE_BLOCK;  // the same for a warp
-    const bool any = block * TRIMUL_STATE_BLOCK < t.numel;
+    const bool any = sure || block * TRIMUL_STATE_BLOCK < t.numel;
     x.m.x = load_codes(t.m, i, t.numel, whole), x.v.x = load_codes(t.v, i, t.numel, whole);
     x.m.y = any ? __float_as_uint(t.m_scale[block]) : 0u, x.v.y = any ? __float_as_uint(t.v_scale[block]) : 0u;
   } else {
@@ -337,62 +367,50 @@ __device__ __forceinline__ void load_part(const Entry& t, long long i, Raw& x) {
   }
 }
 
-template <bool k8, int kKind>
-__device__ __forceinline__ void step_part(const Entry& t, long long i, const Raw& x, const Hyper& h, const Step& s) {
+// p after the step, from the new m and the root of the new v.
+__device__ __forceinline__ float stepped(float p, float m, float r, float keep, const Hyper& h, const Step& s) {
+  return fmaf(-(s.rate * m), reciprocal(fmaf(r, s.over_root_c2, h.eps)), p * keep);
+}
+__device__ __forceinline__ void moments(float g, float& m, float& v, const Hyper& h, const Step& s) {
+  const float ge = __fmul_rn(g, s.clip);
+  m = __fadd_rn(__fmul_rn(h.b1, m), __fmul_rn(h.not_b1, ge));
+  v = __fadd_rn(__fmul_rn(h.b2, v), __fmul_rn(__fmul_rn(h.not_b2, ge), ge));
+}
+// The random bits of four neighbours, the first of them i.
+__device__ __forceinline__ void random_bits(uint32_t tensor_key, long long i, uint32_t (&hashes)[4]) {
+  const uint32_t key = hash(tensor_key + static_cast<uint32_t>(i >> 32)) ^ static_cast<uint32_t>(i);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) hashes[e] = hash(key ^ e);  // (i is a multiple of four)
+}
+__device__ __forceinline__ void round_param(float (&p)[4], const uint32_t (&hashes)[4]) {  // to bf16
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (fabsf(p[e]) < INFINITY) p[e] = __uint_as_float((__float_as_uint(p[e]) + (hash(hashes[e]) & 0xffffu)) & 0xffff0000u);
+}
+
+template <int kKind>
+__device__ __forceinline__ void step_f32(const Entry& t, long long i, const Raw& x, const Hyper& h, const Step& s) {
   const int kind = kKind < 0 ? t.kind : kKind;
   const int ptype = kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32, gtype = kind >> GRAD_SHIFT & 3, copy = kind >> COPY_SHIFT & 3;
-  const bool stochastic = h.stochastic;
   const bool whole = i + 4 <= t.numel, wide = whole && kind & WIDE;
-  if (i / TRIMUL_STATE_BLOCK * TRIMUL_STATE_BLOCK >= t.numel) return;  // the same for a warp
-  float p[4], g[4], m[4], v[4], r[4];
-  unpack4(x.p, ptype, p), unpack4(x.g, gtype, g);
-  if (k8) {
-    unpack_codes(x.m.x, __uint_as_float(x.m.y), m), unpack_codes(x.v.x, __uint_as_float(x.v.y), v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(v[e], v[e]);
-  } else {
-    unpack4(x.m, TRIMUL_F32, m), unpack4(x.v, TRIMUL_F32, v);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float ge = __fmul_rn(g[e], s.clip);
-    m[e] = __fadd_rn(__fmul_rn(h.b1, m[e]), __fmul_rn(h.not_b1, ge));
-    v[e] = __fadd_rn(__fmul_rn(h.b2, v[e]), __fmul_rn(__fmul_rn(h.not_b2, ge), ge));
-  }
-  if (k8) {
-    roots(v, r);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = root_approx(v[e]);
-  }
+  if (i >= t.numel) return;
+  float p[4], g[4], m[4], v[4];
+  unpack4(x.p, ptype, p), unpack4(x.g, gtype, g), unpack4(x.m, TRIMUL_F32, m), unpack4(x.v, TRIMUL_F32, v);
   const float keep = 1.f - s.lr * t.decay;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) p[e] = fmaf(-(s.rate * m[e]), reciprocal(fmaf(r[e], s.over_root_c2, h.eps)), p[e] * keep);
-  uint32_t hashes[4] = {0, 0, 0, 0};
-  if (stochastic && (k8 || ptype == TRIMUL_BF16)) {
-    const uint32_t key = hash(hash(t.index + s.key) + static_cast<uint32_t>(i >> 32)) ^ static_cast<uint32_t>(i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) hashes[e] = hash(key ^ e);  // (i is a multiple of four)
+  for (int e = 0; e < 4; ++e) {
+    moments(g[e], m[e], v[e], h, s);
+    p[e] = stepped(p[e], m[e], root_approx(v[e]), keep, h, s);
   }
   if (copy) store4(t.copy, copy == 1 ? TRIMUL_BF16 : TRIMUL_F16, i, t.numel, wide, p);
-  if (ptype == TRIMUL_BF16 && stochastic) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (fabsf(p[e]) < INFINITY) p[e] = __uint_as_float((__float_as_uint(p[e]) + (hash(hashes[e]) & 0xffffu)) & 0xffff0000u);
+  if (ptype == TRIMUL_BF16 && h.stochastic) {
+    uint32_t hashes[4];
+    random_bits(hash(t.index + s.key), i, hashes);
+    round_param(p, hashes);
   }
   store4(t.param, ptype, i, t.numel, wide, p);
-  if (k8) {
-    const long long block = i / TRIMUL_STATE_BLOCK;
-    uint32_t codes;
-    const float m_scale = quantize<false>(m, hashes, stochastic, codes);
-    store_codes(t.m, i, t.numel, whole, codes);
-    const float v_scale = quantize<true>(r, hashes, stochastic, codes);
-    store_codes(t.v, i, t.numel, whole, codes);
-    if (threadIdx.x % 32 == 0) t.m_scale[block] = m_scale, t.v_scale[block] = v_scale;
-  } else {
-    store4(t.m, TRIMUL_F32, i, t.numel, whole, m);
-    store4(t.v, TRIMUL_F32, i, t.numel, whole, v);
-  }
+  store4(t.m, TRIMUL_F32, i, t.numel, whole, m);
+  store4(t.v, TRIMUL_F32, i, t.numel, whole, v);
 }
 
 // What most programs have gets code without questions about types.
@@ -417,7 +435,7 @@ __device__ __forceinline__ Step run_f32(const Table<N>& tab, const Hyper& h, con
   uint32_t end = tab.chunk[k + 1];
   Raw x;
   auto load = [&](const Entry& t, uint32_t chunk) {
-#define TRIMUL_LOAD(kKind) load_part<false, kKind>(t, place<false>(t, chunk), x)
+#define TRIMUL_LOAD(kKind) load_part<false, kKind>(t, place<false>(t, chunk), false, x)
     TRIMUL_BY_KIND(t.kind, TRIMUL_LOAD);
 #undef TRIMUL_LOAD
   };
@@ -432,7 +450,7 @@ __device__ __forceinline__ Step run_f32(const Table<N>& tab, const Hyper& h, con
       else
         load(t, chunk + 1);
     }
-#define TRIMUL_STEP(kKind) step_part<false, kKind>(t, place<false>(t, chunk), y, h, s)
+#define TRIMUL_STEP(kKind) step_f32<kKind>(t, place<false>(t, chunk), y, h, s)
     TRIMUL_BY_KIND(t.kind, TRIMUL_STEP);
 #undef TRIMUL_STEP
     if (other && chunk + 1 < c1) {
@@ -443,18 +461,93 @@ __device__ __forceinline__ Step run_f32(const Table<N>& tab, const Hyper& h, con
   return s;
 }
 
-// 8-bit states: two fours of a thread are on their way together and then worked on.  The arithmetic is what takes the time; the
-// order above is 2% faster in long tensors and slower, 28 us for 23, in many of some ten thousand bf16 elements.
+// 8-bit states: two fours of a thread are on their way together, and are worked on together.  The arithmetic is what takes the
+// time, by its latency as much as by its instructions: one four after the other takes 185 us for the 96 layers' tensors.
 template <int kKind>
 __device__ __forceinline__ void step_8bit(const Entry& t, uint32_t chunk, const Hyper& h, const int* count, bool& known, Step& s) {
+  constexpr int kParts = parts(true);
+  const int kind = kKind < 0 ? t.kind : kKind;
+  const int ptype = kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32, gtype = kind >> GRAD_SHIFT & 3, copy = kind >> COPY_SHIFT & 3;
   const long long i = place<true>(t, chunk);
-  Raw x[parts(true)];
+  const bool all = i + (kParts - 1) * TRIMUL_STATE_BLOCK + 4 <= t.numel && kind & WIDE;
+  Raw x[kParts];
+  if (all) {
 #pragma unroll
-  for (int u = 0; u < parts(true); ++u) load_part<true, kKind>(t, i + u * kPart, x[u]);
+    for (int u = 0; u < kParts; ++u) load_part<true, kKind>(t, i + u * TRIMUL_STATE_BLOCK, true, x[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) load_part<true, kKind>(t, i + u * TRIMUL_STATE_BLOCK, false, x[u]);
+  }
   if (!known) s = step_of(h, *const_cast<const volatile int*>(count)), known = true;
-  if (!s.run) return;
+  if (!s.run || i / TRIMUL_STATE_BLOCK * TRIMUL_STATE_BLOCK >= t.numel) return;  // the same for a warp
+  float p[kParts][4], v[kParts][4], f[2 * kParts][4];  // f: m, then roots
 #pragma unroll
-  for (int u = 0; u < parts(true); ++u) step_part<true, kKind>(t, i + u * kPart, x[u], h, s);
+  for (int u = 0; u < kParts; ++u) {
+    float g[4];
+    unpack4(x[u].p, ptype, p[u]), unpack4(x[u].g, gtype, g);
+    unpack_codes(x[u].m.x, __uint_as_float(x[u].m.y), f[u]), unpack_codes(x[u].v.x, __uint_as_float(x[u].v.y), v[u]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[u][e] = __fmul_rn(v[u][e], v[u][e]);
+      moments(g[e], f[u][e], v[u][e], h, s);
+    }
+  }
+  // lanes past the tensor's end have zeros, which would send their warp the longer ways: their v is one until the root is taken
+  bool inside[kParts];
+#pragma unroll
+  for (int u = 0; u < kParts; ++u) inside[u] = all || i + u * TRIMUL_STATE_BLOCK < t.numel;
+  if (!all) {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[u][e] = inside[u] ? v[u][e] : 1.f;
+  }
+  roots<kParts>(v, f);
+  if (!all) {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[kParts + u][e] = inside[u] ? f[kParts + u][e] : 0.f;
+  }
+  const float keep = 1.f - s.lr * t.decay;
+  const uint32_t tensor_key = hash(t.index + s.key);
+  uint32_t hashes[kParts][4];
+#pragma unroll
+  for (int u = 0; u < kParts; ++u) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[u][e] = stepped(p[u][e], f[u][e], f[kParts + u][e], keep, h, s);
+    random_bits(tensor_key, i + u * TRIMUL_STATE_BLOCK, hashes[u]);
+  }
+  auto put_params = [&](bool sure) {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) {
+      const long long j = i + u * TRIMUL_STATE_BLOCK;
+      const bool wide = sure || (j + 4 <= t.numel && kind & WIDE);
+      if (copy) store4(t.copy, copy == 1 ? TRIMUL_BF16 : TRIMUL_F16, j, t.numel, wide, p[u]);
+      if (ptype == TRIMUL_BF16 && h.stochastic) round_param(p[u], hashes[u]);
+      store4(t.param, ptype, j, t.numel, wide, p[u]);
+    }
+  };
+  if (all)
+    put_params(true);
+  else
+    put_params(false);
+  float scale[2 * kParts];
+  uint32_t codes[2 * kParts];
+  quantize<kParts>(f, inside, hashes, h.stochastic, scale, codes);
+  auto put_states = [&](bool sure) {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) {
+      const long long j = i + u * TRIMUL_STATE_BLOCK, block = j / TRIMUL_STATE_BLOCK;
+      const bool whole = sure || j + 4 <= t.numel;
+      store_codes(t.m, j, t.numel, whole, codes[u]), store_codes(t.v, j, t.numel, whole, codes[kParts + u]);
+      if (threadIdx.x % 32 == 0 && (sure || j < t.numel)) t.m_scale[block] = scale[u], t.v_scale[block] = scale[kParts + u];
+    }
+  };
+  if (all)
+    put_states(true);
+  else
+    put_states(false);
 }
 template <int N>
 __device__ __forceinline__ Step run_8bit(const Table<N>& tab, const Hyper& h, const int* count, uint32_t c0, uint32_t c1) {
