@@ -86,6 +86,17 @@ def test_linear8(P, rows, K, N, wdt, bias, spread):
     check_backward(lin.backward(x, dy, flags=P.FLAG_CHECK), x, w, dy)
 
 
+@pytest.mark.parametrize("rows,K,N", [(700, 16, 4104), (40000, 256, 2056), (1, 8, 65536), (3, 65536, 16), (130, 384, 5000)])
+def test_linear8_wide_with_a_bias(P, rows, K, N):
+    """More outputs than a block of processors keeps biases for, and the widest layers."""
+    g = rng_of(rows + N)
+    x, w, dy = inputs(g, rows, K, N)
+    b = randn(g, N)
+    lin = P.Linear8(w, b)
+    check_forward(lin(x, flags=P.FLAG_CHECK), x, w, b)
+    check_backward(lin.backward(x, dy, flags=P.FLAG_CHECK), x, w, dy)
+
+
 @pytest.mark.parametrize("rows,K,N", [(100003, 264, 136), (70000, 1024, 520), (4096 * 9 + 1, 8, 8)])
 def test_linear8_gradients_over_many_rows(P, rows, K, N):
     """Several accumulations and slices of rows, tiles with ragged ends."""

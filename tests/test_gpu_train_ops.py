@@ -162,6 +162,17 @@ def test_adamw(P, states, pdt, gdt, cdt, offset, rounding, count):
         check_step(opt, before, params, grads, copies, SIZES, t)
 
 
+@pytest.mark.parametrize("pdt,gdt,cdt,offset,rounding", [(F32, F32, BF, 0, "stochastic"), (BF, BF, None, 0, "nearest"), (F32, F16, None, 1, "stochastic")], ids=str)
+def test_adamw_8bit_where_blocks_take_more_than_one_turn(P, pdt, gdt, cdt, offset, rounding):
+    """Warps with two blocks of states each, one, a part of one, and none."""
+    sizes = [600001, 130, 127, 128, 129, 256, 257, 383, 384, 385, 1, 2047, 2048, 2049, 0, 4095]
+    opt, params, grads, copies = make(P, rng_of(31), sizes, pdt, gdt, cdt, offset, "8bit", rounding, 3)
+    for t in (4, 5):
+        before = snapshot(opt, params, sizes)
+        opt.step(grads, flags=P.FLAG_CHECK)
+        check_step(opt, before, params, grads, copies, sizes, t)
+
+
 @pytest.mark.parametrize("states", ["float32", "8bit"])
 @pytest.mark.parametrize("n", [64, 65, 384, 385, 900])
 def test_adamw_many_tensors(P, states, n):
