@@ -42,10 +42,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kEach = 4;                    // neighbours of a thread
 constexpr int kPart = kThreads * kEach;     // elements that a block takes at once
-// What a kernel is for: states in 32 bits, or in 8 with one or two blocks of them a warp's turn.
-enum Form { F32_STATES = 0, ONE_BLOCK = 1, TWO_BLOCKS = 2 };
-constexpr int parts(Form form) { return form == TWO_BLOCKS ? 2 : 1; }  // of a chunk, which is a thread block's turn
-constexpr int kBlocksPerSm = 3;             // what the registers allow
+// What a kernel is for: states in 32 bits, or in 8 with one or two blocks of them a warp's turn, and the next turn's numbers on their
+// way while one is worked on.
+enum Form { F32_STATES, ONE_BLOCK, TWO_BLOCKS, TWO_AHEAD };
+constexpr int parts(Form form) { return form == TWO_BLOCKS || form == TWO_AHEAD ? 2 : 1; }  // of a chunk, which is a thread block's turn
+constexpr int blocks_per_sm(Form form) { return form == TWO_AHEAD ? 2 : 3; }                // what the registers allow
 constexpr int kMostBlocks = 1024;
 constexpr int kTableSmall = 64, kTableMax = 384;  // tensors of one launch
 static_assert(32 * kEach == TRIMUL_STATE_BLOCK, "a warp has one block of the 8-bit states");
@@ -464,24 +465,35 @@ __device__ __forceinline__ Step run_f32(const Table<N>& tab, const Hyper& h, con
 }
 
 // 8-bit states: two fours of a thread are on their way together, and are worked on together.  The arithmetic is what takes the
-// time, by its latency as much as by its instructions: one four after the other takes 185 us for the 96 layers' tensors.
+// time, by its latency as much as by its instructions: one four after the other takes 185 us for the 96 layers' tensors, together 162, and
+// with the next ones on their way (TWO_AHEAD) 150.
+template <Form kForm>
+struct Raws {
+  Raw x[parts(kForm)];
+};
 template <Form kForm, int kKind>
-__device__ __forceinline__ void step_8bit(const Entry& t, uint32_t chunk, const Hyper& h, const int* count, bool& known, Step& s) {
+__device__ __forceinline__ void load_8bit(const Entry& t, uint32_t chunk, Raws<kForm>& r) {
+  constexpr int kParts = parts(kForm);
+  const int kind = kKind < 0 ? t.kind : kKind;
+  const long long i = place<kForm>(t, chunk);
+  const bool all = i + (kParts - 1) * TRIMUL_STATE_BLOCK + 4 <= t.numel && kind & WIDE;
+  if (all) {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) load_part<true, kKind>(t, i + u * TRIMUL_STATE_BLOCK, true, r.x[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) load_part<true, kKind>(t, i + u * TRIMUL_STATE_BLOCK, false, r.x[u]);
+  }
+}
+template <Form kForm, int kKind>
+__device__ __forceinline__ void step_8bit(const Entry& t, uint32_t chunk, const Raws<kForm>& raws, const Hyper& h, const Step& s) {
+  const Raw (&x)[parts(kForm)] = raws.x;
   constexpr int kParts = parts(kForm);
   const int kind = kKind < 0 ? t.kind : kKind;
   const int ptype = kind & PARAM_BF16 ? TRIMUL_BF16 : TRIMUL_F32, gtype = kind >> GRAD_SHIFT & 3, copy = kind >> COPY_SHIFT & 3;
   const long long i = place<kForm>(t, chunk);
   const bool all = i + (kParts - 1) * TRIMUL_STATE_BLOCK + 4 <= t.numel && kind & WIDE;
-  Raw x[kParts];
-  if (all) {
-#pragma unroll
-    for (int u = 0; u < kParts; ++u) load_part<true, kKind>(t, i + u * TRIMUL_STATE_BLOCK, true, x[u]);
-  } else {
-#pragma unroll
-    for (int u = 0; u < kParts; ++u) load_part<true, kKind>(t, i + u * TRIMUL_STATE_BLOCK, false, x[u]);
-  }
-  if (!known) s = step_of(h, *const_cast<const volatile int*>(count)), known = true;
-  if (!s.run || i / TRIMUL_STATE_BLOCK * TRIMUL_STATE_BLOCK >= t.numel) return;  // the same for a warp
+  if (i / TRIMUL_STATE_BLOCK * TRIMUL_STATE_BLOCK >= t.numel) return;  // the same for a warp
   float p[kParts][4], v[kParts][4], f[2 * kParts][4];  // f: m, then roots
 #pragma unroll
   for (int u = 0; u < kParts; ++u) {
@@ -558,16 +570,49 @@ __device__ __forceinline__ Step run_8bit(const Table<N>& tab, const Hyper& h, co
   int k = tab.begin[blockIdx.x];
   Entry t = entry(tab, k);
   uint32_t end = tab.chunk[k + 1];
-  bool known = false;
-  for (uint32_t chunk = c0; chunk < c1; ++chunk) {
-    if (chunk >= end) {
-      t = entry(tab, ++k);
-      end = tab.chunk[k + 1];
-    }
-#define TRIMUL_STEP(kKind) step_8bit<kForm, kKind>(t, chunk, h, count, known, s)
-    TRIMUL_BY_KIND(t.kind, TRIMUL_STEP);
+  Raws<kForm> x;
+  if constexpr (kForm == TWO_AHEAD) {
+    auto load = [&](const Entry& t, uint32_t chunk) {
+#define TRIMUL_LOAD(kKind) load_8bit<kForm, kKind>(t, chunk, x)
+      TRIMUL_BY_KIND(t.kind, TRIMUL_LOAD);
+#undef TRIMUL_LOAD
+    };
+    load(t, c0);
+    s = step_of(h, *const_cast<const volatile int*>(count));
+    for (uint32_t chunk = c0; chunk < c1 && s.run; ++chunk) {
+      const Raws<kForm> y = x;
+      const bool other = chunk + 1 >= end;
+      if (chunk + 1 < c1) {
+        if (other)
+          load(entry(tab, k + 1), chunk + 1);
+        else
+          load(t, chunk + 1);
+      }
+#define TRIMUL_STEP(kKind) step_8bit<kForm, kKind>(t, chunk, y, h, s)
+      TRIMUL_BY_KIND(t.kind, TRIMUL_STEP);
 #undef TRIMUL_STEP
-    if (!s.run) break;
+      if (other && chunk + 1 < c1) {
+        t = entry(tab, ++k);
+        end = tab.chunk[k + 1];
+      }
+    }
+  } else {
+    bool known = false;
+    for (uint32_t chunk = c0; chunk < c1; ++chunk) {
+      if (chunk >= end) {
+        t = entry(tab, ++k);
+        end = tab.chunk[k + 1];
+      }
+#define TRIMUL_STEP(kKind)                                                                       \
+  do {                                                                                           \
+    load_8bit<kForm, kKind>(t, chunk, x);                                                        \
+    if (!known) s = step_of(h, *const_cast<const volatile int*>(count)), known = true;           \
+    if (s.run) step_8bit<kForm, kKind>(t, chunk, x, h, s);                                       \
+  } while (0)
+      TRIMUL_BY_KIND(t.kind, TRIMUL_STEP);
+#undef TRIMUL_STEP
+      if (!s.run) break;
+    }
   }
   return s;
 }
@@ -583,7 +628,7 @@ __host__ __device__ __forceinline__ uint32_t run_begin(uint32_t chunks, uint32_t
 // one before leaves (their tensors are others), and wait for it before they end, so that what
 // comes behind the last one comes behind all.
 template <Form kForm, int N>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(kForm))
     k10_adamw(const __grid_constant__ Table<N> tab, const __grid_constant__ Hyper h, int* count, int last_launch) {
   let_next_begin();
   const uint32_t c0 = run_begin(tab.chunks, blockIdx.x, gridDim.x), c1 = run_begin(tab.chunks, blockIdx.x + 1, gridDim.x);
@@ -649,7 +694,7 @@ cudaError_t run(const Hyper& h, const trimul_adamw_tensor* t, const trimul_grad_
   Table<N> tab;
   int k = 0;
   for (bool first = true; first || k < n; first = false) {
-    const int grid = fill<kForm>(tab, t, g, n, k, kBlocksPerSm * num_sms);
+    const int grid = fill<kForm>(tab, t, g, n, k, blocks_per_sm(kForm) * num_sms);
     cudaError_t e = cudaSuccess;
     if (first) {  // behind all that was before the call
       k10_adamw<kForm, N><<<grid, kThreads, 0, s>>>(tab, h, count, k >= n);
@@ -675,12 +720,18 @@ cudaError_t launch_adamw(const trimul_adamw_params& p, const trimul_adamw_tensor
   h.seed = p.seed, h.stochastic = p.rounding == TRIMUL_ROUND_STOCHASTIC;
   if (p.states != TRIMUL_STATES_E4M3)
     return n <= kTableSmall ? run<F32_STATES, kTableSmall>(h, t, g, n, count, num_sms, s) : run<F32_STATES, kTableMax>(h, t, g, n, count, num_sms, s);
-  if (n > kTableSmall) return run<TWO_BLOCKS, kTableMax>(h, t, g, n, count, num_sms, s);
-  // As long as a thread block has one turn at most, one block of states a warp: a layer's 98k numbers take 5.3 us, with two 6.1.
+  // us, 152 SMs:                                       one block   two   two, ahead
+  //   a layer's 98k numbers                                 5.3     6.1
+  //   460k (as many turns of one block as thread blocks)    5.1     5.1
+  //   3.7M bf16 numbers in 240 tensors                     27      22.5    24.7
+  //   37.8M in 960 tensors                                198     162     150
   long long turns = 0;
   for (int k = 0; k < n; ++k) turns += (t[k].numel + kPart - 1) / kPart;
-  return turns <= kBlocksPerSm * num_sms ? run<ONE_BLOCK, kTableSmall>(h, t, g, n, count, num_sms, s)
-                                         : run<TWO_BLOCKS, kTableSmall>(h, t, g, n, count, num_sms, s);
+  const bool small = n <= kTableSmall;
+  if (turns > 32ll * num_sms)
+    return small ? run<TWO_AHEAD, kTableSmall>(h, t, g, n, count, num_sms, s) : run<TWO_AHEAD, kTableMax>(h, t, g, n, count, num_sms, s);
+  if (small && turns <= blocks_per_sm(ONE_BLOCK) * num_sms) return run<ONE_BLOCK, kTableSmall>(h, t, g, n, count, num_sms, s);
+  return small ? run<TWO_BLOCKS, kTableSmall>(h, t, g, n, count, num_sms, s) : run<TWO_BLOCKS, kTableMax>(h, t, g, n, count, num_sms, s);
 }
 
 }  // namespace trimul
