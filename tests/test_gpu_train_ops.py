@@ -173,6 +173,18 @@ def test_adamw_8bit_where_blocks_take_more_than_one_turn(P, pdt, gdt, cdt, offse
         check_step(opt, before, params, grads, copies, sizes, t)
 
 
+@pytest.mark.parametrize("pdt,gdt,cdt,offset", [(F32, F32, BF, 0), (BF, F32, None, 1)], ids=str)
+@pytest.mark.parametrize("many", [False, True])
+def test_adamw_8bit_where_blocks_take_many_turns(P, pdt, gdt, cdt, offset, many):
+    """Past five million numbers, from tensor to tensor within a block's turns; with more tensors than the small table has."""
+    sizes = [70001 + 128 * k for k in range(70)] + [1, 0, 136, 2047, 2049] if many else [3000001, 2049, 128, 2100000, 1, 0, 257]
+    opt, params, grads, copies = make(P, rng_of(32), sizes, pdt, gdt, cdt, offset, "8bit", "stochastic", 3)
+    for t in (4, 5):
+        before = snapshot(opt, params, sizes)
+        opt.step(grads, flags=P.FLAG_CHECK)
+        check_step(opt, before, params, grads, copies, sizes, t)
+
+
 @pytest.mark.parametrize("states", ["float32", "8bit"])
 @pytest.mark.parametrize("n", [64, 65, 384, 385, 900])
 def test_adamw_many_tensors(P, states, n):
