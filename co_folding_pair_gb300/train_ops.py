@@ -13,6 +13,7 @@ they raise.
 
 from __future__ import annotations
 
+import functools
 
 import numpy as np
 import torch
@@ -141,6 +142,26 @@ class AdamW:
 
 
 # ------------------------------------------------------------------ linear layer in 8 bits
+# The smallest calls' workspace is the word in which a kernel says that it gave up.  Calls on one stream come one after the other, so
+# each stream keeps one (an allocation is a tenth of such a call's time); what is captured has its own.
+_WORD = 256
+_words = {}
+
+
+def _workspace(need, dev, device, stream, raw):
+    if need > _WORD or stream is not None or torch.cuda.is_current_stream_capturing():
+        return _empty(need, torch.uint8, device, stream)
+    word = _words.get((dev, raw))
+    if word is None:
+        word = _words[dev, raw] = _empty(_WORD, torch.uint8, device, stream)
+    return word
+
+
+@functools.lru_cache(maxsize=1024)
+def _forward_bytes(rows, N, K):
+    return _lib.load().trimul_linear8_forward_workspace_bytes(rows, N, K)
+
+
 def _rows(x, width, dev, name):
     """The rows of a bf16 tensor [..., width]."""
     if x.dim() < 1 or x.shape[-1] != width:
@@ -148,6 +169,11 @@ def _rows(x, width, dev, name):
     if not _fits(x, torch.bfloat16, x.shape, dev):
         _refuse(x, torch.bfloat16, x.shape, dev, name)
     return x.numel() // width
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_bytes(rows, N, K):
+    return _lib.load().trimul_linear8_backward_workspace_bytes(rows, N, K)
 
 
 def trimul_linear8_pack(weight, packed=None, stream=None, flags: int = 0):
@@ -178,17 +204,18 @@ def trimul_linear8_forward(packed, N, K, x, bias=None, out=None, stream=None, fl
 
 
 def _forward(packed, N, K, dev, x, bias, out, stream, flags):  # packed and bias have been looked at
-    rows = _rows(x, K, dev, "x")
-    shape = (*x.shape[:-1], N)
+    shape = x.shape
+    if len(shape) == 0 or shape[-1] != K or not _fits(x, torch.bfloat16, shape, dev):
+        _rows(x, K, dev, "x")
+    rows, shape = x.numel() // K, (*shape[:-1], N)
     if out is None:
         out = _empty(shape, torch.bfloat16, x.device, stream)
     elif not _fits(out, torch.bfloat16, shape, dev):
         _refuse(out, torch.bfloat16, shape, dev, "out")
-    lib = _lib.load()
-    need = lib.trimul_linear8_forward_workspace_bytes(rows, N, K)
-    ws = _empty(need, torch.uint8, x.device, stream)
-    _check(lib.trimul_linear8_forward(packed.data_ptr(), _ptr(bias), x.data_ptr(), rows, N, K, out.data_ptr(), ws.data_ptr(), need,
-                                      dev, _raw(stream, dev), flags))
+    need, raw = _forward_bytes(rows, N, K), _raw(stream, dev)
+    ws = _workspace(need, dev, x.device, stream, raw)
+    _check(_lib.load().trimul_linear8_forward(packed.data_ptr(), _ptr(bias), x.data_ptr(), rows, N, K, out.data_ptr(), ws.data_ptr(), need,
+                                              dev, raw, flags))
     return out
 
 
@@ -218,11 +245,10 @@ def _backward(packed, N, K, dev, x, dy, dx, dw, dbias, want, stream, flags):  # 
             if not _fits(t, dtype, shape, dev):
                 _refuse(t, dtype, shape, dev, name)
             got[name] = t
-    lib = _lib.load()
-    need = lib.trimul_linear8_backward_workspace_bytes(rows, N, K)
+    need = _backward_bytes(rows, N, K)
     ws = _empty(need, torch.uint8, x.device, stream)
-    _check(lib.trimul_linear8_backward(packed.data_ptr(), x.data_ptr(), dy.data_ptr(), rows, N, K, _ptr(got["dx"]), _ptr(got["dw"]),
-                                       _ptr(got["dbias"]), ws.data_ptr(), need, dev, _raw(stream, dev), flags))
+    _check(_lib.load().trimul_linear8_backward(packed.data_ptr(), x.data_ptr(), dy.data_ptr(), rows, N, K, _ptr(got["dx"]),
+                                               _ptr(got["dw"]), _ptr(got["dbias"]), ws.data_ptr(), need, dev, _raw(stream, dev), flags))
     return got
 
 

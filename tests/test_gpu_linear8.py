@@ -272,6 +272,28 @@ def test_linear8_in_a_graph_and_on_streams(P):
     check_backward(g, *passes[0][:3])
 
 
+def test_linear8_small_calls_of_many_streams(P):
+    """Each stream keeps the word in which its calls' kernels say that they gave up."""
+    x, w, _ = inputs(rng_of(13), 300, 32, 72)
+    lin = P.Linear8(w)
+    want = lin(x)
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(50):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(lin(x))
+    with pytest.raises(Exception, match="bounded wait"):  # on one of them a stall, which no other call sees
+        with torch.cuda.stream(streams[2]):
+            lin(x, flags=P.FLAG_CHECK | P.FLAG_INJECT_STALL)
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(lin(x, flags=P.FLAG_CHECK))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
+
+
 def test_linear8_writes_nothing_else(P):
     """Outputs, workspaces and packed weights with bands around them."""
     from co_folding_pair_gb300 import _lib
