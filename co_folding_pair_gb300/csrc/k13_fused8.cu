@@ -53,9 +53,9 @@ constexpr uint32_t BIAS_BYTES = 8192;
 constexpr int ALL_BIAS = BIAS_BYTES / 4;  // up to so many outputs it is all there; past that each epilogue warp has that of its tile
 constexpr uint32_t TMEM_COLS = 512, ACC_STEP = 192;
 constexpr uint32_t A_COLS = 448, A_SETS = 8, B_COLS = 480, B_SETS = 4;
-constexpr uint32_t A_COLS_END = A_COLS + 4 * A_SETS;
-static_assert(A_COLS_END <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
-constexpr int EPI0 = 2, TEAM_WARPS = 8;
+static_assert(A_COLS + 4 * A_SETS <= B_COLS && B_COLS + 8 * B_SETS <= TMEM_COLS, "TMEM");
+constexpr int EPI0 = 2, EPI_WARPS = 8, ROUND0 = EPI0 + EPI_WARPS, TEAM_WARPS = 8;
+constexpr int TURNS = 16 / EPI_WARPS;  // 64-column blocks of an epilogue warp
 // How the warps and the shared memory are shared out.  kFew: by rows, with few blocks of depth (FUSED8_FEW_BLOCKS).  There the
 // way out counts: a tile goes by way of shared memory and TMA.  (Turned in registers by shuffles and stored by the warps, 2^20 rows of
 // 256 to 1024 channels take 455 us and with a bias 531; this way 440 and 443.  128 to 128: 119 and 145, now 91 and 93.)
@@ -64,8 +64,7 @@ constexpr int EPI0 = 2, TEAM_WARPS = 8;
 template <bool kFew>
 struct Plan {
   static constexpr int A_SLOTS = 3, B_STAGES = 3, RAW_SLOTS = kFew ? 1 : 2;
-  static constexpr int EPI_WARPS = 8, TEAMS = kFew ? 1 : 2;
-  static constexpr int ROUND0 = EPI0 + EPI_WARPS, RAW = ROUND0 + TEAMS * TEAM_WARPS, THREADS = 32 * (RAW + 1);
+  static constexpr int TEAMS = kFew ? 1 : 2, RAW = ROUND0 + TEAMS * TEAM_WARPS, THREADS = 32 * (RAW + 1);
   // rings: A's codes, B's codes, tiles of t, what is on its way out, A's and B's scales
   static constexpr uint32_t B0 = A_SLOTS * CODE_BYTES, RAW0 = B0 + B_STAGES * B_BYTES, OUT0 = RAW0 + RAW_SLOTS * RAW_BYTES;
   static constexpr uint32_t AS0 = OUT0 + (kFew ? EPI_WARPS * OUT_BYTES : 0);
@@ -276,9 +275,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
     k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_b_scale, const __grid_constant__ CUtensorMap tm_c, const Fused8Args p) {
   using P = Plan<kFew>;
-  constexpr int A_SLOTS = P::A_SLOTS, B_STAGES = P::B_STAGES, RAW_SLOTS = P::RAW_SLOTS, EPI_WARPS = P::EPI_WARPS, TEAMS = P::TEAMS, ROUND0 = P::ROUND0, RAW = P::RAW;
+  constexpr int A_SLOTS = P::A_SLOTS, B_STAGES = P::B_STAGES, RAW_SLOTS = P::RAW_SLOTS, TEAMS = P::TEAMS, RAW = P::RAW;
   constexpr uint32_t B0 = P::B0, RAW0 = P::RAW0, AS0 = P::AS0, BS0 = P::BS0, BARS = P::BARS;
-  constexpr int TURNS = 16 / EPI_WARPS;  // 64-column blocks of a warp
   constexpr bool kBias = kMore && !kCols, kSums = kMore && kCols;
   let_next_begin();
   extern __shared__ uint8_t smem_raw[];
@@ -451,10 +449,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
   } else if (warp < ROUND0) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;               // TMEM lane quadrant of this warp
-    // which of the four 64-column blocks: with two a warp, 0 the outer two and 1 the inner two (an element has one thread, whichever
-    // accumulator it is in)
+    // 0: the outer two of the 64-column blocks, 1: the inner two (an element has one thread, whichever accumulator it is in)
     const int sub = (warp - EPI0) >> 2;
-    auto block_of = [&](int turn, int acc) { return TURNS == 1 ? sub : (turn ^ acc) ? sub : 3 - sub; };
+    auto block_of = [&](int turn, int acc) { return (turn ^ acc) ? sub : 3 - sub; };
     const uint32_t gb = lane & 7, ga = lane >> 3;
     int acc = 0;
     uint32_t aphase = 0;
