@@ -90,10 +90,11 @@ int pairs_of(int device, int sms) {
 
 int tiles_of(int n) { return (n + L8_TILE - 1) / L8_TILE; }
 
-// Slices of `blocks` of depth for M x N outputs: one tile a pair, each a multiple of four blocks (a group of scales).
+// Slices of `blocks` of depth for M x N outputs: one tile a pair, each a multiple of four blocks (a group of scales).  None
+// where there are no blocks (the workspace of no rows is asked for too).
 void slices(int M, int N, int blocks, int pairs, int* per_z, int* n_z) {
   const int tiles = tiles_of(M) * tiles_of(N), want = std::max(1, std::min((blocks + 3) / 4, pairs / tiles));
-  *per_z = ((blocks + want - 1) / want + 3) / 4 * 4;
+  *per_z = std::max(4, ((blocks + want - 1) / want + 3) / 4 * 4);
   *n_z = (blocks + *per_z - 1) / *per_z;
 }
 

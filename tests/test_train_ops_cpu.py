@@ -160,3 +160,10 @@ def test_linear8_sizes(lib):
     assert lib.trimul_linear8_backward_workspace_bytes(128, 16384, 16384) < 64 << 20
     # codes [N][K] in rows of whole 16 bytes, and the tiles of scales for both of its uses
     assert lib.trimul_linear8_packed_bytes(128, 24) == 128 * 32 + 512 + 512
+
+
+@pytest.mark.parametrize("N,K", [(8, 8), (264, 136), (256, 1024), (65536, 65536)])
+def test_linear8_workspaces_of_no_rows(lib, N, K):
+    """Asked for before each call, one of no rows among them, which needs no more than the smallest one with rows."""
+    assert 0 < lib.trimul_linear8_forward_workspace_bytes(0, N, K) <= lib.trimul_linear8_forward_workspace_bytes(1, N, K)
+    assert 0 < lib.trimul_linear8_backward_workspace_bytes(0, N, K) <= lib.trimul_linear8_backward_workspace_bytes(1, N, K)
