@@ -65,20 +65,22 @@ template <bool kFew>
 struct Plan {
   static constexpr int A_SLOTS = 3, B_STAGES = 3, RAW_SLOTS = kFew ? 1 : 2;
   static constexpr int TEAMS = kFew ? 1 : 2, RAW = ROUND0 + TEAMS * TEAM_WARPS, THREADS = 32 * (RAW + 1);
+  static constexpr int EMPTIES = B_STAGES * TEAMS;  // barriers of B's stages that say they are free
   // rings: A's codes, B's codes, tiles of t, what is on its way out, A's and B's scales
   static constexpr uint32_t B0 = A_SLOTS * CODE_BYTES, RAW0 = B0 + B_STAGES * B_BYTES, OUT0 = RAW0 + RAW_SLOTS * RAW_BYTES;
   static constexpr uint32_t AS0 = OUT0 + (kFew ? EPI_WARPS * OUT_BYTES : 0);
   static constexpr uint32_t BS0 = AS0 + A_SLOTS * L8_SCALE_TILE, BARS = BS0 + B_STAGES * 2 * L8_SCALE_TILE;
   static constexpr size_t SMEM = 1024 + BARS + BAR_BYTES + BIAS_BYTES;
   static_assert(SMEM <= 232448, "shared memory of a CTA");
-  static_assert(8 * (2 * B_STAGES + 2 * A_SLOTS + 2 * RAW_SLOTS + 6) + 4 <= BAR_BYTES && 16 * 64 * 4 <= BIAS_BYTES, "the barriers and the bias fit");
+  static_assert(8 * (B_STAGES + EMPTIES + 2 * A_SLOTS + 2 * RAW_SLOTS + 6) + 4 <= BAR_BYTES && 16 * 64 * 4 <= BIAS_BYTES, "the barriers and the bias fit");
   static_assert(kFew ? FUSED8_FEW_BLOCKS <= A_SLOTS : A_SLOTS == B_STAGES, "a run's codes wait in their slots, or go with a stage of B's");
   static_assert(A_SETS > B_STAGES + 1 && B_STAGES <= B_SETS, "a set's readers are done when it is written again");
-  // A team waits for its own blocks alone.  A wait that has skipped a use of its barrier would take the phase before for the one it
-  // wants, and pass at once.  So a slot of t is always the same team's.  With three slots of codes and two teams a team comes to a slot every
-  // second use; what it skipped (the multiplications of the block six before its own) was done when it was last let on, by those of the block five before.
+  // A team waits for its own blocks alone.  A wait that has skipped a phase of its barrier would take the one before for the one it
+  // wants, and pass at once.  So a slot of t is always the same team's, and a stage of B, whose uses fall to the teams in
+  // turns, has a barrier for each: block m's multiplications arrive at barrier m % EMPTIES, and the block B_STAGES behind,
+  // always the same team's, waits there.
   static_assert(RAW_SLOTS % TEAMS == 0, "a slot of t is always the same team's");
-  static_assert(TEAMS == 1 || (TEAMS == 2 && (A_SLOTS == 3 || A_SLOTS % 2 == 0)), "a team knows its slot's phase");
+  static_assert(EMPTIES % TEAMS == 0 && EMPTIES % B_STAGES == 0, "a free stage's barrier is always the same team's");
 };
 constexpr uint32_t SITE_ROUND = 0x500;
 constexpr uint32_t kIdesc128 = (kIdesc8 & ~(0x1Fu << 24)) | ((ROWS >> 4) << 24);
@@ -275,7 +277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
     k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_b_scale, const __grid_constant__ CUtensorMap tm_c, const Fused8Args p) {
   using P = Plan<kFew>;
-  constexpr int A_SLOTS = P::A_SLOTS, B_STAGES = P::B_STAGES, RAW_SLOTS = P::RAW_SLOTS, TEAMS = P::TEAMS, RAW = P::RAW;
+  constexpr int A_SLOTS = P::A_SLOTS, B_STAGES = P::B_STAGES, RAW_SLOTS = P::RAW_SLOTS, TEAMS = P::TEAMS, EMPTIES = P::EMPTIES,
+                RAW = P::RAW;
   constexpr uint32_t B0 = P::B0, RAW0 = P::RAW0, AS0 = P::AS0, BS0 = P::BS0, BARS = P::BARS;
   constexpr bool kBias = kMore && !kCols, kSums = kMore && kCols;
   let_next_begin();
@@ -284,8 +287,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
   const uint32_t bars = base + BARS;
-  // bfull bempty [B_STAGES] afull aempty [A_SLOTS] rfull rempty [RAW_SLOTS] tfull tempty [2] over drain, then the TMEM base word
-  const uint32_t bfull0 = bars, bempty0 = bfull0 + 8 * B_STAGES, afull0 = bempty0 + 8 * B_STAGES, aempty0 = kFew ? afull0 + 8 * A_SLOTS : bempty0;
+  // bfull [B_STAGES] bempty [EMPTIES] afull aempty [A_SLOTS] rfull rempty [RAW_SLOTS] tfull tempty [2] over drain, then the TMEM base word
+  const uint32_t bfull0 = bars, bempty0 = bfull0 + 8 * B_STAGES, afull0 = bempty0 + 8 * EMPTIES, aempty0 = kFew ? afull0 + 8 * A_SLOTS : bempty0;
   const uint32_t rfull0 = afull0 + 16 * A_SLOTS, rempty0 = rfull0 + 8 * RAW_SLOTS;
   const uint32_t tfull0 = rempty0 + 8 * RAW_SLOTS, tempty0 = tfull0 + 16, over = tempty0 + 16, drain = over + 8;
   const uint32_t tmem_slot = drain + 8;
@@ -301,8 +304,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
   if (threadIdx.x == 0) {
     for (int s = 0; s < B_STAGES; ++s) {
       mbar_init(bfull0 + 8 * s, 1);            // one expect_tx arrival; bytes that both CTAs load
-      mbar_init(bempty0 + 8 * s, 2);           // one commit of each CTA: B's tile is written for both
     }
+    for (int s = 0; s < EMPTIES; ++s) mbar_init(bempty0 + 8 * s, 2);  // one commit of each CTA: B's tile is written for both
     for (int s = 0; s < A_SLOTS; ++s) {
       mbar_init(afull0 + 8 * s, TEAM_WARPS);
       if (kFew) mbar_init(aempty0 + 8 * s, 1);  // one commit
@@ -341,17 +344,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
       tma_prefetch_desc(&tm_b);
       tma_prefetch_desc(&tm_b_scale);
       const int groups = (p.g.blocks + 3) / 4, b_tiles = (p.g.N + ROWS - 1) / ROWS;
-      int stage = 0;
-      uint32_t phase = 0;
+      int stage = 0, empty = EMPTIES - B_STAGES;
+      uint32_t phase = 0, ephase = 1;  // (the first uses pass)
       long long issued = 0;
       bool ok = true;
       for (; w.more() && ok; w.next()) {
         const int bt = w.tn * 2 + static_cast<int>(rank);
         const int rb = bt < b_tiles ? bt * ROWS : 0;  // (a box wholly past N loads row 0)
         for (int b = w.b0; b < w.b1; ++b) {
-          if (!mbar_wait(bempty0 + 8 * stage, phase ^ 1u, st, SITE_PRODUCER)) {
+          if (!mbar_wait(bempty0 + 8 * empty, ephase, st, SITE_PRODUCER)) {
             ok = false;
             break;
+          }
+          if (++empty == EMPTIES) {
+            empty = 0;
+            ephase ^= 1u;
           }
           const uint32_t fb = bfull0 + 8 * stage;
           const bool scales = b % 4 == 0 || b == w.b0;
@@ -387,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
       const uint64_t as0 = sdesc_scales(base + AS0), bs0 = sdesc_scales(base + BS0);
       const uint32_t astep = kCols ? 32 * 128 >> 4 : 32 >> 4, bstep = p.g.b_mn ? 32 * 128 >> 4 : 32 >> 4;
       const uint32_t majors = static_cast<uint32_t>(kCols) << 15 | static_cast<uint32_t>(p.g.b_mn) << 16;
-      int stage = 0, acc = 0, slot = 0, run_slot = 0;
+      int stage = 0, empty = 0, acc = 0, slot = 0, run_slot = 0;
       uint32_t phase = 0, sphase = 0, run_phase = 0, aphase = 0, ophase = 1, a_set = 0, b_set = 0;
       bool ok = true;
       for (; w.more() && ok; w.next()) {
@@ -422,7 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
           for (int kk = 0; kk < L8_BLOCK / 32; ++kk)
             mma_block_scaled(d_tmem, adesc0 + aoff + kk * astep, bdesc0 + boff + kk * bstep, idesc, sfa, sfb,
                                   (b != w.b0 || kk != 0) ? 1u : 0u);
-          mma_commit_both(bempty0 + 8 * stage);
+          mma_commit_both(bempty0 + 8 * empty);
+          if (++empty == EMPTIES) empty = 0;
           if (give_back) mma_commit(aempty0 + 8 * slot);
           if (++stage == B_STAGES) {
             stage = 0;
@@ -584,8 +592,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
     const int team = (warp - ROUND0) / TEAM_WARPS, t = threadIdx.x - 32 * (ROUND0 + team * TEAM_WARPS);
     // by columns: the chunk and the first row
     const int lanes = kCols ? t / 32 * 2 + (lane >> 3 & 1) : t % 8, group = kCols ? (lane & 7) + (lane >> 4) * 8 : t / 8;
-    int slot = 0, raw_slot = 0, turn = 0;
-    uint32_t sphase = 0, rphase = 0;
+    constexpr int kFrees = kFew ? A_SLOTS : EMPTIES;  // the barriers that say that a slot of A's is free
+    int slot = 0, free = kFrees - A_SLOTS, raw_slot = 0, turn = 0;
+    uint32_t fphase = 1, rphase = 0;
     bool ok = true;
     f2 sums[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
     int first_turn = 0;
@@ -594,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
       for (int b = w.b0; b < w.b1; ++b) {
         if (turn == team) {
           ok = __all_sync(0xffffffffu, mbar_wait(rfull0 + 8 * raw_slot, rphase, st, SITE_ROUND) &&
-                                           mbar_wait(aempty0 + 8 * slot, sphase ^ 1u, st, SITE_ROUND));
+                                           mbar_wait(aempty0 + 8 * free, fphase, st, SITE_ROUND));
           if (!ok) break;
           const uint32_t sr = base + RAW0 + raw_slot * RAW_BYTES, sa = base + slot * CODE_BYTES, ss = base + AS0 + slot * L8_SCALE_TILE;
           Numbers x;
@@ -621,9 +630,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
           if (lane == 0) mbar_arrive(afull0 + 8 * slot);
         }
         if (++turn == TEAMS) turn = 0;
-        if (++slot == A_SLOTS) {
-          slot = 0;
-          sphase ^= 1u;
+        if (++slot == A_SLOTS) slot = 0;
+        if (++free == kFrees) {
+          free = 0;
+          fphase ^= 1u;
         }
         if (++raw_slot == RAW_SLOTS) {
           raw_slot = 0;
