@@ -10,11 +10,11 @@
 // write and read half of the input again.  The price is that a tile of t is
 // rounded once for every 256 columns of C, unless it has few blocks (below).
 //
-// Two CTAs of a cluster have 128 rows of A each and one tile of B between them:
-// each loads half of it (TMA) for both.  Unlike k12_gemm8.cu each multiplies by
-// itself (M = 128, N = 256, cta_group::1): as one pair, the odd CTA's codes had to be made
-// known to the even CTA by a release at cluster scope for every block, which takes
-// about as long as rounding it (550 to 860 us at 2^20 rows of 1024 to 256, whichever warps did it).
+// Two neighbouring CTAs have 128 rows of a tile each, and share nothing else: each loads
+// all of B's tile (TMA; the second read is L2's) and multiplies by itself (M = 128, N = 256,
+// cta_group::1).  As one pair as in k12_gemm8.cu, the odd CTA's codes had to be made known to the even CTA by a release at
+// cluster scope for every block, which takes about as long as rounding it (550 to 860 us at 2^20 rows of 1024 to 256,
+// whichever warps did it).
 //
 // Per CTA: warp 0 loads B and the last one the CTA's tile of t, 1 issues the
 // multiplications, 2..9 are the epilogue, and the others round, in teams of eight.  A tile of t waits as bf16
@@ -97,21 +97,6 @@ __device__ __forceinline__ void mma_block_scaled(uint32_t d_tmem, uint64_t adesc
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(sdesc) : "memory");
 }
-// Arrive once at the offset `bar` in both CTAs when what this thread has issued is done.
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-// A box to the same place in both CTAs, its bytes counted on the barrier at the same place in each.
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, uint32_t src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(c0),
                "r"(c1)
@@ -273,7 +258,7 @@ __device__ __forceinline__ void round_cols(const Numbers& x, f2 (&sums)[4], uint
 // kMore: with a bias; by columns, with the sums of t's columns (dbias), which the rounding warps take as they pass: a lane adds its
 // eight rows of each of its team's blocks, the sixteen lanes of a column are joined, and every slice leaves two sums.
 template <bool kCols, bool kFew, bool kMore>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS, 1)
+__global__ void __launch_bounds__(Plan<kFew>::THREADS, 1)
     k13_fused8(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_b,
                const __grid_constant__ CUtensorMap tm_b_scale, const __grid_constant__ CUtensorMap tm_c, const Fused8Args p) {
   using P = Plan<kFew>;
@@ -296,16 +281,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
 
   const KStatus st{p.g.status, p.g.timeout_ns};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank = blockIdx.x & 1;  // which half of a tile's rows
 
   // a first kernel has nobody before it to clear the status word: the first block does, and no other looks at it sooner
   // than a millisecond into a wait
   if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.g.status = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < B_STAGES; ++s) {
-      mbar_init(bfull0 + 8 * s, 1);            // one expect_tx arrival; bytes that both CTAs load
+      mbar_init(bfull0 + 8 * s, 1);            // one expect_tx arrival
     }
-    for (int s = 0; s < EMPTIES; ++s) mbar_init(bempty0 + 8 * s, 2);  // one commit of each CTA: B's tile is written for both
+    for (int s = 0; s < EMPTIES; ++s) mbar_init(bempty0 + 8 * s, 1);  // one commit
     for (int s = 0; s < A_SLOTS; ++s) {
       mbar_init(afull0 + 8 * s, TEAM_WARPS);
       if (kFew) mbar_init(aempty0 + 8 * s, 1);  // one commit
@@ -332,14 +317,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
     for (int i = threadIdx.x; i < ALL_BIAS; i += P::THREADS) bias_at[i] = i < p.g.N ? p.g.bias[i] : 0.f;
   }
   tc_fence_before();
-  cluster_sync_all();
+  __syncthreads();
   tc_fence_after();
   after_previous();  // (the bias is older than the call)
   const uint32_t tmem_base = *tmem_slot_ptr;
   Walk w(p.g, blockIdx.x >> 1, gridDim.x >> 1);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer of B: this CTA's half, for both
+    // ------------------------------------------------------------ producer of B
     if (lane == 0 && !p.g.stall) {
       tma_prefetch_desc(&tm_b);
       tma_prefetch_desc(&tm_b_scale);
@@ -349,8 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
       long long issued = 0;
       bool ok = true;
       for (; w.more() && ok; w.next()) {
-        const int bt = w.tn * 2 + static_cast<int>(rank);
-        const int rb = bt < b_tiles ? bt * ROWS : 0;  // (a box wholly past N loads row 0)
+        // (a half wholly past N is not loaded: what is there instead makes columns that are not stored)
+        const int bt = 2 * w.tn, halves = bt + 1 < b_tiles ? 2 : 1;
         for (int b = w.b0; b < w.b1; ++b) {
           if (!mbar_wait(bempty0 + 8 * empty, ephase, st, SITE_PRODUCER)) {
             ok = false;
@@ -362,11 +347,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
           }
           const uint32_t fb = bfull0 + 8 * stage;
           const bool scales = b % 4 == 0 || b == w.b0;
-          mbar_arrive_expect_tx(fb, 2 * (CODE_BYTES + (scales ? L8_SCALE_TILE : 0)));
+          mbar_arrive_expect_tx(fb, halves * (CODE_BYTES + (scales ? L8_SCALE_TILE : 0)));
           const int d = b * L8_BLOCK;
-          tma_load_2d_both(base + B0 + stage * B_BYTES + rank * CODE_BYTES, &tm_b, fb, p.g.b_mn ? rb : d, p.g.b_mn ? d : rb);
-          if (scales)
-            tma_load_2d_both(base + BS0 + (2 * stage + rank) * L8_SCALE_TILE, &tm_b_scale, fb, 0, (bt < b_tiles ? bt : 0) * groups + b / 4);
+          for (int h = 0; h < halves; ++h) {
+            const int rb = (bt + h) * ROWS;
+            tma_load_2d(base + B0 + stage * B_BYTES + h * CODE_BYTES, &tm_b, fb, p.g.b_mn ? rb : d, p.g.b_mn ? d : rb);
+            if (scales) tma_load_2d(base + BS0 + (2 * stage + h) * L8_SCALE_TILE, &tm_b_scale, fb, 0, (bt + h) * groups + b / 4);
+          }
           ++issued;
           if (++stage == B_STAGES) {
             stage = 0;
@@ -429,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
           for (int kk = 0; kk < L8_BLOCK / 32; ++kk)
             mma_block_scaled(d_tmem, adesc0 + aoff + kk * astep, bdesc0 + boff + kk * bstep, idesc, sfa, sfb,
                                   (b != w.b0 || kk != 0) ? 1u : 0u);
-          mma_commit_both(bempty0 + 8 * empty);
+          mma_commit(bempty0 + 8 * empty);
           if (++empty == EMPTIES) empty = 0;
           if (give_back) mma_commit(aempty0 + 8 * slot);
           if (++stage == B_STAGES) {
@@ -716,7 +703,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Plan<kFew>::THREADS,
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no CTA leaves while the other may still write to it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);

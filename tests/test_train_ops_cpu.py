@@ -167,3 +167,13 @@ def test_linear8_workspaces_of_no_rows(lib, N, K):
     """Asked for before each call, one of no rows among them, which needs no more than the smallest one with rows."""
     assert 0 < lib.trimul_linear8_forward_workspace_bytes(0, N, K) <= lib.trimul_linear8_forward_workspace_bytes(1, N, K)
     assert 0 < lib.trimul_linear8_backward_workspace_bytes(0, N, K) <= lib.trimul_linear8_backward_workspace_bytes(1, N, K)
+
+
+def test_no_copy_is_sent_to_several_processors():
+    """The library also runs on machines with several GPUs, where a load that a cluster shares may be closed: each block of threads
+    loads what it reads."""
+    import os
+    import re
+    for f in sorted(os.listdir(_lib.CSRC)):
+        text = re.sub(r'"\s*\n\s*"', "", open(os.path.join(_lib.CSRC, f)).read())
+        assert not re.search(r"cp\.async[\w.:]*multi" + "cast", text), f
