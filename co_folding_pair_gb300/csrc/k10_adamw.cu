@@ -221,13 +221,13 @@ __device__ __forceinline__ uint32_t pack_codes(const float (&f)[4]) {
 
 __device__ __forceinline__ float least_of(const float (&f)[4]) { return fminf(fminf(fabsf(f[0]), fabsf(f[1])), fminf(fabsf(f[2]), fabsf(f[3]))); }
 
+__device__ __forceinline__ float larger(float a, float b) {  // NaN if one is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // The largest magnitude of a warp's 128 numbers (a NaN's bits are above infinity's).
 __device__ __forceinline__ float warp_largest(const float (&f)[4]) {
-  auto larger = [](float a, float b) {  // NaN if one is
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-  };
   const float top = larger(larger(fabsf(f[0]), fabsf(f[1])), larger(fabsf(f[2]), fabsf(f[3])));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
@@ -246,6 +246,7 @@ __device__ __forceinline__ float at_random_low(float x, uint32_t bits) {
 // A warp's blocks as codes with their scales; the first kParts are of m, the others of roots: none negative, the random bits from
 // the hashes' upper halves, and what is above zero keeps a code above zero.  Few blocks have what takes longer (numbers below the evenly
 // spaced codes, scales past the reciprocal's range), so it is asked once for all.  A lane that is not `inside` is not asked.
+// A block with a number that is not finite gets such a scale, whatever its codes: they all stand for NaN.
 template <int kParts>
 __device__ __forceinline__ void quantize(const float (&f)[2 * kParts][4], const bool (&inside)[kParts], const uint32_t (&hashes)[kParts][4], bool stochastic,
                                          float (&scale)[2 * kParts], uint32_t (&codes)[2 * kParts]) {
@@ -253,7 +254,7 @@ __device__ __forceinline__ void quantize(const float (&f)[2 * kParts][4], const 
   bool normal = true, low = false;
 #pragma unroll
   for (int k = 0; k < 2 * kParts; ++k) {
-    scale[k] = __fmul_rn(fmaxf(warp_largest(f[k]), 0x1p-90f), 1.f / 448.f);
+    scale[k] = __fmul_rn(larger(warp_largest(f[k]), 0x1p-90f), 1.f / 448.f);
     inv[k] = reciprocal_rn(scale[k]);
     normal = normal && scale[k] < 0x1p100f;
   }

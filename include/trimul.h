@@ -548,7 +548,7 @@ trimul_status trimul_grad_clip(const trimul_grad_tensor* tensors, int n, float m
  * States in 8 bits (TRIMUL_STATES_E4M3): m, and r = sqrt(v), are held as e4m3
  * codes with an f32 scale for each 128 neighbours of a tensor (the last block
  * may have fewer).  A block with a value that is not finite is not finite
- * afterwards, all of it.
+ * afterwards, all of it, and from the next step on its parameters are not.
  *
  *   scale = max(max |x|, 2^-90) / 448,   code = e4m3(x / scale),   r's code at least 2^-9 where r > 0
  *
