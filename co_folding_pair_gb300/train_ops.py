@@ -8,7 +8,7 @@ only.
 
 The functions keep the C names; the classes wrap them as those of ``pair_ops`` do: calls take ``stream`` (default:
 the current one), do not wait on the host and may be captured; without the library or an sm_103 device
-they raise.
+they raise.  Making an object waits, so that it may be used on any stream.
 """
 
 from __future__ import annotations
@@ -37,6 +37,14 @@ def _listed(v, n, name):
     if len(v) != n:
         raise ValueError(f"{len(v)} {name} for {n} params")
     return list(v)
+
+
+def _ready(dev):
+    """Waits for what the current stream has been given, so that an object made there may be used on any stream (in a capture the
+    graph's order holds)."""
+    with torch.cuda.device(dev):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
 
 
 class AdamW:
@@ -107,6 +115,7 @@ class AdamW:
         self.table = (_lib.AdamwTensor * n).from_buffer(rows) if n else (_lib.AdamwTensor * 0)()
         self._p = _lib.AdamwParams(beta1=betas[0], beta2=betas[1], eps=eps, lr=0.0, states=int(self.eight),
                                    rounding=_one_of(_ROUNDING, rounding, "rounding"), seed=seed & 0xFFFFFFFF)
+        _ready(self.device)
 
     def step(self, grads, lr=None, norm=None, max_norm=None, stream=None, flags: int = 0):
         """One step with `grads` (a GradSet, a list or a dict, in the parameters' order; bf16, float16 or float32).
@@ -277,6 +286,7 @@ class Linear8:
         if bias is not None and not _fits(bias, torch.float32, (self.N,), self.device):
             _refuse(bias, torch.float32, (self.N,), self.device, "bias")
         self.bias = bias
+        _ready(self.device)
 
     def pack(self, weight, stream=None, flags: int = 0):
         if tuple(weight.shape) != (self.N, self.K):

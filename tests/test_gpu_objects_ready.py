@@ -1,0 +1,79 @@
+"""Linear8 and AdamW on streams other than the one that they are made on, on a GB300: ready at once, and their memory theirs
+until the last kernel that uses it has ended."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+SLEEP = 20_000_000  # some ten milliseconds
+
+
+@pytest.fixture(scope="module")
+def P():
+    from co_folding_pair_gb300 import train_ops
+    return train_ops
+
+
+def randn(*shape, seed=1):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def raw(t):
+    return t.view(torch.uint8) if t.element_size() == 1 else t
+
+
+def test_a_linear_layer_is_ready_for_any_stream(P):
+    """The stream that it is made on is busy when its weight is laid out."""
+    x, w, dy = randn(200, 64, seed=2).to(BF), randn(136, 64, seed=3), randn(200, 136, seed=4).to(BF)
+    lin = P.Linear8(w)
+    want = [lin(x), *(v for v in lin.backward(x, dy).values() if v is not None)]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    torch.cuda._sleep(SLEEP)
+    lin = P.Linear8(w)
+    lin.forward(x, stream=stream)
+    got = [lin.forward(x, stream=stream), *(v for v in lin.backward(x, dy, stream=stream).values() if v is not None)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("states", ["float32", "8bit"])
+def test_an_optimiser_is_ready_for_any_stream(P, states):
+    """Its states are zeros, and the count, when the first step reads them."""
+    sizes, g = [70000, 5, 1000], [randn(n, seed=n) for n in (70000, 5, 1000)]
+
+    def after(busy):
+        params = [torch.ones(n, device="cuda") for n in sizes]
+        stream = torch.cuda.Stream()
+        junk = torch.full((1 << 20,), 3.0, device="cuda")  # what the allocator gives out again is not zeros
+        torch.cuda.synchronize()
+        del junk
+        if busy:
+            torch.cuda._sleep(SLEEP)
+        opt = P.AdamW(params, states=states, seed=3)
+        opt.step(g, stream=stream)
+        torch.cuda.synchronize()
+        return [*params, *(raw(v).clone() for v in opt.state.values())]
+
+    want = after(False)  # (a kernel's first launch may wait by itself)
+    assert all(torch.equal(a, b) for a, b in zip(after(True), want))
+
+
+def test_objects_may_be_made_in_a_capture(P):
+    """Where waiting is not possible: the graph's order holds."""
+    x, w = randn(64, 32, seed=5).to(BF), randn(40, 32, seed=6)
+    p, g = torch.ones(300, device="cuda"), randn(300, seed=7)
+    want = P.Linear8(w)(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lin, opt = P.Linear8(w), P.AdamW([p], lr=1e-2, weight_decay=0.0)
+        y = lin(x)
+        opt.step([g])
+    for _ in range(2):
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y, want) and int(opt.state["count"]) == 1  # (the states are made anew in each replay)
+    assert float((1 - p).abs().max()) < 0.03 and float((1 - p).abs().max()) > 0.01
