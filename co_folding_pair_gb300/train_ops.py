@@ -47,6 +47,20 @@ def _ready(dev):
             torch.cuda.current_stream().synchronize()
 
 
+class _Own:
+    """An object's own memory, and the streams that it is used on: it is given out again behind the last kernel of each."""
+
+    def __init__(self, tensors, dev):
+        self.tensors, self.streams = tensors, {_raw(None, dev)}
+
+    def use(self, stream, dev):
+        raw = _raw(stream, dev)
+        if raw not in self.streams:
+            self.streams.add(raw)
+            for t in self.tensors:
+                t.record_stream(torch.cuda.current_stream(dev) if stream is None else stream)
+
+
 class AdamW:
     """AdamW (decoupled weight decay) over a list (or dict) of parameters: step(grads).
 
@@ -93,6 +107,7 @@ class AdamW:
         self.state = {k: torch.zeros(total, dtype=kind, device=dev) for k in "mv"}
         if self.eight:
             self.state.update({k + "_scale": torch.zeros(total // BLOCK, dtype=torch.float32, device=dev) for k in "mv"})
+        self._own = _Own([*self.state.values(), self._count], self.device)
         self.state["count"], self._count_at = self._count[0], self._count.data_ptr()
         # one row of numbers for each tensor, as _lib.AdamwTensor lays them out
         rows = np.zeros(n, dtype=np.dtype([("param", "<i8"), ("copy", "<i8"), ("m", "<i8"), ("v", "<i8"),
@@ -139,6 +154,7 @@ class AdamW:
             p.lr, p.lr_device = 0.0, self._one(self.lr, "lr")
         else:
             p.lr, p.lr_device = self.lr, None
+        self._own.use(stream, self.device)
         _check(_lib.load().trimul_adamw_step(p, self.table, grads.table, len(self.table), self._count_at, self.device,
                                              _raw(stream, self.device), flags))
 
@@ -286,14 +302,17 @@ class Linear8:
         if bias is not None and not _fits(bias, torch.float32, (self.N,), self.device):
             _refuse(bias, torch.float32, (self.N,), self.device, "bias")
         self.bias = bias
+        self._own = _Own([self.packed], self.device)
         _ready(self.device)
 
     def pack(self, weight, stream=None, flags: int = 0):
         if tuple(weight.shape) != (self.N, self.K):
             raise ValueError(f"weight must be {(self.N, self.K)}, got {tuple(weight.shape)}")
+        self._own.use(stream, self.device)
         trimul_linear8_pack(weight, self.packed, stream, flags)
 
     def forward(self, x, out=None, stream=None, flags: int = 0):
+        self._own.use(stream, self.device)
         return _forward(self.packed, self.N, self.K, self.device, x, self.bias, out, stream, flags)
 
     __call__ = forward
@@ -303,4 +322,5 @@ class Linear8:
         not name."""
         if want is None:
             want = ("dx", "dw", "dbias") if self.bias is not None else ("dx", "dw")
+        self._own.use(stream, self.device)
         return _backward(self.packed, self.N, self.K, self.device, x, dy, dx, dw, dbias, want, stream, flags)

@@ -77,3 +77,55 @@ def test_objects_may_be_made_in_a_capture(P):
         graph.replay()
         assert torch.equal(y, want) and int(opt.state["count"]) == 1  # (the states are made anew in each replay)
     assert float((1 - p).abs().max()) < 0.03 and float((1 - p).abs().max()) > 0.01
+
+
+@pytest.mark.parametrize("how", ["stream=", "current"])
+def test_a_linear_layers_memory_outlives_its_last_call(P, how):
+    """The object goes while another stream still has its call before it; the next tensor of its size is another's memory."""
+    x, w, dy = randn(300, 256, seed=2).to(BF), randn(520, 256, seed=3), randn(300, 520, seed=4).to(BF)
+    lin = P.Linear8(w)
+    want = [lin(x), lin.backward(x, dy)["dx"]]
+    stream = torch.cuda.Stream()
+    y, dx = torch.empty_like(want[0]), torch.empty_like(want[1])
+    torch.cuda.synchronize()
+    lin, junk = P.Linear8(w), []
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(SLEEP)
+        if how == "current":
+            lin(x, out=y)
+            lin.backward(x, dy, dx=dx, want=("dx",))
+    if how == "stream=":
+        lin(x, out=y, stream=stream)
+        lin.backward(x, dy, dx=dx, want=("dx",), stream=stream)
+    size = lin.packed.numel()
+    del lin
+    for _ in range(4):
+        junk.append(torch.full((size,), 0x33, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(dx, want[1])
+
+
+@pytest.mark.parametrize("states", ["float32", "8bit"])
+def test_an_optimisers_memory_outlives_its_last_step(P, states):
+    n = 300000
+    g = randn(n, seed=1)
+
+    def after(busy):
+        p = torch.ones(n, device="cuda")
+        stream = torch.cuda.Stream()
+        opt = P.AdamW([p], states=states, seed=3)
+        opt.step([g])
+        torch.cuda.synchronize()
+        if busy:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(SLEEP)
+        opt.step([g], stream=stream)
+        sizes = [(v.numel(), v.dtype) for v in opt.state.values()]
+        del opt
+        junk = [torch.full((k,), 3, device="cuda").to(dt) for k, dt in sizes for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk
+        return p
+
+    want = after(False)
+    assert torch.equal(after(True), want)
