@@ -28,10 +28,16 @@ BLOCK = 128  # neighbours that share a scale in the 8-bit states
 _BYTES = np.array([2, 4, 2], dtype=np.int64)  # of _TYPES
 
 
-def _listed(v, n, name):
+def _values(v, names):
+    """A list or a dict as a list: a dict with the parameters' names (None: they have none) in the parameters' order, else as it is."""
+    if not isinstance(v, dict):
+        return v
+    return [v[k] for k in names] if names is not None and v.keys() == set(names) else list(v.values())
+
+
+def _listed(v, n, name, names=None):
     """A value for each of n tensors, from one for all, a list or a dict."""
-    if isinstance(v, dict):
-        v = list(v.values())
+    v = _values(v, names)
     if not isinstance(v, (list, tuple)):
         return [v] * n
     if len(v) != n:
@@ -66,7 +72,7 @@ class AdamW:
 
     params: float32 or bf16, updated in place; copies: for each parameter a bf16 or float16 tensor of its shape that
     gets the new value rounded to nearest, or None (default: none); weight_decay: one number, or one for each
-    parameter.  states: "float32", or "8bit" for e4m3 codes with a scale for each 128 neighbours.  rounding: how bf16
+    parameter.  Dicts of these and of gradients that have the parameters' names go by them, others by their order.  states: "float32", or "8bit" for e4m3 codes with a scale for each 128 neighbours.  rounding: how bf16
     parameters and 8-bit states are rounded, "stochastic" (at random, by a hash of `seed`, the step and the element)
     or "nearest".
 
@@ -79,10 +85,11 @@ class AdamW:
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, states="float32", copies=None,
                  rounding="stochastic", seed=0):
+        self._names = list(params) if isinstance(params, dict) else None
         params = list(params.values() if isinstance(params, dict) else params)
         n = len(params)
-        copies = _listed(copies, n, "copies")
-        decay = _listed(weight_decay, n, "weight_decay")
+        copies = _listed(copies, n, "copies", self._names)
+        decay = _listed(weight_decay, n, "weight_decay", self._names)
         self.params, self.copies, self.lr = params, copies, lr
         self.device = _cuda(params[0], "params[0]") if params else torch.cuda.current_device()
         for k, (p, c) in enumerate(zip(params, copies)):
@@ -139,7 +146,7 @@ class AdamW:
         each time; norm (GradSet.norm's, on the device) and max_norm: clip by it in the same pass; a norm that is not
         finite makes the step nothing."""
         if not isinstance(grads, GradSet):
-            grads = GradSet(grads)
+            grads = GradSet(_values(grads, self._names))
         p = self._p
         if len(grads.table) != len(self.table):
             raise ValueError(f"{len(grads.table)} grads for {len(self.table)} params")

@@ -129,3 +129,16 @@ def test_an_optimisers_memory_outlives_its_last_step(P, states):
 
     want = after(False)
     assert torch.equal(after(True), want)
+
+
+def test_an_optimisers_dicts_go_by_name(P):
+    """Gradients, copies and weight decays in another order than the parameters', of the same shape."""
+    def after(flip):
+        order = lambda d: dict(reversed(d.items())) if flip else d  # noqa: E731
+        p = {"a": torch.ones(200, device="cuda"), "b": 2 * torch.ones(200, device="cuda")}
+        copies = {k: torch.zeros(200, dtype=BF, device="cuda") for k in p}
+        opt = P.AdamW(p, lr=0.1, weight_decay=order({"a": 0.0, "b": 0.5}), copies=order(copies))
+        opt.step(order({"a": randn(200, seed=8), "b": randn(200, seed=9)}))
+        return [*p.values(), *(copies[k] for k in p)]
+
+    assert all(torch.equal(a, b) for a, b in zip(after(False), after(True)))

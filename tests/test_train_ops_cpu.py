@@ -177,3 +177,11 @@ def test_no_copy_is_sent_to_several_processors():
     for f in sorted(os.listdir(_lib.CSRC)):
         text = re.sub(r'"\s*\n\s*"', "", open(os.path.join(_lib.CSRC, f)).read())
         assert not re.search(r"cp\.async[\w.:]*multi" + "cast", text), f
+
+
+def test_dicts_go_by_the_parameters_names():
+    assert P._listed({"b": 2, "a": 1}, 2, "copies", ["a", "b"]) == [1, 2]
+    assert P._listed({"b": 2, "a": 1}, 2, "copies") == P._listed({"b": 2, "a": 1}, 2, "copies", ["x", "y"]) == [2, 1]
+    assert P._listed(0.1, 2, "weight_decay", ["a", "b"]) == [0.1, 0.1]
+    with pytest.raises(ValueError, match="1 copies for 2 params"):
+        P._listed({"a": 1}, 2, "copies", ["a", "b"])
