@@ -152,18 +152,18 @@ class AdamW:
             raise ValueError(f"{len(grads.table)} grads for {len(self.table)} params")
         if grads.device != self.device and len(self.table):
             raise ValueError(f"grads must be on cuda:{self.device}, got cuda:{grads.device}")
-        if lr is not None:
-            self.lr = lr
+        lr = self.lr if lr is None else lr
         if (norm is None) != (max_norm is None):
             raise ValueError("give both norm and max_norm, or neither")
         p.norm, p.max_norm = self._one(norm, "norm"), 0.0 if max_norm is None else max_norm
-        if isinstance(self.lr, torch.Tensor):
-            p.lr, p.lr_device = 0.0, self._one(self.lr, "lr")
+        if isinstance(lr, torch.Tensor):
+            p.lr, p.lr_device = 0.0, self._one(lr, "lr")
         else:
-            p.lr, p.lr_device = self.lr, None
+            p.lr, p.lr_device = lr, None
         self._own.use(stream, self.device)
         _check(_lib.load().trimul_adamw_step(p, self.table, grads.table, len(self.table), self._count_at, self.device,
                                              _raw(stream, self.device), flags))
+        self.lr = lr  # (a step that is refused leaves it)
 
     def _one(self, t, name):
         if t is None:

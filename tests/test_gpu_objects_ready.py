@@ -142,3 +142,16 @@ def test_an_optimisers_dicts_go_by_name(P):
         return [*p.values(), *(copies[k] for k in p)]
 
     assert all(torch.equal(a, b) for a, b in zip(after(False), after(True)))
+
+
+def test_a_refused_step_leaves_the_learning_rate(P):
+    p, g = torch.ones(64, device="cuda"), randn(64, seed=8)
+    opt = P.AdamW([p], lr=0.25)
+    for bad in (float("nan"), torch.ones(2, device="cuda"), torch.ones(())):
+        with pytest.raises(Exception, match="lr must be"):
+            opt.step([g], lr=bad)
+    with pytest.raises(Exception, match="its gradient has 8 elements"):
+        opt.step([g[:8]], lr=1.0)
+    assert opt.lr == 0.25 and int(opt.state["count"]) == 0
+    opt.step([g], lr=0.5)
+    assert opt.lr == 0.5 and int(opt.state["count"]) == 1
