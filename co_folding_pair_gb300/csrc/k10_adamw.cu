@@ -191,8 +191,8 @@ __device__ __forceinline__ float reciprocal(float x) {  // of a normal number, w
   return r;
 }
 // The root of x in [2^-60, inf), rounded to nearest: Newton's step from an approximation, with the remainder x - r^2
-// exact in the fused product (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  Compared
-// with the correctly rounded root for every x.
+// exact in the fused product (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  The
+// tests compare a million of them, of all sizes, with the correctly rounded root.
 __device__ __forceinline__ float root(float x) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
