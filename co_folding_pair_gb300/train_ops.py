@@ -54,7 +54,8 @@ def _ready(dev):
 
 
 class _Own:
-    """An object's own memory, and the streams that it is used on: it is given out again behind the last kernel of each."""
+    """An object's own memory, and the streams that it is used on: it is given out again behind the last kernel of each.  An external
+    stream may be gone by then: there the caller keeps the object until its kernels have ended."""
 
     def __init__(self, tensors, dev):
         self.tensors, self.streams = tensors, {_raw(None, dev)}
@@ -63,8 +64,10 @@ class _Own:
         raw = _raw(stream, dev)
         if raw not in self.streams:
             self.streams.add(raw)
-            for t in self.tensors:
-                t.record_stream(torch.cuda.current_stream(dev) if stream is None else stream)
+            at = torch.cuda.current_stream(dev) if stream is None else stream
+            if raw == 0 or at.stream_id != raw:  # (an external stream's number is its handle)
+                for t in self.tensors:
+                    t.record_stream(at)
 
 
 class AdamW:
@@ -72,9 +75,9 @@ class AdamW:
 
     params: float32 or bf16, updated in place; copies: for each parameter a bf16 or float16 tensor of its shape that
     gets the new value rounded to nearest, or None (default: none); weight_decay: one number, or one for each
-    parameter.  Dicts of these and of gradients that have the parameters' names go by them, others by their order.  states: "float32", or "8bit" for e4m3 codes with a scale for each 128 neighbours.  rounding: how bf16
-    parameters and 8-bit states are rounded, "stochastic" (at random, by a hash of `seed`, the step and the element)
-    or "nearest".
+    parameter.  Dicts of these and of gradients that have the parameters' names go by them, others by their order.
+    states: "float32", or "8bit" for e4m3 codes with a scale for each 128 neighbours.  rounding: how bf16 parameters and
+    8-bit states are rounded, "stochastic" (at random, by a hash of `seed`, the step and the element) or "nearest".
 
     `state` has the states of all parameters behind one another, each from a multiple of 128 on (`starts`): "m", "v" and
     "count", the steps taken (int32, on the device), and with "8bit" "m_scale" and "v_scale" by blocks, "v" then being

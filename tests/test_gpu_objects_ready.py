@@ -155,3 +155,25 @@ def test_a_refused_step_leaves_the_learning_rate(P):
     assert opt.lr == 0.25 and int(opt.state["count"]) == 0
     opt.step([g], lr=0.5)
     assert opt.lr == 0.5 and int(opt.state["count"]) == 1
+
+
+def test_objects_used_on_a_stream_that_is_gone(P):
+    """A stream that torch does not own: the objects go after it, and their memory is given out again."""
+    import ctypes
+    x, w, g = randn(64, 32, seed=5).to(BF), randn(40, 32, seed=6), randn(300, seed=7)
+    want = P.Linear8(w)(x)
+    lin, opt = P.Linear8(w), P.AdamW([torch.ones(300, device="cuda")])
+    cuda, handle = torch.cuda.cudart(), ctypes.c_uint64(0)
+    assert int(cuda.cudaStreamCreate(ctypes.addressof(handle))) == 0
+    stream = torch.cuda.ExternalStream(handle.value)
+    y = torch.empty_like(want)
+    torch.cuda.synchronize()
+    lin(x, out=y, stream=stream)
+    with torch.cuda.stream(stream):
+        opt.step([g])
+    stream.synchronize()
+    assert torch.equal(y, want) and int(opt.state["count"]) == 1
+    assert int(cuda.cudaStreamDestroy(handle.value)) == 0
+    del lin, opt
+    assert torch.equal(P.Linear8(w)(x), want)
+    torch.cuda.synchronize()
