@@ -32,7 +32,7 @@
 // what it has written before.  Each element has one thread, whichever accumulator
 // it is in, whose additions to it come in its program's order: the order is fixed.
 // They are done in L2 (red): with a load, an addition and a store the warps waited for the
-// loads, and dW of 2^20 rows of 1024 to 256 channels took 649 us for 569.
+// loads, and dW of 2^20 rows of 1024 to 256 channels took 80 us more (579 now, dy's codes among them).
 #include "gemm8.cuh"
 #include "quantize8.cuh"
 
@@ -41,8 +41,8 @@ namespace trimul {
 namespace {
 constexpr int ROWS = 128;
 // Blocks of t that are asked for in L2 ahead of their turn, as the tiles that are on their way are too few: 2^20 rows of 1024 to 256
-// channels 454 us without, 414 with two (and with four, but then 256 to 256 takes 198 for 166).  Where a run's tiles share the
-// codes it does not help: 446 us became 503.
+// channels take 459 us without, 417 with two and 419 with four, 256 to 256 take 241, 163 and 209.  Where a run's tiles share the
+// codes it does not help: 256 to 1024 takes 433 to 435 us without and 429 to 435 with two.
 constexpr int AHEAD = 2;
 constexpr uint32_t CODE_BYTES = ROWS * L8_BLOCK;
 constexpr uint32_t B_BYTES = 2 * CODE_BYTES;  // 256 rows of B
@@ -58,7 +58,7 @@ constexpr int EPI0 = 2, EPI_WARPS = 8, ROUND0 = EPI0 + EPI_WARPS, TEAM_WARPS = 8
 constexpr int TURNS = 16 / EPI_WARPS;  // 64-column blocks of an epilogue warp
 // How the warps and the shared memory are shared out.  kFew: by rows, with few blocks of depth (FUSED8_FEW_BLOCKS).  There the
 // way out counts: a tile goes by way of shared memory and TMA.  (Turned in registers by shuffles and stored by the warps, 2^20 rows of
-// 256 to 1024 channels take 455 us and with a bias 531; this way 440 and 443.  128 to 128: 119 and 145, now 91 and 93.)
+// 256 to 1024 channels took 455 us and with a bias 531; this way 433 and 435.  128 to 128: 119 and 145, now 89 and 93.)
 // The room is a tile of t's, one team is enough for what is left to round, and the warps have more registers.
 // Else rounding has two teams: with one, or with one tile of t on its way, it falls behind.
 template <bool kFew>

@@ -21,8 +21,8 @@ constexpr int kMostWidth = 65536;
 constexpr int kMostPairs = 128, kMostSms = 256;  // what workspaces are sized for
 constexpr int kChunk = 32;                       // blocks of 128 rows that a weight gradient's accumulation takes
 // 256-wide tiles of the other operand up to which rounding on the way (k13_fused8.cu) is faster than a pass of its own: each tile
-// rounds again.  us: by rows 2^20 of 256 to 256 channels (one tile) 165 to 280, 2^19 of 512 to 512 (two) 253 to 287, 2^18 of 1024 to 768
-// (three) 321 to 303; by columns 2^20 of 1024 to 256 569 to 933, 2^19 of 512 to 512 346 to 400, 2^18 of 1024 to 1024 (four) 601 to 491.
+// rounds again.  us: by rows 2^20 of 1024 to 256 channels (one tile) 415 to 794, 2^19 of 512 to 512 (two) 236 to 282, 2^18 of 1024 to 768
+// (three) 311 to 303; by columns 2^20 of 1024 to 256 579 to 929, 2^19 of 512 to 512 358 to 398, 2^18 of 1024 to 1024 (four) 588 to 488.
 constexpr int kFusedRows = 2, kFusedColumns = 2;
 constexpr unsigned long long kTimeoutNs = 4000000000ull, kStallTimeoutNs = 200000000ull;
 constexpr size_t kStatusBytes = 256;

@@ -1,5 +1,5 @@
-// step_ops.h -- launchers of the operators that end a training step, and of the
-// linear layer in 8 bits (internal).
+// step_ops.h -- the launcher of AdamW, which ends a training step (internal).
+// Those of the linear layer in 8 bits are in linear8.h.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -1,5 +1,5 @@
-// step_ops_api.cu -- the C ABI's entry points of the training step's end and of
-// the linear layer in 8 bits (include/trimul.h): argument checks and launches.
+// step_ops_api.cu -- the C ABI's entry point of AdamW (include/trimul.h): argument
+// checks and the launch.  Those of the linear layer in 8 bits are in linear8_api.cu.
 #include <cuda_runtime.h>
 
 #include <cmath>

@@ -143,7 +143,8 @@ class AdamW:
         _ready(self.device)
 
     def step(self, grads, lr=None, norm=None, max_norm=None, stream=None, flags: int = 0):
-        """One step with `grads` (a GradSet, a list or a dict, in the parameters' order; bf16, float16 or float32).
+        """One step with `grads` (a GradSet, a list or a dict, in the parameters' order; bf16, float16 or float32).  Of a
+        GradSet its tensors are read, not its `outs`: after a clip() into those, give the outs themselves.
 
         lr: for this step and the later ones, a number or a float32 tensor on the device, which a captured step reads
         each time; norm (GradSet.norm's, on the device) and max_norm: clip by it in the same pass; a norm that is not

@@ -609,11 +609,13 @@ trimul_status trimul_adamw_step(const trimul_adamw_params* p, const trimul_adamw
  *   dW    = Qcol(dy)^T Qcol(x)                   Qcol: 128 rows of a channel
  *   dbias = the sum of dy over the rows          (not rounded to 8 bits)
  *
- * Sums are in 32 bits; those over rows are cut into parts of 4096 on the tensor
- * cores, which are added in a fixed order.  A number that is not finite becomes NaN,
- * in every output that it takes part in, and leaves its block's power to the others.  As the
- * TRIMUL_FLAG_FP8 path, this is less accurate than 16 bits: some 3e-2 of an
- * output's norm for operands of normal distribution.
+ * Sums are in 32 bits.  The tensor cores may cut off what is below the last bit,
+ * once for each 32 of depth, over all of K for y and of N for dx; sums over rows
+ * are cut into parts of 4096, which are added to nearest in a fixed order.  A
+ * number that is not finite becomes NaN, in every output that it takes part in
+ * (dbias adds it as it is), and leaves its block's power to the others.  As the TRIMUL_FLAG_FP8 path, this
+ * is less accurate than 16 bits: some 3e-2 of an output's norm for operands of
+ * normal distribution.
  *
  * N and K are multiples of 8 in [8, 65536], 0 <= rows < 2^31 - 256.  The caller
  * keeps the weight as codes (trimul_linear8_pack after each change of it) and gives
