@@ -8,7 +8,8 @@ only.
 
 The functions keep the C names; the classes wrap them as those of ``pair_ops`` do: calls take ``stream`` (default:
 the current one), do not wait on the host and may be captured; without the library or an sm_103 device
-they raise.  Making an object waits, so that it may be used on any stream.
+they raise.  Making an object waits, so that it may be used on any stream; in a capture it is made on the captured stream, and does
+not wait.
 """
 
 from __future__ import annotations
